@@ -38,6 +38,10 @@ What it computes, in plain numpy float64 (slow and obviously correct):
                      ``rtn_quantize_sym`` take bits=8 for 8-bit weights ("AWQ +
                      GPTQ Quantization, in depth", 4-bit bigger or 8-bit smaller).
 * ``dequant`` / ``linear``   W^ = (q - Z)*S and y = x W^T in float64.
+* ``lora_forward`` / ``lora_backward``   low-rank adapters of many rows and their
+                     gradients in float64 (pinned by differences of the forward).
+* ``act_quantize`` / ``act_values``   activations in 8 bits per row and group, the
+                     symmetric 8-bit scheme applied to activations.
 * ``layer_bytes`` / ``bits_per_weight``   storage cost of a packed layer.
 
 Pins (tests/test_oracle_*.py, run without a GPU): the S/2 round-trip bound,
@@ -59,6 +63,7 @@ from .packing import (pack_codes, unpack_codes, pack_zeros, unpack_zeros,
                       sorted_k_order, pack_codes_act_order,
                       pack_codes8, unpack_codes8, pack_zeros8, unpack_zeros8)
 from .layer import dequant, dequant_fp16, linear, rel_err
+from .adapters import lora_forward, lora_backward, act_quantize, act_values
 from .storage import layer_bytes, bits_per_weight
 
 __all__ = [
@@ -68,5 +73,6 @@ __all__ = [
     "sorted_k_order", "pack_codes_act_order",
     "dequant", "dequant_fp16", "linear", "rel_err",
     "awq_search", "gptq_hessian", "gptq_quantize", "output_error",
+    "lora_forward", "lora_backward", "act_quantize", "act_values",
     "layer_bytes", "bits_per_weight",
 ]

@@ -1,0 +1,148 @@
+"""The adapter entry points without a GPU: exported symbols, workspace sizes, and every
+refusal of the C ABI and the binding (nothing is launched here: the pointers are made up,
+and each call is refused before it would use them)."""
+
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import w4a16_gemm_amd as w4
+from w4a16_gemm_amd import adapters
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+BASE = 1 << 20      # a 16-byte aligned address that is never read
+
+
+def test_library_exports_the_adapter_header():
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "w4a16_adapters.h")).read(), flags=re.S)
+    declared = sorted(set(re.findall(r"\b(w4a16_\w+)\s*\(", text)))
+    assert declared == sorted(adapters.SIGNATURES)
+    for name in declared:
+        assert hasattr(w4.lib(), name), name
+
+
+FORWARD = dict(y=BASE, x=BASE, a=BASE, b=BASE, index=BASE, scaling=BASE, M=4, N=64, K=128, R=16, L=2, out=BASE, h=BASE,
+               workspace=BASE, bytes=1 << 30, stream=None)
+BACKWARD = dict(dy=BASE, x=BASE, a=BASE, b=BASE, h=BASE, index=BASE, scaling=BASE, dx0=BASE, M=4, N=64, K=128, R=16, L=2,
+                dx=BASE, da=BASE, db=BASE, workspace=BASE, bytes=1 << 30, stream=None)
+Q8 = dict(dy=BASE, codes=BASE, scales=BASE, group=32, a=BASE, b=BASE, h=BASE, index=BASE, scaling=BASE, dx0=BASE, M=4,
+          N=64, K=128, R=16, L=2, dx=BASE, da=BASE, db=BASE, workspace=BASE, bytes=1 << 30, stream=None)
+QUANT = dict(x=BASE, M=4, K=128, group=32, codes=BASE, scales=BASE, stream=None)
+DEQUANT = dict(codes=BASE, scales=BASE, M=4, K=128, group=32, x=BASE, stream=None)
+
+SHAPE = [({"M": 0}, w4.ERR_INVALID_ARG), ({"M": -1}, w4.ERR_INVALID_ARG), ({"N": 0}, w4.ERR_INVALID_ARG),
+         ({"K": 0}, w4.ERR_INVALID_ARG), ({"N": 60}, w4.ERR_INVALID_ARG), ({"K": 100}, w4.ERR_INVALID_ARG),
+         ({"R": 0}, w4.ERR_UNSUPPORTED), ({"R": 12}, w4.ERR_UNSUPPORTED), ({"R": 136}, w4.ERR_UNSUPPORTED),
+         ({"L": 0}, w4.ERR_UNSUPPORTED), ({"L": 65536}, w4.ERR_UNSUPPORTED), ({"M": (1 << 27) + 1}, w4.ERR_UNSUPPORTED),
+         ({"N": (1 << 24) + 8}, w4.ERR_UNSUPPORTED), ({"bytes": 16}, w4.ERR_INVALID_ARG),
+         ({"workspace": None}, w4.ERR_INVALID_ARG), ({"workspace": BASE + 8}, w4.ERR_MISALIGNED)]
+GROUP = [({"group": 16}, w4.ERR_UNSUPPORTED), ({"group": 0}, w4.ERR_UNSUPPORTED), ({"group": 128, "K": 192}, w4.ERR_INVALID_ARG),
+         ({"codes": None}, w4.ERR_INVALID_ARG), ({"scales": None}, w4.ERR_INVALID_ARG),
+         ({"codes": BASE + 4}, w4.ERR_MISALIGNED), ({"scales": BASE + 1}, w4.ERR_MISALIGNED)]
+
+
+def _pointers(names):
+    return [({n: None}, w4.ERR_INVALID_ARG) for n in names] + [({n: BASE + 2}, w4.ERR_MISALIGNED) for n in names]
+
+
+REFUSED = (
+    [("w4a16_lora_forward", FORWARD, c) for c in SHAPE + _pointers(["y", "x", "a", "b", "out"])
+     + [({"index": BASE + 2}, w4.ERR_MISALIGNED), ({"scaling": BASE + 2}, w4.ERR_MISALIGNED), ({"h": BASE + 4}, w4.ERR_MISALIGNED)]]
+    + [("w4a16_lora_backward", BACKWARD, c) for c in SHAPE + _pointers(["dy", "x", "a", "b", "h", "da", "db"])
+       + [({"dx": None}, w4.ERR_INVALID_ARG), ({"dx0": BASE + 2}, w4.ERR_MISALIGNED)]]
+    + [("w4a16_lora_backward_q8", Q8, c) for c in SHAPE + GROUP + _pointers(["dy", "a", "b", "h", "da", "db"])]
+    + [("w4a16_act_quantize", QUANT, c) for c in GROUP + _pointers(["x"]) + [({"M": 0}, w4.ERR_INVALID_ARG), ({"K": -32}, w4.ERR_INVALID_ARG), ({"M": 1 << 30}, w4.ERR_UNSUPPORTED)]]
+    + [("w4a16_act_dequantize", DEQUANT, c) for c in GROUP + _pointers(["x"]) + [({"M": 0}, w4.ERR_INVALID_ARG), ({"M": 1 << 30}, w4.ERR_UNSUPPORTED)]])
+
+
+@pytest.mark.parametrize("name,good,change", REFUSED, ids=[f"{n}-{c[0]}" for n, _, c in REFUSED])
+def test_c_abi_refuses(name, good, change):
+    args, status = change
+    fn = getattr(adapters._lib(), name)
+    assert fn(*dict(good, **args).values()) == status
+    assert w4.lib().w4a16_last_error()
+
+
+def test_workspace_sizes():
+    lib = adapters._lib()
+    for fn in (lib.w4a16_lora_forward_workspace, lib.w4a16_lora_backward_workspace):
+        assert fn(4, 64, 128, 12, 2, 1) == 0 and fn(0, 64, 128, 16, 2, 1) == 0
+        assert 0 < fn(4, 64, 128, 16, 2, 0) <= fn(4, 64, 128, 16, 2, 1)
+        assert fn(1000, 64, 128, 16, 2, 1) >= fn(1000, 64, 128, 16, 2, 0) + 4 * 1002
+    # sizes that pass 32 bits
+    assert lib.w4a16_lora_backward_workspace(1 << 24, 64, 128, 128, 2, 0) >= 4 * 128 << 24
+
+
+# --- the binding ---------------------------------------------------------------------
+
+def _tensors():
+    t = torch.zeros
+    return dict(y=t(4, 64, dtype=torch.float16), x=t(4, 128, dtype=torch.float16),
+                a=t(2, 16, 128, dtype=torch.float16), b=t(2, 64, 16, dtype=torch.float16),
+                index=t(4, dtype=torch.int32), scaling=t(2), out=t(4, 64, dtype=torch.float16), h=t(4, 16))
+
+
+@pytest.mark.parametrize("change", [
+    {"y": torch.zeros(5, 64, dtype=torch.float16)}, {"x": torch.zeros(4, 120, dtype=torch.float16)},
+    {"b": torch.zeros(2, 16, 64, dtype=torch.float16)}, {"b": torch.zeros(3, 64, 16, dtype=torch.float16)},
+    {"a": torch.zeros(16, 128, dtype=torch.float16)}, {"index": torch.zeros(3, dtype=torch.int32)},
+    {"scaling": torch.zeros(3)}, {"out": torch.zeros(4, 56, dtype=torch.float16)}, {"h": torch.zeros(4, 8)},
+    {"x": torch.zeros(128, dtype=torch.float16)}])
+def test_forward_refuses_shapes(change):
+    with pytest.raises(ValueError):
+        w4.w4a16_lora_forward(**dict(_tensors(), **change))
+
+
+@pytest.mark.parametrize("change", [
+    {"y": torch.zeros(4, 64)}, {"x": torch.zeros(4, 128, dtype=torch.bfloat16)}, {"index": torch.zeros(4, dtype=torch.int64)},
+    {"scaling": torch.zeros(2, dtype=torch.float64)}, {"h": torch.zeros(4, 16, dtype=torch.float16)},
+    {"x": torch.zeros(128, 4, dtype=torch.float16).t()}, {}])
+def test_forward_refuses_types_layouts_and_host_tensors(change):
+    with pytest.raises(TypeError):
+        w4.w4a16_lora_forward(**dict(_tensors(), **change))
+
+
+def _backward_tensors():
+    d = _tensors()
+    return dict(dy=d["y"], x=d["x"], a=d["a"], b=d["b"], h=d["h"], index=d["index"], scaling=d["scaling"],
+                dx=torch.zeros(4, 128, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("change,error", [
+    ({"dy": torch.zeros(3, 64, dtype=torch.float16)}, ValueError), ({"h": torch.zeros(4, 8)}, ValueError),
+    ({"h": None}, TypeError), ({"dx": torch.zeros(4, 64, dtype=torch.float16)}, ValueError), ({}, TypeError)])
+def test_backward_refuses(change, error):
+    with pytest.raises(error):
+        w4.w4a16_lora_backward(**dict(_backward_tensors(), **change))
+
+
+def test_checkpoint_calls_refuse():
+    codes, scales = torch.zeros(4, 128, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.float16)
+    d = _backward_tensors()
+    rest = (d["a"], d["b"], d["h"])
+    with pytest.raises(ValueError):
+        w4.w4a16_lora_backward_q8(d["dy"], codes, scales, 64, *rest)          # scales of another group size
+    with pytest.raises(TypeError):
+        w4.w4a16_lora_backward_q8(d["dy"], codes.to(torch.int8), scales, 32, *rest)
+    with pytest.raises(TypeError):
+        w4.w4a16_lora_backward_q8(d["dy"], codes, None, 32, *rest)
+    with pytest.raises(TypeError):
+        w4.w4a16_lora_backward_q8(d["dy"], codes, scales, 32, *rest)          # host tensors
+    with pytest.raises(TypeError):
+        w4.w4a16_act_quantize(d["x"], 32)
+    with pytest.raises(ValueError):
+        w4.w4a16_act_dequantize(codes, scales, 128)
+    with pytest.raises(ValueError):
+        w4.w4a16_act_dequantize(codes[0], scales, 32)
+
+
+def test_overlapping_outputs_are_found():
+    x = torch.zeros(8, 64, dtype=torch.float16)
+    adapters._overlap(x[:4], (x[4:], "x"))
+    adapters._overlap(None, (x, "x"))
+    with pytest.raises(ValueError):
+        adapters._overlap(x[:5], (x[4:], "x"))

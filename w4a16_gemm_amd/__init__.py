@@ -479,3 +479,11 @@ def w4a16_quantize_device(w, group_size: int, in_scale=None, sym: bool = False, 
                                        None if qzeros is None else qzeros.data_ptr(), _stream_handle(stream, w.device)))
     return qweight, scales, qzeros
 
+
+# --- low-rank adapters and 8-bit activation checkpoints (include/w4a16_adapters.h) ---
+
+from .adapters import (w4a16_act_dequantize, w4a16_act_quantize, w4a16_lora_backward,  # noqa: E402
+                       w4a16_lora_backward_q8, w4a16_lora_forward)
+
+__all__ += ["w4a16_lora_forward", "w4a16_lora_backward", "w4a16_lora_backward_q8", "w4a16_act_quantize",
+            "w4a16_act_dequantize"]

@@ -57,8 +57,10 @@ def build(verbose: bool = False) -> str:
     dev_o = os.path.join(BUILD_DIR, "device.o")
     _run([hipcc, "-c", os.path.join(CSRC, "host.cpp"), *HOST_FLAGS, *inc, "-o", host_o], verbose)
     _run([hipcc, "-c", "-x", "hip", os.path.join(CSRC, "device.hip"), *DEVICE_FLAGS, *inc, "-o", dev_o], verbose)
+    ada_o = os.path.join(BUILD_DIR, "adapters.o")
+    _run([hipcc, "-c", "-x", "hip", os.path.join(CSRC, "adapters.hip"), *DEVICE_FLAGS, *inc, "-o", ada_o], verbose)
     tmp = LIB + ".tmp"
-    _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", host_o, dev_o, "-o", tmp], verbose)
+    _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", host_o, dev_o, ada_o, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     tmp = PEAKS_LIB + ".tmp"
     _run([hipcc, "-shared", "-fPIC", "-x", "hip", os.path.join(CSRC, "peaks.hip"), *DEVICE_FLAGS, *inc, "-o", tmp],

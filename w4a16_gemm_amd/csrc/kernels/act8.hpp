@@ -1,0 +1,97 @@
+// Activation checkpoints in 8 bits: the layer's input kept for the backward pass as one
+// byte per value and one binary16 scale per row and group of 32 / 64 / 128 channels (the
+// int8 absmax scheme of "LLM Quantization: INT8, GPTQ, and AWQ Explained", What
+// quantization actually does, applied to activations).
+//
+//   a = max |x|,  S = smallest binary16 >= a / 127  (1 if a == 0, at most 515.5)
+//   q = clamp(round(x / S), -127, 127),  code = q + 128,  value = binary16(q S)
+//
+// Exactness in fp32.  a / 127 rounded to fp32 and then to binary16 gives a neighbour of
+// the true quotient, and 127 h is exact in fp32 (11 + 7 bits), so one comparison with a
+// decides whether the next binary16 is needed.  x / S is a quotient of two 11-bit
+// significands: unless it is exactly halfway between two integers (and then exact in
+// fp32) it is at least 2^-12 away from that for |q| <= 128, far more than the half ulp
+// (2^-18) of a correctly rounded fp32 division, so rint of the fp32 quotient is the
+// rounded true quotient.
+// 515.5 is the largest binary16 whose 127-fold still rounds to a finite binary16; a group
+// above it (a in {65472, 65504}) has x / S < 127.5 and keeps q = 127.
+#pragma once
+
+#include "nibbles.hpp"
+
+namespace w4a16 {
+
+constexpr float kActMaxScale = 515.5f;
+
+// S of a group with largest magnitude a (not NaN, finite).
+__device__ __forceinline__ half_t act_scale(float a) {
+  half_t h = static_cast<half_t>(a / 127.0f);
+  if (static_cast<float>(h) * 127.0f < a)
+    h = __builtin_bit_cast(half_t, static_cast<uint16_t>(__builtin_bit_cast(uint16_t, h) + 1));
+  if (static_cast<float>(h) > kActMaxScale) h = static_cast<half_t>(kActMaxScale);
+  return a == 0.0f ? static_cast<half_t>(1.0f) : h;
+}
+
+// One lane quantises 8 consecutive channels (16 bytes in, 8 bytes out); a group is
+// LPG = group / 8 neighbouring lanes, whose maximum is formed with lane exchanges.
+// HBM-bound: 3 bytes per value.  A NaN or an infinity in a group makes its scale NaN
+// (codes 128), so that the restored values are NaN and the gradients show it.
+template <int LPG>
+__global__ __launch_bounds__(256) void act_quantize_kernel(const half_t* __restrict__ x, uint8_t* __restrict__ codes,
+                                                           half_t* __restrict__ scales, size_t chunks) {
+  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  const bool in = i < chunks;   // whole groups: chunks is a multiple of LPG
+  half8_t v = {};
+  if (in) v = reinterpret_cast<const half8_t*>(x)[i];
+  float a = 0.0f;
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float f = __builtin_fabsf(static_cast<float>(v[e]));
+    bad |= !(f <= 65504.0f);
+    a = f > a ? f : a;
+  }
+  if (bad) a = __builtin_inff();
+#pragma unroll
+  for (int d = 1; d < LPG; d <<= 1) a = fmaxf(a, __shfl_xor(a, d));
+  if (!in) return;
+  const bool finite = a <= 65504.0f;
+  const half_t s = finite ? act_scale(a) : __builtin_bit_cast(half_t, static_cast<uint16_t>(0x7E00));
+  const float sf = static_cast<float>(s);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = fminf(fmaxf(rintf(static_cast<float>(v[e]) / sf), -127.0f), 127.0f);
+    const uint32_t c = finite ? static_cast<uint32_t>(static_cast<int>(q) + 128) : 128u;
+    w[e >> 2] |= c << (8 * (e & 3));
+  }
+  reinterpret_cast<uint2*>(codes)[i] = uint2{w[0], w[1]};
+  if (i % LPG == 0) scales[i / LPG] = s;
+}
+
+// binary16(q S) for two codes placed in the low bytes of the two halves of `pair`: 0x6400
+// | c is binary16 1024 + c exactly, minus 1152 is q = c - 128 exactly, so the product is
+// the only rounding.
+__device__ __forceinline__ uint32_t act_value_pair(uint32_t pair, half2_t s) {
+  const half2_t q = as_h2(pair | kMagic) + half2_t{static_cast<half_t>(-1152.0f), static_cast<half_t>(-1152.0f)};
+  return __builtin_bit_cast(uint32_t, q * s);
+}
+
+// Restores 8 consecutive values per lane.
+__global__ __launch_bounds__(256) void act_dequantize_kernel(const uint8_t* __restrict__ codes,
+                                                             const half_t* __restrict__ scales,
+                                                             half_t* __restrict__ x, size_t chunks, int lpg_shift) {
+  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= chunks) return;
+  const uint2 c = reinterpret_cast<const uint2*>(codes)[i];
+  const half_t s = scales[i >> lpg_shift];
+  const half2_t ss = {s, s};
+  uint4 o;
+  o.x = act_value_pair(__builtin_amdgcn_perm(0u, c.x, 0x0C010C00u), ss);
+  o.y = act_value_pair(__builtin_amdgcn_perm(0u, c.x, 0x0C030C02u), ss);
+  o.z = act_value_pair(__builtin_amdgcn_perm(0u, c.y, 0x0C010C00u), ss);
+  o.w = act_value_pair(__builtin_amdgcn_perm(0u, c.y, 0x0C030C02u), ss);
+  reinterpret_cast<uint4*>(x)[i] = o;
+}
+
+}  // namespace w4a16
