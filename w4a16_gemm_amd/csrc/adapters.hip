@@ -74,19 +74,14 @@ int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
 // --- row plan -----------------------------------------------------------------------
 
-bool plan_in_memory(int M, bool with_index) { return with_index && M > kInlineRows; }
+size_t plan_bytes(int M, int L) { return up256((static_cast<size_t>(L) + 2 + M) * sizeof(int32_t)); }
 
-size_t plan_bytes(int M, int L, bool with_index) {
-  return plan_in_memory(M, with_index) ? up256((static_cast<size_t>(L) + 2 + M) * sizeof(int32_t)) : 0;
-}
-
-// The plan of a call; takes its memory from the front of the workspace.
+// A plan in memory, taken from the front of the workspace.
 RowPlan make_plan(const int32_t* index, int M, int L, unsigned char*& ws, hipStream_t st) {
   RowPlan p{index, nullptr, nullptr, M, L};
-  if (!plan_in_memory(M, index != nullptr)) return p;
   auto* off = reinterpret_cast<int32_t*>(ws);
   int32_t* perm = off + L + 2;
-  ws += plan_bytes(M, L, true);
+  ws += plan_bytes(M, L);
   hipLaunchKernelGGL(plan_rows_kernel, dim3(L + 1), dim3(1024), 0, st, index, M, L, off, perm);
   p.off = off;
   p.perm = perm;
@@ -121,10 +116,15 @@ void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, in
 template <bool TRANS>
 void run_expand(const float* h, int S, const half_t* w, const float* scaling, const RowPlan& plan, const half_t* base,
                 half_t* out, float* h_out, int C, int R, hipStream_t st) {
-  const dim3 grid(tile_slots(plan, 16), ceil_div(C, 512)), block(256);
+  const bool wide = plan.M / plan.L >= 64;
+  const dim3 grid(tile_slots(plan, wide ? 64 : 16), ceil_div(C, 512)), block(256);
 #define W4A16_EXPAND(F_, P_) \
-  hipLaunchKernelGGL((lora_expand_kernel<F_, P_, 1, TRANS>), grid, block, 0, st, h, S, w, scaling, plan, base, out, \
-                     h_out, C, R)
+  do { \
+    if (wide) hipLaunchKernelGGL((lora_expand_kernel<F_, P_, 4, TRANS>), grid, block, 0, st, h, S, w, scaling, plan, \
+                                 base, out, h_out, C, R); \
+    else hipLaunchKernelGGL((lora_expand_kernel<F_, P_, 1, TRANS>), grid, block, 0, st, h, S, w, scaling, plan, base, \
+                            out, h_out, C, R); \
+  } while (0)
   if (R <= 16) W4A16_EXPAND(1, true);
   else if (R <= 32) W4A16_EXPAND(1, false);
   else if (R <= 64) W4A16_EXPAND(2, false);
@@ -143,14 +143,31 @@ struct Kept {
   int gshift;
 };
 
+struct Frags {
+  half_t* frags;
+  int32_t* exps;
+};
+
+size_t frag_bytes(int slots, int R) {
+  return up256(static_cast<size_t>(slots) * ceil_div(R, 16) * 2048) + up256(static_cast<size_t>(slots) * sizeof(int32_t));
+}
+
+Frags take_frags(int slots, int R, unsigned char*& ws) {
+  Frags f{reinterpret_cast<half_t*>(ws),
+          reinterpret_cast<int32_t*>(ws + up256(static_cast<size_t>(slots) * ceil_div(R, 16) * 2048))};
+  ws += frag_bytes(slots, R);
+  return f;
+}
+
 template <bool Q8, bool CMAJOR>
-void run_outer(const Kept& k, const float* h, int S, const float* scaling, const RowPlan& plan, float* grad, int C,
-               int R, hipStream_t st) {
-#define W4A16_OUTER(NT_) \
-  hipLaunchKernelGGL((lora_outer_kernel<NT_, 8, Q8, CMAJOR>), dim3(ceil_div(C, 128), ceil_div(R, 16 * NT_), plan.L), \
-                     dim3(512), 0, st, k.x, k.codes, k.scales, k.gshift, h, S, scaling, plan, grad, C, R)
-  if (R <= 16) W4A16_OUTER(1);
-  else W4A16_OUTER(2);
+void run_outer(const Kept& k, const Frags& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
+               hipStream_t st) {
+#define W4A16_OUTER(NT_, W_, D_) \
+  hipLaunchKernelGGL((lora_outer_kernel<NT_, W_, D_, Q8, CMAJOR>), dim3(ceil_div(C, 128), ceil_div(R, 16 * NT_), plan.L), \
+                     dim3(64 * W_), 0, st, k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R)
+  if (R <= 16) W4A16_OUTER(1, 8, 3);
+  else if (R <= 32) W4A16_OUTER(2, 8, 2);
+  else W4A16_OUTER(4, 4, 2);
 #undef W4A16_OUTER
 }
 
@@ -168,9 +185,14 @@ struct BackwardArgs {
   void* stream;
 };
 
+int backward_slots(int M, int L, bool with_index) {
+  return with_index ? M / kSlotRows + L + 1 : ceil_div(M, kSlotRows);
+}
+
 size_t backward_bytes(int M, int N, int K, int R, int L, bool with_index) {
   (void)K;
-  return plan_bytes(M, L, with_index) + up256(sizeof(half_t) * L * R * N) + part_bytes(shrink_slices(M, N), M, R);
+  return (with_index ? plan_bytes(M, L) : 0) + up256(sizeof(half_t) * L * R * N) +
+         part_bytes(shrink_slices(M, N), M, R) + 2 * frag_bytes(backward_slots(M, L, with_index), R);
 }
 
 template <bool Q8>
@@ -186,19 +208,25 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, this call needs %zu", c.workspace_bytes, need);
   const auto st = static_cast<hipStream_t>(c.stream);
   auto* ws = static_cast<unsigned char*>(c.workspace);
-  const RowPlan plan = make_plan(c.index, c.M, c.L, ws, st);
+  RowPlan plan{nullptr, nullptr, nullptr, c.M, c.L};
+  if (c.index) plan = make_plan(c.index, c.M, c.L, ws, st);
   auto* bt = reinterpret_cast<half_t*>(ws);
   ws += up256(sizeof(half_t) * c.L * c.R * c.N);
   auto* g = reinterpret_cast<float*>(ws);
+  const int S = shrink_slices(c.M, c.N);
+  ws += part_bytes(S, c.M, c.R);
+  const int slots = backward_slots(c.M, c.L, c.index != nullptr);
+  const Frags fh = take_frags(slots, c.R, ws), fg = take_frags(slots, c.R, ws);
   const auto* dy = reinterpret_cast<const half_t*>(c.dy);
   const auto* a = reinterpret_cast<const half_t*>(c.a);
   const auto* b = reinterpret_cast<const half_t*>(c.b);
   hipLaunchKernelGGL(lora_transpose_kernel, dim3(ceil_div(c.N, kTransposeRows), c.L), dim3(256),
                      sizeof(half_t) * kTransposeRows * (c.R + 2), st, b, bt, c.N, c.R);
-  const int S = shrink_slices(c.M, c.N);
   run_shrink(dy, bt, plan, c.N, c.R, S, g, st);
-  run_outer<false, true>(Kept{dy, nullptr, nullptr, 0}, c.h, 1, c.scaling, plan, c.db, c.N, c.R, st);
-  run_outer<Q8, false>(kept, g, S, c.scaling, plan, c.da, c.K, c.R, st);
+  hipLaunchKernelGGL(lora_split_kernel, dim3(slots, 2), dim3(256), 0, st, SplitTask{c.h, 1, fh.frags, fh.exps},
+                     SplitTask{g, S, fg.frags, fg.exps}, plan, c.R);
+  run_outer<false, true>(Kept{dy, nullptr, nullptr, 0}, fh, c.scaling, plan, c.db, c.N, c.R, st);
+  run_outer<Q8, false>(kept, fg, c.scaling, plan, c.da, c.K, c.R, st);
   if (c.dx)
     run_expand<true>(g, S, a, c.scaling, plan, reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx),
                      nullptr, c.K, c.R, st);
@@ -212,7 +240,7 @@ using namespace w4a16;
 
 extern "C" size_t w4a16_lora_forward_workspace(int M, int N, int K, int R, int L, int with_index) {
   if (check_lora_shape(M, N, K, R, L) != W4A16_OK) return 0;
-  return plan_bytes(M, L, with_index != 0) + part_bytes(shrink_slices(M, K), M, R);
+  return (with_index && M > kInlineRows ? plan_bytes(M, L) : 0) + part_bytes(shrink_slices(M, K), M, R);
 }
 
 extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const uint16_t* a, const uint16_t* b,
@@ -230,7 +258,8 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, this call needs %zu", workspace_bytes, need);
   const auto st = static_cast<hipStream_t>(stream);
   auto* ws = static_cast<unsigned char*>(workspace);
-  const RowPlan plan = make_plan(index, M, L, ws, st);
+  RowPlan plan{index, nullptr, nullptr, M, L};
+  if (index && M > kInlineRows) plan = make_plan(index, M, L, ws, st);
   auto* part = reinterpret_cast<float*>(ws);
   const int S = shrink_slices(M, K);
   run_shrink(reinterpret_cast<const half_t*>(x), reinterpret_cast<const half_t*>(a), plan, K, R, S, part, st);

@@ -154,6 +154,7 @@ __device__ __forceinline__ void split_half(float h, int shift, half_t& hi, half_
 }
 
 constexpr int kSplitTop = 14;   // split operands are below 2^14
+constexpr int kNoExponent = -1000;   // of values that are all zero
 
 // --- shrink: out[s][m][j] = sum over the channels of slice s of x[m][c] w[i][j][c] -------
 //
@@ -258,15 +259,64 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_kernel(const half_t* __res
 // --- expand: out[m][c] = binary16(base[m][c] + s_i sum_j h[m][j] w_i[c][j]) ---------------
 //
 // h = sum of S slices [S][M][R].  TRANS == false: w [L][C][R]; TRANS: w [L][R][C].
-// The weights are the A operand (16 channels x 32 ranks), h the B operand (16 rows), so a
-// lane ends up with channels of one row; the channels are dealt to the MFMA rows so that
-// these are 8 consecutive ones and base and out move as 16-byte accesses.
+// A workgroup of 4 wavefronts takes 16 MT rows x 512 channels.  Each wavefront keeps the
+// weights of its 128 channels in registers (8 MFMA tiles of 16 channels as the A operand)
+// and walks the rows 16 at a time (the B operand, from LDS, where the workgroup put the
+// split h once); base of the next 16 rows is in flight meanwhile.  HBM-bound: 2 bytes
+// read and 2 written per element.
+// The channels are dealt to the MFMA rows so that a lane ends up with four runs of 8
+// consecutive channels of one row (run u at 32 u + 8 q), and base and out move as 16-byte
+// accesses, 64 bytes of a row per quarter wavefront.  !TRANS: MFMA row 4 q + r of tile t
+// is channel 32 (t / 2) + 8 q + 4 (t % 2) + r.  TRANS: lane (r, q) loads octet (r >> 2) + 4
+// (r & 3) of its 8 ranks and transposes the 8 x 8 block in registers; tile t has channel t
+// of every octet, and MFMA row 4 q + r is octet q + 4 r.
 // R <= 16 (PACKED): hi and lo share one MFMA, ranks 0..15 of hi in its first 16 slots and
 // of lo in the last 16, against the same weights.  Larger R: F fragments of 32 ranks,
 // one MFMA for hi and one for lo each.
 // base may equal out (every element is read and written by the same lane); rows without
 // an adapter are copied, bit for bit.  h_out (not NULL): the workgroups of the first
 // channels write the summed h.
+
+// The 8 x 8 block of binary16 values in v (one row per register quad) by columns: element
+// i of column t is element t of row i.
+__device__ __forceinline__ half8_t column8(const uint4 (&v)[8], int t) {
+  const uint32_t sel = (t & 1) ? 0x07060302u : 0x05040100u;
+  uint32_t d[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 &u0 = v[2 * i], &u1 = v[2 * i + 1];
+    const uint32_t e0 = t < 2 ? u0.x : t < 4 ? u0.y : t < 6 ? u0.z : u0.w;
+    const uint32_t e1 = t < 2 ? u1.x : t < 4 ? u1.y : t < 6 ? u1.z : u1.w;
+    d[i] = __builtin_amdgcn_perm(e1, e0, sel);
+  }
+  return __builtin_bit_cast(half8_t, (u32x4_t{d[0], d[1], d[2], d[3]}));
+}
+
+// Sum over the S slices of 8 consecutive floats, 4 slices in flight at a time.
+__device__ __forceinline__ void sum_slices8(const float* __restrict__ p, size_t slice, int S, float (&v)[8]) {
+  float4_t a = {}, b = {};
+  for (int s0 = 0; s0 < S; s0 += 4) {
+    float4_t x[4], y[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float* q = p + min(s0 + k, S - 1) * slice;
+      x[k] = *reinterpret_cast<const float4_t*>(q);
+      y[k] = *reinterpret_cast<const float4_t*>(q + 4);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s0 + k < S) {
+        a += x[k];
+        b += y[k];
+      }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[j] = a[j];
+    v[4 + j] = b[j];
+  }
+}
+
 template <int F, bool PACKED, int MT, bool TRANS>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restrict__ h, int S,
                                                           const half_t* __restrict__ w,
@@ -275,7 +325,10 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
                                                           int C, int R) {
   constexpr int T = 16 * MT;
   constexpr int kBlock = 512;   // channels per workgroup: 4 wavefronts x 128
+  constexpr int P = PACKED ? 1 : 2;
   __shared__ int32_t rows[T];
+  __shared__ float factor[T];
+  __shared__ half8_t split[MT][F][P][64];
   const Tile tile = find_tile<T>(plan, blockIdx.x, rows);
   if (tile.count == 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -296,147 +349,126 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
       for (int i = tid; i < tile.count * R; i += 256) h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
     return;
   }
-  const size_t slice = static_cast<size_t>(plan.M) * R;
-  if (h_out && blockIdx.y == 0)
-    for (int i = tid; i < tile.count * R; i += 256) {
-      const size_t at = static_cast<size_t>(rows[i / R]) * R + i % R;
-      float v = h[at];
-      for (int s = 1; s < S; ++s) v += h[s * slice + at];
-      h_out[at] = v;
-    }
+  const int nm = (tile.count + 15) >> 4;   // groups of 16 rows
   const int c0 = c_lo + wave * 128;
-  if (c0 >= C) return;
-
-  // Split h of this lane's rows (row lr of every 16) and its 8 ranks per fragment.
-  half8_t hi[MT][F], lo[MT][F];
-  float factor[MT];
   const int jq = PACKED ? (lq & 1) * 8 : lq * 8;
-  const float si = scaling ? scaling[tile.adapter] : 1.0f;
+
+  // base of 16 rows, from the first group before anything else
+  auto load_base = [&](int a, uint4 (&y)[4]) {
+    const bool in = base && 16 * a + lr < tile.count;
+    const half_t* p = base + static_cast<size_t>(rows[16 * a + lr]) * C;
 #pragma unroll
-  for (int a = 0; a < MT; ++a) {
-    const float* hr = h + static_cast<size_t>(rows[16 * a + lr]) * R;
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + 32 * u + 8 * lq;
+      y[u] = uint4{0, 0, 0, 0};
+      if (in && c < C) y[u] = *reinterpret_cast<const uint4*>(p + c);
+    }
+  };
+  uint4 y[4];
+  load_base(0, y);
+
+  // weights of 128 channels
+  half8_t wf[F][8];
+  const half_t* wl = w + static_cast<size_t>(tile.adapter) * R * C;
+  if (c0 < C) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int j0 = 32 * f + jq;
+      const bool in = j0 < R;
+      if constexpr (!TRANS) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          const int c = min(c0 + 32 * (t >> 1) + 8 * (lr >> 2) + 4 * (t & 1) + (lr & 3), C - 1);
+          const half8_t v = *reinterpret_cast<const half8_t*>(wl + static_cast<size_t>(c) * R + (in ? j0 : 0));
+          wf[f][t] = in ? v : half8_t{};
+        }
+      } else {
+        const int cc = min(c0 + 8 * ((lr >> 2) + 4 * (lr & 3)), C - 8);
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[i] = *reinterpret_cast<const uint4*>(wl + static_cast<size_t>(in ? j0 + i : i) * C + cc);
+          if (!in) v[i] = uint4{0, 0, 0, 0};
+        }
+#pragma unroll
+        for (int t = 0; t < 8; ++t) wf[f][t] = column8(v, t);
+      }
+    }
+  }
+
+  // split h: wavefront w takes rows 16 a + lr for a = w, w + 4, ...
+  const float si = scaling ? scaling[tile.adapter] : 1.0f;
+  const size_t slice = static_cast<size_t>(plan.M) * R;
+  for (int a = wave; a < nm; a += 4) {
+    const size_t row = static_cast<size_t>(rows[16 * a + lr]) * R;
     float v[F][8];
     float top = 0.0f;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       const int j0 = 32 * f + jq;
       const bool in = j0 < R;
-      const float* p = hr + (in ? j0 : 0);
-      float4_t p0 = *reinterpret_cast<const float4_t*>(p), p1 = *reinterpret_cast<const float4_t*>(p + 4);
-      for (int s = 1; s < S; ++s) {
-        p0 += *reinterpret_cast<const float4_t*>(p + s * slice);
-        p1 += *reinterpret_cast<const float4_t*>(p + s * slice + 4);
+      sum_slices8(h + row + (in ? j0 : 0), slice, S, v[f]);
+      if (h_out && blockIdx.y == 0 && in && 16 * a + lr < tile.count && (!PACKED || lq < 2)) {
+        *reinterpret_cast<float4_t*>(h_out + row + j0) = float4_t{v[f][0], v[f][1], v[f][2], v[f][3]};
+        *reinterpret_cast<float4_t*>(h_out + row + j0 + 4) = float4_t{v[f][4], v[f][5], v[f][6], v[f][7]};
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v[f][j] = in ? (j < 4 ? p0[j] : p1[j - 4]) : 0.0f;
+        v[f][j] = in ? v[f][j] : 0.0f;
         top = fmaxf(top, finite_magnitude(v[f][j]));
       }
     }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
     const int shift = kSplitTop - top_exponent(top);
-    factor[a] = __builtin_ldexpf(si, -shift);
+    if (lq == 0) factor[16 * a + lr] = __builtin_ldexpf(si, -shift);
 #pragma unroll
-    for (int f = 0; f < F; ++f)
+    for (int f = 0; f < F; ++f) {
+      half8_t hi, lo;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         half_t vh, vl;
         split_half(v[f][j], shift, vh, vl);
-        if constexpr (PACKED) {
-          hi[a][f][j] = lq < 2 ? vh : vl;
-        } else {
-          hi[a][f][j] = vh;
-          lo[a][f][j] = vl;
-        }
+        hi[j] = PACKED && lq >= 2 ? vl : vh;
+        lo[j] = vl;
       }
+      split[a][f][0][lane] = hi;
+      if constexpr (!PACKED) split[a][f][P - 1][lane] = lo;
+    }
   }
+  __syncthreads();
+  if (c0 >= C) return;
 
-  const half_t* wl = w + static_cast<size_t>(tile.adapter) * R * C;
-  auto store = [&](int a, int c, const float (&v)[8]) {
-    if (c >= C || 16 * a + lr >= tile.count) return;
-    const size_t at = static_cast<size_t>(rows[16 * a + lr]) * C + c;
-    half8_t y = {};
-    if (base) y = *reinterpret_cast<const half8_t*>(base + at);
-    half8_t o;
+  for (int a = 0; a < nm; ++a) {
+    uint4 next[4];
+    if (a + 1 < nm) load_base(a + 1, next);
+    float4_t acc[8] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = static_cast<half_t>(fmaf(v[i], factor[a], static_cast<float>(y[i])));
-    *reinterpret_cast<half8_t*>(out + at) = o;
-  };
-
-  if constexpr (!TRANS) {
-    // 32 channels at a time: MFMA row 4 q + r of tile t is channel 8 q + 4 t + r.
-    for (int cb = c0; cb < min(c0 + 128, C); cb += 32) {
-      half8_t wa[2][F];
+    for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int c = min(cb + 8 * (lr >> 2) + 4 * t + (lr & 3), C - 1);
+      for (int p = 0; p < P; ++p) {
+        const half8_t hf = split[a][f][p][lane];
 #pragma unroll
-        for (int f = 0; f < F; ++f) {
-          const int j0 = 32 * f + jq;
-          const half8_t v = *reinterpret_cast<const half8_t*>(wl + static_cast<size_t>(c) * R + (j0 < R ? j0 : 0));
-          wa[t][f] = j0 < R ? v : half8_t{};
-        }
+        for (int t = 0; t < 8; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[f][t], hf, acc[t], 0, 0, 0);
       }
+    if (16 * a + lr < tile.count) {
+      const float fa = factor[16 * a + lr];
+      half_t* po = out + static_cast<size_t>(rows[16 * a + lr]) * C;
 #pragma unroll
-      for (int a = 0; a < MT; ++a) {
-        float4_t acc[2] = {};
+      for (int u = 0; u < 4; ++u) {
+        const int c = c0 + 32 * u + 8 * lq;
+        const half8_t yv = __builtin_bit_cast(half8_t, y[u]);
+        half8_t o;
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int f = 0; f < F; ++f) {
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wa[t][f], hi[a][f], acc[t], 0, 0, 0);
-            if constexpr (!PACKED)
-              acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wa[t][f], lo[a][f], acc[t], 0, 0, 0);
-          }
-        const float v[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
-        store(a, cb + 8 * lq, v);
-      }
-    }
-  } else {
-    // 128 channels at once: lane (r, q) loads 8 channels (octet (r >> 2) + 4 (r & 3)) of
-    // its 8 ranks and transposes the 8 x 8 block in registers; tile t then has channel t
-    // of every octet, and MFMA row 4 q + r is octet q + 4 r.
-    const int oct = c0 + 8 * ((lr >> 2) + 4 * (lr & 3));
-    const int cc = min(oct, C - 8);
-    float4_t acc[MT][8] = {};
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      uint4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = 32 * f + jq + i;
-        v[i] = *reinterpret_cast<const uint4*>(wl + static_cast<size_t>(j < R ? j : 0) * C + cc);
-        if (j >= R) v[i] = uint4{0, 0, 0, 0};
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        const uint32_t sel = (t & 1) ? 0x07060302u : 0x05040100u;
-        uint32_t d[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 &u0 = v[2 * i], &u1 = v[2 * i + 1];
-          const uint32_t e0 = t < 2 ? u0.x : t < 4 ? u0.y : t < 6 ? u0.z : u0.w;
-          const uint32_t e1 = t < 2 ? u1.x : t < 4 ? u1.y : t < 6 ? u1.z : u1.w;
-          d[i] = __builtin_amdgcn_perm(e1, e0, sel);
+        for (int i = 0; i < 8; ++i) {
+          const float v = TRANS ? acc[i][u] : acc[2 * u + (i >> 2)][i & 3];
+          o[i] = static_cast<half_t>(fmaf(v, fa, static_cast<float>(yv[i])));
         }
-        const half8_t wa = __builtin_bit_cast(half8_t, (u32x4_t{d[0], d[1], d[2], d[3]}));
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wa, hi[a][f], acc[a][t], 0, 0, 0);
-          if constexpr (!PACKED)
-            acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wa, lo[a][f], acc[a][t], 0, 0, 0);
-        }
+        if (c < C) *reinterpret_cast<half8_t*>(po + c) = o;
       }
     }
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float v[8] = {acc[a][0][r], acc[a][1][r], acc[a][2][r], acc[a][3][r],
-                            acc[a][4][r], acc[a][5][r], acc[a][6][r], acc[a][7][r]};
-        store(a, c0 + 8 * (lq + 4 * r), v);
-      }
+    for (int u = 0; u < 4; ++u) y[u] = next[u];
   }
 }
 
@@ -467,185 +499,247 @@ __global__ __launch_bounds__(256) void lora_transpose_kernel(const half_t* __res
   }
 }
 
+// --- split: h (or the sum of S slices of g) as MFMA operands of the outer products --------
+//
+// One workgroup per slot of 32 rows of one adapter.  Fragment t of a slot holds ranks 16 t
+// .. + 15: lane (r, q) has rank 16 t + r of rows 8 q .. 8 q + 7, first the hi terms of all
+// lanes (1 KB), then the lo terms, in units of 2^exps[slot].  Rows past the slot's count
+// and ranks past R are zero.  Done once per call instead of by every workgroup of 128
+// channels that reads h.  blockIdx.y == 0 splits h (one slice), 1 splits g.
+struct SplitTask {
+  const float* h;
+  int S;
+  half_t* frags;     // [slots][NT][2][64][8]
+  int32_t* exps;     // [slots]
+};
+
+constexpr int kSlotRows = 32;
+
+__global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask t1, RowPlan plan, int R) {
+  __shared__ int32_t rows[kSlotRows];
+  __shared__ float tops[4];
+  const SplitTask task = blockIdx.y == 0 ? t0 : t1;
+  const int slot = blockIdx.x;
+  const Tile tile = find_tile<kSlotRows>(plan, slot, rows);
+  if (tile.count == 0 || tile.adapter == plan.L) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lr = lane & 15, lq = lane >> 4;
+  const int NT = (R + 15) >> 4;
+  const size_t slice = static_cast<size_t>(plan.M) * R;
+  float v[2][8];   // at most 8 fragments: two per wavefront
+  float top = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int j = 16 * (wave + 4 * k) + lr;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
+    if (16 * (wave + 4 * k) >= R) continue;
+    for (int s = 0; s < task.S; ++s)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[k][i] += task.h[s * slice + static_cast<size_t>(rows[8 * lq + i]) * R + min(j, R - 1)];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (j >= R || 8 * lq + i >= tile.count) v[k][i] = 0.0f;
+      top = fmaxf(top, finite_magnitude(v[k][i]));
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+  const int e = top > 0.0f ? top_exponent(top) - kSplitTop : kNoExponent;
+  if (tid == 0) task.exps[slot] = e;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int t = wave + 4 * k;
+    if (t >= NT) continue;
+    half8_t hi, lo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      half_t a, b;
+      split_half(v[k][i], e == kNoExponent ? 0 : -e, a, b);
+      hi[i] = a;
+      lo[i] = b;
+    }
+    half8_t* o = reinterpret_cast<half8_t*>(task.frags) + (static_cast<size_t>(slot) * NT + t) * 128 + lane;
+    o[0] = hi;
+    o[64] = lo;
+  }
+}
+
 // --- outer: grad_i[c][j] = s_i sum over the rows of adapter i of x[m][c] h[m][j] ----------
 //
-// A wavefront sums 128 channels x 16 NT ranks over chunks of 32 rows; the wavefronts of a
-// workgroup take turns along the rows and are added in LDS in a fixed order.  Lane (r, q)
+// A wavefront sums 128 channels x 16 NT ranks over slots of 32 rows; the wavefronts of a
+// workgroup take turns along the slots and are added in LDS in a fixed order.  Lane (r, q)
 // loads 8 channels (octet r) of its 8 rows (8 q ..) and transposes the 8 x 8 block in
-// registers, so that x goes from memory to the MFMA operand without LDS.
-// h is split with one power of two per wavefront that follows the largest value seen (as
-// the running maximum of a softmax does): a chunk that exceeds it rescales the sums.
+// registers, so that x goes from memory to the MFMA operand without LDS; the next slot's
+// rows are in flight meanwhile.  The split h comes as ready operands.
+// Every slot has a power of two of its own; the sums are kept in units of the largest seen
+// (as the running maximum of a softmax is): a larger one rescales the sums, a smaller one
+// the operands.  A slot's missing rows repeat its first one against zero operands.
 // Q8: x is an 8-bit checkpoint, expanded after the transpose (which then moves bytes).
 // CMAJOR: gradient [L][C][R] (channels are MFMA rows), else [L][R][C].
-template <int NT, int W, bool Q8, bool CMAJOR>
+template <int NT, bool Q8>
+struct OuterSlot {
+  uint4 v[8];              // 8 rows of 8 channels (Q8: the codes in x and y)
+  uint32_t s2[Q8 ? 4 : 1]; // scales of rows 2 i, 2 i + 1
+  half8_t h[NT][2];        // hi and lo operands
+  int e;                   // their power of two
+};
+
+// D slots in flight per wavefront.
+template <int NT, int W, int D, bool Q8, bool CMAJOR>
 __global__ __launch_bounds__(64 * W) void lora_outer_kernel(const half_t* __restrict__ x,
                                                             const uint8_t* __restrict__ codes,
                                                             const half_t* __restrict__ xs, int gshift,
-                                                            const float* __restrict__ h, int S,
+                                                            const half_t* __restrict__ frags,
+                                                            const int32_t* __restrict__ exps,
                                                             const float* __restrict__ scaling, RowPlan plan,
                                                             float* __restrict__ grad, int C, int R) {
-  __shared__ int32_t list[kInlineRows];
-  __shared__ float4_t red[(W / 2) * 8 * NT * 64];
+  __shared__ float4_t red[W * NT * 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int c0 = blockIdx.x * 128;
-  const int jb = blockIdx.y * 16 * NT;
+  const int t0 = blockIdx.y * NT;
   const int ad = blockIdx.z;
-  // rows of the adapter: positions [lo, hi) of `src` (NULL: the position is the row)
-  const int32_t* src = nullptr;
-  int lo = 0, hi = plan.M;
-  if (plan.index && plan.off) {
-    lo = plan.off[ad];
-    hi = plan.off[ad + 1];
-    src = plan.perm;
-  } else if (plan.index) {
-    const bool mine = lane < plan.M && row_class(plan.index[min(lane, plan.M - 1)], plan.L) == ad;
-    const uint64_t b = __ballot(mine);
-    if (tid < 64 && mine) list[__popcll(b & ((1ull << lane) - 1ull))] = lane;
-    __syncthreads();
-    src = list;
-    hi = __popcll(b);
-  }
+  const int NTT = (R + 15) >> 4;   // fragments per slot
+  // slots of the adapter: [first_slot, first_slot + n); positions lo .. hi - 1
+  const int lo = plan.index ? plan.off[ad] : 0;
+  const int hi = plan.index ? plan.off[ad + 1] : plan.M;
+  const int first_slot = plan.index ? lo / kSlotRows + ad : 0;
+  const int n = (hi - lo + kSlotRows - 1) / kSlotRows;
   const int cc = min(c0 + 8 * lr, C - 8);
   const int G = Q8 ? C >> gshift : 0;
-  const size_t slice = static_cast<size_t>(plan.M) * R;
-  float4_t acc[8][NT] = {};
-  int E = -1000;   // sums are in units of 2^E
-  float limit = 0.0f;
-  for (int p0 = lo + 32 * wave; p0 < hi; p0 += 32 * W) {
-    int row[8];
-    bool in[8];
+
+  // Rows of slot k (clamped to the last slot: a prefetch past it is not used), one slot
+  // ahead of the loads that need them.
+  int row[8];
+  auto find_rows = [&](int k) {
+    const int p0 = lo + min(k, n - 1) * kSlotRows;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int p = p0 + 8 * lq + i;
-      in[i] = p < hi;
-      const int pc = min(p, hi - 1);
-      row[i] = src ? src[pc] : pc;
+      const int p = p0 + 8 * lq + i < hi ? p0 + 8 * lq + i : p0;
+      row[i] = plan.index ? plan.perm[p] : p;
     }
-    uint4 v[8];
-    uint32_t s2[4] = {};
-    if constexpr (Q8) {
+  };
+  auto load = [&](int k, OuterSlot<NT, Q8>& o) {
+    const int slot = first_slot + min(k, n - 1);
+    o.e = exps[slot];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (Q8) {
         const uint2 c = *reinterpret_cast<const uint2*>(codes + static_cast<size_t>(row[i]) * C + cc);
-        v[i] = uint4{c.x, c.y, 0, 0};
-        const uint32_t sc = in[i] ? __builtin_bit_cast(uint16_t, xs[static_cast<size_t>(row[i]) * G + (cc >> gshift)]) : 0;
-        s2[i >> 1] |= sc << (16 * (i & 1));
-        if (!in[i]) v[i] = uint4{0x80808080u, 0x80808080u, 0, 0};
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(row[i]) * C + cc);
-        if (!in[i]) v[i] = uint4{0, 0, 0, 0};
+        o.v[i] = uint4{c.x, c.y, 0, 0};
+        const uint32_t sc = __builtin_bit_cast(uint16_t, xs[static_cast<size_t>(row[i]) * G + (cc >> gshift)]);
+        if (i & 1) o.s2[i >> 1] |= sc << 16;
+        else o.s2[i >> 1] = sc;
+      } else {
+        o.v[i] = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(row[i]) * C + cc);
       }
     }
-    float hv[NT][8];
-    float top = 0.0f;
+    const half8_t* f = reinterpret_cast<const half8_t*>(frags) + static_cast<size_t>(slot) * NTT * 128 + lane;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int j = min(jb + 16 * t + lr, R - 1);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float* p = h + static_cast<size_t>(row[i]) * R + j;
-        float f = *p;
-        for (int s = 1; s < S; ++s) f += p[s * slice];
-        hv[t][i] = in[i] ? f : 0.0f;
-        top = fmaxf(top, finite_magnitude(hv[t][i]));
-      }
+      const int tt = min(t0 + t, NTT - 1);   // past the last: computed, not stored
+      o.h[t][0] = f[tt * 128];
+      o.h[t][1] = f[tt * 128 + 64];
     }
-    if (__any(top > limit)) {
+  };
+
+  float4_t acc[8][NT] = {};
+  int E = kNoExponent;   // sums are in units of 2^E
+  auto add = [&](OuterSlot<NT, Q8>& o) {
+    const int e = __builtin_amdgcn_readfirstlane(o.e);
+    if (e > E) {
+      if (E != kNoExponent)
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-      const int En = __builtin_amdgcn_readfirstlane(top_exponent(top)) - kSplitTop;
+        for (int c = 0; c < 8; ++c)
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
+          for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[c][t][r] = __builtin_ldexpf(acc[c][t][r], E - En);
-      E = En;
-      limit = __builtin_ldexpf(1.0f, E + kSplitTop + 1);
-    }
-    half8_t hh[NT], hl[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        half_t a, b;
-        split_half(hv[t][i], -E, a, b);
-        hh[t][i] = a;
-        hl[t][i] = b;
-      }
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint32_t d[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 &u0 = v[2 * i], &u1 = v[2 * i + 1];
-        if constexpr (Q8) {
-          const uint32_t e0 = c < 4 ? u0.x : u0.y, e1 = c < 4 ? u1.x : u1.y;
-          // byte c % 4 of both rows into the low bytes of the two halves
-          const uint32_t sel = 0x0C000C00u | static_cast<uint32_t>(c & 3) | (static_cast<uint32_t>(4 + (c & 3)) << 16);
-          d[i] = act_value_pair(__builtin_amdgcn_perm(e1, e0, sel), as_h2(s2[i]));
-        } else {
-          const uint32_t e0 = c < 2 ? u0.x : c < 4 ? u0.y : c < 6 ? u0.z : u0.w;
-          const uint32_t e1 = c < 2 ? u1.x : c < 4 ? u1.y : c < 6 ? u1.z : u1.w;
-          d[i] = __builtin_amdgcn_perm(e1, e0, (c & 1) ? 0x07060302u : 0x05040100u);
-        }
-      }
-      const half8_t xf = __builtin_bit_cast(half8_t, (u32x4_t{d[0], d[1], d[2], d[3]}));
+            for (int r = 0; r < 4; ++r) acc[c][t][r] = __builtin_ldexpf(acc[c][t][r], E - e);
+      E = e;
+    } else if (e < E && e != kNoExponent) {
+      const half_t down = static_cast<half_t>(__builtin_ldexpf(1.0f, max(e - E, -40)));
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        if constexpr (CMAJOR) {
-          acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, hh[t], acc[c][t], 0, 0, 0);
-          acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, hl[t], acc[c][t], 0, 0, 0);
-        } else {
-          acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hh[t], xf, acc[c][t], 0, 0, 0);
-          acc[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(hl[t], xf, acc[c][t], 0, 0, 0);
+        o.h[t][0] *= down;
+        o.h[t][1] *= down;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      half8_t xf;
+      if constexpr (Q8) {
+        uint32_t d[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t e0 = c < 4 ? o.v[2 * i].x : o.v[2 * i].y, e1 = c < 4 ? o.v[2 * i + 1].x : o.v[2 * i + 1].y;
+          // byte c % 4 of both rows into the low bytes of the two halves
+          const uint32_t sel = 0x0C000C00u | static_cast<uint32_t>(c & 3) | (static_cast<uint32_t>(4 + (c & 3)) << 16);
+          d[i] = act_value_pair(__builtin_amdgcn_perm(e1, e0, sel), as_h2(o.s2[i]));
         }
+        xf = __builtin_bit_cast(half8_t, (u32x4_t{d[0], d[1], d[2], d[3]}));
+      } else {
+        xf = column8(o.v, c);
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          acc[c][t] = CMAJOR ? __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, o.h[t][p], acc[c][t], 0, 0, 0)
+                             : __builtin_amdgcn_mfma_f32_16x16x32_f16(o.h[t][p], xf, acc[c][t], 0, 0, 0);
+    }
+  };
+
+  if (n > 0) {
+    OuterSlot<NT, Q8> ring[D];
+    find_rows(wave);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      load(wave + d * W, ring[d]);
+      find_rows(wave + (d + 1) * W);
+    }
+    for (int k = wave; k < n; k += D * W) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        if (k + d * W >= n) break;
+        add(ring[d]);
+        load(k + (d + D) * W, ring[d]);
+        find_rows(k + (d + D + 1) * W);
       }
     }
   }
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[c][t][r] = __builtin_ldexpf(acc[c][t][r], E);
-#pragma unroll
-  for (int half = W / 2; half > 0; half >>= 1) {
-    if (wave >= half && wave < 2 * half)
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) red[((wave - half) * 8 * NT + c * NT + t) * 64 + lane] = acc[c][t];
-    __syncthreads();
-    if (wave < half)
-#pragma unroll
-      for (int c = 0; c < 8; ++c)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[c][t] += red[(wave * 8 * NT + c * NT + t) * 64 + lane];
-    __syncthreads();
-  }
-  if (wave != 0) return;
+
+  // Sum over the wavefronts, one channel fragment at a time, in units of 1.
   const float si = scaling ? scaling[ad] : 1.0f;
   float* g = grad + static_cast<size_t>(ad) * R * C;
 #pragma unroll
-  for (int c = 0; c < 8; ++c)
+  for (int c = 0; c < 8; ++c) {
+    __syncthreads();
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t) {
+      float4_t v = acc[c][t];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] = __builtin_ldexpf(v[r], E);
+      red[(wave * NT + t) * 64 + lane] = v;
+    }
+    __syncthreads();
+    for (int i = tid; i < NT * 64; i += 64 * W) {
+      float4_t v = red[i];
+      for (int w = 1; w < W; ++w) v += red[w * NT * 64 + i];
+      const int j0 = 16 * (t0 + i / 64);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        if constexpr (CMAJOR) {
-          const int ch = c0 + 8 * (4 * lq + r) + c, j = jb + 16 * t + lr;
-          if (ch < C && j < R) g[static_cast<size_t>(ch) * R + j] = si * acc[c][t][r];
-        } else {
-          const int ch = c0 + 8 * lr + c, j = jb + 16 * t + 4 * lq + r;
-          if (ch < C && j < R) g[static_cast<size_t>(j) * C + ch] = si * acc[c][t][r];
-        }
+        const int ch = CMAJOR ? c0 + 8 * (4 * ((i & 63) >> 4) + r) + c : c0 + 8 * (i & 15) + c;
+        const int j = CMAJOR ? j0 + (i & 15) : j0 + 4 * ((i & 63) >> 4) + r;
+        if (ch < C && j < R) g[CMAJOR ? static_cast<size_t>(ch) * R + j : static_cast<size_t>(j) * C + ch] = si * v[r];
       }
+    }
+  }
 }
 
 }  // namespace w4a16
