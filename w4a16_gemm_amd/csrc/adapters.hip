@@ -72,65 +72,140 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 
 int ceil_div(int a, int b) { return a / b + (a % b != 0); }
 
-// --- row plan -----------------------------------------------------------------------
+// --- workspace ----------------------------------------------------------------------
 
-size_t plan_bytes(int M, int L) { return up256((static_cast<size_t>(L) + 2 + M) * sizeof(int32_t)); }
+// Hands out 256-byte aligned pieces of the workspace; with base NULL it only adds them up,
+// which is how the _workspace functions know the size.
+struct Carver {
+  unsigned char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(size_t count) {
+    T* p = base ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += up256(count * sizeof(T));
+    return p;
+  }
+};
 
-// A plan in memory, taken from the front of the workspace.
-RowPlan make_plan(const int32_t* index, int M, int L, unsigned char*& ws, hipStream_t st) {
+struct ByRow {
+  half_t* frags;
+  float* factors;
+};
+
+struct ByRank {
+  half_t* frags;
+  int32_t* exps;
+};
+
+ByRow take_by_row(Carver& ws, int slots, int R) {
+  half_t* f = ws.take<half_t>(static_cast<size_t>(slots) * 2 * row_frags(R) * 512);
+  return {f, ws.take<float>(static_cast<size_t>(slots) * kSlotRows)};
+}
+
+ByRank take_by_rank(Carver& ws, int slots, int R) {
+  half_t* f = ws.take<half_t>(static_cast<size_t>(slots) * ceil_div(R, 16) * 1024);
+  return {f, ws.take<int32_t>(slots)};
+}
+
+SlotTable take_table(Carver& ws, int slots) {
+  int2* meta = ws.take<int2>(slots);
+  return {meta, ws.take<int32_t>(static_cast<size_t>(slots) * kSlotRows)};
+}
+
+// Memory of a row plan; without an index the rows need none.
+RowPlan take_plan(Carver& ws, const int32_t* index, bool with_index, int M, int L) {
   RowPlan p{index, nullptr, nullptr, M, L};
-  auto* off = reinterpret_cast<int32_t*>(ws);
-  int32_t* perm = off + L + 2;
-  ws += plan_bytes(M, L);
-  hipLaunchKernelGGL(plan_rows_kernel, dim3(L + 1), dim3(1024), 0, st, index, M, L, off, perm);
-  p.off = off;
-  p.perm = perm;
+  if (with_index) {
+    p.off = ws.take<int32_t>(static_cast<size_t>(L) + 2);
+    p.perm = ws.take<int32_t>(M);
+  }
   return p;
+}
+
+void run_plan(const RowPlan& p, hipStream_t st) {
+  if (p.index && p.off)
+    hipLaunchKernelGGL(plan_rows_kernel, dim3(p.L + 1), dim3(1024), 0, st, p.index, p.M, p.L,
+                       const_cast<int32_t*>(p.off), const_cast<int32_t*>(p.perm));
+}
+
+int plan_slots(int M, int L, bool with_index) {
+  return with_index ? M / kSlotRows + L + 1 : ceil_div(M, kSlotRows);
 }
 
 // --- shrink -------------------------------------------------------------------------
 
-// Slices of the long axis: enough workgroups to fill the GPU at few rows, at least 512
-// channels (16 steps) per slice.
-int shrink_slices(int M, int C) {
-  const int tiles = ceil_div(M, 16);
-  const int want = std::max(1, 256 / tiles);
-  return std::max(1, std::min({want, C / 512, 16}));
+// Rows per tile (in 16s) of a shrink: one for few rows per adapter, else enough that a
+// tile's reads of w (16 NT ranks) do not outweigh its reads of x.
+int shrink_mt(int M, int L, int R) { return M / L < 64 ? 1 : R <= 32 ? 2 : 4; }
+
+// Slices of the long axis: about one workgroup of 8 wavefronts per compute unit, at least
+// 512 channels (two steps per wavefront) per slice.
+int shrink_slices(int M, int L, int R, int C) {
+  const int tiles = ceil_div(M, 16 * shrink_mt(M, L, R));
+  return std::max(1, std::min({ceil_div(256, tiles), C / 512, 16}));
 }
 
-size_t part_bytes(int S, int M, int R) { return up256(sizeof(float) * S * M * R); }
-
 void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, int R, int S, float* out, hipStream_t st) {
-  const dim3 grid(tile_slots(plan, 16), S), block(256);
-  switch ((R + 15) / 16) {
-#define W4A16_SHRINK(NT_) \
-    case NT_: hipLaunchKernelGGL((lora_shrink_kernel<NT_, 1, 4>), grid, block, 0, st, x, w, plan, C, R, out); break;
-    W4A16_SHRINK(1) W4A16_SHRINK(2) W4A16_SHRINK(3) W4A16_SHRINK(4)
-    W4A16_SHRINK(5) W4A16_SHRINK(6) W4A16_SHRINK(7) W4A16_SHRINK(8)
-#undef W4A16_SHRINK
+  const int mt = shrink_mt(plan.M, plan.L, R);
+  const dim3 grid(tile_slots(plan, 16 * mt) * S), block(512);
+#define W4A16_SHRINK(NT_, MT_, D_) \
+  hipLaunchKernelGGL((lora_shrink_kernel<NT_, MT_, 8, D_>), grid, block, 0, st, x, w, plan, C, R, S, out)
+  const int nt = ceil_div(R, 16);
+  if (mt == 1) {
+    if (nt == 1) W4A16_SHRINK(1, 1, 4);
+    else if (nt == 2) W4A16_SHRINK(2, 1, 4);
+    else if (nt <= 4) W4A16_SHRINK(4, 1, 4);
+    else W4A16_SHRINK(8, 1, 2);
+  } else {
+    if (nt == 1) W4A16_SHRINK(1, 2, 4);
+    else if (nt == 2) W4A16_SHRINK(2, 2, 4);
+    else if (nt <= 4) W4A16_SHRINK(4, 4, 4);
+    else W4A16_SHRINK(8, 4, 2);
   }
+#undef W4A16_SHRINK
 }
 
 // --- expand -------------------------------------------------------------------------
 
-template <bool TRANS>
+// From this many rows on the expand takes ready operands (one launch more).
+constexpr int kStreamRows = 256;
+
 void run_expand(const float* h, int S, const half_t* w, const float* scaling, const RowPlan& plan, const half_t* base,
                 half_t* out, float* h_out, int C, int R, hipStream_t st) {
-  const bool wide = plan.M / plan.L >= 64;
-  const dim3 grid(tile_slots(plan, wide ? 64 : 16), ceil_div(C, 512)), block(256);
+  const dim3 grid(tile_slots(plan, 16), ceil_div(C, 512)), block(256);
 #define W4A16_EXPAND(F_, P_) \
-  do { \
-    if (wide) hipLaunchKernelGGL((lora_expand_kernel<F_, P_, 4, TRANS>), grid, block, 0, st, h, S, w, scaling, plan, \
-                                 base, out, h_out, C, R); \
-    else hipLaunchKernelGGL((lora_expand_kernel<F_, P_, 1, TRANS>), grid, block, 0, st, h, S, w, scaling, plan, base, \
-                            out, h_out, C, R); \
-  } while (0)
+  hipLaunchKernelGGL((lora_expand_kernel<F_, P_>), grid, block, 0, st, h, S, w, scaling, plan, base, out, h_out, C, R)
   if (R <= 16) W4A16_EXPAND(1, true);
   else if (R <= 32) W4A16_EXPAND(1, false);
   else if (R <= 64) W4A16_EXPAND(2, false);
   else if (R <= 96) W4A16_EXPAND(3, false);
   else W4A16_EXPAND(4, false);
 #undef W4A16_EXPAND
+}
+
+template <bool TRANS, bool BASE>
+void run_stream_base(const ByRow& h, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C, int R,
+                     int L, int slots, hipStream_t st) {
+  const int blocks = ceil_div(C, 512);
+  // about 1024 workgroups (two rounds of two per compute unit), 64 slots at most
+  const int group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, static_cast<int64_t>(slots) * blocks / 1024)));
+  const dim3 grid(blocks * ceil_div(slots, group)), block(256);
+#define W4A16_STREAM(F_, P_, D_) \
+  hipLaunchKernelGGL((lora_stream_kernel<F_, P_, TRANS, BASE, D_>), grid, block, 0, st, h.frags, h.factors, table, w, base, \
+                     out, C, R, L, slots, group)
+  if (R <= 16) W4A16_STREAM(1, true, 3);
+  else if (R <= 32) W4A16_STREAM(1, false, 3);
+  else if (R <= 64) W4A16_STREAM(2, false, 2);
+  else if (R <= 96) W4A16_STREAM(3, false, 2);
+  else W4A16_STREAM(4, false, 1);
+#undef W4A16_STREAM
+}
+
+template <bool TRANS>
+void run_stream(const ByRow& h, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C, int R,
+                int L, int slots, hipStream_t st) {
+  if (base) run_stream_base<TRANS, true>(h, table, w, base, out, C, R, L, slots, st);
+  else if constexpr (TRANS) run_stream_base<TRANS, false>(h, table, w, base, out, C, R, L, slots, st);
 }
 
 // --- outer --------------------------------------------------------------------------
@@ -143,32 +218,73 @@ struct Kept {
   int gshift;
 };
 
-struct Frags {
-  half_t* frags;
-  int32_t* exps;
-};
-
-size_t frag_bytes(int slots, int R) {
-  return up256(static_cast<size_t>(slots) * ceil_div(R, 16) * 2048) + up256(static_cast<size_t>(slots) * sizeof(int32_t));
-}
-
-Frags take_frags(int slots, int R, unsigned char*& ws) {
-  Frags f{reinterpret_cast<half_t*>(ws),
-          reinterpret_cast<int32_t*>(ws + up256(static_cast<size_t>(slots) * ceil_div(R, 16) * 2048))};
-  ws += frag_bytes(slots, R);
-  return f;
-}
-
 template <bool Q8, bool CMAJOR>
-void run_outer(const Kept& k, const Frags& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
+void run_outer(const Kept& k, const ByRank& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
                hipStream_t st) {
 #define W4A16_OUTER(NT_, W_, D_) \
-  hipLaunchKernelGGL((lora_outer_kernel<NT_, W_, D_, Q8, CMAJOR>), dim3(ceil_div(C, 128), ceil_div(R, 16 * NT_), plan.L), \
-                     dim3(64 * W_), 0, st, k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R)
+  hipLaunchKernelGGL((lora_outer_kernel<NT_, W_, D_, Q8, CMAJOR>), \
+                     dim3(ceil_div(C, 128), ceil_div(R, 16 * NT_), plan.L), dim3(64 * W_), 0, st, k.x, k.codes, k.scales, \
+                     k.gshift, f.frags, f.exps, scaling, plan, grad, C, R)
   if (R <= 16) W4A16_OUTER(1, 8, 3);
   else if (R <= 32) W4A16_OUTER(2, 8, 2);
   else W4A16_OUTER(4, 4, 2);
 #undef W4A16_OUTER
+}
+
+// --- forward ------------------------------------------------------------------------
+
+struct ForwardMemory {
+  RowPlan plan;
+  float* part;       // [S][M][R]
+  int S, slots;
+  bool stream;
+  ByRow h;
+  SlotTable table;
+};
+
+ForwardMemory forward_memory(Carver& ws, const int32_t* index, bool with_index, int M, int K, int R, int L) {
+  ForwardMemory m{};
+  m.stream = M >= kStreamRows;
+  m.plan = take_plan(ws, index, with_index && M > kInlineRows, M, L);
+  m.S = shrink_slices(M, L, R, K);
+  m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
+  if (m.stream) {
+    m.slots = plan_slots(M, L, with_index);
+    m.h = take_by_row(ws, m.slots, R);
+    m.table = take_table(ws, m.slots);
+  }
+  return m;
+}
+
+// --- backward -----------------------------------------------------------------------
+
+struct BackwardMemory {
+  RowPlan plan;
+  half_t* bt;        // [L][R][N]
+  float* part;       // g: [S][M][R]
+  int S, slots;
+  ByRank h, g;
+  ByRow g_rows;
+  SlotTable table;
+};
+
+BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index, int M, int N, int R, int L) {
+  BackwardMemory m{};
+  m.plan = take_plan(ws, index, with_index, M, L);
+  m.bt = ws.take<half_t>(static_cast<size_t>(L) * R * N);
+  m.S = shrink_slices(M, L, R, N);
+  m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
+  m.slots = plan_slots(M, L, with_index);
+  m.h = take_by_rank(ws, m.slots, R);
+  m.g = take_by_rank(ws, m.slots, R);
+  m.g_rows = take_by_row(ws, m.slots, R);
+  m.table = take_table(ws, m.slots);
+  return m;
+}
+
+int check_workspace(size_t have, size_t need) {
+  if (have >= need) return W4A16_OK;
+  return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, this call needs %zu", have, need);
 }
 
 struct BackwardArgs {
@@ -185,16 +301,6 @@ struct BackwardArgs {
   void* stream;
 };
 
-int backward_slots(int M, int L, bool with_index) {
-  return with_index ? M / kSlotRows + L + 1 : ceil_div(M, kSlotRows);
-}
-
-size_t backward_bytes(int M, int N, int K, int R, int L, bool with_index) {
-  (void)K;
-  return (with_index ? plan_bytes(M, L) : 0) + up256(sizeof(half_t) * L * R * N) +
-         part_bytes(shrink_slices(M, N), M, R) + 2 * frag_bytes(backward_slots(M, L, with_index), R);
-}
-
 template <bool Q8>
 int run_backward(const BackwardArgs& c, const Kept& kept) {
   const Buffer bufs[] = {{c.dy, 16, true, "dy"},       {c.a, 16, true, "a"},     {c.b, 16, true, "b"},
@@ -203,33 +309,26 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
                          {c.scaling, 4, false, "scaling"}, {c.workspace, 16, true, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   if (c.dx0 && !c.dx) return fail(W4A16_ERR_INVALID_ARG, "dx0 is given without dx");
-  const size_t need = backward_bytes(c.M, c.N, c.K, c.R, c.L, c.index != nullptr);
-  if (c.workspace_bytes < need)
-    return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, this call needs %zu", c.workspace_bytes, need);
+  Carver size{nullptr}, ws{static_cast<unsigned char*>(c.workspace)};
+  backward_memory(size, nullptr, c.index != nullptr, c.M, c.N, c.R, c.L);
+  if (int rc = check_workspace(c.workspace_bytes, size.used)) return rc;
+  const BackwardMemory m = backward_memory(ws, c.index, c.index != nullptr, c.M, c.N, c.R, c.L);
   const auto st = static_cast<hipStream_t>(c.stream);
-  auto* ws = static_cast<unsigned char*>(c.workspace);
-  RowPlan plan{nullptr, nullptr, nullptr, c.M, c.L};
-  if (c.index) plan = make_plan(c.index, c.M, c.L, ws, st);
-  auto* bt = reinterpret_cast<half_t*>(ws);
-  ws += up256(sizeof(half_t) * c.L * c.R * c.N);
-  auto* g = reinterpret_cast<float*>(ws);
-  const int S = shrink_slices(c.M, c.N);
-  ws += part_bytes(S, c.M, c.R);
-  const int slots = backward_slots(c.M, c.L, c.index != nullptr);
-  const Frags fh = take_frags(slots, c.R, ws), fg = take_frags(slots, c.R, ws);
   const auto* dy = reinterpret_cast<const half_t*>(c.dy);
-  const auto* a = reinterpret_cast<const half_t*>(c.a);
-  const auto* b = reinterpret_cast<const half_t*>(c.b);
+  run_plan(m.plan, st);
   hipLaunchKernelGGL(lora_transpose_kernel, dim3(ceil_div(c.N, kTransposeRows), c.L), dim3(256),
-                     sizeof(half_t) * kTransposeRows * (c.R + 2), st, b, bt, c.N, c.R);
-  run_shrink(dy, bt, plan, c.N, c.R, S, g, st);
-  hipLaunchKernelGGL(lora_split_kernel, dim3(slots, 2), dim3(256), 0, st, SplitTask{c.h, 1, fh.frags, fh.exps},
-                     SplitTask{g, S, fg.frags, fg.exps}, plan, c.R);
-  run_outer<false, true>(Kept{dy, nullptr, nullptr, 0}, fh, c.scaling, plan, c.db, c.N, c.R, st);
-  run_outer<Q8, false>(kept, fg, c.scaling, plan, c.da, c.K, c.R, st);
+                     sizeof(half_t) * kTransposeRows * (c.R + 2), st, reinterpret_cast<const half_t*>(c.b), m.bt, c.N, c.R);
+  run_shrink(dy, m.bt, m.plan, c.N, c.R, m.S, m.part, st);
+  const SplitTask th{c.h, 1, kByRank, m.h.frags, m.h.exps, nullptr, nullptr};
+  const SplitTask tg{m.part, m.S, kByRank, m.g.frags, m.g.exps, nullptr, nullptr};
+  const SplitTask tr{m.part, m.S, kByRow, m.g_rows.frags, nullptr, m.g_rows.factors, nullptr};
+  hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, c.dx ? 3 : 2), dim3(256), 0, st, th, tg, tr, c.scaling, m.table,
+                     m.plan, c.R);
+  run_outer<false, true>(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, c.db, c.N, c.R, st);
+  run_outer<Q8, false>(kept, m.g, c.scaling, m.plan, c.da, c.K, c.R, st);
   if (c.dx)
-    run_expand<true>(g, S, a, c.scaling, plan, reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx),
-                     nullptr, c.K, c.R, st);
+    run_stream<true>(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a), reinterpret_cast<const half_t*>(c.dx0),
+                     reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L, m.slots, st);
   return check_launch("lora backward launch");
 }
 
@@ -240,7 +339,9 @@ using namespace w4a16;
 
 extern "C" size_t w4a16_lora_forward_workspace(int M, int N, int K, int R, int L, int with_index) {
   if (check_lora_shape(M, N, K, R, L) != W4A16_OK) return 0;
-  return (with_index && M > kInlineRows ? plan_bytes(M, L) : 0) + part_bytes(shrink_slices(M, K), M, R);
+  Carver size{nullptr};
+  forward_memory(size, nullptr, with_index != 0, M, K, R, L);
+  return size.used;
 }
 
 extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const uint16_t* a, const uint16_t* b,
@@ -253,24 +354,31 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
                          {index, 4, false, "index"},   {scaling, 4, false, "scaling"},
                          {workspace, 16, true, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
-  const size_t need = w4a16_lora_forward_workspace(M, N, K, R, L, index != nullptr);
-  if (workspace_bytes < need)
-    return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, this call needs %zu", workspace_bytes, need);
+  Carver size{nullptr}, ws{static_cast<unsigned char*>(workspace)};
+  forward_memory(size, nullptr, index != nullptr, M, K, R, L);
+  if (int rc = check_workspace(workspace_bytes, size.used)) return rc;
+  const ForwardMemory m = forward_memory(ws, index, index != nullptr, M, K, R, L);
   const auto st = static_cast<hipStream_t>(stream);
-  auto* ws = static_cast<unsigned char*>(workspace);
-  RowPlan plan{index, nullptr, nullptr, M, L};
-  if (index && M > kInlineRows) plan = make_plan(index, M, L, ws, st);
-  auto* part = reinterpret_cast<float*>(ws);
-  const int S = shrink_slices(M, K);
-  run_shrink(reinterpret_cast<const half_t*>(x), reinterpret_cast<const half_t*>(a), plan, K, R, S, part, st);
-  run_expand<false>(part, S, reinterpret_cast<const half_t*>(b), scaling, plan, reinterpret_cast<const half_t*>(y),
-                    reinterpret_cast<half_t*>(out), h, N, R, st);
+  const auto* yh = reinterpret_cast<const half_t*>(y);
+  const auto* bh = reinterpret_cast<const half_t*>(b);
+  auto* oh = reinterpret_cast<half_t*>(out);
+  run_plan(m.plan, st);
+  run_shrink(reinterpret_cast<const half_t*>(x), reinterpret_cast<const half_t*>(a), m.plan, K, R, m.S, m.part, st);
+  if (m.stream) {
+    const SplitTask t{m.part, m.S, kByRow, m.h.frags, nullptr, m.h.factors, h};
+    hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(256), 0, st, t, t, t, scaling, m.table, m.plan, R);
+    run_stream<false>(m.h, m.table, bh, yh, oh, N, R, L, m.slots, st);
+  } else {
+    run_expand(m.part, m.S, bh, scaling, m.plan, yh, oh, h, N, R, st);
+  }
   return check_launch("lora forward launch");
 }
 
 extern "C" size_t w4a16_lora_backward_workspace(int M, int N, int K, int R, int L, int with_index) {
   if (check_lora_shape(M, N, K, R, L) != W4A16_OK) return 0;
-  return backward_bytes(M, N, K, R, L, with_index != 0);
+  Carver size{nullptr};
+  backward_memory(size, nullptr, with_index != 0, M, N, R, L);
+  return size.used;
 }
 
 extern "C" int w4a16_lora_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* a, const uint16_t* b,

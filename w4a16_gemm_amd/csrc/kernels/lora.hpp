@@ -41,35 +41,54 @@ __device__ __forceinline__ int row_class(int i, int L) { return i >= 0 && i < L 
 
 // Stable grouping by class: workgroup c counts the rows of smaller classes, then places
 // its own rows in order.  No atomics, so the order (and with it every sum) is fixed.
+constexpr int kPlanRows = 8;   // rows per thread read at once (8192 per workgroup)
+
 __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ index, int M, int L,
                                                          int32_t* __restrict__ off, int32_t* __restrict__ perm) {
-  __shared__ int part[16];
+  __shared__ int part[2][16];
   const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int cls[kPlanRows];
+  auto load = [&](int m0) {   // rows past M: a class above all
+#pragma unroll
+    for (int k = 0; k < kPlanRows; ++k) {
+      const int m = m0 + 1024 * k + tid;
+      cls[k] = m < M ? row_class(index[m], L) : L + 1;
+    }
+  };
   int below = 0;
-  for (int m = tid; m < M; m += 1024) below += row_class(index[m], L) < c ? 1 : 0;
+  for (int m0 = 0; m0 < M; m0 += 1024 * kPlanRows) {
+    load(m0);
+#pragma unroll
+    for (int k = 0; k < kPlanRows; ++k) below += cls[k] < c ? 1 : 0;
+  }
+#pragma unroll
   for (int d = 1; d < 64; d <<= 1) below += __shfl_xor(below, d);
-  if (lane == 0) part[wave] = below;
+  if (lane == 0) part[1][wave] = below;
   __syncthreads();
   int at = 0;
-  for (int w = 0; w < 16; ++w) at += part[w];
+  for (int w = 0; w < 16; ++w) at += part[1][w];
   if (tid == 0) {
     off[c] = at;
     if (c == L) off[L + 1] = M;
   }
-  for (int m0 = 0; m0 < M; m0 += 1024) {
-    const int m = m0 + tid;
-    const bool mine = m < M && row_class(index[m], L) == c;
-    const uint64_t b = __ballot(mine);
-    __syncthreads();   // the previous round's (first: the counts') reads of part are done
-    if (lane == 0) part[wave] = __popcll(b);
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < 16; ++w) {
-      before += w < wave ? part[w] : 0;
-      total += part[w];
+  __syncthreads();
+  for (int m0 = 0; m0 < M; m0 += 1024 * kPlanRows) {
+    if (M > 1024 * kPlanRows) load(m0);
+#pragma unroll
+    for (int k = 0; k < kPlanRows; ++k) {
+      if (m0 + 1024 * k >= M) break;
+      const bool mine = cls[k] == c;
+      const uint64_t b = __ballot(mine);
+      if (lane == 0) part[k & 1][wave] = __popcll(b);
+      __syncthreads();   // the other half of part is free again once everyone is here
+      int before = 0, total = 0;
+      for (int w = 0; w < 16; ++w) {
+        before += w < wave ? part[k & 1][w] : 0;
+        total += part[k & 1][w];
+      }
+      if (mine) perm[at + before + __popcll(b & ((1ull << lane) - 1ull))] = m0 + 1024 * k + tid;
+      at += total;
     }
-    if (mine) perm[at + before + __popcll(b & ((1ull << lane) - 1ull))] = m;
-    at += total;
   }
 }
 
@@ -160,18 +179,25 @@ constexpr int kNoExponent = -1000;   // of values that are all zero
 //
 // x [M][C], w [L][R][C], C % 8 == 0.  A wavefront holds 16 MT rows x 16 NT ranks of sums
 // and walks steps of 32 channels, both operands as they lie in memory (lane (r, q): row r,
-// channels 8 q .. 8 q + 7 of the step).  The wavefronts of a workgroup take turns along
-// the slice; their sums are added in LDS in a fixed order.  A row's result depends on its
-// own x alone, so the rows repeated to fill a tile are computed and not stored.
-template <int NT, int MT, int W>
+// channels 8 q .. 8 q + 7 of the step), D steps in flight.  The W wavefronts of a workgroup
+// take turns along the slice; their sums are added in LDS in a fixed order.  A row's result
+// depends on its own x alone, so the rows repeated to fill a tile are computed and not
+// stored.
+// Every tile reads all of w: with 16 MT >= R that is no more than x, and the slices are
+// dealt to neighbouring workgroups, so that an XCD's L2 holds the w of few slices.
+template <int NT, int MT>
+struct ShrinkStep {
+  half8_t x[MT], w[NT];
+};
+
+template <int NT, int MT, int W, int D>
 __global__ __launch_bounds__(64 * W) void lora_shrink_kernel(const half_t* __restrict__ x, const half_t* __restrict__ w,
-                                                             RowPlan plan, int C, int R, float* __restrict__ out) {
+                                                             RowPlan plan, int C, int R, int S, float* __restrict__ out) {
   constexpr int T = 16 * MT;
-  constexpr int U = NT * MT >= 8 ? 2 : 4;   // steps whose loads are in flight together
   __shared__ int32_t rows[T];
-  __shared__ float4_t red[(W / 2 > 0 ? W / 2 : 1) * MT * NT * 64];
-  const int S = gridDim.y, s = blockIdx.y;
-  const Tile tile = find_tile<T>(plan, blockIdx.x, rows);
+  __shared__ float4_t red[W / 2 * MT * NT * 64];
+  const int s = blockIdx.x % S;
+  const Tile tile = find_tile<T>(plan, blockIdx.x / S, rows);
   if (tile.count == 0) return;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -189,46 +215,58 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_kernel(const half_t* __res
   for (int t = 0; t < NT; ++t)
     wr[t] = w + (static_cast<size_t>(tile.adapter) * R + min(16 * t + lr, R - 1)) * C;
   float4_t acc[MT][NT] = {};
+  const int full = C >> 5;   // steps of 32 channels
   const int steps = (C + 31) >> 5;
   const int b = static_cast<int>(static_cast<int64_t>(steps) * s / S);
   const int e = static_cast<int>(static_cast<int64_t>(steps) * (s + 1) / S);
-  for (int st = b + wave * U; st < e; st += W * U) {
-    half8_t xa[U][MT], wb[U][NT];
-    if (st + U <= e && (st + U) * 32 <= C) {
+  // Wavefront w takes pairs of steps w, w + W, ... of the slice, so that it reads 128
+  // consecutive bytes of a row.  Loads past the slice are clamped into it, not used.
+  auto step_of = [&](int k) { return b + 2 * (wave + (k >> 1) * W) + (k & 1); };
+  auto load = [&](int k, ShrinkStep<NT, MT>& o) {
+    const int c = min(min(step_of(k), e - 1) * 32 + 8 * lq, C - 8);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = (st + u) * 32 + 8 * lq;
+    for (int a = 0; a < MT; ++a) o.x[a] = *reinterpret_cast<const half8_t*>(xr[a] + c);
 #pragma unroll
-        for (int a = 0; a < MT; ++a) xa[u][a] = *reinterpret_cast<const half8_t*>(xr[a] + c);
+    for (int t = 0; t < NT; ++t) o.w[t] = *reinterpret_cast<const half8_t*>(wr[t] + c);
+  };
+  auto add = [&](int k, ShrinkStep<NT, MT>& o) {
+    const int st = step_of(k);
+    if (st >= full) {   // the last, partial step: channels past C are zero on both sides
+      const bool in = st * 32 + 8 * lq < C;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) wb[u][t] = *reinterpret_cast<const half8_t*>(wr[t] + c);
-      }
-    } else {
+      for (int a = 0; a < MT; ++a) o.x[a] = in ? o.x[a] : half8_t{};
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int c = (st + u) * 32 + 8 * lq;
-        const bool in = st + u < e && c < C;   // channels outside are zero on both sides
-        const int cc = min(c, C - 8);
-#pragma unroll
-        for (int a = 0; a < MT; ++a) {
-          const half8_t v = *reinterpret_cast<const half8_t*>(xr[a] + cc);
-          xa[u][a] = in ? v : half8_t{};
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          const half8_t v = *reinterpret_cast<const half8_t*>(wr[t] + cc);
-          wb[u][t] = in ? v : half8_t{};
-        }
-      }
+      for (int t = 0; t < NT; ++t) o.w[t] = in ? o.w[t] : half8_t{};
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int a = 0; a < MT; ++a)
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
+      for (int t = 0; t < NT; ++t)
+        acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o.x[a], o.w[t], acc[a][t], 0, 0, 0);
+  };
+  // Steps of this wavefront: n.  The main loop reloads a stage as soon as it is used; the
+  // tail loads only what is left.
+  const int whole = (e - b) / (2 * W), rest = (e - b) % (2 * W);
+  const int n = 2 * whole + max(0, min(2, rest - 2 * wave));
+  ShrinkStep<NT, MT> ring[D];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-          acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(xa[u][a], wb[u][t], acc[a][t], 0, 0, 0);
+  for (int d = 0; d < D; ++d) load(d, ring[d]);
+  int k = 0;
+  for (; k + 2 * D <= n; k += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      add(k + d, ring[d]);
+      load(k + d + D, ring[d]);
+    }
   }
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    if (k + d < n) add(k + d, ring[d]);
+    if (k + d + D < n) load(k + d + D, ring[d]);
+  }
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (k + d + D < n) add(k + d + D, ring[d]);
 #pragma unroll
   for (int half = W / 2; half > 0; half >>= 1) {
     if (wave >= half && wave < 2 * half)
@@ -258,24 +296,19 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_kernel(const half_t* __res
 
 // --- expand: out[m][c] = binary16(base[m][c] + s_i sum_j h[m][j] w_i[c][j]) ---------------
 //
-// h = sum of S slices [S][M][R].  TRANS == false: w [L][C][R]; TRANS: w [L][R][C].
-// A workgroup of 4 wavefronts takes 16 MT rows x 512 channels.  Each wavefront keeps the
-// weights of its 128 channels in registers (8 MFMA tiles of 16 channels as the A operand)
-// and walks the rows 16 at a time (the B operand, from LDS, where the workgroup put the
-// split h once); base of the next 16 rows is in flight meanwhile.  HBM-bound: 2 bytes
-// read and 2 written per element.
-// The channels are dealt to the MFMA rows so that a lane ends up with four runs of 8
+// Weights are the A operand (16 channels x 32 ranks), h the B operand (16 rows).  A wavefront
+// holds the weights of 128 channels (8 MFMA tiles) and walks the rows 16 at a time.  The
+// channels are dealt to the MFMA rows so that a lane ends up with four runs of 8
 // consecutive channels of one row (run u at 32 u + 8 q), and base and out move as 16-byte
-// accesses, 64 bytes of a row per quarter wavefront.  !TRANS: MFMA row 4 q + r of tile t
-// is channel 32 (t / 2) + 8 q + 4 (t % 2) + r.  TRANS: lane (r, q) loads octet (r >> 2) + 4
-// (r & 3) of its 8 ranks and transposes the 8 x 8 block in registers; tile t has channel t
-// of every octet, and MFMA row 4 q + r is octet q + 4 r.
+// accesses, 64 bytes of a row per quarter wavefront.
+//   TRANS == false, w [L][C][R]: MFMA row 4 q + r of tile t is channel 32 (t / 2) + 8 q + 4
+//     (t % 2) + r.
+//   TRANS, w [L][R][C]: lane (r, q) loads octet (r >> 2) + 4 (r & 3) of its 8 ranks and
+//     transposes the 8 x 8 block in registers; tile t has channel t of every octet, and
+//     MFMA row 4 q + r is octet q + 4 r.
 // R <= 16 (PACKED): hi and lo share one MFMA, ranks 0..15 of hi in its first 16 slots and
 // of lo in the last 16, against the same weights.  Larger R: F fragments of 32 ranks,
 // one MFMA for hi and one for lo each.
-// base may equal out (every element is read and written by the same lane); rows without
-// an adapter are copied, bit for bit.  h_out (not NULL): the workgroups of the first
-// channels write the summed h.
 
 // The 8 x 8 block of binary16 values in v (one row per register quad) by columns: element
 // i of column t is element t of row i.
@@ -317,215 +350,169 @@ __device__ __forceinline__ void sum_slices8(const float* __restrict__ p, size_t 
   }
 }
 
-template <int F, bool PACKED, int MT, bool TRANS>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restrict__ h, int S,
-                                                          const half_t* __restrict__ w,
-                                                          const float* __restrict__ scaling, RowPlan plan,
-                                                          const half_t* base, half_t* out, float* __restrict__ h_out,
-                                                          int C, int R) {
-  constexpr int T = 16 * MT;
-  constexpr int kBlock = 512;   // channels per workgroup: 4 wavefronts x 128
-  constexpr int P = PACKED ? 1 : 2;
-  __shared__ int32_t rows[T];
-  __shared__ float factor[T];
-  __shared__ half8_t split[MT][F][P][64];
-  const Tile tile = find_tile<T>(plan, blockIdx.x, rows);
-  if (tile.count == 0) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+// Weights of the 128 channels from c0 (channels past C repeat valid ones).
+template <int F, bool PACKED, bool TRANS>
+__device__ __forceinline__ void load_expand_weights(const half_t* __restrict__ w, int c0, int C, int R, int lane,
+                                                    half8_t (&wf)[F][8]) {
   const int lr = lane & 15, lq = lane >> 4;
-  const int c_lo = blockIdx.y * kBlock;
-  if (tile.adapter == plan.L) {
-    if (base != out) {
-      const int chunks = min(kBlock, C - c_lo) / 8;
-      for (int i = tid; i < tile.count * chunks; i += 256) {
-        const size_t at = static_cast<size_t>(rows[i / chunks]) * C + c_lo + 8 * (i % chunks);
-        uint4 v = {0, 0, 0, 0};
-        if (base) v = *reinterpret_cast<const uint4*>(base + at);
-        *reinterpret_cast<uint4*>(out + at) = v;
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
+    const bool in = j0 < R;
+    if constexpr (!TRANS) {
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const int c = min(c0 + 32 * (t >> 1) + 8 * (lr >> 2) + 4 * (t & 1) + (lr & 3), C - 1);
+        const half8_t v = *reinterpret_cast<const half8_t*>(w + static_cast<size_t>(c) * R + (in ? j0 : 0));
+        wf[f][t] = in ? v : half8_t{};
       }
+    } else {
+      const int cc = min(c0 + 8 * ((lr >> 2) + 4 * (lr & 3)), C - 8);
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = *reinterpret_cast<const uint4*>(w + static_cast<size_t>(in ? j0 + i : i) * C + cc);
+        if (!in) v[i] = uint4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t) wf[f][t] = column8(v, t);
     }
-    if (h_out && blockIdx.y == 0)
-      for (int i = tid; i < tile.count * R; i += 256) h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
-    return;
-  }
-  const int nm = (tile.count + 15) >> 4;   // groups of 16 rows
-  const int c0 = c_lo + wave * 128;
-  const int jq = PACKED ? (lq & 1) * 8 : lq * 8;
-
-  // base of 16 rows, from the first group before anything else
-  auto load_base = [&](int a, uint4 (&y)[4]) {
-    const bool in = base && 16 * a + lr < tile.count;
-    const half_t* p = base + static_cast<size_t>(rows[16 * a + lr]) * C;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int c = c0 + 32 * u + 8 * lq;
-      y[u] = uint4{0, 0, 0, 0};
-      if (in && c < C) y[u] = *reinterpret_cast<const uint4*>(p + c);
-    }
-  };
-  uint4 y[4];
-  load_base(0, y);
-
-  // weights of 128 channels
-  half8_t wf[F][8];
-  const half_t* wl = w + static_cast<size_t>(tile.adapter) * R * C;
-  if (c0 < C) {
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const int j0 = 32 * f + jq;
-      const bool in = j0 < R;
-      if constexpr (!TRANS) {
-#pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const int c = min(c0 + 32 * (t >> 1) + 8 * (lr >> 2) + 4 * (t & 1) + (lr & 3), C - 1);
-          const half8_t v = *reinterpret_cast<const half8_t*>(wl + static_cast<size_t>(c) * R + (in ? j0 : 0));
-          wf[f][t] = in ? v : half8_t{};
-        }
-      } else {
-        const int cc = min(c0 + 8 * ((lr >> 2) + 4 * (lr & 3)), C - 8);
-        uint4 v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] = *reinterpret_cast<const uint4*>(wl + static_cast<size_t>(in ? j0 + i : i) * C + cc);
-          if (!in) v[i] = uint4{0, 0, 0, 0};
-        }
-#pragma unroll
-        for (int t = 0; t < 8; ++t) wf[f][t] = column8(v, t);
-      }
-    }
-  }
-
-  // split h: wavefront w takes rows 16 a + lr for a = w, w + 4, ...
-  const float si = scaling ? scaling[tile.adapter] : 1.0f;
-  const size_t slice = static_cast<size_t>(plan.M) * R;
-  for (int a = wave; a < nm; a += 4) {
-    const size_t row = static_cast<size_t>(rows[16 * a + lr]) * R;
-    float v[F][8];
-    float top = 0.0f;
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const int j0 = 32 * f + jq;
-      const bool in = j0 < R;
-      sum_slices8(h + row + (in ? j0 : 0), slice, S, v[f]);
-      if (h_out && blockIdx.y == 0 && in && 16 * a + lr < tile.count && (!PACKED || lq < 2)) {
-        *reinterpret_cast<float4_t*>(h_out + row + j0) = float4_t{v[f][0], v[f][1], v[f][2], v[f][3]};
-        *reinterpret_cast<float4_t*>(h_out + row + j0 + 4) = float4_t{v[f][4], v[f][5], v[f][6], v[f][7]};
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[f][j] = in ? v[f][j] : 0.0f;
-        top = fmaxf(top, finite_magnitude(v[f][j]));
-      }
-    }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const int shift = kSplitTop - top_exponent(top);
-    if (lq == 0) factor[16 * a + lr] = __builtin_ldexpf(si, -shift);
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      half8_t hi, lo;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        half_t vh, vl;
-        split_half(v[f][j], shift, vh, vl);
-        hi[j] = PACKED && lq >= 2 ? vl : vh;
-        lo[j] = vl;
-      }
-      split[a][f][0][lane] = hi;
-      if constexpr (!PACKED) split[a][f][P - 1][lane] = lo;
-    }
-  }
-  __syncthreads();
-  if (c0 >= C) return;
-
-  for (int a = 0; a < nm; ++a) {
-    uint4 next[4];
-    if (a + 1 < nm) load_base(a + 1, next);
-    float4_t acc[8] = {};
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-#pragma unroll
-      for (int p = 0; p < P; ++p) {
-        const half8_t hf = split[a][f][p][lane];
-#pragma unroll
-        for (int t = 0; t < 8; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[f][t], hf, acc[t], 0, 0, 0);
-      }
-    if (16 * a + lr < tile.count) {
-      const float fa = factor[16 * a + lr];
-      half_t* po = out + static_cast<size_t>(rows[16 * a + lr]) * C;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = c0 + 32 * u + 8 * lq;
-        const half8_t yv = __builtin_bit_cast(half8_t, y[u]);
-        half8_t o;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = TRANS ? acc[i][u] : acc[2 * u + (i >> 2)][i & 3];
-          o[i] = static_cast<half_t>(fmaf(v, fa, static_cast<float>(yv[i])));
-        }
-        if (c < C) *reinterpret_cast<half8_t*>(po + c) = o;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) y[u] = next[u];
   }
 }
 
-// --- transpose: b [L][N][R] -> bt [L][R][N], the layout the shrink reads ------------------
-constexpr int kTransposeRows = 128;
-
-__global__ __launch_bounds__(256) void lora_transpose_kernel(const half_t* __restrict__ b, half_t* __restrict__ bt,
-                                                             int N, int R) {
-  extern __shared__ __align__(16) half_t tile[];   // [kTransposeRows][R + 2]
-  const int n0 = blockIdx.x * kTransposeRows, nr = min(kTransposeRows, N - n0);
-  const half_t* src = b + (static_cast<size_t>(blockIdx.y) * N + n0) * R;
-  half_t* dst = bt + static_cast<size_t>(blockIdx.y) * R * N + n0;
-  const int ld = R + 2;
-  for (int i = threadIdx.x; i < nr * R / 8; i += 256) {
-    const half8_t v = *reinterpret_cast<const half8_t*>(src + 8 * i);
-    const int n = 8 * i / R, j = 8 * i % R;
+// Products of one group of 16 rows with the weights.
+template <int F, int P>
+__device__ __forceinline__ void expand_products(const half8_t (&wf)[F][8], const half8_t (&hf)[F][P], float4_t (&acc)[8]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) tile[n * ld + j + e] = v[e];
-  }
-  __syncthreads();
-  const int oct = nr / 8;   // N % 8 == 0
-  for (int i = threadIdx.x; i < R * oct; i += 256) {
-    const int j = i / oct, n = 8 * (i % oct);
-    half8_t v;
+  for (int t = 0; t < 8; ++t) acc[t] = float4_t{};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = tile[(n + e) * ld + j];
-    *reinterpret_cast<half8_t*>(dst + static_cast<size_t>(j) * N + n) = v;
-  }
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+      for (int t = 0; t < 8; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[f][t], hf[f][p], acc[t], 0, 0, 0);
 }
 
-// --- split: h (or the sum of S slices of g) as MFMA operands of the outer products --------
+// Run u of a lane: 8 results from the sums and the base values.
+template <bool TRANS>
+__device__ __forceinline__ half8_t expand_run(const float4_t (&acc)[8], int u, uint4 y, float factor) {
+  const half8_t yv = __builtin_bit_cast(half8_t, y);
+  half8_t o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = TRANS ? acc[i][u] : acc[2 * u + (i >> 2)][i & 3];
+    o[i] = static_cast<half_t>(fmaf(v, factor, static_cast<float>(yv[i])));
+  }
+  return o;
+}
+
+// --- split: h or g (the sum of S slices) as ready MFMA operands ---------------------------
 //
-// One workgroup per slot of 32 rows of one adapter.  Fragment t of a slot holds ranks 16 t
-// .. + 15: lane (r, q) has rank 16 t + r of rows 8 q .. 8 q + 7, first the hi terms of all
-// lanes (1 KB), then the lo terms, in units of 2^exps[slot].  Rows past the slot's count
-// and ranks past R are zero.  Done once per call instead of by every workgroup of 128
-// channels that reads h.  blockIdx.y == 0 splits h (one slice), 1 splits g.
+// One workgroup per slot of 32 rows of one adapter and task, once per call instead of by
+// every workgroup of 128 channels that multiplies with h.
+//   kByRank (outer)   fragment t: lane (r, q) has rank 16 t + r of rows 8 q .. 8 q + 7, in
+//                     units of 2^exps[slot]; [slots][NT][hi, lo][64][8]
+//   kByRow (stream)   group g of 16 rows, fragment f: lane (r, q) has ranks 32 f + 8 q .. + 7
+//                     of row 16 g + r, in units of 2^e of that row, with factors[row of the
+//                     slot] = s_i 2^e; [slots][2][F][hi, lo][64][8].  R <= 16: one fragment
+//                     with hi of ranks 0 .. 15 in its first two quarters and lo in the
+//                     others; [slots][2][64][8]
+// Rows past the slot's count and ranks past R are zero.  The by-row task also writes the
+// summed h, the slot table (rows, adapter, count) and, for rows without an adapter, h = 0.
+enum SplitKind { kByRank, kByRow };
+
 struct SplitTask {
-  const float* h;
+  const float* h;    // [S][M][R]
   int S;
-  half_t* frags;     // [slots][NT][2][64][8]
-  int32_t* exps;     // [slots]
+  int kind;
+  half_t* frags;
+  int32_t* exps;     // by rank: [slots]
+  float* factors;    // by row: [slots][32]
+  float* sum;        // by row: [M][R] or NULL
 };
 
 constexpr int kSlotRows = 32;
 
-__global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask t1, RowPlan plan, int R) {
+struct SlotTable {
+  int2* meta;        // [slots] adapter (L: none), count (0: empty slot)
+  int32_t* rows;     // [slots][32], entries past the count repeat the first
+};
+
+// Fragments of a row group by row, and halves (hi, lo) of each.
+__host__ __device__ constexpr int row_frags(int R) { return R <= 16 ? 1 : 2 * ((R + 31) / 32); }
+
+__global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask t1, SplitTask t2,
+                                                         const float* __restrict__ scaling, SlotTable table,
+                                                         RowPlan plan, int R) {
   __shared__ int32_t rows[kSlotRows];
   __shared__ float tops[4];
-  const SplitTask task = blockIdx.y == 0 ? t0 : t1;
+  const SplitTask task = blockIdx.y == 0 ? t0 : blockIdx.y == 1 ? t1 : t2;
   const int slot = blockIdx.x;
   const Tile tile = find_tile<kSlotRows>(plan, slot, rows);
-  if (tile.count == 0 || tile.adapter == plan.L) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
-  const int NT = (R + 15) >> 4;
   const size_t slice = static_cast<size_t>(plan.M) * R;
+  if (task.kind == kByRow) {
+    if (tid == 0) table.meta[slot] = int2{tile.adapter, tile.count};
+    if (tile.count == 0) return;
+    if (tid < kSlotRows) table.rows[slot * kSlotRows + tid] = rows[tid < tile.count ? tid : 0];
+    if (tile.adapter == plan.L) {
+      if (task.sum)
+        for (int i = tid; i < tile.count * R; i += 256) task.sum[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+      return;
+    }
+    // wavefronts 0, 1: row groups 0, 1 (a lane holds at most 4 fragments of 8 ranks)
+    if (wave >= 2) return;
+    const int m = 16 * wave + lr;
+    const bool mine = m < tile.count;
+    const size_t at = static_cast<size_t>(rows[mine ? m : 0]) * R;
+    const bool packed = R <= 16;
+    const int F = packed ? 1 : (R + 31) / 32;
+    float v[4][8];
+    float top = 0.0f;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int j0 = packed ? 8 * (lq & 1) : 32 * f + 8 * lq;
+      const bool in = f < F && j0 < R && mine;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[f][j] = 0.0f;
+      if (!in) continue;
+      sum_slices8(task.h + at + j0, slice, task.S, v[f]);
+      if (task.sum && (!packed || lq < 2)) {
+        *reinterpret_cast<float4_t*>(task.sum + at + j0) = float4_t{v[f][0], v[f][1], v[f][2], v[f][3]};
+        *reinterpret_cast<float4_t*>(task.sum + at + j0 + 4) = float4_t{v[f][4], v[f][5], v[f][6], v[f][7]};
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_magnitude(v[f][j]));
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const int shift = kSplitTop - top_exponent(top);
+    const float si = scaling ? scaling[tile.adapter] : 1.0f;
+    if (lq == 0) task.factors[slot * kSlotRows + m] = __builtin_ldexpf(si, -shift);
+    half8_t* o = reinterpret_cast<half8_t*>(task.frags) + (static_cast<size_t>(slot) * 2 + wave) * row_frags(R) * 64 + lane;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      if (f >= F) break;
+      half8_t hi, lo;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        half_t a, b;
+        split_half(v[f][j], shift, a, b);
+        hi[j] = packed && lq >= 2 ? b : a;
+        lo[j] = b;
+      }
+      if (packed) {
+        o[0] = hi;
+      } else {
+        o[2 * f * 64] = hi;
+        o[(2 * f + 1) * 64] = lo;
+      }
+    }
+    return;
+  }
+  if (tile.count == 0 || tile.adapter == plan.L) return;
+  const int NT = (R + 15) >> 4;
   float v[2][8];   // at most 8 fragments: two per wavefront
   float top = 0.0f;
 #pragma unroll
@@ -566,6 +553,248 @@ __global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask
     half8_t* o = reinterpret_cast<half8_t*>(task.frags) + (static_cast<size_t>(slot) * NT + t) * 128 + lane;
     o[0] = hi;
     o[64] = lo;
+  }
+}
+
+// --- expand, few rows: sums and splits h itself -------------------------------------------
+//
+// h = sum of S slices [S][M][R].  A workgroup of 4 wavefronts takes one tile of 16 rows x
+// 512 channels; its first wavefront splits h into LDS while the weights and base are on
+// their way.  Latency-bound: what counts is one launch less.
+// base may equal out (every element is read and written by the same lane); rows without
+// an adapter are copied, bit for bit.  h_out (not NULL): the workgroups of the first
+// channels write the summed h.
+template <int F, bool PACKED>
+__global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restrict__ h, int S,
+                                                          const half_t* __restrict__ w,
+                                                          const float* __restrict__ scaling, RowPlan plan,
+                                                          const half_t* base, half_t* out, float* __restrict__ h_out,
+                                                          int C, int R) {
+  constexpr int kBlock = 512;   // channels per workgroup: 4 wavefronts x 128
+  constexpr int P = PACKED ? 1 : 2;
+  __shared__ int32_t rows[16];
+  __shared__ float factor[16];
+  __shared__ half8_t split[F][P][64];
+  const Tile tile = find_tile<16>(plan, blockIdx.x, rows);
+  if (tile.count == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int c_lo = blockIdx.y * kBlock;
+  if (tile.adapter == plan.L) {
+    if (base != out) {
+      const int chunks = min(kBlock, C - c_lo) / 8;
+      for (int i = tid; i < tile.count * chunks; i += 256) {
+        const size_t at = static_cast<size_t>(rows[i / chunks]) * C + c_lo + 8 * (i % chunks);
+        *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(base + at);
+      }
+    }
+    if (h_out && blockIdx.y == 0)
+      for (int i = tid; i < tile.count * R; i += 256) h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+    return;
+  }
+  const int c0 = c_lo + wave * 128;
+  const bool mine = lr < tile.count;
+  const size_t at = static_cast<size_t>(rows[mine ? lr : 0]);
+  uint4 y[4];
+  half8_t wf[F][8];
+  if (c0 < C) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      y[u] = *reinterpret_cast<const uint4*>(base + at * C + min(c0 + 32 * u + 8 * lq, C - 8));
+    load_expand_weights<F, PACKED, false>(w + static_cast<size_t>(tile.adapter) * R * C, c0, C, R, lane, wf);
+  }
+  if (wave == 0) {
+    const float si = scaling ? scaling[tile.adapter] : 1.0f;
+    float v[F][8];
+    float top = 0.0f;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
+      const bool in = j0 < R;
+      sum_slices8(h + at * R + (in ? j0 : 0), static_cast<size_t>(plan.M) * R, S, v[f]);
+      if (h_out && blockIdx.y == 0 && in && mine && (!PACKED || lq < 2)) {
+        *reinterpret_cast<float4_t*>(h_out + at * R + j0) = float4_t{v[f][0], v[f][1], v[f][2], v[f][3]};
+        *reinterpret_cast<float4_t*>(h_out + at * R + j0 + 4) = float4_t{v[f][4], v[f][5], v[f][6], v[f][7]};
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[f][j] = in ? v[f][j] : 0.0f;
+        top = fmaxf(top, finite_magnitude(v[f][j]));
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const int shift = kSplitTop - top_exponent(top);
+    if (lq == 0) factor[lr] = __builtin_ldexpf(si, -shift);
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      half8_t hi, lo;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        half_t vh, vl;
+        split_half(v[f][j], shift, vh, vl);
+        hi[j] = PACKED && lq >= 2 ? vl : vh;
+        lo[j] = vl;
+      }
+      split[f][0][lane] = hi;
+      if constexpr (!PACKED) split[f][P - 1][lane] = lo;
+    }
+  }
+  __syncthreads();
+  if (c0 >= C) return;
+  half8_t hf[F][P];
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int p = 0; p < P; ++p) hf[f][p] = split[f][p][lane];
+  float4_t acc[8];
+  expand_products<F, P>(wf, hf, acc);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int c = c0 + 32 * u + 8 * lq;
+    const half8_t o = expand_run<false>(acc, u, y[u], factor[lr]);
+    if (c < C && mine) *reinterpret_cast<half8_t*>(out + at * C + c) = o;
+  }
+}
+
+// --- expand, many rows: a stream over slots of 32 rows ------------------------------------
+//
+// HBM-bound: 2 bytes read and 2 written per element.  Operands come ready from the split
+// kernel, so the wavefronts share nothing: no LDS, no barrier.  A wavefront takes `group`
+// (at most 64) consecutive slots; slots of one adapter are a run with the weights in
+// registers and the operands and base values of the next D row groups in flight.  The
+// workgroups of one group of slots are neighbours, so an XCD's L2 holds few channels of w.
+// base may equal out, or be absent (BASE == false: 0); rows without an adapter are copied.
+template <int F, int P>
+struct StreamRows {
+  uint4 y[4];
+  half8_t h[F][P];
+  int row;
+  float factor;
+};
+
+template <int F, bool PACKED, bool TRANS, bool BASE, int D>
+__global__ __launch_bounds__(256) void lora_stream_kernel(const half_t* __restrict__ frags,
+                                                          const float* __restrict__ factors, SlotTable table,
+                                                          const half_t* __restrict__ w, const half_t* base, half_t* out,
+                                                          int C, int R, int L, int slots, int group) {
+  constexpr int P = PACKED ? 1 : 2;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  const int blocks = (C + 511) >> 9;
+  const int c0 = (blockIdx.x % blocks) * 512 + wave * 128;
+  const int s0 = (blockIdx.x / blocks) * group;
+  if (c0 >= C) return;
+  const int ns = min(group, slots - s0);
+  // lane l: slot s0 + l
+  const int2 meta = lane < ns ? table.meta[s0 + lane] : int2{-1, 0};
+  half8_t wf[F][8];
+
+  for (int i = 0; i < ns;) {
+    const int adapter = __builtin_amdgcn_readlane(meta.x, i);
+    const int count = __builtin_amdgcn_readlane(meta.y, i);
+    if (count == 0 || adapter == L) {
+      if (count > 0 && base != out)
+        for (int m = lq; m < count; m += 4) {
+          const size_t at = static_cast<size_t>(table.rows[(s0 + i) * kSlotRows + m]) * C;
+          const int c = c0 + 8 * lr;
+          if (c < C) *reinterpret_cast<uint4*>(out + at + c) = BASE ? *reinterpret_cast<const uint4*>(base + at + c) : uint4{0, 0, 0, 0};
+        }
+      ++i;
+      continue;
+    }
+    // the run: slots i .. end - 1 of the same adapter, all but the last full
+    const uint64_t other = __ballot(meta.x != adapter || meta.y == 0) >> i;
+    const int end = other ? i + __builtin_ctzll(other) : 64;
+    const int last = __builtin_amdgcn_readlane(meta.y, end - 1);
+    const int n = 2 * (end - i - 1) + ((last + 15) >> 4);            // row groups
+    const int total = 32 * (end - i - 1) + last;                      // rows
+    load_expand_weights<F, PACKED, TRANS>(w + static_cast<size_t>(adapter) * R * C, c0, C, R, lane, wf);
+    const int g0 = 2 * (s0 + i);
+    auto load = [&](int g, int row, StreamRows<F, P>& o) {   // g < n
+      o.row = row;
+      o.factor = factors[(g0 + g) * 16 + lr];
+      const half8_t* f8 = reinterpret_cast<const half8_t*>(frags) + static_cast<size_t>(g0 + g) * F * P * 64 + lane;
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int p = 0; p < P; ++p) o.h[f][p] = f8[(f * P + p) * 64];
+      if constexpr (BASE) {
+        const half_t* b = base + static_cast<size_t>(row) * C;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) o.y[u] = *reinterpret_cast<const uint4*>(b + min(c0 + 32 * u + 8 * lq, C - 8));
+      }
+    };
+    auto finish = [&](int g, const StreamRows<F, P>& o) {
+      float4_t acc[8];
+      expand_products<F, P>(wf, o.h, acc);
+      if (16 * g + lr < total) {
+        half_t* po = out + static_cast<size_t>(o.row) * C;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int c = c0 + 32 * u + 8 * lq;
+          if (c < C) *reinterpret_cast<half8_t*>(po + c) = expand_run<TRANS>(acc, u, BASE ? o.y[u] : uint4{0, 0, 0, 0}, o.factor);
+        }
+      }
+    };
+    // rows are looked up D groups ahead of their loads
+    auto row_of = [&](int g) { return table.rows[(g0 + min(g, n - 1)) * 16 + lr]; };
+    StreamRows<F, P> ring[D];
+    int ahead[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) ahead[d] = row_of(d);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      load(min(d, n - 1), ahead[d], ring[d]);
+      ahead[d] = row_of(d + D);
+    }
+    int g = 0;
+    for (; g + 2 * D <= n; g += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        finish(g + d, ring[d]);
+        load(g + d + D, ahead[d], ring[d]);
+        ahead[d] = row_of(g + d + 2 * D);
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (g + d < n) finish(g + d, ring[d]);
+      if (g + d + D < n) load(g + d + D, ahead[d], ring[d]);
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (g + d + D < n) finish(g + d + D, ring[d]);
+    i = end;
+  }
+}
+
+// --- transpose: b [L][N][R] -> bt [L][R][N], the layout the shrink reads ------------------
+constexpr int kTransposeRows = 128;
+
+__global__ __launch_bounds__(256) void lora_transpose_kernel(const half_t* __restrict__ b, half_t* __restrict__ bt,
+                                                             int N, int R) {
+  extern __shared__ __align__(16) half_t tile[];   // [kTransposeRows][R + 2]
+  const int n0 = blockIdx.x * kTransposeRows, nr = min(kTransposeRows, N - n0);
+  const half_t* src = b + (static_cast<size_t>(blockIdx.y) * N + n0) * R;
+  half_t* dst = bt + static_cast<size_t>(blockIdx.y) * R * N + n0;
+  const int ld = R + 2;
+  for (int i = threadIdx.x; i < nr * R / 8; i += 256) {
+    const half8_t v = *reinterpret_cast<const half8_t*>(src + 8 * i);
+    const int n = 8 * i / R, j = 8 * i % R;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) tile[n * ld + j + e] = v[e];
+  }
+  __syncthreads();
+  const int oct = nr / 8;   // N % 8 == 0
+  for (int i = threadIdx.x; i < R * oct; i += 256) {
+    const int j = i / oct, n = 8 * (i % oct);
+    half8_t v;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = tile[(n + e) * ld + j];
+    *reinterpret_cast<half8_t*>(dst + static_cast<size_t>(j) * N + n) = v;
   }
 }
 
