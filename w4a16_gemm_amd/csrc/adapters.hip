@@ -134,33 +134,35 @@ int plan_slots(int M, int L, bool with_index) {
 
 // --- shrink -------------------------------------------------------------------------
 
-// Rows per tile (in 16s) of a shrink: one for few rows per adapter, else enough that a
-// tile's reads of w (16 NT ranks) do not outweigh its reads of x.
-int shrink_mt(int M, int L, int R) { return M / L < 64 ? 1 : R <= 32 ? 2 : 4; }
+// Tiles of 64 rows once an adapter has that many on average; below, tiles of 16 rows with
+// the wavefronts along the channels.
+bool shrink_tall(int M, int L) { return M / L >= 64; }
 
-// Slices of the long axis: about one workgroup of 8 wavefronts per compute unit, at least
-// 512 channels (two steps per wavefront) per slice.
+// Slices of the long axis: enough workgroups for four per compute unit (few rows: one), at
+// least 512 channels each, and sums of the slices that stay small (4 MB) or a quarter of x.
 int shrink_slices(int M, int L, int R, int C) {
-  const int tiles = ceil_div(M, 16 * shrink_mt(M, L, R));
-  return std::max(1, std::min({ceil_div(256, tiles), C / 512, 16}));
+  const bool tall = shrink_tall(M, L);
+  const int want = ceil_div(tall ? 1024 : 256, ceil_div(M, tall ? 64 : 16));
+  const int64_t light = std::max<int64_t>(C / (16 * R), (int64_t{1} << 20) / (static_cast<int64_t>(M) * R));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, C / 512, 16, light})));
 }
 
 void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, int R, int S, float* out, hipStream_t st) {
-  const int mt = shrink_mt(plan.M, plan.L, R);
-  const dim3 grid(tile_slots(plan, 16 * mt) * S), block(512);
-#define W4A16_SHRINK(NT_, MT_, D_) \
-  hipLaunchKernelGGL((lora_shrink_kernel<NT_, MT_, 8, D_>), grid, block, 0, st, x, w, plan, C, R, S, out)
+  const bool tall = shrink_tall(plan.M, plan.L);
+  const dim3 grid(tile_slots(plan, tall ? 64 : 16) * S), block(256);
+#define W4A16_SHRINK(NT_, TALL_, D_) \
+  hipLaunchKernelGGL((lora_shrink_kernel<NT_, TALL_, D_>), grid, block, 0, st, x, w, plan, C, R, S, out)
   const int nt = ceil_div(R, 16);
-  if (mt == 1) {
-    if (nt == 1) W4A16_SHRINK(1, 1, 4);
-    else if (nt == 2) W4A16_SHRINK(2, 1, 4);
-    else if (nt <= 4) W4A16_SHRINK(4, 1, 4);
-    else W4A16_SHRINK(8, 1, 2);
+  if (tall) {
+    if (nt == 1) W4A16_SHRINK(1, true, 8);
+    else if (nt == 2) W4A16_SHRINK(2, true, 6);
+    else if (nt <= 4) W4A16_SHRINK(4, true, 4);
+    else W4A16_SHRINK(8, true, 2);
   } else {
-    if (nt == 1) W4A16_SHRINK(1, 2, 4);
-    else if (nt == 2) W4A16_SHRINK(2, 2, 4);
-    else if (nt <= 4) W4A16_SHRINK(4, 4, 4);
-    else W4A16_SHRINK(8, 4, 2);
+    if (nt == 1) W4A16_SHRINK(1, false, 4);
+    else if (nt == 2) W4A16_SHRINK(2, false, 4);
+    else if (nt <= 4) W4A16_SHRINK(4, false, 4);
+    else W4A16_SHRINK(8, false, 2);
   }
 #undef W4A16_SHRINK
 }
@@ -218,13 +220,21 @@ struct Kept {
   int gshift;
 };
 
+// Workgroups that share the rows of 128 channels: enough for one per compute unit, as long
+// as every wavefront keeps two slots of an average adapter.
+int outer_parts(int M, int L, int C, int R) {
+  const int64_t groups = static_cast<int64_t>(ceil_div(C, 128)) * ceil_div(R, 64) * L;
+  const int64_t most = M / L / kSlotRows / (2 * (R <= 32 ? 8 : 4));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(256 + groups - 1) / groups, most, 16})));
+}
+
 template <bool Q8, bool CMAJOR>
 void run_outer(const Kept& k, const ByRank& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
-               hipStream_t st) {
+               int parts, hipStream_t st) {
 #define W4A16_OUTER(NT_, W_, D_) \
   hipLaunchKernelGGL((lora_outer_kernel<NT_, W_, D_, Q8, CMAJOR>), \
-                     dim3(ceil_div(C, 128), ceil_div(R, 16 * NT_), plan.L), dim3(64 * W_), 0, st, k.x, k.codes, k.scales, \
-                     k.gshift, f.frags, f.exps, scaling, plan, grad, C, R)
+                     dim3(ceil_div(C, 128), ceil_div(R, 16 * NT_) * parts, plan.L), dim3(64 * W_), 0, st, k.x, k.codes, \
+                     k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts)
   if (R <= 16) W4A16_OUTER(1, 8, 3);
   else if (R <= 32) W4A16_OUTER(2, 8, 2);
   else W4A16_OUTER(4, 4, 2);
@@ -266,9 +276,12 @@ struct BackwardMemory {
   ByRank h, g;
   ByRow g_rows;
   SlotTable table;
+  int a_parts, b_parts;
+  float *da, *db;    // [parts][L][R][K], [parts][L][N][R], where there is more than one part
 };
 
-BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index, int M, int N, int R, int L) {
+BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index, int M, int N, int K, int R,
+                               int L) {
   BackwardMemory m{};
   m.plan = take_plan(ws, index, with_index, M, L);
   m.bt = ws.take<half_t>(static_cast<size_t>(L) * R * N);
@@ -279,6 +292,10 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
   m.g = take_by_rank(ws, m.slots, R);
   m.g_rows = take_by_row(ws, m.slots, R);
   m.table = take_table(ws, m.slots);
+  m.a_parts = outer_parts(M, L, K, R);
+  m.b_parts = outer_parts(M, L, N, R);
+  if (m.a_parts > 1) m.da = ws.take<float>(static_cast<size_t>(m.a_parts) * L * R * K);
+  if (m.b_parts > 1) m.db = ws.take<float>(static_cast<size_t>(m.b_parts) * L * N * R);
   return m;
 }
 
@@ -310,22 +327,31 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   if (int rc = check_buffers(bufs)) return rc;
   if (c.dx0 && !c.dx) return fail(W4A16_ERR_INVALID_ARG, "dx0 is given without dx");
   Carver size{nullptr}, ws{static_cast<unsigned char*>(c.workspace)};
-  backward_memory(size, nullptr, c.index != nullptr, c.M, c.N, c.R, c.L);
+  backward_memory(size, nullptr, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
   if (int rc = check_workspace(c.workspace_bytes, size.used)) return rc;
-  const BackwardMemory m = backward_memory(ws, c.index, c.index != nullptr, c.M, c.N, c.R, c.L);
+  const BackwardMemory m = backward_memory(ws, c.index, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
   const auto st = static_cast<hipStream_t>(c.stream);
   const auto* dy = reinterpret_cast<const half_t*>(c.dy);
-  run_plan(m.plan, st);
-  hipLaunchKernelGGL(lora_transpose_kernel, dim3(ceil_div(c.N, kTransposeRows), c.L), dim3(256),
-                     sizeof(half_t) * kTransposeRows * (c.R + 2), st, reinterpret_cast<const half_t*>(c.b), m.bt, c.N, c.R);
+  const int plans = c.index ? c.L + 1 : 0;
+  hipLaunchKernelGGL(lora_prepare_kernel, dim3(plans + ceil_div(c.N, transpose_rows(c.R)) * c.L), dim3(1024), 0, st,
+                     m.plan, const_cast<int32_t*>(m.plan.off), const_cast<int32_t*>(m.plan.perm), plans,
+                     reinterpret_cast<const half_t*>(c.b), m.bt, c.N, c.R);
   run_shrink(dy, m.bt, m.plan, c.N, c.R, m.S, m.part, st);
-  const SplitTask th{c.h, 1, kByRank, m.h.frags, m.h.exps, nullptr, nullptr};
-  const SplitTask tg{m.part, m.S, kByRank, m.g.frags, m.g.exps, nullptr, nullptr};
-  const SplitTask tr{m.part, m.S, kByRow, m.g_rows.frags, nullptr, m.g_rows.factors, nullptr};
-  hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, c.dx ? 3 : 2), dim3(256), 0, st, th, tg, tr, c.scaling, m.table,
-                     m.plan, c.R);
-  run_outer<false, true>(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, c.db, c.N, c.R, st);
-  run_outer<Q8, false>(kept, m.g, c.scaling, m.plan, c.da, c.K, c.R, st);
+  const SplitTask th{c.h, 1, m.h.frags, m.h.exps, nullptr, nullptr, nullptr};
+  const SplitTask tg{m.part, m.S, m.g.frags, m.g.exps, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors, nullptr};
+  hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 2), dim3(256), 0, st, th, tg, c.scaling, m.table, m.plan, c.R);
+  run_outer<false, true>(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, m.b_parts > 1 ? m.db : c.db, c.N, c.R,
+                         m.b_parts, st);
+  run_outer<Q8, false>(kept, m.g, c.scaling, m.plan, m.a_parts > 1 ? m.da : c.da, c.K, c.R, m.a_parts, st);
+  if (m.a_parts > 1 || m.b_parts > 1) {
+    auto task = [](float* parts, float* out, size_t count, int n) {
+      return PartsTask{reinterpret_cast<const float4_t*>(parts), reinterpret_cast<float4_t*>(out), n > 1 ? count / 4 : 0, n};
+    };
+    const PartsTask ta = task(m.da, c.da, static_cast<size_t>(c.L) * c.R * c.K, m.a_parts);
+    const PartsTask tb = task(m.db, c.db, static_cast<size_t>(c.L) * c.N * c.R, m.b_parts);
+    const size_t most = std::max(ta.quads, tb.quads);
+    hipLaunchKernelGGL(lora_sum_parts_kernel, dim3(static_cast<unsigned>((most + 255) / 256), 2), dim3(256), 0, st, ta, tb);
+  }
   if (c.dx)
     run_stream<true>(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a), reinterpret_cast<const half_t*>(c.dx0),
                      reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L, m.slots, st);
@@ -365,8 +391,8 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
   run_plan(m.plan, st);
   run_shrink(reinterpret_cast<const half_t*>(x), reinterpret_cast<const half_t*>(a), m.plan, K, R, m.S, m.part, st);
   if (m.stream) {
-    const SplitTask t{m.part, m.S, kByRow, m.h.frags, nullptr, m.h.factors, h};
-    hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(256), 0, st, t, t, t, scaling, m.table, m.plan, R);
+    const SplitTask t{m.part, m.S, nullptr, nullptr, m.h.frags, m.h.factors, h};
+    hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(256), 0, st, t, t, scaling, m.table, m.plan, R);
     run_stream<false>(m.h, m.table, bh, yh, oh, N, R, L, m.slots, st);
   } else {
     run_expand(m.part, m.S, bh, scaling, m.plan, yh, oh, h, N, R, st);
@@ -377,7 +403,7 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
 extern "C" size_t w4a16_lora_backward_workspace(int M, int N, int K, int R, int L, int with_index) {
   if (check_lora_shape(M, N, K, R, L) != W4A16_OK) return 0;
   Carver size{nullptr};
-  backward_memory(size, nullptr, with_index != 0, M, N, R, L);
+  backward_memory(size, nullptr, with_index != 0, M, N, K, R, L);
   return size.used;
 }
 

@@ -43,10 +43,9 @@ __device__ __forceinline__ int row_class(int i, int L) { return i >= 0 && i < L 
 // its own rows in order.  No atomics, so the order (and with it every sum) is fixed.
 constexpr int kPlanRows = 8;   // rows per thread read at once (8192 per workgroup)
 
-__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ index, int M, int L,
-                                                         int32_t* __restrict__ off, int32_t* __restrict__ perm) {
-  __shared__ int part[2][16];
-  const int c = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+__device__ __forceinline__ void plan_rows(int c, const int32_t* __restrict__ index, int M, int L,
+                                          int32_t* __restrict__ off, int32_t* __restrict__ perm, int (*part)[16]) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int cls[kPlanRows];
   auto load = [&](int m0) {   // rows past M: a class above all
 #pragma unroll
@@ -90,6 +89,12 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restri
       at += total;
     }
   }
+}
+
+__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ index, int M, int L,
+                                                         int32_t* __restrict__ off, int32_t* __restrict__ perm) {
+  __shared__ int part[2][16];
+  plan_rows(blockIdx.x, index, M, L, off, perm, part);
 }
 
 // Number of tile slots for T rows per tile (host and device agree on it): slots of class
@@ -177,25 +182,27 @@ constexpr int kNoExponent = -1000;   // of values that are all zero
 
 // --- shrink: out[s][m][j] = sum over the channels of slice s of x[m][c] w[i][j][c] -------
 //
-// x [M][C], w [L][R][C], C % 8 == 0.  A wavefront holds 16 MT rows x 16 NT ranks of sums
-// and walks steps of 32 channels, both operands as they lie in memory (lane (r, q): row r,
-// channels 8 q .. 8 q + 7 of the step), D steps in flight.  The W wavefronts of a workgroup
-// take turns along the slice; their sums are added in LDS in a fixed order.  A row's result
-// depends on its own x alone, so the rows repeated to fill a tile are computed and not
-// stored.
-// Every tile reads all of w: with 16 MT >= R that is no more than x, and the slices are
-// dealt to neighbouring workgroups, so that an XCD's L2 holds the w of few slices.
-template <int NT, int MT>
+// x [M][C], w [L][R][C], C % 8 == 0.  A wavefront holds 16 rows x 16 NT ranks of sums and
+// walks steps of 32 channels, both operands as they lie in memory (lane (r, q): row r,
+// channels 8 q .. 8 q + 7 of the step), D steps in flight.  A row's result depends on its
+// own x alone, so the rows repeated to fill a tile are computed and not stored.
+//   TALL == false, few rows: a tile of 16 rows per workgroup, whose 4 wavefronts take turns
+//     (pairs of steps) along the slice and are added in LDS in a fixed order.
+//   TALL: a tile of 64 rows, 16 per wavefront; all of them walk the whole slice together,
+//     so that w comes from the L1 after the first.  w is read once per tile of 64 rows; the
+//     slices are dealt to neighbouring workgroups, so an XCD's L2 holds the w of few slices.
+template <int NT>
 struct ShrinkStep {
-  half8_t x[MT], w[NT];
+  half8_t x, w[NT];
 };
 
-template <int NT, int MT, int W, int D>
-__global__ __launch_bounds__(64 * W) void lora_shrink_kernel(const half_t* __restrict__ x, const half_t* __restrict__ w,
-                                                             RowPlan plan, int C, int R, int S, float* __restrict__ out) {
-  constexpr int T = 16 * MT;
+template <int NT, bool TALL, int D>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restrict__ x, const half_t* __restrict__ w,
+                                                          RowPlan plan, int C, int R, int S, float* __restrict__ out) {
+  constexpr int T = TALL ? 64 : 16;
+  constexpr int W = 4;
   __shared__ int32_t rows[T];
-  __shared__ float4_t red[W / 2 * MT * NT * 64];
+  __shared__ float4_t red[TALL ? 1 : W / 2 * NT * 64];
   const int s = blockIdx.x % S;
   const Tile tile = find_tile<T>(plan, blockIdx.x / S, rows);
   if (tile.count == 0) return;
@@ -204,51 +211,44 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_kernel(const half_t* __res
   const int lr = lane & 15, lq = lane >> 4;
   float* o = out + static_cast<size_t>(s) * plan.M * R;
   if (tile.adapter == plan.L) {
-    for (int i = tid; i < tile.count * R; i += 64 * W) o[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+    for (int i = tid; i < tile.count * R; i += 256) o[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
     return;
   }
-  const half_t* xr[MT];
+  const int m0 = TALL ? 16 * wave : 0;
+  if (m0 >= tile.count) return;   // TALL has no barrier from here on
+  const half_t* xr = x + static_cast<size_t>(rows[m0 + lr]) * C;
   const half_t* wr[NT];
-#pragma unroll
-  for (int a = 0; a < MT; ++a) xr[a] = x + static_cast<size_t>(rows[16 * a + lr]) * C;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
     wr[t] = w + (static_cast<size_t>(tile.adapter) * R + min(16 * t + lr, R - 1)) * C;
-  float4_t acc[MT][NT] = {};
-  const int full = C >> 5;   // steps of 32 channels
+  float4_t acc[NT] = {};
+  const int full = C >> 5;   // whole steps of 32 channels
   const int steps = (C + 31) >> 5;
   const int b = static_cast<int>(static_cast<int64_t>(steps) * s / S);
   const int e = static_cast<int>(static_cast<int64_t>(steps) * (s + 1) / S);
-  // Wavefront w takes pairs of steps w, w + W, ... of the slice, so that it reads 128
-  // consecutive bytes of a row.  Loads past the slice are clamped into it, not used.
-  auto step_of = [&](int k) { return b + 2 * (wave + (k >> 1) * W) + (k & 1); };
-  auto load = [&](int k, ShrinkStep<NT, MT>& o) {
+  // Step k of this wavefront, of n.  Loads past the slice are clamped into it, not used.
+  auto step_of = [&](int k) { return TALL ? b + k : b + 2 * (wave + (k >> 1) * W) + (k & 1); };
+  const int whole = (e - b) / (2 * W), rest = (e - b) % (2 * W);
+  const int n = TALL ? e - b : 2 * whole + max(0, min(2, rest - 2 * wave));
+  auto load = [&](int k, ShrinkStep<NT>& o) {
     const int c = min(min(step_of(k), e - 1) * 32 + 8 * lq, C - 8);
-#pragma unroll
-    for (int a = 0; a < MT; ++a) o.x[a] = *reinterpret_cast<const half8_t*>(xr[a] + c);
+    o.x = *reinterpret_cast<const half8_t*>(xr + c);
 #pragma unroll
     for (int t = 0; t < NT; ++t) o.w[t] = *reinterpret_cast<const half8_t*>(wr[t] + c);
   };
-  auto add = [&](int k, ShrinkStep<NT, MT>& o) {
+  auto add = [&](int k, ShrinkStep<NT>& o) {
     const int st = step_of(k);
     if (st >= full) {   // the last, partial step: channels past C are zero on both sides
       const bool in = st * 32 + 8 * lq < C;
-#pragma unroll
-      for (int a = 0; a < MT; ++a) o.x[a] = in ? o.x[a] : half8_t{};
+      o.x = in ? o.x : half8_t{};
 #pragma unroll
       for (int t = 0; t < NT; ++t) o.w[t] = in ? o.w[t] : half8_t{};
     }
 #pragma unroll
-    for (int a = 0; a < MT; ++a)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        acc[a][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o.x[a], o.w[t], acc[a][t], 0, 0, 0);
+    for (int t = 0; t < NT; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(o.x, o.w[t], acc[t], 0, 0, 0);
   };
-  // Steps of this wavefront: n.  The main loop reloads a stage as soon as it is used; the
-  // tail loads only what is left.
-  const int whole = (e - b) / (2 * W), rest = (e - b) % (2 * W);
-  const int n = 2 * whole + max(0, min(2, rest - 2 * wave));
-  ShrinkStep<NT, MT> ring[D];
+  // The main loop reloads a stage as soon as it is used; the tail loads only what is left.
+  ShrinkStep<NT> ring[D];
 #pragma unroll
   for (int d = 0; d < D; ++d) load(d, ring[d]);
   int k = 0;
@@ -267,31 +267,27 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_kernel(const half_t* __res
 #pragma unroll
   for (int d = 0; d < D; ++d)
     if (k + d + D < n) add(k + d + D, ring[d]);
+  if constexpr (!TALL) {
 #pragma unroll
-  for (int half = W / 2; half > 0; half >>= 1) {
-    if (wave >= half && wave < 2 * half)
+    for (int half = W / 2; half > 0; half >>= 1) {
+      if (wave >= half && wave < 2 * half)
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
+        for (int t = 0; t < NT; ++t) red[((wave - half) * NT + t) * 64 + lane] = acc[t];
+      __syncthreads();
+      if (wave < half)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) red[((wave - half) * MT * NT + a * NT + t) * 64 + lane] = acc[a][t];
-    __syncthreads();
-    if (wave < half)
-#pragma unroll
-      for (int a = 0; a < MT; ++a)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[a][t] += red[(wave * MT * NT + a * NT + t) * 64 + lane];
-    __syncthreads();
+        for (int t = 0; t < NT; ++t) acc[t] += red[(wave * NT + t) * 64 + lane];
+      __syncthreads();
+    }
+    if (wave != 0) return;
   }
-  if (wave != 0) return;
 #pragma unroll
-  for (int a = 0; a < MT; ++a)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * a + 4 * lq + r, j = 16 * t + lr;
-        if (i < tile.count && j < R) o[static_cast<size_t>(rows[i]) * R + j] = acc[a][t][r];
-      }
+    for (int r = 0; r < 4; ++r) {
+      const int i = m0 + 4 * lq + r, j = 16 * t + lr;
+      if (i < tile.count && j < R) o[static_cast<size_t>(rows[i]) * R + j] = acc[t][r];
+    }
 }
 
 // --- expand: out[m][c] = binary16(base[m][c] + s_i sum_j h[m][j] w_i[c][j]) ---------------
@@ -409,150 +405,144 @@ __device__ __forceinline__ half8_t expand_run(const float4_t (&acc)[8], int u, u
 // --- split: h or g (the sum of S slices) as ready MFMA operands ---------------------------
 //
 // One workgroup per slot of 32 rows of one adapter and task, once per call instead of by
-// every workgroup of 128 channels that multiplies with h.
-//   kByRank (outer)   fragment t: lane (r, q) has rank 16 t + r of rows 8 q .. 8 q + 7, in
+// every workgroup of 128 channels that multiplies with h.  The sum goes through LDS, from
+// where it is written in either or both of two orders:
+//   by_rank (outer)   fragment t: lane (r, q) has rank 16 t + r of rows 8 q .. 8 q + 7, in
 //                     units of 2^exps[slot]; [slots][NT][hi, lo][64][8]
-//   kByRow (stream)   group g of 16 rows, fragment f: lane (r, q) has ranks 32 f + 8 q .. + 7
+//   by_row (stream)   group g of 16 rows, fragment f: lane (r, q) has ranks 32 f + 8 q .. + 7
 //                     of row 16 g + r, in units of 2^e of that row, with factors[row of the
 //                     slot] = s_i 2^e; [slots][2][F][hi, lo][64][8].  R <= 16: one fragment
 //                     with hi of ranks 0 .. 15 in its first two quarters and lo in the
 //                     others; [slots][2][64][8]
-// Rows past the slot's count and ranks past R are zero.  The by-row task also writes the
-// summed h, the slot table (rows, adapter, count) and, for rows without an adapter, h = 0.
-enum SplitKind { kByRank, kByRow };
-
+// Rows past the slot's count and ranks past R are zero.  A by-row task also writes the slot
+// table and, where wanted, the summed h (0 for rows without an adapter).
 struct SplitTask {
   const float* h;    // [S][M][R]
   int S;
-  int kind;
-  half_t* frags;
-  int32_t* exps;     // by rank: [slots]
-  float* factors;    // by row: [slots][32]
-  float* sum;        // by row: [M][R] or NULL
+  half_t* by_rank;   // or NULL
+  int32_t* exps;     // [slots]
+  half_t* by_row;    // or NULL
+  float* factors;    // [slots][32]
+  float* sum;        // [M][R] or NULL
 };
 
 constexpr int kSlotRows = 32;
+constexpr int kMaxRank = 128;
 
 struct SlotTable {
   int2* meta;        // [slots] adapter (L: none), count (0: empty slot)
   int32_t* rows;     // [slots][32], entries past the count repeat the first
 };
 
-// Fragments of a row group by row, and halves (hi, lo) of each.
+// By-row operands (of 1 KB) of a row group.
 __host__ __device__ constexpr int row_frags(int R) { return R <= 16 ? 1 : 2 * ((R + 31) / 32); }
 
-__global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask t1, SplitTask t2,
-                                                         const float* __restrict__ scaling, SlotTable table,
-                                                         RowPlan plan, int R) {
+__global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask t1, const float* __restrict__ scaling,
+                                                         SlotTable table, RowPlan plan, int R) {
   __shared__ int32_t rows[kSlotRows];
   __shared__ float tops[4];
-  const SplitTask task = blockIdx.y == 0 ? t0 : blockIdx.y == 1 ? t1 : t2;
+  __shared__ float row_top[kSlotRows];
+  __shared__ float4_t sums[kSlotRows * (kMaxRank / 4 + 1)];   // rows of R / 4 + 1
+  const SplitTask task = blockIdx.y == 0 ? t0 : t1;
   const int slot = blockIdx.x;
   const Tile tile = find_tile<kSlotRows>(plan, slot, rows);
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lq = lane >> 4;
   const size_t slice = static_cast<size_t>(plan.M) * R;
-  if (task.kind == kByRow) {
+  if (task.by_row) {
     if (tid == 0) table.meta[slot] = int2{tile.adapter, tile.count};
-    if (tile.count == 0) return;
-    if (tid < kSlotRows) table.rows[slot * kSlotRows + tid] = rows[tid < tile.count ? tid : 0];
-    if (tile.adapter == plan.L) {
-      if (task.sum)
-        for (int i = tid; i < tile.count * R; i += 256) task.sum[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
-      return;
-    }
-    // wavefronts 0, 1: row groups 0, 1 (a lane holds at most 4 fragments of 8 ranks)
-    if (wave >= 2) return;
-    const int m = 16 * wave + lr;
-    const bool mine = m < tile.count;
-    const size_t at = static_cast<size_t>(rows[mine ? m : 0]) * R;
-    const bool packed = R <= 16;
-    const int F = packed ? 1 : (R + 31) / 32;
-    float v[4][8];
-    float top = 0.0f;
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const int j0 = packed ? 8 * (lq & 1) : 32 * f + 8 * lq;
-      const bool in = f < F && j0 < R && mine;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[f][j] = 0.0f;
-      if (!in) continue;
-      sum_slices8(task.h + at + j0, slice, task.S, v[f]);
-      if (task.sum && (!packed || lq < 2)) {
-        *reinterpret_cast<float4_t*>(task.sum + at + j0) = float4_t{v[f][0], v[f][1], v[f][2], v[f][3]};
-        *reinterpret_cast<float4_t*>(task.sum + at + j0 + 4) = float4_t{v[f][4], v[f][5], v[f][6], v[f][7]};
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_magnitude(v[f][j]));
-    }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const int shift = kSplitTop - top_exponent(top);
-    const float si = scaling ? scaling[tile.adapter] : 1.0f;
-    if (lq == 0) task.factors[slot * kSlotRows + m] = __builtin_ldexpf(si, -shift);
-    half8_t* o = reinterpret_cast<half8_t*>(task.frags) + (static_cast<size_t>(slot) * 2 + wave) * row_frags(R) * 64 + lane;
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      if (f >= F) break;
-      half8_t hi, lo;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        half_t a, b;
-        split_half(v[f][j], shift, a, b);
-        hi[j] = packed && lq >= 2 ? b : a;
-        lo[j] = b;
-      }
-      if (packed) {
-        o[0] = hi;
-      } else {
-        o[2 * f * 64] = hi;
-        o[(2 * f + 1) * 64] = lo;
-      }
-    }
+    if (tid < kSlotRows && tile.count > 0) table.rows[slot * kSlotRows + tid] = rows[tid < tile.count ? tid : 0];
+  }
+  if (tile.count == 0) return;
+  if (tile.adapter == plan.L) {
+    if (task.sum)
+      for (int i = tid; i < tile.count * R; i += 256) task.sum[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
     return;
   }
-  if (tile.count == 0 || tile.adapter == plan.L) return;
-  const int NT = (R + 15) >> 4;
-  float v[2][8];   // at most 8 fragments: two per wavefront
+  const int quads = R >> 2, ld = quads + 1;
   float top = 0.0f;
+  for (int i = tid; i < kSlotRows * quads; i += 256) {
+    const int m = i / quads, j = i % quads;
+    float4_t v = {};
+    if (m < tile.count) {
+      const size_t at = static_cast<size_t>(rows[m]) * R + 4 * j;
+      for (int s0 = 0; s0 < task.S; s0 += 8) {
+        float4_t p[8];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int j = 16 * (wave + 4 * k) + lr;
+        for (int k = 0; k < 8; ++k)
+          p[k] = *reinterpret_cast<const float4_t*>(task.h + min(s0 + k, task.S - 1) * slice + at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
-    if (16 * (wave + 4 * k) >= R) continue;
-    for (int s = 0; s < task.S; ++s)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[k][i] += task.h[s * slice + static_cast<size_t>(rows[8 * lq + i]) * R + min(j, R - 1)];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (j >= R || 8 * lq + i >= tile.count) v[k][i] = 0.0f;
-      top = fmaxf(top, finite_magnitude(v[k][i]));
+        for (int k = 0; k < 8; ++k)
+          if (s0 + k < task.S) v += p[k];
+      }
+      if (task.sum) *reinterpret_cast<float4_t*>(task.sum + at) = v;
     }
+    sums[m * ld + j] = v;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) top = fmaxf(top, finite_magnitude(v[k]));
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
   if (lane == 0) tops[wave] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-  const int e = top > 0.0f ? top_exponent(top) - kSplitTop : kNoExponent;
-  if (tid == 0) task.exps[slot] = e;
+  const float* f = reinterpret_cast<const float*>(sums);
+  if (task.by_rank) {
+    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+    const int e = top > 0.0f ? top_exponent(top) - kSplitTop : kNoExponent;
+    if (tid == 0) task.exps[slot] = e;
+    const int NT = (R + 15) >> 4;
+    for (int t = wave; t < NT; t += 4) {
+      const int j = 16 * t + lr;
+      half8_t hi, lo;
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int t = wave + 4 * k;
-    if (t >= NT) continue;
+      for (int i = 0; i < 8; ++i) {
+        half_t a, b;
+        split_half(j < R ? f[(8 * lq + i) * 4 * ld + j] : 0.0f, e == kNoExponent ? 0 : -e, a, b);
+        hi[i] = a;
+        lo[i] = b;
+      }
+      half8_t* o = reinterpret_cast<half8_t*>(task.by_rank) + (static_cast<size_t>(slot) * NT + t) * 128 + lane;
+      o[0] = hi;
+      o[64] = lo;
+    }
+  }
+  if (!task.by_row) return;
+  // largest of every row: 8 threads per row
+  {
+    const int m = tid >> 3;
+    float rt = 0.0f;
+    for (int j = tid & 7; j < R; j += 8) rt = fmaxf(rt, finite_magnitude(f[m * 4 * ld + j]));
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) rt = fmaxf(rt, __shfl_xor(rt, d));
+    if ((tid & 7) == 0) {
+      row_top[m] = rt;
+      const float si = scaling ? scaling[tile.adapter] : 1.0f;
+      task.factors[slot * kSlotRows + m] = __builtin_ldexpf(si, top_exponent(rt) - kSplitTop);
+    }
+  }
+  __syncthreads();
+  const bool packed = R <= 16;
+  const int F = packed ? 1 : (R + 31) / 32;
+  for (int i = wave; i < 2 * F; i += 4) {   // operand pairs (row group, fragment)
+    const int g = i / F, k = i % F;
+    const int m = 16 * g + lr;
+    const int j0 = packed ? 8 * (lq & 1) : 32 * k + 8 * lq;
+    const int shift = kSplitTop - top_exponent(row_top[m]);
     half8_t hi, lo;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int j = 0; j < 8; ++j) {
       half_t a, b;
-      split_half(v[k][i], e == kNoExponent ? 0 : -e, a, b);
-      hi[i] = a;
-      lo[i] = b;
+      split_half(j0 < R ? f[m * 4 * ld + j0 + j] : 0.0f, shift, a, b);
+      hi[j] = packed && lq >= 2 ? b : a;
+      lo[j] = b;
     }
-    half8_t* o = reinterpret_cast<half8_t*>(task.frags) + (static_cast<size_t>(slot) * NT + t) * 128 + lane;
-    o[0] = hi;
-    o[64] = lo;
+    half8_t* o = reinterpret_cast<half8_t*>(task.by_row) + ((static_cast<size_t>(slot) * 2 + g) * row_frags(R)) * 64 + lane;
+    if (packed) {
+      o[0] = hi;
+    } else {
+      o[2 * k * 64] = hi;
+      o[(2 * k + 1) * 64] = lo;
+    }
   }
 }
 
@@ -771,17 +761,32 @@ __global__ __launch_bounds__(256) void lora_stream_kernel(const half_t* __restri
   }
 }
 
-// --- transpose: b [L][N][R] -> bt [L][R][N], the layout the shrink reads ------------------
-constexpr int kTransposeRows = 128;
+// --- prepare: what the backward pass needs before its products, in one launch --------------
+//
+// Workgroups 0 .. plans - 1 group the rows; the others transpose b [L][N][R] to bt [L][R][N],
+// the layout the shrink reads, through LDS, about 8192 values at a time.
+constexpr int kTransposeValues = 8192;
 
-__global__ __launch_bounds__(256) void lora_transpose_kernel(const half_t* __restrict__ b, half_t* __restrict__ bt,
-                                                             int N, int R) {
-  extern __shared__ __align__(16) half_t tile[];   // [kTransposeRows][R + 2]
-  const int n0 = blockIdx.x * kTransposeRows, nr = min(kTransposeRows, N - n0);
-  const half_t* src = b + (static_cast<size_t>(blockIdx.y) * N + n0) * R;
-  half_t* dst = bt + static_cast<size_t>(blockIdx.y) * R * N + n0;
+__host__ __device__ constexpr int transpose_rows(int R) { return (kTransposeValues / R) & ~7; }
+
+__global__ __launch_bounds__(1024) void lora_prepare_kernel(RowPlan plan, int32_t* __restrict__ off,
+                                                            int32_t* __restrict__ perm, int plans,
+                                                            const half_t* __restrict__ b, half_t* __restrict__ bt, int N,
+                                                            int R) {
+  __shared__ int part[2][16];
+  __shared__ half_t tile[kTransposeValues + kTransposeValues / 4];   // rows of R + 2 values, R >= 8
+  if (static_cast<int>(blockIdx.x) < plans) {
+    plan_rows(blockIdx.x, plan.index, plan.M, plan.L, off, perm, part);
+    return;
+  }
+  const int nrow = transpose_rows(R), nblk = (N + nrow - 1) / nrow;
+  const int blk = blockIdx.x - plans;
+  const size_t ad = blk / nblk;
+  const int n0 = (blk % nblk) * nrow, nr = min(nrow, N - n0);
+  const half_t* src = b + (ad * N + n0) * R;
+  half_t* dst = bt + ad * R * N + n0;
   const int ld = R + 2;
-  for (int i = threadIdx.x; i < nr * R / 8; i += 256) {
+  for (int i = threadIdx.x; i < nr * R / 8; i += 1024) {
     const half8_t v = *reinterpret_cast<const half8_t*>(src + 8 * i);
     const int n = 8 * i / R, j = 8 * i % R;
 #pragma unroll
@@ -789,7 +794,7 @@ __global__ __launch_bounds__(256) void lora_transpose_kernel(const half_t* __res
   }
   __syncthreads();
   const int oct = nr / 8;   // N % 8 == 0
-  for (int i = threadIdx.x; i < R * oct; i += 256) {
+  for (int i = threadIdx.x; i < R * oct; i += 1024) {
     const int j = i / oct, n = 8 * (i % oct);
     half8_t v;
 #pragma unroll
@@ -810,6 +815,8 @@ __global__ __launch_bounds__(256) void lora_transpose_kernel(const half_t* __res
 // the operands.  A slot's missing rows repeat its first one against zero operands.
 // Q8: x is an 8-bit checkpoint, expanded after the transpose (which then moves bytes).
 // CMAJOR: gradient [L][C][R] (channels are MFMA rows), else [L][R][C].
+// Few channels leave compute units idle, so the slots are dealt to `parts` workgroups (the
+// low part of blockIdx.y), each with a gradient of its own, added by lora_sum_parts_kernel.
 template <int NT, bool Q8>
 struct OuterSlot {
   uint4 v[8];              // 8 rows of 8 channels (Q8: the codes in x and y)
@@ -826,13 +833,14 @@ __global__ __launch_bounds__(64 * W) void lora_outer_kernel(const half_t* __rest
                                                             const half_t* __restrict__ frags,
                                                             const int32_t* __restrict__ exps,
                                                             const float* __restrict__ scaling, RowPlan plan,
-                                                            float* __restrict__ grad, int C, int R) {
+                                                            float* __restrict__ grad, int C, int R, int parts) {
   __shared__ float4_t red[W * NT * 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int c0 = blockIdx.x * 128;
-  const int t0 = blockIdx.y * NT;
+  const int part = blockIdx.y % parts;
+  const int t0 = (blockIdx.y / parts) * NT;
   const int ad = blockIdx.z;
   const int NTT = (R + 15) >> 4;   // fragments per slot
   // slots of the adapter: [first_slot, first_slot + n); positions lo .. hi - 1
@@ -926,26 +934,27 @@ __global__ __launch_bounds__(64 * W) void lora_outer_kernel(const half_t* __rest
 
   if (n > 0) {
     OuterSlot<NT, Q8> ring[D];
-    find_rows(wave);
+    const int first = part * W + wave, stride = parts * W;
+    find_rows(first);
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      load(wave + d * W, ring[d]);
-      find_rows(wave + (d + 1) * W);
+      load(first + d * stride, ring[d]);
+      find_rows(first + (d + 1) * stride);
     }
-    for (int k = wave; k < n; k += D * W) {
+    for (int k = first; k < n; k += D * stride) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (k + d * W >= n) break;
+        if (k + d * stride >= n) break;
         add(ring[d]);
-        load(k + (d + D) * W, ring[d]);
-        find_rows(k + (d + D + 1) * W);
+        load(k + (d + D) * stride, ring[d]);
+        find_rows(k + (d + D + 1) * stride);
       }
     }
   }
 
   // Sum over the wavefronts, one channel fragment at a time, in units of 1.
   const float si = scaling ? scaling[ad] : 1.0f;
-  float* g = grad + static_cast<size_t>(ad) * R * C;
+  float* g = grad + (static_cast<size_t>(part) * plan.L + ad) * R * C;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     __syncthreads();
@@ -969,6 +978,23 @@ __global__ __launch_bounds__(64 * W) void lora_outer_kernel(const half_t* __rest
       }
     }
   }
+}
+
+// out = sum of the parts, in order; both gradients in one launch (blockIdx.y).
+struct PartsTask {
+  const float4_t* parts;
+  float4_t* out;
+  size_t quads;
+  int count;
+};
+
+__global__ __launch_bounds__(256) void lora_sum_parts_kernel(PartsTask t0, PartsTask t1) {
+  const PartsTask t = blockIdx.y == 0 ? t0 : t1;
+  const size_t i = static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= t.quads) return;
+  float4_t v = t.parts[i];
+  for (int p = 1; p < t.count; ++p) v += t.parts[p * t.quads + i];
+  t.out[i] = v;
 }
 
 }  // namespace w4a16
