@@ -134,36 +134,34 @@ int plan_slots(int M, int L, bool with_index) {
 
 // --- shrink -------------------------------------------------------------------------
 
-// Tiles of 64 rows once an adapter has that many on average; below, tiles of 16 rows with
-// the wavefronts along the channels.
-bool shrink_tall(int M, int L) { return M / L >= 64; }
+// Rows per tile of a shrink, in 16s (wavefronts): 128 or 64 rows, once an adapter has twice
+// that many on average, else 16 with the wavefronts along the channels.
+int shrink_waves(int M, int L) { return M / L >= 256 ? 8 : M / L >= 64 ? 4 : 1; }
 
-// Slices of the long axis: enough workgroups for four per compute unit (few rows: one), at
-// least 512 channels each, and sums of the slices that stay small (4 MB) or a quarter of x.
+// Slices of the long axis: enough workgroups for the GPU (8 wavefronts per compute unit),
+// at least 256 channels each (few rows: 512), and sums of the slices that stay small (4 MB)
+// or a quarter of x.
 int shrink_slices(int M, int L, int R, int C) {
-  const bool tall = shrink_tall(M, L);
-  const int want = ceil_div(tall ? 1024 : 256, ceil_div(M, tall ? 64 : 16));
+  const int waves = shrink_waves(M, L);
+  const int want = ceil_div(waves == 4 ? 512 : 256, ceil_div(M, 16 * waves));
   const int64_t light = std::max<int64_t>(C / (16 * R), (int64_t{1} << 20) / (static_cast<int64_t>(M) * R));
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, C / 512, 16, light})));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, C / (waves == 1 ? 512 : 256), 16, light})));
 }
 
 void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, int R, int S, float* out, hipStream_t st) {
-  const bool tall = shrink_tall(plan.M, plan.L);
-  const dim3 grid(tile_slots(plan, tall ? 64 : 16) * S), block(256);
-#define W4A16_SHRINK(NT_, TALL_, D_) \
-  hipLaunchKernelGGL((lora_shrink_kernel<NT_, TALL_, D_>), grid, block, 0, st, x, w, plan, C, R, S, out)
+  const int waves = shrink_waves(plan.M, plan.L);
+  const dim3 grid(tile_slots(plan, 16 * waves) * S);
+#define W4A16_SHRINK(NT_, D_) \
+  do { \
+    if (waves == 8) hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 8>), grid, dim3(512), 0, st, x, w, plan, C, R, S, out); \
+    else if (waves == 4) hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 4>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
+    else hipLaunchKernelGGL((lora_shrink_kernel<NT_, D_>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
+  } while (0)
   const int nt = ceil_div(R, 16);
-  if (tall) {
-    if (nt == 1) W4A16_SHRINK(1, true, 8);
-    else if (nt == 2) W4A16_SHRINK(2, true, 6);
-    else if (nt <= 4) W4A16_SHRINK(4, true, 4);
-    else W4A16_SHRINK(8, true, 2);
-  } else {
-    if (nt == 1) W4A16_SHRINK(1, false, 4);
-    else if (nt == 2) W4A16_SHRINK(2, false, 4);
-    else if (nt <= 4) W4A16_SHRINK(4, false, 4);
-    else W4A16_SHRINK(8, false, 2);
-  }
+  if (nt == 1) W4A16_SHRINK(1, 4);
+  else if (nt == 2) W4A16_SHRINK(2, 4);
+  else if (nt <= 4) W4A16_SHRINK(4, 4);
+  else W4A16_SHRINK(8, 2);
 #undef W4A16_SHRINK
 }
 

@@ -183,26 +183,25 @@ constexpr int kNoExponent = -1000;   // of values that are all zero
 // --- shrink: out[s][m][j] = sum over the channels of slice s of x[m][c] w[i][j][c] -------
 //
 // x [M][C], w [L][R][C], C % 8 == 0.  A wavefront holds 16 rows x 16 NT ranks of sums and
-// walks steps of 32 channels, both operands as they lie in memory (lane (r, q): row r,
-// channels 8 q .. 8 q + 7 of the step), D steps in flight.  A row's result depends on its
-// own x alone, so the rows repeated to fill a tile are computed and not stored.
-//   TALL == false, few rows: a tile of 16 rows per workgroup, whose 4 wavefronts take turns
-//     (pairs of steps) along the slice and are added in LDS in a fixed order.
-//   TALL: a tile of 64 rows, 16 per wavefront; all of them walk the whole slice together,
-//     so that w comes from the L1 after the first.  w is read once per tile of 64 rows; the
-//     slices are dealt to neighbouring workgroups, so an XCD's L2 holds the w of few slices.
+// walks steps of 32 channels, x as it lies in memory (lane (r, q): row r, channels 8 q ..
+// 8 q + 7 of the step).  A row's result depends on its own x alone, so the rows repeated to
+// fill a tile are computed and not stored.  Consecutive workgroups take the slices of one
+// tile, so that an XCD's L2 holds the w of few slices.
+
+// Few rows: a tile of 16 rows per workgroup, whose W wavefronts take turns (pairs of steps)
+// along the slice, w as it lies in memory, D steps in flight; their sums are added in LDS
+// in a fixed order.
 template <int NT>
 struct ShrinkStep {
   half8_t x, w[NT];
 };
 
-template <int NT, bool TALL, int D>
+template <int NT, int D>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restrict__ x, const half_t* __restrict__ w,
                                                           RowPlan plan, int C, int R, int S, float* __restrict__ out) {
-  constexpr int T = TALL ? 64 : 16;
-  constexpr int W = 4;
+  constexpr int T = 16, W = 4;
   __shared__ int32_t rows[T];
-  __shared__ float4_t red[TALL ? 1 : W / 2 * NT * 64];
+  __shared__ float4_t red[W / 2 * NT * 64];
   const int s = blockIdx.x % S;
   const Tile tile = find_tile<T>(plan, blockIdx.x / S, rows);
   if (tile.count == 0) return;
@@ -211,12 +210,10 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
   const int lr = lane & 15, lq = lane >> 4;
   float* o = out + static_cast<size_t>(s) * plan.M * R;
   if (tile.adapter == plan.L) {
-    for (int i = tid; i < tile.count * R; i += 256) o[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+    for (int i = tid; i < tile.count * R; i += 64 * W) o[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
     return;
   }
-  const int m0 = TALL ? 16 * wave : 0;
-  if (m0 >= tile.count) return;   // TALL has no barrier from here on
-  const half_t* xr = x + static_cast<size_t>(rows[m0 + lr]) * C;
+  const half_t* xr = x + static_cast<size_t>(rows[lr]) * C;
   const half_t* wr[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -227,9 +224,9 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
   const int b = static_cast<int>(static_cast<int64_t>(steps) * s / S);
   const int e = static_cast<int>(static_cast<int64_t>(steps) * (s + 1) / S);
   // Step k of this wavefront, of n.  Loads past the slice are clamped into it, not used.
-  auto step_of = [&](int k) { return TALL ? b + k : b + 2 * (wave + (k >> 1) * W) + (k & 1); };
+  auto step_of = [&](int k) { return b + 2 * (wave + (k >> 1) * W) + (k & 1); };
   const int whole = (e - b) / (2 * W), rest = (e - b) % (2 * W);
-  const int n = TALL ? e - b : 2 * whole + max(0, min(2, rest - 2 * wave));
+  const int n = 2 * whole + max(0, min(2, rest - 2 * wave));
   auto load = [&](int k, ShrinkStep<NT>& o) {
     const int c = min(min(step_of(k), e - 1) * 32 + 8 * lq, C - 8);
     o.x = *reinterpret_cast<const half8_t*>(xr + c);
@@ -267,25 +264,126 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
 #pragma unroll
   for (int d = 0; d < D; ++d)
     if (k + d + D < n) add(k + d + D, ring[d]);
-  if constexpr (!TALL) {
 #pragma unroll
-    for (int half = W / 2; half > 0; half >>= 1) {
-      if (wave >= half && wave < 2 * half)
+  for (int half = W / 2; half > 0; half >>= 1) {
+    if (wave >= half && wave < 2 * half)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) red[((wave - half) * NT + t) * 64 + lane] = acc[t];
-      __syncthreads();
-      if (wave < half)
+      for (int t = 0; t < NT; ++t) red[((wave - half) * NT + t) * 64 + lane] = acc[t];
+    __syncthreads();
+    if (wave < half)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[t] += red[(wave * NT + t) * 64 + lane];
-      __syncthreads();
+      for (int t = 0; t < NT; ++t) acc[t] += red[(wave * NT + t) * 64 + lane];
+    __syncthreads();
+  }
+  if (wave != 0) return;
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int i = 4 * lq + r, j = 16 * t + lr;
+      if (i < tile.count && j < R) o[static_cast<size_t>(rows[i]) * R + j] = acc[t][r];
     }
-    if (wave != 0) return;
+}
+
+// Many rows: HBM-bound on x.  A tile of 16 W rows per workgroup, 16 per wavefront, so that w
+// is read once per tile; it goes through LDS (two buffers of 128 channels in operand order,
+// conflict-free 16-byte accesses) while x streams into registers two chunks ahead.  With w
+// read by every wavefront for itself the kernel was bound by L2 traffic: 4096 rows x 28672
+// channels at rank 64 took 83 us with 64 rows per wavefront, 138 us with 16.
+// The barrier orders LDS only: the x and w loads in flight pass it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int NT, int W>
+__global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* __restrict__ x,
+                                                                  const half_t* __restrict__ w, RowPlan plan, int C,
+                                                                  int R, int S, float* __restrict__ out) {
+  constexpr int T = 16 * W, SC = 4;                       // steps per chunk
+  constexpr int kPieces = NT * 16 * SC * 4;               // 16-byte pieces of w per chunk
+  constexpr int PT = (kPieces + 64 * W - 1) / (64 * W);   // per thread
+  __shared__ int32_t rows[T];
+  __shared__ half8_t lds[2][SC * NT * 64];
+  const int s = blockIdx.x % S;
+  const Tile tile = find_tile<T>(plan, blockIdx.x / S, rows);
+  if (tile.count == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  float* o = out + static_cast<size_t>(s) * plan.M * R;
+  if (tile.adapter == plan.L) {
+    for (int i = tid; i < tile.count * R; i += 64 * W) o[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+    return;
+  }
+  const half_t* xr = x + static_cast<size_t>(rows[16 * wave + lr]) * C;
+  const half_t* wl = w + static_cast<size_t>(tile.adapter) * R * C;
+  const int chunks = (C + 32 * SC - 1) / (32 * SC);
+  const int b = static_cast<int>(static_cast<int64_t>(chunks) * s / S);
+  const int e = static_cast<int>(static_cast<int64_t>(chunks) * (s + 1) / S);
+  float4_t acc[NT] = {};
+  half8_t wreg[PT];
+  half8_t xs[2][SC];
+  // Loads past the slice or past C are clamped; channels past C are zeroed on both sides.
+  auto load_w = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int p = min(tid + 64 * W * i, kPieces - 1);
+      const int j = min(p / (SC * 4), R - 1), q = p % (SC * 4);
+      wreg[i] = *reinterpret_cast<const half8_t*>(wl + static_cast<size_t>(j) * C + min(min(k, e - 1) * 32 * SC + 8 * q, C - 8));
+    }
+  };
+  auto store_w = [&](int k, int buf) {
+#pragma unroll
+    for (int i = 0; i < PT; ++i) {
+      const int p = tid + 64 * W * i;
+      const int j = p / (SC * 4), q = p % (SC * 4);
+      const bool in = k * 32 * SC + 8 * q < C;
+      if (kPieces % (64 * W) == 0 || p < kPieces)
+        lds[buf][((q >> 2) * NT + (j >> 4)) * 64 + (q & 3) * 16 + (j & 15)] = in ? wreg[i] : half8_t{};
+    }
+  };
+  auto load_x = [&](int k, half8_t (&v)[SC]) {
+#pragma unroll
+    for (int u = 0; u < SC; ++u)
+      v[u] = *reinterpret_cast<const half8_t*>(xr + min(min(k, e - 1) * 32 * SC + 32 * u + 8 * lq, C - 8));
+  };
+  auto add = [&](int k, int buf, half8_t (&v)[SC]) {
+    if ((k + 1) * 32 * SC > C)
+#pragma unroll
+      for (int u = 0; u < SC; ++u) v[u] = k * 32 * SC + 32 * u + 8 * lq < C ? v[u] : half8_t{};
+#pragma unroll
+    for (int u = 0; u < SC; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[u], lds[buf][(u * NT + t) * 64 + lane], acc[t], 0, 0, 0);
+  };
+  load_w(b);
+  load_x(b, xs[0]);
+  load_x(b + 1, xs[1]);
+  store_w(b, 0);
+  load_w(b + 1);
+  lds_barrier();
+  for (int k = b; k < e;) {
+    add(k, 0, xs[0]);
+    load_x(k + 2, xs[0]);
+    store_w(k + 1, 1);
+    load_w(k + 2);
+    lds_barrier();
+    if (++k >= e) break;
+    add(k, 1, xs[1]);
+    load_x(k + 2, xs[1]);
+    store_w(k + 1, 0);
+    load_w(k + 2);
+    lds_barrier();
+    ++k;
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int i = m0 + 4 * lq + r, j = 16 * t + lr;
+      const int i = 16 * wave + 4 * lq + r, j = 16 * t + lr;
       if (i < tile.count && j < R) o[static_cast<size_t>(rows[i]) * R + j] = acc[t][r];
     }
 }
