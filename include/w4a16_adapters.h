@@ -37,8 +37,8 @@
 extern "C" {
 #endif
 
-/* Workspace bytes of w4a16_lora_forward; 0 on sizes that the call refuses.  with_index: 1
- * when index is not NULL. */
+/* Workspace bytes of w4a16_lora_forward: 0 where the call needs none (workspace may then be
+ * NULL), and on sizes that it refuses.  with_index: 1 when index is not NULL. */
 size_t w4a16_lora_forward_workspace(int M, int N, int K, int R, int L, int with_index);
 
 /* out[m] = binary16(y[m] + s_i B_i (A_i x[m])), i = index[m]: binary16 operands, fp32 sums,

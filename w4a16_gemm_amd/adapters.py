@@ -40,54 +40,65 @@ def _check(status: int) -> None:
         raise W4A16Error(status, _lib().w4a16_last_error().decode())
 
 
-def _operands(*specs):
+def _operands(specs):
     """Check (tensor, dtype, shape, name) rows, skipping absent tensors: types and shapes
     first, then that all of them are contiguous and on one ROCm device.  Returns it."""
-    import torch
+    Tensor = _torch().Tensor
     for t, dtype, shape, name in specs:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype != dtype:
-            raise TypeError(f"{name} must be a {dtype} tensor")
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t is not None:
+            if not isinstance(t, Tensor) or t.dtype != dtype:
+                raise TypeError(f"{name} must be a {dtype} tensor")
+            if t.shape != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     device = None
     for t, dtype, shape, name in specs:
-        if t is None:
-            continue
-        if not t.is_contiguous():
-            raise TypeError(f"{name} must be contiguous")
-        if not t.is_cuda:
-            raise TypeError(f"{name} must live on a ROCm device")
-        if device is None:
-            device = t.device
-        elif t.device != device:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+        if t is not None:
+            if not t.is_contiguous():
+                raise TypeError(f"{name} must be contiguous")
+            if device is None:
+                if not t.is_cuda:
+                    raise TypeError(f"{name} must live on a ROCm device")
+                device = t.device
+            elif t.device != device:
+                if not t.is_cuda:
+                    raise TypeError(f"{name} must live on a ROCm device")
+                raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
     return device
+
+
+@functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+    return torch
 
 
 @contextlib.contextmanager
 def _other(device, stream):
-    import torch
+    torch = _torch()
     with torch.cuda.device(device), torch.cuda.stream(stream):
         yield
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device, stream):
     """Context in which `device` is current and allocations belong to the call's stream."""
-    import torch
+    cuda = _torch().cuda
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"stream of {stream.device}, tensors on {device}")
         return _other(device, stream)
-    if torch.cuda.current_device() != device.index:
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    if cuda.current_device() != device.index:
+        return cuda.device(device)
+    return _HERE
 
 
 def _handle(device):
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    """Raw handle of the device's current stream (torch's own accessor for it where there is
+    one: the Stream object costs 1.7 us more)."""
+    raw = getattr(_torch()._C, "_cuda_getCurrentRawStream", None)
+    return _torch().cuda.current_stream(device).cuda_stream if raw is None else raw(device.index)
 
 
 def _ptr(t):
@@ -95,32 +106,33 @@ def _ptr(t):
 
 
 def _matrix(t, name):
-    import torch
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+    if not isinstance(t, _torch().Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-d tensor")
     return t.shape
 
 
-def _adapter_sizes(a, b, K, N):
-    import torch
-    if not isinstance(a, torch.Tensor) or a.dim() != 3:
+def _adapter_sizes(a):
+    if not isinstance(a, _torch().Tensor) or a.dim() != 3:
         raise ValueError("a must be a 3-d tensor [L][R][K]")
     return a.shape[0], a.shape[1]
 
 
 def _overlap(out, *others):
     """Refuse an output that shares memory with another operand."""
-    if out is None:
-        return
     lo, hi = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
     for t, name in others:
-        if t is not None and t is not out and t.data_ptr() < hi and lo < t.data_ptr() + t.numel() * t.element_size():
+        if t is not None and t.data_ptr() < hi and lo < t.data_ptr() + t.numel() * t.element_size():
             raise ValueError(f"an output overlaps {name}")
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(name, *sizes):
+    return getattr(_lib(), name)(*sizes)
+
+
 def _workspace(nbytes, device):
-    import torch
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    torch = _torch()
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def w4a16_lora_forward(y, x, a, b, index=None, scaling=None, out=None, h=None, stream=None):
@@ -132,41 +144,43 @@ def w4a16_lora_forward(y, x, a, b, index=None, scaling=None, out=None, h=None, s
     L): no adapter, the row passes through); scaling float32 [L] (None: 1).  Returns out
     (allocated unless given; out=y works in place).  h float32 [M][R], if given, receives
     A_i x for the backward pass."""
-    import torch
+    torch = _torch()
     M, K = _matrix(x, "x")
     N = _matrix(y, "y")[1]
-    L, R = _adapter_sizes(a, b, K, N)
+    L, R = _adapter_sizes(a)
     f16, f32 = torch.float16, torch.float32
-    device = _operands((x, f16, (M, K), "x"), (y, f16, (M, N), "y"), (a, f16, (L, R, K), "a"), (b, f16, (L, N, R), "b"),
-                       (index, torch.int32, (M,), "index"), (scaling, f32, (L,), "scaling"),
-                       (out, f16, (M, N), "out"), (h, f32, (M, R), "h"))
-    ins = ((x, "x"), (a, "a"), (b, "b"), (index, "index"), (scaling, "scaling"))
-    if out is not None:
-        if out.data_ptr() != y.data_ptr():
-            _overlap(out, (y, "y"))
-        _overlap(out, *ins, (h, "h"))
-    _overlap(h, *ins, (y, "y"))
-    lib = _lib()
+    device = _operands(((x, f16, (M, K), "x"), (y, f16, (M, N), "y"), (a, f16, (L, R, K), "a"), (b, f16, (L, N, R), "b"),
+                        (index, torch.int32, (M,), "index"), (scaling, f32, (L,), "scaling"),
+                        (out, f16, (M, N), "out"), (h, f32, (M, R), "h")))
+    if out is not None or h is not None:
+        ins = ((x, "x"), (a, "a"), (b, "b"), (index, "index"), (scaling, "scaling"))
+        if out is not None:
+            if out.data_ptr() != y.data_ptr():
+                _overlap(out, (y, "y"))
+            _overlap(out, *ins, (h, "h"))
+        if h is not None:
+            _overlap(h, *ins, (y, "y"))
     with _on(device, stream):
         if out is None:
             out = torch.empty_like(y)
-        need = lib.w4a16_lora_forward_workspace(M, N, K, R, L, index is not None)
+        need = _workspace_bytes("w4a16_lora_forward_workspace", M, N, K, R, L, index is not None)
         ws = _workspace(need, device)
-        _check(lib.w4a16_lora_forward(y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(index), _ptr(scaling),
-                                      M, N, K, R, L, out.data_ptr(), _ptr(h), ws.data_ptr(), need, _handle(device)))
+        _check(_lib().w4a16_lora_forward(y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(), _ptr(index),
+                                         _ptr(scaling), M, N, K, R, L, out.data_ptr(), _ptr(h), _ptr(ws), need,
+                                         _handle(device)))
     return out
 
 
 def _backward(dy, kept, specs, K, a, b, h, index, scaling, dx, out, need_dx, stream, entry):
-    import torch
+    torch = _torch()
     M, N = _matrix(dy, "dy")
-    L, R = _adapter_sizes(a, b, K, N)
+    L, R = _adapter_sizes(a)
     f16, f32 = torch.float16, torch.float32
-    device = _operands((dy, f16, (M, N), "dy"), *specs, (a, f16, (L, R, K), "a"), (b, f16, (L, N, R), "b"),
-                       (h, f32, (M, R), "h"), (index, torch.int32, (M,), "index"), (scaling, f32, (L,), "scaling"),
-                       (dx, f16, (M, K), "dx"), (out, f16, (M, K), "out"))
     if h is None:
         raise TypeError("h must be a torch.float32 tensor")
+    device = _operands(((dy, f16, (M, N), "dy"), *specs, (a, f16, (L, R, K), "a"), (b, f16, (L, N, R), "b"),
+                        (h, f32, (M, R), "h"), (index, torch.int32, (M,), "index"), (scaling, f32, (L,), "scaling"),
+                        (dx, f16, (M, K), "dx"), (out, f16, (M, K), "out")))
     if not need_dx and (dx is not None or out is not None):
         raise ValueError("need_dx=False takes neither dx nor out")
     if out is not None:
@@ -174,17 +188,16 @@ def _backward(dy, kept, specs, K, a, b, h, index, scaling, dx, out, need_dx, str
             _overlap(out, (dx, "dx"))
         _overlap(out, (dy, "dy"), (a, "a"), (b, "b"), (h, "h"), (index, "index"), (scaling, "scaling"),
                  *((s[0], s[3]) for s in specs))
-    lib = _lib()
     with _on(device, stream):
         if need_dx and out is None:
             out = torch.empty((M, K), dtype=f16, device=device)
         da = torch.empty((L, R, K), dtype=f32, device=device)
         db = torch.empty((L, N, R), dtype=f32, device=device)
-        need = lib.w4a16_lora_backward_workspace(M, N, K, R, L, index is not None)
+        need = _workspace_bytes("w4a16_lora_backward_workspace", M, N, K, R, L, index is not None)
         ws = _workspace(need, device)
-        _check(getattr(lib, entry)(dy.data_ptr(), *kept, a.data_ptr(), b.data_ptr(), h.data_ptr(), _ptr(index),
-                                   _ptr(scaling), _ptr(dx), M, N, K, R, L, _ptr(out), da.data_ptr(), db.data_ptr(),
-                                   ws.data_ptr(), need, _handle(device)))
+        _check(getattr(_lib(), entry)(dy.data_ptr(), *kept, a.data_ptr(), b.data_ptr(), h.data_ptr(), _ptr(index),
+                                      _ptr(scaling), _ptr(dx), M, N, K, R, L, _ptr(out), da.data_ptr(), db.data_ptr(),
+                                      _ptr(ws), need, _handle(device)))
     return out, da, db
 
 
@@ -195,9 +208,8 @@ def w4a16_lora_backward(dy, x, a, b, h, index=None, scaling=None, dx=None, out=N
     x (through the quantised weights) and is added to (None: 0); the sum goes to out
     (allocated unless given; out=dx works in place).  need_dx=False: dx is not computed and
     None is returned in its place."""
-    import torch
     M, K = _matrix(x, "x")
-    return _backward(dy, (x.data_ptr(),), ((x, torch.float16, (_matrix(dy, "dy")[0], K), "x"),), K, a, b, h, index,
+    return _backward(dy, (x.data_ptr(),), ((x, _torch().float16, (_matrix(dy, "dy")[0], K), "x"),), K, a, b, h, index,
                      scaling, dx, out, need_dx, stream, "w4a16_lora_backward")
 
 
@@ -205,7 +217,6 @@ def w4a16_lora_backward_q8(dy, codes, scales, group_size: int, a, b, h, index=No
                            need_dx=True, stream=None):
     """w4a16_lora_backward with x as an 8-bit checkpoint (codes, scales of
     w4a16_act_quantize): the same bits as from the restored x, which is never stored."""
-    import torch
     K = _matrix(codes, "codes")[1]
     rows = _matrix(dy, "dy")[0]
     specs = _checkpoint(codes, scales, group_size, rows, K)
@@ -216,7 +227,7 @@ def w4a16_lora_backward_q8(dy, codes, scales, group_size: int, a, b, h, index=No
 def _checkpoint(codes, scales, group_size, M, K):
     """Specs of a checkpoint's tensors (groups of a size that does not divide K are left to
     the library to refuse)."""
-    import torch
+    torch = _torch()
     G = K // group_size if group_size > 0 else 0
     if scales is None:
         raise TypeError("scales must be a torch.float16 tensor")
@@ -226,35 +237,36 @@ def _checkpoint(codes, scales, group_size, M, K):
 def w4a16_act_quantize(x, group_size: int, codes=None, scales=None, stream=None):
     """Keep x binary16 [M][K] in 8 bits: (codes uint8 [M][K], scales binary16
     [M][K/group_size]), group_size 32, 64 or 128 (allocated unless given)."""
-    import torch
+    torch = _torch()
     M, K = _matrix(x, "x")
     G = K // group_size if group_size > 0 else 0
-    device = _operands((x, torch.float16, (M, K), "x"), (codes, torch.uint8, (M, K), "codes"),
-                       (scales, torch.float16, (M, G), "scales"))
-    _overlap(codes, (x, "x"), (scales, "scales"))
-    _overlap(scales, (x, "x"))
-    lib = _lib()
+    device = _operands(((x, torch.float16, (M, K), "x"), (codes, torch.uint8, (M, K), "codes"),
+                        (scales, torch.float16, (M, G), "scales")))
+    if codes is not None:
+        _overlap(codes, (x, "x"), (scales, "scales"))
+    if scales is not None:
+        _overlap(scales, (x, "x"))
     with _on(device, stream):
         if codes is None:
             codes = torch.empty((M, K), dtype=torch.uint8, device=device)
         if scales is None:
             scales = torch.empty((M, G), dtype=torch.float16, device=device)
-        _check(lib.w4a16_act_quantize(x.data_ptr(), M, K, group_size, codes.data_ptr(), scales.data_ptr(),
-                                      _handle(device)))
+        _check(_lib().w4a16_act_quantize(x.data_ptr(), M, K, group_size, codes.data_ptr(), scales.data_ptr(),
+                                         _handle(device)))
     return codes, scales
 
 
 def w4a16_act_dequantize(codes, scales, group_size: int, out=None, stream=None):
     """binary16 [M][K] from a checkpoint: binary16((codes - 128) * scale)."""
-    import torch
+    torch = _torch()
     M, K = _matrix(codes, "codes")
     specs = _checkpoint(codes, scales, group_size, M, K)
-    device = _operands(*specs, (out, torch.float16, (M, K), "out"))
-    _overlap(out, (codes, "codes"), (scales, "scales"))
-    lib = _lib()
+    device = _operands((*specs, (out, torch.float16, (M, K), "out")))
+    if out is not None:
+        _overlap(out, (codes, "codes"), (scales, "scales"))
     with _on(device, stream):
         if out is None:
             out = torch.empty((M, K), dtype=torch.float16, device=device)
-        _check(lib.w4a16_act_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, group_size, out.data_ptr(),
-                                        _handle(device)))
+        _check(_lib().w4a16_act_dequantize(codes.data_ptr(), scales.data_ptr(), M, K, group_size, out.data_ptr(),
+                                           _handle(device)))
     return out

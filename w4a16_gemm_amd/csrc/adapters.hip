@@ -128,8 +128,10 @@ void run_plan(const RowPlan& p, hipStream_t st) {
                        const_cast<int32_t*>(p.off), const_cast<int32_t*>(p.perm));
 }
 
+int tiles_of(const RowPlan& p, int T) { return tile_slots(p.M, p.L, p.index != nullptr, p.off != nullptr, T); }
+
 int plan_slots(int M, int L, bool with_index) {
-  return with_index ? M / kSlotRows + L + 1 : ceil_div(M, kSlotRows);
+  return tile_slots(M, L, with_index, true, kSlotRows);
 }
 
 // --- shrink -------------------------------------------------------------------------
@@ -150,7 +152,7 @@ int shrink_slices(int M, int L, int R, int C) {
 
 void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, int R, int S, float* out, hipStream_t st) {
   const int waves = shrink_waves(plan.M, plan.L);
-  const dim3 grid(tile_slots(plan, 16 * waves) * S);
+  const dim3 grid(tiles_of(plan, 16 * waves) * S);
 #define W4A16_SHRINK(NT_, D_) \
   do { \
     if (waves == 8) hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 8>), grid, dim3(512), 0, st, x, w, plan, C, R, S, out); \
@@ -167,12 +169,9 @@ void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, in
 
 // --- expand -------------------------------------------------------------------------
 
-// From this many rows on the expand takes ready operands (one launch more).
-constexpr int kStreamRows = 256;
-
 void run_expand(const float* h, int S, const half_t* w, const float* scaling, const RowPlan& plan, const half_t* base,
                 half_t* out, float* h_out, int C, int R, hipStream_t st) {
-  const dim3 grid(tile_slots(plan, 16), ceil_div(C, 512)), block(256);
+  const dim3 grid(tiles_of(plan, 16), ceil_div(C, 512)), block(256);
 #define W4A16_EXPAND(F_, P_) \
   hipLaunchKernelGGL((lora_expand_kernel<F_, P_>), grid, block, 0, st, h, S, w, scaling, plan, base, out, h_out, C, R)
   if (R <= 16) W4A16_EXPAND(1, true);
@@ -183,29 +182,50 @@ void run_expand(const float* h, int S, const half_t* w, const float* scaling, co
 #undef W4A16_EXPAND
 }
 
-template <bool TRANS, bool BASE>
-void run_stream_base(const ByRow& h, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C, int R,
-                     int L, int slots, hipStream_t st) {
-  const int blocks = ceil_div(C, 512);
-  // about 1024 workgroups (two rounds of two per compute unit), 64 slots at most
-  const int group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, static_cast<int64_t>(slots) * blocks / 1024)));
-  const dim3 grid(blocks * ceil_div(slots, group)), block(256);
-#define W4A16_STREAM(F_, P_, D_) \
-  hipLaunchKernelGGL((lora_stream_kernel<F_, P_, TRANS, BASE, D_>), grid, block, 0, st, h.frags, h.factors, table, w, base, \
-                     out, C, R, L, slots, group)
-  if (R <= 16) W4A16_STREAM(1, true, 3);
-  else if (R <= 32) W4A16_STREAM(1, false, 3);
-  else if (R <= 64) W4A16_STREAM(2, false, 2);
-  else if (R <= 96) W4A16_STREAM(3, false, 2);
-  else W4A16_STREAM(4, false, 1);
-#undef W4A16_STREAM
+// The whole forward in one launch where every workgroup (of 1024 output channels) can read
+// its adapter's A again in the time of a launch: up to 96 KB of A.  Measured (graph replay,
+// both ways): K = 1536, rank 16, one row 6.7 us against 7.5 us in two launches; 256 rows of
+// 32 adapters at rank 32 24.1 against 28.7; K = 4096, rank 16, one row 9.1 against 8.2.
+constexpr int kFusedA = 48 << 10;   // values
+
+bool forward_fused(int M, int K, int R) { return M <= kInlineRows && R <= 64 && R * K <= kFusedA; }
+
+void run_fused(const half_t* x, const half_t* a, const half_t* b, const float* scaling, const RowPlan& plan,
+               const half_t* base, half_t* out, float* h_out, int K, int N, int R, hipStream_t st) {
+  const dim3 grid(tiles_of(plan, 16) * ceil_div(N, 1024)), block(512);
+#define W4A16_FUSED(F_, P_, D_) \
+  hipLaunchKernelGGL((lora_fused_kernel<F_, P_, D_>), grid, block, 0, st, x, a, b, scaling, plan, base, out, h_out, K, N, R)
+  if (R <= 16) W4A16_FUSED(1, true, 8);
+  else if (R <= 32) W4A16_FUSED(1, false, 4);
+  else W4A16_FUSED(2, false, 4);
+#undef W4A16_FUSED
 }
 
-template <bool TRANS>
-void run_stream(const ByRow& h, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C, int R,
-                int L, int slots, hipStream_t st) {
-  if (base) run_stream_base<TRANS, true>(h, table, w, base, out, C, R, L, slots, st);
-  else if constexpr (TRANS) run_stream_base<TRANS, false>(h, table, w, base, out, C, R, L, slots, st);
+StreamArgs stream_args(const ByRow& h, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C,
+                       int R, int L, int slots) {
+  // about 1024 workgroups (two rounds of two per compute unit), 64 slots at most
+  const int64_t group = std::max<int64_t>(1, std::min<int64_t>(64, static_cast<int64_t>(slots) * ceil_div(C, 512) / 1024));
+  return {h.frags, h.factors, table, w, base, out, C, R, L, slots, static_cast<int>(group)};
+}
+
+int stream_blocks(const StreamArgs& s) { return ceil_div(s.C, 512) * ceil_div(s.slots, s.group); }
+
+template <bool TRANS, bool BASE>
+void run_stream(const StreamArgs& s, hipStream_t st) {
+  const dim3 grid(stream_blocks(s)), block(256);
+#define W4A16_STREAM(F_, P_, D_) \
+  hipLaunchKernelGGL((lora_stream_kernel<F_, P_, TRANS, BASE, D_>), grid, block, 0, st, s)
+  if constexpr (!TRANS) {   // ranks up to 32 of the backward pass are in the products kernel
+    if (s.R <= 32) {
+      if (s.R <= 16) W4A16_STREAM(1, true, 2);
+      else W4A16_STREAM(1, false, 2);
+      return;
+    }
+  }
+  if (s.R <= 64) W4A16_STREAM(2, false, 2);
+  else if (s.R <= 96) W4A16_STREAM(3, false, 2);
+  else W4A16_STREAM(4, false, 1);
+#undef W4A16_STREAM
 }
 
 // --- outer --------------------------------------------------------------------------
@@ -218,25 +238,39 @@ struct Kept {
   int gshift;
 };
 
-// Workgroups that share the rows of 128 channels: enough for one per compute unit, as long
-// as every wavefront keeps two slots of an average adapter.
-int outer_parts(int M, int L, int C, int R) {
-  const int64_t groups = static_cast<int64_t>(ceil_div(C, 128)) * ceil_div(R, 64) * L;
-  const int64_t most = M / L / kSlotRows / (2 * (R <= 32 ? 8 : 4));
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({(256 + groups - 1) / groups, most, 16})));
+// Workgroups that share the rows of 128 channels, `groups` of them being there with one
+// each: up to one per compute unit, as long as each keeps 32 slots of an average adapter.
+int outer_parts(int M, int L, int64_t groups) {
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({256 / groups, M / L / (32 * kSlotRows), 16})));
 }
 
+int64_t outer_groups(int C, int R, int L) { return static_cast<int64_t>(ceil_div(C, 128)) * ceil_div(R, 64) * L; }
+
+OuterArgs outer_args(const Kept& k, const ByRank& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
+                     int parts) {
+  return {k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts};
+}
+
+// Ranks 33 .. 128: blocks of 64 ranks, whose sums take half the registers of a wavefront.
 template <bool Q8, bool CMAJOR>
-void run_outer(const Kept& k, const ByRank& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
-               int parts, hipStream_t st) {
-#define W4A16_OUTER(NT_, W_, D_) \
-  hipLaunchKernelGGL((lora_outer_kernel<NT_, W_, D_, Q8, CMAJOR>), \
-                     dim3(ceil_div(C, 128), ceil_div(R, 16 * NT_) * parts, plan.L), dim3(64 * W_), 0, st, k.x, k.codes, \
-                     k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts)
-  if (R <= 16) W4A16_OUTER(1, 8, 3);
-  else if (R <= 32) W4A16_OUTER(2, 8, 2);
-  else W4A16_OUTER(4, 4, 2);
-#undef W4A16_OUTER
+void run_outer(const OuterArgs& o, hipStream_t st) {
+  const int64_t grid = outer_groups(o.C, o.R, o.plan.L) * o.parts;
+  hipLaunchKernelGGL((lora_outer_kernel<4, 4, 2, Q8, CMAJOR>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, o);
+}
+
+template <int NT, bool Q8>
+void run_products(const OuterArgs& b, const OuterArgs& a, const StreamArgs& dx, hipStream_t st) {
+  const int nb = static_cast<int>(outer_groups(b.C, b.R, b.plan.L)) * b.parts;
+  const int na = static_cast<int>(outer_groups(a.C, a.R, a.plan.L)) * a.parts;
+  const dim3 block(256);
+  if (!dx.out)
+    hipLaunchKernelGGL((lora_products_kernel<NT, Q8, false, false>), dim3(nb + na), block, 0, st, b, nb, a, na, dx);
+  else if (!dx.base)
+    hipLaunchKernelGGL((lora_products_kernel<NT, Q8, true, false>), dim3(nb + na + stream_blocks(dx)), block, 0, st, b, nb, a,
+                       na, dx);
+  else
+    hipLaunchKernelGGL((lora_products_kernel<NT, Q8, true, true>), dim3(nb + na + stream_blocks(dx)), block, 0, st, b, nb, a,
+                       na, dx);
 }
 
 // --- forward ------------------------------------------------------------------------
@@ -245,14 +279,19 @@ struct ForwardMemory {
   RowPlan plan;
   float* part;       // [S][M][R]
   int S, slots;
-  bool stream;
+  bool fused, stream;
   ByRow h;
   SlotTable table;
 };
 
 ForwardMemory forward_memory(Carver& ws, const int32_t* index, bool with_index, int M, int K, int R, int L) {
   ForwardMemory m{};
-  m.stream = M >= kStreamRows;
+  m.fused = forward_fused(M, K, R);
+  if (m.fused) {
+    m.plan = RowPlan{index, nullptr, nullptr, M, L};
+    return m;
+  }
+  m.stream = M > kInlineRows;
   m.plan = take_plan(ws, index, with_index && M > kInlineRows, M, L);
   m.S = shrink_slices(M, L, R, K);
   m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
@@ -290,14 +329,16 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
   m.g = take_by_rank(ws, m.slots, R);
   m.g_rows = take_by_row(ws, m.slots, R);
   m.table = take_table(ws, m.slots);
-  m.a_parts = outer_parts(M, L, K, R);
-  m.b_parts = outer_parts(M, L, N, R);
+  const int64_t ga = outer_groups(K, R, L), gb = outer_groups(N, R, L);
+  m.a_parts = outer_parts(M, L, R <= 32 ? ga + gb : ga);
+  m.b_parts = outer_parts(M, L, R <= 32 ? ga + gb : gb);
   if (m.a_parts > 1) m.da = ws.take<float>(static_cast<size_t>(m.a_parts) * L * R * K);
   if (m.b_parts > 1) m.db = ws.take<float>(static_cast<size_t>(m.b_parts) * L * N * R);
   return m;
 }
 
-int check_workspace(size_t have, size_t need) {
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (need > 0 && !ws) return fail(W4A16_ERR_INVALID_ARG, "NULL workspace, this call needs %zu bytes", need);
   if (have >= need) return W4A16_OK;
   return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, this call needs %zu", have, need);
 }
@@ -321,12 +362,12 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const Buffer bufs[] = {{c.dy, 16, true, "dy"},       {c.a, 16, true, "a"},     {c.b, 16, true, "b"},
                          {c.h, 16, true, "h"},         {c.da, 16, true, "da"},   {c.db, 16, true, "db"},
                          {c.dx0, 16, false, "dx0"},    {c.dx, 16, false, "dx"},  {c.index, 4, false, "index"},
-                         {c.scaling, 4, false, "scaling"}, {c.workspace, 16, true, "workspace"}};
+                         {c.scaling, 4, false, "scaling"}, {c.workspace, 16, false, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   if (c.dx0 && !c.dx) return fail(W4A16_ERR_INVALID_ARG, "dx0 is given without dx");
   Carver size{nullptr}, ws{static_cast<unsigned char*>(c.workspace)};
   backward_memory(size, nullptr, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
-  if (int rc = check_workspace(c.workspace_bytes, size.used)) return rc;
+  if (int rc = check_workspace(c.workspace, c.workspace_bytes, size.used)) return rc;
   const BackwardMemory m = backward_memory(ws, c.index, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
   const auto st = static_cast<hipStream_t>(c.stream);
   const auto* dy = reinterpret_cast<const half_t*>(c.dy);
@@ -338,9 +379,21 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const SplitTask th{c.h, 1, m.h.frags, m.h.exps, nullptr, nullptr, nullptr};
   const SplitTask tg{m.part, m.S, m.g.frags, m.g.exps, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors, nullptr};
   hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 2), dim3(256), 0, st, th, tg, c.scaling, m.table, m.plan, c.R);
-  run_outer<false, true>(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, m.b_parts > 1 ? m.db : c.db, c.N, c.R,
-                         m.b_parts, st);
-  run_outer<Q8, false>(kept, m.g, c.scaling, m.plan, m.a_parts > 1 ? m.da : c.da, c.K, c.R, m.a_parts, st);
+  const OuterArgs ob = outer_args(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, m.b_parts > 1 ? m.db : c.db, c.N,
+                                  c.R, m.b_parts);
+  const OuterArgs oa = outer_args(kept, m.g, c.scaling, m.plan, m.a_parts > 1 ? m.da : c.da, c.K, c.R, m.a_parts);
+  const StreamArgs dx = stream_args(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a),
+                                    reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L,
+                                    m.slots);
+  if (c.R <= 16) {
+    run_products<1, Q8>(ob, oa, dx, st);
+  } else if (c.R <= 32) {
+    run_products<2, Q8>(ob, oa, dx, st);
+  } else {
+    run_outer<false, true>(ob, st);
+    run_outer<Q8, false>(oa, st);
+    if (dx.out) dx.base ? run_stream<true, true>(dx, st) : run_stream<true, false>(dx, st);
+  }
   if (m.a_parts > 1 || m.b_parts > 1) {
     auto task = [](float* parts, float* out, size_t count, int n) {
       return PartsTask{reinterpret_cast<const float4_t*>(parts), reinterpret_cast<float4_t*>(out), n > 1 ? count / 4 : 0, n};
@@ -350,9 +403,6 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
     const size_t most = std::max(ta.quads, tb.quads);
     hipLaunchKernelGGL(lora_sum_parts_kernel, dim3(static_cast<unsigned>((most + 255) / 256), 2), dim3(256), 0, st, ta, tb);
   }
-  if (c.dx)
-    run_stream<true>(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a), reinterpret_cast<const half_t*>(c.dx0),
-                     reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L, m.slots, st);
   return check_launch("lora backward launch");
 }
 
@@ -376,22 +426,28 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
   const Buffer bufs[] = {{y, 16, true, "y"},           {x, 16, true, "x"},          {a, 16, true, "a"},
                          {b, 16, true, "b"},           {out, 16, true, "out"},      {h, 16, false, "h"},
                          {index, 4, false, "index"},   {scaling, 4, false, "scaling"},
-                         {workspace, 16, true, "workspace"}};
+                         {workspace, 16, false, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   Carver size{nullptr}, ws{static_cast<unsigned char*>(workspace)};
   forward_memory(size, nullptr, index != nullptr, M, K, R, L);
-  if (int rc = check_workspace(workspace_bytes, size.used)) return rc;
+  if (int rc = check_workspace(workspace, workspace_bytes, size.used)) return rc;
   const ForwardMemory m = forward_memory(ws, index, index != nullptr, M, K, R, L);
   const auto st = static_cast<hipStream_t>(stream);
   const auto* yh = reinterpret_cast<const half_t*>(y);
   const auto* bh = reinterpret_cast<const half_t*>(b);
   auto* oh = reinterpret_cast<half_t*>(out);
+  const auto* xh = reinterpret_cast<const half_t*>(x);
+  const auto* ah = reinterpret_cast<const half_t*>(a);
+  if (m.fused) {
+    run_fused(xh, ah, bh, scaling, m.plan, yh, oh, h, K, N, R, st);
+    return check_launch("lora forward launch");
+  }
   run_plan(m.plan, st);
-  run_shrink(reinterpret_cast<const half_t*>(x), reinterpret_cast<const half_t*>(a), m.plan, K, R, m.S, m.part, st);
+  run_shrink(xh, ah, m.plan, K, R, m.S, m.part, st);
   if (m.stream) {
     const SplitTask t{m.part, m.S, nullptr, nullptr, m.h.frags, m.h.factors, h};
     hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(256), 0, st, t, t, scaling, m.table, m.plan, R);
-    run_stream<false>(m.h, m.table, bh, yh, oh, N, R, L, m.slots, st);
+    run_stream<false, true>(stream_args(m.h, m.table, bh, yh, oh, N, R, L, m.slots), st);
   } else {
     run_expand(m.part, m.S, bh, scaling, m.plan, yh, oh, h, N, R, st);
   }

@@ -25,7 +25,7 @@ namespace w4a16 {
 // How rows are grouped by adapter.  Class of a row: its adapter, or L ("none") for an
 // index outside [0, L).
 //   index == NULL             every row belongs to adapter 0
-//   off == NULL (M <= 64)     each wavefront groups the rows itself, one row per lane
+//   off == NULL (M <= 256)    each workgroup groups the rows itself, one row per thread
 //   else                      off[c] = first sorted position of class c (L + 2 entries),
 //                             perm[p] = row at sorted position p (plan_rows_kernel)
 struct RowPlan {
@@ -35,7 +35,7 @@ struct RowPlan {
   int M, L;
 };
 
-constexpr int kInlineRows = 64;
+constexpr int kInlineRows = 256;
 
 __device__ __forceinline__ int row_class(int i, int L) { return i >= 0 && i < L ? i : L; }
 
@@ -97,12 +97,12 @@ __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restri
   plan_rows(blockIdx.x, index, M, L, off, perm, part);
 }
 
-// Number of tile slots for T rows per tile (host and device agree on it): slots of class
-// c start at off[c] / T + c, which leaves room for every class's last partial tile.
-__host__ __device__ inline int tile_slots(const RowPlan& p, int T) {
-  if (!p.index) return (p.M + T - 1) / T;
-  const int most = p.M / T + p.L + 1;
-  return !p.off && p.M < most ? p.M : most;
+// Number of tile slots for T rows per tile.  With a plan in memory the slots of class c
+// start at off[c] / T + c, which leaves room for every class's last partial tile.
+__host__ __device__ inline int tile_slots(int M, int L, bool with_index, bool in_memory, int T) {
+  if (!with_index) return (M + T - 1) / T;
+  const int most = M / T + L + 1;
+  return !in_memory && M < most ? M : most;
 }
 
 struct Tile {
@@ -110,8 +110,8 @@ struct Tile {
   int count;     // rows in the tile, 0: empty slot
 };
 
-// Tile of a slot; every thread of the workgroup calls it, `rows` (LDS, T entries) holds
-// the tile's rows afterwards, entries past the count repeating a valid row.
+// Tile of a slot; every thread of the workgroup (256 or more) calls it, `rows` (LDS, T
+// entries) holds the tile's rows afterwards, entries past the count repeating a valid row.
 template <int T>
 __device__ __forceinline__ Tile find_tile(const RowPlan& p, int slot, int32_t* rows) {
   const int tid = threadIdx.x, lane = tid & 63;
@@ -135,25 +135,49 @@ __device__ __forceinline__ Tile find_tile(const RowPlan& p, int slot, int32_t* r
     t.adapter = c;
     t.count = max(0, min(T, hi - first));
     if (tid < T && t.count > 0) rows[tid] = p.perm[first + min(tid, t.count - 1)];
+  } else if (p.M == 1) {
+    t.adapter = row_class(p.index[0], p.L);
+    t.count = slot == 0 ? 1 : 0;
+    if (tid < T) rows[tid] = 0;
   } else {
-    const int cls = lane < p.M ? row_class(p.index[min(lane, p.M - 1)], p.L) : -1;
-    int rank = 0;   // among the earlier rows of the same class
-    for (int k = 0; k < p.M; ++k) rank += (__shfl(cls, k) == cls && k < lane) ? 1 : 0;
-    uint64_t starts = __ballot(lane < p.M && rank % T == 0);
-    for (int k = 0; k < slot; ++k) starts &= starts - 1;
-    t.adapter = p.L;
-    t.count = 0;
-    if (starts != 0) {
-      const int s = __builtin_ctzll(starts);
-      t.adapter = __shfl(cls, s);
-      const int r0 = __shfl(rank, s);
-      const bool mine = lane < p.M && cls == t.adapter && rank >= r0 && rank < r0 + T;
-      t.count = __popcll(__ballot(mine));
-      if (tid < 64) {
-        if (mine) rows[rank - r0] = lane;
-        if (lane >= t.count && lane < T) rows[lane] = s;
-      }
+    // Thread m counts the earlier rows of its class.  A tile starts at every T-th row of a
+    // class; slots number the starts in the order of the rows.
+    __shared__ __align__(16) int32_t cls[kInlineRows];
+    __shared__ int32_t starts[4], start[2], members[4];
+    const int wave = tid >> 6;
+    if (tid < kInlineRows) cls[tid] = tid < p.M ? row_class(p.index[tid], p.L) : -1;
+    if (tid < 2) start[tid] = 0;
+    __syncthreads();
+    const int mine = tid < p.M ? cls[tid] : -1;
+    int rank = 0;
+    for (int k = 0; k < p.M; k += 4) {
+      const int4 c = *reinterpret_cast<const int4*>(cls + k);   // entries from M on are -1
+      rank += (c.x == mine && k < tid) + (c.y == mine && k + 1 < tid) + (c.z == mine && k + 2 < tid) +
+              (c.w == mine && k + 3 < tid);
     }
+    const bool starts_tile = mine >= 0 && rank % T == 0;
+    const uint64_t sb = __ballot(starts_tile);
+    if (lane == 0 && wave < 4) starts[wave] = __popcll(sb);
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < 4; ++w) {
+      before += w < wave ? starts[w] : 0;
+      total += starts[w];
+    }
+    if (starts_tile && before + __popcll(sb & ((1ull << lane) - 1ull)) == slot) {
+      start[0] = tid;
+      start[1] = rank;
+    }
+    __syncthreads();
+    const int s = start[0], r0 = start[1];
+    t.adapter = cls[s];
+    const bool in = slot < total && mine == t.adapter && rank >= r0 && rank < r0 + T;
+    const uint64_t mb = __ballot(in);
+    if (lane == 0 && wave < 4) members[wave] = __popcll(mb);
+    if (in) rows[rank - r0] = tid;
+    __syncthreads();
+    t.count = members[0] + members[1] + members[2] + members[3];
+    if (tid < T && tid >= t.count) rows[tid] = s;
   }
   t.adapter = __builtin_amdgcn_readfirstlane(t.adapter);
   t.count = __builtin_amdgcn_readfirstlane(t.count);
@@ -188,41 +212,21 @@ constexpr int kNoExponent = -1000;   // of values that are all zero
 // fill a tile are computed and not stored.  Consecutive workgroups take the slices of one
 // tile, so that an XCD's L2 holds the w of few slices.
 
-// Few rows: a tile of 16 rows per workgroup, whose W wavefronts take turns (pairs of steps)
-// along the slice, w as it lies in memory, D steps in flight; their sums are added in LDS
-// in a fixed order.
+// Steps [b, e) of 32 channels of 16 rows, dealt in pairs to W wavefronts, w as it lies in
+// memory, D steps in flight.  xr: this lane's row; w [R][C].
 template <int NT>
 struct ShrinkStep {
   half8_t x, w[NT];
 };
 
-template <int NT, int D>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restrict__ x, const half_t* __restrict__ w,
-                                                          RowPlan plan, int C, int R, int S, float* __restrict__ out) {
-  constexpr int T = 16, W = 4;
-  __shared__ int32_t rows[T];
-  __shared__ float4_t red[W / 2 * NT * 64];
-  const int s = blockIdx.x % S;
-  const Tile tile = find_tile<T>(plan, blockIdx.x / S, rows);
-  if (tile.count == 0) return;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+template <int NT, int W, int D>
+__device__ __forceinline__ void shrink_steps(const half_t* __restrict__ xr, const half_t* __restrict__ w, int C, int R,
+                                             int b, int e, int wave, int lane, float4_t (&acc)[NT]) {
   const int lr = lane & 15, lq = lane >> 4;
-  float* o = out + static_cast<size_t>(s) * plan.M * R;
-  if (tile.adapter == plan.L) {
-    for (int i = tid; i < tile.count * R; i += 64 * W) o[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
-    return;
-  }
-  const half_t* xr = x + static_cast<size_t>(rows[lr]) * C;
   const half_t* wr[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-    wr[t] = w + (static_cast<size_t>(tile.adapter) * R + min(16 * t + lr, R - 1)) * C;
-  float4_t acc[NT] = {};
-  const int full = C >> 5;   // whole steps of 32 channels
-  const int steps = (C + 31) >> 5;
-  const int b = static_cast<int>(static_cast<int64_t>(steps) * s / S);
-  const int e = static_cast<int>(static_cast<int64_t>(steps) * (s + 1) / S);
+  for (int t = 0; t < NT; ++t) wr[t] = w + static_cast<size_t>(min(16 * t + lr, R - 1)) * C;
+  const int full = C >> 5;   // whole steps
   // Step k of this wavefront, of n.  Loads past the slice are clamped into it, not used.
   auto step_of = [&](int k) { return b + 2 * (wave + (k >> 1) * W) + (k & 1); };
   const int whole = (e - b) / (2 * W), rest = (e - b) % (2 * W);
@@ -264,6 +268,12 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
 #pragma unroll
   for (int d = 0; d < D; ++d)
     if (k + d + D < n) add(k + d + D, ring[d]);
+}
+
+// Sum of acc over the wavefronts of a workgroup, in a fixed order, left in wavefront 0.
+// red: W / 2 * NT * 64 entries of LDS; every thread calls it.
+template <int NT, int W>
+__device__ __forceinline__ void add_wavefronts(float4_t* red, int wave, int lane, float4_t (&acc)[NT]) {
 #pragma unroll
   for (int half = W / 2; half > 0; half >>= 1) {
     if (wave >= half && wave < 2 * half)
@@ -275,6 +285,33 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
       for (int t = 0; t < NT; ++t) acc[t] += red[(wave * NT + t) * 64 + lane];
     __syncthreads();
   }
+}
+
+// Few rows: a tile of 16 rows and a slice per workgroup of 4 wavefronts.
+template <int NT, int D>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restrict__ x, const half_t* __restrict__ w,
+                                                          RowPlan plan, int C, int R, int S, float* __restrict__ out) {
+  constexpr int W = 4;
+  __shared__ int32_t rows[16];
+  __shared__ float4_t red[W / 2 * NT * 64];
+  const int s = blockIdx.x % S;
+  const Tile tile = find_tile<16>(plan, blockIdx.x / S, rows);
+  if (tile.count == 0) return;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  float* o = out + static_cast<size_t>(s) * plan.M * R;
+  if (tile.adapter == plan.L) {
+    for (int i = tid; i < tile.count * R; i += 64 * W) o[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+    return;
+  }
+  const int steps = (C + 31) >> 5;
+  const int b = static_cast<int>(static_cast<int64_t>(steps) * s / S);
+  const int e = static_cast<int>(static_cast<int64_t>(steps) * (s + 1) / S);
+  float4_t acc[NT] = {};
+  shrink_steps<NT, W, D>(x + static_cast<size_t>(rows[lr]) * C, w + static_cast<size_t>(tile.adapter) * R * C, C, R, b, e,
+                         wave, lane, acc);
+  add_wavefronts<NT, W>(red, wave, lane, acc);
   if (wave != 0) return;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -500,6 +537,30 @@ __device__ __forceinline__ half8_t expand_run(const float4_t (&acc)[8], int u, u
   return o;
 }
 
+// Splits the ranks of a row held by the four lanes (r, 0 .. 3): operands, and the row's
+// factor s_i 2^e.
+template <int F, bool PACKED>
+__device__ __forceinline__ float split_row(const float (&v)[F][8], int lq, float si, half8_t (&hf)[F][PACKED ? 1 : 2]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_magnitude(v[f][j]));
+  top = fmaxf(top, __shfl_xor(top, 16));
+  top = fmaxf(top, __shfl_xor(top, 32));
+  const int shift = kSplitTop - top_exponent(top);
+#pragma unroll
+  for (int f = 0; f < F; ++f)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      half_t hi, lo;
+      split_half(v[f][j], shift, hi, lo);
+      hf[f][0][j] = PACKED && lq >= 2 ? lo : hi;
+      if constexpr (!PACKED) hf[f][1][j] = lo;
+    }
+  return __builtin_ldexpf(si, -shift);
+}
+
 // --- split: h or g (the sum of S slices) as ready MFMA operands ---------------------------
 //
 // One workgroup per slot of 32 rows of one adapter and task, once per call instead of by
@@ -693,9 +754,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
     load_expand_weights<F, PACKED, false>(w + static_cast<size_t>(tile.adapter) * R * C, c0, C, R, lane, wf);
   }
   if (wave == 0) {
-    const float si = scaling ? scaling[tile.adapter] : 1.0f;
     float v[F][8];
-    float top = 0.0f;
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
@@ -706,28 +765,15 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
         *reinterpret_cast<float4_t*>(h_out + at * R + j0 + 4) = float4_t{v[f][4], v[f][5], v[f][6], v[f][7]};
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[f][j] = in ? v[f][j] : 0.0f;
-        top = fmaxf(top, finite_magnitude(v[f][j]));
-      }
+      for (int j = 0; j < 8; ++j) v[f][j] = in ? v[f][j] : 0.0f;
     }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const int shift = kSplitTop - top_exponent(top);
-    if (lq == 0) factor[lr] = __builtin_ldexpf(si, -shift);
+    half8_t hf[F][P];
+    const float fr = split_row<F, PACKED>(v, lq, scaling ? scaling[tile.adapter] : 1.0f, hf);
+    if (lq == 0) factor[lr] = fr;
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
-      half8_t hi, lo;
+    for (int f = 0; f < F; ++f)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        half_t vh, vl;
-        split_half(v[f][j], shift, vh, vl);
-        hi[j] = PACKED && lq >= 2 ? vl : vh;
-        lo[j] = vl;
-      }
-      split[f][0][lane] = hi;
-      if constexpr (!PACKED) split[f][P - 1][lane] = lo;
-    }
+      for (int p = 0; p < P; ++p) split[f][p][lane] = hf[f][p];
   }
   __syncthreads();
   if (c0 >= C) return;
@@ -743,6 +789,86 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
     const int c = c0 + 32 * u + 8 * lq;
     const half8_t o = expand_run<false>(acc, u, y[u], factor[lr]);
     if (c < C && mine) *reinterpret_cast<half8_t*>(out + at * C + c) = o;
+  }
+}
+
+// --- forward of few rows in one launch ----------------------------------------------------
+//
+// Every workgroup (8 wavefronts, one tile of 16 rows x 1024 channels) computes h of its
+// tile for itself: R K weights more from the L2 per workgroup, against a launch and a round
+// trip of h through memory.  Weights and base of the wavefront's 128 channels are requested
+// first and arrive during the shrink.
+template <int F, bool PACKED, int D>
+__global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restrict__ x, const half_t* __restrict__ a,
+                                                         const half_t* __restrict__ w,
+                                                         const float* __restrict__ scaling, RowPlan plan,
+                                                         const half_t* base, half_t* out, float* __restrict__ h_out,
+                                                         int K, int N, int R) {
+  constexpr int W = 8, NT = PACKED ? 1 : 2 * F, P = PACKED ? 1 : 2;
+  constexpr int ld = 16 * NT + 4;   // floats per row of h
+  __shared__ int32_t rows[16];
+  __shared__ float4_t red[W / 2 * NT * 64];
+  __shared__ __align__(16) float hs[16 * ld];
+  const int blocks = (N + 128 * W - 1) / (128 * W);
+  const Tile tile = find_tile<16>(plan, blockIdx.x / blocks, rows);
+  if (tile.count == 0) return;
+  const int block = blockIdx.x % blocks;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lq = lane >> 4;
+  if (tile.adapter == plan.L) {
+    const int c_lo = block * 128 * W;
+    if (base != out) {
+      const int chunks = min(128 * W, N - c_lo) / 8;
+      for (int i = tid; i < tile.count * chunks; i += 64 * W) {
+        const size_t at = static_cast<size_t>(rows[i / chunks]) * N + c_lo + 8 * (i % chunks);
+        *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(base + at);
+      }
+    }
+    if (h_out && block == 0)
+      for (int i = tid; i < tile.count * R; i += 64 * W) h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+    return;
+  }
+  const size_t at = static_cast<size_t>(rows[lr]);
+  const int c0 = (block * W + wave) * 128;
+  uint4 y[4];
+  half8_t wf[F][8];
+  if (c0 < N) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      y[u] = *reinterpret_cast<const uint4*>(base + at * N + min(c0 + 32 * u + 8 * lq, N - 8));
+    load_expand_weights<F, PACKED, false>(w + static_cast<size_t>(tile.adapter) * R * N, c0, N, R, lane, wf);
+  }
+
+  float4_t acc[NT] = {};
+  shrink_steps<NT, W, D>(x + at * K, a + static_cast<size_t>(tile.adapter) * R * K, K, R, 0, (K + 31) >> 5, wave, lane, acc);
+  add_wavefronts<NT, W>(red, wave, lane, acc);
+  if (wave == 0)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) hs[(4 * lq + r) * ld + 16 * t + lr] = acc[t][r];
+  __syncthreads();
+  if (h_out && block == 0)
+    for (int i = tid; i < tile.count * R; i += 64 * W)
+      h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = hs[(i / R) * ld + i % R];
+  if (c0 >= N) return;
+  float v[F][8];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[f][j] = j0 < R ? hs[lr * ld + j0 + j] : 0.0f;
+  }
+  half8_t hf[F][P];
+  const float factor = split_row<F, PACKED>(v, lq, scaling ? scaling[tile.adapter] : 1.0f, hf);
+  float4_t sums[8];
+  expand_products<F, P>(wf, hf, sums);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int c = c0 + 32 * u + 8 * lq;
+    const half8_t o = expand_run<false>(sums, u, y[u], factor);
+    if (c < N && lr < tile.count) *reinterpret_cast<half8_t*>(out + at * N + c) = o;
   }
 }
 
@@ -762,18 +888,32 @@ struct StreamRows {
   float factor;
 };
 
+struct StreamArgs {
+  const half_t* frags;
+  const float* factors;
+  SlotTable table;
+  const half_t* w;
+  const half_t* base;
+  half_t* out;
+  int C, R, L, slots, group;
+};
+
 template <int F, bool PACKED, bool TRANS, bool BASE, int D>
-__global__ __launch_bounds__(256) void lora_stream_kernel(const half_t* __restrict__ frags,
-                                                          const float* __restrict__ factors, SlotTable table,
-                                                          const half_t* __restrict__ w, const half_t* base, half_t* out,
-                                                          int C, int R, int L, int slots, int group) {
+__device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
   constexpr int P = PACKED ? 1 : 2;
+  const half_t* __restrict__ frags = args.frags;
+  const float* __restrict__ factors = args.factors;
+  const SlotTable table = args.table;
+  const half_t* __restrict__ w = args.w;
+  const half_t* base = args.base;
+  half_t* out = args.out;
+  const int C = args.C, R = args.R, L = args.L, slots = args.slots, group = args.group;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int blocks = (C + 511) >> 9;
-  const int c0 = (blockIdx.x % blocks) * 512 + wave * 128;
-  const int s0 = (blockIdx.x / blocks) * group;
+  const int c0 = (block % blocks) * 512 + wave * 128;
+  const int s0 = (block / blocks) * group;
   if (c0 >= C) return;
   const int ns = min(group, slots - s0);
   // lane l: slot s0 + l
@@ -859,6 +999,11 @@ __global__ __launch_bounds__(256) void lora_stream_kernel(const half_t* __restri
   }
 }
 
+template <int F, bool PACKED, bool TRANS, bool BASE, int D>
+__global__ __launch_bounds__(256) void lora_stream_kernel(StreamArgs args) {
+  stream_rows<F, PACKED, TRANS, BASE, D>(args, blockIdx.x);
+}
+
 // --- prepare: what the backward pass needs before its products, in one launch --------------
 //
 // Workgroups 0 .. plans - 1 group the rows; the others transpose b [L][N][R] to bt [L][R][N],
@@ -923,23 +1068,42 @@ struct OuterSlot {
   int e;                   // their power of two
 };
 
-// D slots in flight per wavefront.
+struct OuterArgs {
+  const half_t* x;          // or codes and scales (Q8)
+  const uint8_t* codes;
+  const half_t* xs;
+  int gshift;
+  const half_t* frags;
+  const int32_t* exps;
+  const float* scaling;
+  RowPlan plan;
+  float* grad;
+  int C, R, parts;
+};
+
+// Workgroup `block` of columns x parts x rank blocks x adapters, D slots in flight per
+// wavefront.  red: W * NT * 64 entries of LDS.
 template <int NT, int W, int D, bool Q8, bool CMAJOR>
-__global__ __launch_bounds__(64 * W) void lora_outer_kernel(const half_t* __restrict__ x,
-                                                            const uint8_t* __restrict__ codes,
-                                                            const half_t* __restrict__ xs, int gshift,
-                                                            const half_t* __restrict__ frags,
-                                                            const int32_t* __restrict__ exps,
-                                                            const float* __restrict__ scaling, RowPlan plan,
-                                                            float* __restrict__ grad, int C, int R, int parts) {
-  __shared__ float4_t red[W * NT * 64];
+__device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, float4_t* red) {
+  const half_t* __restrict__ x = args.x;
+  const uint8_t* __restrict__ codes = args.codes;
+  const half_t* __restrict__ xs = args.xs;
+  const half_t* __restrict__ frags = args.frags;
+  const int32_t* __restrict__ exps = args.exps;
+  const float* __restrict__ scaling = args.scaling;
+  const RowPlan plan = args.plan;
+  float* __restrict__ grad = args.grad;
+  const int C = args.C, R = args.R, parts = args.parts, gshift = args.gshift;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int c0 = blockIdx.x * 128;
-  const int part = blockIdx.y % parts;
-  const int t0 = (blockIdx.y / parts) * NT;
-  const int ad = blockIdx.z;
+  const int cols = (C + 127) >> 7, ranks = (R + 16 * NT - 1) / (16 * NT);
+  const int c0 = (block % cols) * 128;
+  block /= cols;
+  const int part = block % parts;
+  block /= parts;
+  const int t0 = (block % ranks) * NT;
+  const int ad = block / ranks;
   const int NTT = (R + 15) >> 4;   // fragments per slot
   // slots of the adapter: [first_slot, first_slot + n); positions lo .. hi - 1
   const int lo = plan.index ? plan.off[ad] : 0;
@@ -1075,6 +1239,29 @@ __global__ __launch_bounds__(64 * W) void lora_outer_kernel(const half_t* __rest
         if (ch < C && j < R) g[CMAJOR ? static_cast<size_t>(ch) * R + j : static_cast<size_t>(j) * C + ch] = si * v[r];
       }
     }
+  }
+}
+
+template <int NT, int W, int D, bool Q8, bool CMAJOR>
+__global__ __launch_bounds__(64 * W) void lora_outer_kernel(OuterArgs args) {
+  __shared__ float4_t red[W * NT * 64];
+  outer_sums<NT, W, D, Q8, CMAJOR>(args, blockIdx.x, red);
+}
+
+// The three products of the backward pass in one launch, for R <= 32: their workgroups fill
+// the GPU together (the outer products alone have one per 128 channels), and two launches
+// fall away.  Workgroups: dB, then dA, then dx.
+template <int NT, bool Q8, bool DX, bool BASE>
+__global__ __launch_bounds__(256) void lora_products_kernel(OuterArgs b, int b_blocks, OuterArgs a, int a_blocks,
+                                                            StreamArgs dx) {
+  __shared__ float4_t red[4 * NT * 64];
+  const int block = blockIdx.x;
+  if (block < b_blocks) {
+    outer_sums<NT, 4, 2, false, true>(b, block, red);
+  } else if (block < b_blocks + a_blocks) {
+    outer_sums<NT, 4, 2, Q8, false>(a, block - b_blocks, red);
+  } else {
+    if constexpr (DX) stream_rows<1, NT == 1, true, BASE, 2>(dx, block - b_blocks - a_blocks);
   }
 }
 
