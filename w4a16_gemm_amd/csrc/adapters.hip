@@ -136,22 +136,26 @@ int plan_slots(int M, int L, bool with_index) {
 
 // --- shrink -------------------------------------------------------------------------
 
-// Rows per tile of a shrink, in 16s (wavefronts): 128 or 64 rows, once an adapter has twice
-// that many on average, else 16 with the wavefronts along the channels.
-int shrink_waves(int M, int L) { return M / L >= 256 ? 8 : M / L >= 64 ? 4 : 1; }
+// Rows per tile of a shrink, in 16s (wavefronts): 128 or 64 rows, once an adapter has that
+// many on average; below that, and for up to 512 rows at small rank, 16 with the wavefronts
+// along the channels (512 rows x 11008 at rank 16: 4.8 us, in tiles of 64 rows 5.1).
+int shrink_waves(int M, int L, int R) {
+  if (M <= 512 && R <= 32) return 1;
+  return M / L >= 128 ? 8 : M / L >= 64 ? 4 : 1;
+}
 
-// Slices of the long axis: enough workgroups for the GPU (8 wavefronts per compute unit),
-// at least 256 channels each (few rows: 512), and sums of the slices that stay small (4 MB)
-// or a quarter of x.
+// Slices of the long axis: enough workgroups for the GPU (two per compute unit), at least
+// 256 channels each (few rows: 512), and sums of the slices that stay small (8 MB) or a
+// quarter of x.
 int shrink_slices(int M, int L, int R, int C) {
-  const int waves = shrink_waves(M, L);
-  const int want = ceil_div(waves == 4 ? 512 : 256, ceil_div(M, 16 * waves));
-  const int64_t light = std::max<int64_t>(C / (16 * R), (int64_t{1} << 20) / (static_cast<int64_t>(M) * R));
+  const int waves = shrink_waves(M, L, R);
+  const int want = ceil_div(512, ceil_div(M, 16 * waves));
+  const int64_t light = std::max<int64_t>(C / (16 * R), (int64_t{1} << 21) / (static_cast<int64_t>(M) * R));
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, C / (waves == 1 ? 512 : 256), 16, light})));
 }
 
 void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, int R, int S, float* out, hipStream_t st) {
-  const int waves = shrink_waves(plan.M, plan.L);
+  const int waves = shrink_waves(plan.M, plan.L, R);
   const dim3 grid(tiles_of(plan, 16 * waves) * S);
 #define W4A16_SHRINK(NT_, D_) \
   do { \
@@ -244,33 +248,38 @@ int outer_parts(int M, int L, int64_t groups) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({256 / groups, M / L / (32 * kSlotRows), 16})));
 }
 
-int64_t outer_groups(int C, int R, int L) { return static_cast<int64_t>(ceil_div(C, 128)) * ceil_div(R, 64) * L; }
+// The products of the backward pass go out in one launch for ranks up to 32, and for up to
+// 1024 rows, where each alone leaves most of the GPU idle; then in blocks of 32 ranks, which
+// read x or dy again from the cache for every further block.  Otherwise in a launch each and
+// blocks of 64 ranks (registers for one wavefront per SIMD, which would hold the dx part back).
+bool products_merged(int M, int R) { return R <= 32 || M <= 1024; }
+
+// 16s of ranks per block.
+int outer_nt(int M, int R) { return R <= 16 ? 1 : products_merged(M, R) ? 2 : 4; }
+
+int64_t outer_groups(int M, int C, int R, int L) {
+  return static_cast<int64_t>(ceil_div(C, 128)) * ceil_div(R, 16 * outer_nt(M, R)) * L;
+}
+
+int64_t outer_blocks(const OuterArgs& o) { return outer_groups(o.plan.M, o.C, o.R, o.plan.L) * o.parts; }
 
 OuterArgs outer_args(const Kept& k, const ByRank& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
                      int parts) {
   return {k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts};
 }
 
-// Ranks 33 .. 128: blocks of 64 ranks, whose sums take half the registers of a wavefront.
 template <bool Q8, bool CMAJOR>
 void run_outer(const OuterArgs& o, hipStream_t st) {
-  const int64_t grid = outer_groups(o.C, o.R, o.plan.L) * o.parts;
-  hipLaunchKernelGGL((lora_outer_kernel<4, 4, 2, Q8, CMAJOR>), dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, o);
+  hipLaunchKernelGGL((lora_outer_kernel<4, 4, 2, Q8, CMAJOR>), dim3(static_cast<unsigned>(outer_blocks(o))), dim3(256), 0, st, o);
 }
 
-template <int NT, bool Q8>
+template <int NT, int F, bool Q8>
 void run_products(const OuterArgs& b, const OuterArgs& a, const StreamArgs& dx, hipStream_t st) {
-  const int nb = static_cast<int>(outer_groups(b.C, b.R, b.plan.L)) * b.parts;
-  const int na = static_cast<int>(outer_groups(a.C, a.R, a.plan.L)) * a.parts;
-  const dim3 block(256);
-  if (!dx.out)
-    hipLaunchKernelGGL((lora_products_kernel<NT, Q8, false, false>), dim3(nb + na), block, 0, st, b, nb, a, na, dx);
-  else if (!dx.base)
-    hipLaunchKernelGGL((lora_products_kernel<NT, Q8, true, false>), dim3(nb + na + stream_blocks(dx)), block, 0, st, b, nb, a,
-                       na, dx);
-  else
-    hipLaunchKernelGGL((lora_products_kernel<NT, Q8, true, true>), dim3(nb + na + stream_blocks(dx)), block, 0, st, b, nb, a,
-                       na, dx);
+  const int nb = static_cast<int>(outer_blocks(b)), na = static_cast<int>(outer_blocks(a));
+  const dim3 grid(nb + na + (dx.out ? stream_blocks(dx) : 0)), block(256);
+  if (!dx.out) hipLaunchKernelGGL((lora_products_kernel<NT, F, Q8, false, false>), grid, block, 0, st, b, nb, a, na, dx);
+  else if (!dx.base) hipLaunchKernelGGL((lora_products_kernel<NT, F, Q8, true, false>), grid, block, 0, st, b, nb, a, na, dx);
+  else hipLaunchKernelGGL((lora_products_kernel<NT, F, Q8, true, true>), grid, block, 0, st, b, nb, a, na, dx);
 }
 
 // --- forward ------------------------------------------------------------------------
@@ -329,9 +338,10 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
   m.g = take_by_rank(ws, m.slots, R);
   m.g_rows = take_by_row(ws, m.slots, R);
   m.table = take_table(ws, m.slots);
-  const int64_t ga = outer_groups(K, R, L), gb = outer_groups(N, R, L);
-  m.a_parts = outer_parts(M, L, R <= 32 ? ga + gb : ga);
-  m.b_parts = outer_parts(M, L, R <= 32 ? ga + gb : gb);
+  const int64_t ga = outer_groups(M, K, R, L), gb = outer_groups(M, N, R, L);
+  const bool merged = products_merged(M, R);
+  m.a_parts = outer_parts(M, L, merged ? ga + gb : ga);
+  m.b_parts = outer_parts(M, L, merged ? ga + gb : gb);
   if (m.a_parts > 1) m.da = ws.take<float>(static_cast<size_t>(m.a_parts) * L * R * K);
   if (m.b_parts > 1) m.db = ws.take<float>(static_cast<size_t>(m.b_parts) * L * N * R);
   return m;
@@ -385,10 +395,12 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const StreamArgs dx = stream_args(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a),
                                     reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L,
                                     m.slots);
-  if (c.R <= 16) {
-    run_products<1, Q8>(ob, oa, dx, st);
-  } else if (c.R <= 32) {
-    run_products<2, Q8>(ob, oa, dx, st);
+  if (products_merged(c.M, c.R)) {
+    if (c.R <= 16) run_products<1, 1, Q8>(ob, oa, dx, st);
+    else if (c.R <= 32) run_products<2, 1, Q8>(ob, oa, dx, st);
+    else if (c.R <= 64) run_products<2, 2, Q8>(ob, oa, dx, st);
+    else if (c.R <= 96) run_products<2, 3, Q8>(ob, oa, dx, st);
+    else run_products<2, 4, Q8>(ob, oa, dx, st);
   } else {
     run_outer<false, true>(ob, st);
     run_outer<Q8, false>(oa, st);

@@ -150,10 +150,16 @@ __device__ __forceinline__ Tile find_tile(const RowPlan& p, int slot, int32_t* r
     __syncthreads();
     const int mine = tid < p.M ? cls[tid] : -1;
     int rank = 0;
-    for (int k = 0; k < p.M; k += 4) {
-      const int4 c = *reinterpret_cast<const int4*>(cls + k);   // entries from M on are -1
-      rank += (c.x == mine && k < tid) + (c.y == mine && k + 1 < tid) + (c.z == mine && k + 2 < tid) +
-              (c.w == mine && k + 3 < tid);
+    for (int k0 = 0; k0 < p.M; k0 += 32) {
+      int4 c[8];   // entries from M on are -1
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[i] = *reinterpret_cast<const int4*>(cls + k0 + 4 * i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = k0 + 4 * i;
+        rank += (c[i].x == mine && k < tid) + (c[i].y == mine && k + 1 < tid) + (c[i].z == mine && k + 2 < tid) +
+                (c[i].w == mine && k + 3 < tid);
+      }
     }
     const bool starts_tile = mine >= 0 && rank % T == 0;
     const uint64_t sb = __ballot(starts_tile);
@@ -323,7 +329,7 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
 }
 
 // Many rows: HBM-bound on x.  A tile of 16 W rows per workgroup, 16 per wavefront, so that w
-// is read once per tile; it goes through LDS (two buffers of 128 channels in operand order,
+// is read once per tile; it goes through LDS (two buffers of 64 channels in operand order,
 // conflict-free 16-byte accesses) while x streams into registers two chunks ahead.  With w
 // read by every wavefront for itself the kernel was bound by L2 traffic: 4096 rows x 28672
 // channels at rank 64 took 83 us with 64 rows per wavefront, 138 us with 16.
@@ -338,7 +344,7 @@ template <int NT, int W>
 __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* __restrict__ x,
                                                                   const half_t* __restrict__ w, RowPlan plan, int C,
                                                                   int R, int S, float* __restrict__ out) {
-  constexpr int T = 16 * W, SC = 4;                       // steps per chunk
+  constexpr int T = 16 * W, SC = 2;                       // steps per chunk
   constexpr int kPieces = NT * 16 * SC * 4;               // 16-byte pieces of w per chunk
   constexpr int PT = (kPieces + 64 * W - 1) / (64 * W);   // per thread
   __shared__ int32_t rows[T];
@@ -427,16 +433,19 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* 
 
 // --- expand: out[m][c] = binary16(base[m][c] + s_i sum_j h[m][j] w_i[c][j]) ---------------
 //
-// Weights are the A operand (16 channels x 32 ranks), h the B operand (16 rows).  A wavefront
-// holds the weights of 128 channels (8 MFMA tiles) and walks the rows 16 at a time.  The
-// channels are dealt to the MFMA rows so that a lane ends up with four runs of 8
-// consecutive channels of one row (run u at 32 u + 8 q), and base and out move as 16-byte
-// accesses, 64 bytes of a row per quarter wavefront.
-//   TRANS == false, w [L][C][R]: MFMA row 4 q + r of tile t is channel 32 (t / 2) + 8 q + 4
-//     (t % 2) + r.
-//   TRANS, w [L][R][C]: lane (r, q) loads octet (r >> 2) + 4 (r & 3) of its 8 ranks and
-//     transposes the 8 x 8 block in registers; tile t has channel t of every octet, and
-//     MFMA row 4 q + r is octet q + 4 r.
+// One operand of an MFMA is 16 rows x 32 ranks of h, the other 32 ranks x 16 channels of the
+// weights; a wavefront holds the weights of 128 channels (8 tiles).  Two arrangements:
+//   many rows   h is the A operand; column r of tile t is channel 8 r + t, so a lane (r, q)
+//               ends up with 8 consecutive channels of each of the rows 4 q .. 4 q + 3, and
+//               base and out move as 16-byte accesses of 256 consecutive bytes per row.
+//               w [L][C][R], or TRANS: w [L][R][C], where lane (r, q) loads octet r of its 8
+//               ranks and transposes the 8 x 8 block in registers.
+//   few rows    the weights are the A operand; row 4 q + r of tile t is channel 32 (t / 2) +
+//               8 q + 4 (t % 2) + r, so a lane has four runs of 8 channels (at 32 u + 8 q) of
+//               row r: 64 bytes of a row per access, but the weights, here the larger part,
+//               are read as 4 whole rows of w (the first arrangement reads every eighth).
+// Measured: 4096 rows x 28672 channels at rank 64 94 us in the first, 114 us in the second;
+// one row, 1536 channels, rank 16 (whole forward) 7.2 us in the first, 6.0 us in the second.
 // R <= 16 (PACKED): hi and lo share one MFMA, ranks 0..15 of hi in its first 16 slots and
 // of lo in the last 16, against the same weights.  Larger R: F fragments of 32 ranks,
 // one MFMA for hi and one for lo each.
@@ -481,10 +490,12 @@ __device__ __forceinline__ void sum_slices8(const float* __restrict__ p, size_t 
   }
 }
 
-// Weights of the 128 channels from c0 (channels past C repeat valid ones).
-template <int F, bool PACKED, bool TRANS>
+// Weights of the 128 channels from c0 (channels past C repeat valid ones), in the order of
+// many rows or of few.
+template <int F, bool PACKED, bool TRANS, bool MANY>
 __device__ __forceinline__ void load_expand_weights(const half_t* __restrict__ w, int c0, int C, int R, int lane,
                                                     half8_t (&wf)[F][8]) {
+  static_assert(MANY || !TRANS, "few rows read w [L][C][R]");
   const int lr = lane & 15, lq = lane >> 4;
 #pragma unroll
   for (int f = 0; f < F; ++f) {
@@ -493,12 +504,12 @@ __device__ __forceinline__ void load_expand_weights(const half_t* __restrict__ w
     if constexpr (!TRANS) {
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
-        const int c = min(c0 + 32 * (t >> 1) + 8 * (lr >> 2) + 4 * (t & 1) + (lr & 3), C - 1);
+        const int c = min(c0 + (MANY ? 8 * lr + t : 32 * (t >> 1) + 8 * (lr >> 2) + 4 * (t & 1) + (lr & 3)), C - 1);
         const half8_t v = *reinterpret_cast<const half8_t*>(w + static_cast<size_t>(c) * R + (in ? j0 : 0));
         wf[f][t] = in ? v : half8_t{};
       }
     } else {
-      const int cc = min(c0 + 8 * ((lr >> 2) + 4 * (lr & 3)), C - 8);
+      const int cc = min(c0 + 8 * lr, C - 8);
       uint4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -512,7 +523,7 @@ __device__ __forceinline__ void load_expand_weights(const half_t* __restrict__ w
 }
 
 // Products of one group of 16 rows with the weights.
-template <int F, int P>
+template <int F, int P, bool MANY>
 __device__ __forceinline__ void expand_products(const half8_t (&wf)[F][8], const half8_t (&hf)[F][P], float4_t (&acc)[8]) {
 #pragma unroll
   for (int t = 0; t < 8; ++t) acc[t] = float4_t{};
@@ -521,19 +532,19 @@ __device__ __forceinline__ void expand_products(const half8_t (&wf)[F][8], const
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int t = 0; t < 8; ++t) acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[f][t], hf[f][p], acc[t], 0, 0, 0);
+      for (int t = 0; t < 8; ++t)
+        acc[t] = MANY ? __builtin_amdgcn_mfma_f32_16x16x32_f16(hf[f][p], wf[f][t], acc[t], 0, 0, 0)
+                      : __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[f][t], hf[f][p], acc[t], 0, 0, 0);
 }
 
-// Run u of a lane: 8 results from the sums and the base values.
-template <bool TRANS>
-__device__ __forceinline__ half8_t expand_run(const float4_t (&acc)[8], int u, uint4 y, float factor) {
+// 8 consecutive results of a lane: row 4 q + u (many rows), run u (few rows).
+template <bool MANY>
+__device__ __forceinline__ half8_t expand_result(const float4_t (&acc)[8], int u, uint4 y, float factor) {
   const half8_t yv = __builtin_bit_cast(half8_t, y);
   half8_t o;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = TRANS ? acc[i][u] : acc[2 * u + (i >> 2)][i & 3];
-    o[i] = static_cast<half_t>(fmaf(v, factor, static_cast<float>(yv[i])));
-  }
+  for (int i = 0; i < 8; ++i)
+    o[i] = static_cast<half_t>(fmaf(MANY ? acc[i][u] : acc[2 * u + (i >> 2)][i & 3], factor, static_cast<float>(yv[i])));
   return o;
 }
 
@@ -744,16 +755,16 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
   }
   const int c0 = c_lo + wave * 128;
   const bool mine = lr < tile.count;
-  const size_t at = static_cast<size_t>(rows[mine ? lr : 0]);
+  const size_t at = static_cast<size_t>(rows[lr]);
   uint4 y[4];
   half8_t wf[F][8];
   if (c0 < C) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       y[u] = *reinterpret_cast<const uint4*>(base + at * C + min(c0 + 32 * u + 8 * lq, C - 8));
-    load_expand_weights<F, PACKED, false>(w + static_cast<size_t>(tile.adapter) * R * C, c0, C, R, lane, wf);
+    load_expand_weights<F, PACKED, false, false>(w + static_cast<size_t>(tile.adapter) * R * C, c0, C, R, lane, wf);
   }
-  if (wave == 0) {
+  if (wave == 0) {   // lane (r, q): ranks 8 q .. of row r
     float v[F][8];
 #pragma unroll
     for (int f = 0; f < F; ++f) {
@@ -783,11 +794,11 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
 #pragma unroll
     for (int p = 0; p < P; ++p) hf[f][p] = split[f][p][lane];
   float4_t acc[8];
-  expand_products<F, P>(wf, hf, acc);
+  expand_products<F, P, false>(wf, hf, acc);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int c = c0 + 32 * u + 8 * lq;
-    const half8_t o = expand_run<false>(acc, u, y[u], factor[lr]);
+    const half8_t o = expand_result<false>(acc, u, y[u], factor[lr]);
     if (c < C && mine) *reinterpret_cast<half8_t*>(out + at * C + c) = o;
   }
 }
@@ -829,15 +840,15 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
       for (int i = tid; i < tile.count * R; i += 64 * W) h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
     return;
   }
-  const size_t at = static_cast<size_t>(rows[lr]);
   const int c0 = (block * W + wave) * 128;
+  const size_t at = static_cast<size_t>(rows[lr]);
   uint4 y[4];
   half8_t wf[F][8];
   if (c0 < N) {
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       y[u] = *reinterpret_cast<const uint4*>(base + at * N + min(c0 + 32 * u + 8 * lq, N - 8));
-    load_expand_weights<F, PACKED, false>(w + static_cast<size_t>(tile.adapter) * R * N, c0, N, R, lane, wf);
+    load_expand_weights<F, PACKED, false, false>(w + static_cast<size_t>(tile.adapter) * R * N, c0, N, R, lane, wf);
   }
 
   float4_t acc[NT] = {};
@@ -852,7 +863,6 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
   if (h_out && block == 0)
     for (int i = tid; i < tile.count * R; i += 64 * W)
       h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = hs[(i / R) * ld + i % R];
-  if (c0 >= N) return;
   float v[F][8];
 #pragma unroll
   for (int f = 0; f < F; ++f) {
@@ -860,14 +870,15 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[f][j] = j0 < R ? hs[lr * ld + j0 + j] : 0.0f;
   }
+  if (c0 >= N) return;
   half8_t hf[F][P];
   const float factor = split_row<F, PACKED>(v, lq, scaling ? scaling[tile.adapter] : 1.0f, hf);
   float4_t sums[8];
-  expand_products<F, P>(wf, hf, sums);
+  expand_products<F, P, false>(wf, hf, sums);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int c = c0 + 32 * u + 8 * lq;
-    const half8_t o = expand_run<false>(sums, u, y[u], factor);
+    const half8_t o = expand_result<false>(sums, u, y[u], factor);
     if (c < N && lr < tile.count) *reinterpret_cast<half8_t*>(out + at * N + c) = o;
   }
 }
@@ -880,13 +891,19 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
 // registers and the operands and base values of the next D row groups in flight.  The
 // workgroups of one group of slots are neighbours, so an XCD's L2 holds few channels of w.
 // base may equal out, or be absent (BASE == false: 0); rows without an adapter are copied.
+// out is written past the L2 (nobody reads it here): with plain stores 114 -> 99 us in the
+// example above, 94 us with these; 2048 rows x 14336 at rank 16 25.3 -> 19.6 us.
 template <int F, int P>
 struct StreamRows {
   uint4 y[4];
   half8_t h[F][P];
-  int row;
-  float factor;
+  int4 row;          // rows 4 q .. 4 q + 3 of the group
+  float4_t factor;
 };
+
+__device__ __forceinline__ void store_past_l2(half_t* p, half8_t v) {
+  __builtin_nontemporal_store(__builtin_bit_cast(u32x4_t, v), reinterpret_cast<u32x4_t*>(p));
+}
 
 struct StreamArgs {
   const half_t* frags;
@@ -913,6 +930,7 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
   const int lr = lane & 15, lq = lane >> 4;
   const int blocks = (C + 511) >> 9;
   const int c0 = (block % blocks) * 512 + wave * 128;
+  const int c = c0 + 8 * lr;
   const int s0 = (block / blocks) * group;
   if (c0 >= C) return;
   const int ns = min(group, slots - s0);
@@ -927,7 +945,6 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
       if (count > 0 && base != out)
         for (int m = lq; m < count; m += 4) {
           const size_t at = static_cast<size_t>(table.rows[(s0 + i) * kSlotRows + m]) * C;
-          const int c = c0 + 8 * lr;
           if (c < C) *reinterpret_cast<uint4*>(out + at + c) = BASE ? *reinterpret_cast<const uint4*>(base + at + c) : uint4{0, 0, 0, 0};
         }
       ++i;
@@ -939,38 +956,40 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
     const int last = __builtin_amdgcn_readlane(meta.y, end - 1);
     const int n = 2 * (end - i - 1) + ((last + 15) >> 4);            // row groups
     const int total = 32 * (end - i - 1) + last;                      // rows
-    load_expand_weights<F, PACKED, TRANS>(w + static_cast<size_t>(adapter) * R * C, c0, C, R, lane, wf);
+    load_expand_weights<F, PACKED, TRANS, true>(w + static_cast<size_t>(adapter) * R * C, c0, C, R, lane, wf);
     const int g0 = 2 * (s0 + i);
-    auto load = [&](int g, int row, StreamRows<F, P>& o) {   // g < n
+    auto load = [&](int g, int4 row, StreamRows<F, P>& o) {   // g < n
       o.row = row;
-      o.factor = factors[(g0 + g) * 16 + lr];
+      o.factor = *reinterpret_cast<const float4_t*>(factors + (g0 + g) * 16 + 4 * lq);
       const half8_t* f8 = reinterpret_cast<const half8_t*>(frags) + static_cast<size_t>(g0 + g) * F * P * 64 + lane;
 #pragma unroll
       for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int p = 0; p < P; ++p) o.h[f][p] = f8[(f * P + p) * 64];
       if constexpr (BASE) {
-        const half_t* b = base + static_cast<size_t>(row) * C;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) o.y[u] = *reinterpret_cast<const uint4*>(b + min(c0 + 32 * u + 8 * lq, C - 8));
+        const half_t* b = base + min(c, C - 8);
+        o.y[0] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.x) * C);
+        o.y[1] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.y) * C);
+        o.y[2] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.z) * C);
+        o.y[3] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.w) * C);
       }
     };
     auto finish = [&](int g, const StreamRows<F, P>& o) {
       float4_t acc[8];
-      expand_products<F, P>(wf, o.h, acc);
-      if (16 * g + lr < total) {
-        half_t* po = out + static_cast<size_t>(o.row) * C;
+      expand_products<F, P, true>(wf, o.h, acc);
+      const int rows[4] = {o.row.x, o.row.y, o.row.z, o.row.w};
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int c = c0 + 32 * u + 8 * lq;
-          if (c < C) *reinterpret_cast<half8_t*>(po + c) = expand_run<TRANS>(acc, u, BASE ? o.y[u] : uint4{0, 0, 0, 0}, o.factor);
-        }
+      for (int r = 0; r < 4; ++r) {
+        const half8_t v = expand_result<true>(acc, r, BASE ? o.y[r] : uint4{0, 0, 0, 0}, o.factor[r]);
+        if (c < C && 16 * g + 4 * lq + r < total) store_past_l2(out + static_cast<size_t>(rows[r]) * C + c, v);
       }
     };
     // rows are looked up D groups ahead of their loads
-    auto row_of = [&](int g) { return table.rows[(g0 + min(g, n - 1)) * 16 + lr]; };
+    auto row_of = [&](int g) {
+      return *reinterpret_cast<const int4*>(table.rows + (g0 + min(g, n - 1)) * 16 + 4 * lq);
+    };
     StreamRows<F, P> ring[D];
-    int ahead[D];
+    int4 ahead[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) ahead[d] = row_of(d);
 #pragma unroll
@@ -1000,7 +1019,7 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
 }
 
 template <int F, bool PACKED, bool TRANS, bool BASE, int D>
-__global__ __launch_bounds__(256) void lora_stream_kernel(StreamArgs args) {
+__global__ __launch_bounds__(256, F <= 2 ? 2 : 1) void lora_stream_kernel(StreamArgs args) {
   stream_rows<F, PACKED, TRANS, BASE, D>(args, blockIdx.x);
 }
 
@@ -1082,7 +1101,7 @@ struct OuterArgs {
 };
 
 // Workgroup `block` of columns x parts x rank blocks x adapters, D slots in flight per
-// wavefront.  red: W * NT * 64 entries of LDS.
+// wavefront.  red: outer_lds(NT, W) entries of LDS.
 template <int NT, int W, int D, bool Q8, bool CMAJOR>
 __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, float4_t* red) {
   const half_t* __restrict__ x = args.x;
@@ -1197,26 +1216,53 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
   if (n > 0) {
     OuterSlot<NT, Q8> ring[D];
     const int first = part * W + wave, stride = parts * W;
-    find_rows(first);
+    const int mine = first < n ? (n - first + stride - 1) / stride : 0;   // slots of this wavefront
+    auto slot_of = [&](int k) { return first + k * stride; };
+    find_rows(slot_of(0));
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      load(first + d * stride, ring[d]);
-      find_rows(first + (d + 1) * stride);
+      load(slot_of(d), ring[d]);
+      find_rows(slot_of(d + 1));
     }
-    for (int k = first; k < n; k += D * stride) {
+    int k = 0;
+    if constexpr (NT <= 2) {   // the tail loads only what is left
+      for (; k + 2 * D <= mine; k += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          add(ring[d]);
+          load(slot_of(k + d + D), ring[d]);
+          find_rows(slot_of(k + d + D + 1));
+        }
+      }
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (k + d * stride >= n) break;
-        add(ring[d]);
-        load(k + (d + D) * stride, ring[d]);
-        find_rows(k + (d + D + 1) * stride);
+        if (k + d < mine) add(ring[d]);
+        if (k + d + D < mine) {
+          load(slot_of(k + d + D), ring[d]);
+          find_rows(slot_of(k + d + D + 1));
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < D; ++d)
+        if (k + d + D < mine) add(ring[d]);
+    } else {   // many slots per wavefront: D loads of the last slot in vain, but one copy of the code
+      for (; k < mine; k += D) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+          if (k + d >= mine) break;
+          add(ring[d]);
+          load(slot_of(k + d + D), ring[d]);
+          find_rows(slot_of(k + d + D + 1));
+        }
       }
     }
   }
 
-  // Sum over the wavefronts, one channel fragment at a time, in units of 1.
+  // Sum over the wavefronts, one channel fragment at a time, in units of 1; the sums are
+  // collected in LDS in the order of the gradient and leave as whole rows.
   const float si = scaling ? scaling[ad] : 1.0f;
-  float* g = grad + (static_cast<size_t>(part) * plan.L + ad) * R * C;
+  float* sums = reinterpret_cast<float*>(red + W * NT * 64);   // [128][16 NT + 4] or [16 NT][128 + 4]
+  constexpr int ld = CMAJOR ? 16 * NT + 4 : 128 + 4;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     __syncthreads();
@@ -1231,37 +1277,53 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
     for (int i = tid; i < NT * 64; i += 64 * W) {
       float4_t v = red[i];
       for (int w = 1; w < W; ++w) v += red[w * NT * 64 + i];
-      const int j0 = 16 * (t0 + i / 64);
+      const int j0 = 16 * (i / 64), l = i & 63;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int ch = CMAJOR ? c0 + 8 * (4 * ((i & 63) >> 4) + r) + c : c0 + 8 * (i & 15) + c;
-        const int j = CMAJOR ? j0 + (i & 15) : j0 + 4 * ((i & 63) >> 4) + r;
-        if (ch < C && j < R) g[CMAJOR ? static_cast<size_t>(ch) * R + j : static_cast<size_t>(j) * C + ch] = si * v[r];
+        const int ch = CMAJOR ? 8 * (4 * (l >> 4) + r) + c : 8 * (l & 15) + c;
+        const int j = CMAJOR ? j0 + (l & 15) : j0 + 4 * (l >> 4) + r;
+        sums[CMAJOR ? ch * ld + j : j * ld + ch] = si * v[r];
       }
     }
   }
+  __syncthreads();
+  float* g = grad + (static_cast<size_t>(part) * plan.L + ad) * R * C;
+  const int nj = min(16 * NT, R - 16 * t0), nc = min(128, C - c0);   // both multiples of 8
+  const int quads = (CMAJOR ? nj : nc) >> 2, lines = CMAJOR ? nc : nj;
+  for (int i = tid; i < quads * lines; i += 64 * W) {
+    const int line = i / quads, q = i % quads;
+    const float4_t v = *reinterpret_cast<const float4_t*>(sums + line * ld + 4 * q);
+    float* o = CMAJOR ? g + static_cast<size_t>(c0 + line) * R + 16 * t0 : g + static_cast<size_t>(16 * t0 + line) * C + c0;
+    *reinterpret_cast<float4_t*>(o + 4 * q) = v;
+  }
+}
+
+// Entries of LDS that outer_sums needs (the larger of its two gradient layouts).
+constexpr int outer_lds(int NT, int W) {
+  const int by_channel = 128 * (16 * NT + 4), by_rank = 16 * NT * (128 + 4);
+  return W * NT * 64 + (by_channel > by_rank ? by_channel : by_rank) / 4;
 }
 
 template <int NT, int W, int D, bool Q8, bool CMAJOR>
 __global__ __launch_bounds__(64 * W) void lora_outer_kernel(OuterArgs args) {
-  __shared__ float4_t red[W * NT * 64];
+  __shared__ float4_t red[outer_lds(NT, W)];
   outer_sums<NT, W, D, Q8, CMAJOR>(args, blockIdx.x, red);
 }
 
-// The three products of the backward pass in one launch, for R <= 32: their workgroups fill
-// the GPU together (the outer products alone have one per 128 channels), and two launches
-// fall away.  Workgroups: dB, then dA, then dx.
-template <int NT, bool Q8, bool DX, bool BASE>
-__global__ __launch_bounds__(256) void lora_products_kernel(OuterArgs b, int b_blocks, OuterArgs a, int a_blocks,
-                                                            StreamArgs dx) {
-  __shared__ float4_t red[4 * NT * 64];
+// The three products of the backward pass in one launch: their workgroups fill the GPU
+// together (the outer products alone have one per 128 channels and block of ranks), and two
+// launches fall away.  Workgroups: dB, then dA, then dx (F fragments of 32 ranks).
+template <int NT, int F, bool Q8, bool DX, bool BASE>
+__global__ __launch_bounds__(256, F <= 2 ? 2 : 1) void lora_products_kernel(OuterArgs b, int b_blocks, OuterArgs a,
+                                                                           int a_blocks, StreamArgs dx) {
+  __shared__ float4_t red[outer_lds(NT, 4)];
   const int block = blockIdx.x;
   if (block < b_blocks) {
     outer_sums<NT, 4, 2, false, true>(b, block, red);
   } else if (block < b_blocks + a_blocks) {
     outer_sums<NT, 4, 2, Q8, false>(a, block - b_blocks, red);
   } else {
-    if constexpr (DX) stream_rows<1, NT == 1, true, BASE, 2>(dx, block - b_blocks - a_blocks);
+    if constexpr (DX) stream_rows<F, NT == 1, true, BASE, F == 4 ? 1 : 2>(dx, block - b_blocks - a_blocks);
   }
 }
 
