@@ -138,30 +138,36 @@ int plan_slots(int M, int L, bool with_index) {
 
 // Rows per tile of a shrink, in 16s (wavefronts): 128 or 64 rows, once an adapter has that
 // many on average; below that, and for up to 512 rows at small rank, 16 with the wavefronts
-// along the channels (512 rows x 11008 at rank 16: 4.8 us, in tiles of 64 rows 5.1).
-int shrink_waves(int M, int L, int R) {
-  if (M <= 512 && R <= 32) return 1;
-  return M / L >= 128 ? 8 : M / L >= 64 ? 4 : 1;
+// along the channels (512 rows x 11008 at rank 16: 4.8 us, in tiles of 64 rows 5.1).  With
+// w transposed only the tiles of 64 rows and more, which take w through LDS.
+int shrink_waves(int M, int L, int R, bool trans) {
+  if (!trans && (M / L < 64 || (M <= 512 && R <= 32))) return 1;
+  return M / L >= 128 && (M > 512 || R > 32) ? 8 : 4;
 }
 
 // Slices of the long axis: enough workgroups for the GPU (two per compute unit), at least
-// 256 channels each (few rows: 512), and sums of the slices that stay small (8 MB) or a
-// quarter of x.
-int shrink_slices(int M, int L, int R, int C) {
-  const int waves = shrink_waves(M, L, R);
+// 256 channels each (tiles of 16 rows: 512), and sums of the slices that stay small (8 MB)
+// or a quarter of x.
+int shrink_slices(int M, int L, int R, int C, bool trans) {
+  const int waves = shrink_waves(M, L, R, trans);
   const int want = ceil_div(512, ceil_div(M, 16 * waves));
   const int64_t light = std::max<int64_t>(C / (16 * R), (int64_t{1} << 21) / (static_cast<int64_t>(M) * R));
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, C / (waves == 1 ? 512 : 256), 16, light})));
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, C / (waves == 1 ? 512 : 256), M > 512 ? 16 : 32, light})));
 }
 
+template <bool TRANS>
 void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, int R, int S, float* out, hipStream_t st) {
-  const int waves = shrink_waves(plan.M, plan.L, R);
+  const int waves = shrink_waves(plan.M, plan.L, R, TRANS);
   const dim3 grid(tiles_of(plan, 16 * waves) * S);
 #define W4A16_SHRINK(NT_, D_) \
   do { \
-    if (waves == 8) hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 8>), grid, dim3(512), 0, st, x, w, plan, C, R, S, out); \
-    else if (waves == 4) hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 4>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
-    else hipLaunchKernelGGL((lora_shrink_kernel<NT_, D_>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
+    if (waves == 8) { \
+      hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 8, TRANS>), grid, dim3(512), 0, st, x, w, plan, C, R, S, out); \
+    } else if (waves == 4) { \
+      hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 4, TRANS>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
+    } else if constexpr (!TRANS) { \
+      hipLaunchKernelGGL((lora_shrink_kernel<NT_, D_>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
+    } \
   } while (0)
   const int nt = ceil_div(R, 16);
   if (nt == 1) W4A16_SHRINK(1, 4);
@@ -248,14 +254,16 @@ int outer_parts(int M, int L, int64_t groups) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({256 / groups, M / L / (32 * kSlotRows), 16})));
 }
 
-// The products of the backward pass go out in one launch for ranks up to 32, and for up to
-// 1024 rows, where each alone leaves most of the GPU idle; then in blocks of 32 ranks, which
-// read x or dy again from the cache for every further block.  Otherwise in a launch each and
-// blocks of 64 ranks (registers for one wavefront per SIMD, which would hold the dx part back).
-bool products_merged(int M, int R) { return R <= 32 || M <= 1024; }
+// The products of the backward pass go out in one launch for ranks up to 32, and up to 64
+// for up to 1024 rows, where each alone leaves most of the GPU idle.  Beyond that dx has a
+// launch of its own: the registers of its weights, or of the outer products in blocks of 64
+// ranks, would hold the other part back.
+bool products_merged(int M, int R) { return R <= 32 || (M <= 1024 && R <= 64); }
 
-// 16s of ranks per block.
-int outer_nt(int M, int R) { return R <= 16 ? 1 : products_merged(M, R) ? 2 : 4; }
+// 16s of ranks per block of an outer product.  Blocks of 32 ranks read x or dy again (from
+// the cache) for every further block; with few rows that costs less than one wavefront per
+// SIMD, which is what blocks of 64 ranks leave room for.
+int outer_nt(int M, int R) { return R <= 16 ? 1 : R <= 32 || M <= 1024 ? 2 : 4; }
 
 int64_t outer_groups(int M, int C, int R, int L) {
   return static_cast<int64_t>(ceil_div(C, 128)) * ceil_div(R, 16 * outer_nt(M, R)) * L;
@@ -268,9 +276,12 @@ OuterArgs outer_args(const Kept& k, const ByRank& f, const float* scaling, const
   return {k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts};
 }
 
-template <bool Q8, bool CMAJOR>
-void run_outer(const OuterArgs& o, hipStream_t st) {
-  hipLaunchKernelGGL((lora_outer_kernel<4, 4, 2, Q8, CMAJOR>), dim3(static_cast<unsigned>(outer_blocks(o))), dim3(256), 0, st, o);
+template <bool Q8>
+void run_outers(const OuterArgs& b, const OuterArgs& a, hipStream_t st) {
+  const int nb = static_cast<int>(outer_blocks(b)), na = static_cast<int>(outer_blocks(a));
+  const dim3 grid(nb + na), block(256);
+  if (outer_nt(b.plan.M, b.R) == 2) hipLaunchKernelGGL((lora_outers_kernel<2, Q8>), grid, block, 0, st, b, nb, a);
+  else hipLaunchKernelGGL((lora_outers_kernel<4, Q8>), grid, block, 0, st, b, nb, a);
 }
 
 template <int NT, int F, bool Q8>
@@ -302,7 +313,7 @@ ForwardMemory forward_memory(Carver& ws, const int32_t* index, bool with_index, 
   }
   m.stream = M > kInlineRows;
   m.plan = take_plan(ws, index, with_index && M > kInlineRows, M, L);
-  m.S = shrink_slices(M, L, R, K);
+  m.S = shrink_slices(M, L, R, K, false);
   m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
   if (m.stream) {
     m.slots = plan_slots(M, L, with_index);
@@ -316,7 +327,6 @@ ForwardMemory forward_memory(Carver& ws, const int32_t* index, bool with_index, 
 
 struct BackwardMemory {
   RowPlan plan;
-  half_t* bt;        // [L][R][N]
   float* part;       // g: [S][M][R]
   int S, slots;
   ByRank h, g;
@@ -330,8 +340,7 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
                                int L) {
   BackwardMemory m{};
   m.plan = take_plan(ws, index, with_index, M, L);
-  m.bt = ws.take<half_t>(static_cast<size_t>(L) * R * N);
-  m.S = shrink_slices(M, L, R, N);
+  m.S = shrink_slices(M, L, R, N, true);
   m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
   m.slots = plan_slots(M, L, with_index);
   m.h = take_by_rank(ws, m.slots, R);
@@ -339,6 +348,8 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
   m.g_rows = take_by_row(ws, m.slots, R);
   m.table = take_table(ws, m.slots);
   const int64_t ga = outer_groups(M, K, R, L), gb = outer_groups(M, N, R, L);
+  // One launch with dx: counted together.  Otherwise the workgroups of both do not fit on the
+  // GPU at once, and what comes second should be in smaller pieces than the first.
   const bool merged = products_merged(M, R);
   m.a_parts = outer_parts(M, L, merged ? ga + gb : ga);
   m.b_parts = outer_parts(M, L, merged ? ga + gb : gb);
@@ -381,14 +392,11 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const BackwardMemory m = backward_memory(ws, c.index, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
   const auto st = static_cast<hipStream_t>(c.stream);
   const auto* dy = reinterpret_cast<const half_t*>(c.dy);
-  const int plans = c.index ? c.L + 1 : 0;
-  hipLaunchKernelGGL(lora_prepare_kernel, dim3(plans + ceil_div(c.N, transpose_rows(c.R)) * c.L), dim3(1024), 0, st,
-                     m.plan, const_cast<int32_t*>(m.plan.off), const_cast<int32_t*>(m.plan.perm), plans,
-                     reinterpret_cast<const half_t*>(c.b), m.bt, c.N, c.R);
-  run_shrink(dy, m.bt, m.plan, c.N, c.R, m.S, m.part, st);
+  run_plan(m.plan, st);
+  run_shrink<true>(dy, reinterpret_cast<const half_t*>(c.b), m.plan, c.N, c.R, m.S, m.part, st);
   const SplitTask th{c.h, 1, m.h.frags, m.h.exps, nullptr, nullptr, nullptr};
   const SplitTask tg{m.part, m.S, m.g.frags, m.g.exps, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors, nullptr};
-  hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 2), dim3(256), 0, st, th, tg, c.scaling, m.table, m.plan, c.R);
+  hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 2), dim3(512), 0, st, th, tg, c.scaling, m.table, m.plan, c.R);
   const OuterArgs ob = outer_args(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, m.b_parts > 1 ? m.db : c.db, c.N,
                                   c.R, m.b_parts);
   const OuterArgs oa = outer_args(kept, m.g, c.scaling, m.plan, m.a_parts > 1 ? m.da : c.da, c.K, c.R, m.a_parts);
@@ -398,12 +406,9 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   if (products_merged(c.M, c.R)) {
     if (c.R <= 16) run_products<1, 1, Q8>(ob, oa, dx, st);
     else if (c.R <= 32) run_products<2, 1, Q8>(ob, oa, dx, st);
-    else if (c.R <= 64) run_products<2, 2, Q8>(ob, oa, dx, st);
-    else if (c.R <= 96) run_products<2, 3, Q8>(ob, oa, dx, st);
-    else run_products<2, 4, Q8>(ob, oa, dx, st);
+    else run_products<2, 2, Q8>(ob, oa, dx, st);
   } else {
-    run_outer<false, true>(ob, st);
-    run_outer<Q8, false>(oa, st);
+    run_outers<Q8>(ob, oa, st);
     if (dx.out) dx.base ? run_stream<true, true>(dx, st) : run_stream<true, false>(dx, st);
   }
   if (m.a_parts > 1 || m.b_parts > 1) {
@@ -455,10 +460,10 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
     return check_launch("lora forward launch");
   }
   run_plan(m.plan, st);
-  run_shrink(xh, ah, m.plan, K, R, m.S, m.part, st);
+  run_shrink<false>(xh, ah, m.plan, K, R, m.S, m.part, st);
   if (m.stream) {
     const SplitTask t{m.part, m.S, nullptr, nullptr, m.h.frags, m.h.factors, h};
-    hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(256), 0, st, t, t, scaling, m.table, m.plan, R);
+    hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(512), 0, st, t, t, scaling, m.table, m.plan, R);
     run_stream<false, true>(stream_args(m.h, m.table, bh, yh, oh, N, R, L, m.slots), st);
   } else {
     run_expand(m.part, m.S, bh, scaling, m.plan, yh, oh, h, N, R, st);

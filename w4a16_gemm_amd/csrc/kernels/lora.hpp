@@ -43,8 +43,10 @@ __device__ __forceinline__ int row_class(int i, int L) { return i >= 0 && i < L 
 // its own rows in order.  No atomics, so the order (and with it every sum) is fixed.
 constexpr int kPlanRows = 8;   // rows per thread read at once (8192 per workgroup)
 
-__device__ __forceinline__ void plan_rows(int c, const int32_t* __restrict__ index, int M, int L,
-                                          int32_t* __restrict__ off, int32_t* __restrict__ perm, int (*part)[16]) {
+__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ index, int M, int L,
+                                                         int32_t* __restrict__ off, int32_t* __restrict__ perm) {
+  __shared__ int part[2][16];
+  const int c = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int cls[kPlanRows];
   auto load = [&](int m0) {   // rows past M: a class above all
@@ -89,12 +91,6 @@ __device__ __forceinline__ void plan_rows(int c, const int32_t* __restrict__ ind
       at += total;
     }
   }
-}
-
-__global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ index, int M, int L,
-                                                         int32_t* __restrict__ off, int32_t* __restrict__ perm) {
-  __shared__ int part[2][16];
-  plan_rows(blockIdx.x, index, M, L, off, perm, part);
 }
 
 // Number of tile slots for T rows per tile.  With a plan in memory the slots of class c
@@ -330,7 +326,7 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
 
 // Many rows: HBM-bound on x.  A tile of 16 W rows per workgroup, 16 per wavefront, so that w
 // is read once per tile; it goes through LDS (two buffers of 64 channels in operand order,
-// conflict-free 16-byte accesses) while x streams into registers two chunks ahead.  With w
+// 16-byte accesses) while x streams into registers two chunks ahead.  With w
 // read by every wavefront for itself the kernel was bound by L2 traffic: 4096 rows x 28672
 // channels at rank 64 took 83 us with 64 rows per wavefront, 138 us with 16.
 // The barrier orders LDS only: the x and w loads in flight pass it.
@@ -340,7 +336,10 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int NT, int W>
+// TRANS: w is [L][C][R] (the b of the forward): it comes from memory as 8 ranks of a channel,
+// and takes its operand order on the way into LDS (16-bit writes, 8 per 16 bytes; the
+// operands' padding keeps the 16 pieces of a channel on different banks).
+template <int NT, int W, bool TRANS>
 __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* __restrict__ x,
                                                                   const half_t* __restrict__ w, RowPlan plan, int C,
                                                                   int R, int S, float* __restrict__ out) {
@@ -348,7 +347,8 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* 
   constexpr int kPieces = NT * 16 * SC * 4;               // 16-byte pieces of w per chunk
   constexpr int PT = (kPieces + 64 * W - 1) / (64 * W);   // per thread
   __shared__ int32_t rows[T];
-  __shared__ half8_t lds[2][SC * NT * 64];
+  constexpr int TS = 65;                                  // operand of a step and 16 ranks, padded
+  __shared__ half8_t lds[2][SC * NT * TS];
   const int s = blockIdx.x % S;
   const Tile tile = find_tile<T>(plan, blockIdx.x / S, rows);
   if (tile.count == 0) return;
@@ -368,23 +368,43 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* 
   float4_t acc[NT] = {};
   half8_t wreg[PT];
   half8_t xs[2][SC];
+  // Pieces of 8 values of w per thread: ranks or channels of the chunk, and which.
+  const int octs = TRANS ? R >> 3 : SC * 4;   // pieces per channel or rank
+  int line[PT], oct[PT];
+#pragma unroll
+  for (int i = 0; i < PT; ++i) {
+    line[i] = (tid + 64 * W * i) / octs;
+    oct[i] = (tid + 64 * W * i) % octs;
+  }
   // Loads past the slice or past C are clamped; channels past C are zeroed on both sides.
   auto load_w = [&](int k) {
+    const int cb = min(k, e - 1) * 32 * SC;
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
-      const int p = min(tid + 64 * W * i, kPieces - 1);
-      const int j = min(p / (SC * 4), R - 1), q = p % (SC * 4);
-      wreg[i] = *reinterpret_cast<const half8_t*>(wl + static_cast<size_t>(j) * C + min(min(k, e - 1) * 32 * SC + 8 * q, C - 8));
+      const size_t at = TRANS ? static_cast<size_t>(min(cb + line[i], C - 1)) * R + 8 * oct[i]
+                              : static_cast<size_t>(min(line[i], R - 1)) * C + min(cb + 8 * oct[i], C - 8);
+      wreg[i] = *reinterpret_cast<const half8_t*>(wl + at);
     }
   };
   auto store_w = [&](int k, int buf) {
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
-      const int p = tid + 64 * W * i;
-      const int j = p / (SC * 4), q = p % (SC * 4);
-      const bool in = k * 32 * SC + 8 * q < C;
-      if (kPieces % (64 * W) == 0 || p < kPieces)
-        lds[buf][((q >> 2) * NT + (j >> 4)) * 64 + (q & 3) * 16 + (j & 15)] = in ? wreg[i] : half8_t{};
+      if constexpr (TRANS) {
+        const int c = line[i];   // channel of the chunk
+        if (c >= 32 * SC) continue;
+        const half8_t v = k * 32 * SC + c < C ? wreg[i] : half8_t{};
+        half_t* to = reinterpret_cast<half_t*>(lds[buf]) + (((c >> 5) * NT * TS + ((c >> 3) & 3) * 16) * 8 + (c & 7));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int rank = 8 * oct[i] + j;
+          to[((rank >> 4) * TS + (rank & 15)) * 8] = v[j];
+        }
+      } else {
+        const int j = line[i], q = oct[i];
+        if (j >= 16 * NT) continue;
+        lds[buf][((q >> 2) * NT + (j >> 4)) * TS + (q & 3) * 16 + (j & 15)] =
+            k * 32 * SC + 8 * q < C ? wreg[i] : half8_t{};
+      }
     }
   };
   auto load_x = [&](int k, half8_t (&v)[SC]) {
@@ -400,7 +420,7 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* 
     for (int u = 0; u < SC; ++u)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[u], lds[buf][(u * NT + t) * 64 + lane], acc[t], 0, 0, 0);
+        acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[u], lds[buf][(u * NT + t) * TS + lane], acc[t], 0, 0, 0);
   };
   load_w(b);
   load_x(b, xs[0]);
@@ -607,10 +627,10 @@ struct SlotTable {
 // By-row operands (of 1 KB) of a row group.
 __host__ __device__ constexpr int row_frags(int R) { return R <= 16 ? 1 : 2 * ((R + 31) / 32); }
 
-__global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask t1, const float* __restrict__ scaling,
+__global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask t1, const float* __restrict__ scaling,
                                                          SlotTable table, RowPlan plan, int R) {
   __shared__ int32_t rows[kSlotRows];
-  __shared__ float tops[4];
+  __shared__ float tops[8];
   __shared__ float row_top[kSlotRows];
   __shared__ float4_t sums[kSlotRows * (kMaxRank / 4 + 1)];   // rows of R / 4 + 1
   const SplitTask task = blockIdx.y == 0 ? t0 : t1;
@@ -626,12 +646,12 @@ __global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask
   if (tile.count == 0) return;
   if (tile.adapter == plan.L) {
     if (task.sum)
-      for (int i = tid; i < tile.count * R; i += 256) task.sum[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+      for (int i = tid; i < tile.count * R; i += 512) task.sum[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
     return;
   }
   const int quads = R >> 2, ld = quads + 1;
   float top = 0.0f;
-  for (int i = tid; i < kSlotRows * quads; i += 256) {
+  for (int i = tid; i < kSlotRows * quads; i += 512) {
     const int m = i / quads, j = i % quads;
     float4_t v = {};
     if (m < tile.count) {
@@ -657,11 +677,12 @@ __global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask
   __syncthreads();
   const float* f = reinterpret_cast<const float*>(sums);
   if (task.by_rank) {
-    top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, tops[w]);
     const int e = top > 0.0f ? top_exponent(top) - kSplitTop : kNoExponent;
     if (tid == 0) task.exps[slot] = e;
     const int NT = (R + 15) >> 4;
-    for (int t = wave; t < NT; t += 4) {
+    for (int t = wave; t < NT; t += 8) {
       const int j = 16 * t + lr;
       half8_t hi, lo;
 #pragma unroll
@@ -677,14 +698,14 @@ __global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask
     }
   }
   if (!task.by_row) return;
-  // largest of every row: 8 threads per row
+  // largest of every row: 16 threads per row
   {
-    const int m = tid >> 3;
+    const int m = tid >> 4;
     float rt = 0.0f;
-    for (int j = tid & 7; j < R; j += 8) rt = fmaxf(rt, finite_magnitude(f[m * 4 * ld + j]));
+    for (int j = tid & 15; j < R; j += 16) rt = fmaxf(rt, finite_magnitude(f[m * 4 * ld + j]));
 #pragma unroll
-    for (int d = 1; d < 8; d <<= 1) rt = fmaxf(rt, __shfl_xor(rt, d));
-    if ((tid & 7) == 0) {
+    for (int d = 1; d < 16; d <<= 1) rt = fmaxf(rt, __shfl_xor(rt, d));
+    if ((tid & 15) == 0) {
       row_top[m] = rt;
       const float si = scaling ? scaling[tile.adapter] : 1.0f;
       task.factors[slot * kSlotRows + m] = __builtin_ldexpf(si, top_exponent(rt) - kSplitTop);
@@ -693,7 +714,7 @@ __global__ __launch_bounds__(256) void lora_split_kernel(SplitTask t0, SplitTask
   __syncthreads();
   const bool packed = R <= 16;
   const int F = packed ? 1 : (R + 31) / 32;
-  for (int i = wave; i < 2 * F; i += 4) {   // operand pairs (row group, fragment)
+  for (int i = wave; i < 2 * F; i += 8) {   // operand pairs (row group, fragment)
     const int g = i / F, k = i % F;
     const int m = 16 * g + lr;
     const int j0 = packed ? 8 * (lq & 1) : 32 * k + 8 * lq;
@@ -1023,48 +1044,6 @@ __global__ __launch_bounds__(256, F <= 2 ? 2 : 1) void lora_stream_kernel(Stream
   stream_rows<F, PACKED, TRANS, BASE, D>(args, blockIdx.x);
 }
 
-// --- prepare: what the backward pass needs before its products, in one launch --------------
-//
-// Workgroups 0 .. plans - 1 group the rows; the others transpose b [L][N][R] to bt [L][R][N],
-// the layout the shrink reads, through LDS, about 8192 values at a time.
-constexpr int kTransposeValues = 8192;
-
-__host__ __device__ constexpr int transpose_rows(int R) { return (kTransposeValues / R) & ~7; }
-
-__global__ __launch_bounds__(1024) void lora_prepare_kernel(RowPlan plan, int32_t* __restrict__ off,
-                                                            int32_t* __restrict__ perm, int plans,
-                                                            const half_t* __restrict__ b, half_t* __restrict__ bt, int N,
-                                                            int R) {
-  __shared__ int part[2][16];
-  __shared__ half_t tile[kTransposeValues + kTransposeValues / 4];   // rows of R + 2 values, R >= 8
-  if (static_cast<int>(blockIdx.x) < plans) {
-    plan_rows(blockIdx.x, plan.index, plan.M, plan.L, off, perm, part);
-    return;
-  }
-  const int nrow = transpose_rows(R), nblk = (N + nrow - 1) / nrow;
-  const int blk = blockIdx.x - plans;
-  const size_t ad = blk / nblk;
-  const int n0 = (blk % nblk) * nrow, nr = min(nrow, N - n0);
-  const half_t* src = b + (ad * N + n0) * R;
-  half_t* dst = bt + ad * R * N + n0;
-  const int ld = R + 2;
-  for (int i = threadIdx.x; i < nr * R / 8; i += 1024) {
-    const half8_t v = *reinterpret_cast<const half8_t*>(src + 8 * i);
-    const int n = 8 * i / R, j = 8 * i % R;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) tile[n * ld + j + e] = v[e];
-  }
-  __syncthreads();
-  const int oct = nr / 8;   // N % 8 == 0
-  for (int i = threadIdx.x; i < R * oct; i += 1024) {
-    const int j = i / oct, n = 8 * (i % oct);
-    half8_t v;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = tile[(n + e) * ld + j];
-    *reinterpret_cast<half8_t*>(dst + static_cast<size_t>(j) * N + n) = v;
-  }
-}
-
 // --- outer: grad_i[c][j] = s_i sum over the rows of adapter i of x[m][c] h[m][j] ----------
 //
 // A wavefront sums 128 channels x 16 NT ranks over slots of 32 rows; the wavefronts of a
@@ -1304,18 +1283,21 @@ constexpr int outer_lds(int NT, int W) {
   return W * NT * 64 + (by_channel > by_rank ? by_channel : by_rank) / 4;
 }
 
-template <int NT, int W, int D, bool Q8, bool CMAJOR>
-__global__ __launch_bounds__(64 * W) void lora_outer_kernel(OuterArgs args) {
-  __shared__ float4_t red[outer_lds(NT, W)];
-  outer_sums<NT, W, D, Q8, CMAJOR>(args, blockIdx.x, red);
+// dB and dA in one launch: the workgroups of the second fill what the first leaves idle.
+template <int NT, bool Q8>
+__global__ __launch_bounds__(256, NT <= 2 ? 2 : 1) void lora_outers_kernel(OuterArgs b, int b_blocks, OuterArgs a) {
+  __shared__ float4_t red[outer_lds(NT, 4)];
+  const int block = blockIdx.x;
+  if (block < b_blocks) outer_sums<NT, 4, 2, false, true>(b, block, red);
+  else outer_sums<NT, 4, 2, Q8, false>(a, block - b_blocks, red);
 }
 
 // The three products of the backward pass in one launch: their workgroups fill the GPU
 // together (the outer products alone have one per 128 channels and block of ranks), and two
 // launches fall away.  Workgroups: dB, then dA, then dx (F fragments of 32 ranks).
 template <int NT, int F, bool Q8, bool DX, bool BASE>
-__global__ __launch_bounds__(256, F <= 2 ? 2 : 1) void lora_products_kernel(OuterArgs b, int b_blocks, OuterArgs a,
-                                                                           int a_blocks, StreamArgs dx) {
+__global__ __launch_bounds__(256, 2) void lora_products_kernel(OuterArgs b, int b_blocks, OuterArgs a, int a_blocks,
+                                                               StreamArgs dx) {
   __shared__ float4_t red[outer_lds(NT, 4)];
   const int block = blockIdx.x;
   if (block < b_blocks) {
@@ -1323,7 +1305,7 @@ __global__ __launch_bounds__(256, F <= 2 ? 2 : 1) void lora_products_kernel(Oute
   } else if (block < b_blocks + a_blocks) {
     outer_sums<NT, 4, 2, Q8, false>(a, block - b_blocks, red);
   } else {
-    if constexpr (DX) stream_rows<F, NT == 1, true, BASE, F == 4 ? 1 : 2>(dx, block - b_blocks - a_blocks);
+    if constexpr (DX) stream_rows<F, NT == 1, true, BASE, 2>(dx, block - b_blocks - a_blocks);
   }
 }
 
