@@ -234,7 +234,7 @@ void run_stream(const StreamArgs& s, hipStream_t st) {
   }
   if (s.R <= 64) W4A16_STREAM(2, false, 2);
   else if (s.R <= 96) W4A16_STREAM(3, false, 2);
-  else W4A16_STREAM(4, false, 1);
+  else W4A16_STREAM(4, false, 2);
 #undef W4A16_STREAM
 }
 
@@ -266,7 +266,7 @@ bool products_merged(int M, int R) { return R <= 32 || (M <= 1024 && R <= 64); }
 int outer_nt(int M, int R) { return R <= 16 ? 1 : R <= 32 || M <= 1024 ? 2 : 4; }
 
 int64_t outer_groups(int M, int C, int R, int L) {
-  return static_cast<int64_t>(ceil_div(C, 128)) * ceil_div(R, 16 * outer_nt(M, R)) * L;
+  return static_cast<int64_t>(ceil_div(C, 1024)) * 8 * ceil_div(R, 16 * outer_nt(M, R)) * L;
 }
 
 int64_t outer_blocks(const OuterArgs& o) { return outer_groups(o.plan.M, o.C, o.R, o.plan.L) * o.parts; }
@@ -513,7 +513,7 @@ extern "C" int w4a16_act_quantize(const uint16_t* x, int M, int K, int group_siz
   const Buffer bufs[] = {{x, 16, true, "x"}, {codes, 8, true, "codes"}, {scales, 2, true, "scales"}};
   if (int rc = check_buffers(bufs)) return rc;
   const size_t chunks = static_cast<size_t>(M) * (K / 8);
-  const dim3 grid(static_cast<unsigned>((chunks + 255) / 256)), block(256);
+  const dim3 grid(static_cast<unsigned>((chunks + 256 * kActRuns - 1) / (256 * kActRuns))), block(256);
   const auto st = static_cast<hipStream_t>(stream);
   const auto* xh = reinterpret_cast<const half_t*>(x);
   auto* sh = reinterpret_cast<half_t*>(scales);

@@ -1095,13 +1095,19 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  const int cols = (C + 127) >> 7, ranks = (R + 16 * NT - 1) / (16 * NT);
-  const int c0 = (block % cols) * 128;
-  block /= cols;
-  const int part = block % parts;
-  block /= parts;
+  // Neighbouring workgroups go to different XCDs (8, in turn): eight blocks of channels, then
+  // their further blocks of ranks, which thus find x in the same L2; then the next eight.
+  const int ranks = (R + 16 * NT - 1) / (16 * NT), eights = (C + 1023) >> 10;
+  int col = block & 7;
+  block >>= 3;
   const int t0 = (block % ranks) * NT;
-  const int ad = block / ranks;
+  block /= ranks;
+  col += 8 * (block % eights);
+  block /= eights;
+  const int part = block % parts;
+  const int ad = block / parts;
+  const int c0 = col * 128;
+  if (c0 >= C) return;
   const int NTT = (R + 15) >> 4;   // fragments per slot
   // slots of the adapter: [first_slot, first_slot + n); positions lo .. hi - 1
   const int lo = plan.index ? plan.off[ad] : 0;
