@@ -132,9 +132,11 @@ def backward(d, h, dx0=True, **kw):
 
 CASES = [
     # M, N, K, R, L, order, bare: one row; every tile edge around 16, 32 and 64 rows; the
-    # last row count the wavefronts group themselves (64) and the first beyond it; channel
-    # counts below one step, off every tile, and over several workgroups and slices; ranks
-    # at and between the fragment sizes; adapters without rows, rows without an adapter
+    # last row count the workgroups group themselves (256) and the first beyond it; more
+    # adapters than lanes, more rows than the grouping reads at once (8192); channel counts
+    # below one step, off every tile, and over several workgroups and slices; ranks at and
+    # between the fragment sizes, each with few and with many rows; few channels under many
+    # rows (gradients in parts); adapters without rows, rows without an adapter
     (1, 8, 8, 8, 1, "one", 0), (1, 1536, 1536, 16, 4, "mixed", 0), (2, 136, 40, 8, 3, "mixed", 0),
     (15, 520, 512, 16, 1, "one", 0), (16, 512, 1024, 24, 2, "mixed", 0.2), (17, 1000, 1032, 32, 17, "mixed", 0.1),
     (33, 264, 2048, 40, 5, "runs", 0.2), (63, 640, 264, 48, 100, "mixed", 0.1), (64, 1544, 520, 64, 3, "runs", 0),
@@ -143,6 +145,10 @@ CASES = [
     (700, 648, 392, 16, 11, "mixed", 0.2), (1111, 1032, 520, 112, 4, "runs", 0.1), (1500, 264, 264, 56, 1, "one", 0),
     (2100, 136, 1032, 32, 1, "one", 0), (40, 64, 64, 16, 4, "none", 0), (100, 64, 64, 16, 4, "none", 0),
     (5, 64, 64, 8, 300, "mixed", 0), (90, 64, 64, 8, 300, "mixed", 0.2),
+    (256, 136, 264, 16, 5, "mixed", 0.1), (400, 64, 72, 8, 300, "mixed", 0.2), (9000, 64, 64, 8, 3, "mixed", 0.1),
+    (600, 264, 520, 40, 8, "runs", 0.1), (1100, 264, 520, 64, 1, "one", 0), (1300, 520, 264, 96, 1, "one", 0),
+    (1300, 264, 520, 128, 2, "runs", 0.1), (2100, 136, 264, 72, 1, "one", 0), (3, 1544, 2056, 24, 2, "mixed", 0),
+    (48, 1032, 6152, 8, 2, "mixed", 0.1), (20, 4104, 1032, 64, 3, "mixed", 0.1), (30, 2056, 1544, 104, 2, "mixed", 0.1),
 ]
 IDS = ["M{}-N{}-K{}-R{}-L{}-{}-{}".format(*c) for c in CASES]
 
@@ -277,6 +283,14 @@ def test_rows_do_not_touch_each_other(M):
         assert same(got[1][i], want[1][i]) and same(got[2][i], want[2][i])
 
 
+def test_adapters_without_rows_get_zero_gradients():
+    d = make(300, 64, 64, 16, 4, "last", seed=2)
+    d["scaling"][:3] = [np.nan, np.inf, 1.0]
+    _, da, db = backward(d, dev(np.ones((300, 16), np.float32)))
+    assert not bool(da[:3].any()) and not bool(db[:3].any())
+    assert bool(da[3].any()) and bool(da[3].isfinite().all())
+
+
 def test_non_finite_values_show_in_the_gradients():
     d = make(96, 64, 128, 16, 1, "one")
     d["x"][70, 5] = np.inf
@@ -319,10 +333,26 @@ def test_rows_of_growing_size_rescale_the_sums():
     for power in (np.arange(M) / 8.0 - 40, 35 - np.arange(M) / 8.0):
         hp = (h * 2.0 ** power[:, None]).astype(np.float32)
         hp[10:20] = 0
+        hp[300:340] = 0
         ref = oracle.lora_backward(d["dy"], d["x"], d["a"], d["b"], hp, None, d["scaling"], d["dx0"])
         got = backward(d, dev(hp))
         for name, g, r, t in zip(("dx", "da", "db"), got, ref, backward_tol(d, hp, ref)):
             within(name, g, r, t)
+
+
+def test_slots_far_below_the_largest_are_not_dropped():
+    """256 rows of h of order 1, then 256 rows 2^-k smaller under a dy 2^19 larger: their part
+    of the gradient, 2^(19 - k) of the whole, is far above the bound for every k here."""
+    N = K = 64
+    for k in (18, 22, 24, 25, 26, 28, 30):
+        d = make(512, N, K, 16, 1, "one", seed=20 + k)
+        _, h = oracle.lora_forward(d["y"], d["x"], d["a"], d["b"])
+        h[256:] *= 2.0 ** -k
+        d["dy"] = np.concatenate([d["dy"][:256] * np.float16(2.0 ** -9), d["dy"][256:] * np.float16(2.0 ** 10)])
+        hp = h.astype(np.float32)
+        ref = oracle.lora_backward(d["dy"], d["x"], d["a"], d["b"], hp, None, d["scaling"], d["dx0"])
+        got = backward(d, dev(hp))
+        within(f"db k={k}", got[2], ref[2], backward_tol(d, hp, ref)[2])
 
 
 def test_offsets_beyond_32_bits():

@@ -390,6 +390,9 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
                          {c.scaling, 4, false, "scaling"}, {c.workspace, 16, false, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   if (c.dx0 && !c.dx) return fail(W4A16_ERR_INVALID_ARG, "dx0 is given without dx");
+  // the only grid that the bounds on the sizes do not keep below 2^32 threads
+  if (outer_groups(c.M, c.N, c.R, c.L) + outer_groups(c.M, c.K, c.R, c.L) >= int64_t{1} << 23)
+    return fail(W4A16_ERR_UNSUPPORTED, "gradients of %d adapters for N=%d, K=%d are too large for one call", c.L, c.N, c.K);
   Carver size{nullptr}, ws{static_cast<unsigned char*>(c.workspace)};
   backward_memory(size, nullptr, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
   if (int rc = check_workspace(c.workspace, c.workspace_bytes, size.used)) return rc;

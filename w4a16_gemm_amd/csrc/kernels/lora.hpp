@@ -4,7 +4,7 @@
 //   h[m] = A_i x[m]                                  (shrink, K -> R)
 //   out[m] = y[m] + s_i B_i h[m]                     (expand, R -> N)
 // Backward:
-//   g[m] = B_i^T dy[m]                               (shrink, N -> R, B transposed first)
+//   g[m] = B_i^T dy[m]                               (shrink, N -> R)
 //   dx[m] = dx0[m] + s_i A_i^T g[m]                  (expand, R -> K)
 //   dB_i = s_i sum_m dy[m] h[m]^T,  dA_i = s_i sum_m g[m] x[m]^T       (outer)
 //
@@ -14,7 +14,7 @@
 // by a power of two that brings the largest of them to [2^13, 2^14), so nothing overflows
 // and the split loses less than the fp32 sums do.
 //
-// Rows are worked on in tiles of 16 MT rows of one adapter each; rows of one adapter are
+// Rows are worked on in tiles of 16 to 128 rows of one adapter each; rows of one adapter are
 // found through a row plan (below), so any order of rows costs the same products.
 #pragma once
 
@@ -1166,11 +1166,14 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
             for (int r = 0; r < 4; ++r) acc[c][t][r] = __builtin_ldexpf(acc[c][t][r], E - e);
       E = e;
     } else if (e < E && e != kNoExponent) {
-      const half_t down = static_cast<half_t>(__builtin_ldexpf(1.0f, max(e - E, -40)));
+      // 2^(e - E) in two factors that binary16 holds; beyond 2^-40 nothing is left
+      const int d = max(e - E, -40), d0 = max(d, -20);
+      const half_t down0 = static_cast<half_t>(__builtin_ldexpf(1.0f, d0));
+      const half_t down1 = static_cast<half_t>(__builtin_ldexpf(1.0f, d - d0));
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        o.h[t][0] *= down;
-        o.h[t][1] *= down;
+        o.h[t][0] = o.h[t][0] * down0 * down1;
+        o.h[t][1] = o.h[t][1] * down0 * down1;
       }
     }
 #pragma unroll
@@ -1245,7 +1248,7 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
 
   // Sum over the wavefronts, one channel fragment at a time, in units of 1; the sums are
   // collected in LDS in the order of the gradient and leave as whole rows.
-  const float si = scaling ? scaling[ad] : 1.0f;
+  const float si = n == 0 ? 0.0f : scaling ? scaling[ad] : 1.0f;
   float* sums = reinterpret_cast<float*>(red + W * NT * 64);   // [128][16 NT + 4] or [16 NT][128 + 4]
   constexpr int ld = CMAJOR ? 16 * NT + 4 : 128 + 4;
 #pragma unroll
