@@ -107,9 +107,9 @@ ByRank take_by_rank(Carver& ws, int slots, int R) {
   return {f, ws.take<int32_t>(slots)};
 }
 
-SlotTable take_table(Carver& ws, int slots) {
+SlotTable take_table(Carver& ws, int slots, int rows) {
   int2* meta = ws.take<int2>(slots);
-  return {meta, ws.take<int32_t>(static_cast<size_t>(slots) * kSlotRows)};
+  return {meta, ws.take<int32_t>(static_cast<size_t>(slots) * rows)};
 }
 
 // Memory of a row plan; without an index the rows need none.
@@ -148,16 +148,17 @@ int shrink_waves(int M, int L, int R, bool trans) {
 // Slices of the long axis: enough workgroups for the GPU (two per compute unit), at least
 // 256 channels each (tiles of 16 rows: 512), and sums of the slices that stay small (8 MB)
 // or a quarter of x.
-int shrink_slices(int M, int L, int R, int C, bool trans) {
-  const int waves = shrink_waves(M, L, R, trans);
+int shrink_slices(int M, int L, int R, int C, bool trans, bool stream) {
+  const int waves = stream ? shrink_waves(M, L, R, trans) : 1;
   const int want = ceil_div(512, ceil_div(M, 16 * waves));
   const int64_t light = std::max<int64_t>(C / (16 * R), (int64_t{1} << 21) / (static_cast<int64_t>(M) * R));
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, C / (waves == 1 ? 512 : 256), M > 512 ? 16 : 32, light})));
 }
 
 template <bool TRANS>
-void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, int R, int S, float* out, hipStream_t st) {
-  const int waves = shrink_waves(plan.M, plan.L, R, TRANS);
+void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, int R, int S, float* out, SlotTable few,
+                hipStream_t st) {
+  const int waves = few.meta ? 1 : shrink_waves(plan.M, plan.L, R, TRANS);
   const dim3 grid(tiles_of(plan, 16 * waves) * S);
 #define W4A16_SHRINK(NT_, D_) \
   do { \
@@ -166,7 +167,7 @@ void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, in
     } else if (waves == 4) { \
       hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 4, TRANS>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
     } else if constexpr (!TRANS) { \
-      hipLaunchKernelGGL((lora_shrink_kernel<NT_, D_>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
+      hipLaunchKernelGGL((lora_shrink_kernel<NT_, D_>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out, few); \
     } \
   } while (0)
   const int nt = ceil_div(R, 16);
@@ -179,11 +180,11 @@ void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, in
 
 // --- expand -------------------------------------------------------------------------
 
-void run_expand(const float* h, int S, const half_t* w, const float* scaling, const RowPlan& plan, const half_t* base,
-                half_t* out, float* h_out, int C, int R, hipStream_t st) {
-  const dim3 grid(tiles_of(plan, 16), ceil_div(C, 512)), block(256);
+void run_expand(const float* h, int S, const SlotTable& table, int slots, const half_t* w, const float* scaling, int L,
+                const half_t* base, half_t* out, float* h_out, int C, int R, hipStream_t st) {
+  const dim3 grid(slots, ceil_div(C, 512)), block(256);
 #define W4A16_EXPAND(F_, P_) \
-  hipLaunchKernelGGL((lora_expand_kernel<F_, P_>), grid, block, 0, st, h, S, w, scaling, plan, base, out, h_out, C, R)
+  hipLaunchKernelGGL((lora_expand_kernel<F_, P_>), grid, block, 0, st, h, S, table, w, scaling, L, base, out, h_out, C, R)
   if (R <= 16) W4A16_EXPAND(1, true);
   else if (R <= 32) W4A16_EXPAND(1, false);
   else if (R <= 64) W4A16_EXPAND(2, false);
@@ -192,13 +193,17 @@ void run_expand(const float* h, int S, const half_t* w, const float* scaling, co
 #undef W4A16_EXPAND
 }
 
-// The whole forward in one launch where every workgroup (of 1024 output channels) can read
-// its adapter's A again in the time of a launch: up to 96 KB of A.  Measured (graph replay,
-// both ways): K = 1536, rank 16, one row 6.7 us against 7.5 us in two launches; 256 rows of
-// 32 adapters at rank 32 24.1 against 28.7; K = 4096, rank 16, one row 9.1 against 8.2.
+// The whole forward in one launch where every workgroup (of one tile and 1024 output channels)
+// can read its adapter's A again in the time of a launch, up to 96 KB of A, and all of them
+// run at once.  Measured (graph replay, one launch against two): K = 1536, N = 1536, rank 16,
+// one row 6.0 us against 7.4; K = 4096, N = 11008, rank 16, one row 9.1 against 7.9; K =
+// 1536, N = 8960, rank 32, 256 rows of 32 adapters 30.5 against 19.2.
 constexpr int kFusedA = 48 << 10;   // values
 
-bool forward_fused(int M, int K, int R) { return M <= kInlineRows && R <= 64 && R * K <= kFusedA; }
+bool forward_fused(int M, int N, int K, int R, int L, bool with_index) {
+  return M <= kInlineRows && R <= 64 && R * K <= kFusedA &&
+         tile_slots(M, L, with_index, false, kFewRows) * ceil_div(N, 1024) <= 256;
+}
 
 void run_fused(const half_t* x, const half_t* a, const half_t* b, const float* scaling, const RowPlan& plan,
                const half_t* base, half_t* out, float* h_out, int K, int N, int R, hipStream_t st) {
@@ -301,28 +306,33 @@ void run_products(const OuterArgs& b, const OuterArgs& a, const StreamArgs& dx, 
 
 struct ForwardMemory {
   RowPlan plan;
-  float* part;       // [S][M][R]
+  float* part;       // [S][M][R], or [slots][S][16][R] for few rows
   int S, slots;
   bool fused, stream;
   ByRow h;
   SlotTable table;
 };
 
-ForwardMemory forward_memory(Carver& ws, const int32_t* index, bool with_index, int M, int K, int R, int L) {
+ForwardMemory forward_memory(Carver& ws, const int32_t* index, bool with_index, int M, int N, int K, int R,
+                             int L) {
   ForwardMemory m{};
-  m.fused = forward_fused(M, K, R);
+  m.fused = forward_fused(M, N, K, R, L, with_index);
   if (m.fused) {
     m.plan = RowPlan{index, nullptr, nullptr, M, L};
     return m;
   }
   m.stream = M > kInlineRows;
-  m.plan = take_plan(ws, index, with_index && M > kInlineRows, M, L);
-  m.S = shrink_slices(M, L, R, K, false);
-  m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
+  m.plan = take_plan(ws, index, with_index && m.stream, M, L);
+  m.S = shrink_slices(M, L, R, K, false, m.stream);
   if (m.stream) {
     m.slots = plan_slots(M, L, with_index);
+    m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
     m.h = take_by_row(ws, m.slots, R);
-    m.table = take_table(ws, m.slots);
+    m.table = take_table(ws, m.slots, kSlotRows);
+  } else {
+    m.slots = tile_slots(M, L, with_index, false, kFewRows);
+    m.part = ws.take<float>(static_cast<size_t>(m.slots) * m.S * kFewRows * R);
+    m.table = take_table(ws, m.slots, kFewRows);
   }
   return m;
 }
@@ -344,13 +354,13 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
                                int L) {
   BackwardMemory m{};
   m.plan = take_plan(ws, index, with_index, M, L);
-  m.S = shrink_slices(M, L, R, N, true);
+  m.S = shrink_slices(M, L, R, N, true, true);
   m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
   m.slots = plan_slots(M, L, with_index);
   m.h = take_by_rank(ws, m.slots, R);
   m.g = take_by_rank(ws, m.slots, R);
   m.g_rows = take_by_row(ws, m.slots, R);
-  m.table = take_table(ws, m.slots);
+  m.table = take_table(ws, m.slots, kSlotRows);
   const int64_t ga = outer_groups(M, K, R, L), gb = outer_groups(M, N, R, L);
   // One launch with dx: counted together.  Otherwise the workgroups of both do not fit on the
   // GPU at once, and what comes second should be in smaller pieces than the first.
@@ -400,7 +410,7 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const auto st = static_cast<hipStream_t>(c.stream);
   const auto* dy = reinterpret_cast<const half_t*>(c.dy);
   run_plan(m.plan, st);
-  run_shrink<true>(dy, reinterpret_cast<const half_t*>(c.b), m.plan, c.N, c.R, m.S, m.part, st);
+  run_shrink<true>(dy, reinterpret_cast<const half_t*>(c.b), m.plan, c.N, c.R, m.S, m.part, SlotTable{}, st);
   const SplitTask th{c.h, 1, m.h.frags, m.h.exps, nullptr, nullptr, nullptr};
   const SplitTask tg{m.part, m.S, m.g.frags, m.g.exps, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors, nullptr};
   hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 2), dim3(512), 0, st, th, tg, c.scaling, m.table, m.plan, c.R);
@@ -438,7 +448,7 @@ using namespace w4a16;
 extern "C" size_t w4a16_lora_forward_workspace(int M, int N, int K, int R, int L, int with_index) {
   if (check_lora_shape(M, N, K, R, L) != W4A16_OK) return 0;
   Carver size{nullptr};
-  forward_memory(size, nullptr, with_index != 0, M, K, R, L);
+  forward_memory(size, nullptr, with_index != 0, M, N, K, R, L);
   return size.used;
 }
 
@@ -453,9 +463,9 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
                          {workspace, 16, false, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   Carver size{nullptr}, ws{static_cast<unsigned char*>(workspace)};
-  forward_memory(size, nullptr, index != nullptr, M, K, R, L);
+  forward_memory(size, nullptr, index != nullptr, M, N, K, R, L);
   if (int rc = check_workspace(workspace, workspace_bytes, size.used)) return rc;
-  const ForwardMemory m = forward_memory(ws, index, index != nullptr, M, K, R, L);
+  const ForwardMemory m = forward_memory(ws, index, index != nullptr, M, N, K, R, L);
   const auto st = static_cast<hipStream_t>(stream);
   const auto* yh = reinterpret_cast<const half_t*>(y);
   const auto* bh = reinterpret_cast<const half_t*>(b);
@@ -467,13 +477,13 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
     return check_launch("lora forward launch");
   }
   run_plan(m.plan, st);
-  run_shrink<false>(xh, ah, m.plan, K, R, m.S, m.part, st);
+  run_shrink<false>(xh, ah, m.plan, K, R, m.S, m.part, m.stream ? SlotTable{} : m.table, st);
   if (m.stream) {
     const SplitTask t{m.part, m.S, nullptr, nullptr, m.h.frags, m.h.factors, h};
     hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(512), 0, st, t, t, scaling, m.table, m.plan, R);
     run_stream<false, true>(stream_args(m.h, m.table, bh, yh, oh, N, R, L, m.slots), st);
   } else {
-    run_expand(m.part, m.S, bh, scaling, m.plan, yh, oh, h, N, R, st);
+    run_expand(m.part, m.S, m.table, m.slots, bh, scaling, L, yh, oh, h, N, R, st);
   }
   return check_launch("lora forward launch");
 }

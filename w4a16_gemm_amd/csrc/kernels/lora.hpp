@@ -101,6 +101,15 @@ __host__ __device__ inline int tile_slots(int M, int L, bool with_index, bool in
   return !in_memory && M < most ? M : most;
 }
 
+// Tiles found by one kernel for the next.
+struct SlotTable {
+  int2* meta;        // [slots] adapter (L: none), count (0: empty slot)
+  int32_t* rows;     // [slots][rows per tile], entries past the count repeat a valid row
+};
+
+constexpr int kSlotRows = 32;    // of the split and stream kernels
+constexpr int kFewRows = 16;     // of the kernels for few rows
+
 struct Tile {
   int adapter;   // L: rows without an adapter
   int count;     // rows in the tile, 0: empty slot
@@ -203,6 +212,7 @@ __device__ __forceinline__ void split_half(float h, int shift, half_t& hi, half_
   lo = static_cast<half_t>(__builtin_fabsf(v) <= 65504.0f ? r : 0.0f);
 }
 
+constexpr int kMaxRank = 128;
 constexpr int kSplitTop = 14;   // split operands are below 2^14
 constexpr int kNoExponent = -1000;   // of values that are all zero
 
@@ -289,17 +299,25 @@ __device__ __forceinline__ void add_wavefronts(float4_t* red, int wave, int lane
   }
 }
 
-// Few rows: a tile of 16 rows and a slice per workgroup of 4 wavefronts.
+// Few rows: a tile of 16 rows and a slice per workgroup of 4 wavefronts.  table.meta != NULL:
+// the next kernel works on the same tiles, so the tiles are written down and the sums go out
+// by tile, [slots][S][16][R], where that kernel can read them without looking up rows.
 template <int NT, int D>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restrict__ x, const half_t* __restrict__ w,
-                                                          RowPlan plan, int C, int R, int S, float* __restrict__ out) {
+                                                          RowPlan plan, int C, int R, int S, float* __restrict__ out,
+                                                          SlotTable table) {
   constexpr int W = 4;
-  __shared__ int32_t rows[16];
+  __shared__ int32_t rows[kFewRows];
   __shared__ float4_t red[W / 2 * NT * 64];
-  const int s = blockIdx.x % S;
-  const Tile tile = find_tile<16>(plan, blockIdx.x / S, rows);
-  if (tile.count == 0) return;
+  const int s = blockIdx.x % S, slot = blockIdx.x / S;
+  const bool by_slot = table.meta != nullptr;
+  const Tile tile = find_tile<kFewRows>(plan, slot, rows);
   const int tid = threadIdx.x, lane = tid & 63;
+  if (by_slot && s == 0) {
+    if (tid == 0) table.meta[slot] = int2{tile.adapter, tile.count};
+    if (tid < kFewRows && tile.count > 0) table.rows[slot * kFewRows + tid] = rows[tid];
+  }
+  if (tile.count == 0 || (by_slot && tile.adapter == plan.L)) return;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   float* o = out + static_cast<size_t>(s) * plan.M * R;
@@ -320,7 +338,8 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = 4 * lq + r, j = 16 * t + lr;
-      if (i < tile.count && j < R) o[static_cast<size_t>(rows[i]) * R + j] = acc[t][r];
+      float* to = by_slot ? out + (static_cast<size_t>(blockIdx.x) * kFewRows + i) * R : o + static_cast<size_t>(rows[i]) * R;
+      if (i < tile.count && j < R) to[j] = acc[t][r];
     }
 }
 
@@ -485,29 +504,47 @@ __device__ __forceinline__ half8_t column8(const uint4 (&v)[8], int t) {
   return __builtin_bit_cast(half8_t, (u32x4_t{d[0], d[1], d[2], d[3]}));
 }
 
-// Sum over the S slices of 8 consecutive floats, 4 slices in flight at a time.
-__device__ __forceinline__ void sum_slices8(const float* __restrict__ p, size_t slice, int S, float (&v)[8]) {
-  float4_t a = {}, b = {};
-  for (int s0 = 0; s0 < S; s0 += 4) {
-    float4_t x[4], y[4];
+// Sum of S slices of ROWS x R floats into LDS: sums[m (R / 4 + 1) + j] holds ranks 4 j .. of
+// row m, zero from row `count` on.  at(m): offset of row m in a slice.  Where R leaves threads
+// over, groups of them take every G-th slice each, and their sums are added in order.  Every
+// thread calls it; `sums` has room for sum_quads(ROWS, THREADS) entries.
+constexpr int sum_quads(int rows, int threads) {
+  // rows (kMaxRank / 4 + 1) for one group; G rows (R / 4 + 1) with G = threads / (rows R / 4)
+  const int one = rows * (kMaxRank / 4 + 1), most = threads + threads / 2;   // R >= 8: (R / 4 + 1) / (R / 4) <= 3 / 2
+  return one > most ? one : most;
+}
+
+template <int ROWS, int THREADS, typename At>
+__device__ __forceinline__ void sum_slices(const float* __restrict__ h, size_t slice, int S, int R, int count,
+                                           float4_t* sums, At at) {
+  const int tid = threadIdx.x;
+  const int quads = R >> 2, ld = quads + 1, items = ROWS * quads;
+  const int G = min(max(1, THREADS / items), S);
+  for (int i = tid; i < items * G; i += THREADS) {
+    const int g = i / items, m = i % items / quads, j = i % quads;
+    float4_t v = {};
+    if (m < count) {
+      const float* p = h + at(m) + 4 * j;
+      for (int s0 = g; s0 < S; s0 += 4 * G) {
+        float4_t q[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float* q = p + min(s0 + k, S - 1) * slice;
-      x[k] = *reinterpret_cast<const float4_t*>(q);
-      y[k] = *reinterpret_cast<const float4_t*>(q + 4);
-    }
+        for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const float4_t*>(p + min(s0 + k * G, S - 1) * slice);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (s0 + k < S) {
-        a += x[k];
-        b += y[k];
+        for (int k = 0; k < 4; ++k)
+          if (s0 + k * G < S) v += q[k];
       }
+    }
+    sums[(g * ROWS + m) * ld + j] = v;
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[j] = a[j];
-    v[4 + j] = b[j];
+  __syncthreads();
+  if (G == 1) return;
+  for (int i = tid; i < items; i += THREADS) {
+    const int at0 = i / quads * ld + i % quads;
+    float4_t v = sums[at0];
+    for (int g = 1; g < G; ++g) v += sums[g * ROWS * ld + at0];
+    sums[at0] = v;
   }
+  __syncthreads();
 }
 
 // Weights of the 128 channels from c0 (channels past C repeat valid ones), in the order of
@@ -616,14 +653,6 @@ struct SplitTask {
   float* sum;        // [M][R] or NULL
 };
 
-constexpr int kSlotRows = 32;
-constexpr int kMaxRank = 128;
-
-struct SlotTable {
-  int2* meta;        // [slots] adapter (L: none), count (0: empty slot)
-  int32_t* rows;     // [slots][32], entries past the count repeat the first
-};
-
 // By-row operands (of 1 KB) of a row group.
 __host__ __device__ constexpr int row_frags(int R) { return R <= 16 ? 1 : 2 * ((R + 31) / 32); }
 
@@ -632,7 +661,7 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
   __shared__ int32_t rows[kSlotRows];
   __shared__ float tops[8];
   __shared__ float row_top[kSlotRows];
-  __shared__ float4_t sums[kSlotRows * (kMaxRank / 4 + 1)];   // rows of R / 4 + 1
+  __shared__ float4_t sums[sum_quads(kSlotRows, 512)];
   const SplitTask task = blockIdx.y == 0 ? t0 : t1;
   const int slot = blockIdx.x;
   const Tile tile = find_tile<kSlotRows>(plan, slot, rows);
@@ -650,33 +679,24 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
     return;
   }
   const int quads = R >> 2, ld = quads + 1;
-  float top = 0.0f;
-  for (int i = tid; i < kSlotRows * quads; i += 512) {
-    const int m = i / quads, j = i % quads;
-    float4_t v = {};
-    if (m < tile.count) {
-      const size_t at = static_cast<size_t>(rows[m]) * R + 4 * j;
-      for (int s0 = 0; s0 < task.S; s0 += 8) {
-        float4_t p[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          p[k] = *reinterpret_cast<const float4_t*>(task.h + min(s0 + k, task.S - 1) * slice + at);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (s0 + k < task.S) v += p[k];
-      }
-      if (task.sum) *reinterpret_cast<float4_t*>(task.sum + at) = v;
-    }
-    sums[m * ld + j] = v;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) top = fmaxf(top, finite_magnitude(v[k]));
-  }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-  if (lane == 0) tops[wave] = top;
-  __syncthreads();
+  sum_slices<kSlotRows, 512>(task.h, slice, task.S, R, tile.count, sums,
+                             [&](int m) { return static_cast<size_t>(rows[m]) * R; });
+  if (task.sum)
+    for (int i = tid; i < tile.count * quads; i += 512)
+      *reinterpret_cast<float4_t*>(task.sum + static_cast<size_t>(rows[i / quads]) * R + 4 * (i % quads)) =
+          sums[i / quads * ld + i % quads];
   const float* f = reinterpret_cast<const float*>(sums);
   if (task.by_rank) {
+    float top = 0.0f;
+    for (int i = tid; i < kSlotRows * quads; i += 512) {
+      const float4_t v = sums[i / quads * ld + i % quads];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = fmaxf(top, finite_magnitude(v[k]));
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if (lane == 0) tops[wave] = top;
+    __syncthreads();
 #pragma unroll
     for (int w = 0; w < 8; ++w) top = fmaxf(top, tops[w]);
     const int e = top > 0.0f ? top_exponent(top) - kSplitTop : kNoExponent;
@@ -739,43 +759,43 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
 
 // --- expand, few rows: sums and splits h itself -------------------------------------------
 //
-// h = sum of S slices [S][M][R].  A workgroup of 4 wavefronts takes one tile of 16 rows x
-// 512 channels; its first wavefront splits h into LDS while the weights and base are on
-// their way.  Latency-bound: what counts is one launch less.
+// h by tile, [slots][S][16][R], and the tiles as the shrink wrote them.  A workgroup of 4
+// wavefronts takes one tile of 16 rows x 512 channels; h is summed into LDS by all of it
+// while the weights and base are on their way, and every wavefront splits it for itself.
+// Latency-bound: what counts is one launch less, and few loads that wait for another.
 // base may equal out (every element is read and written by the same lane); rows without
 // an adapter are copied, bit for bit.  h_out (not NULL): the workgroups of the first
 // channels write the summed h.
 template <int F, bool PACKED>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restrict__ h, int S,
+__global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restrict__ h, int S, SlotTable table,
                                                           const half_t* __restrict__ w,
-                                                          const float* __restrict__ scaling, RowPlan plan,
-                                                          const half_t* base, half_t* out, float* __restrict__ h_out,
-                                                          int C, int R) {
+                                                          const float* __restrict__ scaling, int L, const half_t* base,
+                                                          half_t* out, float* __restrict__ h_out, int C, int R) {
   constexpr int kBlock = 512;   // channels per workgroup: 4 wavefronts x 128
   constexpr int P = PACKED ? 1 : 2;
-  __shared__ int32_t rows[16];
-  __shared__ float factor[16];
-  __shared__ half8_t split[F][P][64];
-  const Tile tile = find_tile<16>(plan, blockIdx.x, rows);
-  if (tile.count == 0) return;
+  __shared__ float4_t sums[sum_quads(kFewRows, 256)];
+  const int slot = blockIdx.x;
+  const int2 meta = table.meta[slot];
+  const int adapter = __builtin_amdgcn_readfirstlane(meta.x), count = __builtin_amdgcn_readfirstlane(meta.y);
+  if (count == 0) return;
+  const int32_t* rows = table.rows + slot * kFewRows;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
   const int c_lo = blockIdx.y * kBlock;
-  if (tile.adapter == plan.L) {
+  if (adapter == L) {
     if (base != out) {
       const int chunks = min(kBlock, C - c_lo) / 8;
-      for (int i = tid; i < tile.count * chunks; i += 256) {
+      for (int i = tid; i < count * chunks; i += 256) {
         const size_t at = static_cast<size_t>(rows[i / chunks]) * C + c_lo + 8 * (i % chunks);
         *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(base + at);
       }
     }
     if (h_out && blockIdx.y == 0)
-      for (int i = tid; i < tile.count * R; i += 256) h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
+      for (int i = tid; i < count * R; i += 256) h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = 0.0f;
     return;
   }
   const int c0 = c_lo + wave * 128;
-  const bool mine = lr < tile.count;
   const size_t at = static_cast<size_t>(rows[lr]);
   uint4 y[4];
   half8_t wf[F][8];
@@ -783,44 +803,33 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
 #pragma unroll
     for (int u = 0; u < 4; ++u)
       y[u] = *reinterpret_cast<const uint4*>(base + at * C + min(c0 + 32 * u + 8 * lq, C - 8));
-    load_expand_weights<F, PACKED, false, false>(w + static_cast<size_t>(tile.adapter) * R * C, c0, C, R, lane, wf);
+    load_expand_weights<F, PACKED, false, false>(w + static_cast<size_t>(adapter) * R * C, c0, C, R, lane, wf);
   }
-  if (wave == 0) {   // lane (r, q): ranks 8 q .. of row r
-    float v[F][8];
-#pragma unroll
-    for (int f = 0; f < F; ++f) {
-      const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
-      const bool in = j0 < R;
-      sum_slices8(h + at * R + (in ? j0 : 0), static_cast<size_t>(plan.M) * R, S, v[f]);
-      if (h_out && blockIdx.y == 0 && in && mine && (!PACKED || lq < 2)) {
-        *reinterpret_cast<float4_t*>(h_out + at * R + j0) = float4_t{v[f][0], v[f][1], v[f][2], v[f][3]};
-        *reinterpret_cast<float4_t*>(h_out + at * R + j0 + 4) = float4_t{v[f][4], v[f][5], v[f][6], v[f][7]};
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[f][j] = in ? v[f][j] : 0.0f;
-    }
-    half8_t hf[F][P];
-    const float fr = split_row<F, PACKED>(v, lq, scaling ? scaling[tile.adapter] : 1.0f, hf);
-    if (lq == 0) factor[lr] = fr;
-#pragma unroll
-    for (int f = 0; f < F; ++f)
-#pragma unroll
-      for (int p = 0; p < P; ++p) split[f][p][lane] = hf[f][p];
-  }
-  __syncthreads();
+  const int quads = R >> 2, ld = quads + 1;
+  sum_slices<kFewRows, 256>(h + static_cast<size_t>(slot) * S * kFewRows * R, static_cast<size_t>(kFewRows) * R, S, R, count,
+                            sums, [&](int m) { return static_cast<size_t>(m) * R; });
+  if (h_out && blockIdx.y == 0)
+    for (int i = tid; i < count * quads; i += 256)
+      *reinterpret_cast<float4_t*>(h_out + static_cast<size_t>(rows[i / quads]) * R + 4 * (i % quads)) =
+          sums[i / quads * ld + i % quads];
   if (c0 >= C) return;
+  const float* hs = reinterpret_cast<const float*>(sums);
+  float v[F][8];
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[f][j] = j0 < R ? hs[lr * 4 * ld + j0 + j] : 0.0f;
+  }
   half8_t hf[F][P];
-#pragma unroll
-  for (int f = 0; f < F; ++f)
-#pragma unroll
-    for (int p = 0; p < P; ++p) hf[f][p] = split[f][p][lane];
+  const float factor = split_row<F, PACKED>(v, lq, scaling ? scaling[adapter] : 1.0f, hf);
   float4_t acc[8];
   expand_products<F, P, false>(wf, hf, acc);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int c = c0 + 32 * u + 8 * lq;
-    const half8_t o = expand_result<false>(acc, u, y[u], factor[lr]);
-    if (c < C && mine) *reinterpret_cast<half8_t*>(out + at * C + c) = o;
+    const half8_t o = expand_result<false>(acc, u, y[u], factor);
+    if (c < C && lr < count) *reinterpret_cast<half8_t*>(out + at * C + c) = o;
   }
 }
 
@@ -838,11 +847,11 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
                                                          int K, int N, int R) {
   constexpr int W = 8, NT = PACKED ? 1 : 2 * F, P = PACKED ? 1 : 2;
   constexpr int ld = 16 * NT + 4;   // floats per row of h
-  __shared__ int32_t rows[16];
+  __shared__ int32_t rows[kFewRows];
   __shared__ float4_t red[W / 2 * NT * 64];
   __shared__ __align__(16) float hs[16 * ld];
   const int blocks = (N + 128 * W - 1) / (128 * W);
-  const Tile tile = find_tile<16>(plan, blockIdx.x / blocks, rows);
+  const Tile tile = find_tile<kFewRows>(plan, blockIdx.x / blocks, rows);
   if (tile.count == 0) return;
   const int block = blockIdx.x % blocks;
   const int tid = threadIdx.x, lane = tid & 63;
