@@ -275,7 +275,8 @@ bool products_merged(int M, int R) { return R <= 32 || (M <= 1024 && R <= 64); }
 int outer_nt(int M, int R) { return R <= 16 ? 1 : R <= 32 || M <= 1024 ? 2 : 4; }
 
 int64_t outer_groups(int M, int C, int R, int L) {
-  return static_cast<int64_t>(ceil_div(C, 1024)) * 8 * ceil_div(R, 16 * outer_nt(M, R)) * L;
+  const int ranks = ceil_div(R, 16 * outer_nt(M, R));   // more than one: whole eights of blocks
+  return static_cast<int64_t>(ranks == 1 ? ceil_div(C, 128) : ceil_div(C, 1024) * 8 * ranks) * L;
 }
 
 int64_t outer_blocks(const OuterArgs& o) { return outer_groups(o.plan.M, o.C, o.R, o.plan.L) * o.parts; }

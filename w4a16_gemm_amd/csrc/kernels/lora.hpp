@@ -1104,15 +1104,24 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lq = lane >> 4;
-  // Neighbouring workgroups go to different XCDs (8, in turn): eight blocks of channels, then
-  // their further blocks of ranks, which thus find x in the same L2; then the next eight.
-  const int ranks = (R + 16 * NT - 1) / (16 * NT), eights = (C + 1023) >> 10;
-  int col = block & 7;
-  block >>= 3;
-  const int t0 = (block % ranks) * NT;
-  block /= ranks;
-  col += 8 * (block % eights);
-  block /= eights;
+  // Neighbouring workgroups go to different XCDs (8, in turn).  Where there are several blocks
+  // of ranks, eight blocks of channels are followed by their further blocks of ranks, which
+  // thus find x in the same L2.
+  const int ranks = (R + 16 * NT - 1) / (16 * NT);
+  int col, t0 = 0;
+  if (ranks == 1) {
+    const int cols = (C + 127) >> 7;
+    col = block % cols;
+    block /= cols;
+  } else {
+    const int eights = (C + 1023) >> 10;
+    col = block & 7;
+    block >>= 3;
+    t0 = (block % ranks) * NT;
+    block /= ranks;
+    col += 8 * (block % eights);
+    block /= eights;
+  }
   const int part = block % parts;
   const int ad = block / parts;
   const int c0 = col * 128;
