@@ -1129,7 +1129,7 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
   const int NTT = (R + 15) >> 4;   // fragments per slot
   // slots of the adapter: [first_slot, first_slot + n); positions lo .. hi - 1
   const int lo = plan.index ? plan.off[ad] : 0;
-  const int hi = plan.index ? plan.off[ad + 1] : plan.M;
+  const int hi = plan.index ? plan.off[ad + 1] : ad == 0 ? plan.M : 0;   // no index: all rows are adapter 0's
   const int first_slot = plan.index ? lo / kSlotRows + ad : 0;
   const int n = (hi - lo + kSlotRows - 1) / kSlotRows;
   const int cc = min(c0 + 8 * lr, C - 8);
