@@ -234,15 +234,15 @@ void run_stream(const StreamArgs& s, hipStream_t st) {
   const dim3 grid(stream_blocks(s)), block(256);
 #define W4A16_STREAM(F_, P_, D_) \
   hipLaunchKernelGGL((lora_stream_kernel<F_, P_, TRANS, BASE, D_>), grid, block, 0, st, s)
-  if constexpr (!TRANS) {   // ranks up to 32 of the backward pass are in the products kernel
-    if (s.R <= 32) {
+  if constexpr (!TRANS) {   // ranks up to 64 of the backward pass are in the products kernel
+    if (s.R <= 64) {
       if (s.R <= 16) W4A16_STREAM(1, true, 2);
-      else W4A16_STREAM(1, false, 2);
+      else if (s.R <= 32) W4A16_STREAM(1, false, 2);
+      else W4A16_STREAM(2, false, 2);
       return;
     }
   }
-  if (s.R <= 64) W4A16_STREAM(2, false, 2);
-  else if (s.R <= 96) W4A16_STREAM(3, false, 2);
+  if (s.R <= 96) W4A16_STREAM(3, false, 2);
   else W4A16_STREAM(4, false, 2);
 #undef W4A16_STREAM
 }
@@ -263,40 +263,37 @@ int outer_parts(int M, int L, int64_t groups) {
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({256 / groups, M / L / (32 * kSlotRows), 16})));
 }
 
-// The products of the backward pass go out in one launch for ranks up to 32, and up to 64
-// for up to 1024 rows, where each alone leaves most of the GPU idle.  Beyond that dx has a
-// launch of its own: the registers of its weights, or of the outer products in blocks of 64
-// ranks, would hold the other part back.
-bool products_merged(int M, int R) { return R <= 32 || (M <= 1024 && R <= 64); }
+// Ranks per block of an outer product, in 16s.  Blocks of 32 ranks read x or dy again, from
+// the L2 of their XCD, for every further block; blocks of 64 leave registers for one wavefront
+// per SIMD, and were slower for every size (4096 rows, K = 8192, N = 28672, rank 64, with dx:
+// 103 us in one launch in blocks of 32, 117 us in blocks of 64 and two launches).
+int outer_nt(int R) { return R <= 16 ? 1 : 2; }
 
-// 16s of ranks per block of an outer product.  Blocks of 32 ranks read x or dy again (from
-// the cache) for every further block; with few rows that costs less than one wavefront per
-// SIMD, which is what blocks of 64 ranks leave room for.
-int outer_nt(int M, int R) { return R <= 16 ? 1 : R <= 32 || M <= 1024 ? 2 : 4; }
-
-int64_t outer_groups(int M, int C, int R, int L) {
-  const int ranks = ceil_div(R, 16 * outer_nt(M, R));   // more than one: whole eights of blocks
+int64_t outer_groups(int C, int R, int L) {
+  const int ranks = ceil_div(R, 16 * outer_nt(R));   // more than one: whole eights of blocks of channels
   return static_cast<int64_t>(ranks == 1 ? ceil_div(C, 128) : ceil_div(C, 1024) * 8 * ranks) * L;
 }
 
-int64_t outer_blocks(const OuterArgs& o) { return outer_groups(o.plan.M, o.C, o.R, o.plan.L) * o.parts; }
+// dB, dA and dx go out in one launch up to rank 64.  Above, the registers for the weights of dx
+// would hold the outer products back (300 rows, rank 128: 27 us in one launch, 24 us in two).
+bool products_together(int R) { return R <= 64; }
 
 OuterArgs outer_args(const Kept& k, const ByRank& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
                      int parts) {
   return {k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts};
 }
 
+int outer_blocks(const OuterArgs& o) { return static_cast<int>(outer_groups(o.C, o.R, o.plan.L) * o.parts); }
+
 template <bool Q8>
 void run_outers(const OuterArgs& b, const OuterArgs& a, hipStream_t st) {
-  const int nb = static_cast<int>(outer_blocks(b)), na = static_cast<int>(outer_blocks(a));
-  const dim3 grid(nb + na), block(256);
-  if (outer_nt(b.plan.M, b.R) == 2) hipLaunchKernelGGL((lora_outers_kernel<2, Q8>), grid, block, 0, st, b, nb, a);
-  else hipLaunchKernelGGL((lora_outers_kernel<4, Q8>), grid, block, 0, st, b, nb, a);
+  const int nb = outer_blocks(b), na = outer_blocks(a);
+  hipLaunchKernelGGL((lora_outers_kernel<Q8>), dim3(nb + na), dim3(256), 0, st, b, nb, a);
 }
 
 template <int NT, int F, bool Q8>
 void run_products(const OuterArgs& b, const OuterArgs& a, const StreamArgs& dx, hipStream_t st) {
-  const int nb = static_cast<int>(outer_blocks(b)), na = static_cast<int>(outer_blocks(a));
+  const int nb = outer_blocks(b), na = outer_blocks(a);
   const dim3 grid(nb + na + (dx.out ? stream_blocks(dx) : 0)), block(256);
   if (!dx.out) hipLaunchKernelGGL((lora_products_kernel<NT, F, Q8, false, false>), grid, block, 0, st, b, nb, a, na, dx);
   else if (!dx.base) hipLaunchKernelGGL((lora_products_kernel<NT, F, Q8, true, false>), grid, block, 0, st, b, nb, a, na, dx);
@@ -362,12 +359,7 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
   m.g = take_by_rank(ws, m.slots, R);
   m.g_rows = take_by_row(ws, m.slots, R);
   m.table = take_table(ws, m.slots, kSlotRows);
-  const int64_t ga = outer_groups(M, K, R, L), gb = outer_groups(M, N, R, L);
-  // One launch with dx: counted together.  Otherwise the workgroups of both do not fit on the
-  // GPU at once, and what comes second should be in smaller pieces than the first.
-  const bool merged = products_merged(M, R);
-  m.a_parts = outer_parts(M, L, merged ? ga + gb : ga);
-  m.b_parts = outer_parts(M, L, merged ? ga + gb : gb);
+  m.a_parts = m.b_parts = outer_parts(M, L, outer_groups(K, R, L) + outer_groups(N, R, L));
   if (m.a_parts > 1) m.da = ws.take<float>(static_cast<size_t>(m.a_parts) * L * R * K);
   if (m.b_parts > 1) m.db = ws.take<float>(static_cast<size_t>(m.b_parts) * L * N * R);
   return m;
@@ -402,7 +394,7 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   if (int rc = check_buffers(bufs)) return rc;
   if (c.dx0 && !c.dx) return fail(W4A16_ERR_INVALID_ARG, "dx0 is given without dx");
   // the only grid that the bounds on the sizes do not keep below 2^32 threads
-  if (outer_groups(c.M, c.N, c.R, c.L) + outer_groups(c.M, c.K, c.R, c.L) >= int64_t{1} << 23)
+  if (outer_groups(c.N, c.R, c.L) + outer_groups(c.K, c.R, c.L) >= int64_t{1} << 23)
     return fail(W4A16_ERR_UNSUPPORTED, "gradients of %d adapters for N=%d, K=%d are too large for one call", c.L, c.N, c.K);
   Carver size{nullptr}, ws{static_cast<unsigned char*>(c.workspace)};
   backward_memory(size, nullptr, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
@@ -421,7 +413,7 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const StreamArgs dx = stream_args(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a),
                                     reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L,
                                     m.slots);
-  if (products_merged(c.M, c.R)) {
+  if (products_together(c.R)) {
     if (c.R <= 16) run_products<1, 1, Q8>(ob, oa, dx, st);
     else if (c.R <= 32) run_products<2, 1, Q8>(ob, oa, dx, st);
     else run_products<2, 2, Q8>(ob, oa, dx, st);

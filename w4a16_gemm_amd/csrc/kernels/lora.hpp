@@ -1230,38 +1230,27 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
       load(slot_of(d), ring[d]);
       find_rows(slot_of(d + 1));
     }
+    // The main loop reloads a stage as soon as it is used; the tail loads only what is left.
     int k = 0;
-    if constexpr (NT <= 2) {   // the tail loads only what is left
-      for (; k + 2 * D <= mine; k += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-          add(ring[d]);
-          load(slot_of(k + d + D), ring[d]);
-          find_rows(slot_of(k + d + D + 1));
-        }
-      }
+    for (; k + 2 * D <= mine; k += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        if (k + d < mine) add(ring[d]);
-        if (k + d + D < mine) {
-          load(slot_of(k + d + D), ring[d]);
-          find_rows(slot_of(k + d + D + 1));
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < D; ++d)
-        if (k + d + D < mine) add(ring[d]);
-    } else {   // many slots per wavefront: D loads of the last slot in vain, but one copy of the code
-      for (; k < mine; k += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-          if (k + d >= mine) break;
-          add(ring[d]);
-          load(slot_of(k + d + D), ring[d]);
-          find_rows(slot_of(k + d + D + 1));
-        }
+        add(ring[d]);
+        load(slot_of(k + d + D), ring[d]);
+        find_rows(slot_of(k + d + D + 1));
       }
     }
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (k + d < mine) add(ring[d]);
+      if (k + d + D < mine) {
+        load(slot_of(k + d + D), ring[d]);
+        find_rows(slot_of(k + d + D + 1));
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < D; ++d)
+      if (k + d + D < mine) add(ring[d]);
   }
 
   // Sum over the wavefronts, one channel fragment at a time, in units of 1; the sums are
@@ -1311,12 +1300,12 @@ constexpr int outer_lds(int NT, int W) {
 }
 
 // dB and dA in one launch: the workgroups of the second fill what the first leaves idle.
-template <int NT, bool Q8>
-__global__ __launch_bounds__(256, NT <= 2 ? 2 : 1) void lora_outers_kernel(OuterArgs b, int b_blocks, OuterArgs a) {
-  __shared__ float4_t red[outer_lds(NT, 4)];
+template <bool Q8>
+__global__ __launch_bounds__(256, 2) void lora_outers_kernel(OuterArgs b, int b_blocks, OuterArgs a) {
+  __shared__ float4_t red[outer_lds(2, 4)];
   const int block = blockIdx.x;
-  if (block < b_blocks) outer_sums<NT, 4, 2, false, true>(b, block, red);
-  else outer_sums<NT, 4, 2, Q8, false>(a, block - b_blocks, red);
+  if (block < b_blocks) outer_sums<2, 4, 2, false, true>(b, block, red);
+  else outer_sums<2, 4, 2, Q8, false>(a, block - b_blocks, red);
 }
 
 // The three products of the backward pass in one launch: their workgroups fill the GPU
