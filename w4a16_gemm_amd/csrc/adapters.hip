@@ -269,9 +269,19 @@ int outer_parts(int M, int L, int64_t groups) {
 // 103 us in one launch in blocks of 32, 117 us in blocks of 64 and two launches).
 int outer_nt(int R) { return R <= 16 ? 1 : 2; }
 
-int64_t outer_groups(int C, int R, int L) {
+int64_t outer_groups(int C, int R, int L, int row_waves) {
   const int ranks = ceil_div(R, 16 * outer_nt(R));   // more than one: whole eights of blocks of channels
-  return static_cast<int64_t>(ranks == 1 ? ceil_div(C, 128) : ceil_div(C, 1024) * 8 * ranks) * L;
+  const int width = 512 / row_waves;
+  return static_cast<int64_t>(ranks == 1 ? ceil_div(C, width) : ceil_div(C, 8 * width) * 8 * ranks) * L;
+}
+
+// Wavefronts of a workgroup (of 4) that share the rows of 128 channels.  With few rows per
+// adapter and more workgroups than fit at once, each wavefront takes channels of its own and
+// all the rows: a quarter of the workgroups, and no sums to add (700 rows of 12 adapters, K =
+// N = 4096, rank 40: 27 -> 15 us; 1024 rows of 16, rank 16: 19 -> 13 us; but 1111 rows of 6, K =
+// 1536, N = 8960, rank 32: 14 -> 19 us).
+int outer_row_waves(int M, int N, int K, int R, int L) {
+  return M / L <= 128 && outer_groups(K, R, L, 4) + outer_groups(N, R, L, 4) >= 768 ? 1 : 4;
 }
 
 // dB, dA and dx go out in one launch up to rank 64.  Above, the registers for the weights of dx
@@ -279,11 +289,11 @@ int64_t outer_groups(int C, int R, int L) {
 bool products_together(int R) { return R <= 64; }
 
 OuterArgs outer_args(const Kept& k, const ByRank& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
-                     int parts) {
-  return {k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts};
+                     int parts, int row_waves) {
+  return {k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts, row_waves};
 }
 
-int outer_blocks(const OuterArgs& o) { return static_cast<int>(outer_groups(o.C, o.R, o.plan.L) * o.parts); }
+int outer_blocks(const OuterArgs& o) { return static_cast<int>(outer_groups(o.C, o.R, o.plan.L, o.row_waves) * o.parts); }
 
 template <bool Q8>
 void run_outers(const OuterArgs& b, const OuterArgs& a, hipStream_t st) {
@@ -344,7 +354,7 @@ struct BackwardMemory {
   ByRank h, g;
   ByRow g_rows;
   SlotTable table;
-  int a_parts, b_parts;
+  int parts, row_waves;   // of the outer products
   float *da, *db;    // [parts][L][R][K], [parts][L][N][R], where there is more than one part
 };
 
@@ -359,9 +369,12 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
   m.g = take_by_rank(ws, m.slots, R);
   m.g_rows = take_by_row(ws, m.slots, R);
   m.table = take_table(ws, m.slots, kSlotRows);
-  m.a_parts = m.b_parts = outer_parts(M, L, outer_groups(K, R, L) + outer_groups(N, R, L));
-  if (m.a_parts > 1) m.da = ws.take<float>(static_cast<size_t>(m.a_parts) * L * R * K);
-  if (m.b_parts > 1) m.db = ws.take<float>(static_cast<size_t>(m.b_parts) * L * N * R);
+  m.row_waves = outer_row_waves(M, N, K, R, L);
+  m.parts = outer_parts(M, L, outer_groups(K, R, L, m.row_waves) + outer_groups(N, R, L, m.row_waves));
+  if (m.parts > 1) {
+    m.da = ws.take<float>(static_cast<size_t>(m.parts) * L * R * K);
+    m.db = ws.take<float>(static_cast<size_t>(m.parts) * L * N * R);
+  }
   return m;
 }
 
@@ -394,7 +407,7 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   if (int rc = check_buffers(bufs)) return rc;
   if (c.dx0 && !c.dx) return fail(W4A16_ERR_INVALID_ARG, "dx0 is given without dx");
   // the only grid that the bounds on the sizes do not keep below 2^32 threads
-  if (outer_groups(c.N, c.R, c.L) + outer_groups(c.K, c.R, c.L) >= int64_t{1} << 23)
+  if (outer_groups(c.N, c.R, c.L, 4) + outer_groups(c.K, c.R, c.L, 4) >= int64_t{1} << 23)
     return fail(W4A16_ERR_UNSUPPORTED, "gradients of %d adapters for N=%d, K=%d are too large for one call", c.L, c.N, c.K);
   Carver size{nullptr}, ws{static_cast<unsigned char*>(c.workspace)};
   backward_memory(size, nullptr, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
@@ -407,9 +420,10 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const SplitTask th{c.h, 1, m.h.frags, m.h.exps, nullptr, nullptr, nullptr};
   const SplitTask tg{m.part, m.S, m.g.frags, m.g.exps, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors, nullptr};
   hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 2), dim3(512), 0, st, th, tg, c.scaling, m.table, m.plan, c.R);
-  const OuterArgs ob = outer_args(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, m.b_parts > 1 ? m.db : c.db, c.N,
-                                  c.R, m.b_parts);
-  const OuterArgs oa = outer_args(kept, m.g, c.scaling, m.plan, m.a_parts > 1 ? m.da : c.da, c.K, c.R, m.a_parts);
+  const bool whole = m.parts == 1;
+  const OuterArgs ob = outer_args(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, whole ? c.db : m.db, c.N, c.R,
+                                  m.parts, m.row_waves);
+  const OuterArgs oa = outer_args(kept, m.g, c.scaling, m.plan, whole ? c.da : m.da, c.K, c.R, m.parts, m.row_waves);
   const StreamArgs dx = stream_args(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a),
                                     reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L,
                                     m.slots);
@@ -421,12 +435,12 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
     run_outers<Q8>(ob, oa, st);
     if (dx.out) dx.base ? run_stream<true, true>(dx, st) : run_stream<true, false>(dx, st);
   }
-  if (m.a_parts > 1 || m.b_parts > 1) {
-    auto task = [](float* parts, float* out, size_t count, int n) {
-      return PartsTask{reinterpret_cast<const float4_t*>(parts), reinterpret_cast<float4_t*>(out), n > 1 ? count / 4 : 0, n};
+  if (!whole) {
+    auto task = [&](const float* parts, float* out, size_t count) {
+      return PartsTask{reinterpret_cast<const float4_t*>(parts), reinterpret_cast<float4_t*>(out), count / 4, m.parts};
     };
-    const PartsTask ta = task(m.da, c.da, static_cast<size_t>(c.L) * c.R * c.K, m.a_parts);
-    const PartsTask tb = task(m.db, c.db, static_cast<size_t>(c.L) * c.N * c.R, m.b_parts);
+    const PartsTask ta = task(m.da, c.da, static_cast<size_t>(c.L) * c.R * c.K);
+    const PartsTask tb = task(m.db, c.db, static_cast<size_t>(c.L) * c.N * c.R);
     const size_t most = std::max(ta.quads, tb.quads);
     hipLaunchKernelGGL(lora_sum_parts_kernel, dim3(static_cast<unsigned>((most + 255) / 256), 2), dim3(256), 0, st, ta, tb);
   }

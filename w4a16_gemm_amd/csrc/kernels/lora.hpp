@@ -1086,6 +1086,7 @@ struct OuterArgs {
   RowPlan plan;
   float* grad;
   int C, R, parts;
+  int row_waves;            // 4: 128 channels per workgroup; 1: 128 per wavefront
 };
 
 // Workgroup `block` of columns x parts x rank blocks x adapters, D slots in flight per
@@ -1108,13 +1109,14 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
   // of ranks, eight blocks of channels are followed by their further blocks of ranks, which
   // thus find x in the same L2.
   const int ranks = (R + 16 * NT - 1) / (16 * NT);
+  const int row_waves = args.row_waves, width = 128 * W / row_waves;   // channels per workgroup
   int col, t0 = 0;
   if (ranks == 1) {
-    const int cols = (C + 127) >> 7;
+    const int cols = (C + width - 1) / width;
     col = block % cols;
     block /= cols;
   } else {
-    const int eights = (C + 1023) >> 10;
+    const int eights = (C + 8 * width - 1) / (8 * width);
     col = block & 7;
     block >>= 3;
     t0 = (block % ranks) * NT;
@@ -1124,8 +1126,10 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
   }
   const int part = block % parts;
   const int ad = block / parts;
-  const int c0 = col * 128;
-  if (c0 >= C) return;
+  const int c_block = col * width;
+  if (c_block >= C) return;
+  const int row_wave = row_waves == 1 ? 0 : wave;
+  const int c0 = c_block + (row_waves == 1 ? 128 * wave : 0);
   const int NTT = (R + 15) >> 4;   // fragments per slot
   // slots of the adapter: [first_slot, first_slot + n); positions lo .. hi - 1
   const int lo = plan.index ? plan.off[ad] : 0;
@@ -1221,7 +1225,7 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
 
   if (n > 0) {
     OuterSlot<NT, Q8> ring[D];
-    const int first = part * W + wave, stride = parts * W;
+    const int first = part * row_waves + row_wave, stride = parts * row_waves;
     const int mine = first < n ? (n - first + stride - 1) / stride : 0;   // slots of this wavefront
     auto slot_of = [&](int k) { return first + k * stride; };
     find_rows(slot_of(0));
@@ -1253,44 +1257,65 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
       if (k + d + D < mine) add(ring[d]);
   }
 
-  // Sum over the wavefronts, one channel fragment at a time, in units of 1; the sums are
-  // collected in LDS in the order of the gradient and leave as whole rows.
+  // The sums are collected in LDS in the order of the gradient, in units of 1, and leave as
+  // whole rows: the workgroup's 128 channels, one channel fragment of all wavefronts at a
+  // time, or the 128 channels of one wavefront after the other.
   const float si = n == 0 ? 0.0f : scaling ? scaling[ad] : 1.0f;
   float* sums = reinterpret_cast<float*>(red + W * NT * 64);   // [128][16 NT + 4] or [16 NT][128 + 4]
   constexpr int ld = CMAJOR ? 16 * NT + 4 : 128 + 4;
+  float* g = grad + (static_cast<size_t>(part) * plan.L + ad) * R * C;
+  auto collect = [&](int c, int j0, int l, const float4_t& v) {   // lane l's sums of fragment c
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int ch = CMAJOR ? 8 * (4 * (l >> 4) + r) + c : 8 * (l & 15) + c;
+      const int j = CMAJOR ? j0 + (l & 15) : j0 + 4 * (l >> 4) + r;
+      sums[CMAJOR ? ch * ld + j : j * ld + ch] = si * v[r];
+    }
+  };
+  auto leave = [&](int cb) {   // channels cb .. cb + 127
+    const int nj = min(16 * NT, R - 16 * t0), nc = min(128, C - cb);   // both multiples of 8
+    const int quads = (CMAJOR ? nj : nc) >> 2, lines = CMAJOR ? nc : nj;
+    for (int i = tid; i < quads * lines; i += 64 * W) {
+      const int line = i / quads, q = i % quads;
+      const float4_t v = *reinterpret_cast<const float4_t*>(sums + line * ld + 4 * q);
+      float* o = CMAJOR ? g + static_cast<size_t>(cb + line) * R + 16 * t0 : g + static_cast<size_t>(16 * t0 + line) * C + cb;
+      *reinterpret_cast<float4_t*>(o + 4 * q) = v;
+    }
+  };
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[c][t][r] = __builtin_ldexpf(acc[c][t][r], E);
+  if (row_waves == 1) {
+    for (int turn = 0; turn < W; ++turn) {
+      if (c_block + 128 * turn >= C) break;
+      if (wave == turn)
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) collect(c, 16 * t, lane, acc[c][t]);
+      __syncthreads();
+      leave(c_block + 128 * turn);
+      __syncthreads();
+    }
+    return;
+  }
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     __syncthreads();
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float4_t v = acc[c][t];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = __builtin_ldexpf(v[r], E);
-      red[(wave * NT + t) * 64 + lane] = v;
-    }
+    for (int t = 0; t < NT; ++t) red[(wave * NT + t) * 64 + lane] = acc[c][t];
     __syncthreads();
     for (int i = tid; i < NT * 64; i += 64 * W) {
       float4_t v = red[i];
       for (int w = 1; w < W; ++w) v += red[w * NT * 64 + i];
-      const int j0 = 16 * (i / 64), l = i & 63;
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int ch = CMAJOR ? 8 * (4 * (l >> 4) + r) + c : 8 * (l & 15) + c;
-        const int j = CMAJOR ? j0 + (l & 15) : j0 + 4 * (l >> 4) + r;
-        sums[CMAJOR ? ch * ld + j : j * ld + ch] = si * v[r];
-      }
+      collect(c, 16 * (i / 64), i & 63, v);
     }
   }
   __syncthreads();
-  float* g = grad + (static_cast<size_t>(part) * plan.L + ad) * R * C;
-  const int nj = min(16 * NT, R - 16 * t0), nc = min(128, C - c0);   // both multiples of 8
-  const int quads = (CMAJOR ? nj : nc) >> 2, lines = CMAJOR ? nc : nj;
-  for (int i = tid; i < quads * lines; i += 64 * W) {
-    const int line = i / quads, q = i % quads;
-    const float4_t v = *reinterpret_cast<const float4_t*>(sums + line * ld + 4 * q);
-    float* o = CMAJOR ? g + static_cast<size_t>(c0 + line) * R + 16 * t0 : g + static_cast<size_t>(16 * t0 + line) * C + c0;
-    *reinterpret_cast<float4_t*>(o + 4 * q) = v;
-  }
+  leave(c_block);
 }
 
 // Entries of LDS that outer_sums needs (the larger of its two gradient layouts).
