@@ -26,7 +26,9 @@
  *                   streams) that may run at once need a workspace each.
  * Buffers must be 16-byte aligned (index and scaling: 4-byte aligned).  Outputs must not
  * overlap inputs or the workspace, but for the two pairs named below.  Results do not
- * depend on timing: every sum has a fixed order.
+ * depend on timing: every sum has a fixed order.  An infinity or a NaN in an operand makes the
+ * results that it enters infinite or NaN (not always which of the two the formula gives), and
+ * no others: rows keep to themselves, gradients to their adapter.
  */
 #ifndef W4A16_ADAPTERS_H
 #define W4A16_ADAPTERS_H

@@ -137,7 +137,8 @@ CASES = [
     # below one step, off every tile, and over several workgroups and slices; ranks at and
     # between the fragment sizes, each with few and with many rows; few channels under many
     # rows (gradients in parts); adapters without rows, rows without an adapter, no index
-    # with several adapters; many adapters of few rows each under many channels
+    # with several adapters; many adapters of few rows each under many channels; numbers of
+    # adapters at and beyond those that one, two and three looks of 64 find
     (1, 8, 8, 8, 1, "one", 0), (1, 1536, 1536, 16, 4, "mixed", 0), (2, 136, 40, 8, 3, "mixed", 0),
     (15, 520, 512, 16, 1, "one", 0), (16, 512, 1024, 24, 2, "mixed", 0.2), (17, 1000, 1032, 32, 17, "mixed", 0.1),
     (33, 264, 2048, 40, 5, "runs", 0.2), (63, 640, 264, 48, 100, "mixed", 0.1), (64, 1544, 520, 64, 3, "runs", 0),
@@ -152,6 +153,7 @@ CASES = [
     (48, 1032, 6152, 8, 2, "mixed", 0.1), (20, 4104, 1032, 64, 3, "mixed", 0.1), (30, 2056, 1544, 104, 2, "mixed", 0.1),
     (700, 1032, 2056, 40, 12, "mixed", 0.1), (500, 2056, 1032, 16, 40, "runs", 0.1),
     (6, 104, 40, 8, 9, "one", 0), (300, 136, 264, 48, 3, "one", 0), (2100, 136, 136, 40, 2, "one", 0),
+    (700, 64, 64, 8, 5000, "mixed", 0.1), (1500, 8, 8, 8, 64, "mixed", 0.1), (700, 8, 8, 8, 4096, "mixed", 0.1),
 ]
 IDS = ["M{}-N{}-K{}-R{}-L{}-{}-{}".format(*c) for c in CASES]
 
