@@ -163,9 +163,9 @@ void run_shrink(const half_t* x, const half_t* w, const RowPlan& plan, int C, in
 #define W4A16_SHRINK(NT_, D_) \
   do { \
     if (waves == 8) { \
-      hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 8, TRANS>), grid, dim3(512), 0, st, x, w, plan, C, R, S, out); \
+      hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 8, TRANS, (NT_ == 8 ? 2 : 4)>), grid, dim3(512), 0, st, x, w, plan, C, R, S, out); \
     } else if (waves == 4) { \
-      hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 4, TRANS>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
+      hipLaunchKernelGGL((lora_shrink_tall_kernel<NT_, 4, TRANS, (NT_ == 8 ? 2 : 4)>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out); \
     } else if constexpr (!TRANS) { \
       hipLaunchKernelGGL((lora_shrink_kernel<NT_, D_>), grid, dim3(256), 0, st, x, w, plan, C, R, S, out, few); \
     } \

@@ -359,7 +359,7 @@ __device__ __forceinline__ void lds_barrier() {
 // TRANS: w is [L][C][R] (the b of the forward): it comes from memory as 8 ranks of a channel,
 // and takes its operand order on the way into LDS (16-bit writes, 8 per 16 bytes; the
 // operands' padding keeps the 16 pieces of a channel on different banks).
-template <int NT, int W, bool TRANS>
+template <int NT, int W, bool TRANS, int D>
 __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* __restrict__ x,
                                                                   const half_t* __restrict__ w, RowPlan plan, int C,
                                                                   int R, int S, float* __restrict__ out) {
@@ -386,8 +386,8 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* 
   const int b = static_cast<int>(static_cast<int64_t>(chunks) * s / S);
   const int e = static_cast<int>(static_cast<int64_t>(chunks) * (s + 1) / S);
   float4_t acc[NT] = {};
-  half8_t wreg[PT];
-  half8_t xs[2][SC];
+  half8_t wreg[D][PT];
+  half8_t xs[D][SC];
   // Pieces of 8 values of w per thread: ranks or channels of the chunk, and which.
   const int octs = TRANS ? R >> 3 : SC * 4;   // pieces per channel or rank
   int line[PT], oct[PT];
@@ -397,22 +397,22 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* 
     oct[i] = (tid + 64 * W * i) % octs;
   }
   // Loads past the slice or past C are clamped; channels past C are zeroed on both sides.
-  auto load_w = [&](int k) {
+  auto load_w = [&](int k, half8_t (&v)[PT]) {
     const int cb = min(k, e - 1) * 32 * SC;
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
       const size_t at = TRANS ? static_cast<size_t>(min(cb + line[i], C - 1)) * R + 8 * oct[i]
                               : static_cast<size_t>(min(line[i], R - 1)) * C + min(cb + 8 * oct[i], C - 8);
-      wreg[i] = *reinterpret_cast<const half8_t*>(wl + at);
+      v[i] = *reinterpret_cast<const half8_t*>(wl + at);
     }
   };
-  auto store_w = [&](int k, int buf) {
+  auto store_w = [&](int k, int buf, const half8_t (&w8)[PT]) {
 #pragma unroll
     for (int i = 0; i < PT; ++i) {
       if constexpr (TRANS) {
         const int c = line[i];   // channel of the chunk
         if (c >= 32 * SC) continue;
-        const half8_t v = k * 32 * SC + c < C ? wreg[i] : half8_t{};
+        const half8_t v = k * 32 * SC + c < C ? w8[i] : half8_t{};
         half_t* to = reinterpret_cast<half_t*>(lds[buf]) + (((c >> 5) * NT * TS + ((c >> 3) & 3) * 16) * 8 + (c & 7));
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -423,7 +423,7 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* 
         const int j = line[i], q = oct[i];
         if (j >= 16 * NT) continue;
         lds[buf][((q >> 2) * NT + (j >> 4)) * TS + (q & 3) * 16 + (j & 15)] =
-            k * 32 * SC + 8 * q < C ? wreg[i] : half8_t{};
+            k * 32 * SC + 8 * q < C ? w8[i] : half8_t{};
       }
     }
   };
@@ -442,26 +442,31 @@ __global__ __launch_bounds__(64 * W) void lora_shrink_tall_kernel(const half_t* 
       for (int t = 0; t < NT; ++t)
         acc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v[u], lds[buf][(u * NT + t) * TS + lane], acc[t], 0, 0, 0);
   };
-  load_w(b);
-  load_x(b, xs[0]);
-  load_x(b + 1, xs[1]);
-  store_w(b, 0);
-  load_w(b + 1);
-  lds_barrier();
-  for (int k = b; k < e;) {
-    add(k, 0, xs[0]);
-    load_x(k + 2, xs[0]);
-    store_w(k + 1, 1);
-    load_w(k + 2);
-    lds_barrier();
-    if (++k >= e) break;
-    add(k, 1, xs[1]);
-    load_x(k + 2, xs[1]);
-    store_w(k + 1, 0);
-    load_w(k + 2);
-    lds_barrier();
-    ++k;
+  // Chunk k: x in xs[k % D] (from b on), w in wreg[k % D] until it is in LDS.  Loads complete
+  // in order, so w is as far ahead as x.
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    load_w(b + d, wreg[d]);
+    load_x(b + d, xs[d]);
   }
+  store_w(b, 0, wreg[0]);
+  load_w(b + D, wreg[0]);
+  lds_barrier();
+  auto step = [&](int k, int d, bool inside) {   // d = (k - b) % D; inside: nothing ends yet
+    add(k, d & 1, xs[d]);
+    if (inside || k + D < e) load_x(k + D, xs[d]);
+    if (inside || k + 1 < e) store_w(k + 1, (d + 1) & 1, wreg[(d + 1) % D]);
+    if (inside || k + 1 + D < e) load_w(k + 1 + D, wreg[(d + 1) % D]);
+    lds_barrier();
+  };
+  int k = b;
+  for (; k + 2 * D < e; k += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) step(k + d, d, true);
+  }
+#pragma unroll
+  for (int d = 0; d < 2 * D; ++d)
+    if (k + d < e) step(k + d, d % D, false);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
