@@ -216,14 +216,17 @@ void run_fused(const half_t* x, const half_t* a, const half_t* b, const float* s
 #undef W4A16_FUSED
 }
 
+// `most` workgroups, 64 slots each at most.  Fewer of them read the weights less often, down
+// to one round of two per compute unit in the forward pass (512; 2048 rows x 14336 in runs of
+// eight adapters at rank 64: 30 us, with 1024 32 us, with 2048 37 us; 4096 x 28672 at rank 64:
+// 96 us, 99 us with 1024, 120 us with 256).  dx runs beside the outer products, whose end it
+// has to fill: 1024 (2500 rows of four adapters, K = N = 4096, rank 64: 25 us, with 512 29 us).
+constexpr int kForwardBlocks = 512, kBackwardBlocks = 1024;
+
 StreamArgs stream_args(const ByRow& h, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C,
-                       int R, int L, int slots) {
-  // At most 1024 workgroups (two rounds of two per compute unit) and 64 slots each: more slots
-  // per workgroup read the weights less often (2048 rows x 14336 in runs of eight adapters at
-  // rank 64: 37 us with one, 31 us with two), fewer workgroups leave compute units idle at the
-  // end (4096 rows x 8192: 30 us with 1024 of them, 35 us with 512).
+                       int R, int L, int slots, int most) {
   const int64_t all = static_cast<int64_t>(slots) * ceil_div(C, 512);
-  const int64_t group = std::max<int64_t>(1, std::min<int64_t>(64, (all + 1023) / 1024));
+  const int64_t group = std::max<int64_t>(1, std::min<int64_t>(64, (all + most - 1) / most));
   return {h.frags, h.factors, table, w, base, out, C, R, L, slots, static_cast<int>(group)};
 }
 
@@ -426,7 +429,7 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const OuterArgs oa = outer_args(kept, m.g, c.scaling, m.plan, whole ? c.da : m.da, c.K, c.R, m.parts, m.row_waves);
   const StreamArgs dx = stream_args(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a),
                                     reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L,
-                                    m.slots);
+                                    m.slots, kBackwardBlocks);
   if (products_together(c.R)) {
     if (c.R <= 16) run_products<1, 1, Q8>(ob, oa, dx, st);
     else if (c.R <= 32) run_products<2, 1, Q8>(ob, oa, dx, st);
@@ -488,7 +491,7 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
   if (m.stream) {
     const SplitTask t{m.part, m.S, nullptr, nullptr, m.h.frags, m.h.factors, h};
     hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(512), 0, st, t, t, scaling, m.table, m.plan, R);
-    run_stream<false, true>(stream_args(m.h, m.table, bh, yh, oh, N, R, L, m.slots), st);
+    run_stream<false, true>(stream_args(m.h, m.table, bh, yh, oh, N, R, L, m.slots, kForwardBlocks), st);
   } else {
     run_expand(m.part, m.S, m.table, m.slots, bh, scaling, L, yh, oh, h, N, R, st);
   }
