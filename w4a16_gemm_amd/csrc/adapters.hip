@@ -145,12 +145,18 @@ int shrink_waves(int M, int L, int R, bool trans) {
   return M / L >= 128 && (M > 512 || R > 32) ? 8 : 4;
 }
 
-// Slices of the long axis: enough workgroups for the GPU (two per compute unit), at least
-// 256 channels each (tiles of 16 rows: 512), and sums of the slices that stay small (8 MB)
-// or a quarter of x.
-int shrink_slices(int M, int L, int R, int C, bool trans, bool stream) {
+// Slices of the long axis: a workgroup per compute unit (tiles of 16 rows: two), at least 256
+// channels each (tiles of 16 rows: 512), and sums of the slices that stay small (8 MB) or a
+// quarter of x.  A second workgroup on some compute units only makes the others wait (4096 rows
+// x 28672 channels at rank 64: 50 us with 256, 52 us with 512; 2048 rows: 12 us with 256, 18 us
+// with 128).  With an index an adapter's last tile is half full on average.  A power of two, so
+// that a slice always falls to the same XCDs (8, in turn) and their L2 keeps its part of w (2048
+// rows x 4096 of eight adapters at rank 64: 11.3 us in 8 slices, 13.8 us in 12).
+int shrink_slices(int M, int L, int R, int C, bool with_index, bool trans, bool stream) {
   const int waves = stream ? shrink_waves(M, L, R, trans) : 1;
-  const int want = ceil_div(512, ceil_div(M, 16 * waves));
+  const int tiles = ceil_div(M, 16 * waves) + (with_index ? L / 2 : 0);
+  int want = waves == 1 ? ceil_div(512, ceil_div(M, 16)) : 256 / tiles;
+  if (waves > 1) while (want & (want - 1)) want &= want - 1;
   const int64_t light = std::max<int64_t>(C / (16 * R), (int64_t{1} << 21) / (static_cast<int64_t>(M) * R));
   return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, C / (waves == 1 ? 512 : 256), M > 512 ? 16 : 32, light})));
 }
@@ -334,7 +340,7 @@ ForwardMemory forward_memory(Carver& ws, const int32_t* index, bool with_index, 
   }
   m.stream = M > kInlineRows;
   m.plan = take_plan(ws, index, with_index && m.stream, M, L);
-  m.S = shrink_slices(M, L, R, K, false, m.stream);
+  m.S = shrink_slices(M, L, R, K, with_index, false, m.stream);
   if (m.stream) {
     m.slots = plan_slots(M, L, with_index);
     m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
@@ -365,7 +371,7 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
                                int L) {
   BackwardMemory m{};
   m.plan = take_plan(ws, index, with_index, M, L);
-  m.S = shrink_slices(M, L, R, N, true, true);
+  m.S = shrink_slices(M, L, R, N, with_index, true, true);
   m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
   m.slots = plan_slots(M, L, with_index);
   m.h = take_by_rank(ws, m.slots, R);

@@ -526,17 +526,18 @@ __device__ __forceinline__ void sum_slices(const float* __restrict__ h, size_t s
   const int tid = threadIdx.x;
   const int quads = R >> 2, ld = quads + 1, items = ROWS * quads;
   const int G = min(max(1, THREADS / items), S);
+  constexpr int U = 8;   // slices in flight
   for (int i = tid; i < items * G; i += THREADS) {
     const int g = i / items, m = i % items / quads, j = i % quads;
     float4_t v = {};
     if (m < count) {
       const float* p = h + at(m) + 4 * j;
-      for (int s0 = g; s0 < S; s0 += 4 * G) {
-        float4_t q[4];
+      for (int s0 = g; s0 < S; s0 += U * G) {
+        float4_t q[U];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const float4_t*>(p + min(s0 + k * G, S - 1) * slice);
+        for (int k = 0; k < U; ++k) q[k] = *reinterpret_cast<const float4_t*>(p + min(s0 + k * G, S - 1) * slice);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < U; ++k)
           if (s0 + k * G < S) v += q[k];
       }
     }
