@@ -137,11 +137,11 @@ int plan_slots(int M, int L, bool with_index) {
 // --- shrink -------------------------------------------------------------------------
 
 // Rows per tile of a shrink, in 16s (wavefronts): 128 or 64 rows, once an adapter has that
-// many on average; below that, and for up to 512 rows at small rank, 16 with the wavefronts
-// along the channels (512 rows x 11008 at rank 16: 4.8 us, in tiles of 64 rows 5.1).  With
-// w transposed only the tiles of 64 rows and more, which take w through LDS.
+// many on average; below that 16, with the wavefronts along the channels (512 rows x 11008 at
+// rank 16: 6.4 us, in tiles of 64 rows 6.2).  With w transposed only the tiles of 64 rows and
+// more, which take w through LDS.
 int shrink_waves(int M, int L, int R, bool trans) {
-  if (!trans && (M / L < 64 || (M <= 512 && R <= 32))) return 1;
+  if (!trans && M / L < 64) return 1;
   return M / L >= 128 && (M > 512 || R > 32) ? 8 : 4;
 }
 

@@ -14,7 +14,7 @@
 // + (x - t S) r: the residual is a few ulps of t times S, exact in fp32, so the result is
 // within an ulp (2^-17) of the quotient, and equal to it where it is representable, as the
 // halfway values are; rint of it is the rounded true quotient.  (A division per value cost
-// more than the memory traffic: 8192 x 8192 values 57 us with it, 37 us without.)
+// more than the memory traffic: 8192 x 8192 values 57 us with it, 39 us without.)
 // 515.5 is the largest binary16 whose 127-fold still rounds to a finite binary16; a group
 // above it (a in {65472, 65504}) has x / S < 127.5 and keeps q = 127.
 #pragma once
@@ -36,7 +36,7 @@ __device__ __forceinline__ half_t act_scale(float a) {
 
 // One lane quantises 2 x 8 consecutive channels (16 bytes in, 8 bytes out each); a group is
 // LPG = group / 8 neighbouring lanes, whose maximum is formed with lane exchanges.
-// HBM-bound: 3 bytes per value, 5.4 TB/s at 8192 x 8192.  The codes are written past the L2,
+// HBM-bound: 3 bytes per value, 5.2 TB/s at 8192 x 8192.  The codes are written past the L2,
 // their reader being the backward pass.  A NaN or an infinity in a group makes its scale
 // NaN (codes 128), so that the restored values are NaN and the gradients show it.
 constexpr int kActRuns = 2;   // of 256 lanes per workgroup

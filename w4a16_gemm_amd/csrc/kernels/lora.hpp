@@ -346,8 +346,9 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restri
 
 // Many rows: HBM-bound on x.  A tile of 16 W rows per workgroup, 16 per wavefront, so that w
 // is read once per tile; it goes through LDS (two buffers of 64 channels in operand order,
-// 16-byte accesses) while x streams into registers two chunks ahead: 4096 rows x 28672
-// channels at rank 64 in 52 us, 4.5 TB/s.  With w read by every wavefront for itself the
+// 16-byte accesses) while x and w stream into registers D chunks ahead: 4096 rows x 28672
+// channels at rank 64 in 51 us, 4.6 TB/s (with D = 2 54 us; eight operands of 16 ranks leave
+// registers for no more).  With w read by every wavefront for itself the
 // kernel was bound by L2 traffic: 83 us with 64 rows per wavefront, 138 us with 16.
 // The barrier orders LDS only: the x and w loads in flight pass it.
 __device__ __forceinline__ void lds_barrier() {
