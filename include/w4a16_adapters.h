@@ -16,7 +16,8 @@
  *   a               binary16 [L][R][K];  b  binary16 [L][N][R]
  *   index           int32 [M], adapter of every row, or NULL: adapter 0 for every row.  A
  *                   value outside [0, L) (-1 by convention) is a row without an adapter.
- *                   Rows may come in any order.
+ *                   Rows may come in any order.  Grouping them (more than 256 rows, or a
+ *                   backward pass) reads the index twice per adapter.
  *   scaling         float [L] (alpha / rank of every adapter) or NULL: 1
  *   h               float [M][R], A_i x of every row, 0 for rows without an adapter
  *   workspace       16-byte aligned device memory of at least the size that the matching

@@ -147,3 +147,29 @@ def test_overlapping_outputs_are_found():
     adapters._overlap(x[:4], (x[4:], "x"))
     with pytest.raises(ValueError):
         adapters._overlap(x[:5], (x[4:], "x"))
+
+
+def test_sizes_beyond_the_int_arguments_are_refused():
+    big = lambda *shape, dtype=torch.float16: torch.empty(*shape, dtype=dtype, device="meta")   # noqa: E731
+    rows = 2 ** 32 + 4      # 4 rows, if cut to 32 bits
+    d = dict(_tensors(), x=big(rows, 128), y=big(rows, 64), index=None, out=None, h=None)
+    with pytest.raises(ValueError, match="beyond 32 bits"):
+        w4.w4a16_lora_forward(**d)
+    with pytest.raises(ValueError, match="beyond 32 bits"):
+        w4.w4a16_lora_forward(**dict(_tensors(), a=big(2 ** 32 + 2, 16, 128), b=big(2 ** 32 + 2, 64, 16)))
+    with pytest.raises(ValueError, match="beyond 32 bits"):
+        w4.w4a16_act_quantize(big(rows, 128), 32)
+    with pytest.raises(ValueError, match="beyond 32 bits"):
+        w4.w4a16_act_dequantize(big(rows, 128, dtype=torch.uint8), big(rows, 4), 32)
+    b = _backward_tensors()
+    with pytest.raises(ValueError, match="beyond 32 bits"):
+        w4.w4a16_lora_backward(**dict(b, dy=big(rows, 64), x=big(rows, 128), h=big(rows, 16, dtype=torch.float32)))
+
+
+def test_missing_operands_are_refused():
+    for name in ("y", "x", "a", "b"):
+        with pytest.raises((TypeError, ValueError)):
+            w4.w4a16_lora_forward(**dict(_tensors(), **{name: None}))
+    for name in ("dy", "x", "a", "b", "h"):
+        with pytest.raises((TypeError, ValueError)):
+            w4.w4a16_lora_backward(**dict(_backward_tensors(), **{name: None}))

@@ -105,16 +105,23 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _matrix(t, name):
-    if not isinstance(t, _torch().Tensor) or t.dim() != 2:
-        raise ValueError(f"{name} must be a 2-d tensor")
+def _sizes(t, dims, name):
+    """The shape, whose entries have to fit the int arguments of the library."""
+    if not isinstance(t, _torch().Tensor) or t.dim() != dims:
+        raise ValueError(f"{name} must be a {dims}-d tensor")
+    if max(t.shape) > 2 ** 31 - 1:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, a size beyond 32 bits")
     return t.shape
 
 
-def _adapter_sizes(a):
-    if not isinstance(a, _torch().Tensor) or a.dim() != 3:
-        raise ValueError("a must be a 3-d tensor [L][R][K]")
-    return a.shape[0], a.shape[1]
+def _matrix(t, name):
+    return _sizes(t, 2, name)
+
+
+def _adapter_sizes(a, b):
+    L, R = _sizes(a, 3, "a [L][R][K]")[:2]
+    _sizes(b, 3, "b [L][N][R]")
+    return L, R
 
 
 def _overlap(out, *others):
@@ -147,7 +154,7 @@ def w4a16_lora_forward(y, x, a, b, index=None, scaling=None, out=None, h=None, s
     torch = _torch()
     M, K = _matrix(x, "x")
     N = _matrix(y, "y")[1]
-    L, R = _adapter_sizes(a)
+    L, R = _adapter_sizes(a, b)
     f16, f32 = torch.float16, torch.float32
     device = _operands(((x, f16, (M, K), "x"), (y, f16, (M, N), "y"), (a, f16, (L, R, K), "a"), (b, f16, (L, N, R), "b"),
                         (index, torch.int32, (M,), "index"), (scaling, f32, (L,), "scaling"),
@@ -174,7 +181,7 @@ def w4a16_lora_forward(y, x, a, b, index=None, scaling=None, out=None, h=None, s
 def _backward(dy, kept, specs, K, a, b, h, index, scaling, dx, out, need_dx, stream, entry):
     torch = _torch()
     M, N = _matrix(dy, "dy")
-    L, R = _adapter_sizes(a)
+    L, R = _adapter_sizes(a, b)
     f16, f32 = torch.float16, torch.float32
     if h is None:
         raise TypeError("h must be a torch.float32 tensor")
