@@ -41,6 +41,8 @@ __device__ __forceinline__ int row_class(int i, int L) { return i >= 0 && i < L 
 
 // Stable grouping by class: workgroup c counts the rows of smaller classes, then places
 // its own rows in order.  No atomics, so the order (and with it every sum) is fixed.
+// Latency-bound: 4 us for 2048 rows of eight adapters.  (Grouping inside the kernel that
+// follows, beside workgroups that write the plan, cost that kernel as much.)
 constexpr int kPlanRows = 8;   // rows per thread read at once (8192 per workgroup)
 
 __global__ __launch_bounds__(1024) void plan_rows_kernel(const int32_t* __restrict__ index, int M, int L,
@@ -303,6 +305,7 @@ __device__ __forceinline__ void add_wavefronts(float4_t* red, int wave, int lane
 // Few rows: a tile of 16 rows and a slice per workgroup of 4 wavefronts.  table.meta != NULL:
 // the next kernel works on the same tiles, so the tiles are written down and the sums go out
 // by tile, [slots][S][16][R], where that kernel can read them without looking up rows.
+// Latency-bound: 16 rows x 8192 of eight adapters at rank 16 5.4 us, 0.4 of them for the bytes.
 template <int NT, int D>
 __global__ __launch_bounds__(256) void lora_shrink_kernel(const half_t* __restrict__ x, const half_t* __restrict__ w,
                                                           RowPlan plan, int C, int R, int S, float* __restrict__ out,
@@ -639,6 +642,7 @@ __device__ __forceinline__ float split_row(const float (&v)[F][8], int lq, float
 
 // --- split: h or g (the sum of S slices) as ready MFMA operands ---------------------------
 //
+// Latency-bound (5 - 8 us; 4096 rows at rank 64, eight slices, all loaded at once: 6.4 us).
 // One workgroup per slot of 32 rows of one adapter and task, once per call instead of by
 // every workgroup of 128 channels that multiplies with h.  The sum goes through LDS, from
 // where it is written in either or both of two orders:
@@ -770,7 +774,8 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
 // h by tile, [slots][S][16][R], and the tiles as the shrink wrote them.  A workgroup of 4
 // wavefronts takes one tile of 16 rows x 512 channels; h is summed into LDS by all of it
 // while the weights and base are on their way, and every wavefront splits it for itself.
-// Latency-bound: what counts is one launch less, and few loads that wait for another.
+// Latency-bound: what counts is one launch less, and few loads that wait for another (16 rows
+// x 28672 of eight adapters at rank 16: 6.8 us).
 // base may equal out (every element is read and written by the same lane); rows without
 // an adapter are copied, bit for bit.  h_out (not NULL): the workgroups of the first
 // channels write the summed h.
@@ -1343,7 +1348,8 @@ __global__ __launch_bounds__(256, 2) void lora_outers_kernel(OuterArgs b, int b_
 
 // The three products of the backward pass in one launch: their workgroups fill the GPU
 // together (the outer products alone have one per 128 channels and block of ranks), and two
-// launches fall away.  Workgroups: dB, then dA, then dx (F fragments of 32 ranks).
+// launches fall away.  HBM-bound where it is large: 4096 rows, K = 8192 in 8 bits, N = 28672, rank
+// 64: 105 us for 459 MB, 4.4 TB/s.  Workgroups: dB, then dA, then dx (F fragments of 32 ranks).
 template <int NT, int F, bool Q8, bool DX, bool BASE>
 __global__ __launch_bounds__(256, 2) void lora_products_kernel(OuterArgs b, int b_blocks, OuterArgs a, int a_blocks,
                                                                StreamArgs dx) {
@@ -1358,7 +1364,7 @@ __global__ __launch_bounds__(256, 2) void lora_products_kernel(OuterArgs b, int 
   }
 }
 
-// out = sum of the parts, in order; both gradients in one launch (blockIdx.y).
+// out = sum of the parts, in order; both gradients in one launch (blockIdx.y), 4 us.
 struct PartsTask {
   const float4_t* parts;
   float4_t* out;
