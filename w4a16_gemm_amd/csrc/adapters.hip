@@ -94,7 +94,7 @@ struct ByRow {
 
 struct ByRank {
   half_t* frags;
-  int32_t* exps;
+  float* units;
 };
 
 ByRow take_by_row(Carver& ws, int slots, int R) {
@@ -103,8 +103,9 @@ ByRow take_by_row(Carver& ws, int slots, int R) {
 }
 
 ByRank take_by_rank(Carver& ws, int slots, int R) {
-  half_t* f = ws.take<half_t>(static_cast<size_t>(slots) * ceil_div(R, 16) * 1024);
-  return {f, ws.take<int32_t>(slots)};
+  const size_t frags = static_cast<size_t>(slots) * ceil_div(R, 16);
+  half_t* f = ws.take<half_t>(frags * 1024);
+  return {f, ws.take<float>(frags * 16)};
 }
 
 SlotTable take_table(Carver& ws, int slots, int rows) {
@@ -297,9 +298,9 @@ int outer_row_waves(int M, int N, int K, int R, int L) {
 // would hold the outer products back (300 rows, rank 128: 27 us in one launch, 24 us in two).
 bool products_together(int R) { return R <= 64; }
 
-OuterArgs outer_args(const Kept& k, const ByRank& f, const float* scaling, const RowPlan& plan, float* grad, int C, int R,
-                     int parts, int row_waves) {
-  return {k.x, k.codes, k.scales, k.gshift, f.frags, f.exps, scaling, plan, grad, C, R, parts, row_waves};
+OuterArgs outer_args(const Kept& k, const ByRank& f, const float* h, const float* scaling, const RowPlan& plan,
+                     float* grad, int C, int R, int parts, int row_waves) {
+  return {k.x, k.codes, k.scales, k.gshift, f.frags, f.units, h, scaling, plan, grad, C, R, parts, row_waves};
 }
 
 int outer_blocks(const OuterArgs& o) { return static_cast<int>(outer_groups(o.C, o.R, o.plan.L, o.row_waves) * o.parts); }
@@ -361,6 +362,7 @@ struct BackwardMemory {
   float* part;       // g: [S][M][R]
   int S, slots;
   ByRank h, g;
+  float* g_sum;      // [M][R]
   ByRow g_rows;
   SlotTable table;
   int parts, row_waves;   // of the outer products
@@ -376,6 +378,7 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
   m.slots = plan_slots(M, L, with_index);
   m.h = take_by_rank(ws, m.slots, R);
   m.g = take_by_rank(ws, m.slots, R);
+  m.g_sum = ws.take<float>(static_cast<size_t>(M) * R);
   m.g_rows = take_by_row(ws, m.slots, R);
   m.table = take_table(ws, m.slots, kSlotRows);
   m.row_waves = outer_row_waves(M, N, K, R, L);
@@ -426,13 +429,14 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const auto* dy = reinterpret_cast<const half_t*>(c.dy);
   run_plan(m.plan, st);
   run_shrink<true>(dy, reinterpret_cast<const half_t*>(c.b), m.plan, c.N, c.R, m.S, m.part, SlotTable{}, st);
-  const SplitTask th{c.h, 1, m.h.frags, m.h.exps, nullptr, nullptr, nullptr};
-  const SplitTask tg{m.part, m.S, m.g.frags, m.g.exps, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors, nullptr};
+  const SplitTask th{c.h, 1, m.h.frags, m.h.units, nullptr, nullptr, nullptr};
+  const SplitTask tg{m.part, m.S, m.g.frags, m.g.units, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors, m.g_sum};
   hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 2), dim3(512), 0, st, th, tg, c.scaling, m.table, m.plan, c.R);
   const bool whole = m.parts == 1;
-  const OuterArgs ob = outer_args(Kept{dy, nullptr, nullptr, 0}, m.h, c.scaling, m.plan, whole ? c.db : m.db, c.N, c.R,
-                                  m.parts, m.row_waves);
-  const OuterArgs oa = outer_args(kept, m.g, c.scaling, m.plan, whole ? c.da : m.da, c.K, c.R, m.parts, m.row_waves);
+  const OuterArgs ob = outer_args(Kept{dy, nullptr, nullptr, 0}, m.h, c.h, c.scaling, m.plan, whole ? c.db : m.db, c.N,
+                                  c.R, m.parts, m.row_waves);
+  const OuterArgs oa = outer_args(kept, m.g, m.g_sum, c.scaling, m.plan, whole ? c.da : m.da, c.K, c.R, m.parts,
+                                  m.row_waves);
   const StreamArgs dx = stream_args(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a),
                                     reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L,
                                     m.slots, kBackwardBlocks);

@@ -10,9 +10,12 @@
 //
 // All of them are tall products with one side of R <= 128, on v_mfma_f32_16x16x32_f16
 // with fp32 sums.  Every operand that comes from memory is binary16 and enters exactly; h
-// and g are fp32 sums and enter as two binary16 terms (hi + lo, 22 bits) after a division
-// by a power of two that brings the largest of them to [2^13, 2^14), so nothing overflows
-// and the split loses less than the fp32 sums do.
+// and g are fp32 sums and enter as two binary16 terms (hi + lo) after a division by a power of
+// two that brings the largest of them to [2^13, 2^14), so nothing overflows.  The two terms hold
+// a value to 2^-23 of itself as long as it lies within 2^15 of that largest one.  In the outer
+// products, where the largest is that of a rank in a slot of 32 rows, a slot with a smaller value
+// that the terms do not hold is multiplied in fp32.  In out and dx, where it is that of a row,
+// a smaller value is off by up to 2^-39 of the largest.
 //
 // Rows are worked on in tiles of 16 to 128 rows of one adapter each; rows of one adapter are
 // found through a row plan (below), so any order of rows costs the same products.
@@ -207,17 +210,20 @@ __device__ __forceinline__ float finite_magnitude(float v) {
 // Exponent e with m < 2^e (m > 0), 0 for m == 0.
 __device__ __forceinline__ int top_exponent(float m) { return m > 0.0f ? __builtin_amdgcn_frexp_expf(m) : 0; }
 
-// v = h 2^shift as hi + lo in binary16.  An infinite or NaN h keeps it in hi alone.
-__device__ __forceinline__ void split_half(float h, int shift, half_t& hi, half_t& lo) {
+// v = h 2^shift as hi + lo in binary16.  An infinite or NaN h keeps it in hi alone.  Where lo
+// is subnormal it holds multiples of 2^-24: a v of at least 2^-2 is still within 2^-23 of itself.
+// Below, false is returned if anything is lost.
+__device__ __forceinline__ bool split_half(float h, int shift, half_t& hi, half_t& lo) {
   const float v = __builtin_ldexpf(h, shift);
   hi = static_cast<half_t>(v);
   const float r = v - static_cast<float>(hi);
   lo = static_cast<half_t>(__builtin_fabsf(v) <= 65504.0f ? r : 0.0f);
+  return !(__builtin_fabsf(v) < 0.25f && static_cast<float>(lo) != r);
 }
 
 constexpr int kMaxRank = 128;
 constexpr int kSplitTop = 14;   // split operands are below 2^14
-constexpr int kNoExponent = -1000;   // of values that are all zero
+constexpr int kLeastExponent = -148;   // of an outer operand: 2^e is an fp32 number, h 2^-e exact
 
 // --- shrink: out[s][m][j] = sum over the channels of slice s of x[m][c] w[i][j][c] -------
 //
@@ -647,19 +653,21 @@ __device__ __forceinline__ float split_row(const float (&v)[F][8], int lq, float
 // every workgroup of 128 channels that multiplies with h.  The sum goes through LDS, from
 // where it is written in either or both of two orders:
 //   by_rank (outer)   fragment t: lane (r, q) has rank 16 t + r of rows 8 q .. 8 q + 7, in
-//                     units of 2^exps[slot]; [slots][NT][hi, lo][64][8]
+//                     units of |unit| of that slot and rank, a power of two (ranks never meet in
+//                     a gradient); [slots][NT][hi, lo][64][8].  A fragment that holds a value
+//                     which two terms beside the largest of its rank cannot hold has negative units
 //   by_row (stream)   group g of 16 rows, fragment f: lane (r, q) has ranks 32 f + 8 q .. + 7
 //                     of row 16 g + r, in units of 2^e of that row, with factors[row of the
 //                     slot] = s_i 2^e; [slots][2][F][hi, lo][64][8].  R <= 16: one fragment
 //                     with hi of ranks 0 .. 15 in its first two quarters and lo in the
 //                     others; [slots][2][64][8]
 // Rows past the slot's count and ranks past R are zero.  A by-row task also writes the slot
-// table and, where wanted, the summed h (0 for rows without an adapter).
+// table.  Where wanted, the summed h is written (0 for rows without an adapter).
 struct SplitTask {
   const float* h;    // [S][M][R]
   int S;
   half_t* by_rank;   // or NULL
-  int32_t* exps;     // [slots]
+  float* units;      // [slots][16 NT]
   half_t* by_row;    // or NULL
   float* factors;    // [slots][32]
   float* sum;        // [M][R] or NULL
@@ -671,7 +679,6 @@ __host__ __device__ constexpr int row_frags(int R) { return R <= 16 ? 1 : 2 * ((
 __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask t1, const float* __restrict__ scaling,
                                                          SlotTable table, RowPlan plan, int R) {
   __shared__ int32_t rows[kSlotRows];
-  __shared__ float tops[8];
   __shared__ float row_top[kSlotRows];
   __shared__ float4_t sums[sum_quads(kSlotRows, 512)];
   const SplitTask task = blockIdx.y == 0 ? t0 : t1;
@@ -699,34 +706,33 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
           sums[i / quads * ld + i % quads];
   const float* f = reinterpret_cast<const float*>(sums);
   if (task.by_rank) {
-    float top = 0.0f;
-    for (int i = tid; i < kSlotRows * quads; i += 512) {
-      const float4_t v = sums[i / quads * ld + i % quads];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) top = fmaxf(top, finite_magnitude(v[k]));
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if (lane == 0) tops[wave] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, tops[w]);
-    const int e = top > 0.0f ? top_exponent(top) - kSplitTop : kNoExponent;
-    if (tid == 0) task.exps[slot] = e;
     const int NT = (R + 15) >> 4;
     for (int t = wave; t < NT; t += 8) {
       const int j = 16 * t + lr;
+      float v[8], top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = j < R ? f[(8 * lq + i) * 4 * ld + j] : 0.0f;
+        top = fmaxf(top, finite_magnitude(v[i]));
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const int e = top > 0.0f ? max(top_exponent(top) - kSplitTop, kLeastExponent) : 0;
+      bool whole = true;
       half8_t hi, lo;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         half_t a, b;
-        split_half(j < R ? f[(8 * lq + i) * 4 * ld + j] : 0.0f, e == kNoExponent ? 0 : -e, a, b);
+        whole &= split_half(v[i], -e, a, b);
         hi[i] = a;
         lo[i] = b;
       }
       half8_t* o = reinterpret_cast<half8_t*>(task.by_rank) + (static_cast<size_t>(slot) * NT + t) * 128 + lane;
       o[0] = hi;
       o[64] = lo;
+      const float unit = __builtin_ldexpf(1.0f, e);
+      const bool all = __all(whole);
+      if (lq == 0) task.units[(static_cast<size_t>(slot) * NT + t) * 16 + lr] = all ? unit : -unit;
     }
   }
   if (!task.by_row) return;
@@ -1073,19 +1079,24 @@ __global__ __launch_bounds__(256, F <= 2 ? 2 : 1) void lora_stream_kernel(Stream
 // loads 8 channels (octet r) of its 8 rows (8 q ..) and transposes the 8 x 8 block in
 // registers, so that x goes from memory to the MFMA operand without LDS; the next slot's
 // rows are in flight meanwhile.  The split h comes as ready operands.
-// Every slot has a power of two of its own; the sums are kept in units of the largest seen
-// (as the running maximum of a softmax is): a larger one rescales the sums, a smaller one
-// the operands.  A slot's missing rows repeat its first one against zero operands.
+// The products of a slot are summed from zero and join the sums in fp32, times the unit of their
+// slot and rank.  A slot whose operands are not whole (negative units; values that lie more than 2^16
+// apart within a rank and take more than two terms) is multiplied in fp32 instead, from the summed
+// h (8 times the MFMA cycles; 3% of the slots and blocks of 32 ranks of a normally distributed h):
+// training step 291 -> 294 us, backward of 2048 rows 40.1 -> 40.6 us, the other backward passes
+// within 1%, against scaling slots and ranks by one power of two for all of a slot.
+// A slot's missing rows repeat its first one against zero operands.
 // Q8: x is an 8-bit checkpoint, expanded after the transpose (which then moves bytes).
 // CMAJOR: gradient [L][C][R] (channels are MFMA rows), else [L][R][C].
-// Few channels leave compute units idle, so the slots are dealt to `parts` workgroups (the
-// low part of blockIdx.y), each with a gradient of its own, added by lora_sum_parts_kernel.
-template <int NT, bool Q8>
+// Few channels leave compute units idle, so the slots are dealt to `parts` workgroups (decoded
+// from the block after its channels and block of ranks), each with a gradient of its own, added by
+// lora_sum_parts_kernel.
+template <int NT, bool Q8, bool CMAJOR>
 struct OuterSlot {
   uint4 v[8];              // 8 rows of 8 channels (Q8: the codes in x and y)
   uint32_t s2[Q8 ? 4 : 1]; // scales of rows 2 i, 2 i + 1
   half8_t h[NT][2];        // hi and lo operands
-  int e;                   // their power of two
+  float unit[NT][CMAJOR ? 1 : 4];   // of the ranks of this lane's sums
 };
 
 struct OuterArgs {
@@ -1094,7 +1105,8 @@ struct OuterArgs {
   const half_t* xs;
   int gshift;
   const half_t* frags;
-  const int32_t* exps;
+  const float* units;
+  const float* h;           // [M][R], summed
   const float* scaling;
   RowPlan plan;
   float* grad;
@@ -1110,7 +1122,7 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
   const uint8_t* __restrict__ codes = args.codes;
   const half_t* __restrict__ xs = args.xs;
   const half_t* __restrict__ frags = args.frags;
-  const int32_t* __restrict__ exps = args.exps;
+  const float* __restrict__ units = args.units;
   const float* __restrict__ scaling = args.scaling;
   const RowPlan plan = args.plan;
   float* __restrict__ grad = args.grad;
@@ -1163,9 +1175,8 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
       row[i] = plan.index ? plan.perm[p] : p;
     }
   };
-  auto load = [&](int k, OuterSlot<NT, Q8>& o) {
+  auto load = [&](int k, OuterSlot<NT, Q8, CMAJOR>& o) {
     const int slot = first_slot + min(k, n - 1);
-    o.e = exps[slot];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if constexpr (Q8) {
@@ -1184,32 +1195,29 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
       const int tt = min(t0 + t, NTT - 1);   // past the last: computed, not stored
       o.h[t][0] = f[tt * 128];
       o.h[t][1] = f[tt * 128 + 64];
+      const float* u = units + (static_cast<size_t>(slot) * NTT + tt) * 16;
+      if constexpr (CMAJOR) {
+        o.unit[t][0] = u[lr];
+      } else {
+        const float4_t u4 = *reinterpret_cast<const float4_t*>(u + 4 * lq);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o.unit[t][r] = u4[r];
+      }
     }
   };
 
   float4_t acc[8][NT] = {};
-  int E = kNoExponent;   // sums are in units of 2^E
-  auto add = [&](OuterSlot<NT, Q8>& o) {
-    const int e = __builtin_amdgcn_readfirstlane(o.e);
-    if (e > E) {
-      if (E != kNoExponent)
+  // Slots that are not whole are left for later: bit i for this wavefront's slots from i <<
+  // left_shift on, 64 such runs at most.
+  uint64_t left = 0;
+  int left_shift = 0;
+  auto add = [&](int k, const OuterSlot<NT, Q8, CMAJOR>& o) {
+    bool whole = true;   // the 16 units of a fragment have one sign
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-#pragma unroll
-          for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[c][t][r] = __builtin_ldexpf(acc[c][t][r], E - e);
-      E = e;
-    } else if (e < E && e != kNoExponent) {
-      // 2^(e - E) in two factors that binary16 holds; beyond 2^-40 nothing is left
-      const int d = max(e - E, -40), d0 = max(d, -20);
-      const half_t down0 = static_cast<half_t>(__builtin_ldexpf(1.0f, d0));
-      const half_t down1 = static_cast<half_t>(__builtin_ldexpf(1.0f, d - d0));
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        o.h[t][0] = o.h[t][0] * down0 * down1;
-        o.h[t][1] = o.h[t][1] * down0 * down1;
-      }
+    for (int t = 0; t < NT; ++t) whole &= __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, o.unit[t][0])) >= 0;
+    if (!whole) {
+      left |= 1ull << (k >> left_shift);
+      return;
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
@@ -1228,19 +1236,61 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
         xf = column8(o.v, c);
       }
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        float4_t v = {};
 #pragma unroll
         for (int p = 0; p < 2; ++p)
-          acc[c][t] = CMAJOR ? __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, o.h[t][p], acc[c][t], 0, 0, 0)
-                             : __builtin_amdgcn_mfma_f32_16x16x32_f16(o.h[t][p], xf, acc[c][t], 0, 0, 0);
+          v = CMAJOR ? __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, o.h[t][p], v, 0, 0, 0)
+                     : __builtin_amdgcn_mfma_f32_16x16x32_f16(o.h[t][p], xf, v, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[c][t][r] = fmaf(v[r], o.unit[t][CMAJOR ? 0 : r], acc[c][t][r]);
+      }
+    }
+  };
+  // A slot in fp32, four rows at a time: step i takes row 8 q + i of every quarter q.
+  auto add_fp32 = [&](int k) {
+    bool whole = true;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float u = units[(static_cast<size_t>(first_slot + k) * NTT + min(t0 + t, NTT - 1)) * 16];
+      whole &= __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, u)) >= 0;
+    }
+    if (whole) return;
+    const int p0 = lo + k * kSlotRows;
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+      const bool in = p0 + 8 * lq + i < hi;
+      const int p = in ? p0 + 8 * lq + i : p0;
+      const size_t m = plan.index ? plan.perm[p] : p;
+      half8_t xv;
+      if constexpr (Q8) {
+        const uint2 c = *reinterpret_cast<const uint2*>(codes + m * C + cc);
+        const half_t s = xs[m * G + (cc >> gshift)];
+        xv = act_values(c, half2_t{s, s});
+      } else {
+        xv = *reinterpret_cast<const half8_t*>(x + m * C + cc);
+      }
+      float h[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int j = 16 * (t0 + t) + lr;
+        h[t] = in && j < R ? args.h[m * R + j] : 0.0f;
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+          acc[c][t] = CMAJOR ? __builtin_amdgcn_mfma_f32_16x16x4f32(static_cast<float>(xv[c]), h[t], acc[c][t], 0, 0, 0)
+                             : __builtin_amdgcn_mfma_f32_16x16x4f32(h[t], static_cast<float>(xv[c]), acc[c][t], 0, 0, 0);
     }
   };
 
   if (n > 0) {
-    OuterSlot<NT, Q8> ring[D];
+    OuterSlot<NT, Q8, CMAJOR> ring[D];
     const int first = part * row_waves + row_wave, stride = parts * row_waves;
     const int mine = first < n ? (n - first + stride - 1) / stride : 0;   // slots of this wavefront
     auto slot_of = [&](int k) { return first + k * stride; };
+    while (mine > 64 << left_shift) ++left_shift;
     find_rows(slot_of(0));
 #pragma unroll
     for (int d = 0; d < D; ++d) {
@@ -1252,14 +1302,14 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
     for (; k + 2 * D <= mine; k += D) {
 #pragma unroll
       for (int d = 0; d < D; ++d) {
-        add(ring[d]);
+        add(k + d, ring[d]);
         load(slot_of(k + d + D), ring[d]);
         find_rows(slot_of(k + d + D + 1));
       }
     }
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (k + d < mine) add(ring[d]);
+      if (k + d < mine) add(k + d, ring[d]);
       if (k + d + D < mine) {
         load(slot_of(k + d + D), ring[d]);
         find_rows(slot_of(k + d + D + 1));
@@ -1267,10 +1317,16 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
     }
 #pragma unroll
     for (int d = 0; d < D; ++d)
-      if (k + d + D < mine) add(ring[d]);
+      if (k + d + D < mine) add(k + d + D, ring[d]);
+    while (left) {
+      const int at = __builtin_ctzll(left) << left_shift;
+      left &= left - 1;
+#pragma unroll 1
+      for (k = at; k < min(mine, at + (1 << left_shift)); ++k) add_fp32(slot_of(k));
+    }
   }
 
-  // The sums are collected in LDS in the order of the gradient, in units of 1, and leave as
+  // The sums are collected in LDS in the order of the gradient and leave as
   // whole rows: the workgroup's 128 channels, one channel fragment of all wavefronts at a
   // time, or the 128 channels of one wavefront after the other.
   const float si = n == 0 ? 0.0f : scaling ? scaling[ad] : 1.0f;
@@ -1295,12 +1351,6 @@ __device__ __forceinline__ void outer_sums(const OuterArgs& args, int block, flo
       *reinterpret_cast<float4_t*>(o + 4 * q) = v;
     }
   };
-#pragma unroll
-  for (int c = 0; c < 8; ++c)
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) acc[c][t][r] = __builtin_ldexpf(acc[c][t][r], E);
   if (row_waves == 1) {
     for (int turn = 0; turn < W; ++turn) {
       if (c_block + 128 * turn >= C) break;
