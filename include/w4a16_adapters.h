@@ -45,7 +45,7 @@ extern "C" {
 size_t w4a16_lora_forward_workspace(int M, int N, int K, int R, int L, int with_index);
 
 /* out[m] = binary16(y[m] + s_i B_i (A_i x[m])), i = index[m]: binary16 operands, fp32 sums,
- * A_i x kept to 22 bits between the two products, one rounding at the end.  Rows without an
+ * A_i x within 2^-23 of itself between the two products, one rounding at the end.  Rows without an
  * adapter: out[m] = y[m], bit for bit.  out may be y (in place).  h: NULL, or where A_i x
  * is written for the backward pass.
  * Errors: INVALID_ARG (also a workspace that is too small), UNSUPPORTED (R, L),
@@ -58,7 +58,8 @@ int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const uint16_t* a, 
 size_t w4a16_lora_backward_workspace(int M, int N, int K, int R, int L, int with_index);
 
 /* Gradients of w4a16_lora_forward for the output gradient dy binary16 [M][N], with
- * g[m] = B_i^T dy[m] (fp32):
+ * g[m] = B_i^T dy[m] (fp32; every g and h enters the products within 2^-23 of itself, however
+ * far rows and ranks lie apart):
  *   da float [L][R][K]: da_i = s_i sum g[m] x[m]^T,   db float [L][N][R]: db_i = s_i sum
  *   dy[m] h[m]^T, over the rows with index i (zeros for an adapter without rows);
  *   dx binary16 [M][K]: dx[m] = binary16(dx0[m] + s_i A_i^T g[m]); rows without an adapter

@@ -158,3 +158,70 @@ def test_many_tiles_of_one_adapter_far_apart():
     got = backward(d, dev(h))
     for name, g, r, t in list(zip(("dx", "da", "db"), got, ref, backward_bound(few, h[rows], ref)))[1:]:
         within(name, g, r, t)
+
+
+def spread(d, R, first, second, seed):
+    """Ranks of `first` [.., R on axis 1 or 2 ..] fall by up to 2^31, those of `second` rise by as
+    much: every rank has a like part of the output, from h or g that lie that far apart."""
+    k = np.random.default_rng(seed).permutation(np.linspace(0, 31, R).astype(int))
+    rng = np.random.default_rng(seed + 1)
+    for name, power in ((first, 12 - k), (second, k - 18)):
+        along = 2.0 ** (power[:, None] if name == "a" else power[None, :])
+        d[name] = (np.clip(rng.standard_normal(d[name].shape), -4, 4) * along).astype(np.float16)
+
+
+# one launch, two launches, and the stream, each with its ranks; rows of several adapters and
+# rows without one
+OUTPUTS = [(1, 1536, 1536, 16, 4, "mixed", 0), (9, 520, 776, 32, 2, "mixed", 0), (33, 264, 1024, 48, 5, "runs", 0.2),
+           (17, 1000, 8200, 16, 3, "mixed", 0.1), (30, 2056, 2056, 24, 2, "mixed", 0), (20, 4104, 1032, 64, 3, "mixed", 0.1),
+           (30, 520, 1544, 96, 1, "one", 0), (65, 264, 1544, 128, 2, "mixed", 0.1),
+           (300, 264, 520, 16, 3, "mixed", 0.1), (700, 136, 264, 24, 2, "runs", 0.1), (300, 648, 136, 64, 1, "one", 0),
+           (333, 264, 264, 96, 3, "mixed", 0.1), (450, 136, 264, 128, 2, "mixed", 0.1)]
+OUTPUT_IDS = ["M{}-N{}-K{}-R{}-L{}-{}-{}".format(*c) for c in OUTPUTS]
+
+
+@pytest.mark.parametrize("case", OUTPUTS, ids=OUTPUT_IDS)
+def test_outputs_of_ranks_far_apart(case):
+    import torch
+    M, R = case[0], case[3]
+    note(f"lora range: out {case}")
+    d = make(*case, seed=51)
+    d["y"][:] = 0
+    spread(d, R, "a", "b", 52)
+    d["x"][:M // 2] = 0          # some tiles far apart, some zero
+    ref, _ = oracle.lora_forward(d["y"], d["x"], d["a"], d["b"], d["index"], d["scaling"])
+    out = forward(d)
+    within("out", out, ref, forward_bound(d, ref))
+    y, h = dev(d["y"]), torch.empty((M, R), device=device())
+    w4.w4a16_lora_forward(y, dev(d["x"]), dev(d["a"]), dev(d["b"]), dev(d["index"]), dev(d["scaling"]), out=y, h=h)
+    assert same(y, out)
+    # beside a base that is not zero, and only one adapter far apart
+    e = make(*case, seed=53)
+    e["a"][-1], e["b"][-1] = d["a"][-1], d["b"][-1]
+    ref, _ = oracle.lora_forward(e["y"], e["x"], e["a"], e["b"], e["index"], e["scaling"])
+    within("out of one adapter", forward(e), ref, forward_bound(e, ref))
+
+
+@pytest.mark.parametrize("case", [c for c in OUTPUTS if c[2] < 2000] + [(96, 64, 72, 32, 2, "mixed", 0.1)],
+                         ids=lambda c: "M{}-N{}-K{}-R{}-L{}-{}-{}".format(*c))
+def test_input_gradients_of_ranks_far_apart(case):
+    M, R = case[0], case[3]
+    note(f"lora range: dx {case}")
+    d = make(*case, seed=61)
+    spread(d, R, "b", "a", 62)
+    d["dy"][M // 2:] = 0
+    _, h = oracle.lora_forward(d["y"], d["x"], d["a"], d["b"], d["index"], d["scaling"])
+    h = h.astype(np.float32)
+    for dx0 in (False, True):
+        if not dx0:
+            d["dx0"][:] = 0
+        else:
+            d["dx0"] = make(*case, seed=63)["dx0"]
+        ref = oracle.lora_backward(d["dy"], d["x"], d["a"], d["b"], h, d["index"], d["scaling"], d["dx0"])
+        got = backward(d, dev(h), dx0=dx0)
+        for name, g, r, t in zip(("dx", "da", "db"), got, ref, backward_bound(d, h, ref)):
+            within(name, g, r, t)
+    dx = dev(d["dx0"])
+    w4.w4a16_lora_backward(dev(d["dy"]), dev(d["x"]), dev(d["a"]), dev(d["b"]), dev(h), dev(d["index"]),
+                           dev(d["scaling"]), dx=dx, out=dx)
+    assert same(dx, got[0])

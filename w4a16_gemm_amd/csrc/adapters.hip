@@ -90,6 +90,7 @@ struct Carver {
 struct ByRow {
   half_t* frags;
   float* factors;
+  uint8_t* wide;
 };
 
 struct ByRank {
@@ -99,7 +100,8 @@ struct ByRank {
 
 ByRow take_by_row(Carver& ws, int slots, int R) {
   half_t* f = ws.take<half_t>(static_cast<size_t>(slots) * 2 * row_frags(R) * 512);
-  return {f, ws.take<float>(static_cast<size_t>(slots) * kSlotRows)};
+  float* factors = ws.take<float>(static_cast<size_t>(slots) * kSlotRows);
+  return {f, factors, ws.take<uint8_t>(static_cast<size_t>(slots) * 8)};
 }
 
 ByRank take_by_rank(Carver& ws, int slots, int R) {
@@ -230,11 +232,11 @@ void run_fused(const half_t* x, const half_t* a, const half_t* b, const float* s
 // has to fill: 1024 (2500 rows of four adapters, K = N = 4096, rank 64: 25 us, with 512 29 us).
 constexpr int kForwardBlocks = 512, kBackwardBlocks = 1024;
 
-StreamArgs stream_args(const ByRow& h, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C,
+StreamArgs stream_args(const ByRow& f, const float* h, const float* scaling, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C,
                        int R, int L, int slots, int most) {
   const int64_t all = static_cast<int64_t>(slots) * ceil_div(C, 512);
   const int64_t group = std::max<int64_t>(1, std::min<int64_t>(64, (all + most - 1) / most));
-  return {h.frags, h.factors, table, w, base, out, C, R, L, slots, static_cast<int>(group)};
+  return {f.frags, f.factors, f.wide, h, scaling, table, w, base, out, C, R, L, slots, static_cast<int>(group)};
 }
 
 int stream_blocks(const StreamArgs& s) { return ceil_div(s.C, 512) * ceil_div(s.slots, s.group); }
@@ -328,6 +330,7 @@ struct ForwardMemory {
   int S, slots;
   bool fused, stream;
   ByRow h;
+  float* h_far;      // [M][R]: h of the slots that are not whole, where the caller does not want it
   SlotTable table;
 };
 
@@ -346,6 +349,7 @@ ForwardMemory forward_memory(Carver& ws, const int32_t* index, bool with_index, 
     m.slots = plan_slots(M, L, with_index);
     m.part = ws.take<float>(static_cast<size_t>(m.S) * M * R);
     m.h = take_by_row(ws, m.slots, R);
+    m.h_far = ws.take<float>(static_cast<size_t>(M) * R);
     m.table = take_table(ws, m.slots, kSlotRows);
   } else {
     m.slots = tile_slots(M, L, with_index, false, kFewRows);
@@ -362,7 +366,7 @@ struct BackwardMemory {
   float* part;       // g: [S][M][R]
   int S, slots;
   ByRank h, g;
-  float* g_sum;      // [M][R]
+  float* g_far;      // [M][R]: g of the slots that are not whole
   ByRow g_rows;
   SlotTable table;
   int parts, row_waves;   // of the outer products
@@ -378,7 +382,7 @@ BackwardMemory backward_memory(Carver& ws, const int32_t* index, bool with_index
   m.slots = plan_slots(M, L, with_index);
   m.h = take_by_rank(ws, m.slots, R);
   m.g = take_by_rank(ws, m.slots, R);
-  m.g_sum = ws.take<float>(static_cast<size_t>(M) * R);
+  m.g_far = ws.take<float>(static_cast<size_t>(M) * R);
   m.g_rows = take_by_row(ws, m.slots, R);
   m.table = take_table(ws, m.slots, kSlotRows);
   m.row_waves = outer_row_waves(M, N, K, R, L);
@@ -429,15 +433,16 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
   const auto* dy = reinterpret_cast<const half_t*>(c.dy);
   run_plan(m.plan, st);
   run_shrink<true>(dy, reinterpret_cast<const half_t*>(c.b), m.plan, c.N, c.R, m.S, m.part, SlotTable{}, st);
-  const SplitTask th{c.h, 1, m.h.frags, m.h.units, nullptr, nullptr, nullptr};
-  const SplitTask tg{m.part, m.S, m.g.frags, m.g.units, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors, m.g_sum};
+  const SplitTask th{c.h, 1, m.h.frags, m.h.units, nullptr, nullptr, nullptr, nullptr, nullptr};
+  const SplitTask tg{m.part, m.S, m.g.frags, m.g.units, c.dx ? m.g_rows.frags : nullptr, m.g_rows.factors,
+                     m.g_rows.wide, nullptr, m.g_far};
   hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 2), dim3(512), 0, st, th, tg, c.scaling, m.table, m.plan, c.R);
   const bool whole = m.parts == 1;
   const OuterArgs ob = outer_args(Kept{dy, nullptr, nullptr, 0}, m.h, c.h, c.scaling, m.plan, whole ? c.db : m.db, c.N,
                                   c.R, m.parts, m.row_waves);
-  const OuterArgs oa = outer_args(kept, m.g, m.g_sum, c.scaling, m.plan, whole ? c.da : m.da, c.K, c.R, m.parts,
+  const OuterArgs oa = outer_args(kept, m.g, m.g_far, c.scaling, m.plan, whole ? c.da : m.da, c.K, c.R, m.parts,
                                   m.row_waves);
-  const StreamArgs dx = stream_args(m.g_rows, m.table, reinterpret_cast<const half_t*>(c.a),
+  const StreamArgs dx = stream_args(m.g_rows, m.g_far, c.scaling, m.table, reinterpret_cast<const half_t*>(c.a),
                                     reinterpret_cast<const half_t*>(c.dx0), reinterpret_cast<half_t*>(c.dx), c.K, c.R, c.L,
                                     m.slots, kBackwardBlocks);
   if (products_together(c.R)) {
@@ -499,9 +504,9 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
   run_plan(m.plan, st);
   run_shrink<false>(xh, ah, m.plan, K, R, m.S, m.part, m.stream ? SlotTable{} : m.table, st);
   if (m.stream) {
-    const SplitTask t{m.part, m.S, nullptr, nullptr, m.h.frags, m.h.factors, h};
+    const SplitTask t{m.part, m.S, nullptr, nullptr, m.h.frags, m.h.factors, m.h.wide, h, h ? nullptr : m.h_far};
     hipLaunchKernelGGL(lora_split_kernel, dim3(m.slots, 1), dim3(512), 0, st, t, t, scaling, m.table, m.plan, R);
-    run_stream<false, true>(stream_args(m.h, m.table, bh, yh, oh, N, R, L, m.slots, kForwardBlocks), st);
+    run_stream<false, true>(stream_args(m.h, h ? h : m.h_far, scaling, m.table, bh, yh, oh, N, R, L, m.slots, kForwardBlocks), st);
   } else {
     run_expand(m.part, m.S, m.table, m.slots, bh, scaling, L, yh, oh, h, N, R, st);
   }

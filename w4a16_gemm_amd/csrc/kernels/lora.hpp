@@ -12,10 +12,9 @@
 // with fp32 sums.  Every operand that comes from memory is binary16 and enters exactly; h
 // and g are fp32 sums and enter as two binary16 terms (hi + lo) after a division by a power of
 // two that brings the largest of them to [2^13, 2^14), so nothing overflows.  The two terms hold
-// a value to 2^-23 of itself as long as it lies within 2^15 of that largest one.  In the outer
-// products, where the largest is that of a rank in a slot of 32 rows, a slot with a smaller value
-// that the terms do not hold is multiplied in fp32.  In out and dx, where it is that of a row,
-// a smaller value is off by up to 2^-39 of the largest.
+// a value to 2^-23 of itself as long as it lies within 2^15 of that largest one: of a rank in a
+// slot of 32 rows in the outer products, of a row in out and dx.  A slot or 16 rows with a smaller
+// value that the terms do not hold are multiplied in fp32 (v_mfma_f32_16x16x4_f32).
 //
 // Rows are worked on in tiles of 16 to 128 rows of one adapter each; rows of one adapter are
 // found through a row plan (below), so any order of rows costs the same products.
@@ -596,19 +595,37 @@ __device__ __forceinline__ void load_expand_weights(const half_t* __restrict__ w
   }
 }
 
-// Products of one group of 16 rows with the weights.
-template <int F, int P, bool MANY>
-__device__ __forceinline__ void expand_products(const half8_t (&wf)[F][8], const half8_t (&hf)[F][P], float4_t (&acc)[8]) {
+// Products of one group of 16 rows with the weights, in fp32 (8 times the cycles): v holds this
+// lane's ranks of row r, in the order of its operands.
+template <int F, bool PACKED, bool MANY>
+__device__ __forceinline__ void expand_products_fp32(const half8_t (&wf)[F][8], const float (&v)[F][8], int lq,
+                                                     float4_t (&acc)[8]) {
 #pragma unroll
   for (int t = 0; t < 8; ++t) acc[t] = float4_t{};
 #pragma unroll
   for (int f = 0; f < F; ++f)
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+    for (int i = 0; i < 8; ++i) {   // step i: ranks 8 q + i of every quarter q
+      const float h = PACKED && lq >= 2 ? 0.0f : v[f][i];
 #pragma unroll
-      for (int t = 0; t < 8; ++t)
-        acc[t] = MANY ? __builtin_amdgcn_mfma_f32_16x16x32_f16(hf[f][p], wf[f][t], acc[t], 0, 0, 0)
-                      : __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[f][t], hf[f][p], acc[t], 0, 0, 0);
+      for (int t = 0; t < 8; ++t) {
+        const float w = PACKED && lq >= 2 ? 0.0f : static_cast<float>(wf[f][t][i]);
+        acc[t] = MANY ? __builtin_amdgcn_mfma_f32_16x16x4f32(h, w, acc[t], 0, 0, 0)
+                      : __builtin_amdgcn_mfma_f32_16x16x4f32(w, h, acc[t], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);   // one step's weights in registers at a time
+    }
+}
+
+// Products of one fragment of 16 rows with the weights, added to acc.
+template <int P, bool MANY>
+__device__ __forceinline__ void expand_products(const half8_t (&wf)[8], const half8_t (&hf)[P], float4_t (&acc)[8]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p)
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+      acc[t] = MANY ? __builtin_amdgcn_mfma_f32_16x16x32_f16(hf[p], wf[t], acc[t], 0, 0, 0)
+                    : __builtin_amdgcn_mfma_f32_16x16x32_f16(wf[t], hf[p], acc[t], 0, 0, 0);
 }
 
 // 8 consecutive results of a lane: row 4 q + u (many rows), run u (few rows).
@@ -622,10 +639,24 @@ __device__ __forceinline__ half8_t expand_result(const float4_t (&acc)[8], int u
   return o;
 }
 
-// Splits the ranks of a row held by the four lanes (r, 0 .. 3): operands, and the row's
-// factor s_i 2^e.
+// This lane's ranks of its row.
 template <int F, bool PACKED>
-__device__ __forceinline__ float split_row(const float (&v)[F][8], int lq, float si, half8_t (&hf)[F][PACKED ? 1 : 2]) {
+__device__ __forceinline__ void load_ranks(const float* row, int R, int lq, float (&v)[F][8]) {
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[f][j] = j0 < R ? row[j0 + j] : 0.0f;
+  }
+}
+
+// Few rows: 16 of them (row: that of lane (r, q), in LDS) with the weights.  Returns the factor
+// that acc is still to be multiplied with.
+template <int F, bool PACKED>
+__device__ __forceinline__ float split_and_expand(const half8_t (&wf)[F][8], const float* row, int R, int lq, float si,
+                                                  float4_t (&acc)[8]) {
+  float v[F][8];
+  load_ranks<F, PACKED>(row, R, lq, v);
   float top = 0.0f;
 #pragma unroll
   for (int f = 0; f < F; ++f)
@@ -634,16 +665,26 @@ __device__ __forceinline__ float split_row(const float (&v)[F][8], int lq, float
   top = fmaxf(top, __shfl_xor(top, 16));
   top = fmaxf(top, __shfl_xor(top, 32));
   const int shift = kSplitTop - top_exponent(top);
+  bool whole = true;
 #pragma unroll
-  for (int f = 0; f < F; ++f)
+  for (int t = 0; t < 8; ++t) acc[t] = float4_t{};
+#pragma unroll
+  for (int f = 0; f < F; ++f) {
+    half8_t hf[PACKED ? 1 : 2];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       half_t hi, lo;
-      split_half(v[f][j], shift, hi, lo);
-      hf[f][0][j] = PACKED && lq >= 2 ? lo : hi;
-      if constexpr (!PACKED) hf[f][1][j] = lo;
+      whole &= split_half(v[f][j], shift, hi, lo);
+      hf[0][j] = PACKED && lq >= 2 ? lo : hi;
+      if constexpr (!PACKED) hf[1][j] = lo;
     }
-  return __builtin_ldexpf(si, -shift);
+    expand_products<PACKED ? 1 : 2, false>(wf[f], hf, acc);
+  }
+  if (__all(whole)) return __builtin_ldexpf(si, -shift);
+  asm volatile("" ::: "memory");   // read again here, not held in registers meanwhile
+  load_ranks<F, PACKED>(row, R, lq, v);
+  expand_products_fp32<F, PACKED, false>(wf, v, lq, acc);
+  return si;
 }
 
 // --- split: h or g (the sum of S slices) as ready MFMA operands ---------------------------
@@ -660,7 +701,8 @@ __device__ __forceinline__ float split_row(const float (&v)[F][8], int lq, float
 //                     of row 16 g + r, in units of 2^e of that row, with factors[row of the
 //                     slot] = s_i 2^e; [slots][2][F][hi, lo][64][8].  R <= 16: one fragment
 //                     with hi of ranks 0 .. 15 in its first two quarters and lo in the
-//                     others; [slots][2][64][8]
+//                     others; [slots][2][64][8].  wide[slot][g][f] is 1 where a value is too far
+//                     below the largest of its row for two terms, else 0
 // Rows past the slot's count and ranks past R are zero.  A by-row task also writes the slot
 // table.  Where wanted, the summed h is written (0 for rows without an adapter).
 struct SplitTask {
@@ -670,7 +712,9 @@ struct SplitTask {
   float* units;      // [slots][16 NT]
   half_t* by_row;    // or NULL
   float* factors;    // [slots][32]
-  float* sum;        // [M][R] or NULL
+  uint8_t* wide;     // [slots][2][4]
+  float* sum;        // [M][R]: the summed h, or NULL
+  float* far;        // [M][R]: the same of the slots that are not whole, or NULL
 };
 
 // By-row operands (of 1 KB) of a row group.
@@ -705,6 +749,12 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
       *reinterpret_cast<float4_t*>(task.sum + static_cast<size_t>(rows[i / quads]) * R + 4 * (i % quads)) =
           sums[i / quads * ld + i % quads];
   const float* f = reinterpret_cast<const float*>(sums);
+  auto keep = [&] {   // by the wavefront that finds a value, for those that multiply in fp32
+    if (task.far)
+      for (int i = lane; i < tile.count * quads; i += 64)
+        *reinterpret_cast<float4_t*>(task.far + static_cast<size_t>(rows[i / quads]) * R + 4 * (i % quads)) =
+            sums[i / quads * ld + i % quads];
+  };
   if (task.by_rank) {
     const int NT = (R + 15) >> 4;
     for (int t = wave; t < NT; t += 8) {
@@ -733,6 +783,7 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
       const float unit = __builtin_ldexpf(1.0f, e);
       const bool all = __all(whole);
       if (lq == 0) task.units[(static_cast<size_t>(slot) * NT + t) * 16 + lr] = all ? unit : -unit;
+      if (!all) keep();
     }
   }
   if (!task.by_row) return;
@@ -757,11 +808,12 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
     const int m = 16 * g + lr;
     const int j0 = packed ? 8 * (lq & 1) : 32 * k + 8 * lq;
     const int shift = kSplitTop - top_exponent(row_top[m]);
+    bool whole = true;
     half8_t hi, lo;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       half_t a, b;
-      split_half(j0 < R ? f[m * 4 * ld + j0 + j] : 0.0f, shift, a, b);
+      whole &= split_half(j0 < R ? f[m * 4 * ld + j0 + j] : 0.0f, shift, a, b);
       hi[j] = packed && lq >= 2 ? b : a;
       lo[j] = b;
     }
@@ -772,6 +824,9 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
       o[2 * k * 64] = hi;
       o[(2 * k + 1) * 64] = lo;
     }
+    const bool all = __all(whole);
+    if (lane == 0) task.wide[slot * 8 + g * 4 + k] = all ? 0 : 1;
+    if (!all) keep();
   }
 }
 
@@ -786,12 +841,11 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
 // an adapter are copied, bit for bit.  h_out (not NULL): the workgroups of the first
 // channels write the summed h.
 template <int F, bool PACKED>
-__global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restrict__ h, int S, SlotTable table,
+__global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float* __restrict__ h, int S, SlotTable table,
                                                           const half_t* __restrict__ w,
                                                           const float* __restrict__ scaling, int L, const half_t* base,
                                                           half_t* out, float* __restrict__ h_out, int C, int R) {
   constexpr int kBlock = 512;   // channels per workgroup: 4 wavefronts x 128
-  constexpr int P = PACKED ? 1 : 2;
   __shared__ float4_t sums[sum_quads(kFewRows, 256)];
   const int slot = blockIdx.x;
   const int2 meta = table.meta[slot];
@@ -832,18 +886,9 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float* __restric
       *reinterpret_cast<float4_t*>(h_out + static_cast<size_t>(rows[i / quads]) * R + 4 * (i % quads)) =
           sums[i / quads * ld + i % quads];
   if (c0 >= C) return;
-  const float* hs = reinterpret_cast<const float*>(sums);
-  float v[F][8];
-#pragma unroll
-  for (int f = 0; f < F; ++f) {
-    const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[f][j] = j0 < R ? hs[lr * 4 * ld + j0 + j] : 0.0f;
-  }
-  half8_t hf[F][P];
-  const float factor = split_row<F, PACKED>(v, lq, scaling ? scaling[adapter] : 1.0f, hf);
+  const float* hs = reinterpret_cast<const float*>(sums) + lr * 4 * ld;
   float4_t acc[8];
-  expand_products<F, P, false>(wf, hf, acc);
+  const float factor = split_and_expand<F, PACKED>(wf, hs, R, lq, scaling ? scaling[adapter] : 1.0f, acc);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int c = c0 + 32 * u + 8 * lq;
@@ -864,7 +909,7 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
                                                          const float* __restrict__ scaling, RowPlan plan,
                                                          const half_t* base, half_t* out, float* __restrict__ h_out,
                                                          int K, int N, int R) {
-  constexpr int W = 8, NT = PACKED ? 1 : 2 * F, P = PACKED ? 1 : 2;
+  constexpr int W = 8, NT = PACKED ? 1 : 2 * F;
   constexpr int ld = 16 * NT + 4;   // floats per row of h
   __shared__ int32_t rows[kFewRows];
   __shared__ float4_t red[W / 2 * NT * 64];
@@ -912,18 +957,9 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
   if (h_out && block == 0)
     for (int i = tid; i < tile.count * R; i += 64 * W)
       h_out[static_cast<size_t>(rows[i / R]) * R + i % R] = hs[(i / R) * ld + i % R];
-  float v[F][8];
-#pragma unroll
-  for (int f = 0; f < F; ++f) {
-    const int j0 = PACKED ? (lq & 1) * 8 : 32 * f + 8 * lq;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[f][j] = j0 < R ? hs[lr * ld + j0 + j] : 0.0f;
-  }
   if (c0 >= N) return;
-  half8_t hf[F][P];
-  const float factor = split_row<F, PACKED>(v, lq, scaling ? scaling[tile.adapter] : 1.0f, hf);
   float4_t sums[8];
-  expand_products<F, P, false>(wf, hf, sums);
+  const float factor = split_and_expand<F, PACKED>(wf, hs + lr * ld, R, lq, scaling ? scaling[tile.adapter] : 1.0f, sums);
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int c = c0 + 32 * u + 8 * lq;
@@ -940,6 +976,9 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
 // registers and the operands and base values of the next D row groups in flight.  The
 // workgroups of one group of slots are neighbours, so an XCD's L2 holds few channels of w.
 // base may equal out, or be absent (BASE == false: 0); rows without an adapter are copied.
+// Groups of 16 rows that the split marked as wide (4% of a normally distributed h at rank 64) are
+// multiplied in fp32 at the end of their run, from the summed h: 29.4 -> 31.5 us for 2048 rows x
+// 14336 of eight adapters at rank 64, 94 -> 95 us for 4096 x 28672, against two terms for all.
 // out is written past the L2 (nobody reads it here): with plain stores 114 -> 99 us in the
 // example above, 94 us with these; 2048 rows x 14336 at rank 16 25.3 -> 19.6 us.
 template <int F, int P>
@@ -957,6 +996,9 @@ __device__ __forceinline__ void store_past_l2(half_t* p, half8_t v) {
 struct StreamArgs {
   const half_t* frags;
   const float* factors;
+  const uint8_t* wide;
+  const float* h;          // [M][R], summed
+  const float* scaling;
   SlotTable table;
   const half_t* w;
   const half_t* base;
@@ -985,6 +1027,9 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
   const int ns = min(group, slots - s0);
   // lane l: slot s0 + l
   const int2 meta = lane < ns ? table.meta[s0 + lane] : int2{-1, 0};
+  constexpr uint32_t kFrags = F == 4 ? ~0u : (1u << 8 * F) - 1u;   // the bytes that the split wrote
+  const uint2 far = lane < ns ? reinterpret_cast<const uint2*>(args.wide)[s0 + lane] : uint2{0, 0};
+  const int wide = ((far.x & kFrags) != 0 ? 1 : 0) | ((far.y & kFrags) != 0 ? 2 : 0);   // bit g: row group g
   half8_t wf[F][8];
 
   for (int i = 0; i < ns;) {
@@ -1023,15 +1068,20 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
         o.y[3] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.w) * C);
       }
     };
-    auto finish = [&](int g, const StreamRows<F, P>& o) {
-      float4_t acc[8];
-      expand_products<F, P, true>(wf, o.h, acc);
+    auto is_wide = [&](int g) { return (__builtin_amdgcn_readlane(wide, i + (g >> 1)) >> (g & 1) & 1) != 0; };
+    auto leave = [&](int g, const StreamRows<F, P>& o, const float4_t (&acc)[8], float4_t factor, int count) {
       const int rows[4] = {o.row.x, o.row.y, o.row.z, o.row.w};
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const half8_t v = expand_result<true>(acc, r, BASE ? o.y[r] : uint4{0, 0, 0, 0}, o.factor[r]);
-        if (c < C && 16 * g + 4 * lq + r < total) store_past_l2(out + static_cast<size_t>(rows[r]) * C + c, v);
+        const half8_t v = expand_result<true>(acc, r, BASE ? o.y[r] : uint4{0, 0, 0, 0}, factor[r]);
+        if (c < C && 16 * g + 4 * lq + r < count) store_past_l2(out + static_cast<size_t>(rows[r]) * C + c, v);
       }
+    };
+    auto finish = [&](int g, const StreamRows<F, P>& o) {
+      float4_t acc[8] = {};
+#pragma unroll
+      for (int f = 0; f < F; ++f) expand_products<P, true>(wf[f], o.h[f], acc);
+      leave(g, o, acc, o.factor, is_wide(g) ? 0 : total);   // wide ones leave below
     };
     // rows are looked up D groups ahead of their loads
     auto row_of = [&](int g) {
@@ -1063,6 +1113,27 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
 #pragma unroll
     for (int d = 0; d < D; ++d)
       if (g + d + D < n) finish(g + d + D, ring[d]);
+    // Row groups of the run in fp32.
+    for (uint64_t left = __ballot(lane >= i && lane < end && wide != 0); left; left &= left - 1) {
+      const int first = 2 * (__builtin_ctzll(left) - i);
+#pragma unroll 1
+      for (g = first; g < min(first + 2, n); ++g) {
+        if (!is_wide(g)) continue;
+        float v[F][8];
+        load_ranks<F, PACKED>(args.h + static_cast<size_t>(table.rows[(g0 + g) * 16 + lr]) * R, R, lq, v);
+        StreamRows<F, P> o;
+        load(g, row_of(g), o);
+        // the fp32 weights stay in here: kept for all groups they would not fit the registers
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int t = 0; t < 8; ++t) asm volatile("" : "+v"(wf[f][t]));
+        float4_t acc[8];
+        expand_products_fp32<F, PACKED, true>(wf, v, lq, acc);
+        const float si = args.scaling ? args.scaling[adapter] : 1.0f;
+        leave(g, o, acc, float4_t{si, si, si, si}, total);
+      }
+    }
     i = end;
   }
 }
