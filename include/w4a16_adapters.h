@@ -11,7 +11,9 @@
  *
  * Shapes: M rows, K input and N output channels, rank R, L adapters; M, K, N > 0,
  * K % 8 == 0, N % 8 == 0, R % 8 == 0, 8 <= R <= 128 (pad a smaller rank with zeros),
- * 1 <= L <= 65535, M <= 2^27, N and K <= 2^24.
+ * 1 <= L <= 65535, M <= 2^27, N and K <= 2^24.  Sizes whose launches would pass 2^32 threads
+ * are refused as well: the gradients of L adapters from L (N + K) of about 2^30 on (half of it
+ * for a rank above 32, and so on per 32 ranks), and rows and channels that no device holds.
  *   x, y, out       binary16 [M][K], [M][N], [M][N], row-major
  *   a               binary16 [L][R][K];  b  binary16 [L][N][R]
  *   index           int32 [M], adapter of every row, or NULL: adapter 0 for every row.  A
@@ -48,7 +50,7 @@ size_t w4a16_lora_forward_workspace(int M, int N, int K, int R, int L, int with_
  * A_i x within 2^-23 of itself between the two products, one rounding at the end.  Rows without an
  * adapter: out[m] = y[m], bit for bit.  out may be y (in place).  h: NULL, or where A_i x
  * is written for the backward pass.
- * Errors: INVALID_ARG (also a workspace that is too small), UNSUPPORTED (R, L),
+ * Errors: INVALID_ARG (also a workspace that is too small), UNSUPPORTED (R, L, sizes),
  * MISALIGNED, HIP. */
 int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const uint16_t* a, const uint16_t* b,
                        const int32_t* index, const float* scaling, int M, int N, int K, int R, int L,
@@ -75,7 +77,8 @@ int w4a16_lora_backward(const uint16_t* dy, const uint16_t* x, const uint16_t* a
 
 /* The same from a checkpoint of x in 8 bits (w4a16_act_quantize): x[m][k] is the value that
  * w4a16_act_dequantize restores, expanded in registers.  Bit-identical to
- * w4a16_lora_backward on the restored x.  group_size in {32, 64, 128}, K % group_size == 0.
+ * w4a16_lora_backward on the restored x.  group_size in {32, 64, 128}, K % group_size == 0,
+ * M K < 2^34.
  * codes are 8-byte aligned, scales 2-byte aligned. */
 int w4a16_lora_backward_q8(const uint16_t* dy, const uint8_t* codes, const uint16_t* scales, int group_size,
                            const uint16_t* a, const uint16_t* b, const float* h, const int32_t* index,

@@ -173,3 +173,36 @@ def test_missing_operands_are_refused():
     for name in ("dy", "x", "a", "b", "h"):
         with pytest.raises((TypeError, ValueError)):
             w4.w4a16_lora_backward(**dict(_backward_tensors(), **{name: None}))
+
+
+# Sizes within the bounds of every argument whose grids would pass 2^32 threads, or the int that
+# holds their workgroups: the output stream of the forward and of the input's gradient, and the
+# gradients of many adapters.  Too small a workspace keeps them off the device in any case.
+LARGE_FORWARD = [dict(M=1 << 27, N=1 << 24, K=8), dict(M=1 << 27, N=(1 << 24) - 8, K=64), dict(M=1 << 26, N=1 << 23, K=8, L=65535)]
+LARGE_BACKWARD = [dict(M=1 << 27, N=8, K=1 << 24), dict(M=1 << 27, N=64, K=(1 << 24) - 8), dict(M=64, N=1 << 20, K=8, L=65535)]
+
+
+@pytest.mark.parametrize("sizes", LARGE_FORWARD)
+def test_forward_refuses_grids_beyond_the_launch_limits(sizes):
+    lib = adapters._lib()
+    c = dict(FORWARD, **sizes, bytes=0, workspace=None)
+    assert lib.w4a16_lora_forward(*c.values()) == w4.ERR_UNSUPPORTED
+    assert lib.w4a16_lora_forward_workspace(c["M"], c["N"], c["K"], c["R"], c["L"], 1) == 0
+
+
+@pytest.mark.parametrize("sizes", LARGE_BACKWARD)
+def test_backward_refuses_grids_beyond_the_launch_limits(sizes):
+    lib = adapters._lib()
+    c = dict(BACKWARD, **sizes, bytes=0, workspace=None)
+    assert lib.w4a16_lora_backward(*c.values()) == w4.ERR_UNSUPPORTED
+    assert lib.w4a16_lora_backward_workspace(c["M"], c["N"], c["K"], c["R"], c["L"], 1) == 0
+
+
+def test_largest_grids_that_a_device_can_hold_are_taken():
+    """Operands of about 256 GB each, more than one GPU holds together.  (The gradients of many
+    adapters are bounded by L (N + K) < 2^30 besides.)"""
+    lib = adapters._lib()
+    for M, N, K, L in ((1 << 27, 1024, 8, 1), (8192, 1 << 24, 8, 1), (512, 1 << 18, 8, 65535), (1 << 27, 8, 1024, 65535)):
+        assert lib.w4a16_lora_forward_workspace(M, N, K, 8, L, 1) > 0, (M, N, K, L)
+    for M, N, K, L in ((1 << 27, 8, 1024, 1), (8192, 8, 1 << 24, 1), (512, 8, 1 << 13, 65535), (1 << 27, 1024, 8, 65535)):
+        assert lib.w4a16_lora_backward_workspace(M, N, K, 8, L, 1) > 0, (M, N, K, L)

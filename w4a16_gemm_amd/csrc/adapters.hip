@@ -44,9 +44,13 @@ int check_buffers(const Buffer (&bufs)[COUNT]) {
   return W4A16_OK;
 }
 
-// Bounds of the launch grids (their sizes in threads stay below 2^32).
+// Bounds on the sizes, which keep the launch grids below 2^32 threads but for those of the outer
+// products and of the stream.  These, of 256 threads per workgroup, are checked by
+// check_forward_shape and check_backward_shape: each may have half of what one launch takes.
+// (No device holds the operands of a stream that is refused.)
 constexpr int kMaxRows = 1 << 27;
 constexpr int kMaxChannels = 1 << 24;
+constexpr int64_t kMaxBlocks = int64_t{1} << 23;
 
 int check_lora_shape(int M, int N, int K, int R, int L) {
   if (M <= 0 || N <= 0 || K <= 0) return fail(W4A16_ERR_INVALID_ARG, "sizes must be positive: M=%d N=%d K=%d", M, N, K);
@@ -232,14 +236,21 @@ void run_fused(const half_t* x, const half_t* a, const half_t* b, const float* s
 // has to fill: 1024 (2500 rows of four adapters, K = N = 4096, rank 64: 25 us, with 512 29 us).
 constexpr int kForwardBlocks = 512, kBackwardBlocks = 1024;
 
-StreamArgs stream_args(const ByRow& f, const float* h, const float* scaling, const SlotTable& table, const half_t* w, const half_t* base, half_t* out, int C,
-                       int R, int L, int slots, int most) {
+int stream_group(int C, int slots, int most) {
   const int64_t all = static_cast<int64_t>(slots) * ceil_div(C, 512);
-  const int64_t group = std::max<int64_t>(1, std::min<int64_t>(64, (all + most - 1) / most));
-  return {f.frags, f.factors, f.wide, h, scaling, table, w, base, out, C, R, L, slots, static_cast<int>(group)};
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(64, (all + most - 1) / most)));
 }
 
-int stream_blocks(const StreamArgs& s) { return ceil_div(s.C, 512) * ceil_div(s.slots, s.group); }
+int64_t stream_blocks(int C, int slots, int group) {
+  return static_cast<int64_t>(ceil_div(C, 512)) * ceil_div(slots, group);
+}
+
+StreamArgs stream_args(const ByRow& f, const float* h, const float* scaling, const SlotTable& table, const half_t* w,
+                       const half_t* base, half_t* out, int C, int R, int L, int slots, int most) {
+  return {f.frags, f.factors, f.wide, h, scaling, table, w, base, out, C, R, L, slots, stream_group(C, slots, most)};
+}
+
+int stream_blocks(const StreamArgs& s) { return static_cast<int>(stream_blocks(s.C, s.slots, s.group)); }
 
 template <bool TRANS, bool BASE>
 void run_stream(const StreamArgs& s, hipStream_t st) {
@@ -320,6 +331,27 @@ void run_products(const OuterArgs& b, const OuterArgs& a, const StreamArgs& dx, 
   if (!dx.out) hipLaunchKernelGGL((lora_products_kernel<NT, F, Q8, false, false>), grid, block, 0, st, b, nb, a, na, dx);
   else if (!dx.base) hipLaunchKernelGGL((lora_products_kernel<NT, F, Q8, true, false>), grid, block, 0, st, b, nb, a, na, dx);
   else hipLaunchKernelGGL((lora_products_kernel<NT, F, Q8, true, true>), grid, block, 0, st, b, nb, a, na, dx);
+}
+
+// --- sizes --------------------------------------------------------------------------
+
+int check_stream(int M, int L, bool with_index, int C, int most) {
+  const int slots = plan_slots(M, L, with_index);
+  if (stream_blocks(C, slots, stream_group(C, slots, most)) > kMaxBlocks)
+    return fail(W4A16_ERR_UNSUPPORTED, "M=%d rows of %d adapters over %d channels are too many for one call", M, L, C);
+  return W4A16_OK;
+}
+
+int check_forward_shape(int M, int N, int K, int R, int L, bool with_index) {
+  if (int rc = check_lora_shape(M, N, K, R, L)) return rc;
+  return M > kInlineRows ? check_stream(M, L, with_index, N, kForwardBlocks) : W4A16_OK;
+}
+
+int check_backward_shape(int M, int N, int K, int R, int L, bool with_index) {
+  if (int rc = check_lora_shape(M, N, K, R, L)) return rc;
+  if (outer_groups(N, R, L, 4) + outer_groups(K, R, L, 4) >= kMaxBlocks)
+    return fail(W4A16_ERR_UNSUPPORTED, "gradients of %d adapters for N=%d, K=%d are too large for one call", L, N, K);
+  return check_stream(M, L, with_index, K, kBackwardBlocks);
 }
 
 // --- forward ------------------------------------------------------------------------
@@ -422,9 +454,6 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
                          {c.scaling, 4, false, "scaling"}, {c.workspace, 16, false, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   if (c.dx0 && !c.dx) return fail(W4A16_ERR_INVALID_ARG, "dx0 is given without dx");
-  // the only grid that the bounds on the sizes do not keep below 2^32 threads
-  if (outer_groups(c.N, c.R, c.L, 4) + outer_groups(c.K, c.R, c.L, 4) >= int64_t{1} << 23)
-    return fail(W4A16_ERR_UNSUPPORTED, "gradients of %d adapters for N=%d, K=%d are too large for one call", c.L, c.N, c.K);
   Carver size{nullptr}, ws{static_cast<unsigned char*>(c.workspace)};
   backward_memory(size, nullptr, c.index != nullptr, c.M, c.N, c.K, c.R, c.L);
   if (int rc = check_workspace(c.workspace, c.workspace_bytes, size.used)) return rc;
@@ -471,7 +500,7 @@ int run_backward(const BackwardArgs& c, const Kept& kept) {
 using namespace w4a16;
 
 extern "C" size_t w4a16_lora_forward_workspace(int M, int N, int K, int R, int L, int with_index) {
-  if (check_lora_shape(M, N, K, R, L) != W4A16_OK) return 0;
+  if (check_forward_shape(M, N, K, R, L, with_index != 0) != W4A16_OK) return 0;
   Carver size{nullptr};
   forward_memory(size, nullptr, with_index != 0, M, N, K, R, L);
   return size.used;
@@ -481,7 +510,7 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
                                   const int32_t* index, const float* scaling, int M, int N, int K, int R, int L,
                                   uint16_t* out, float* h, void* workspace, size_t workspace_bytes, void* stream) {
   begin_call();
-  if (int rc = check_lora_shape(M, N, K, R, L)) return rc;
+  if (int rc = check_forward_shape(M, N, K, R, L, index != nullptr)) return rc;
   const Buffer bufs[] = {{y, 16, true, "y"},           {x, 16, true, "x"},          {a, 16, true, "a"},
                          {b, 16, true, "b"},           {out, 16, true, "out"},      {h, 16, false, "h"},
                          {index, 4, false, "index"},   {scaling, 4, false, "scaling"},
@@ -514,7 +543,7 @@ extern "C" int w4a16_lora_forward(const uint16_t* y, const uint16_t* x, const ui
 }
 
 extern "C" size_t w4a16_lora_backward_workspace(int M, int N, int K, int R, int L, int with_index) {
-  if (check_lora_shape(M, N, K, R, L) != W4A16_OK) return 0;
+  if (check_backward_shape(M, N, K, R, L, with_index != 0) != W4A16_OK) return 0;
   Carver size{nullptr};
   backward_memory(size, nullptr, with_index != 0, M, N, K, R, L);
   return size.used;
@@ -525,7 +554,7 @@ extern "C" int w4a16_lora_backward(const uint16_t* dy, const uint16_t* x, const 
                                    int M, int N, int K, int R, int L, uint16_t* dx, float* da, float* db,
                                    void* workspace, size_t workspace_bytes, void* stream) {
   begin_call();
-  if (int rc = check_lora_shape(M, N, K, R, L)) return rc;
+  if (int rc = check_backward_shape(M, N, K, R, L, index != nullptr)) return rc;
   const Buffer bufs[] = {{x, 16, true, "x"}};
   if (int rc = check_buffers(bufs)) return rc;
   return run_backward<false>(
@@ -539,7 +568,7 @@ extern "C" int w4a16_lora_backward_q8(const uint16_t* dy, const uint8_t* codes, 
                                       uint16_t* dx, float* da, float* db, void* workspace, size_t workspace_bytes,
                                       void* stream) {
   begin_call();
-  if (int rc = check_lora_shape(M, N, K, R, L)) return rc;
+  if (int rc = check_backward_shape(M, N, K, R, L, index != nullptr)) return rc;
   if (int rc = check_act_shape(M, K, group_size)) return rc;
   const Buffer bufs[] = {{codes, 8, true, "codes"}, {scales, 2, true, "scales"}};
   if (int rc = check_buffers(bufs)) return rc;
