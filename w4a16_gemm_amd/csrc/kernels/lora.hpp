@@ -211,7 +211,8 @@ __device__ __forceinline__ int top_exponent(float m) { return m > 0.0f ? __built
 
 // v = h 2^shift as hi + lo in binary16.  An infinite or NaN h keeps it in hi alone.  Where lo
 // is subnormal it holds multiples of 2^-24: a v of at least 2^-2 is still within 2^-23 of itself.
-// Below, false is returned if anything is lost.
+// Below, false is returned if anything is lost.  Sums of like products hardly ever lose: what is small
+// beside the others is so by cancellation and has few bits (none of 128 slots of h or of g at rank 64).
 __device__ __forceinline__ bool split_half(float h, int shift, half_t& hi, half_t& lo) {
   const float v = __builtin_ldexpf(h, shift);
   hi = static_cast<half_t>(v);
@@ -836,12 +837,15 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
 // wavefronts takes one tile of 16 rows x 512 channels; h is summed into LDS by all of it
 // while the weights and base are on their way, and every wavefront splits it for itself.
 // Latency-bound: what counts is one launch less, and few loads that wait for another (16 rows
-// x 28672 of eight adapters at rank 16: 6.8 us).
+// x 28672 of eight adapters at rank 16: 6.8 us).  Two workgroups per compute unit up to rank 32 (256
+// rows x 11008 of 16 adapters at rank 16, whole forward: 18.4 us, without the bound 20.4 us); above, the
+// registers go to the loads (64 rows of 8 adapters at rank 128: 21.6 us, with the bound 25.4 us; 16
+// rows x 28672 at rank 64: 18.1 us, with it 19.8 us).
 // base may equal out (every element is read and written by the same lane); rows without
 // an adapter are copied, bit for bit.  h_out (not NULL): the workgroups of the first
 // channels write the summed h.
 template <int F, bool PACKED>
-__global__ __launch_bounds__(256, 2) void lora_expand_kernel(const float* __restrict__ h, int S, SlotTable table,
+__global__ __launch_bounds__(256, F == 1 ? 2 : 1) void lora_expand_kernel(const float* __restrict__ h, int S, SlotTable table,
                                                           const half_t* __restrict__ w,
                                                           const float* __restrict__ scaling, int L, const half_t* base,
                                                           half_t* out, float* __restrict__ h_out, int C, int R) {
@@ -976,9 +980,9 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
 // registers and the operands and base values of the next D row groups in flight.  The
 // workgroups of one group of slots are neighbours, so an XCD's L2 holds few channels of w.
 // base may equal out, or be absent (BASE == false: 0); rows without an adapter are copied.
-// Groups of 16 rows that the split marked as wide (4% of a normally distributed h at rank 64) are
-// multiplied in fp32 at the end of their run, from the summed h: 29.4 -> 31.5 us for 2048 rows x
-// 14336 of eight adapters at rank 64, 94 -> 95 us for 4096 x 28672, against two terms for all.
+// Groups of 16 rows that the split marked as wide are multiplied in fp32 at the end of their run,
+// from the summed h.  Where there are none, looking for them costs 29.4 -> 31.5 us for 2048 rows x
+// 14336 of eight adapters at rank 64, 94 -> 95 us for 4096 x 28672.
 // out is written past the L2 (nobody reads it here): with plain stores 114 -> 99 us in the
 // example above, 94 us with these; 2048 rows x 14336 at rank 16 25.3 -> 19.6 us.
 template <int F, int P>
@@ -1153,9 +1157,9 @@ __global__ __launch_bounds__(256, F <= 2 ? 2 : 1) void lora_stream_kernel(Stream
 // The products of a slot are summed from zero and join the sums in fp32, times the unit of their
 // slot and rank.  A slot whose operands are not whole (negative units; values that lie more than 2^16
 // apart within a rank and take more than two terms) is multiplied in fp32 instead, from the summed
-// h (8 times the MFMA cycles; 3% of the slots and blocks of 32 ranks of a normally distributed h):
-// training step 291 -> 294 us, backward of 2048 rows 40.1 -> 40.6 us, the other backward passes
-// within 1%, against scaling slots and ranks by one power of two for all of a slot.
+// h, at 8 times the MFMA cycles.  Where there are none: training step 291 -> 294 us, backward of 2048
+// rows 40.1 -> 40.6 us, the other backward passes within 1%, against one power of two for all ranks
+// of a slot and sums in units of the largest slot's.
 // A slot's missing rows repeat its first one against zero operands.
 // Q8: x is an 8-bit checkpoint, expanded after the transpose (which then moves bytes).
 // CMAJOR: gradient [L][C][R] (channels are MFMA rows), else [L][R][C].
