@@ -980,11 +980,12 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
 // registers and the operands and base values of the next D row groups in flight.  The
 // workgroups of one group of slots are neighbours, so an XCD's L2 holds few channels of w.
 // base may equal out, or be absent (BASE == false: 0); rows without an adapter are copied.
-// Groups of 16 rows that the split marked as wide are multiplied in fp32 at the end of their run,
-// from the summed h.  Where there are none, looking for them costs 29.4 -> 31.5 us for 2048 rows x
-// 14336 of eight adapters at rank 64, 94 -> 95 us for 4096 x 28672.
-// out is written past the L2 (nobody reads it here): with plain stores 114 -> 99 us in the
-// example above, 94 us with these; 2048 rows x 14336 at rank 16 25.3 -> 19.6 us.
+// Groups of 16 rows that the split marked as wide are multiplied in fp32 after all the others, from the
+// summed h.  Where there are none, looking for them costs 29.1 -> 29.5 us for 2048 rows x 14336 of
+// eight adapters at rank 64 (31.5 us with their products at the end of each run), 94.0 -> 94.7 us
+// for 4096 x 28672.
+// out is written past the L2 (nobody reads it here): with plain stores 4096 x 28672 took 99 us
+// against 94 us; 2048 rows x 14336 at rank 16 25.3 us against 19.6 us.
 template <int F, int P>
 struct StreamRows {
   uint4 y[4];
@@ -1034,7 +1035,25 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
   constexpr uint32_t kFrags = F == 4 ? ~0u : (1u << 8 * F) - 1u;   // the bytes that the split wrote
   const uint2 far = lane < ns ? reinterpret_cast<const uint2*>(args.wide)[s0 + lane] : uint2{0, 0};
   const int wide = ((far.x & kFrags) != 0 ? 1 : 0) | ((far.y & kFrags) != 0 ? 2 : 0);   // bit g: row group g
+  auto is_wide = [&](int i, int g) { return (__builtin_amdgcn_readlane(wide, i) >> g & 1) != 0; };
   half8_t wf[F][8];
+  auto load_base = [&](StreamRows<F, P>& o) {
+    if constexpr (BASE) {
+      const half_t* b = base + min(c, C - 8);
+      o.y[0] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(o.row.x) * C);
+      o.y[1] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(o.row.y) * C);
+      o.y[2] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(o.row.z) * C);
+      o.y[3] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(o.row.w) * C);
+    }
+  };
+  auto leave = [&](const StreamRows<F, P>& o, const float4_t (&acc)[8], float4_t factor, int count) {
+    const int rows[4] = {o.row.x, o.row.y, o.row.z, o.row.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const half8_t v = expand_result<true>(acc, r, BASE ? o.y[r] : uint4{0, 0, 0, 0}, factor[r]);
+      if (c < C && 4 * lq + r < count) store_past_l2(out + static_cast<size_t>(rows[r]) * C + c, v);
+    }
+  };
 
   for (int i = 0; i < ns;) {
     const int adapter = __builtin_amdgcn_readlane(meta.x, i);
@@ -1064,28 +1083,13 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
       for (int f = 0; f < F; ++f)
 #pragma unroll
         for (int p = 0; p < P; ++p) o.h[f][p] = f8[(f * P + p) * 64];
-      if constexpr (BASE) {
-        const half_t* b = base + min(c, C - 8);
-        o.y[0] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.x) * C);
-        o.y[1] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.y) * C);
-        o.y[2] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.z) * C);
-        o.y[3] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(row.w) * C);
-      }
-    };
-    auto is_wide = [&](int g) { return (__builtin_amdgcn_readlane(wide, i + (g >> 1)) >> (g & 1) & 1) != 0; };
-    auto leave = [&](int g, const StreamRows<F, P>& o, const float4_t (&acc)[8], float4_t factor, int count) {
-      const int rows[4] = {o.row.x, o.row.y, o.row.z, o.row.w};
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const half8_t v = expand_result<true>(acc, r, BASE ? o.y[r] : uint4{0, 0, 0, 0}, factor[r]);
-        if (c < C && 16 * g + 4 * lq + r < count) store_past_l2(out + static_cast<size_t>(rows[r]) * C + c, v);
-      }
+      load_base(o);
     };
     auto finish = [&](int g, const StreamRows<F, P>& o) {
       float4_t acc[8] = {};
 #pragma unroll
       for (int f = 0; f < F; ++f) expand_products<P, true>(wf[f], o.h[f], acc);
-      leave(g, o, acc, o.factor, is_wide(g) ? 0 : total);   // wide ones leave below
+      leave(o, acc, o.factor, (is_wide(i + (g >> 1), g & 1) ? 0 : total) - 16 * g);   // wide ones leave below
     };
     // rows are looked up D groups ahead of their loads
     auto row_of = [&](int g) {
@@ -1117,28 +1121,33 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
 #pragma unroll
     for (int d = 0; d < D; ++d)
       if (g + d + D < n) finish(g + d + D, ring[d]);
-    // Row groups of the run in fp32.
-    for (uint64_t left = __ballot(lane >= i && lane < end && wide != 0); left; left &= left - 1) {
-      const int first = 2 * (__builtin_ctzll(left) - i);
-#pragma unroll 1
-      for (g = first; g < min(first + 2, n); ++g) {
-        if (!is_wide(g)) continue;
-        float v[F][8];
-        load_ranks<F, PACKED>(args.h + static_cast<size_t>(table.rows[(g0 + g) * 16 + lr]) * R, R, lq, v);
-        StreamRows<F, P> o;
-        load(g, row_of(g), o);
-        // the fp32 weights stay in here: kept for all groups they would not fit the registers
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-          for (int t = 0; t < 8; ++t) asm volatile("" : "+v"(wf[f][t]));
-        float4_t acc[8];
-        expand_products_fp32<F, PACKED, true>(wf, v, lq, acc);
-        const float si = args.scaling ? args.scaling[adapter] : 1.0f;
-        leave(g, o, acc, float4_t{si, si, si, si}, total);
-      }
-    }
     i = end;
+  }
+
+  // Row groups in fp32 (weights read again, so that the loop above keeps its registers).
+  for (uint64_t left = __ballot(wide != 0 && meta.y > 0 && meta.x != L); left; left &= left - 1) {
+    const int i = __builtin_ctzll(left);
+    const int adapter = __builtin_amdgcn_readlane(meta.x, i);
+    load_expand_weights<F, PACKED, TRANS, true>(w + static_cast<size_t>(adapter) * R * C, c0, C, R, lane, wf);
+    const float si = args.scaling ? args.scaling[adapter] : 1.0f;
+#pragma unroll 1
+    for (int g = 0; g < 2; ++g) {
+      if (!is_wide(i, g)) continue;
+      const int32_t* rows = table.rows + (s0 + i) * kSlotRows + 16 * g;
+      StreamRows<F, P> o;
+      o.row = *reinterpret_cast<const int4*>(rows + 4 * lq);
+      load_base(o);
+      float v[F][8];
+      load_ranks<F, PACKED>(args.h + static_cast<size_t>(rows[lr]) * R, R, lq, v);
+      // converted anew for each group: in fp32 the weights would not fit the registers
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int t = 0; t < 8; ++t) asm volatile("" : "+v"(wf[f][t]));
+      float4_t acc[8];
+      expand_products_fp32<F, PACKED, true>(wf, v, lq, acc);
+      leave(o, acc, float4_t{si, si, si, si}, __builtin_amdgcn_readlane(meta.y, i) - 16 * g);
+    }
   }
 }
 
