@@ -141,6 +141,16 @@ int plan_slots(int M, int L, bool with_index) {
   return tile_slots(M, L, with_index, true, kSlotRows);
 }
 
+// The rules below take M / L for the rows per adapter, as if every one of the L adapters that are
+// passed had the same part of the rows: the index lies on the device.  Results do not depend on it,
+// times do where few of many adapters are used.  2048 rows, K = 4096, N = 14336, rank 16, all on one
+// adapter, forward / backward with dx: of 1 adapter 35 / 45 us, of 8 36 / 59 us, of 64 36 / 94 us, and
+// 16 adapters with nearly all rows on one 38 / 85 us; at rank 64 41 / 59, 41 / 74, 45 / 174 and 48 /
+// 113 us; 4096 rows, K = N = 1536, rank 16: of 1 23 / 35 us, of 64 23 / 121 us.  (The gradients of 64
+// adapters are 75 MB at rank 16 and 302 MB at rank 64 in the first shape, 15 and 60 us by
+// themselves.)  A caller that knows which adapters a batch uses passes those alone.  Without an
+// index the same figure is taken, so L = 1 is the call for one adapter.
+
 // --- shrink -------------------------------------------------------------------------
 
 // Rows per tile of a shrink, in 16s (wavefronts): 128 or 64 rows, once an adapter has that
@@ -153,8 +163,8 @@ int shrink_waves(int M, int L, int R, bool trans) {
 }
 
 // Slices of the long axis: a workgroup per compute unit (tiles of 16 rows: two), at least 256
-// channels each (tiles of 16 rows: 512), and sums of the slices that stay small (8 MB) or a
-// quarter of x.  A second workgroup on some compute units only makes the others wait (4096 rows
+// channels each (tiles of 16 rows: 512), and sums of the slices that stay small (8 MB) or an
+// eighth of x (as much again when they are read).  A second workgroup on some compute units only makes the others wait (4096 rows
 // x 28672 channels at rank 64: 50 us with 256, 52 us with 512; 2048 rows: 12 us with 256, 18 us
 // with 128).  With an index an adapter's last tile is half full on average.  A power of two, so
 // that a slice always falls to the same XCDs (8, in turn) and their L2 keeps its part of w (2048
