@@ -225,3 +225,39 @@ def test_input_gradients_of_ranks_far_apart(case):
     w4.w4a16_lora_backward(dev(d["dy"]), dev(d["x"]), dev(d["a"]), dev(d["b"]), dev(h), dev(d["index"]),
                            dev(d["scaling"]), dx=dx, out=dx)
     assert same(dx, got[0])
+
+
+def floored(d):
+    """Operands whose bounds count for subnormal ones.  A matrix instruction aligns its products by
+    their operands' exponents, in which every subnormal counts as 2^-14: the steps in which it sums
+    are 2^-24 of a product of operands of at least that size."""
+    out = dict(d)
+    for name in ("x", "a", "b", "dy"):
+        v = np.abs(d[name].astype(np.float64))
+        out[name] = np.where(v > 0, np.maximum(v, 2.0 ** -14), 0.0)
+    return out
+
+
+@pytest.mark.parametrize("case", [(9, 72, 24, 16, 2, "mixed", 0), (40, 136, 1544, 24, 1, "one", 0), (300, 264, 136, 40, 3, "mixed", 0.1),
+                                  (600, 72, 264, 72, 1, "one", 0)], ids=lambda c: "M{}-N{}-K{}-R{}-L{}-{}-{}".format(*c))
+def test_subnormal_operands(case):
+    """x, A, dy and B around and below 2^-14, down to the smallest binary16."""
+    import torch
+    note(f"lora range: subnormal {case}")
+    d = make(*case, seed=91)
+    rng = np.random.default_rng(92)
+    for name in ("x", "a", "b", "dy"):
+        d[name] = (rng.standard_normal(d[name].shape) * 2.0 ** -rng.integers(13, 24, d[name].shape)).astype(np.float16)
+    d["y"][:] = 0
+    d["scaling"][:] = 2.0 ** 20
+    f = floored(d)
+    ref, ref_h = oracle.lora_forward(d["y"], d["x"], d["a"], d["b"], d["index"], d["scaling"])
+    h = torch.empty(ref_h.shape, device=device())
+    out = forward(d, h=h)
+    _, h_mag = oracle.lora_forward(d["y"], f["x"], f["a"], f["b"], d["index"])
+    within("h", h, ref_h, 2 * d["x"].shape[1] * U * h_mag + 1e-45)
+    within("out", out, ref, forward_bound(f, ref))
+    h32 = h.cpu().numpy()
+    refs = oracle.lora_backward(d["dy"], d["x"], d["a"], d["b"], h32, d["index"], d["scaling"], d["dx0"])
+    for name, g, r, t in zip(("dx", "da", "db"), backward(d, h), refs, backward_bound(f, h32, refs)):
+        within(name, g, r, t)

@@ -9,7 +9,11 @@
 //   dB_i = s_i sum_m dy[m] h[m]^T,  dA_i = s_i sum_m g[m] x[m]^T       (outer)
 //
 // All of them are tall products with one side of R <= 128, on v_mfma_f32_16x16x32_f16
-// with fp32 sums.  Every operand that comes from memory is binary16 and enters exactly; h
+// with fp32 sums.  Every operand that comes from memory is binary16 and enters exactly.  (The
+// instruction aligns the products it adds by their operands' exponents, a subnormal operand
+// counting as 2^-14: measured, 2^-24 * 1 + 2^-24 * 2^-g comes out exact up to g = 14 and as 2^-24
+// above.  Sums of products of subnormal values thus have steps of 2^-24 of what the products would
+// be with operands of 2^-14.)  h
 // and g are fp32 sums and enter as two binary16 terms (hi + lo) after a division by a power of
 // two that brings the largest of them to [2^13, 2^14), so nothing overflows.  The two terms hold
 // a value to 2^-23 of itself as long as it lies within 2^15 of that largest one: of a rank in a
