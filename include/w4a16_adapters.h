@@ -29,10 +29,11 @@
  *                   streams) that may run at once need a workspace each.
  * Buffers must be 16-byte aligned (index and scaling: 4-byte aligned).  Outputs must not
  * overlap inputs or the workspace, but for the two pairs named below.  Results do not
- * depend on timing: every sum has a fixed order.  Sums of products are fp32 sums, except that an
- * operand x, a, b or dy below 2^-14 (subnormal) counts as 2^-14 in their rounding errors.  An infinity or a NaN in an operand makes the
- * results that it enters infinite or NaN (not always which of the two the formula gives), and
- * no others: rows keep to themselves, gradients to their adapter.
+ * depend on timing: every sum has a fixed order.  Sums of products are fp32 sums, except that
+ * an operand x, a, b or dy below 2^-14 (subnormal) counts as 2^-14 in their rounding errors.
+ * An infinity or a NaN in an operand makes the results that it enters infinite or NaN (not
+ * always which of the two the formula gives), and no others: rows keep to themselves,
+ * gradients to their adapter.
  */
 #ifndef W4A16_ADAPTERS_H
 #define W4A16_ADAPTERS_H

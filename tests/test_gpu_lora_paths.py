@@ -142,3 +142,39 @@ def test_refusals_on_the_device():
         at = ("dy", "x", "a", "b").index(name)
         with pytest.raises(TypeError):
             w4.w4a16_lora_backward(*bwd[:at], bwd[at].cpu(), *bwd[at + 1:])
+
+
+@pytest.mark.parametrize("M,K,R", [(14, 64, 16), (14, 64, 24), (14, 6152, 16), (30, 1544, 64), (30, 1544, 96), (300, 64, 16),
+                                   (300, 64, 32), (300, 64, 48), (300, 64, 72), (300, 64, 128)])
+def test_a_row_does_not_depend_on_rows_far_apart(M, K, R):
+    """Ranks 0 .. R - 2 read one half of the channels, the last rank the other half.  Every third
+    row has a tiny second half, so that its ranks lie 2^24 apart: the others keep their bits, in out
+    and (with the roles of A and B exchanged) in dx."""
+    import torch
+    N = 136
+    d = make(M, N, K, R, 1, "one", seed=77)
+    d["a"][0, :-1, K // 2:] = 0
+    d["a"][0, -1, :K // 2] = 0
+    far = np.arange(M) % 3 == 1
+    e = dict(d, x=d["x"].copy())
+    e["x"][far, :K // 2] *= np.float16(2.0 ** 10)
+    e["x"][far, K // 2:] *= np.float16(2.0 ** -14)
+    plain, other = w4.w4a16_lora_forward, {}
+    for name, c in (("d", d), ("e", e)):
+        h = torch.empty((M, R), device=device())
+        other[name] = (plain(dev(c["y"]), dev(c["x"]), dev(c["a"]), dev(c["b"]), None, dev(c["scaling"]), h=h), h)
+    assert same(other["d"][0][dev(~far)], other["e"][0][dev(~far)])
+    assert same(other["d"][1][dev(~far)], other["e"][1][dev(~far)])
+    h = np.abs(other["e"][1].cpu().numpy())
+    assert np.median(h[far, :-1].max(axis=1) / h[far, -1]) > 2.0 ** 20      # far apart indeed
+    # dx: the first half of dy's channels reaches all ranks but the last
+    d["b"] = np.zeros((1, N, R), np.float16)
+    d["b"][0, :N // 2, :-1] = make(1, N // 2, 8, R, 1, "one", seed=78)["b"][0][:, :-1]
+    d["b"][0, N // 2:, -1] = 0.5
+    e = dict(d, dy=d["dy"].copy())
+    e["dy"][far, :N // 2] *= np.float16(2.0 ** 10)
+    e["dy"][far, N // 2:] *= np.float16(2.0 ** -10)
+    h0 = torch.zeros((M, R), device=device())
+    got = [w4.w4a16_lora_backward(dev(c["dy"]), dev(c["x"]), dev(c["a"]), dev(c["b"]), h0, None, dev(c["scaling"]),
+                                  dx=dev(c["dx0"]))[0] for c in (d, e)]
+    assert same(got[0][dev(~far)], got[1][dev(~far)])

@@ -94,7 +94,7 @@ struct Carver {
 struct ByRow {
   half_t* frags;
   float* factors;
-  uint8_t* wide;
+  uint16_t* wide;
 };
 
 struct ByRank {
@@ -105,7 +105,7 @@ struct ByRank {
 ByRow take_by_row(Carver& ws, int slots, int R) {
   half_t* f = ws.take<half_t>(static_cast<size_t>(slots) * 2 * row_frags(R) * 512);
   float* factors = ws.take<float>(static_cast<size_t>(slots) * kSlotRows);
-  return {f, factors, ws.take<uint8_t>(static_cast<size_t>(slots) * 8)};
+  return {f, factors, ws.take<uint16_t>(static_cast<size_t>(slots) * 8)};
 }
 
 ByRank take_by_rank(Carver& ws, int slots, int R) {

@@ -13,12 +13,11 @@
 // instruction aligns the products it adds by their operands' exponents, a subnormal operand
 // counting as 2^-14: measured, 2^-24 * 1 + 2^-24 * 2^-g comes out exact up to g = 14 and as 2^-24
 // above.  Sums of products of subnormal values thus have steps of 2^-24 of what the products would
-// be with operands of 2^-14.)  h
-// and g are fp32 sums and enter as two binary16 terms (hi + lo) after a division by a power of
-// two that brings the largest of them to [2^13, 2^14), so nothing overflows.  The two terms hold
-// a value to 2^-23 of itself as long as it lies within 2^15 of that largest one: of a rank in a
-// slot of 32 rows in the outer products, of a row in out and dx.  A slot or 16 rows with a smaller
-// value that the terms do not hold are multiplied in fp32 (v_mfma_f32_16x16x4_f32).
+// be with operands of 2^-14.)  h and g are fp32 sums and enter as two binary16 terms (hi + lo)
+// after a division by a power of two that brings the largest of them to [2^13, 2^14), so nothing
+// overflows.  The two terms hold a value to 2^-23 of itself within 2^15 of that largest one: of a rank in a
+// slot of 32 rows in the outer products, of a row in out and dx.  A slot or row with a smaller value
+// that the terms do not hold is multiplied in fp32 (v_mfma_f32_16x16x4_f32).
 //
 // Rows are worked on in tiles of 16 to 128 rows of one adapter each; rows of one adapter are
 // found through a row plan (below), so any order of rows costs the same products.
@@ -655,6 +654,12 @@ __device__ __forceinline__ void load_ranks(const float* row, int R, int lq, floa
   }
 }
 
+// Of a ballot over lanes (r, q), the 16 rows r.
+__device__ __forceinline__ uint32_t wide_rows(uint64_t lanes) {
+  lanes |= lanes >> 32;
+  return static_cast<uint32_t>(lanes | lanes >> 16) & 0xFFFFu;
+}
+
 // Few rows: 16 of them (row: that of lane (r, q), in LDS) with the weights.  Returns the factor
 // that acc is still to be multiplied with.
 template <int F, bool PACKED>
@@ -685,11 +690,17 @@ __device__ __forceinline__ float split_and_expand(const half8_t (&wf)[F][8], con
     }
     expand_products<PACKED ? 1 : 2, false>(wf[f], hf, acc);
   }
-  if (__all(whole)) return __builtin_ldexpf(si, -shift);
+  const float factor = __builtin_ldexpf(si, -shift);
+  const uint64_t wide = __ballot(!whole);
+  if (!wide) return factor;
   asm volatile("" ::: "memory");   // read again here, not held in registers meanwhile
   load_ranks<F, PACKED>(row, R, lq, v);
-  expand_products_fp32<F, PACKED, false>(wf, v, lq, acc);
-  return si;
+  float4_t fp32[8];
+  expand_products_fp32<F, PACKED, false>(wf, v, lq, fp32);
+  const bool mine = wide_rows(wide) >> (threadIdx.x & 15) & 1;   // the others do not depend on them
+#pragma unroll
+  for (int t = 0; t < 8; ++t) acc[t] = mine ? fp32[t] : acc[t];
+  return mine ? si : factor;
 }
 
 // --- split: h or g (the sum of S slices) as ready MFMA operands ---------------------------
@@ -706,8 +717,8 @@ __device__ __forceinline__ float split_and_expand(const half8_t (&wf)[F][8], con
 //                     of row 16 g + r, in units of 2^e of that row, with factors[row of the
 //                     slot] = s_i 2^e; [slots][2][F][hi, lo][64][8].  R <= 16: one fragment
 //                     with hi of ranks 0 .. 15 in its first two quarters and lo in the
-//                     others; [slots][2][64][8].  wide[slot][g][f] is 1 where a value is too far
-//                     below the largest of its row for two terms, else 0
+//                     others; [slots][2][64][8].  Bit r of wide[slot][f][g]: row 16 g + r has a
+//                     value that two terms beside its largest one cannot hold
 // Rows past the slot's count and ranks past R are zero.  A by-row task also writes the slot
 // table.  Where wanted, the summed h is written (0 for rows without an adapter).
 struct SplitTask {
@@ -717,7 +728,7 @@ struct SplitTask {
   float* units;      // [slots][16 NT]
   half_t* by_row;    // or NULL
   float* factors;    // [slots][32]
-  uint8_t* wide;     // [slots][2][4]
+  uint16_t* wide;    // [slots][4][2]
   float* sum;        // [M][R]: the summed h, or NULL
   float* far;        // [M][R]: the same of the slots that are not whole, or NULL
 };
@@ -829,9 +840,9 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
       o[2 * k * 64] = hi;
       o[(2 * k + 1) * 64] = lo;
     }
-    const bool all = __all(whole);
-    if (lane == 0) task.wide[slot * 8 + g * 4 + k] = all ? 0 : 1;
-    if (!all) keep();
+    const uint32_t wide = wide_rows(__ballot(!whole));
+    if (lane == 0) task.wide[slot * 8 + k * 2 + g] = static_cast<uint16_t>(wide);
+    if (wide) keep();
   }
 }
 
@@ -849,10 +860,9 @@ __global__ __launch_bounds__(512) void lora_split_kernel(SplitTask t0, SplitTask
 // an adapter are copied, bit for bit.  h_out (not NULL): the workgroups of the first
 // channels write the summed h.
 template <int F, bool PACKED>
-__global__ __launch_bounds__(256, F == 1 ? 2 : 1) void lora_expand_kernel(const float* __restrict__ h, int S, SlotTable table,
-                                                          const half_t* __restrict__ w,
-                                                          const float* __restrict__ scaling, int L, const half_t* base,
-                                                          half_t* out, float* __restrict__ h_out, int C, int R) {
+__global__ __launch_bounds__(256, F == 1 ? 2 : 1) void lora_expand_kernel(
+    const float* __restrict__ h, int S, SlotTable table, const half_t* __restrict__ w, const float* __restrict__ scaling,
+    int L, const half_t* base, half_t* out, float* __restrict__ h_out, int C, int R) {
   constexpr int kBlock = 512;   // channels per workgroup: 4 wavefronts x 128
   __shared__ float4_t sums[sum_quads(kFewRows, 256)];
   const int slot = blockIdx.x;
@@ -984,8 +994,8 @@ __global__ __launch_bounds__(512) void lora_fused_kernel(const half_t* __restric
 // registers and the operands and base values of the next D row groups in flight.  The
 // workgroups of one group of slots are neighbours, so an XCD's L2 holds few channels of w.
 // base may equal out, or be absent (BASE == false: 0); rows without an adapter are copied.
-// Groups of 16 rows that the split marked as wide are multiplied in fp32 after all the others, from the
-// summed h.  Where there are none, looking for them costs 29.1 -> 29.5 us for 2048 rows x 14336 of
+// Rows that the split marked as wide are multiplied in fp32 after all the others, from the summed h
+// (in groups of 16, but stored alone: a row's result depends on its own values).  Where there are none, looking for them costs 29.1 -> 29.5 us for 2048 rows x 14336 of
 // eight adapters at rank 64 (31.5 us with their products at the end of each run), 94.0 -> 94.7 us
 // for 4096 x 28672.
 // out is written past the L2 (nobody reads it here): with plain stores 4096 x 28672 took 99 us
@@ -1005,7 +1015,7 @@ __device__ __forceinline__ void store_past_l2(half_t* p, half8_t v) {
 struct StreamArgs {
   const half_t* frags;
   const float* factors;
-  const uint8_t* wide;
+  const uint16_t* wide;
   const float* h;          // [M][R], summed
   const float* scaling;
   SlotTable table;
@@ -1036,10 +1046,9 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
   const int ns = min(group, slots - s0);
   // lane l: slot s0 + l
   const int2 meta = lane < ns ? table.meta[s0 + lane] : int2{-1, 0};
-  constexpr uint32_t kFrags = F == 4 ? ~0u : (1u << 8 * F) - 1u;   // the bytes that the split wrote
-  const uint2 far = lane < ns ? reinterpret_cast<const uint2*>(args.wide)[s0 + lane] : uint2{0, 0};
-  const int wide = ((far.x & kFrags) != 0 ? 1 : 0) | ((far.y & kFrags) != 0 ? 2 : 0);   // bit g: row group g
-  auto is_wide = [&](int i, int g) { return (__builtin_amdgcn_readlane(wide, i) >> g & 1) != 0; };
+  const uint4 far = lane < ns ? reinterpret_cast<const uint4*>(args.wide)[s0 + lane] : uint4{0, 0, 0, 0};
+  const uint32_t wide = far.x | (F > 1 ? far.y : 0) | (F > 2 ? far.z : 0) | (F > 3 ? far.w : 0);   // a bit per row
+  auto wide_of = [&](int i, int g) { return static_cast<uint32_t>(__builtin_amdgcn_readlane(wide, i)) >> (16 * g) & 0xFFFFu; };
   half8_t wf[F][8];
   auto load_base = [&](StreamRows<F, P>& o) {
     if constexpr (BASE) {
@@ -1050,14 +1059,16 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
       o.y[3] = *reinterpret_cast<const uint4*>(b + static_cast<size_t>(o.row.w) * C);
     }
   };
-  auto leave = [&](const StreamRows<F, P>& o, const float4_t (&acc)[8], float4_t factor, int count) {
+  auto leave = [&](const StreamRows<F, P>& o, const float4_t (&acc)[8], float4_t factor, uint32_t which) {   // a bit per row
     const int rows[4] = {o.row.x, o.row.y, o.row.z, o.row.w};
+    which = c < C ? which >> (4 * lq) : 0;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const half8_t v = expand_result<true>(acc, r, BASE ? o.y[r] : uint4{0, 0, 0, 0}, factor[r]);
-      if (c < C && 4 * lq + r < count) store_past_l2(out + static_cast<size_t>(rows[r]) * C + c, v);
+      if (which >> r & 1) store_past_l2(out + static_cast<size_t>(rows[r]) * C + c, v);
     }
   };
+  auto first_rows = [](int count) { return count < 16 ? (1u << count) - 1u : 0xFFFFu; };   // count > 0
 
   for (int i = 0; i < ns;) {
     const int adapter = __builtin_amdgcn_readlane(meta.x, i);
@@ -1093,7 +1104,7 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
       float4_t acc[8] = {};
 #pragma unroll
       for (int f = 0; f < F; ++f) expand_products<P, true>(wf[f], o.h[f], acc);
-      leave(o, acc, o.factor, (is_wide(i + (g >> 1), g & 1) ? 0 : total) - 16 * g);   // wide ones leave below
+      leave(o, acc, o.factor, first_rows(total - 16 * g) & ~wide_of(i + (g >> 1), g & 1));   // wide ones: below
     };
     // rows are looked up D groups ahead of their loads
     auto row_of = [&](int g) {
@@ -1128,7 +1139,7 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
     i = end;
   }
 
-  // Row groups in fp32 (weights read again, so that the loop above keeps its registers).
+  // Rows in fp32 (weights read again, so that the loop above keeps its registers).
   for (uint64_t left = __ballot(wide != 0 && meta.y > 0 && meta.x != L); left; left &= left - 1) {
     const int i = __builtin_ctzll(left);
     const int adapter = __builtin_amdgcn_readlane(meta.x, i);
@@ -1136,7 +1147,7 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
     const float si = args.scaling ? args.scaling[adapter] : 1.0f;
 #pragma unroll 1
     for (int g = 0; g < 2; ++g) {
-      if (!is_wide(i, g)) continue;
+      if (!wide_of(i, g)) continue;
       const int32_t* rows = table.rows + (s0 + i) * kSlotRows + 16 * g;
       StreamRows<F, P> o;
       o.row = *reinterpret_cast<const int4*>(rows + 4 * lq);
@@ -1150,7 +1161,7 @@ __device__ __forceinline__ void stream_rows(const StreamArgs& args, int block) {
         for (int t = 0; t < 8; ++t) asm volatile("" : "+v"(wf[f][t]));
       float4_t acc[8];
       expand_products_fp32<F, PACKED, true>(wf, v, lq, acc);
-      leave(o, acc, float4_t{si, si, si, si}, __builtin_amdgcn_readlane(meta.y, i) - 16 * g);
+      leave(o, acc, float4_t{si, si, si, si}, first_rows(__builtin_amdgcn_readlane(meta.y, i) - 16 * g) & wide_of(i, g));
     }
   }
 }
