@@ -42,6 +42,10 @@ What it computes, in plain numpy float64 (slow and obviously correct):
                      gradients in float64 (pinned by differences of the forward).
 * ``act_quantize`` / ``act_values``   activations in 8 bits per row and group, the
                      symmetric 8-bit scheme applied to activations.
+* ``route`` / ``experts_gemm`` / ``experts_combine`` and their ``_backward``   mixtures of
+                     experts of the layer and their gradients (pinned by differences).
+* ``head_loss`` / ``head_loss_backward``   softmax cross entropy over a quantised head and
+                     its gradient (pinned by differences).
 * ``layer_bytes`` / ``bits_per_weight``   storage cost of a packed layer.
 
 Pins (tests/test_oracle_*.py, run without a GPU): the S/2 round-trip bound,
@@ -64,6 +68,8 @@ from .packing import (pack_codes, unpack_codes, pack_zeros, unpack_zeros,
                       pack_codes8, unpack_codes8, pack_zeros8, unpack_zeros8)
 from .layer import dequant, dequant_fp16, linear, rel_err
 from .adapters import lora_forward, lora_backward, act_quantize, act_values
+from .experts import (route, route_backward, experts_gemm, experts_backward, experts_combine,
+                      experts_combine_backward, head_loss, head_loss_backward)
 from .storage import layer_bytes, bits_per_weight
 
 __all__ = [
@@ -74,5 +80,7 @@ __all__ = [
     "dequant", "dequant_fp16", "linear", "rel_err",
     "awq_search", "gptq_hessian", "gptq_quantize", "output_error",
     "lora_forward", "lora_backward", "act_quantize", "act_values",
+    "route", "route_backward", "experts_gemm", "experts_backward", "experts_combine", "experts_combine_backward",
+    "head_loss", "head_loss_backward",
     "layer_bytes", "bits_per_weight",
 ]

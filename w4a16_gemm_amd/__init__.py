@@ -487,3 +487,16 @@ from .adapters import (w4a16_act_dequantize, w4a16_act_quantize, w4a16_lora_back
 
 __all__ += ["w4a16_lora_forward", "w4a16_lora_backward", "w4a16_lora_backward_q8", "w4a16_act_quantize",
             "w4a16_act_dequantize"]
+
+
+# --- mixtures of experts (include/w4a16_experts.h) and the vocabulary head's loss (include/w4a16_head.h) ---
+
+from .experts import (w4a16_experts_backward, w4a16_experts_combine, w4a16_experts_combine_backward,  # noqa: E402
+                      w4a16_experts_gemm, w4a16_gemm_backward, w4a16_route, w4a16_route_backward,
+                      w8a16_experts_backward, w8a16_experts_gemm, w8a16_gemm_backward)
+from .head import (w4a16_head_loss, w4a16_head_loss_backward, w8a16_head_loss, w8a16_head_loss_backward)  # noqa: E402
+
+__all__ += ["w4a16_route", "w4a16_route_backward", "w4a16_experts_gemm", "w8a16_experts_gemm", "w4a16_experts_backward",
+            "w8a16_experts_backward", "w4a16_gemm_backward", "w8a16_gemm_backward", "w4a16_experts_combine",
+            "w4a16_experts_combine_backward", "w4a16_head_loss", "w8a16_head_loss", "w4a16_head_loss_backward",
+            "w8a16_head_loss_backward"]

@@ -10,6 +10,7 @@ temporary name and renamed into place, so a reader never sees half a file.
 
 from __future__ import annotations
 
+import concurrent.futures
 import os
 import shutil
 import subprocess
@@ -22,6 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libw4a16.so")
 PEAKS_LIB = os.path.join(HERE, "libw4a16_peaks.so")   # achievable-peak probes (bench only)
+
+SOURCES = ("host.cpp", "device.hip", "adapters.hip", "experts.hip", "head.hip")
 
 ARCH = "gfx950"
 DEVICE_FLAGS = [
@@ -53,14 +56,17 @@ def build(verbose: bool = False) -> str:
     hipcc = _hipcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     inc = ["-I", INCLUDE, "-I", CSRC]
-    host_o = os.path.join(BUILD_DIR, "host.o")
-    dev_o = os.path.join(BUILD_DIR, "device.o")
-    _run([hipcc, "-c", os.path.join(CSRC, "host.cpp"), *HOST_FLAGS, *inc, "-o", host_o], verbose)
-    _run([hipcc, "-c", "-x", "hip", os.path.join(CSRC, "device.hip"), *DEVICE_FLAGS, *inc, "-o", dev_o], verbose)
-    ada_o = os.path.join(BUILD_DIR, "adapters.o")
-    _run([hipcc, "-c", "-x", "hip", os.path.join(CSRC, "adapters.hip"), *DEVICE_FLAGS, *inc, "-o", ada_o], verbose)
+    def compile_one(source):
+        obj = os.path.join(BUILD_DIR, os.path.splitext(source)[0] + ".o")
+        kind = DEVICE_FLAGS if source.endswith(".hip") else HOST_FLAGS
+        lang = ["-x", "hip"] if source.endswith(".hip") else []
+        _run([hipcc, "-c", *lang, os.path.join(CSRC, source), *kind, *inc, "-o", obj], verbose)
+        return obj
+
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as pool:
+        objects = list(pool.map(compile_one, SOURCES))
     tmp = LIB + ".tmp"
-    _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", host_o, dev_o, ada_o, "-o", tmp], verbose)
+    _run([hipcc, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objects, "-o", tmp], verbose)
     os.replace(tmp, LIB)
     tmp = PEAKS_LIB + ".tmp"
     _run([hipcc, "-shared", "-fPIC", "-x", "hip", os.path.join(CSRC, "peaks.hip"), *DEVICE_FLAGS, *inc, "-o", tmp],

@@ -1,0 +1,424 @@
+// Entry points of the mixtures of experts (w4a16_experts.h): argument checks, kernel choice
+// and launches.  Every launch is asynchronous on the caller's stream; the only scratch
+// memory is the caller's workspace.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "entry.hpp"
+#include "kernels/experts.hpp"
+#include "kernels/route.hpp"
+#include "kernels/slots.hpp"
+#include "kernels/transposed.hpp"
+#include "w4a16_experts.h"
+
+namespace w4a16 {
+
+void run_plan(const SlotPlan& p, const int32_t* index, int S, int E, int limit, int height, bool fill, hipStream_t st) {
+  hipLaunchKernelGGL(plan_slots_kernel, dim3(1), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (E + 1), st, index, S,
+                     E, limit, height, fill ? 1 : 0, p);
+}
+
+void run_gather(const SlotPlan& p, const half_t* x, const int32_t* index, const Layers& l, int S, int T, half_t* out,
+                hipStream_t st) {
+  hipLaunchKernelGGL(gather_slots_kernel, dim3(S), dim3(256), 0, st, x, index, p, l, T, out);
+}
+
+void run_invert(const Layers& l, int E, int32_t* inverse, hipStream_t st) {
+  hipLaunchKernelGGL(invert_order_kernel, dim3(static_cast<unsigned>(ceil_div(l.K, 256)), E), dim3(256), 0, st, l, inverse);
+}
+
+namespace {
+
+template <int BITS>
+int launch_transposed(int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
+                      const SlotPlan& p, int n_begin, int n_end, int split_n, int splits, const TOut& to, hipStream_t st) {
+  auto kern = transposed_kernel<BITS>;
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), transposed_lds<BITS>());
+  if (int rc = lds_status(lds_ok)) return rc;
+  const dim3 grid(static_cast<unsigned>(up8(tiles * ceil_div(l.K, 256) * splits)));
+  hipLaunchKernelGGL(kern, grid, dim3(512), transposed_lds<BITS>(), st, a, a_rows, a_pitch, by_place ? 1 : 0, l, p, n_begin,
+                     n_end, split_n, splits, to);
+  return check_launch("transposed product launch");
+}
+
+}  // namespace
+
+int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
+                   const SlotPlan& p, int n_begin, int n_end, int split_n, int splits, const TOut& to, hipStream_t st) {
+  return bits == 4 ? launch_transposed<4>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, split_n, splits, to, st)
+                   : launch_transposed<8>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, split_n, splits, to, st);
+}
+
+namespace {
+
+constexpr int kUnits = 256;   // compute units
+
+int check_experts(int M, int T, int E, int N, int K, int group_size, int bits) {
+  if (M <= 0 || T <= 0) return fail(W4A16_ERR_INVALID_ARG, "M and T must be positive (M=%d T=%d)", M, T);
+  if (E < 1 || E > kMaxExperts) return fail(W4A16_ERR_UNSUPPORTED, "%d experts, not 1..%d", E, kMaxExperts);
+  if (static_cast<int64_t>(M) * T > kMaxSlots)
+    return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d: more than 2^27 slots", M, T);
+  return check_layer(N, K, group_size, bits);
+}
+
+// --- tile shapes ----------------------------------------------------------------------
+
+// Height of the full row tiles, and 64-column blocks of a column tile, for S slots over E
+// experts and `cols` output columns.  The groups' sizes are known on the device only; they
+// are taken as equal.  Cost of a tile against one of 256 x 256: half the rows 0.64, a quarter
+// 0.45 (the weights are expanded for fewer rows), 64 columns instead of 256 0.35 (the rows
+// are read for fewer columns); and the rounds that the tiles need over the compute units.
+struct TileShape {
+  int height, nb;
+};
+
+double tiles_of(int64_t S, int E, int height) {
+  const double used = static_cast<double>(std::min<int64_t>(E, S));
+  const double per = static_cast<double>(S) / used;
+  return used * std::max(1.0, static_cast<double>(ceil_div(static_cast<int64_t>(per + 0.999), height)));
+}
+
+double height_cost(int height) { return height == 256 ? 1.0 : height == 128 ? 0.64 : 0.45; }
+
+TileShape pick_shape(int64_t S, int E, int cols) {
+  TileShape best{256, 4};
+  double least = 1e300;
+  for (int height : {256, 128, 64})
+    for (int nb : {4, 1}) {
+      const double wgs = tiles_of(S, E, height) * ceil_div(cols, 64 * nb);
+      const double rounds = wgs > 8 * kUnits ? wgs / kUnits : static_cast<double>(ceil_div(static_cast<int64_t>(wgs), kUnits));
+      const double cost = rounds * height_cost(height) * (nb == 4 ? 1.0 : 0.35);
+      if (cost < 0.999 * least) least = cost, best = {height, nb};
+    }
+  return best;
+}
+
+// Height and contraction parts of the transposed product: tiles of 256 channels, and parts of
+// at least 512 outputs where the tiles leave compute units without work.
+struct SplitShape {
+  int height, splits, split_n;
+};
+
+SplitShape pick_split(int64_t S, int E, int N, int K) {
+  SplitShape best{256, 1, 0};
+  double least = 1e300;
+  for (int height : {256, 128, 64}) {
+    const double tiles = tiles_of(S, E, height) * ceil_div(K, 256);
+    for (int splits = 1; splits <= 16 && (splits == 1 || N / splits >= 512); ++splits) {
+      const double wgs = tiles * splits;
+      const double rounds = wgs > 8 * kUnits ? wgs / kUnits : static_cast<double>(ceil_div(static_cast<int64_t>(wgs), kUnits));
+      const double cost = rounds * height_cost(height) / splits * (1.0 + 0.02 * (splits - 1));
+      if (cost < 0.999 * least) least = cost, best = {height, splits, 0};
+    }
+  }
+  best.split_n = static_cast<int>(ceil_div(ceil_div(N, best.splits), 64) * 64);
+  best.splits = static_cast<int>(ceil_div(N, best.split_n));
+  return best;
+}
+
+// --- forward ----------------------------------------------------------------------------
+
+struct ForwardMemory {
+  SlotPlan plan;
+  half_t* gathered;
+};
+
+ForwardMemory forward_memory(Carver& ws, int64_t S, int E, int K, bool act, int height) {
+  ForwardMemory m;
+  m.plan = take_plan(ws, S, most_tiles(S, E, height));
+  m.gathered = act ? ws.take<half_t>(static_cast<size_t>(S) * K) : nullptr;
+  return m;
+}
+
+int check_forward(int M, int T, int E, int N, int K, bool act) {
+  const int64_t S = static_cast<int64_t>(M) * T;
+  if ((act ? S : M) * static_cast<int64_t>(K) >= kMaxElements)
+    return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d K=%d: 2^31 elements or more", M, T, K);
+  const TileShape shape = pick_shape(S, E, N);
+  if (most_tiles(S, E, shape.height) * ceil_div(N, 64 * shape.nb) > kMaxBlocks)
+    return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d N=%d: more tiles than one launch takes", M, T, N);
+  return W4A16_OK;
+}
+
+template <int NB, int BITS>
+int launch_forward(dim3 grid, hipStream_t st, const half_t* x, int x_rows, int gathered, int T, const Layers& l,
+                   const SlotPlan& plan, half_t* y) {
+  auto kern = experts_gemm_kernel<NB, BITS>;
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), experts_lds<BITS>());
+  if (int rc = lds_status(lds_ok)) return rc;
+  hipLaunchKernelGGL(kern, grid, dim3(512), experts_lds<BITS>(), st, x, x_rows, gathered, T, l, plan, y);
+  return check_launch("experts launch");
+}
+
+template <int BITS>
+int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                 const int32_t* g_idx, int group_size, const int32_t* index, int M, int T, int E, int N, int K,
+                 uint16_t* y, void* workspace, size_t workspace_bytes, void* stream) {
+  begin_call();
+  if (int rc = check_experts(M, T, E, N, K, group_size, BITS)) return rc;
+  const Buffer bufs[] = {{x, 16, true, "x"},          {qweight, 16, true, "qweight"}, {scales, 16, true, "scales"},
+                         {qzeros, 16, false, "qzeros"}, {index, 4, true, "index"},    {y, 16, true, "y"},
+                         {workspace, 16, true, "workspace"}};
+  if (int rc = check_buffers(bufs)) return rc;
+  const bool act = g_idx != nullptr;
+  if (int rc = check_forward(M, T, E, N, K, act)) return rc;
+  const int S = M * T;
+  const TileShape shape = pick_shape(S, E, N);
+  Carver ws{static_cast<unsigned char*>(workspace)};
+  const ForwardMemory mem = forward_memory(ws, S, E, K, act, shape.height);
+  if (workspace_bytes < ws.used)
+    return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.used);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const Layers l = make_layers(qweight, scales, qzeros, group_size, N, K, BITS, act);
+  run_plan(mem.plan, index, S, E, E, shape.height, true, st);
+  const half_t* hx = reinterpret_cast<const half_t*>(x);
+  if (act)
+    run_gather(mem.plan, hx, index, l, S, T, mem.gathered, st);
+  const dim3 grid(static_cast<unsigned>(up8(most_tiles(S, E, shape.height) * ceil_div(N, 64 * shape.nb))));
+  const half_t* rows = act ? mem.gathered : hx;
+  half_t* hy = reinterpret_cast<half_t*>(y);
+  if (shape.nb == 4) return launch_forward<4, BITS>(grid, st, rows, act ? S : M, act, T, l, mem.plan, hy);
+  return launch_forward<1, BITS>(grid, st, rows, act ? S : M, act, T, l, mem.plan, hy);
+}
+
+// --- backward ---------------------------------------------------------------------------
+
+struct BackwardMemory {
+  SlotPlan plan;
+  float* part;        // NULL: straight to dx
+  int32_t* inverse;   // act order
+};
+
+bool straight(int T, const SplitShape& s, bool act) { return T == 1 && s.splits == 1 && !act; }
+
+BackwardMemory backward_memory(Carver& ws, int64_t S, int T, int E, int K, bool act, const SplitShape& shape) {
+  BackwardMemory m;
+  m.plan = take_plan(ws, S, most_tiles(S, E, shape.height));
+  m.part = straight(T, shape, act) ? nullptr : ws.take<float>(static_cast<size_t>(shape.splits) * S * K);
+  m.inverse = act ? ws.take<int32_t>(static_cast<size_t>(E) * K) : nullptr;
+  return m;
+}
+
+int check_backward(int M, int T, int E, int N, int K) {
+  const int64_t S = static_cast<int64_t>(M) * T;
+  if (S * N >= kMaxElements) return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d N=%d: 2^31 elements or more", M, T, N);
+  const SplitShape shape = pick_split(S, E, N, K);
+  if (most_tiles(S, E, shape.height) * ceil_div(K, 256) * shape.splits > kMaxBlocks)
+    return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d K=%d: more tiles than one launch takes", M, T, K);
+  return W4A16_OK;
+}
+
+template <int BITS>
+int launch_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros, bool act,
+                    int group_size, const int32_t* index, const uint16_t* dx0, int M, int T, int E, int N, int K,
+                    uint16_t* dx, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int rc = check_backward(M, T, E, N, K)) return rc;
+  const int S = M * T;
+  const SplitShape shape = pick_split(S, E, N, K);
+  Carver ws{static_cast<unsigned char*>(workspace)};
+  const BackwardMemory mem = backward_memory(ws, S, T, E, K, act, shape);
+  if (workspace_bytes < ws.used)
+    return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.used);
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  const Layers l = make_layers(qweight, scales, qzeros, group_size, N, K, BITS, act);
+  run_plan(mem.plan, index, S, E, E, shape.height, mem.part == nullptr, st);
+  const half_t* h0 = reinterpret_cast<const half_t*>(dx0);
+  half_t* hx = reinterpret_cast<half_t*>(dx);
+  TOut to{};
+  if (mem.part)
+    to = {nullptr, nullptr, mem.part, static_cast<size_t>(S), 0};
+  else
+    to = {hx, h0, nullptr, 0, 0};
+  if (int rc = run_transposed(BITS, most_tiles(S, E, shape.height), reinterpret_cast<const half_t*>(dy), S, N, false, l,
+                              mem.plan, 0, N, shape.split_n, shape.splits, to, st))
+    return rc;
+  if (mem.part) {
+    if (act) run_invert(l, E, mem.inverse, st);
+    hipLaunchKernelGGL(sum_slots_kernel, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.splits, T,
+                       index, E, mem.inverse, K, h0, hx);
+  }
+  return check_launch("experts backward launch");
+}
+
+template <int BITS>
+int experts_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                     const int32_t* g_idx, int group_size, const int32_t* index, bool with_index, const uint16_t* dx0,
+                     int M, int T, int E, int N, int K, uint16_t* dx, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  begin_call();
+  if (int rc = check_experts(M, T, E, N, K, group_size, BITS)) return rc;
+  const Buffer bufs[] = {{dy, 16, true, "dy"},          {qweight, 16, true, "qweight"},
+                         {scales, 16, true, "scales"},  {qzeros, 16, false, "qzeros"},
+                         {index, 4, with_index, "index"}, {dx0, 16, false, "dx0"},
+                         {dx, 16, true, "dx"},          {workspace, 16, true, "workspace"}};
+  if (int rc = check_buffers(bufs)) return rc;
+  return launch_backward<BITS>(dy, qweight, scales, qzeros, g_idx != nullptr, group_size, index, dx0, M, T, E, N, K, dx,
+                               workspace, workspace_bytes, stream);
+}
+
+// --- routing ----------------------------------------------------------------------------
+
+int check_route(int logit_bits, int M, int E, int top_k) {
+  if (M <= 0 || top_k <= 0) return fail(W4A16_ERR_INVALID_ARG, "M and top_k must be positive (M=%d top_k=%d)", M, top_k);
+  if (logit_bits != 16 && logit_bits != 32) return fail(W4A16_ERR_UNSUPPORTED, "logits of %d bits, not 16 or 32", logit_bits);
+  if (E < 1 || E > kMaxExperts) return fail(W4A16_ERR_UNSUPPORTED, "%d experts, not 1..%d", E, kMaxExperts);
+  if (top_k > E) return fail(W4A16_ERR_INVALID_ARG, "top_k=%d of %d experts", top_k, E);
+  if (M > kMaxSlots) return fail(W4A16_ERR_UNSUPPORTED, "M=%d: at most 2^27 rows", M);
+  return W4A16_OK;
+}
+
+// Sixteen lanes per row up to 128 experts, a wavefront above.
+template <typename F>
+void by_experts(int M, int E, F launch) {
+  const auto blocks = [&](int lanes) { return dim3(static_cast<unsigned>(ceil_div(M, 256 / lanes))); };
+  if (E <= 16) launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{}, blocks(16));
+  else if (E <= 64) launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{}, blocks(16));
+  else if (E <= 128) launch(std::integral_constant<int, 16>{}, std::integral_constant<int, 8>{}, blocks(16));
+  else if (E <= 256) launch(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{}, blocks(64));
+  else launch(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{}, blocks(64));
+}
+
+int check_combine(int M, int T, int N) {
+  if (M <= 0 || T <= 0 || N <= 0) return fail(W4A16_ERR_INVALID_ARG, "sizes must be positive: M=%d T=%d N=%d", M, T, N);
+  if (N % 8 != 0) return fail(W4A16_ERR_INVALID_ARG, "N=%d is not a multiple of 8", N);
+  if (static_cast<int64_t>(M) * N >= int64_t{1} << 34 || static_cast<int64_t>(M) * T > kMaxSlots || N > kMaxOutputs)
+    return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d N=%d: too large for one launch", M, T, N);
+  return W4A16_OK;
+}
+
+}  // namespace
+}  // namespace w4a16
+
+using namespace w4a16;
+
+extern "C" {
+
+int w4a16_route(const void* logits, int logit_bits, int M, int E, int top_k, int renormalise, int32_t* index,
+                float* weights, void* stream) {
+  begin_call();
+  if (int rc = check_route(logit_bits, M, E, top_k)) return rc;
+  const Buffer bufs[] = {{logits, 4, true, "logits"}, {index, 4, true, "index"}, {weights, 4, true, "weights"}};
+  if (int rc = check_buffers(bufs)) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  by_experts(M, E, [&](auto lanes, auto per, dim3 grid) {
+    if (logit_bits == 16)
+      hipLaunchKernelGGL((route_kernel<lanes.value, per.value, half_t>), grid, dim3(256), 0, st,
+                         static_cast<const half_t*>(logits), M, E, top_k, renormalise != 0, index, weights);
+    else
+      hipLaunchKernelGGL((route_kernel<lanes.value, per.value, float>), grid, dim3(256), 0, st,
+                         static_cast<const float*>(logits), M, E, top_k, renormalise != 0, index, weights);
+  });
+  return check_launch("route launch");
+}
+
+int w4a16_route_backward(const float* dweights, const void* logits, int logit_bits, const int32_t* index,
+                         const float* weights, int M, int E, int top_k, int renormalise, void* dlogits, void* stream) {
+  begin_call();
+  if (int rc = check_route(logit_bits, M, E, top_k)) return rc;
+  const Buffer bufs[] = {{dweights, 4, true, "dweights"}, {logits, 4, true, "logits"},   {index, 4, true, "index"},
+                         {weights, 4, true, "weights"},   {dlogits, 4, true, "dlogits"}};
+  if (int rc = check_buffers(bufs)) return rc;
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  by_experts(M, E, [&](auto lanes, auto per, dim3 grid) {
+    if (logit_bits == 16)
+      hipLaunchKernelGGL((route_backward_kernel<lanes.value, per.value, half_t>), grid, dim3(256), 0, st, dweights,
+                         static_cast<const half_t*>(logits), index, weights, M, E, top_k, renormalise != 0,
+                         static_cast<half_t*>(dlogits));
+    else
+      hipLaunchKernelGGL((route_backward_kernel<lanes.value, per.value, float>), grid, dim3(256), 0, st, dweights,
+                         static_cast<const float*>(logits), index, weights, M, E, top_k, renormalise != 0,
+                         static_cast<float*>(dlogits));
+  });
+  return check_launch("route backward launch");
+}
+
+size_t w4a16_experts_gemm_workspace(int M, int T, int E, int N, int K, int act_order) {
+  const bool ok = check_experts(M, T, E, N, K, K, 4) == W4A16_OK && check_forward(M, T, E, N, K, act_order != 0) == W4A16_OK;
+  clear_error();
+  if (!ok) return 0;
+  Carver ws{nullptr};
+  const int64_t S = static_cast<int64_t>(M) * T;
+  forward_memory(ws, S, E, K, act_order != 0, pick_shape(S, E, N).height);
+  return ws.used;
+}
+
+int w4a16_experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                       const int32_t* g_idx, int group_size, const int32_t* index, int M, int T, int E, int N, int K,
+                       uint16_t* y, void* workspace, size_t workspace_bytes, void* stream) {
+  return experts_gemm<4>(x, qweight, scales, qzeros, g_idx, group_size, index, M, T, E, N, K, y, workspace,
+                         workspace_bytes, stream);
+}
+
+int w8a16_experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                       const int32_t* g_idx, int group_size, const int32_t* index, int M, int T, int E, int N, int K,
+                       uint16_t* y, void* workspace, size_t workspace_bytes, void* stream) {
+  return experts_gemm<8>(x, qweight, scales, qzeros, g_idx, group_size, index, M, T, E, N, K, y, workspace,
+                         workspace_bytes, stream);
+}
+
+size_t w4a16_experts_backward_workspace(int M, int T, int E, int N, int K, int act_order) {
+  const bool ok = check_experts(M, T, E, N, K, K, 4) == W4A16_OK && check_backward(M, T, E, N, K) == W4A16_OK;
+  clear_error();
+  if (!ok) return 0;
+  Carver ws{nullptr};
+  const int64_t S = static_cast<int64_t>(M) * T;
+  backward_memory(ws, S, T, E, K, act_order != 0, pick_split(S, E, N, K));
+  return ws.used;
+}
+
+int w4a16_experts_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                           const int32_t* g_idx, int group_size, const int32_t* index, const uint16_t* dx0, int M, int T,
+                           int E, int N, int K, uint16_t* dx, void* workspace, size_t workspace_bytes, void* stream) {
+  return experts_backward<4>(dy, qweight, scales, qzeros, g_idx, group_size, index, true, dx0, M, T, E, N, K, dx,
+                             workspace, workspace_bytes, stream);
+}
+
+int w8a16_experts_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                           const int32_t* g_idx, int group_size, const int32_t* index, const uint16_t* dx0, int M, int T,
+                           int E, int N, int K, uint16_t* dx, void* workspace, size_t workspace_bytes, void* stream) {
+  return experts_backward<8>(dy, qweight, scales, qzeros, g_idx, group_size, index, true, dx0, M, T, E, N, K, dx,
+                             workspace, workspace_bytes, stream);
+}
+
+int w4a16_gemm_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                        const int32_t* g_idx, int group_size, const uint16_t* dx0, int M, int N, int K, uint16_t* dx,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  return experts_backward<4>(dy, qweight, scales, qzeros, g_idx, group_size, nullptr, false, dx0, M, 1, 1, N, K, dx,
+                             workspace, workspace_bytes, stream);
+}
+
+int w8a16_gemm_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
+                        const int32_t* g_idx, int group_size, const uint16_t* dx0, int M, int N, int K, uint16_t* dx,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  return experts_backward<8>(dy, qweight, scales, qzeros, g_idx, group_size, nullptr, false, dx0, M, 1, 1, N, K, dx,
+                             workspace, workspace_bytes, stream);
+}
+
+int w4a16_experts_combine(const uint16_t* y, const float* weights, int M, int T, int N, uint16_t* out, void* stream) {
+  begin_call();
+  if (int rc = check_combine(M, T, N)) return rc;
+  const Buffer bufs[] = {{y, 16, true, "y"}, {weights, 4, true, "weights"}, {out, 16, true, "out"}};
+  if (int rc = check_buffers(bufs)) return rc;
+  const int64_t runs = static_cast<int64_t>(M) * (N / 8);
+  hipLaunchKernelGGL(combine_kernel, dim3(static_cast<unsigned>(ceil_div(runs, 256))), dim3(256), 0,
+                     static_cast<hipStream_t>(stream), reinterpret_cast<const half_t*>(y), weights, runs, T, N,
+                     reinterpret_cast<half_t*>(out));
+  return check_launch("combine launch");
+}
+
+int w4a16_experts_combine_backward(const uint16_t* dout, const uint16_t* y, const float* weights, int M, int T, int N,
+                                   uint16_t* dy, float* dweights, void* stream) {
+  begin_call();
+  if (int rc = check_combine(M, T, N)) return rc;
+  if (M > 1 << 23) return fail(W4A16_ERR_UNSUPPORTED, "M=%d: at most 2^23 rows", M);
+  const Buffer bufs[] = {{dout, 16, true, "dout"}, {y, 16, true, "y"}, {weights, 4, true, "weights"},
+                         {dy, 16, true, "dy"},     {dweights, 4, true, "dweights"}};
+  if (int rc = check_buffers(bufs)) return rc;
+  hipLaunchKernelGGL(combine_backward_kernel, dim3(M), dim3(256), 0, static_cast<hipStream_t>(stream),
+                     reinterpret_cast<const half_t*>(dout), reinterpret_cast<const half_t*>(y), weights, T, N,
+                     reinterpret_cast<half_t*>(dy), dweights);
+  return check_launch("combine backward launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,120 @@
+// Products grouped by expert: y[slot] = x[slot / T] W^_e^T on the large tile of gemm.hpp, a
+// workgroup per row tile of the plan and 256 (64 NB) output channels.
+//  * The rows of a tile lie anywhere in x: the loader's lane offsets are those of the rows
+//    of its slots, fixed over the K loop, so the gather costs nothing there.  Results go to
+//    the slots' rows of y.
+//  * A row's result does not depend on the other rows of its tile, and neither on the place
+//    of the row in it: the same bits whatever else is in the batch, for one tile height.
+//  * Tiles of 256 rows take the 16x16x32 product, smaller ones of 4-bit weights the 32x32x16
+//    product, as in the layer itself.
+#pragma once
+
+#include "gemm.hpp"
+#include "plan.hpp"
+
+namespace w4a16 {
+
+constexpr size_t kTileRowsLds = 2 * kBigBM * 4;   // the tile's slots and source rows, behind the ring
+
+template <int BITS>
+constexpr size_t experts_lds() { return static_cast<size_t>(kBigStages) * big_stage_bytes<BITS>() + kTileRowsLds; }
+
+// Loader of a tile whose rows are rows source[0 .. rows) of x (LDS), x_rows rows in all.
+template <int NB, int MB, int BITS>
+__device__ __forceinline__ BigLoader<NB, MB, BITS> rows_loader(const half_t* x, int x_rows, const Layers& l,
+                                                               unsigned char* smem, const int32_t* source, int rows,
+                                                               int n0, int n_end, int tid, int wave) {
+  using Loader = BigLoader<NB, MB, BITS>;
+  Loader ld(x, l.qw, l.scales, l.zeros, smem, x_rows, l.N, l.K, l.gshift, 0, n0, n_end, tid, wave);
+#pragma unroll
+  for (int i = 0; i < Loader::APT; ++i) {
+    const int c = (wave * Loader::APT + i) * 64 + (tid & 63);
+    const int row = c >> 3, slot = c & 7;
+    ld.a_off[i] = (static_cast<uint32_t>(source[min(row, rows - 1)]) * l.K + 8 * (slot ^ (row & 7))) * 2u;
+  }
+  return ld;
+}
+
+// Calls store(row, column, value) for every accumulator of a 16x16 tile; row inside the
+// tile, column from its first.
+template <int NB, int MB, class Store>
+__device__ __forceinline__ void each_value(const float4_t (&acc)[MB][NB], int tid, Store store) {
+  const int lane = tid & 63, wave = tid >> 6, wm = wave >> 2, wn = wave & 3, lr = lane & 15, lq = lane >> 4;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        store(wm * 16 * MB + 16 * mb + 4 * lq + r, wn * 16 * NB + 16 * nb + lr, acc[mb][nb][r]);
+}
+
+template <int NB, int MB, class Store>
+__device__ __forceinline__ void each_value32(const f32x16_t (&acc)[MB / 2][NB / 2], int tid, Store store) {
+  const int lane = tid & 63, wave = tid >> 6, wm = wave >> 2, wn = wave & 3, lc = lane & 31, lh = lane >> 5;
+#pragma unroll
+  for (int rb = 0; rb < MB / 2; ++rb)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+#pragma unroll
+      for (int cb = 0; cb < NB / 2; ++cb)
+        store(wm * 16 * MB + 32 * rb + 8 * (r >> 2) + 4 * lh + (r & 3), wn * 16 * NB + 32 * cb + lc, acc[rb][cb][r]);
+}
+
+template <int NB, int MB, int BITS>
+__device__ __forceinline__ void experts_tile(const half_t* x, int x_rows, const Layers& l, half_t* y, unsigned char* smem,
+                                             const int32_t* source, const int32_t* slots, int rows, int n0) {
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const auto ld = rows_loader<NB, MB, BITS>(x, x_rows, l, smem, source, rows, n0, l.N, tid, wave);
+  const int N = l.N;
+  auto store = [&](int row, int col, float v) {
+    if (row < rows && n0 + col < N) y[static_cast<size_t>(slots[row]) * N + n0 + col] = static_cast<half_t>(v);
+  };
+  if constexpr (MB < 8 && BITS == 4 && NB % 2 == 0) {
+    f32x16_t acc[MB / 2][NB / 2];
+    big_tile32_product<NB, MB>(ld, l.zeros, smem, l.K, l.gshift, tid, wave, 1, acc);
+    each_value32<NB, MB>(acc, tid, store);
+  } else {
+    float4_t acc[MB][NB];
+    big_tile_product<NB, MB, BITS>(ld, l.zeros, smem, l.K, l.gshift, tid, wave, 1, acc);
+    each_value<NB, MB>(acc, tid, store);
+  }
+}
+
+// gathered: x holds the valid slots' rows in the plan's order (act order), else row m of x
+// is that of slots [m T, (m + 1) T).
+template <int NB, int BITS>
+__global__ __launch_bounds__(512) void experts_gemm_kernel(const half_t* __restrict__ x, int x_rows, int gathered, int T,
+                                                           Layers layers, SlotPlan plan, half_t* __restrict__ y) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int BN = 64 * NB;
+  const int tid = threadIdx.x, N = layers.N;
+  RowTile tile;
+  int col;
+  if (!find_tile(plan, (N + BN - 1) / BN, blockIdx.x, tile, col)) return;
+  int32_t* slots = reinterpret_cast<int32_t*>(smem + experts_lds<BITS>() - kTileRowsLds);
+  int32_t* source = slots + kBigBM;
+  if (tid < tile.rows) {
+    const int s = plan.order[tile.first + tid];
+    slots[tid] = s;
+    source[tid] = gathered ? tile.first + tid : s / T;
+  }
+  __syncthreads();
+  const int n0 = col * BN;
+  if (tile.expert < 0) {   // slots without an expert
+    const int cols = min(BN, N - n0);
+    for (int i = tid; i < tile.rows * (cols / 8); i += 512)
+      *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slots[i / (cols / 8)]) * N + n0 + i % (cols / 8) * 8) = half8_t{};
+    return;
+  }
+  const Layers l = layers.at<BITS>(tile.expert);
+  if (tile.height == 256)
+    experts_tile<NB, 8, BITS>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
+  else if (tile.height == 128)
+    experts_tile<NB, 4, BITS>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
+  else
+    experts_tile<NB, 2, BITS>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
+}
+
+}  // namespace w4a16

@@ -1,0 +1,389 @@
+// Products through the frozen weights the other way: dx[row] = sum_n dy[row][n] W^[n][k],
+// straight from the packed codes, which lie along k while the contraction runs along n.
+//
+// A workgroup of 8 wavefronts (2 along the rows x 4 along k) takes a tile of BM = 32 MB
+// rows by 256 channels k, the contraction in tiles of 64 outputs n through a 3-stage LDS
+// ring filled by direct-to-LDS loads two tiles ahead, as in the forward tile:
+//  * dy: BM rows of 8 chunks of 8 outputs, chunk j of row r at slot j ^ (r % 8);
+//  * codes: 64 rows n of 256 channels, as they lie in memory, in 8 chunks of 8 rows; a
+//    chunk is followed by 32 bytes (64 at 8 bits) of padding, so that the four chunks that
+//    one MFMA operand reads lie in distinct banks;
+//  * scales and zero points of the groups of the tile's eight 32-channel columns.
+// The transposition costs one v_perm per two words.  Lane (r, q) of a wavefront reads, for
+// the 8 outputs n of chunk j = 4 s + q of MFMA step s, the word of its channels: 4 bits: the
+// channels [8 (r % 8), +8) of the wavefront's 64, of which lanes r < 8 take the even ones and
+// the others the odd ones.  Even channels sit in the low half of a word and odd ones in the
+// high half (nibbles.hpp), so one v_perm of the words of outputs n and n + 1 gives a register
+// whose nibble i holds the codes of channel 2 i (+ 1) for both outputs, and the same masks as
+// in the forward product turn it into pairs along n.  Block i = 0..3 of the wavefront then has
+// the channels 8 (r % 8) + 2 i + r / 8.  8 bits: lane r takes the word of channels
+// [4 r, +4), one v_perm per pair and channel; block i has the channels 4 r + i.
+// The weights are binary16((q - Z) S), the values of the forward product.
+// VALU work per MFMA is that of the forward product plus the v_perm and the zero points'
+// constants, which here change with every output n instead of staying with the lane.
+#pragma once
+
+#include "experts.hpp"
+
+namespace w4a16 {
+
+template <int BITS>
+struct TStage {
+  static constexpr uint32_t ROW = 256 * BITS / 8;                 // code bytes of a row
+  static constexpr uint32_t CHUNK = 8 * ROW + (BITS == 4 ? 32 : 64);
+  static constexpr uint32_t A = kBigBM * 64 * 2;
+  static constexpr uint32_t C = 8 * CHUNK;
+  static constexpr uint32_t S = 8 * 64 * 2;                       // [column / 32][output]
+  static constexpr uint32_t Z = BITS == 4 ? 256 : 1024;           // [column / 32][output], 64 lanes' loads
+  static constexpr uint32_t BYTES = A + C + S + Z;
+  static_assert(BYTES % 16 == 0, "stage alignment");
+};
+
+template <int BITS>
+constexpr size_t transposed_lds() { return 3 * static_cast<size_t>(TStage<BITS>::BYTES) + kTileRowsLds; }
+
+// Loads of one tile: rows source[0 .. rows) of a [a_rows][a_pitch] from column a0 on against
+// the outputs [n_begin, n_end) and the channels from k0 on.
+template <int MB, int BITS>
+struct TLoader {
+  using L = TStage<BITS>;
+  static constexpr int APT = 32 * MB / 64;   // activation chunks (16 B) per thread and stage
+  static constexpr int CL = BITS / 4;        // code loads per thread and stage
+
+  __amdgpu_buffer_rsrc_t ar, qr;
+  const half_t* s_ptr;      // this lane's scales of tile 0 (wavefront 0)
+  const uint32_t* z_ptr;    // this lane's zero points of tile 0 (wavefront 1)
+  unsigned char* smem;
+  int KT, wave, s_step, z_step, s_tail, z_tail;
+  uint32_t a_off[APT], b_off[CL], b_tail[CL], b_step;
+
+  __device__ __forceinline__ TLoader(const half_t* a, int a_rows, int a_pitch, int a0, const Layers& l, int n_begin,
+                                     int n_end, int k0, const int32_t* source, int rows, unsigned char* smem_, int tid,
+                                     int wave_)
+      : smem(smem_), KT((n_end - n_begin + 63) / 64), wave(wave_) {
+    const int lane = tid & 63;
+    const uint32_t pitch = static_cast<uint32_t>(l.K) * BITS / 8;   // code bytes of a row
+    ar = __builtin_amdgcn_make_buffer_rsrc(const_cast<half_t*>(a + a0), 0,
+                                           static_cast<int>((static_cast<uint32_t>(a_rows) * a_pitch - a0) * 2u),
+                                           kBufferWord3);
+    const size_t first = static_cast<size_t>(n_begin) * pitch;
+    qr = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<unsigned char*>(const_cast<uint32_t*>(l.qw)) + first, 0,
+        static_cast<int>(static_cast<uint32_t>(n_end - n_begin) * pitch), kBufferWord3);
+#pragma unroll
+    for (int i = 0; i < APT; ++i) {
+      const int c = (wave * APT + i) * 64 + lane;
+      const int row = c >> 3, slot = c & 7;
+      a_off[i] = (static_cast<uint32_t>(source[min(row, rows - 1)]) * a_pitch + 8 * (slot ^ (row & 7))) * 2u;
+    }
+    // Codes: load i of wavefront w fills rows 8 w .. (4 bits: 8 rows, 8 bits: 4 rows each),
+    // 16 bytes per lane; channels past K re-read the row's last ones, outputs past the end
+    // the last one (their dy is masked).
+    constexpr int PIECES = L::ROW / 16;
+    const int last = static_cast<int>((n_end - n_begin - 1) % 64);   // last output of the last tile
+#pragma unroll
+    for (int i = 0; i < CL; ++i) {
+      const int row = 8 * wave + (i * 64 + lane) / PIECES, piece = lane % PIECES;
+      const uint32_t col = min(static_cast<uint32_t>(k0) * BITS / 8 + 16 * piece, pitch - 16);
+      b_off[i] = static_cast<uint32_t>(row) * pitch + col;
+      b_tail[i] = static_cast<uint32_t>(min(row, last)) * pitch + col;
+    }
+    b_step = 64 * pitch;
+    // Scales: lane = 8 (column / 32) + piece of 8 outputs.  Zero points: 4 bits, lane = 8
+    // (column / 32) + word of 8 outputs; 8 bits, lane = 4 (column / 32) + piece of 16 outputs
+    // (the upper lanes fill 512 bytes behind them again).
+    auto group = [&](int c32) { return min(k0 + 32 * c32, l.K - 1) >> l.gshift; };
+    const int sp = 8 * (lane & 7);
+    s_ptr = l.scales + static_cast<size_t>(group(lane >> 3)) * l.N + n_begin + sp;
+    s_step = 64;
+    s_tail = min(sp, last / 8 * 8) - sp;
+    constexpr int ZP = BITS == 4 ? 8 : 16;   // outputs per zero-point load of a lane
+    const int zl = BITS == 4 ? lane : lane & 31;
+    const int zp = ZP * (zl % (64 / ZP));
+    const size_t z_at = (static_cast<size_t>(group(zl / (64 / ZP))) * l.N + n_begin + zp) / (32 / BITS);
+    z_ptr = l.zeros.words + (l.zeros.sym ? 0 : z_at);
+    z_step = l.zeros.sym ? 0 : 64 / (32 / BITS);
+    z_tail = l.zeros.sym ? 0 : (min(zp, last / ZP * ZP) - zp) / (32 / BITS);
+  }
+
+  // Tile t to stage t % 3; tiles past the end re-load the last one.  The scale and zero-point
+  // loads come first: waiting for tile t never waits for more than those of tile t + 1.
+  __device__ __forceinline__ void load(int t) const {
+    unsigned char* stage = smem + (t % 3) * L::BYTES;
+    const int tc = min(t, KT - 1);
+    const bool tail = tc == KT - 1;
+    if (wave == 0)
+      __builtin_amdgcn_global_load_lds(
+          reinterpret_cast<const void*>(s_ptr + static_cast<ptrdiff_t>(tc) * s_step + (tail ? s_tail : 0)),
+          reinterpret_cast<void*>(stage + L::A + L::C), 16, 0, 0);
+    else if (wave == 1) {
+      const uint32_t* z = z_ptr + static_cast<ptrdiff_t>(tc) * z_step + (tail ? z_tail : 0);
+      if constexpr (BITS == 4)
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z),
+                                         reinterpret_cast<void*>(stage + L::A + L::C + L::S), 4, 0, 0);
+      else
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z),
+                                         reinterpret_cast<void*>(stage + L::A + L::C + L::S), 16, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < APT; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, as_lds(stage + (wave * APT + i) * 1024), 16,
+                                               static_cast<int>(a_off[i]), tc * 128, 0, 0);
+#pragma unroll
+    for (int i = 0; i < CL; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, as_lds(stage + L::A + wave * L::CHUNK + i * 1024), 16,
+                                               static_cast<int>(tail ? b_tail[i] : b_off[i]),
+                                               static_cast<int>(static_cast<uint32_t>(tc) * b_step), 0, 0);
+  }
+};
+
+// (zero point of output 2 p, of output 2 p + 1) as 16-bit halves, p = 0..3.
+__device__ __forceinline__ void zero_pairs4(uint32_t word, uint32_t (&z)[4]) {
+  const uint32_t even = word & 0x0F0F0F0Fu, odd = (word >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) z[p] = __builtin_amdgcn_perm(odd, even, 0x0c000c00u | p | ((4u + p) << 16));
+}
+
+__device__ __forceinline__ uint32_t perm_bytes(uint32_t hi, uint32_t lo, uint32_t sel) {
+  return __builtin_amdgcn_perm(hi, lo, sel);
+}
+
+// acc[mb][i]: rows 16 mb + 4 q + reg of the wavefront's 16 MB, block i of its channels.
+template <int MB, int BITS>
+__device__ __forceinline__ void transposed_product(const TLoader<MB, BITS>& ld, Zeros zeros, unsigned char* smem,
+                                                   int outputs, int tid, int wave, float4_t (&acc)[MB][4]) {
+  using L = TStage<BITS>;
+  constexpr int INFLIGHT = TLoader<MB, BITS>::APT + TLoader<MB, BITS>::CL;
+  const int lane = tid & 63;
+  const int wm = wave >> 2, wn = wave & 3;
+  const int lr = lane & 15, lq = lane >> 4;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[mb][i] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+  const uint32_t a_lane = (wm * 16 * MB + lr) * 128;
+  const uint32_t c_lane = L::A + lq * L::CHUNK + (BITS == 4 ? wn * 8 + (lr & 7) : wn * 16 + lr) * 4;
+  const int c32 = 2 * wn + (BITS == 4 ? (lr & 7) >> 2 : lr >> 3);   // column / 32 of this lane's channels
+  const uint32_t s_lane = L::A + L::C + c32 * 128 + lq * 16;
+  const uint32_t z_lane = L::A + L::C + L::S + c32 * (8 * BITS) + lq * BITS;
+  const uint32_t half_sel = lr & 8 ? 0x07060302u : 0x05040100u;   // high or low halves of two words
+  const int last = outputs - (ld.KT - 1) * 64;                    // outputs of the last tile
+
+  ld.load(0);
+  ld.load(1);
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(INFLIGHT) : "memory");
+  block_barrier();
+
+  for (int t = 0; t < ld.KT; ++t) {
+    ld.load(t + 2);
+    const unsigned char* st = smem + (t % 3) * L::BYTES;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i] = *reinterpret_cast<const uint32_t*>(st + c_lane + s * 4 * L::CHUNK + i * L::ROW);
+      const uint4 sv = *reinterpret_cast<const uint4*>(st + s_lane + 64 * s);
+      const uint32_t sc[4] = {sv.x, sv.y, sv.z, sv.w};
+      uint32_t z[4];
+      if constexpr (BITS == 4) {
+        zero_pairs4(zeros.word(*reinterpret_cast<const uint32_t*>(st + z_lane + 16 * s)), z);
+      } else {
+        const uint2 zw = *reinterpret_cast<const uint2*>(st + z_lane + 32 * s);
+        const uint32_t z0 = zeros.word8(zw.x), z1 = zeros.word8(zw.y);
+        z[0] = perm_bytes(0, z0, 0x0c010c00u), z[1] = perm_bytes(0, z0, 0x0c030c02u);
+        z[2] = perm_bytes(0, z1, 0x0c010c00u), z[3] = perm_bytes(0, z1, 0x0c030c02u);
+      }
+      half8_t af[MB];
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+        af[mb] = *reinterpret_cast<const half8_t*>(st + a_lane + 16 * ((4 * s + lq) ^ (lr & 7)) + 2048 * mb);
+      if (t == ld.KT - 1 && 8 * (4 * s + lq) >= last) {   // outputs past the end: nothing of dy there
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) af[mb] = half8_t{};
+      }
+      uint32_t b[4][4];   // [block][pair of outputs]
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const half2_t n1024 = as_h2(z[p] | 0xE400E400u), scale = as_h2(sc[p]);
+        if constexpr (BITS == 4) {
+          const half2_t n64 = as_h2((z[p] << 4) | 0xD400D400u);
+          const half2_t sixteenth = half2_t{static_cast<half_t>(0.0625f), static_cast<half_t>(0.0625f)};
+          const uint32_t v = perm_bytes(w[2 * p + 1], w[2 * p], half_sel);
+          const uint32_t u = v >> 8;
+          b[0][p] = __builtin_bit_cast(uint32_t, (as_h2(and_or(v, 0x000F000Fu, kMagic)) + n1024) * scale);
+          b[1][p] = __builtin_bit_cast(
+              uint32_t, __builtin_elementwise_fma(as_h2(and_or(v, 0x00F000F0u, kMagic)), sixteenth, n64) * scale);
+          b[2][p] = __builtin_bit_cast(uint32_t, (as_h2(and_or(u, 0x000F000Fu, kMagic)) + n1024) * scale);
+          b[3][p] = __builtin_bit_cast(
+              uint32_t, __builtin_elementwise_fma(as_h2(and_or(u, 0x00F000F0u, kMagic)), sixteenth, n64) * scale);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {   // element i of a word is its byte 0, 2, 1, 3
+            const uint32_t byte = i == 1 ? 2 : i == 2 ? 1 : i;
+            const uint32_t v = perm_bytes(w[2 * p + 1], w[2 * p], 0x0c000c00u | byte | ((4 + byte) << 16));
+            b[i][p] = __builtin_bit_cast(uint32_t, (as_h2(v | kMagic) + n1024) * scale);
+          }
+        }
+      }
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[mb][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+              af[mb], __builtin_bit_cast(half8_t, uint4{b[i][0], b[i][1], b[i][2], b[i][3]}), acc[mb][i], 0, 0, 0);
+      __builtin_amdgcn_s_setprio(0);
+    }
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(INFLIGHT) : "memory");
+    block_barrier();
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// Calls store(row, channel, v0..v7 or v0..v3) with consecutive channels: row inside the
+// tile, channel from the tile's first.  4 bits: lanes r and r + 8 hold the even and the odd
+// channels of the same eight; each gives the other two of its four rows.
+template <int MB, int BITS, class Store>
+__device__ __forceinline__ void each_run(const float4_t (&acc)[MB][4], int tid, Store store) {
+  const int lane = tid & 63, wave = tid >> 6, wm = wave >> 2, wn = wave & 3, lr = lane & 15, lq = lane >> 4;
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const int row0 = wm * 16 * MB + 16 * mb + 4 * lq;
+    if constexpr (BITS == 4) {
+      const bool odd = (lr & 8) != 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float keep = odd ? acc[mb][i][2 + h] : acc[mb][i][h];
+          const float give = odd ? acc[mb][i][h] : acc[mb][i][2 + h];
+          const float got = __builtin_bit_cast(
+              float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, give), 0x128, 0xF, 0xF, true));   // lane r ^ 8
+          v[2 * i] = odd ? got : keep;
+          v[2 * i + 1] = odd ? keep : got;
+        }
+        store(row0 + (odd ? 2 : 0) + h, wn * 64 + 8 * (lr & 7), v);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float v[4] = {acc[mb][0][r], acc[mb][1][r], acc[mb][2][r], acc[mb][3][r]};
+        store(row0 + r, wn * 64 + 4 * lr, v);
+      }
+    }
+  }
+}
+
+template <int MB, int BITS>
+__device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int a_pitch, int a0, const Layers& l,
+                                                int n_begin, int n_end, int k0, const int32_t* source,
+                                                const int32_t* target, int rows, const TOut& to, int split,
+                                                unsigned char* smem) {
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const TLoader<MB, BITS> ld(a, a_rows, a_pitch, a0, l, n_begin, n_end, k0, source, rows, smem, tid, wave);
+  float4_t acc[MB][4];
+  transposed_product<MB, BITS>(ld, l.zeros, smem, n_end - n_begin, tid, wave, acc);
+  const int K = l.K;
+  constexpr int RUN = BITS == 4 ? 8 : 4;
+  each_run<MB, BITS>(acc, tid, [&](int row, int col, const float* v) {
+    if (row >= rows || k0 + col >= K) return;
+    if (to.out) {
+      typedef _Float16 run_t __attribute__((ext_vector_type(RUN)));
+      const size_t at = static_cast<size_t>(target[row]) * K + k0 + col;
+      run_t d{}, o;
+      if (to.dx0) d = *reinterpret_cast<const run_t*>(to.dx0 + at);
+#pragma unroll
+      for (int i = 0; i < RUN; ++i) o[i] = static_cast<half_t>(v[i] + static_cast<float>(d[i]));
+      *reinterpret_cast<run_t*>(to.out + at) = o;
+    } else {
+      float4_t* p = reinterpret_cast<float4_t*>(to.part + (split * to.part_rows + target[row]) * K + k0 + col);
+#pragma unroll
+      for (int i = 0; i < RUN / 4; ++i) {
+        float4_t s = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+        if (to.add) s += p[i];
+        p[i] = s;
+      }
+    }
+  });
+}
+
+// a [a_rows][a_pitch]: by_place: row p belongs to place p of the plan's order, else row s to
+// slot s.  The outputs [n_begin, n_end) against columns [0, n_end - n_begin) of a, in
+// `splits` parts of `split_n` outputs (a multiple of 64).  Sums go to the places or slots
+// alike.
+template <int BITS>
+__global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restrict__ a, int a_rows, int a_pitch,
+                                                         int by_place, Layers layers, SlotPlan plan, int n_begin,
+                                                         int n_end, int split_n, int splits, TOut to) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, K = layers.K;
+  RowTile tile;
+  int col;
+  const int tiles_k = (K + 255) / 256;
+  if (!find_tile(plan, tiles_k * splits, blockIdx.x, tile, col)) return;
+  const int split = col / tiles_k, k0 = col % tiles_k * 256;
+  int32_t* rows = reinterpret_cast<int32_t*>(smem + transposed_lds<BITS>() - kTileRowsLds);
+  if (tid < tile.rows) rows[tid] = by_place ? tile.first + tid : plan.order[tile.first + tid];
+  __syncthreads();
+  if (tile.expert < 0) {   // slots without an expert: dx0 alone (only with one part and T == 1)
+    const int runs = min(256, K - k0) / 8;
+    for (int i = tid; i < tile.rows * runs; i += 512) {
+      const size_t at = static_cast<size_t>(rows[i / runs]) * K + k0 + i % runs * 8;
+      *reinterpret_cast<half8_t*>(to.out + at) = to.dx0 ? *reinterpret_cast<const half8_t*>(to.dx0 + at) : half8_t{};
+    }
+    return;
+  }
+  const Layers l = layers.at<BITS>(tile.expert);
+  const int a0 = split * split_n, n0 = n_begin + a0, n1 = min(n_end, n0 + split_n);
+  if (tile.height == 256)
+    transposed_tile<8, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, rows, tile.rows, to, split, smem);
+  else if (tile.height == 128)
+    transposed_tile<4, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, rows, tile.rows, to, split, smem);
+  else
+    transposed_tile<2, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, rows, tile.rows, to, split, smem);
+}
+
+// Partial sums part[split][slot][K] of the slots [m T, (m + 1) T) -> dx[m], in a fixed
+// order, plus dx0, rounded once.  Slots without an expert have no sums.  inverse (act
+// order): stored position of every channel of every expert.
+__global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict__ part, size_t slots, int splits, int T,
+                                                        const int32_t* __restrict__ index, int E,
+                                                        const int32_t* __restrict__ inverse, int K,
+                                                        const half_t* __restrict__ dx0, half_t* __restrict__ out) {
+  const size_t m = blockIdx.x;
+  for (int k = 8 * threadIdx.x; k < K; k += 8 * 256) {
+    float s[8] = {};
+    if (dx0) {
+      const half8_t d = *reinterpret_cast<const half8_t*>(dx0 + m * K + k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[i] = static_cast<float>(d[i]);
+    }
+    for (int t = 0; t < T; ++t) {
+      const size_t slot = m * T + t;
+      const int e = index ? index[slot] : 0;
+      if (e < 0 || e >= E) continue;
+      for (int p = 0; p < splits; ++p) {
+        const float* row = part + (p * slots + slot) * K;
+        if (inverse) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            s[i] += row[min(static_cast<uint32_t>(inverse[static_cast<size_t>(e) * K + k + i]), static_cast<uint32_t>(K - 1))];
+        } else {
+          const float4_t lo = *reinterpret_cast<const float4_t*>(row + k), hi = *reinterpret_cast<const float4_t*>(row + k + 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] += lo[i], s[4 + i] += hi[i];
+        }
+      }
+    }
+    half8_t o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = static_cast<half_t>(s[i]);
+    *reinterpret_cast<half8_t*>(out + m * K + k) = o;
+  }
+}
+
+}  // namespace w4a16
