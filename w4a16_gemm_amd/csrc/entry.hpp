@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "internal.hpp"
 #include "kernels/plan.hpp"
 
@@ -92,12 +94,51 @@ Layers make_layers(const int32_t* qweight, const uint16_t* scales, const int32_t
 // Row tiles that S slots of E experts can need, one more expert for the slots without one.
 int64_t most_tiles(int64_t S, int E, int height) { return S / height + (E + 1 < S ? E + 1 : S); }
 
-SlotPlan take_plan(Carver& ws, int64_t S, int64_t tiles) {
+SlotPlan take_plan(Carver& ws, int64_t S, int64_t tiles, bool tile_of) {
   SlotPlan p;
+  p.tile_of = tile_of ? ws.take<int32_t>(S) : nullptr;
   p.counts = ws.take<int32_t>(2);
   p.order = ws.take<int32_t>(S);
   p.tiles = ws.take<RowTile>(tiles);
   return p;
+}
+
+// --- tile shapes ------------------------------------------------------------------------
+
+constexpr int kUnits = 256;   // compute units
+
+// Cost of a row tile against one of 256 rows: the weights are expanded for fewer rows.
+double height_cost(int height) { return height == 256 ? 1.0 : height == 128 ? 0.64 : 0.45; }
+
+// Row tiles of S slots over E experts, whose sizes are known on the device only: taken as
+// equal, with half a tile more for each where there is more than one.
+double tiles_of(int64_t S, int E, int height) {
+  if (E == 1) return static_cast<double>(ceil_div(S, height));
+  const double used = static_cast<double>(E < S ? E : S);
+  const double per = static_cast<double>(S) / used / height;
+  return used * (per <= 0.7 ? 1.0 : per + 0.5);
+}
+
+// Height of the full row tiles and the most parts of a tile of the transposed product (see
+// Pieces): parts of at least 512 outputs, partial sums of at most 512 MB.
+struct TransposedShape {
+  int height, most;
+};
+
+TransposedShape pick_transposed(int64_t S, int E, int outputs, int K) {
+  const int64_t fit = (int64_t{512} << 20) / (4 * S * K);
+  TransposedShape best{256, 1};
+  best.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({int64_t{16}, fit, outputs / 512})));
+  double least = 1e300;
+  for (int height : {256, 128, 64}) {
+    const int64_t chunk = ceil_div(static_cast<int64_t>(tiles_of(S, E, height) * ceil_div(K, 256) + 0.999), 8);
+    const int64_t rest = chunk % 32;
+    double tail = rest ? 1.0 : 0.0;
+    for (int f = 2; f <= best.most && f * rest <= 64; ++f) tail = std::min(tail, static_cast<double>(ceil_div(rest * f, 32)) / f + 0.02 * f);
+    const double cost = (static_cast<double>(chunk / 32) + tail) * height_cost(height);
+    if (cost < 0.999 * least) least = cost, best.height = height;
+  }
+  return best;
 }
 
 int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
@@ -124,6 +165,6 @@ void run_gather(const SlotPlan& p, const half_t* x, const int32_t* index, const 
 void run_invert(const Layers& l, int E, int32_t* inverse, hipStream_t st);
 // The transposed product over at most `tiles` row tiles; arguments as transposed_kernel.
 int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                   const SlotPlan& p, int n_begin, int n_end, int split_n, int splits, const TOut& to, hipStream_t st);
+                   const SlotPlan& p, int n_begin, int n_end, int n_most, int most, const TOut& to, hipStream_t st);
 
 }  // namespace w4a16

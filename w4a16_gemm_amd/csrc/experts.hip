@@ -32,27 +32,25 @@ namespace {
 
 template <int BITS>
 int launch_transposed(int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                      const SlotPlan& p, int n_begin, int n_end, int split_n, int splits, const TOut& to, hipStream_t st) {
+                      const SlotPlan& p, int n_begin, int n_end, int n_most, int most, const TOut& to, hipStream_t st) {
   auto kern = transposed_kernel<BITS>;
   static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), transposed_lds<BITS>());
   if (int rc = lds_status(lds_ok)) return rc;
-  const dim3 grid(static_cast<unsigned>(up8(tiles * ceil_div(l.K, 256) * splits)));
+  const dim3 grid(static_cast<unsigned>(piece_blocks(tiles * ceil_div(l.K, 256))));
   hipLaunchKernelGGL(kern, grid, dim3(512), transposed_lds<BITS>(), st, a, a_rows, a_pitch, by_place ? 1 : 0, l, p, n_begin,
-                     n_end, split_n, splits, to);
+                     n_end, n_most, most, to);
   return check_launch("transposed product launch");
 }
 
 }  // namespace
 
 int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                   const SlotPlan& p, int n_begin, int n_end, int split_n, int splits, const TOut& to, hipStream_t st) {
-  return bits == 4 ? launch_transposed<4>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, split_n, splits, to, st)
-                   : launch_transposed<8>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, split_n, splits, to, st);
+                   const SlotPlan& p, int n_begin, int n_end, int n_most, int most, const TOut& to, hipStream_t st) {
+  return bits == 4 ? launch_transposed<4>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, n_most, most, to, st)
+                   : launch_transposed<8>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, n_most, most, to, st);
 }
 
 namespace {
-
-constexpr int kUnits = 256;   // compute units
 
 int check_experts(int M, int T, int E, int N, int K, int group_size, int bits) {
   if (M <= 0 || T <= 0) return fail(W4A16_ERR_INVALID_ARG, "M and T must be positive (M=%d T=%d)", M, T);
@@ -65,21 +63,11 @@ int check_experts(int M, int T, int E, int N, int K, int group_size, int bits) {
 // --- tile shapes ----------------------------------------------------------------------
 
 // Height of the full row tiles, and 64-column blocks of a column tile, for S slots over E
-// experts and `cols` output columns.  The groups' sizes are known on the device only; they
-// are taken as equal.  Cost of a tile against one of 256 x 256: half the rows 0.64, a quarter
-// 0.45 (the weights are expanded for fewer rows), 64 columns instead of 256 0.35 (the rows
-// are read for fewer columns); and the rounds that the tiles need over the compute units.
+// experts and `cols` output columns, by the rounds that the tiles need over the compute units
+// and a tile's cost: 64 columns instead of 256 0.35 (the rows are read for fewer columns).
 struct TileShape {
   int height, nb;
 };
-
-double tiles_of(int64_t S, int E, int height) {
-  const double used = static_cast<double>(std::min<int64_t>(E, S));
-  const double per = static_cast<double>(S) / used;
-  return used * std::max(1.0, static_cast<double>(ceil_div(static_cast<int64_t>(per + 0.999), height)));
-}
-
-double height_cost(int height) { return height == 256 ? 1.0 : height == 128 ? 0.64 : 0.45; }
 
 TileShape pick_shape(int64_t S, int E, int cols) {
   TileShape best{256, 4};
@@ -94,29 +82,6 @@ TileShape pick_shape(int64_t S, int E, int cols) {
   return best;
 }
 
-// Height and contraction parts of the transposed product: tiles of 256 channels, and parts of
-// at least 512 outputs where the tiles leave compute units without work.
-struct SplitShape {
-  int height, splits, split_n;
-};
-
-SplitShape pick_split(int64_t S, int E, int N, int K) {
-  SplitShape best{256, 1, 0};
-  double least = 1e300;
-  for (int height : {256, 128, 64}) {
-    const double tiles = tiles_of(S, E, height) * ceil_div(K, 256);
-    for (int splits = 1; splits <= 16 && (splits == 1 || N / splits >= 512); ++splits) {
-      const double wgs = tiles * splits;
-      const double rounds = wgs > 8 * kUnits ? wgs / kUnits : static_cast<double>(ceil_div(static_cast<int64_t>(wgs), kUnits));
-      const double cost = rounds * height_cost(height) / splits * (1.0 + 0.02 * (splits - 1));
-      if (cost < 0.999 * least) least = cost, best = {height, splits, 0};
-    }
-  }
-  best.split_n = static_cast<int>(ceil_div(ceil_div(N, best.splits), 64) * 64);
-  best.splits = static_cast<int>(ceil_div(N, best.split_n));
-  return best;
-}
-
 // --- forward ----------------------------------------------------------------------------
 
 struct ForwardMemory {
@@ -126,7 +91,7 @@ struct ForwardMemory {
 
 ForwardMemory forward_memory(Carver& ws, int64_t S, int E, int K, bool act, int height) {
   ForwardMemory m;
-  m.plan = take_plan(ws, S, most_tiles(S, E, height));
+  m.plan = take_plan(ws, S, most_tiles(S, E, height), false);
   m.gathered = act ? ws.take<half_t>(static_cast<size_t>(S) * K) : nullptr;
   return m;
 }
@@ -190,12 +155,15 @@ struct BackwardMemory {
   int32_t* inverse;   // act order
 };
 
-bool straight(int T, const SplitShape& s, bool act) { return T == 1 && s.splits == 1 && !act; }
+// Sums go to dx themselves where a row has one slot and its channels their own order;
+// partial sums are kept for the tiles that are in parts.
+bool is_direct(int T, bool act) { return T == 1 && !act; }
 
-BackwardMemory backward_memory(Carver& ws, int64_t S, int T, int E, int K, bool act, const SplitShape& shape) {
+BackwardMemory backward_memory(Carver& ws, int64_t S, int T, int E, int K, bool act, const TransposedShape& shape) {
   BackwardMemory m;
-  m.plan = take_plan(ws, S, most_tiles(S, E, shape.height));
-  m.part = straight(T, shape, act) ? nullptr : ws.take<float>(static_cast<size_t>(shape.splits) * S * K);
+  const bool parts = !is_direct(T, act) || shape.most > 1;
+  m.plan = take_plan(ws, S, most_tiles(S, E, shape.height), parts);
+  m.part = parts ? ws.take<float>(static_cast<size_t>(shape.most) * S * K) : nullptr;
   m.inverse = act ? ws.take<int32_t>(static_cast<size_t>(E) * K) : nullptr;
   return m;
 }
@@ -203,8 +171,8 @@ BackwardMemory backward_memory(Carver& ws, int64_t S, int T, int E, int K, bool 
 int check_backward(int M, int T, int E, int N, int K) {
   const int64_t S = static_cast<int64_t>(M) * T;
   if (S * N >= kMaxElements) return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d N=%d: 2^31 elements or more", M, T, N);
-  const SplitShape shape = pick_split(S, E, N, K);
-  if (most_tiles(S, E, shape.height) * ceil_div(K, 256) * shape.splits > kMaxBlocks)
+  const TransposedShape shape = pick_transposed(S, E, N, K);
+  if (piece_blocks(most_tiles(S, E, shape.height) * ceil_div(K, 256)) > kMaxBlocks)
     return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d K=%d: more tiles than one launch takes", M, T, K);
   return W4A16_OK;
 }
@@ -215,28 +183,25 @@ int launch_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* 
                     uint16_t* dx, void* workspace, size_t workspace_bytes, void* stream) {
   if (int rc = check_backward(M, T, E, N, K)) return rc;
   const int S = M * T;
-  const SplitShape shape = pick_split(S, E, N, K);
+  const TransposedShape shape = pick_transposed(S, E, N, K);
   Carver ws{static_cast<unsigned char*>(workspace)};
   const BackwardMemory mem = backward_memory(ws, S, T, E, K, act, shape);
   if (workspace_bytes < ws.used)
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.used);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Layers l = make_layers(qweight, scales, qzeros, group_size, N, K, BITS, act);
-  run_plan(mem.plan, index, S, E, E, shape.height, mem.part == nullptr, st);
+  const bool direct = is_direct(T, act);
+  run_plan(mem.plan, index, S, E, E, shape.height, direct, st);
   const half_t* h0 = reinterpret_cast<const half_t*>(dx0);
   half_t* hx = reinterpret_cast<half_t*>(dx);
-  TOut to{};
-  if (mem.part)
-    to = {nullptr, nullptr, mem.part, static_cast<size_t>(S), 0};
-  else
-    to = {hx, h0, nullptr, 0, 0};
+  const TOut to{direct ? hx : nullptr, direct ? h0 : nullptr, mem.part, static_cast<size_t>(S), 0};
   if (int rc = run_transposed(BITS, most_tiles(S, E, shape.height), reinterpret_cast<const half_t*>(dy), S, N, false, l,
-                              mem.plan, 0, N, shape.split_n, shape.splits, to, st))
+                              mem.plan, 0, N, N, shape.most, to, st))
     return rc;
   if (mem.part) {
     if (act) run_invert(l, E, mem.inverse, st);
-    hipLaunchKernelGGL(sum_slots_kernel, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.splits, T,
-                       index, E, mem.inverse, K, h0, hx);
+    hipLaunchKernelGGL(sum_slots_kernel, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.most, T, index,
+                       E, mem.plan, mem.inverse, K, direct ? 1 : 0, h0, hx);
   }
   return check_launch("experts backward launch");
 }
@@ -363,7 +328,7 @@ size_t w4a16_experts_backward_workspace(int M, int T, int E, int N, int K, int a
   if (!ok) return 0;
   Carver ws{nullptr};
   const int64_t S = static_cast<int64_t>(M) * T;
-  backward_memory(ws, S, T, E, K, act_order != 0, pick_split(S, E, N, K));
+  backward_memory(ws, S, T, E, K, act_order != 0, pick_transposed(S, E, N, K));
   return ws.used;
 }
 

@@ -12,7 +12,6 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kUnits = 256;                             // compute units
 constexpr int kChunkRows = 32768;                       // rows taken at once: bounds the workspace
 constexpr int64_t kCoeffElements = int64_t{1} << 27;    // coefficients of one piece: 256 MB
 
@@ -33,7 +32,7 @@ int pick_height(int M, int64_t tiles) {
   for (int height : {256, 128, 64}) {
     const double wgs = static_cast<double>(ceil_div(M, height) * tiles);
     const double rounds = wgs > 8 * kUnits ? wgs / kUnits : static_cast<double>(ceil_div(static_cast<int64_t>(wgs), kUnits));
-    const double cost = rounds * (height == 256 ? 1.0 : height == 128 ? 0.64 : 0.45);
+    const double cost = rounds * height_cost(height);
     if (cost < 0.999 * least) least = cost, best = height;
   }
   return best;
@@ -53,7 +52,7 @@ struct LossMemory {
 LossMemory loss_memory(Carver& ws, int rows, int N, int K, bool act) {
   const int64_t tiles = ceil_div(N, 256);
   LossMemory m;
-  m.plan = take_plan(ws, rows, most_tiles(rows, 1, pick_height(rows, tiles)));
+  m.plan = take_plan(ws, rows, most_tiles(rows, 1, pick_height(rows, tiles)), false);
   m.part = ws.take<MaxSum>(static_cast<size_t>(tiles) * rows);
   m.label = ws.take<float>(rows);
   m.gathered = act ? ws.take<half_t>(static_cast<size_t>(rows) * K) : nullptr;
@@ -109,12 +108,12 @@ int head_loss(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
 
 // --- backward ---------------------------------------------------------------------------
 
-// A piece of the vocabulary: whole tiles of 256 columns, as many as kCoeffElements hold.
-// The product of a piece's coefficients with its weights: tiles of `height` rows by 256
-// channels, the piece's outputs in `splits` parts where these tiles alone leave compute units
-// without work.
+// A piece of the vocabulary: whole tiles of 256 columns, as many as kCoeffElements hold; the
+// tile heights of its logits and of the product of its coefficients with its weights, and the
+// most parts of a tile of that product.
 struct PieceShape {
-  int cols, height, logit_height, splits, split_n;
+  int cols, logit_height;
+  TransposedShape product;
 };
 
 PieceShape pick_piece(int rows, int N, int K) {
@@ -123,18 +122,7 @@ PieceShape pick_piece(int rows, int N, int K) {
   const int64_t pieces = ceil_div(N, fit);
   p.cols = static_cast<int>(ceil_div(ceil_div(N, pieces), 256) * 256);
   p.logit_height = pick_height(rows, p.cols / 256);
-  double least = 1e300;
-  for (int height : {256, 128, 64}) {
-    const int64_t tiles = ceil_div(rows, height) * ceil_div(K, 256);
-    for (int splits = 1; splits <= 16 && (splits == 1 || p.cols / splits >= 1024); ++splits) {
-      const double wgs = static_cast<double>(tiles * splits);
-      const double rounds = wgs > 8 * kUnits ? wgs / kUnits : static_cast<double>(ceil_div(static_cast<int64_t>(wgs), kUnits));
-      const double cost = rounds * (height == 256 ? 1.0 : height == 128 ? 0.64 : 0.45) / splits * (1.0 + 0.02 * (splits - 1));
-      if (cost < 0.999 * least) least = cost, p.height = height, p.splits = splits;
-    }
-  }
-  p.split_n = static_cast<int>(ceil_div(ceil_div(p.cols, p.splits), 64) * 64);
-  p.splits = static_cast<int>(ceil_div(p.cols, p.split_n));
+  p.product = pick_transposed(rows, 1, p.cols, K);
   return p;
 }
 
@@ -150,10 +138,11 @@ struct GradMemory {
 GradMemory grad_memory(Carver& ws, int rows, int N, int K, bool act) {
   const PieceShape p = pick_piece(rows, N, K);
   GradMemory m;
-  m.plan = take_plan(ws, rows, most_tiles(rows, 1, p.height));
-  m.logit_plan = p.logit_height == p.height ? m.plan : take_plan(ws, rows, most_tiles(rows, 1, p.logit_height));
+  const int height = p.product.height;
+  m.plan = take_plan(ws, rows, most_tiles(rows, 1, height), true);
+  m.logit_plan = p.logit_height == height ? m.plan : take_plan(ws, rows, most_tiles(rows, 1, p.logit_height), false);
   m.coeff = ws.take<half_t>(static_cast<size_t>(rows) * p.cols);
-  m.part = ws.take<float>(static_cast<size_t>(p.splits) * rows * K);
+  m.part = ws.take<float>(static_cast<size_t>(p.product.most) * rows * K);
   m.remainder = ws.take<float>(rows);
   m.gathered = act ? ws.take<half_t>(static_cast<size_t>(rows) * K) : nullptr;
   m.inverse = act ? ws.take<int32_t>(K) : nullptr;
@@ -186,8 +175,9 @@ int head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qwe
   for (int64_t m0 = 0; m0 < M; m0 += most) {
     const int rows = static_cast<int>(std::min<int64_t>(most, M - m0));
     const half_t* hx = reinterpret_cast<const half_t*>(x) + m0 * K;
-    run_plan(mem.plan, target + m0, rows, 1, vocab, p.height, false, st);
-    if (p.logit_height != p.height) run_plan(mem.logit_plan, target + m0, rows, 1, vocab, p.logit_height, false, st);
+    const int height = p.product.height;
+    run_plan(mem.plan, target + m0, rows, 1, vocab, height, false, st);
+    if (p.logit_height != height) run_plan(mem.logit_plan, target + m0, rows, 1, vocab, p.logit_height, false, st);
     if (act) run_gather(mem.plan, hx, nullptr, l, rows, 1, mem.gathered, st);
     const HeadRows hr{target + m0, mem.remainder, lse + m0};
     for (int v0 = 0; v0 < vocab; v0 += p.cols) {
@@ -198,17 +188,12 @@ int head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qwe
                                            mem.logit_plan, hr, to))
         return rc;
       const TOut out{nullptr, nullptr, mem.part, static_cast<size_t>(rows), v0 > 0};
-      const int splits = static_cast<int>(ceil_div(v1 - v0, p.split_n));
-      if (int rc = run_transposed(BITS, most_tiles(rows, 1, p.height), mem.coeff, rows, p.cols, true, l, mem.plan, v0, v1,
-                                  p.split_n, splits, out, st))
+      if (int rc = run_transposed(BITS, most_tiles(rows, 1, height), mem.coeff, rows, p.cols, true, l, mem.plan, v0, v1,
+                                  p.cols, p.product.most, out, st))
         return rc;
     }
-    // a last piece with fewer parts adds to the first ones only; a single piece may have
-    // fewer parts than the workspace has room for
-    const int parts = vocab > p.cols ? p.splits
-                                     : static_cast<int>(ceil_div(std::min<int64_t>(ceil_div(vocab, 16) * 16, N), p.split_n));
-    hipLaunchKernelGGL(head_dx_kernel<BITS>, dim3(rows), dim3(256), 0, st, mem.part, static_cast<size_t>(rows), parts,
-                       mem.plan, l, act ? mem.inverse : nullptr, target + m0, mem.remainder, dloss + m0,
+    hipLaunchKernelGGL(head_dx_kernel<BITS>, dim3(rows), dim3(256), 0, st, mem.part, static_cast<size_t>(rows),
+                       p.product.most, mem.plan, l, act ? mem.inverse : nullptr, target + m0, mem.remainder, dloss + m0,
                        reinterpret_cast<half_t*>(dx) + m0 * K);
   }
   return check_launch("head backward launch");

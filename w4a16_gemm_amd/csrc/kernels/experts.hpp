@@ -14,7 +14,7 @@
 
 namespace w4a16 {
 
-constexpr size_t kTileRowsLds = 2 * kBigBM * 4;   // the tile's slots and source rows, behind the ring
+constexpr size_t kTileRowsLds = 4 * kBigBM * 4;   // four words per row of the tile, behind the ring
 
 template <int BITS>
 constexpr size_t experts_lds() { return static_cast<size_t>(kBigStages) * big_stage_bytes<BITS>() + kTileRowsLds; }
@@ -35,30 +35,63 @@ __device__ __forceinline__ BigLoader<NB, MB, BITS> rows_loader(const half_t* x, 
   return ld;
 }
 
-// Calls store(row, column, value) for every accumulator of a 16x16 tile; row inside the
-// tile, column from its first.
-template <int NB, int MB, class Store>
-__device__ __forceinline__ void each_value(const float4_t (&acc)[MB][NB], int tid, Store store) {
-  const int lane = tid & 63, wave = tid >> 6, wm = wave >> 2, wn = wave & 3, lr = lane & 15, lq = lane >> 4;
+// Stores a tile of accumulators as binary16: value(row, column, v) -> binary16 of the tile's
+// row and column, put(row, column, run of 8 columns) stores them.  An accumulator register
+// holds 16 (32) neighbouring columns of a row, 32 (64) bytes; to store whole 128-byte runs a
+// wavefront turns 32 rows at a time in LDS memory of its own (rows of 16 NB columns and 16
+// bytes of padding, so that the rows that one write meets lie in distinct banks).  The ring's
+// memory is used: every wavefront must be done with its loads.
+template <int NB>
+constexpr int turn_pitch() { return 16 * NB + 8; }
+
+template <int NB, int MB, class Put>
+__device__ __forceinline__ void put_turned(const half_t* turn, int tid, int row0, Put put) {
+  const int lane = tid & 63, wn = (tid >> 6) & 3;
+  constexpr int RUNS = 2 * NB;   // runs of 8 columns per row
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-        store(wm * 16 * MB + 16 * mb + 4 * lq + r, wn * 16 * NB + 16 * nb + lr, acc[mb][nb][r]);
+  for (int i = 0; i < 32 * RUNS / 64; ++i) {
+    const int at = i * 64 + lane, row = at / RUNS, run = at % RUNS;
+    put(row0 + row, wn * 16 * NB + 8 * run, *reinterpret_cast<const half8_t*>(turn + row * turn_pitch<NB>() + 8 * run));
+  }
 }
 
-template <int NB, int MB, class Store>
-__device__ __forceinline__ void each_value32(const f32x16_t (&acc)[MB / 2][NB / 2], int tid, Store store) {
-  const int lane = tid & 63, wave = tid >> 6, wm = wave >> 2, wn = wave & 3, lc = lane & 31, lh = lane >> 5;
+template <int NB, int MB, class Value, class Put>
+__device__ __forceinline__ void store_tile(const float4_t (&acc)[MB][NB], unsigned char* smem, int tid, Value value,
+                                           Put put) {
+  const int lane = tid & 63, wave = tid >> 6, wm = wave >> 2, wn = wave & 3, lr = lane & 15, lq = lane >> 4;
+  half_t* turn = reinterpret_cast<half_t*>(smem) + wave * 32 * turn_pitch<NB>();
 #pragma unroll
-  for (int rb = 0; rb < MB / 2; ++rb)
+  for (int m2 = 0; m2 < MB / 2; ++m2) {
+    const int row0 = wm * 16 * MB + 32 * m2;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          turn[(16 * h + 4 * lq + r) * turn_pitch<NB>() + 16 * nb + lr] =
+              value(row0 + 16 * h + 4 * lq + r, wn * 16 * NB + 16 * nb + lr, acc[2 * m2 + h][nb][r]);
+    put_turned<NB, MB>(turn, tid, row0, put);
+  }
+}
+
+template <int NB, int MB, class Value, class Put>
+__device__ __forceinline__ void store_tile32(const f32x16_t (&acc)[MB / 2][NB / 2], unsigned char* smem, int tid,
+                                             Value value, Put put) {
+  const int lane = tid & 63, wave = tid >> 6, wm = wave >> 2, wn = wave & 3, lc = lane & 31, lh = lane >> 5;
+  half_t* turn = reinterpret_cast<half_t*>(smem) + wave * 32 * turn_pitch<NB>();
+#pragma unroll
+  for (int rb = 0; rb < MB / 2; ++rb) {
+    const int row0 = wm * 16 * MB + 32 * rb;
 #pragma unroll
     for (int r = 0; r < 16; ++r)
 #pragma unroll
-      for (int cb = 0; cb < NB / 2; ++cb)
-        store(wm * 16 * MB + 32 * rb + 8 * (r >> 2) + 4 * lh + (r & 3), wn * 16 * NB + 32 * cb + lc, acc[rb][cb][r]);
+      for (int cb = 0; cb < NB / 2; ++cb) {
+        const int row = 8 * (r >> 2) + 4 * lh + (r & 3);
+        turn[row * turn_pitch<NB>() + 32 * cb + lc] = value(row0 + row, wn * 16 * NB + 32 * cb + lc, acc[rb][cb][r]);
+      }
+    put_turned<NB, MB>(turn, tid, row0, put);
+  }
 }
 
 template <int NB, int MB, int BITS>
@@ -68,17 +101,20 @@ __device__ __forceinline__ void experts_tile(const half_t* x, int x_rows, const 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const auto ld = rows_loader<NB, MB, BITS>(x, x_rows, l, smem, source, rows, n0, l.N, tid, wave);
   const int N = l.N;
-  auto store = [&](int row, int col, float v) {
-    if (row < rows && n0 + col < N) y[static_cast<size_t>(slots[row]) * N + n0 + col] = static_cast<half_t>(v);
+  auto value = [&](int, int, float v) { return static_cast<half_t>(v); };
+  auto put = [&](int row, int col, half8_t v) {
+    if (row < rows && n0 + col < N) *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slots[row]) * N + n0 + col) = v;
   };
   if constexpr (MB < 8 && BITS == 4 && NB % 2 == 0) {
     f32x16_t acc[MB / 2][NB / 2];
     big_tile32_product<NB, MB>(ld, l.zeros, smem, l.K, l.gshift, tid, wave, 1, acc);
-    each_value32<NB, MB>(acc, tid, store);
+    __syncthreads();
+    store_tile32<NB, MB>(acc, smem, tid, value, put);
   } else {
     float4_t acc[MB][NB];
     big_tile_product<NB, MB, BITS>(ld, l.zeros, smem, l.K, l.gshift, tid, wave, 1, acc);
-    each_value<NB, MB>(acc, tid, store);
+    __syncthreads();
+    store_tile<NB, MB>(acc, smem, tid, value, put);
   }
 }
 

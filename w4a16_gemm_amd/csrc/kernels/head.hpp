@@ -68,34 +68,43 @@ struct HeadOut {
   size_t places;
 };
 
+// What a tile knows of its rows, in LDS.
+struct HeadTileRows {
+  int32_t* source;   // row of x
+  int32_t* label;
+  float* lse;        // backward
+};
+
 template <int MB, int BITS, bool GRAD>
 __device__ __forceinline__ void head_tile(const half_t* x, int x_rows, const Layers& l, unsigned char* smem,
-                                          const int32_t* source, const int32_t* row_of, const RowTile& tile,
-                                          const HeadRows& rows, const HeadOut& to, int n0, int ct) {
+                                          const HeadTileRows& own, const RowTile& tile, const HeadRows& rows,
+                                          const HeadOut& to, int n0, int ct) {
   constexpr int BM = 32 * MB;
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const auto ld = rows_loader<4, MB, BITS>(x, x_rows, l, smem, source, tile.rows, n0, l.N, tid, wave);
+  const auto ld = rows_loader<4, MB, BITS>(x, x_rows, l, smem, own.source, tile.rows, n0, l.N, tid, wave);
   float4_t acc[MB][4];
   big_tile_product<4, MB, BITS>(ld, l.zeros, smem, l.K, l.gshift, tid, wave, 1, acc);
+  __syncthreads();   // the ring's memory is used again
   const int lane = tid & 63, wm = wave >> 2, wn = wave & 3, lr = lane & 15, lq = lane >> 4;
-  const int c0 = n0 + wn * 64 + lr;   // this lane's column of block 0
   if constexpr (!GRAD) {
-    __syncthreads();   // the ring's memory is used again
+    const int c0 = n0 + wn * 64 + lr;   // this lane's column of block 0
+    const bool whole = n0 + 256 <= to.vocab;
     MaxSum* red = reinterpret_cast<MaxSum*>(smem);   // [wn][row]
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = wm * 16 * MB + 16 * mb + 4 * lq + r;
-        const int label = rows.target[row_of[min(row, tile.rows - 1)]];
+        const int at = own.label[row] - c0;   // 16 nb: the target's logit is this lane's
         float v[4], m = -INFINITY;
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) {
-          v[nb] = c0 + 16 * nb < to.vocab ? acc[mb][nb][r] : -INFINITY;
-          if (c0 + 16 * nb == label && row < tile.rows) rows.label[tile.first + row] = v[nb];
+          v[nb] = whole || c0 + 16 * nb < to.vocab ? acc[mb][nb][r] : -INFINITY;
           m = fmaxf(m, v[nb]);
         }
+        if (at >= 0 && at < 64 && at % 16 == 0 && row < tile.rows)
+          rows.label[tile.first + row] = at < 32 ? (at < 16 ? v[0] : v[1]) : (at < 48 ? v[2] : v[3]);
         m = row16_max(m);
         const float base = m == -INFINITY ? 0.f : m;
         float s = 0.f;
@@ -109,27 +118,21 @@ __device__ __forceinline__ void head_tile(const half_t* x, int x_rows, const Lay
       to.part[static_cast<size_t>(ct) * to.places + tile.first + tid] =
           join(join(red[tid], red[BM + tid]), join(red[2 * BM + tid], red[3 * BM + tid]));
   } else {
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = wm * 16 * MB + 16 * mb + 4 * lq + r;
-        if (row >= tile.rows) continue;
-        const int m = row_of[row];
-        const int label = rows.target[m];
-        const float lse = rows.lse[m];
-        half_t* out = to.coeff + static_cast<size_t>(tile.first + row) * to.pitch - to.v0;
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb) {
-          const int col = c0 + 16 * nb;
-          if (col >= to.v1) continue;
-          float c = col < to.vocab ? exp_diff(acc[mb][nb][r], lse) : 0.f;
-          if (col == label) c -= 1.f;
+    store_tile<4, MB>(
+        acc, smem, tid,
+        [&](int row, int col, float v) {
+          float c = n0 + col < to.vocab ? exp_diff(v, own.lse[row]) : 0.f;
+          const bool is_label = n0 + col == own.label[row];
+          if (is_label) c -= 1.f;
           const half_t h = static_cast<half_t>(c * kCoeffScale);
-          if (col == label) rows.label[tile.first + row] = c - static_cast<float>(h) * (1.f / kCoeffScale);
-          out[col] = h;
-        }
-      }
+          if (is_label && row < tile.rows)
+            rows.label[tile.first + row] = c - static_cast<float>(h) * (1.f / kCoeffScale);
+          return h;
+        },
+        [&](int row, int col, half8_t v) {
+          if (row < tile.rows && n0 + col < to.v1)
+            *reinterpret_cast<half8_t*>(to.coeff + static_cast<size_t>(tile.first + row) * to.pitch + n0 + col - to.v0) = v;
+        });
   }
 }
 
@@ -142,20 +145,22 @@ __global__ __launch_bounds__(512) void head_kernel(const half_t* __restrict__ x,
   RowTile tile;
   int ct;
   if (!find_tile(plan, (to.v1 - to.v0 + 255) / 256, blockIdx.x, tile, ct)) return;
-  int32_t* m = reinterpret_cast<int32_t*>(smem + experts_lds<BITS>() - kTileRowsLds);
-  int32_t* source = m + kBigBM;
-  if (tid < tile.rows) {
-    m[tid] = plan.order[tile.first + tid];
-    source[tid] = gathered ? tile.first + tid : m[tid];
+  int32_t* words = reinterpret_cast<int32_t*>(smem + experts_lds<BITS>() - kTileRowsLds);
+  const HeadTileRows own{words, words + kBigBM, reinterpret_cast<float*>(words + 2 * kBigBM)};
+  if (tid < tile.height) {
+    const int place = tile.first + min(tid, tile.rows - 1), m = plan.order[place];
+    own.source[tid] = gathered ? place : m;
+    own.label[tid] = rows.target[m];
+    if (GRAD) own.lse[tid] = rows.lse[m];
   }
   __syncthreads();
   const int n0 = to.v0 + 256 * ct;
   if (tile.height == 256)
-    head_tile<8, BITS, GRAD>(x, x_rows, layers, smem, source, m, tile, rows, to, n0, ct);
+    head_tile<8, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
   else if (tile.height == 128)
-    head_tile<4, BITS, GRAD>(x, x_rows, layers, smem, source, m, tile, rows, to, n0, ct);
+    head_tile<4, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
   else
-    head_tile<2, BITS, GRAD>(x, x_rows, layers, smem, source, m, tile, rows, to, n0, ct);
+    head_tile<2, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
 }
 
 // Joins the column tiles of 64 places per workgroup, 16 of them side by side in a fixed
@@ -185,9 +190,9 @@ __global__ __launch_bounds__(1024) void head_join_kernel(const MaxSum* __restric
 }
 
 // dx[m] = dloss[m] (sum of the parts 2^-14 + remainder W^_target), rounded once; zeros for
-// rows without a target.  One workgroup per place.
+// rows without a target.  One workgroup per place, eight channels per thread.
 template <int BITS>
-__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ part, size_t places, int splits,
+__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ part, size_t places, int most,
                                                       SlotPlan plan, Layers l, const int32_t* __restrict__ inverse,
                                                       const int32_t* __restrict__ target,
                                                       const float* __restrict__ remainder,
@@ -195,26 +200,54 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ 
   const int p = blockIdx.x, K = l.K;
   const size_t m = plan.order[p];
   const bool valid = p < plan.counts[1];
+  const int cols = (K + 255) / 256;
   const int label = valid ? target[m] : 0;
   const float rest = valid ? remainder[p] : 0.f, d = valid ? dloss[m] : 0.f;
+  const int tile = valid ? plan.tile_of[m] : 0;
+  const Pieces rule(max(1, plan.counts[0] * cols), most);
+  constexpr int PER = 32 / BITS;   // channels per word
+  const uint32_t* codes = l.qw + static_cast<size_t>(label) * (K / PER);
+  auto consts = [&](int k) {
+    const int g = k >> l.gshift;
+    return make_consts(load_zero<BITS>(l.zeros, g, l.N, label), l.scales[static_cast<size_t>(g) * l.N + label]);
+  };
   for (int k0 = 8 * threadIdx.x; k0 < K; k0 += 8 * 256) {
     half8_t o{};
     if (valid) {
+      const RowTile row = plan.tiles[tile];
+      float s[8] = {}, w[8];
+      if (inverse) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t k = k0 + i;
-        if (inverse) k = min(static_cast<uint32_t>(inverse[k]), static_cast<uint32_t>(K - 1));
-        float s = 0.f;
-        for (int q = 0; q < splits; ++q) s += part[(q * places + p) * K + k];
-        const int g = k >> l.gshift;
-        const DequantConsts c = make_consts(load_zero<BITS>(l.zeros, g, l.N, label), l.scales[static_cast<size_t>(g) * l.N + label]);
-        float w;
-        if constexpr (BITS == 4)
-          w = static_cast<float>(dequant_word(l.qw[static_cast<size_t>(label) * (K / 8) + k / 8], c)[k % 8]);
-        else
-          w = static_cast<float>(dequant_word8(l.qw[static_cast<size_t>(label) * (K / 4) + k / 4], c)[k % 4]);
-        o[i] = static_cast<half_t>(d * (s * (1.f / kCoeffScale) + rest * w));
+        for (int i = 0; i < 8; ++i) {
+          const int k = min(static_cast<uint32_t>(inverse[k0 + i]), static_cast<uint32_t>(K - 1));
+          const int pieces = rule.of(row, tile, k / 256, cols);
+          for (int q = 0; q < pieces; ++q) s[i] += part[(q * places + p) * K + k];
+          if constexpr (BITS == 4)
+            w[i] = static_cast<float>(dequant_word(codes[k / 8], consts(k))[k % 8]);
+          else
+            w[i] = static_cast<float>(dequant_word8(codes[k / 4], consts(k))[k % 4]);
+        }
+      } else {
+        const int pieces = rule.of(row, tile, k0 / 256, cols);
+        for (int q = 0; q < pieces; ++q) {
+          const float* at = part + (q * places + p) * K + k0;
+          const float4_t lo = *reinterpret_cast<const float4_t*>(at), hi = *reinterpret_cast<const float4_t*>(at + 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[i] += lo[i], s[4 + i] += hi[i];
+        }
+        const DequantConsts c = consts(k0);
+        if constexpr (BITS == 4) {
+          const half8_t v = dequant_word(codes[k0 / 8], c);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = static_cast<float>(v[i]);
+        } else {
+          const half4_t lo = dequant_word8(codes[k0 / 4], c), hi = dequant_word8(codes[k0 / 4 + 1], c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = static_cast<float>(lo[i]), w[4 + i] = static_cast<float>(hi[i]);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = static_cast<half_t>(d * (s[i] * (1.f / kCoeffScale) + rest * w[i]));
     }
     *reinterpret_cast<half8_t*>(dx + m * K + k0) = o;
   }

@@ -102,7 +102,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_slots_kernel(const int32_t*
         same &= (e[u] >> b) & 1 ? set : ~set;
       }
       const int rank = __popcll(same & ((1ull << lane) - 1));
-      if (e[u] >= 0) plan.order[first[e[u]] + mine[e[u]] + rank] = s0 + 64 * u + lane;
+      if (e[u] >= 0) {
+        const int within = mine[e[u]] + rank;
+        plan.order[first[e[u]] + within] = s0 + 64 * u + lane;
+        if (plan.tile_of) plan.tile_of[s0 + 64 * u + lane] = tile0[e[u]] + within / height;
+      }
       __builtin_amdgcn_wave_barrier();
       if (e[u] >= 0 && rank == 0) mine[e[u]] += __popcll(same);
       __builtin_amdgcn_wave_barrier();

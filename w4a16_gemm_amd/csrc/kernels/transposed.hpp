@@ -280,27 +280,36 @@ __device__ __forceinline__ void each_run(const float4_t (&acc)[MB][4], int tid, 
 template <int MB, int BITS>
 __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int a_pitch, int a0, const Layers& l,
                                                 int n_begin, int n_end, int k0, const int32_t* source,
-                                                const int32_t* target, int rows, const TOut& to, int split,
+                                                const RowTile& tile, const TOut& to, int piece, int pieces,
                                                 unsigned char* smem) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const TLoader<MB, BITS> ld(a, a_rows, a_pitch, a0, l, n_begin, n_end, k0, source, rows, smem, tid, wave);
+  const int rows = tile.rows;
   float4_t acc[MB][4];
-  transposed_product<MB, BITS>(ld, l.zeros, smem, n_end - n_begin, tid, wave, acc);
+  if (n_begin < n_end) {
+    const TLoader<MB, BITS> ld(a, a_rows, a_pitch, a0, l, n_begin, n_end, k0, source, rows, smem, tid, wave);
+    transposed_product<MB, BITS>(ld, l.zeros, smem, n_end - n_begin, tid, wave, acc);
+  } else {   // a part without outputs: nothing to add
+    if (to.add) return;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[mb][i] = float4_t{0.f, 0.f, 0.f, 0.f};
+  }
   const int K = l.K;
   constexpr int RUN = BITS == 4 ? 8 : 4;
   each_run<MB, BITS>(acc, tid, [&](int row, int col, const float* v) {
     if (row >= rows || k0 + col >= K) return;
-    if (to.out) {
+    if (to.out && pieces == 1) {
       typedef _Float16 run_t __attribute__((ext_vector_type(RUN)));
-      const size_t at = static_cast<size_t>(target[row]) * K + k0 + col;
+      const size_t at = static_cast<size_t>(source[row]) * K + k0 + col;
       run_t d{}, o;
       if (to.dx0) d = *reinterpret_cast<const run_t*>(to.dx0 + at);
 #pragma unroll
       for (int i = 0; i < RUN; ++i) o[i] = static_cast<half_t>(v[i] + static_cast<float>(d[i]));
       *reinterpret_cast<run_t*>(to.out + at) = o;
     } else {
-      float4_t* p = reinterpret_cast<float4_t*>(to.part + (split * to.part_rows + target[row]) * K + k0 + col);
+      float4_t* p = reinterpret_cast<float4_t*>(to.part + (piece * to.part_rows + source[row]) * K + k0 + col);
 #pragma unroll
       for (int i = 0; i < RUN / 4; ++i) {
         float4_t s = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
@@ -312,24 +321,24 @@ __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int
 }
 
 // a [a_rows][a_pitch]: by_place: row p belongs to place p of the plan's order, else row s to
-// slot s.  The outputs [n_begin, n_end) against columns [0, n_end - n_begin) of a, in
-// `splits` parts of `split_n` outputs (a multiple of 64).  Sums go to the places or slots
-// alike.
+// slot s.  The outputs [n_begin, n_end) against columns [0, n_end - n_begin) of a.  A tile
+// in parts takes ceil(n_most / parts) outputs each, n_most >= n_end - n_begin (the same for
+// every launch that adds to the same sums).  Sums go to the places or slots alike.
 template <int BITS>
 __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restrict__ a, int a_rows, int a_pitch,
                                                          int by_place, Layers layers, SlotPlan plan, int n_begin,
-                                                         int n_end, int split_n, int splits, TOut to) {
+                                                         int n_end, int n_most, int most, TOut to) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, K = layers.K;
   RowTile tile;
-  int col;
-  const int tiles_k = (K + 255) / 256;
-  if (!find_tile(plan, tiles_k * splits, blockIdx.x, tile, col)) return;
-  const int split = col / tiles_k, k0 = col % tiles_k * 256;
+  int col, piece, pieces;
+  if (!find_piece(plan, (K + 255) / 256, most, blockIdx.x, tile, col, piece, pieces)) return;
+  const int k0 = col * 256;
   int32_t* rows = reinterpret_cast<int32_t*>(smem + transposed_lds<BITS>() - kTileRowsLds);
   if (tid < tile.rows) rows[tid] = by_place ? tile.first + tid : plan.order[tile.first + tid];
   __syncthreads();
-  if (tile.expert < 0) {   // slots without an expert: dx0 alone (only with one part and T == 1)
+  if (tile.expert < 0) {   // slots without an expert: dx0 alone (only where out takes the sums)
+    if (piece > 0) return;
     const int runs = min(256, K - k0) / 8;
     for (int i = tid; i < tile.rows * runs; i += 512) {
       const size_t at = static_cast<size_t>(rows[i / runs]) * K + k0 + i % runs * 8;
@@ -338,25 +347,30 @@ __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restric
     return;
   }
   const Layers l = layers.at<BITS>(tile.expert);
-  const int a0 = split * split_n, n0 = n_begin + a0, n1 = min(n_end, n0 + split_n);
+  const int len = (n_most + 64 * pieces - 1) / (64 * pieces) * 64;
+  const int a0 = piece * len, n0 = n_begin + a0, n1 = min(n_end, n0 + len);
   if (tile.height == 256)
-    transposed_tile<8, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, rows, tile.rows, to, split, smem);
+    transposed_tile<8, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, tile, to, piece, pieces, smem);
   else if (tile.height == 128)
-    transposed_tile<4, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, rows, tile.rows, to, split, smem);
+    transposed_tile<4, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, tile, to, piece, pieces, smem);
   else
-    transposed_tile<2, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, rows, tile.rows, to, split, smem);
+    transposed_tile<2, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, tile, to, piece, pieces, smem);
 }
 
-// Partial sums part[split][slot][K] of the slots [m T, (m + 1) T) -> dx[m], in a fixed
+// Partial sums part[piece][slot][K] of the slots [m T, (m + 1) T) -> dx[m], in a fixed
 // order, plus dx0, rounded once.  Slots without an expert have no sums.  inverse (act
-// order): stored position of every channel of every expert.
-__global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict__ part, size_t slots, int splits, int T,
-                                                        const int32_t* __restrict__ index, int E,
-                                                        const int32_t* __restrict__ inverse, int K,
+// order): stored position of every channel of every expert.  direct: tiles that are not in
+// parts have been written already.
+__global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict__ part, size_t slots, int most, int T,
+                                                        const int32_t* __restrict__ index, int E, SlotPlan plan,
+                                                        const int32_t* __restrict__ inverse, int K, int direct,
                                                         const half_t* __restrict__ dx0, half_t* __restrict__ out) {
   const size_t m = blockIdx.x;
+  const int cols = (K + 255) / 256, total = plan.counts[0] * cols;
+  const Pieces rule(total, most);
   for (int k = 8 * threadIdx.x; k < K; k += 8 * 256) {
     float s[8] = {};
+    bool any = !direct;
     if (dx0) {
       const half8_t d = *reinterpret_cast<const half8_t*>(dx0 + m * K + k);
 #pragma unroll
@@ -366,19 +380,29 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict_
       const size_t slot = m * T + t;
       const int e = index ? index[slot] : 0;
       if (e < 0 || e >= E) continue;
-      for (int p = 0; p < splits; ++p) {
-        const float* row = part + (p * slots + slot) * K;
-        if (inverse) {
+      const int tile = plan.tile_of[slot];
+      const RowTile row = plan.tiles[tile];
+      const float* sums = part + slot * K;
+      if (inverse) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            s[i] += row[min(static_cast<uint32_t>(inverse[static_cast<size_t>(e) * K + k + i]), static_cast<uint32_t>(K - 1))];
-        } else {
-          const float4_t lo = *reinterpret_cast<const float4_t*>(row + k), hi = *reinterpret_cast<const float4_t*>(row + k + 4);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t at = min(static_cast<uint32_t>(inverse[static_cast<size_t>(e) * K + k + i]), static_cast<uint32_t>(K - 1));
+          const int pieces = rule.of(row, tile, at / 256, cols);
+          for (int p = 0; p < pieces; ++p) s[i] += sums[p * slots * K + at];
+        }
+      } else {
+        const int pieces = rule.of(row, tile, k / 256, cols);
+        if (direct && pieces == 1) continue;
+        any = true;
+        for (int p = 0; p < pieces; ++p) {
+          const float* at = sums + p * slots * K + k;
+          const float4_t lo = *reinterpret_cast<const float4_t*>(at), hi = *reinterpret_cast<const float4_t*>(at + 4);
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[i] += lo[i], s[4 + i] += hi[i];
         }
       }
     }
+    if (!any) continue;
     half8_t o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = static_cast<half_t>(s[i]);
