@@ -32,6 +32,13 @@ SHAPES = [
     (129, 1, 2, 272, 512, 8, 512, False, False, "skewed"),
     (257, 2, 3, 2064, 128, 8, 128, False, True, "distinct"),
     (600, 3, 4, 784, 192, 8, 64, False, False, "padded"),
+    (1, 4, 16, 1544, 4096, 4, 128, False, False, "distinct"),
+    (12, 6, 48, 136, 8960, 4, 128, False, False, "mixed"),
+    (2, 2, 3, 4104, 4224, 4, 32, False, True, "distinct"),
+    (64, 8, 32, 264, 1536, 4, 64, False, False, "one"),
+    (64, 8, 512, 40, 640, 4, 32, True, False, "distinct"),
+    (3, 2, 8, 2064, 12352, 8, 64, False, False, "distinct"),
+    (20, 4, 8, 528, 4096, 8, 128, True, True, "skewed"),
 ]
 
 

@@ -7,6 +7,7 @@
 
 #include "entry.hpp"
 #include "kernels/experts.hpp"
+#include "kernels/few.hpp"
 #include "kernels/route.hpp"
 #include "kernels/slots.hpp"
 #include "kernels/transposed.hpp"
@@ -84,14 +85,32 @@ TileShape pick_shape(int64_t S, int E, int cols) {
 
 // --- forward ----------------------------------------------------------------------------
 
+// Few rows per expert: the streaming kernel, at most 4096 channels per walk over its
+// wavefronts (16 of them with up to 2 steps of 128 channels; 3 and 4 steps spill registers).
+struct FewShape {
+  bool ok;
+  int waves, steps, chunks;
+};
+
+FewShape pick_few(int64_t S, int E, int K) {
+  FewShape f{};
+  f.ok = S <= kFewSlots && S <= 16 * std::min<int64_t>(E, S);
+  const int total = static_cast<int>(ceil_div(K, 128));
+  f.chunks = static_cast<int>(ceil_div(total, 32));
+  const int walk = static_cast<int>(ceil_div(total, f.chunks));
+  f.steps = static_cast<int>(ceil_div(walk, 16));
+  f.waves = static_cast<int>(ceil_div(walk, f.steps));
+  return f;
+}
+
 struct ForwardMemory {
   SlotPlan plan;
   half_t* gathered;
 };
 
 ForwardMemory forward_memory(Carver& ws, int64_t S, int E, int K, bool act, int height) {
-  ForwardMemory m;
-  m.plan = take_plan(ws, S, most_tiles(S, E, height), false);
+  ForwardMemory m{};
+  if (!pick_few(S, E, K).ok) m.plan = take_plan(ws, S, most_tiles(S, E, height), false);
   m.gathered = act ? ws.take<half_t>(static_cast<size_t>(S) * K) : nullptr;
   return m;
 }
@@ -116,6 +135,24 @@ int launch_forward(dim3 grid, hipStream_t st, const half_t* x, int x_rows, int g
   return check_launch("experts launch");
 }
 
+template <int STEPS, int BITS>
+int launch_few_t(const FewShape& f, hipStream_t st, const half_t* x, int by_slot, int T, const int32_t* index, int S,
+                 int E, const Layers& l, half_t* y) {
+  auto kern = experts_few_kernel<STEPS, BITS>;
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), few_lds(16));
+  if (int rc = lds_status(lds_ok)) return rc;
+  hipLaunchKernelGGL(kern, dim3(kUnits), dim3(64 * f.waves), few_lds(f.waves), st, x, by_slot, T, index, S, E, l, f.chunks,
+                     y);
+  return check_launch("experts launch");
+}
+
+template <int BITS>
+int launch_few(const FewShape& f, hipStream_t st, const half_t* x, int by_slot, int T, const int32_t* index, int S, int E,
+               const Layers& l, half_t* y) {
+  if (f.steps == 1) return launch_few_t<1, BITS>(f, st, x, by_slot, T, index, S, E, l, y);
+  return launch_few_t<2, BITS>(f, st, x, by_slot, T, index, S, E, l, y);
+}
+
 template <int BITS>
 int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros,
                  const int32_t* g_idx, int group_size, const int32_t* index, int M, int T, int E, int N, int K,
@@ -136,8 +173,13 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.used);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Layers l = make_layers(qweight, scales, qzeros, group_size, N, K, BITS, act);
-  run_plan(mem.plan, index, S, E, E, shape.height, true, st);
   const half_t* hx = reinterpret_cast<const half_t*>(x);
+  const FewShape few = pick_few(S, E, K);
+  if (few.ok) {
+    if (act) hipLaunchKernelGGL(gather_rows_kernel, dim3(S), dim3(256), 0, st, hx, index, E, l, T, mem.gathered);
+    return launch_few<BITS>(few, st, act ? mem.gathered : hx, act, T, index, S, E, l, reinterpret_cast<half_t*>(y));
+  }
+  run_plan(mem.plan, index, S, E, E, shape.height, true, st);
   if (act)
     run_gather(mem.plan, hx, index, l, S, T, mem.gathered, st);
   const dim3 grid(static_cast<unsigned>(up8(most_tiles(S, E, shape.height) * ceil_div(N, 64 * shape.nb))));
