@@ -39,6 +39,11 @@ SHAPES = [
     (64, 8, 512, 40, 640, 4, 32, True, False, "distinct"),
     (3, 2, 8, 2064, 12352, 8, 64, False, False, "distinct"),
     (20, 4, 8, 528, 4096, 8, 128, True, True, "skewed"),
+    # 17 to 64 rows of an expert
+    (120, 2, 7, 4104, 192, 4, 32, False, False, "distinct"),
+    (90, 2, 4, 6152, 320, 4, 64, True, True, "mixed"),
+    (150, 1, 3, 12304, 128, 8, 64, False, False, "distinct"),
+    (300, 2, 16, 2064, 256, 8, 128, False, False, "padded"),
 ]
 
 

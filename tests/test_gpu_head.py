@@ -25,6 +25,9 @@ SHAPES = [
     (33, 1040, 1025, 256, 8, 64, True, False, 0.2),
     (270, 4112, 4100, 128, 8, 128, False, True, 0.1),
     (520, 784, 784, 320, 8, 32, False, False, 0.0),
+    (20, 66568, 66567, 64, 4, 64, False, False, 0.0),
+    (50, 40016, 40016, 192, 8, 64, False, False, 0.1),
+    (65, 2056, 2050, 1536, 4, 128, False, False, 0.0),
 ]
 
 

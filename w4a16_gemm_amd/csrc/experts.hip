@@ -8,6 +8,7 @@
 #include "entry.hpp"
 #include "kernels/experts.hpp"
 #include "kernels/few.hpp"
+#include "kernels/low.hpp"
 #include "kernels/route.hpp"
 #include "kernels/slots.hpp"
 #include "kernels/transposed.hpp"
@@ -185,6 +186,13 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
   const dim3 grid(static_cast<unsigned>(up8(most_tiles(S, E, shape.height) * ceil_div(N, 64 * shape.nb))));
   const half_t* rows = act ? mem.gathered : hx;
   half_t* hy = reinterpret_cast<half_t*>(y);
+  if (shape.height == 64 && shape.nb == 4) {
+    static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(experts_low_kernel<BITS>), low_lds<BITS>());
+    if (int rc = lds_status(lds_ok)) return rc;
+    hipLaunchKernelGGL(experts_low_kernel<BITS>, grid, dim3(512), low_lds<BITS>(), st, rows, act ? S : M, act ? 1 : 0, T, l,
+                       mem.plan, hy);
+    return check_launch("experts launch");
+  }
   if (shape.nb == 4) return launch_forward<4, BITS>(grid, st, rows, act ? S : M, act, T, l, mem.plan, hy);
   return launch_forward<1, BITS>(grid, st, rows, act ? S : M, act, T, l, mem.plan, hy);
 }

@@ -59,14 +59,17 @@ LossMemory loss_memory(Carver& ws, int rows, int N, int K, bool act) {
   return m;
 }
 
+// height: of the plan's full tiles.
 template <int BITS, bool GRAD>
-int launch_head(int64_t row_tiles, hipStream_t st, const half_t* x, int x_rows, bool gathered, const Layers& l,
-                const SlotPlan& plan, const HeadRows& rows, const HeadOut& to) {
-  auto kern = head_kernel<BITS, GRAD>;
-  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), experts_lds<BITS>());
-  if (int rc = lds_status(lds_ok)) return rc;
+int launch_head(int height, int64_t row_tiles, hipStream_t st, const half_t* x, int x_rows, bool gathered,
+                const Layers& l, const SlotPlan& plan, const HeadRows& rows, const HeadOut& to) {
+  auto kern = height == 64 ? head_low_kernel<BITS, GRAD> : head_kernel<BITS, GRAD>;
+  const size_t lds = height == 64 ? low_lds<BITS>() : experts_lds<BITS>();
+  static const hipError_t low_ok = allow_lds(reinterpret_cast<const void*>(head_low_kernel<BITS, GRAD>), low_lds<BITS>());
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(head_kernel<BITS, GRAD>), experts_lds<BITS>());
+  if (int rc = lds_status(height == 64 ? low_ok : lds_ok)) return rc;
   const dim3 grid(static_cast<unsigned>(up8(row_tiles * ceil_div(to.v1 - to.v0, 256))));
-  hipLaunchKernelGGL(kern, grid, dim3(512), experts_lds<BITS>(), st, x, x_rows, gathered ? 1 : 0, l, plan, rows, to);
+  hipLaunchKernelGGL(kern, grid, dim3(512), lds, st, x, x_rows, gathered ? 1 : 0, l, plan, rows, to);
   return check_launch("head launch");
 }
 
@@ -96,7 +99,7 @@ int head_loss(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
     if (act) run_gather(mem.plan, hx, nullptr, l, rows, 1, mem.gathered, st);
     const HeadRows hr{target + m0, mem.label, nullptr};
     const HeadOut to{mem.part, nullptr, 0, 0, vocab, vocab, static_cast<size_t>(rows)};
-    if (int rc = launch_head<BITS, false>(most_tiles(rows, 1, height), st, act ? mem.gathered : hx, rows, act, l, mem.plan,
+    if (int rc = launch_head<BITS, false>(height, most_tiles(rows, 1, height), st, act ? mem.gathered : hx, rows, act, l, mem.plan,
                                           hr, to))
       return rc;
     hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 64))), dim3(1024), 0, st, mem.part,
@@ -184,7 +187,7 @@ int head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qwe
       // padding columns up to a whole zero-point word have the coefficient 0
       const int v1 = static_cast<int>(std::min<int64_t>(int64_t{v0} + p.cols, std::min<int64_t>(ceil_div(vocab, 16) * 16, N)));
       const HeadOut to{nullptr, mem.coeff, p.cols, v0, v1, vocab, static_cast<size_t>(rows)};
-      if (int rc = launch_head<BITS, true>(most_tiles(rows, 1, p.logit_height), st, act ? mem.gathered : hx, rows, act, l,
+      if (int rc = launch_head<BITS, true>(p.logit_height, most_tiles(rows, 1, p.logit_height), st, act ? mem.gathered : hx, rows, act, l,
                                            mem.logit_plan, hr, to))
         return rc;
       const TOut out{nullptr, nullptr, mem.part, static_cast<size_t>(rows), v0 > 0};

@@ -13,7 +13,7 @@
 // would do to the whole row is taken back: its remainder is added in fp32 at the end.
 #pragma once
 
-#include "experts.hpp"
+#include "low.hpp"
 
 namespace w4a16 {
 
@@ -161,6 +161,84 @@ __global__ __launch_bounds__(512) void head_kernel(const half_t* __restrict__ x,
     head_tile<4, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
   else
     head_tile<2, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
+}
+
+// The same on tiles of up to 64 rows (low.hpp).
+template <int RB, int BITS, bool GRAD>
+__device__ __forceinline__ void head_low_tile(const half_t* x, int x_rows, const Layers& l, unsigned char* smem,
+                                              const HeadTileRows& own, const RowTile& tile, const HeadRows& rows,
+                                              const HeadOut& to, int n0, int ct) {
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const LowLoader<BITS> ld(x, x_rows, l, smem, own.source, tile.rows, n0, tid, wave);
+  LowSums<RB> acc;
+  low_product(ld, l.zeros, smem, tid, wave, acc);
+  __syncthreads();   // the ring's memory is used again
+  const int lane = tid & 63, lc = lane & 31, lh = lane >> 5;
+  if constexpr (!GRAD) {
+    const int col = n0 + 32 * wave + lc;
+    MaxSum* red = reinterpret_cast<MaxSum*>(smem);   // [wave][row]
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int row = 32 * b + 8 * (r >> 2) + 4 * lh + (r & 3);
+        const float v = col < to.vocab ? acc.b[b][r] : -INFINITY;
+        if (own.label[row] == col && row < tile.rows) rows.label[tile.first + row] = v;
+        float m = row16_max(v);
+        m = fmaxf(m, __shfl_xor(m, 16));
+        float s = row16_sum(exp_diff(v, m == -INFINITY ? 0.f : m));
+        s += __shfl_xor(s, 16);
+        if (lc == 0) red[wave * 64 + row] = {m, s};
+      }
+    __syncthreads();
+    if (tid < tile.rows) {
+      MaxSum a = red[tid];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) a = join(a, red[w * 64 + tid]);
+      to.part[static_cast<size_t>(ct) * to.places + tile.first + tid] = a;
+    }
+  } else {
+    store_low<RB>(
+        acc, smem, tid,
+        [&](int row, int col, float v) {
+          float c = n0 + col < to.vocab ? exp_diff(v, own.lse[row]) : 0.f;
+          const bool is_label = n0 + col == own.label[row];
+          if (is_label) c -= 1.f;
+          const half_t h = static_cast<half_t>(c * kCoeffScale);
+          if (is_label && row < tile.rows)
+            rows.label[tile.first + row] = c - static_cast<float>(h) * (1.f / kCoeffScale);
+          return h;
+        },
+        [&](int row, int col, half8_t v) {
+          if (row < tile.rows && n0 + col < to.v1)
+            *reinterpret_cast<half8_t*>(to.coeff + static_cast<size_t>(tile.first + row) * to.pitch + n0 + col - to.v0) = v;
+        });
+  }
+}
+
+template <int BITS, bool GRAD>
+__global__ __launch_bounds__(512, 4) void head_low_kernel(const half_t* __restrict__ x, int x_rows, int gathered,
+                                                          Layers layers, SlotPlan plan, HeadRows rows, HeadOut to) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x;
+  RowTile tile;
+  int ct;
+  if (!find_tile(plan, (to.v1 - to.v0 + 255) / 256, blockIdx.x, tile, ct)) return;
+  int32_t* words = reinterpret_cast<int32_t*>(smem + low_lds<BITS>() - kLowRowsLds);
+  const HeadTileRows own{words, words + 64, reinterpret_cast<float*>(words + 128)};
+  if (tid < 64) {
+    const int place = tile.first + min(tid, tile.rows - 1), m = plan.order[place];
+    own.source[tid] = gathered ? place : m;
+    own.label[tid] = rows.target[m];
+    if (GRAD) own.lse[tid] = rows.lse[m];
+  }
+  __syncthreads();
+  const int n0 = to.v0 + 256 * ct;
+  if (tile.rows > 32)
+    head_low_tile<2, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
+  else
+    head_low_tile<1, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
 }
 
 // Joins the column tiles of 64 places per workgroup, 16 of them side by side in a fixed
