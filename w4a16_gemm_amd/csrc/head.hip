@@ -102,7 +102,7 @@ int head_loss(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
     if (int rc = launch_head<BITS, false>(height, most_tiles(rows, 1, height), st, act ? mem.gathered : hx, rows, act, l, mem.plan,
                                           hr, to))
       return rc;
-    hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 64))), dim3(1024), 0, st, mem.part,
+    hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 16))), dim3(1024), 0, st, mem.part,
                        static_cast<int>(ceil_div(vocab, 256)), static_cast<size_t>(rows), mem.plan, mem.label, rows,
                        loss + m0, lse + m0);
   }

@@ -176,27 +176,40 @@ __device__ __forceinline__ void head_low_tile(const half_t* x, int x_rows, const
   __syncthreads();   // the ring's memory is used again
   const int lane = tid & 63, lc = lane & 31, lh = lane >> 5;
   if constexpr (!GRAD) {
-    const int col = n0 + 32 * wave + lc;
-    MaxSum* red = reinterpret_cast<MaxSum*>(smem);   // [wave][row]
+    // The logits turn in LDS, 4 bytes of padding per row of 256, so that a wavefront has whole
+    // rows, 4 columns per lane: two reductions over a wavefront per row of the tile that is
+    // there, where the accumulators' layout takes one per row and 32 columns (37 rows: 66 -> 56 us).
+    constexpr int PITCH = 260;
+    float* turn = reinterpret_cast<float*>(smem);
+    static_assert(64 * PITCH * 4 <= low_lds<BITS>() - kLowRowsLds, "fits the ring");
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = 32 * b + 8 * (r >> 2) + 4 * lh + (r & 3);
-        const float v = col < to.vocab ? acc.b[b][r] : -INFINITY;
-        if (own.label[row] == col && row < tile.rows) rows.label[tile.first + row] = v;
-        float m = row16_max(v);
-        m = fmaxf(m, __shfl_xor(m, 16));
-        float s = row16_sum(exp_diff(v, m == -INFINITY ? 0.f : m));
-        s += __shfl_xor(s, 16);
-        if (lc == 0) red[wave * 64 + row] = {m, s};
-      }
+      for (int r = 0; r < 16; ++r)
+        turn[(32 * b + 8 * (r >> 2) + 4 * lh + (r & 3)) * PITCH + 32 * wave + lc] = acc.b[b][r];
     __syncthreads();
-    if (tid < tile.rows) {
-      MaxSum a = red[tid];
+    const int col = n0 + 4 * lane;
+    for (int row = wave; row < tile.rows; row += 8) {
+      const float4_t l4 = *reinterpret_cast<const float4_t*>(turn + row * PITCH + 4 * lane);
+      float v[4], m = -INFINITY;
+      const int at = own.label[row] - col;
 #pragma unroll
-      for (int w = 1; w < 8; ++w) a = join(a, red[w * 64 + tid]);
-      to.part[static_cast<size_t>(ct) * to.places + tile.first + tid] = a;
+      for (int i = 0; i < 4; ++i) {
+        v[i] = col + i < to.vocab ? l4[i] : -INFINITY;
+        m = fmaxf(m, v[i]);
+        if (at == i) rows.label[tile.first + row] = v[i];
+      }
+      m = row16_max(m);
+      m = fmaxf(m, __shfl_xor(m, 16));
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float base = m == -INFINITY ? 0.f : m;
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += exp_diff(v[i], base);
+      s = row16_sum(s);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (lane == 0) to.part[static_cast<size_t>(ct) * to.places + tile.first + row] = {m, s};
     }
   } else {
     store_low<RB>(
@@ -241,19 +254,31 @@ __global__ __launch_bounds__(512, 4) void head_low_kernel(const half_t* __restri
     head_low_tile<1, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
 }
 
-// Joins the column tiles of 64 places per workgroup, 16 of them side by side in a fixed
+// Joins the column tiles of 16 places per workgroup, 64 of them side by side in a fixed
 // order; rows without a target get zeros.
 __global__ __launch_bounds__(1024) void head_join_kernel(const MaxSum* __restrict__ part, int tiles, size_t places,
                                                          SlotPlan plan, const float* __restrict__ label, int M,
                                                          float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ MaxSum red[16][64];
-  const int lane = threadIdx.x & 63, group = threadIdx.x >> 6;
-  const int p = blockIdx.x * 64 + lane, valid = plan.counts[1];
+  __shared__ MaxSum red[64][16];
+  const int at = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int p = blockIdx.x * 16 + at, valid = plan.counts[1];
   MaxSum a = {-INFINITY, 0.f};
-  if (p < valid)
-    for (int t = group; t < tiles; t += 16) a = join(a, part[static_cast<size_t>(t) * places + p]);
-  red[group][lane] = a;
+  if (p < valid) {
+    int t = group;
+    for (; t + 3 * 64 < tiles; t += 4 * 64) {
+      MaxSum v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = part[static_cast<size_t>(t + 64 * i) * places + p];
+      a = join(a, join(join(v[0], v[1]), join(v[2], v[3])));
+    }
+    for (; t < tiles; t += 64) a = join(a, part[static_cast<size_t>(t) * places + p]);
+  }
+  red[group][at] = a;
   __syncthreads();
+  for (int step = 32; step > 0; step >>= 1) {
+    if (group < step) red[group][at] = join(red[group][at], red[group + step][at]);
+    __syncthreads();
+  }
   if (group != 0 || p >= M) return;
   const int m = plan.order[p];
   if (p >= valid) {
@@ -261,7 +286,7 @@ __global__ __launch_bounds__(1024) void head_join_kernel(const MaxSum* __restric
     lse[m] = 0.f;
     return;
   }
-  for (int g = 1; g < 16; ++g) a = join(a, red[g][lane]);
+  a = red[0][at];
   const float v = a.m + __builtin_amdgcn_logf(a.s) * kLn2;
   lse[m] = v;
   loss[m] = v - label[p];

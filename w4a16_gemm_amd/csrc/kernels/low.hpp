@@ -1,16 +1,22 @@
 // Tiles of up to 64 rows by 256 outputs: y = x W^^T where the weights' stream bounds the
-// product (64 rows are 128 operations per byte of 4-bit codes, below what the matrix cores
+// product (64 rows are 256 operations per byte of 4-bit codes, below what the matrix cores
 // and the memory balance at).
 //  * The 8 wavefronts share the rows and split the outputs, 32 each, so that every weight is
 //    expanded once (in the tile of gemm.hpp two wavefronts expand the same columns), on
-//    32x32x16 MFMAs: lane (h, c) = (lane / 32, lane % 32) has channels [32 h + 8 s, +8) of
-//    output c in step s, as in the 32x32 tile there.
-//  * K advances in tiles of 64 channels through an LDS ring of low_stages() small stages: rows
-//    8 KB, codes 8 KB (16 KB at 8 bits), scales and zero points; two workgroups fit a compute
-//    unit, so one's start and end hide behind the other's loop.
-//  * Tile t is waited for and a barrier passed before tile t + stages - 1 is requested into the
-//    stage of tile t - 1, which every wavefront has left by then.
-// Measured, 37 rows against a head of 151936 outputs, K 1536: 112 us -> KEPT us in this tile.
+//    32x32x16 MFMAs: lane (h, c) = (lane / 32, lane % 32) has the 8 channels 64 v + 32 h +
+//    8 s of output c in step s of the v-th 64 channels of a stage.
+//  * K advances through an LDS ring in stages of 64 bytes of codes per output (128 channels
+//    at 4 bits, 64 at 8), so that four neighbouring lanes of a load take one whole piece of a
+//    row: stages of 64 channels, 32 bytes per row, were bound by the cache lines that a load
+//    touches and by the work per stage (37 rows against a head of 151936 outputs, K 1536: 80
+//    us against 66 us).  Two workgroups fit a compute unit, so one's start, end and waits
+//    hide behind the other's work.
+//  * Stage t is waited for and a barrier passed before stage t + COUNT - 1 is requested into
+//    the memory of stage t - 1, which every wavefront has left by then.
+//  * Rows: 16 bytes of 8 channels are a chunk; chunk j of row r lies at slot j ^ (r % 16) (8
+//    at 64 channels).  Codes: 16-byte part p of output n lies at slot p ^ (n / 4 % 4) of its
+//    four.  So 16 lanes that read one chunk of 16 rows, or one part of 16 outputs, meet
+//    distinct banks.
 #pragma once
 
 #include "experts.hpp"
@@ -19,12 +25,15 @@ namespace w4a16 {
 
 template <int BITS>
 struct LowStage {
-  static constexpr uint32_t A = 64 * 64 * 2;
-  static constexpr uint32_t C = 256 * 64 * BITS / 8;
-  static constexpr uint32_t S = 2 * 256 * 2;                    // [half][output]
-  static constexpr uint32_t Z = BITS == 4 ? 256 : 1024;         // [half][output], 64 lanes' loads
+  static constexpr int BK = 512 / BITS;                         // channels
+  static constexpr int HALVES = BK / 32;                        // 32-channel parts with a group each
+  static constexpr uint32_t ROW = BK * 2;
+  static constexpr uint32_t A = 64 * ROW;
+  static constexpr uint32_t C = 256 * 64;
+  static constexpr uint32_t S = HALVES * 256 * 2;               // [32 channels][output]
+  static constexpr uint32_t Z = BITS == 4 ? 512 : 1024;         // the same; whole wavefronts' loads
   static constexpr uint32_t BYTES = A + C + S + Z;
-  static constexpr int COUNT = BITS == 4 ? 4 : 3;               // two workgroups' rings in 160 KB
+  static constexpr int COUNT = BITS == 4 ? 2 : 3;               // two workgroups' rings in 160 KB
 };
 
 constexpr size_t kLowRowsLds = 4 * 64 * 4;   // four words per row, behind the ring
@@ -36,71 +45,84 @@ static_assert(low_lds<4>() <= 80 * 1024 && low_lds<8>() <= 80 * 1024, "two workg
 template <int BITS>
 struct LowLoader {
   using L = LowStage<BITS>;
-  static constexpr int CL = BITS / 4;   // code loads per thread and stage
+  static constexpr int BK = L::BK;
+  static constexpr int CPR = BK / 8;               // 16-byte chunks per row
+  static constexpr int AL = 64 * CPR / 512;        // row loads per thread and stage
+  static constexpr int SW = L::S / 1024;           // wavefronts that load scales, and then zero points
   __amdgpu_buffer_rsrc_t xr, qr;
   const half_t* s_ptr;
   const uint32_t* z_ptr;
-  Zeros zeros;
   unsigned char* smem;
-  int N, KT, gshift, wave, half;
-  uint32_t a_off, b_off[CL];
+  int K, KT, gshift, wave, part, s_pitch, z_pitch;
+  uint32_t a_off[AL], b_off[2];
 
   __device__ __forceinline__ LowLoader(const half_t* x, int x_rows, const Layers& l, unsigned char* smem_,
                                        const int32_t* source, int rows, int n0, int tid, int wave_)
-      : zeros(l.zeros), smem(smem_), N(l.N), KT(l.K / 64), gshift(l.gshift), wave(wave_) {
-    const int lane = tid & 63;
+      : smem(smem_), K(l.K), KT((l.K + L::BK - 1) / L::BK), gshift(l.gshift), wave(wave_), s_pitch(l.N) {
+    const int lane = tid & 63, N = l.N;
     const uint32_t pitch = static_cast<uint32_t>(l.K) * BITS / 8;
     xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<half_t*>(x), 0,
                                            static_cast<int>(static_cast<uint32_t>(x_rows) * l.K * 2u), kBufferWord3);
     qr = __builtin_amdgcn_make_buffer_rsrc(
         reinterpret_cast<unsigned char*>(const_cast<uint32_t*>(l.qw)) + static_cast<size_t>(n0) * pitch, 0,
-        static_cast<int>(static_cast<uint32_t>(min(256, l.N - n0)) * pitch), kBufferWord3);
-    // rows: chunk tid = 8 row + slot receives the row's chunk slot ^ (row % 8)
-    const int row = tid >> 3, slot = tid & 7;
-    a_off = (static_cast<uint32_t>(source[min(row, rows - 1)]) * l.K + 8 * (slot ^ (row & 7))) * 2u;
-    // codes: chunk c = part * 256 + output holds the part's channels (32 at 4 bits, 16 at 8)
+        static_cast<int>(static_cast<uint32_t>(min(256, N - n0)) * pitch), kBufferWord3);
 #pragma unroll
-    for (int i = 0; i < CL; ++i) {
-      const int c = tid + 512 * i;
-      b_off[i] = static_cast<uint32_t>(min(c % 256, l.N - 1 - n0)) * pitch + 16u * (c / 256);
+    for (int i = 0; i < AL; ++i) {
+      const int c = tid + 512 * i, row = c / CPR, slot = c % CPR;
+      a_off[i] = (static_cast<uint32_t>(source[min(row, rows - 1)]) * l.K + 8 * (slot ^ (row & (CPR - 1)))) * 2u;
     }
-    half = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = tid + 512 * i, n = c >> 2, slot = c & 3;
+      b_off[i] = static_cast<uint32_t>(min(n, N - 1 - n0)) * pitch + 16u * (slot ^ ((n >> 2) & 3));
+    }
+    // scales: wavefronts 0 .. SW - 1, two 32-channel parts each, 8 outputs per lane; zero
+    // points: the wavefronts after them, 4 bits: two parts each, 8 outputs per lane, 8 bits:
+    // both parts, 16 outputs per lane and half a wavefront
+    const int h = lane >> 5;
+    part = wave < SW ? 2 * wave + h : BITS == 4 ? 2 * (wave - SW) + h : (lane >> 4) & 1;
     s_ptr = l.scales + min(n0 + 8 * (lane & 31), N - 8);
-    const int n = BITS == 4 ? min(n0 / 8 + (lane & 31), N / 8 - 1) : min(n0 / 4 + 4 * (lane & 31), N / 4 - 4);
-    z_ptr = l.zeros.words + (l.zeros.sym ? 0 : n);
+    const int zn = BITS == 4 ? min(n0 / 8 + (lane & 31), N / 8 - 1) : min(n0 / 4 + 4 * (lane & 15), N / 4 - 4);
+    z_ptr = l.zeros.words + (l.zeros.sym ? 0 : zn);
+    z_pitch = l.zeros.sym ? 0 : N / (32 / BITS);
   }
 
-  // Tile t to stage t % COUNT; past the end the last one again.
+  // Stage t to memory t % COUNT; past the end the last one again.  Channels past K (the last
+  // stage of K % 128 = 64) are read from within the buffers and not used.
   __device__ __forceinline__ void load(int t) const {
     unsigned char* stage = smem + (t % L::COUNT) * L::BYTES;
     const int tc = min(t, KT - 1);
-    const int g = (tc * 64 + 32 * half) >> gshift;
-    if (wave == 0)
-      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(s_ptr + static_cast<size_t>(g) * N),
-                                       reinterpret_cast<void*>(stage + L::A + L::C), 16, 0, 0);
-    else if (wave == 1) {
-      const uint32_t* z = z_ptr + (zeros.sym ? 0 : static_cast<size_t>(g) * (N / (32 / BITS)));
+    const int g = min(tc * L::BK + 32 * part, K - 1) >> gshift;
+    unsigned char* scales = stage + L::A + L::C;
+    unsigned char* zeros = scales + L::S;
+    unsigned char* codes = stage + L::A;
+    if (wave < SW)
+      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(s_ptr + static_cast<size_t>(g) * s_pitch),
+                                       reinterpret_cast<void*>(scales + wave * 1024), 16, 0, 0);
+    else if (wave < 2 * SW) {
+      const uint32_t* z = z_ptr + static_cast<size_t>(g) * z_pitch;
       if constexpr (BITS == 4)
         __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z),
-                                         reinterpret_cast<void*>(stage + L::A + L::C + L::S), 4, 0, 0);
+                                         reinterpret_cast<void*>(zeros + (wave - SW) * 256), 4, 0, 0);
       else
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z),
-                                         reinterpret_cast<void*>(stage + L::A + L::C + L::S), 16, 0, 0);
+        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z), reinterpret_cast<void*>(zeros), 16, 0, 0);
     }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, as_lds(stage + wave * 1024), 16, static_cast<int>(a_off), tc * 128, 0, 0);
-    unsigned char* codes = stage + L::A;
 #pragma unroll
-    for (int i = 0; i < CL; ++i)
+    for (int i = 0; i < AL; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, as_lds(stage + (512 * i + wave * 64) * 16), 16,
+                                               static_cast<int>(a_off[i]), tc * (BK * 2), 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, as_lds(codes + (512 * i + wave * 64) * 16), 16,
-                                               static_cast<int>(b_off[i]), tc * (8 * BITS), 0, 0);
+                                               static_cast<int>(b_off[i]), tc * 64, 0, 0);
   }
 
-  // Waits for this wavefront's loads of all but the newest COUNT - 2 tiles.
+  // Waits for this wavefront's loads of all but the newest COUNT - 2 stages.
   __device__ __forceinline__ void wait() const {
-    if (wave < 2)
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::COUNT - 2) * (CL + 2)) : "memory");
+    if (wave < 2 * SW)
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::COUNT - 2) * (AL + 3)) : "memory");
     else
-      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::COUNT - 2) * (CL + 1)) : "memory");
+      asm volatile("s_waitcnt vmcnt(%0)" ::"n"((L::COUNT - 2) * (AL + 2)) : "memory");
   }
 };
 
@@ -115,16 +137,14 @@ template <int BITS, int RB>
 __device__ __forceinline__ void low_product(const LowLoader<BITS>& ld, Zeros zeros, unsigned char* smem, int tid, int wave,
                                             LowSums<RB>& acc) {
   using L = LowStage<BITS>;
+  constexpr int CPR = L::BK / 8;
   const int lane = tid & 63, lc = lane & 31, lh = lane >> 5;
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc.b[b][r] = 0.f;
   const int col = wave * 32 + lc;
-  const uint32_t a_lane = lc * 128;
-  const uint32_t c_lane = L::A + ((BITS == 4 ? lh : 2 * lh) * 256 + col) * 16;
-  const uint32_t s_lane = L::A + L::C + (lh * 256 + col) * 2;
-  const uint32_t z_lane = L::A + L::C + L::S + (BITS == 4 ? (lh * 32 + (col >> 3)) * 4 : lh * 512 + col);
+  const int a_swz = lc & (CPR - 1), c_swz = (col >> 2) & 3;
 #pragma unroll
   for (int t = 0; t < L::COUNT - 1; ++t) ld.load(t);
   DequantConsts dc;
@@ -135,43 +155,56 @@ __device__ __forceinline__ void low_product(const LowLoader<BITS>& ld, Zeros zer
     block_barrier();
     ld.load(t + L::COUNT - 1);
     const unsigned char* st = smem + (t % L::COUNT) * L::BYTES;
-    uint4 cw[BITS / 4];
-    cw[0] = *reinterpret_cast<const uint4*>(st + c_lane);
-    if constexpr (BITS == 8) cw[1] = *reinterpret_cast<const uint4*>(st + c_lane + 4096);
-    if (((t * 64) & gmask) == 0) {
-      const uint32_t sc = *reinterpret_cast<const uint16_t*>(st + s_lane);
-      uint32_t z;
-      if constexpr (BITS == 4)
-        z = (zeros.word(*reinterpret_cast<const uint32_t*>(st + z_lane)) >> (4 * (lc & 7))) & 0xFu;
-      else
-        z = zeros.sym ? 128u : *(st + z_lane);
-      dc = make_consts(z, __builtin_bit_cast(half_t, static_cast<uint16_t>(sc)));
-    }
-    half8_t af[2][RB];
+    const unsigned char* rows = st + lc * L::ROW;
+    const unsigned char* codes = st + L::A + col * 64;
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-      af[0][b] = *reinterpret_cast<const half8_t*>(st + a_lane + 4096 * b + 16 * ((4 * lh) ^ (lc & 7)));
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (s < 3) {
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-          af[(s + 1) & 1][b] = *reinterpret_cast<const half8_t*>(st + a_lane + 4096 * b + 16 * ((4 * lh + s + 1) ^ (lc & 7)));
-      }
-      __builtin_amdgcn_sched_barrier(0);   // keep the reads ahead of this step's MFMAs
-      half8_t w;
+    for (int v = 0; v < L::BK / 64; ++v) {   // 64 channels at a time
+      if (v > 0 && t * L::BK + 64 * v >= ld.K) break;
+      uint4 cw[BITS / 4];   // 4 bits: part 2 v + h; 8 bits: parts 2 h and 2 h + 1
       if constexpr (BITS == 4) {
-        w = dequant_word(s == 0 ? cw[0].x : s == 1 ? cw[0].y : s == 2 ? cw[0].z : cw[0].w, dc);
+        cw[0] = *reinterpret_cast<const uint4*>(codes + 16 * ((2 * v + lh) ^ c_swz));
       } else {
-        const uint4 q = cw[s >> 1];
-        const half4_t lo = dequant_word8((s & 1) ? q.z : q.x, dc), hi = dequant_word8((s & 1) ? q.w : q.y, dc);
-        w = half8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        cw[0] = *reinterpret_cast<const uint4*>(codes + 16 * ((2 * lh) ^ c_swz));
+        cw[1] = *reinterpret_cast<const uint4*>(codes + 16 * ((2 * lh + 1) ^ c_swz));
       }
+      if (((t * L::BK + 64 * v) & gmask) == 0) {
+        const int half = 2 * v + lh;
+        const uint32_t sc = *reinterpret_cast<const uint16_t*>(st + L::A + L::C + (half * 256 + col) * 2);
+        const unsigned char* zs = st + L::A + L::C + L::S;
+        uint32_t z;
+        if constexpr (BITS == 4)
+          z = (zeros.word(*reinterpret_cast<const uint32_t*>(zs + (half * 32 + (col >> 3)) * 4)) >> (4 * (lc & 7))) & 0xFu;
+        else
+          z = zeros.sym ? 128u : *(zs + half * 256 + col);
+        dc = make_consts(z, __builtin_bit_cast(half_t, static_cast<uint16_t>(sc)));
+      }
+      half8_t af[2][RB];
 #pragma unroll
-      for (int b = 0; b < RB; ++b) acc.b[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[s & 1][b], w, acc.b[b], 0, 0, 0);
+      for (int b = 0; b < RB; ++b)
+        af[0][b] = *reinterpret_cast<const half8_t*>(rows + 32 * L::ROW * b + 16 * ((8 * v + 4 * lh) ^ a_swz));
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        if (s < 3) {
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            af[(s + 1) & 1][b] =
+                *reinterpret_cast<const half8_t*>(rows + 32 * L::ROW * b + 16 * ((8 * v + 4 * lh + s + 1) ^ a_swz));
+        }
+        __builtin_amdgcn_sched_barrier(0);   // keep the reads ahead of this step's MFMAs
+        half8_t w;
+        if constexpr (BITS == 4) {
+          w = dequant_word(s == 0 ? cw[0].x : s == 1 ? cw[0].y : s == 2 ? cw[0].z : cw[0].w, dc);
+        } else {
+          const uint4 q = cw[s >> 1];
+          const half4_t lo = dequant_word8((s & 1) ? q.z : q.x, dc), hi = dequant_word8((s & 1) ? q.w : q.y, dc);
+          w = half8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        }
+#pragma unroll
+        for (int b = 0; b < RB; ++b) acc.b[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[s & 1][b], w, acc.b[b], 0, 0, 0);
+      }
     }
   }
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the clamped loads past the last tile
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // the clamped loads past the last stage
 }
 
 // Rows of 32 outputs of a wavefront as runs of 8, turned in LDS as in store_tile.
