@@ -1,0 +1,67 @@
+// Loads from global memory straight into LDS, written as inline asm.
+//
+// With the builtins the compiler knows that such a load writes LDS but not which part of it,
+// and waits for all of them (s_waitcnt vmcnt(0)) before every LDS read that it sees, prefetches
+// of later tiles included: a ring filled ahead of its use is then not ahead at all.  As asm
+// the loads are ordered by what the kernel says: each statement clobbers memory, so no LDS read
+// moves across it, and the kernel's own s_waitcnt vmcnt(N) and barrier come between a load and
+// the reads of what it wrote.  The loads have no result registers, and their operands are read
+// when they are issued, so nothing of them is in flight in registers.  Loads that the compiler
+// issues itself are waited for correctly beside them: it counts fewer loads in flight than
+// there are, so its waits are longer than needed, never shorter.
+//
+// The destination is the LDS byte offset in m0 plus 16 (4) bytes per lane; writing m0 takes
+// one wait state before a load that reads it.
+// Measured (whole calls): KEPT
+#pragma once
+
+#include "nibbles.hpp"
+
+namespace w4a16 {
+
+// Buffer descriptor of `bytes` bytes from p, in scalar registers.
+__device__ __forceinline__ u32x4_t direct_rsrc(const void* p, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  u32x4_t r;
+  r[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+  r[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32) & 0xFFFFu);
+  r[2] = __builtin_amdgcn_readfirstlane(bytes);
+  r[3] = kBufferWord3;
+  return r;
+}
+
+// 16 bytes per lane from byte `lane_off + off` of the buffer; lds and off are the same in
+// every lane.
+__device__ __forceinline__ void direct_load16(u32x4_t rsrc, uint32_t lds, uint32_t lane_off, uint32_t off) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n"
+      "s_nop 0\n"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(lane_off), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(off))
+      : "memory");
+}
+
+// BYTES = 16 or 4 per lane from the lane's own address.
+template <int BYTES>
+__device__ __forceinline__ void direct_load(const void* p, uint32_t lds) {
+  static_assert(BYTES == 16 || BYTES == 4, "16 or 4 bytes per lane");
+  if constexpr (BYTES == 16)
+    asm volatile(
+        "s_mov_b32 m0, %0\n"
+        "s_nop 0\n"
+        "global_load_lds_dwordx4 %1, off"
+        :
+        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p)
+        : "memory");
+  else
+    asm volatile(
+        "s_mov_b32 m0, %0\n"
+        "s_nop 0\n"
+        "global_load_lds_dword %1, off"
+        :
+        : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p)
+        : "memory");
+}
+
+}  // namespace w4a16

@@ -19,6 +19,7 @@
 //    distinct banks.
 #pragma once
 
+#include "direct.hpp"
 #include "experts.hpp"
 
 namespace w4a16 {
@@ -49,23 +50,21 @@ struct LowLoader {
   static constexpr int CPR = BK / 8;               // 16-byte chunks per row
   static constexpr int AL = 64 * CPR / 512;        // row loads per thread and stage
   static constexpr int SW = L::S / 1024;           // wavefronts that load scales, and then zero points
-  __amdgpu_buffer_rsrc_t xr, qr;
+  u32x4_t xr, qr;
   const half_t* s_ptr;
   const uint32_t* z_ptr;
-  unsigned char* smem;
+  uint32_t ring;   // LDS offset
   int K, KT, gshift, wave, part, s_pitch, z_pitch;
   uint32_t a_off[AL], b_off[2];
 
   __device__ __forceinline__ LowLoader(const half_t* x, int x_rows, const Layers& l, unsigned char* smem_,
                                        const int32_t* source, int rows, int n0, int tid, int wave_)
-      : smem(smem_), K(l.K), KT((l.K + L::BK - 1) / L::BK), gshift(l.gshift), wave(wave_), s_pitch(l.N) {
+      : ring(lds_offset(smem_)), K(l.K), KT((l.K + L::BK - 1) / L::BK), gshift(l.gshift), wave(wave_), s_pitch(l.N) {
     const int lane = tid & 63, N = l.N;
     const uint32_t pitch = static_cast<uint32_t>(l.K) * BITS / 8;
-    xr = __builtin_amdgcn_make_buffer_rsrc(const_cast<half_t*>(x), 0,
-                                           static_cast<int>(static_cast<uint32_t>(x_rows) * l.K * 2u), kBufferWord3);
-    qr = __builtin_amdgcn_make_buffer_rsrc(
-        reinterpret_cast<unsigned char*>(const_cast<uint32_t*>(l.qw)) + static_cast<size_t>(n0) * pitch, 0,
-        static_cast<int>(static_cast<uint32_t>(min(256, N - n0)) * pitch), kBufferWord3);
+    xr = direct_rsrc(x, static_cast<uint32_t>(x_rows) * l.K * 2u);
+    qr = direct_rsrc(reinterpret_cast<const unsigned char*>(l.qw) + static_cast<size_t>(n0) * pitch,
+                     static_cast<uint32_t>(min(256, N - n0)) * pitch);
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
       const int c = tid + 512 * i, row = c / CPR, slot = c % CPR;
@@ -90,31 +89,18 @@ struct LowLoader {
   // Stage t to memory t % COUNT; past the end the last one again.  Channels past K (the last
   // stage of K % 128 = 64) are read from within the buffers and not used.
   __device__ __forceinline__ void load(int t) const {
-    unsigned char* stage = smem + (t % L::COUNT) * L::BYTES;
+    const uint32_t stage = ring + (t % L::COUNT) * L::BYTES;
     const int tc = min(t, KT - 1);
-    const int g = min(tc * L::BK + 32 * part, K - 1) >> gshift;
-    unsigned char* scales = stage + L::A + L::C;
-    unsigned char* zeros = scales + L::S;
-    unsigned char* codes = stage + L::A;
+    const int g = min(tc * BK + 32 * part, K - 1) >> gshift;
+    const uint32_t scales = stage + L::A + L::C, zeros = scales + L::S;
     if (wave < SW)
-      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(s_ptr + static_cast<size_t>(g) * s_pitch),
-                                       reinterpret_cast<void*>(scales + wave * 1024), 16, 0, 0);
-    else if (wave < 2 * SW) {
-      const uint32_t* z = z_ptr + static_cast<size_t>(g) * z_pitch;
-      if constexpr (BITS == 4)
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z),
-                                         reinterpret_cast<void*>(zeros + (wave - SW) * 256), 4, 0, 0);
-      else
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z), reinterpret_cast<void*>(zeros), 16, 0, 0);
-    }
+      direct_load<16>(s_ptr + static_cast<size_t>(g) * s_pitch, scales + wave * 1024);
+    else if (wave < 2 * SW)
+      direct_load<BITS == 4 ? 4 : 16>(z_ptr + static_cast<size_t>(g) * z_pitch, BITS == 4 ? zeros + (wave - SW) * 256 : zeros);
 #pragma unroll
-    for (int i = 0; i < AL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, as_lds(stage + (512 * i + wave * 64) * 16), 16,
-                                               static_cast<int>(a_off[i]), tc * (BK * 2), 0, 0);
+    for (int i = 0; i < AL; ++i) direct_load16(xr, stage + (512 * i + wave * 64) * 16, a_off[i], tc * (BK * 2));
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, as_lds(codes + (512 * i + wave * 64) * 16), 16,
-                                               static_cast<int>(b_off[i]), tc * 64, 0, 0);
+    for (int i = 0; i < 2; ++i) direct_load16(qr, stage + L::A + (512 * i + wave * 64) * 16, b_off[i], tc * 64);
   }
 
   // Waits for this wavefront's loads of all but the newest COUNT - 2 stages.

@@ -23,6 +23,7 @@
 // constants, which here change with every output n instead of staying with the lane.
 #pragma once
 
+#include "direct.hpp"
 #include "experts.hpp"
 
 namespace w4a16 {
@@ -50,26 +51,22 @@ struct TLoader {
   static constexpr int APT = 32 * MB / 64;   // activation chunks (16 B) per thread and stage
   static constexpr int CL = BITS / 4;        // code loads per thread and stage
 
-  __amdgpu_buffer_rsrc_t ar, qr;
+  u32x4_t ar, qr;
   const half_t* s_ptr;      // this lane's scales of tile 0 (wavefront 0)
   const uint32_t* z_ptr;    // this lane's zero points of tile 0 (wavefront 1)
-  unsigned char* smem;
+  uint32_t ring;            // LDS offset
   int KT, wave, s_step, z_step, s_tail, z_tail;
   uint32_t a_off[APT], b_off[CL], b_tail[CL], b_step;
 
   __device__ __forceinline__ TLoader(const half_t* a, int a_rows, int a_pitch, int a0, const Layers& l, int n_begin,
                                      int n_end, int k0, const int32_t* source, int rows, unsigned char* smem_, int tid,
                                      int wave_)
-      : smem(smem_), KT((n_end - n_begin + 63) / 64), wave(wave_) {
+      : ring(lds_offset(smem_)), KT((n_end - n_begin + 63) / 64), wave(wave_) {
     const int lane = tid & 63;
     const uint32_t pitch = static_cast<uint32_t>(l.K) * BITS / 8;   // code bytes of a row
-    ar = __builtin_amdgcn_make_buffer_rsrc(const_cast<half_t*>(a + a0), 0,
-                                           static_cast<int>((static_cast<uint32_t>(a_rows) * a_pitch - a0) * 2u),
-                                           kBufferWord3);
-    const size_t first = static_cast<size_t>(n_begin) * pitch;
-    qr = __builtin_amdgcn_make_buffer_rsrc(
-        reinterpret_cast<unsigned char*>(const_cast<uint32_t*>(l.qw)) + first, 0,
-        static_cast<int>(static_cast<uint32_t>(n_end - n_begin) * pitch), kBufferWord3);
+    ar = direct_rsrc(a + a0, (static_cast<uint32_t>(a_rows) * a_pitch - a0) * 2u);
+    qr = direct_rsrc(reinterpret_cast<const unsigned char*>(l.qw) + static_cast<size_t>(n_begin) * pitch,
+                     static_cast<uint32_t>(n_end - n_begin) * pitch);
 #pragma unroll
     for (int i = 0; i < APT; ++i) {
       const int c = (wave * APT + i) * 64 + lane;
@@ -109,31 +106,20 @@ struct TLoader {
   // Tile t to stage t % 3; tiles past the end re-load the last one.  The scale and zero-point
   // loads come first: waiting for tile t never waits for more than those of tile t + 1.
   __device__ __forceinline__ void load(int t) const {
-    unsigned char* stage = smem + (t % 3) * L::BYTES;
+    const uint32_t stage = ring + (t % 3) * L::BYTES;
     const int tc = min(t, KT - 1);
     const bool tail = tc == KT - 1;
+    const uint32_t scales = stage + L::A + L::C;
     if (wave == 0)
-      __builtin_amdgcn_global_load_lds(
-          reinterpret_cast<const void*>(s_ptr + static_cast<ptrdiff_t>(tc) * s_step + (tail ? s_tail : 0)),
-          reinterpret_cast<void*>(stage + L::A + L::C), 16, 0, 0);
-    else if (wave == 1) {
-      const uint32_t* z = z_ptr + static_cast<ptrdiff_t>(tc) * z_step + (tail ? z_tail : 0);
-      if constexpr (BITS == 4)
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z),
-                                         reinterpret_cast<void*>(stage + L::A + L::C + L::S), 4, 0, 0);
-      else
-        __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(z),
-                                         reinterpret_cast<void*>(stage + L::A + L::C + L::S), 16, 0, 0);
-    }
+      direct_load<16>(s_ptr + static_cast<ptrdiff_t>(tc) * s_step + (tail ? s_tail : 0), scales);
+    else if (wave == 1)
+      direct_load<BITS == 4 ? 4 : 16>(z_ptr + static_cast<ptrdiff_t>(tc) * z_step + (tail ? z_tail : 0), scales + L::S);
 #pragma unroll
-    for (int i = 0; i < APT; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, as_lds(stage + (wave * APT + i) * 1024), 16,
-                                               static_cast<int>(a_off[i]), tc * 128, 0, 0);
+    for (int i = 0; i < APT; ++i) direct_load16(ar, stage + (wave * APT + i) * 1024, a_off[i], tc * 128);
 #pragma unroll
     for (int i = 0; i < CL; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, as_lds(stage + L::A + wave * L::CHUNK + i * 1024), 16,
-                                               static_cast<int>(tail ? b_tail[i] : b_off[i]),
-                                               static_cast<int>(static_cast<uint32_t>(tc) * b_step), 0, 0);
+      direct_load16(qr, stage + L::A + wave * L::CHUNK + i * 1024, tail ? b_tail[i] : b_off[i],
+                    static_cast<uint32_t>(tc) * b_step);
   }
 };
 
