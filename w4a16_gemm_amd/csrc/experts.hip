@@ -130,9 +130,9 @@ template <int NB, int BITS>
 int launch_forward(dim3 grid, hipStream_t st, const half_t* x, int x_rows, int gathered, int T, const Layers& l,
                    const SlotPlan& plan, half_t* y) {
   auto kern = experts_gemm_kernel<NB, BITS>;
-  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), experts_lds<BITS>());
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), tile_lds<BITS>());
   if (int rc = lds_status(lds_ok)) return rc;
-  hipLaunchKernelGGL(kern, grid, dim3(512), experts_lds<BITS>(), st, x, x_rows, gathered, T, l, plan, y);
+  hipLaunchKernelGGL(kern, grid, dim3(512), tile_lds<BITS>(), st, x, x_rows, gathered, T, l, plan, y);
   return check_launch("experts launch");
 }
 

@@ -64,9 +64,9 @@ template <int BITS, bool GRAD>
 int launch_head(int height, int64_t row_tiles, hipStream_t st, const half_t* x, int x_rows, bool gathered,
                 const Layers& l, const SlotPlan& plan, const HeadRows& rows, const HeadOut& to) {
   auto kern = height == 64 ? head_low_kernel<BITS, GRAD> : head_kernel<BITS, GRAD>;
-  const size_t lds = height == 64 ? low_lds<BITS>() : experts_lds<BITS>();
+  const size_t lds = height == 64 ? low_lds<BITS>() : tile_lds<BITS>();
   static const hipError_t low_ok = allow_lds(reinterpret_cast<const void*>(head_low_kernel<BITS, GRAD>), low_lds<BITS>());
-  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(head_kernel<BITS, GRAD>), experts_lds<BITS>());
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(head_kernel<BITS, GRAD>), tile_lds<BITS>());
   if (int rc = lds_status(height == 64 ? low_ok : lds_ok)) return rc;
   const dim3 grid(static_cast<unsigned>(up8(row_tiles * ceil_div(to.v1 - to.v0, 256))));
   hipLaunchKernelGGL(kern, grid, dim3(512), lds, st, x, x_rows, gathered ? 1 : 0, l, plan, rows, to);

@@ -1,39 +1,11 @@
-// Products grouped by expert: y[slot] = x[slot / T] W^_e^T on the large tile of gemm.hpp, a
-// workgroup per row tile of the plan and 256 (64 NB) output channels.
-//  * The rows of a tile lie anywhere in x: the loader's lane offsets are those of the rows
-//    of its slots, fixed over the K loop, so the gather costs nothing there.  Results go to
-//    the slots' rows of y.
-//  * A row's result does not depend on the other rows of its tile, and neither on the place
-//    of the row in it: the same bits whatever else is in the batch, for one tile height.
-//  * Tiles of 256 rows take the 16x16x32 product, smaller ones of 4-bit weights the 32x32x16
-//    product, as in the layer itself.
+// Products grouped by expert: y[slot] = x[slot / T] W^_e^T, a workgroup per row tile of the
+// plan and 256 (64 NB) output channels, results to the slots' rows of y.  Tiles of 256 rows
+// take the 16x16x32 product, smaller ones the 32x32x16 product (tile.hpp).
 #pragma once
 
-#include "gemm.hpp"
-#include "plan.hpp"
+#include "tile.hpp"
 
 namespace w4a16 {
-
-constexpr size_t kTileRowsLds = 4 * kBigBM * 4;   // four words per row of the tile, behind the ring
-
-template <int BITS>
-constexpr size_t experts_lds() { return static_cast<size_t>(kBigStages) * big_stage_bytes<BITS>() + kTileRowsLds; }
-
-// Loader of a tile whose rows are rows source[0 .. rows) of x (LDS), x_rows rows in all.
-template <int NB, int MB, int BITS>
-__device__ __forceinline__ BigLoader<NB, MB, BITS> rows_loader(const half_t* x, int x_rows, const Layers& l,
-                                                               unsigned char* smem, const int32_t* source, int rows,
-                                                               int n0, int n_end, int tid, int wave) {
-  using Loader = BigLoader<NB, MB, BITS>;
-  Loader ld(x, l.qw, l.scales, l.zeros, smem, x_rows, l.N, l.K, l.gshift, 0, n0, n_end, tid, wave);
-#pragma unroll
-  for (int i = 0; i < Loader::APT; ++i) {
-    const int c = (wave * Loader::APT + i) * 64 + (tid & 63);
-    const int row = c >> 3, slot = c & 7;
-    ld.a_off[i] = (static_cast<uint32_t>(source[min(row, rows - 1)]) * l.K + 8 * (slot ^ (row & 7))) * 2u;
-  }
-  return ld;
-}
 
 // Stores a tile of accumulators as binary16: value(row, column, v) -> binary16 of the tile's
 // row and column, put(row, column, run of 8 columns) stores them.  An accumulator register
@@ -99,20 +71,20 @@ __device__ __forceinline__ void experts_tile(const half_t* x, int x_rows, const 
                                              const int32_t* source, const int32_t* slots, int rows, int n0) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const auto ld = rows_loader<NB, MB, BITS>(x, x_rows, l, smem, source, rows, n0, l.N, tid, wave);
+  const TileLoader<NB, MB, BITS> ld(x, x_rows, l, smem, source, rows, n0, tid, wave);
   const int N = l.N;
   auto value = [&](int, int, float v) { return static_cast<half_t>(v); };
   auto put = [&](int row, int col, half8_t v) {
     if (row < rows && n0 + col < N) *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slots[row]) * N + n0 + col) = v;
   };
-  if constexpr (MB < 8 && BITS == 4 && NB % 2 == 0) {
+  if constexpr (MB < 8 && NB % 2 == 0) {
     f32x16_t acc[MB / 2][NB / 2];
-    big_tile32_product<NB, MB>(ld, l.zeros, smem, l.K, l.gshift, tid, wave, 1, acc);
+    tile_product32(ld, l.zeros, smem, tid, wave, acc);
     __syncthreads();
     store_tile32<NB, MB>(acc, smem, tid, value, put);
   } else {
     float4_t acc[MB][NB];
-    big_tile_product<NB, MB, BITS>(ld, l.zeros, smem, l.K, l.gshift, tid, wave, 1, acc);
+    tile_product(ld, l.zeros, smem, tid, wave, acc);
     __syncthreads();
     store_tile<NB, MB>(acc, smem, tid, value, put);
   }
@@ -129,8 +101,8 @@ __global__ __launch_bounds__(512) void experts_gemm_kernel(const half_t* __restr
   RowTile tile;
   int col;
   if (!find_tile(plan, (N + BN - 1) / BN, blockIdx.x, tile, col)) return;
-  int32_t* slots = reinterpret_cast<int32_t*>(smem + experts_lds<BITS>() - kTileRowsLds);
-  int32_t* source = slots + kBigBM;
+  int32_t* slots = reinterpret_cast<int32_t*>(smem + tile_lds<BITS>() - kTileRowsLds);
+  int32_t* source = slots + 256;
   if (tid < tile.rows) {
     const int s = plan.order[tile.first + tid];
     slots[tid] = s;

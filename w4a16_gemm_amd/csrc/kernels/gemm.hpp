@@ -500,9 +500,10 @@ struct BigLoader {
 // takes words 2s and 2s + 1; zero points are bytes; LDS read with plain loads at every
 // tile height.
 template <int NB, int MB, int BITS = 4>
-__device__ __forceinline__ void big_tile_product(const BigLoader<NB, MB, BITS>& ld, Zeros qzeros, unsigned char* smem,
-                                                 int K, int gshift, int tid, int wave, int prio,
-                                                 float4_t (&acc)[MB][NB]) {
+__device__ __forceinline__ void big_tile(const half_t* __restrict__ x, const uint32_t* __restrict__ qw,
+                                         const half_t* __restrict__ scales, Zeros qzeros,
+                                         half_t* __restrict__ y, int M, int N, int K, int gshift, int m0, int n0,
+                                         int n_end, int prio) {
   // NB 16-column blocks and MB 16-row blocks per wavefront: the tile is BM x BN with
   // BM = 32 MB and BN = 64 NB.  MB = 8 reads LDS through the inline-asm blocks above;
   // the smaller tiles (few-row batches) use plain loads, which the compiler orders
@@ -512,14 +513,19 @@ __device__ __forceinline__ void big_tile_product(const BigLoader<NB, MB, BITS>& 
   constexpr int BL = Loader::BL, NS = Loader::NS, APT = Loader::APT, CL = Loader::CL;
   constexpr uint32_t STAGE = Loader::STAGE, LB = Loader::LB;
   constexpr bool kAsmReads = MB == 8 && BITS == 4;
+  extern __shared__ __align__(16) unsigned char smem[];
 
+  const int tid = threadIdx.x;
   const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int lr = lane & 15;
   const int lq = lane >> 4;
   const int KT = K / kBigBK;
+  const Loader ld(x, qw, scales, qzeros, smem, M, N, K, gshift, m0, n0, n_end, tid, wave);
   auto load_tile = [&](int t) { ld.load(t); };
 
+  float4_t acc[MB][NB];
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -617,23 +623,6 @@ __device__ __forceinline__ void big_tile_product(const BigLoader<NB, MB, BITS>& 
   }
   // the clamped loads past the last tile must land before the workgroup's LDS is released
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-}
-
-template <int NB, int MB, int BITS = 4>
-__device__ __forceinline__ void big_tile(const half_t* __restrict__ x, const uint32_t* __restrict__ qw,
-                                         const half_t* __restrict__ scales, Zeros qzeros,
-                                         half_t* __restrict__ y, int M, int N, int K, int gshift, int m0, int n0,
-                                         int n_end, int prio) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
-  const int lr = lane & 15;
-  const int lq = lane >> 4;
-  const BigLoader<NB, MB, BITS> ld(x, qw, scales, qzeros, smem, M, N, K, gshift, m0, n0, n_end, tid, wave);
-  float4_t acc[MB][NB];
-  big_tile_product<NB, MB, BITS>(ld, qzeros, smem, K, gshift, tid, wave, prio, acc);
 
   // D layout of the 16x16 MFMA: lane l holds rows 4*(l/16) + r, column l % 16.
   const int nw = n0 + wn * 16 * NB;
@@ -667,21 +656,27 @@ __device__ __forceinline__ void big_tile(const half_t* __restrict__ x, const uin
 //  * D layout of the 32x32 MFMA: lane l holds column l % 32 and, in register r, row
 //    8 (r / 4) + 4 (l / 32) + r % 4.
 template <int NB, int MB>
-__device__ __forceinline__ void big_tile32_product(const BigLoader<NB, MB, 4>& ld, Zeros qzeros, unsigned char* smem,
-                                                   int K, int gshift, int tid, int wave, int prio,
-                                                   f32x16_t (&acc)[MB / 2][NB / 2]) {
+__device__ __forceinline__ void big_tile32(const half_t* __restrict__ x, const uint32_t* __restrict__ qw,
+                                           const half_t* __restrict__ scales, Zeros qzeros,
+                                           half_t* __restrict__ y, int M, int N, int K, int gshift, int m0, int n0,
+                                           int n_end, int prio) {
   using Loader = BigLoader<NB, MB, 4>;
   constexpr int BL = Loader::BL, NS = Loader::NS, APT = Loader::APT, CL = Loader::CL;
   constexpr uint32_t STAGE = Loader::STAGE, LB = Loader::LB;
   static_assert(NB % 2 == 0, "whole 32-column blocks per wavefront");
   constexpr int RB = MB / 2, CB = NB / 2;   // 32-row and 32-column blocks per wavefront
+  extern __shared__ __align__(16) unsigned char smem[];
 
+  const int tid = threadIdx.x;
   const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int lc = lane & 31;
   const int lh = lane >> 5;
   const int KT = K / kBigBK;
+  const Loader ld(x, qw, scales, qzeros, smem, M, N, K, gshift, m0, n0, n_end, tid, wave);
 
+  f32x16_t acc[RB][CB];
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -755,24 +750,6 @@ __device__ __forceinline__ void big_tile32_product(const BigLoader<NB, MB, 4>& l
   }
   // the clamped loads past the last tile must land before the workgroup's LDS is released
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-}
-
-template <int NB, int MB>
-__device__ __forceinline__ void big_tile32(const half_t* __restrict__ x, const uint32_t* __restrict__ qw,
-                                           const half_t* __restrict__ scales, Zeros qzeros,
-                                           half_t* __restrict__ y, int M, int N, int K, int gshift, int m0, int n0,
-                                           int n_end, int prio) {
-  constexpr int RB = MB / 2, CB = NB / 2;
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int tid = threadIdx.x;
-  const int lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
-  const int lc = lane & 31;
-  const int lh = lane >> 5;
-  const BigLoader<NB, MB, 4> ld(x, qw, scales, qzeros, smem, M, N, K, gshift, m0, n0, n_end, tid, wave);
-  f32x16_t acc[RB][CB];
-  big_tile32_product<NB, MB>(ld, qzeros, smem, K, gshift, tid, wave, prio, acc);
 
   const int nw = n0 + wn * 16 * NB;
 #pragma unroll

@@ -13,6 +13,7 @@
 // would do to the whole row is taken back: its remainder is added in fp32 at the end.
 #pragma once
 
+#include "experts.hpp"
 #include "low.hpp"
 
 namespace w4a16 {
@@ -82,9 +83,9 @@ __device__ __forceinline__ void head_tile(const half_t* x, int x_rows, const Lay
   constexpr int BM = 32 * MB;
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const auto ld = rows_loader<4, MB, BITS>(x, x_rows, l, smem, own.source, tile.rows, n0, l.N, tid, wave);
+  const TileLoader<4, MB, BITS> ld(x, x_rows, l, smem, own.source, tile.rows, n0, tid, wave);
   float4_t acc[MB][4];
-  big_tile_product<4, MB, BITS>(ld, l.zeros, smem, l.K, l.gshift, tid, wave, 1, acc);
+  tile_product(ld, l.zeros, smem, tid, wave, acc);
   __syncthreads();   // the ring's memory is used again
   const int lane = tid & 63, wm = wave >> 2, wn = wave & 3, lr = lane & 15, lq = lane >> 4;
   if constexpr (!GRAD) {
@@ -145,8 +146,8 @@ __global__ __launch_bounds__(512) void head_kernel(const half_t* __restrict__ x,
   RowTile tile;
   int ct;
   if (!find_tile(plan, (to.v1 - to.v0 + 255) / 256, blockIdx.x, tile, ct)) return;
-  int32_t* words = reinterpret_cast<int32_t*>(smem + experts_lds<BITS>() - kTileRowsLds);
-  const HeadTileRows own{words, words + kBigBM, reinterpret_cast<float*>(words + 2 * kBigBM)};
+  int32_t* words = reinterpret_cast<int32_t*>(smem + tile_lds<BITS>() - kTileRowsLds);
+  const HeadTileRows own{words, words + 256, reinterpret_cast<float*>(words + 2 * 256)};
   if (tid < tile.height) {
     const int place = tile.first + min(tid, tile.rows - 1), m = plan.order[place];
     own.source[tid] = gathered ? place : m;

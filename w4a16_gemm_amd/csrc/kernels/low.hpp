@@ -19,8 +19,7 @@
 //    distinct banks.
 #pragma once
 
-#include "direct.hpp"
-#include "experts.hpp"
+#include "tile.hpp"
 
 namespace w4a16 {
 

@@ -23,8 +23,7 @@
 // constants, which here change with every output n instead of staying with the lane.
 #pragma once
 
-#include "direct.hpp"
-#include "experts.hpp"
+#include "tile.hpp"
 
 namespace w4a16 {
 
@@ -32,7 +31,7 @@ template <int BITS>
 struct TStage {
   static constexpr uint32_t ROW = 256 * BITS / 8;                 // code bytes of a row
   static constexpr uint32_t CHUNK = 8 * ROW + (BITS == 4 ? 32 : 64);
-  static constexpr uint32_t A = kBigBM * 64 * 2;
+  static constexpr uint32_t A = 256 * 64 * 2;
   static constexpr uint32_t C = 8 * CHUNK;
   static constexpr uint32_t S = 8 * 64 * 2;                       // [column / 32][output]
   static constexpr uint32_t Z = BITS == 4 ? 256 : 1024;           // [column / 32][output], 64 lanes' loads
