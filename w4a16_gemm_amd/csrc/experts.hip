@@ -250,7 +250,8 @@ int launch_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* 
     return rc;
   if (mem.part) {
     if (act) run_invert(l, E, mem.inverse, st);
-    hipLaunchKernelGGL(sum_slots_kernel, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.most, T, index,
+    auto kern = act ? sum_slots_kernel<true> : sum_slots_kernel<false>;
+    hipLaunchKernelGGL(kern, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.most, T, index,
                        E, mem.plan, mem.inverse, K, direct ? 1 : 0, h0, hx);
   }
   return check_launch("experts backward launch");

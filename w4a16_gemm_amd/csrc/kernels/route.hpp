@@ -27,12 +27,25 @@ __device__ __forceinline__ float key_value(unsigned long long key) {
   return __builtin_bit_cast(float, u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+template <int CTRL>
+__device__ __forceinline__ unsigned long long dpp_key(unsigned long long v) {
+  const int lo = __builtin_amdgcn_mov_dpp(static_cast<int>(static_cast<uint32_t>(v)), CTRL, 0xF, 0xF, true);
+  const int hi = __builtin_amdgcn_mov_dpp(static_cast<int>(v >> 32), CTRL, 0xF, 0xF, true);
+  return static_cast<unsigned long long>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo);
+}
+__device__ __forceinline__ unsigned long long larger(unsigned long long a, unsigned long long b) { return a > b ? a : b; }
+
+// Maximum / sum over a group of 16 or 64 neighbouring lanes, in every lane.
 template <int LANES>
 __device__ __forceinline__ unsigned long long lanes_max(unsigned long long v) {
-#pragma unroll
-  for (int d = 1; d < LANES; d <<= 1) {
-    const unsigned long long o = __shfl_xor(v, d);
-    v = o > v ? o : v;
+  static_assert(LANES == 16 || LANES == 64, "16 or 64 lanes");
+  v = larger(v, dpp_key<0xB1>(v));    // quad_perm [1, 0, 3, 2]
+  v = larger(v, dpp_key<0x4E>(v));    // quad_perm [2, 3, 0, 1]
+  v = larger(v, dpp_key<0x141>(v));   // row_half_mirror
+  v = larger(v, dpp_key<0x140>(v));   // row_mirror
+  if constexpr (LANES == 64) {
+    v = larger(v, __shfl_xor(v, 16));
+    v = larger(v, __shfl_xor(v, 32));
   }
   return v;
 }
@@ -43,12 +56,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// Lane l of a row's group holds the logits l + LANES j, j < PER.
+// Lane l of a row's group holds the logits l + LANES j, j < PER, and the results of the
+// rounds t with t % LANES == l.
 template <int LANES, int PER, typename T>
 __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits, int M, int E, int top_k, int renorm,
                                                     int32_t* __restrict__ index, float* __restrict__ weights) {
   const int m = blockIdx.x * (256 / LANES) + threadIdx.x / LANES, l = threadIdx.x % LANES;
-  const T* row = logits + static_cast<size_t>(min(m, M - 1)) * E;
+  const size_t at = static_cast<size_t>(min(m, M - 1));
+  const T* row = logits + at * E;
   float v[PER];
   unsigned long long key[PER];
   unsigned long long best = 0;
@@ -56,8 +71,11 @@ __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits
   for (int j = 0; j < PER; ++j) {
     const int e = l + LANES * j;
     v[j] = e < E ? as_float(row[e]) : -INFINITY;
-    key[j] = route_key(v[j], e);
-    best = key[j] > best ? key[j] : best;
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    key[j] = route_key(v[j], l + LANES * j);
+    best = larger(best, key[j]);
   }
   best = lanes_max<LANES>(best);
   const float top = best ? key_value(best) : 0.f;
@@ -65,28 +83,38 @@ __global__ __launch_bounds__(256) void route_kernel(const T* __restrict__ logits
 #pragma unroll
   for (int j = 0; j < PER; ++j) sum += expf(v[j] - top);
   const float scale = 1.f / lanes_sum<LANES>(sum);
-  // lane t % LANES keeps the weight of round t until the sum of the weights is known
-  float chosen = 0.f;
-  for (int pass = 0; pass < (renorm ? 2 : 1); ++pass) {
-    unsigned long long b = best;
-    unsigned long long k[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) k[j] = key[j];
-    const float by = pass ? 1.f / chosen : 1.f;
-    for (int t = 0; t < top_k; ++t) {
-      const float w = b ? expf(key_value(b) - top) * scale : 0.f;
-      if (pass == 0) chosen += w;
-      if (l == 0 && m < M && (pass || !renorm)) {
-        index[static_cast<size_t>(m) * top_k + t] = b ? static_cast<int32_t>(~static_cast<uint32_t>(b)) : -1;
-        weights[static_cast<size_t>(m) * top_k + t] = b ? w * by : 0.f;
-      }
+  float chosen = 0.f;   // sum of this lane's weights
+  for (int t0 = 0; t0 < top_k; t0 += LANES) {
+    const int rounds = min(LANES, top_k - t0);
+    unsigned long long mine = 0;
+    for (int t = 0; t < rounds; ++t) {
+      if (l == t) mine = best;
       unsigned long long next = 0;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        if (k[j] == b) k[j] = 0;
-        next = k[j] > next ? k[j] : next;
+        if (key[j] == best) key[j] = 0;
+        next = larger(next, key[j]);
       }
-      b = lanes_max<LANES>(next);
+      best = lanes_max<LANES>(next);
+    }
+    const float w = mine ? expf(key_value(mine) - top) * scale : 0.f;
+    chosen += w;
+    // renormalised weights of one group of rounds wait for the sum, of several are written
+    // and scaled below
+    if (l < rounds && m < M) {
+      index[at * top_k + t0 + l] = mine ? static_cast<int32_t>(~static_cast<uint32_t>(mine)) : -1;
+      if (!renorm || top_k > LANES) weights[at * top_k + t0 + l] = w;
+    }
+    if (renorm && top_k <= LANES) {
+      const float total = lanes_sum<LANES>(chosen);
+      if (l < rounds && m < M) weights[at * top_k + l] = mine ? w / total : 0.f;
+    }
+  }
+  if (renorm && top_k > LANES) {
+    const float total = lanes_sum<LANES>(chosen);
+    for (int t = l; t < top_k && m < M; t += LANES) {   // this lane's own
+      const float w = weights[at * top_k + t];
+      if (index[at * top_k + t] >= 0) weights[at * top_k + t] = w / total;
     }
   }
 }
@@ -103,29 +131,43 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
   const int m = blockIdx.x * (256 / LANES) + threadIdx.x / LANES, l = threadIdx.x % LANES;
   const size_t at = static_cast<size_t>(min(m, M - 1));
   float g[PER];
-  float mean = 0.f;
-  for (int t = 0; t < top_k; ++t) {
-    const int e = index[at * top_k + t];
-    if (e >= 0 && e < E) mean += weights[at * top_k + t] * dweights[at * top_k + t];
+  if (!renorm) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int e = l + LANES * j;
+      g[j] = e < E ? as_float(logits[at * E + e]) : -INFINITY;
+    }
   }
+  // a lane's slot: expert, w dw and w (0 where there is none); the last group of slots stays in
+  // registers for the second walk
+  int e = -1;
+  float w = 0.f, wdw = 0.f, part = 0.f;
+  auto load = [&](int t) {
+    e = t < top_k ? index[at * top_k + t] : -1;
+    const bool valid = e >= 0 && e < E;
+    if (!valid) e = -1;
+    w = valid ? weights[at * top_k + t] : 0.f;
+    wdw = valid ? w * dweights[at * top_k + t] : 0.f;
+  };
+  for (int t0 = 0; t0 < top_k; t0 += LANES) {
+    load(t0 + l);
+    part += wdw;
+  }
+  const float mean = lanes_sum<LANES>(part);
   if (renorm) {
 #pragma unroll
     for (int j = 0; j < PER; ++j) g[j] = 0.f;
   } else {
-    float v[PER], top = -INFINITY;
+    float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = l + LANES * j;
-      v[j] = e < E ? as_float(logits[at * E + e]) : -INFINITY;
-      top = fmaxf(top, v[j]);
-    }
+    for (int j = 0; j < PER; ++j) top = fmaxf(top, g[j]);
 #pragma unroll
     for (int d = 1; d < LANES; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     if (top == -INFINITY) top = 0.f;
     float sum = 0.f;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      g[j] = expf(v[j] - top);
+      g[j] = expf(g[j] - top);
       sum += g[j];
     }
     sum = lanes_sum<LANES>(sum);
@@ -133,14 +175,18 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
 #pragma unroll
     for (int j = 0; j < PER; ++j) g[j] *= scale;
   }
-  for (int t = 0; t < top_k; ++t) {
-    const int e = index[at * top_k + t];
-    if (e < 0 || e >= E) continue;
-    const float w = weights[at * top_k + t], dw = dweights[at * top_k + t];
-    const float d = renorm ? w * (dw - mean) : w * dw;
+  for (int t0 = 0; t0 < top_k; t0 += LANES) {
+    if (top_k > LANES) load(t0 + l);
+    const float d = renorm ? wdw - w * mean : wdw;
+    const int rounds = min(LANES, top_k - t0);
+    for (int t = 0; t < rounds; ++t) {
+      const int from = (threadIdx.x & 63 & ~(LANES - 1)) + t;
+      const int et = __shfl(e, from);
+      const float dt = __shfl(d, from);
 #pragma unroll
-    for (int j = 0; j < PER; ++j)
-      if (e == l + LANES * j) g[j] += d;
+      for (int j = 0; j < PER; ++j)
+        if (et == l + LANES * j) g[j] += dt;
+    }
   }
   if (m >= M) return;
 #pragma unroll

@@ -7,7 +7,7 @@
 // odd number of 16-output blocks, else 32x32x16 ones (twice the work per issue).
 //  * Rows lie anywhere in x: the lane offsets of the loads are those of the tile's rows, fixed
 //    over the K loop, so the gather costs nothing there.  A row is 8 chunks of 8 channels,
-//    chunk j of row r at slot j ^ (r % 8).
+//    chunk j of row r at slot j ^ (r / 2 % 8).
 //  * Codes: the 32 (64 at 8 bits) bytes of an output are taken by neighbouring lanes of one
 //    load, part p of output n at slot p ^ (n / 8 % 2) (p ^ (n / 4 % 4)), so that the lanes
 //    that read a part of 16 outputs at once meet distinct banks.
@@ -60,7 +60,7 @@ struct TileLoader {
 #pragma unroll
     for (int i = 0; i < APT; ++i) {
       const int c = (wave * APT + i) * 64 + lane, row = c >> 3, slot = c & 7;
-      a_off[i] = (static_cast<uint32_t>(source[min(row, rows - 1)]) * l.K + 8 * (slot ^ (row & 7))) * 2u;
+      a_off[i] = (static_cast<uint32_t>(source[min(row, rows - 1)]) * l.K + 8 * (slot ^ ((row >> 1) & 7))) * 2u;
     }
 #pragma unroll
     for (int i = 0; i < CL; ++i) {
@@ -152,7 +152,7 @@ __device__ __forceinline__ void tile_product(const TileLoader<NB, MB, BITS>& ld,
       half8_t af[MB], bf[NB];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
-        af[mb] = *reinterpret_cast<const half8_t*>(st + a_lane + 16 * ((2 * lq + s) ^ (lr & 7)) + 2048 * mb);
+        af[mb] = *reinterpret_cast<const half8_t*>(st + a_lane + 16 * ((2 * lq + s) ^ (lr >> 1)) + 2048 * mb);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
         if constexpr (BITS == 4) {
@@ -222,13 +222,13 @@ __device__ __forceinline__ void tile_product32(const TileLoader<NB, MB, BITS>& l
     half8_t af[2][RB];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
-      af[0][rb] = *reinterpret_cast<const half8_t*>(st + a_lane + 4096 * rb + 16 * ((4 * lh) ^ (lc & 7)));
+      af[0][rb] = *reinterpret_cast<const half8_t*>(st + a_lane + 4096 * rb + 16 * ((4 * lh) ^ ((lc >> 1) & 7)));
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       if (s < 3) {
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
-          af[(s + 1) & 1][rb] = *reinterpret_cast<const half8_t*>(st + a_lane + 4096 * rb + 16 * ((4 * lh + s + 1) ^ (lc & 7)));
+          af[(s + 1) & 1][rb] = *reinterpret_cast<const half8_t*>(st + a_lane + 4096 * rb + 16 * ((4 * lh + s + 1) ^ ((lc >> 1) & 7)));
       }
       __builtin_amdgcn_sched_barrier(0);   // keep the reads ahead of this step's MFMAs
       half8_t bf[CB];

@@ -4,7 +4,7 @@
 // A workgroup of 8 wavefronts (2 along the rows x 4 along k) takes a tile of BM = 32 MB
 // rows by 256 channels k, the contraction in tiles of 64 outputs n through a 3-stage LDS
 // ring filled by direct-to-LDS loads two tiles ahead, as in the forward tile:
-//  * dy: BM rows of 8 chunks of 8 outputs, chunk j of row r at slot j ^ (r % 8);
+//  * dy: BM rows of 8 chunks of 8 outputs, chunk j of row r at slot j ^ (r / 2 % 8);
 //  * codes: 64 rows n of 256 channels, as they lie in memory, in 8 chunks of 8 rows; a
 //    chunk is followed by 32 bytes (64 at 8 bits) of padding, so that the four chunks that
 //    one MFMA operand reads lie in distinct banks;
@@ -70,7 +70,7 @@ struct TLoader {
     for (int i = 0; i < APT; ++i) {
       const int c = (wave * APT + i) * 64 + lane;
       const int row = c >> 3, slot = c & 7;
-      a_off[i] = (static_cast<uint32_t>(source[min(row, rows - 1)]) * a_pitch + 8 * (slot ^ (row & 7))) * 2u;
+      a_off[i] = (static_cast<uint32_t>(source[min(row, rows - 1)]) * a_pitch + 8 * (slot ^ ((row >> 1) & 7))) * 2u;
     }
     // Codes: load i of wavefront w fills rows 8 w .. (4 bits: 8 rows, 8 bits: 4 rows each),
     // 16 bytes per lane; channels past K re-read the row's last ones, outputs past the end
@@ -183,7 +183,7 @@ __device__ __forceinline__ void transposed_product(const TLoader<MB, BITS>& ld, 
       half8_t af[MB];
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
-        af[mb] = *reinterpret_cast<const half8_t*>(st + a_lane + 16 * ((4 * s + lq) ^ (lr & 7)) + 2048 * mb);
+        af[mb] = *reinterpret_cast<const half8_t*>(st + a_lane + 16 * ((4 * s + lq) ^ (lr >> 1)) + 2048 * mb);
       if (t == ld.KT - 1 && 8 * (4 * s + lq) >= last) {   // outputs past the end: nothing of dy there
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb) af[mb] = half8_t{};
@@ -343,21 +343,40 @@ __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restric
 }
 
 // Partial sums part[piece][slot][K] of the slots [m T, (m + 1) T) -> dx[m], in a fixed
-// order, plus dx0, rounded once.  Slots without an expert have no sums.  inverse (act
-// order): stored position of every channel of every expert.  direct: tiles that are not in
-// parts have been written already.
+// order, plus dx0, rounded once.  Slots without an expert have no sums.  direct: tiles that
+// are not in parts have been written already.  ORDERED (act order): the sums lie in the stored
+// channel order of the slot's expert, inverse [E][K] has the stored position of every channel;
+// 8192 channels at a time pass through LDS, where they are picked up in the channels' own
+// order (1554 slots of 4096 channels in up to three parts: 74 us picked up from memory, 26 us).
+constexpr int kSumChannels = 8192;
+
+template <bool ORDERED>
 __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict__ part, size_t slots, int most, int T,
                                                         const int32_t* __restrict__ index, int E, SlotPlan plan,
                                                         const int32_t* __restrict__ inverse, int K, int direct,
                                                         const half_t* __restrict__ dx0, half_t* __restrict__ out) {
+  __shared__ __align__(16) float turn[ORDERED ? kSumChannels : 1];
   const size_t m = blockIdx.x;
   const int cols = (K + 255) / 256, total = plan.counts[0] * cols;
   const Pieces rule(total, most);
-  for (int k = 8 * threadIdx.x; k < K; k += 8 * 256) {
+  // sum of the parts of one slot at 8 stored positions
+  auto add = [&](size_t slot, int tile, const RowTile& row, int k, float (&s)[8]) {
+    const int pieces = rule.of(row, tile, k / 256, cols);
+    if (direct && pieces == 1) return false;
+    for (int p = 0; p < pieces; ++p) {
+      const float* at = part + (p * slots + slot) * K + k;
+      const float4_t lo = *reinterpret_cast<const float4_t*>(at), hi = *reinterpret_cast<const float4_t*>(at + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] += lo[i], s[4 + i] += hi[i];
+    }
+    return true;
+  };
+  for (int k0 = 8 * threadIdx.x; k0 - 8 * static_cast<int>(threadIdx.x) < K; k0 += 8 * 256) {
+    const bool mine = k0 < K;
     float s[8] = {};
     bool any = !direct;
-    if (dx0) {
-      const half8_t d = *reinterpret_cast<const half8_t*>(dx0 + m * K + k);
+    if (mine && dx0) {
+      const half8_t d = *reinterpret_cast<const half8_t*>(dx0 + m * K + k0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = static_cast<float>(d[i]);
     }
@@ -367,31 +386,36 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict_
       if (e < 0 || e >= E) continue;
       const int tile = plan.tile_of[slot];
       const RowTile row = plan.tiles[tile];
-      const float* sums = part + slot * K;
-      if (inverse) {
+      if constexpr (ORDERED) {
+        uint32_t at[8];
+        if (mine) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t at = min(static_cast<uint32_t>(inverse[static_cast<size_t>(e) * K + k + i]), static_cast<uint32_t>(K - 1));
-          const int pieces = rule.of(row, tile, at / 256, cols);
-          for (int p = 0; p < pieces; ++p) s[i] += sums[p * slots * K + at];
+          for (int i = 0; i < 8; ++i) at[i] = inverse[static_cast<size_t>(e) * K + k0 + i];
         }
-      } else {
-        const int pieces = rule.of(row, tile, k / 256, cols);
-        if (direct && pieces == 1) continue;
-        any = true;
-        for (int p = 0; p < pieces; ++p) {
-          const float* at = sums + p * slots * K + k;
-          const float4_t lo = *reinterpret_cast<const float4_t*>(at), hi = *reinterpret_cast<const float4_t*>(at + 4);
+        for (int c = 0; c < K; c += kSumChannels) {
+          __syncthreads();
+          for (int k = c + 8 * threadIdx.x; k < min(K, c + kSumChannels); k += 8 * 256) {
+            float v[8] = {};
+            add(slot, tile, row, k, v);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[i] += lo[i], s[4 + i] += hi[i];
+            for (int i = 0; i < 8; ++i) turn[k - c + i] = v[i];
+          }
+          __syncthreads();
+          if (mine) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (at[i] - c < static_cast<uint32_t>(min(K - c, kSumChannels))) s[i] += turn[at[i] - c];
+          }
         }
+      } else if (mine) {
+        any |= add(slot, tile, row, k0, s);
       }
     }
-    if (!any) continue;
+    if (!mine || !any) continue;
     half8_t o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = static_cast<half_t>(s[i]);
-    *reinterpret_cast<half8_t*>(out + m * K + k) = o;
+    *reinterpret_cast<half8_t*>(out + m * K + k0) = o;
   }
 }
 
