@@ -249,10 +249,14 @@ int launch_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* 
                               mem.plan, 0, N, N, shape.most, to, st))
     return rc;
   if (mem.part) {
-    if (act) run_invert(l, E, mem.inverse, st);
-    auto kern = act ? sum_slots_kernel<true> : sum_slots_kernel<false>;
-    hipLaunchKernelGGL(kern, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.most, T, index,
-                       E, mem.plan, mem.inverse, K, direct ? 1 : 0, h0, hx);
+    if (act) {
+      run_invert(l, E, mem.inverse, st);
+      hipLaunchKernelGGL(sum_ordered_kernel, dim3(M), dim3(512), 0, st, mem.part, static_cast<size_t>(S), shape.most, T,
+                         index, E, mem.plan, mem.inverse, K, h0, hx);
+    } else {
+      hipLaunchKernelGGL(sum_slots_kernel, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.most, T,
+                         index, E, mem.plan, K, direct ? 1 : 0, h0, hx);
+    }
   }
   return check_launch("experts backward launch");
 }

@@ -343,26 +343,19 @@ __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restric
 }
 
 // Partial sums part[piece][slot][K] of the slots [m T, (m + 1) T) -> dx[m], in a fixed
-// order, plus dx0, rounded once.  Slots without an expert have no sums.  direct: tiles that
-// are not in parts have been written already.  ORDERED (act order): the sums lie in the stored
-// channel order of the slot's expert, inverse [E][K] has the stored position of every channel;
-// 8192 channels at a time pass through LDS, where they are picked up in the channels' own
-// order (1554 slots of 4096 channels in up to three parts: 74 us picked up from memory, 26 us).
-constexpr int kSumChannels = 8192;
+// order, plus dx0, rounded once.  Slots without an expert have no sums.
+struct SlotSums {
+  const float* part;
+  size_t slots;
+  const SlotPlan& plan;
+  Pieces rule;
+  int K, cols, E;
 
-template <bool ORDERED>
-__global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict__ part, size_t slots, int most, int T,
-                                                        const int32_t* __restrict__ index, int E, SlotPlan plan,
-                                                        const int32_t* __restrict__ inverse, int K, int direct,
-                                                        const half_t* __restrict__ dx0, half_t* __restrict__ out) {
-  __shared__ __align__(16) float turn[ORDERED ? kSumChannels : 1];
-  const size_t m = blockIdx.x;
-  const int cols = (K + 255) / 256, total = plan.counts[0] * cols;
-  const Pieces rule(total, most);
-  // sum of the parts of one slot at 8 stored positions
-  auto add = [&](size_t slot, int tile, const RowTile& row, int k, float (&s)[8]) {
+  // adds the parts of one slot at channels [k, k + 8); false: its tile was not in parts
+  __device__ __forceinline__ bool add(size_t slot, int tile, const RowTile& row, int k, bool direct, float (&s)[8]) const {
     const int pieces = rule.of(row, tile, k / 256, cols);
     if (direct && pieces == 1) return false;
+#pragma unroll 4
     for (int p = 0; p < pieces; ++p) {
       const float* at = part + (p * slots + slot) * K + k;
       const float4_t lo = *reinterpret_cast<const float4_t*>(at), hi = *reinterpret_cast<const float4_t*>(at + 4);
@@ -370,15 +363,66 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict_
       for (int i = 0; i < 4; ++i) s[i] += lo[i], s[4 + i] += hi[i];
     }
     return true;
-  };
-  for (int k0 = 8 * threadIdx.x; k0 - 8 * static_cast<int>(threadIdx.x) < K; k0 += 8 * 256) {
-    const bool mine = k0 < K;
-    float s[8] = {};
-    bool any = !direct;
-    if (mine && dx0) {
-      const half8_t d = *reinterpret_cast<const half8_t*>(dx0 + m * K + k0);
+  }
+};
+
+__device__ __forceinline__ void start_sums(const half_t* dx0, float (&s)[8]) {
+  half8_t d = {};
+  if (dx0) d = *reinterpret_cast<const half8_t*>(dx0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = static_cast<float>(d[i]);
+  for (int i = 0; i < 8; ++i) s[i] = static_cast<float>(d[i]);
+}
+__device__ __forceinline__ void store_sums(const float (&s)[8], half_t* out) {
+  half8_t o;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = static_cast<half_t>(s[i]);
+  *reinterpret_cast<half8_t*>(out) = o;
+}
+
+// direct: tiles that are not in parts have been written already.
+__global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict__ part, size_t slots, int most, int T,
+                                                        const int32_t* __restrict__ index, int E, SlotPlan plan, int K,
+                                                        int direct, const half_t* __restrict__ dx0, half_t* __restrict__ out) {
+  const size_t m = blockIdx.x;
+  const int cols = (K + 255) / 256;
+  const SlotSums sums{part, slots, plan, Pieces(plan.counts[0] * cols, most), K, cols, E};
+  for (int k = 8 * threadIdx.x; k < K; k += 8 * 256) {
+    float s[8];
+    start_sums(dx0 ? dx0 + m * K + k : nullptr, s);
+    bool any = !direct;
+    for (int t = 0; t < T; ++t) {
+      const size_t slot = m * T + t;
+      const int e = index ? index[slot] : 0;
+      if (e < 0 || e >= E) continue;
+      const int tile = plan.tile_of[slot];
+      any |= sums.add(slot, tile, plan.tiles[tile], k, direct != 0, s);
+    }
+    if (any) store_sums(s, out + m * K + k);
+  }
+}
+
+// The same with the sums in the stored channel order of each slot's expert (act order):
+// inverse [E][K] has the stored position of every channel.  kSumChannels positions at a time
+// pass through LDS and are picked up there for kSumChannels channels, so up to that K every
+// sum is read once, in order (1554 slots of 4096 channels in two parts: picked up from memory
+// 74 us, 20 us).
+constexpr int kSumChannels = 8192;
+
+__global__ __launch_bounds__(512) void sum_ordered_kernel(const float* __restrict__ part, size_t slots, int most, int T,
+                                                          const int32_t* __restrict__ index, int E, SlotPlan plan,
+                                                          const int32_t* __restrict__ inverse, int K,
+                                                          const half_t* __restrict__ dx0, half_t* __restrict__ out) {
+  constexpr int PASS = 8 * 512, RUNS = kSumChannels / PASS;
+  __shared__ __align__(16) float turn[kSumChannels];
+  const size_t m = blockIdx.x;
+  const int cols = (K + 255) / 256, k0 = 8 * threadIdx.x;
+  const SlotSums sums{part, slots, plan, Pieces(plan.counts[0] * cols, most), K, cols, E};
+  for (int base = 0; base < K; base += kSumChannels) {
+    float s[RUNS][8];
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      const int k = base + PASS * r + k0;
+      start_sums(dx0 && k < K ? dx0 + m * K + k : nullptr, s[r]);
     }
     for (int t = 0; t < T; ++t) {
       const size_t slot = m * T + t;
@@ -386,36 +430,44 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict_
       if (e < 0 || e >= E) continue;
       const int tile = plan.tile_of[slot];
       const RowTile row = plan.tiles[tile];
-      if constexpr (ORDERED) {
-        uint32_t at[8];
-        if (mine) {
+      uint4 at[RUNS][2];   // stored positions of the thread's channels
 #pragma unroll
-          for (int i = 0; i < 8; ++i) at[i] = inverse[static_cast<size_t>(e) * K + k0 + i];
-        }
-        for (int c = 0; c < K; c += kSumChannels) {
-          __syncthreads();
-          for (int k = c + 8 * threadIdx.x; k < min(K, c + kSumChannels); k += 8 * 256) {
-            float v[8] = {};
-            add(slot, tile, row, k, v);
+      for (int r = 0; r < RUNS; ++r) {
+        const int k = min(base + PASS * r + k0, K - 8);
+        const uint4* from = reinterpret_cast<const uint4*>(inverse + static_cast<size_t>(e) * K + k);
+        at[r][0] = from[0], at[r][1] = from[1];
+      }
+      for (int c = 0; c < K; c += kSumChannels) {
+        const int end = min(K - c, kSumChannels);
+        float v[RUNS][8] = {};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) turn[k - c + i] = v[i];
+        for (int r = 0; r < RUNS; ++r)
+          if (PASS * r + k0 < end) sums.add(slot, tile, row, c + PASS * r + k0, false, v[r]);
+        __syncthreads();   // the last positions are picked up
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r)
+          if (PASS * r + k0 < end) {
+            float4_t* to = reinterpret_cast<float4_t*>(turn + PASS * r + k0);
+            to[0] = float4_t{v[r][0], v[r][1], v[r][2], v[r][3]};
+            to[1] = float4_t{v[r][4], v[r][5], v[r][6], v[r][7]};
           }
-          __syncthreads();
-          if (mine) {
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < RUNS; ++r) {
+          const uint32_t a[8] = {at[r][0].x, at[r][0].y, at[r][0].z, at[r][0].w, at[r][1].x, at[r][1].y, at[r][1].z, at[r][1].w};
+          if (base + PASS * r + k0 < K) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (at[i] - c < static_cast<uint32_t>(min(K - c, kSumChannels))) s[i] += turn[at[i] - c];
+              if (a[i] - c < static_cast<uint32_t>(end)) s[r][i] += turn[a[i] - c];   // not a permutation: left out
           }
         }
-      } else if (mine) {
-        any |= add(slot, tile, row, k0, s);
       }
     }
-    if (!mine || !any) continue;
-    half8_t o;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = static_cast<half_t>(s[i]);
-    *reinterpret_cast<half8_t*>(out + m * K + k0) = o;
+    for (int r = 0; r < RUNS; ++r) {
+      const int k = base + PASS * r + k0;
+      if (k < K) store_sums(s[r], out + m * K + k);
+    }
   }
 }
 
