@@ -13,7 +13,9 @@
  * Shapes: M rows, T experts per row, S = M T slots, E experts (1 .. 512), N output and K input
  * channels; M, T > 0, S <= 2^27.  The layers' shapes are those of w4a16.h and besides K % 64
  * == 0, for 8-bit weights N % 16 == 0, N <= 2^24, fewer than 2^32 bytes of codes per expert, and
- * fewer than 2^31 elements of x, of dy and of the slots' rows of K channels under act order.
+ * fewer than 2^31 elements of x, of dy and of the slots' rows of K channels under act order;
+ * what one launch takes bounds S to 2^23 under act order, and M to 2^22 where the gradients
+ * of several slots are summed or act order is undone.
  *   qweight   int32 [E][w4a16_qweight_words(N, K, act_order)] (w8a16: its own function): the
  *             experts' weight buffers one after the other
  *   scales    binary16 [E][G][N];  qzeros  int32 [E][G][N/8] (8 bits: [N/4]) or NULL: symmetric
@@ -22,13 +24,15 @@
  *             a slot without an expert: padding, or a row that the router left short.
  *   weights   float [M][T]
  *   workspace 16-byte aligned device memory of at least the size that the matching _workspace
- *             function returns for the same sizes (0 on sizes that the call refuses), owned by
+ *             function returns for the same sizes (0 on sizes that both widths refuse, or where
+ *             none is needed: workspace may then be NULL), owned by
  *             the caller and free again once the stream has passed the call.  Calls that may
  *             run at once, two graphs for instance, need a workspace each.
- * Buffers must be 16-byte aligned (index, weights, dweights, logits, dlogits: 4-byte aligned).  Outputs must not
- * overlap inputs or the workspace, but for dx and dx0.  W^ = binary16((q - Z) S), the values
- * of w4a16_dequant, in both directions; sums are fp32 in a fixed order: the same call gives
- * the same bits.  A row's results do not depend on the values of other rows.
+ * Buffers must be 16-byte aligned (index, weights, dweights, logits, dlogits: 4-byte aligned).
+ * Outputs must not overlap inputs or the workspace, but for dx and dx0.
+ * W^ = binary16((q - Z) S), the values of w4a16_dequant, in both directions; sums are fp32 in
+ * a fixed order: the same call gives the same bits.  A row's results do not depend on the
+ * values of other rows.
  */
 #ifndef W4A16_EXPERTS_H
 #define W4A16_EXPERTS_H
@@ -45,7 +49,8 @@ extern "C" {
  * renormalise != 0.  An expert whose logit is -infinity (masked) or NaN is never chosen; where
  * fewer than top_k are left, the rest of the row gets index -1 and weight 0.  A NaN or +infinity
  * in a row makes the weights of its chosen experts NaN.
- *   logits [M][E], binary16 (logit_bits 16) or float (32);  1 <= top_k <= E <= 512, M <= 2^27
+ *   logits [M][E], binary16 (logit_bits 16) or float (32);  1 <= top_k <= E <= 512; M <= 2^27
+ *   (2^25 above 128 experts)
  *   index  out int32 [M][top_k];  weights out float [M][top_k]
  * Errors: INVALID_ARG, UNSUPPORTED (E, logit_bits, M), MISALIGNED, HIP. */
 int w4a16_route(const void* logits, int logit_bits, int M, int E, int top_k, int renormalise, int32_t* index,

@@ -165,6 +165,6 @@ void run_gather(const SlotPlan& p, const half_t* x, const int32_t* index, const 
 void run_invert(const Layers& l, int E, int32_t* inverse, hipStream_t st);
 // The transposed product over at most `tiles` row tiles; arguments as transposed_kernel.
 int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                   const SlotPlan& p, int n_begin, int n_end, int n_most, int most, const TOut& to, hipStream_t st);
+                   const SlotPlan& p, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st);
 
 }  // namespace w4a16

@@ -34,22 +34,22 @@ namespace {
 
 template <int BITS>
 int launch_transposed(int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                      const SlotPlan& p, int n_begin, int n_end, int n_most, int most, const TOut& to, hipStream_t st) {
+                      const SlotPlan& p, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st) {
   auto kern = transposed_kernel<BITS>;
   static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), transposed_lds<BITS>());
   if (int rc = lds_status(lds_ok)) return rc;
   const dim3 grid(static_cast<unsigned>(piece_blocks(tiles * ceil_div(l.K, 256))));
   hipLaunchKernelGGL(kern, grid, dim3(512), transposed_lds<BITS>(), st, a, a_rows, a_pitch, by_place ? 1 : 0, l, p, n_begin,
-                     n_end, n_most, most, to);
+                     n_end, n_valid, n_most, most, to);
   return check_launch("transposed product launch");
 }
 
 }  // namespace
 
 int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                   const SlotPlan& p, int n_begin, int n_end, int n_most, int most, const TOut& to, hipStream_t st) {
-  return bits == 4 ? launch_transposed<4>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, n_most, most, to, st)
-                   : launch_transposed<8>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, n_most, most, to, st);
+                   const SlotPlan& p, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st) {
+  return bits == 4 ? launch_transposed<4>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, n_valid, n_most, most, to, st)
+                   : launch_transposed<8>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, n_valid, n_most, most, to, st);
 }
 
 namespace {
@@ -121,7 +121,7 @@ int check_forward(int M, int T, int E, int N, int K, bool act) {
   if ((act ? S : M) * static_cast<int64_t>(K) >= kMaxElements)
     return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d K=%d: 2^31 elements or more", M, T, K);
   const TileShape shape = pick_shape(S, E, N);
-  if (most_tiles(S, E, shape.height) * ceil_div(N, 64 * shape.nb) > kMaxBlocks)
+  if (most_tiles(S, E, shape.height) * ceil_div(N, 64 * shape.nb) > kMaxBlocks || (act && S > 2 * kMaxBlocks))
     return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d N=%d: more tiles than one launch takes", M, T, N);
   return W4A16_OK;
 }
@@ -162,7 +162,7 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
   if (int rc = check_experts(M, T, E, N, K, group_size, BITS)) return rc;
   const Buffer bufs[] = {{x, 16, true, "x"},          {qweight, 16, true, "qweight"}, {scales, 16, true, "scales"},
                          {qzeros, 16, false, "qzeros"}, {index, 4, true, "index"},    {y, 16, true, "y"},
-                         {workspace, 16, true, "workspace"}};
+                         {workspace, 16, false, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   const bool act = g_idx != nullptr;
   if (int rc = check_forward(M, T, E, N, K, act)) return rc;
@@ -170,6 +170,7 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
   const TileShape shape = pick_shape(S, E, N);
   Carver ws{static_cast<unsigned char*>(workspace)};
   const ForwardMemory mem = forward_memory(ws, S, E, K, act, shape.height);
+  if (!workspace && ws.used > 0) return fail(W4A16_ERR_INVALID_ARG, "NULL buffer workspace");
   if (workspace_bytes < ws.used)
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.used);
   hipStream_t st = static_cast<hipStream_t>(stream);
@@ -218,12 +219,12 @@ BackwardMemory backward_memory(Carver& ws, int64_t S, int T, int E, int K, bool 
   return m;
 }
 
-int check_backward(int M, int T, int E, int N, int K) {
+int check_backward(int M, int T, int E, int N, int K, bool act) {
   const int64_t S = static_cast<int64_t>(M) * T;
   if (S * N >= kMaxElements) return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d N=%d: 2^31 elements or more", M, T, N);
   const TransposedShape shape = pick_transposed(S, E, N, K);
-  if (piece_blocks(most_tiles(S, E, shape.height) * ceil_div(K, 256)) > kMaxBlocks)
-    return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d K=%d: more tiles than one launch takes", M, T, K);
+  if (piece_blocks(most_tiles(S, E, shape.height) * ceil_div(K, 256)) > kMaxBlocks || (!is_direct(T, act) && M > kMaxBlocks))
+    return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d K=%d: more tiles or sums than one launch takes", M, T, K);
   return W4A16_OK;
 }
 
@@ -231,7 +232,7 @@ template <int BITS>
 int launch_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* scales, const int32_t* qzeros, bool act,
                     int group_size, const int32_t* index, const uint16_t* dx0, int M, int T, int E, int N, int K,
                     uint16_t* dx, void* workspace, size_t workspace_bytes, void* stream) {
-  if (int rc = check_backward(M, T, E, N, K)) return rc;
+  if (int rc = check_backward(M, T, E, N, K, act)) return rc;
   const int S = M * T;
   const TransposedShape shape = pick_transposed(S, E, N, K);
   Carver ws{static_cast<unsigned char*>(workspace)};
@@ -246,7 +247,7 @@ int launch_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* 
   half_t* hx = reinterpret_cast<half_t*>(dx);
   const TOut to{direct ? hx : nullptr, direct ? h0 : nullptr, mem.part, static_cast<size_t>(S), 0};
   if (int rc = run_transposed(BITS, most_tiles(S, E, shape.height), reinterpret_cast<const half_t*>(dy), S, N, false, l,
-                              mem.plan, 0, N, N, shape.most, to, st))
+                              mem.plan, 0, N, N, N, shape.most, to, st))
     return rc;
   if (mem.part) {
     if (act) {
@@ -284,7 +285,8 @@ int check_route(int logit_bits, int M, int E, int top_k) {
   if (logit_bits != 16 && logit_bits != 32) return fail(W4A16_ERR_UNSUPPORTED, "logits of %d bits, not 16 or 32", logit_bits);
   if (E < 1 || E > kMaxExperts) return fail(W4A16_ERR_UNSUPPORTED, "%d experts, not 1..%d", E, kMaxExperts);
   if (top_k > E) return fail(W4A16_ERR_INVALID_ARG, "top_k=%d of %d experts", top_k, E);
-  if (M > kMaxSlots) return fail(W4A16_ERR_UNSUPPORTED, "M=%d: at most 2^27 rows", M);
+  // 2^23 workgroups of 256 threads
+  if (M > (E <= 128 ? kMaxSlots : kMaxSlots / 4)) return fail(W4A16_ERR_UNSUPPORTED, "M=%d E=%d: too many rows for one launch", M, E);
   return W4A16_OK;
 }
 
@@ -378,7 +380,7 @@ int w8a16_experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t
 }
 
 size_t w4a16_experts_backward_workspace(int M, int T, int E, int N, int K, int act_order) {
-  const bool ok = check_experts(M, T, E, N, K, K, 4) == W4A16_OK && check_backward(M, T, E, N, K) == W4A16_OK;
+  const bool ok = check_experts(M, T, E, N, K, K, 4) == W4A16_OK && check_backward(M, T, E, N, K, act_order != 0) == W4A16_OK;
   clear_error();
   if (!ok) return 0;
   Carver ws{nullptr};

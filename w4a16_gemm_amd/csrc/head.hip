@@ -184,14 +184,14 @@ int head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qwe
     if (act) run_gather(mem.plan, hx, nullptr, l, rows, 1, mem.gathered, st);
     const HeadRows hr{target + m0, mem.remainder, lse + m0};
     for (int v0 = 0; v0 < vocab; v0 += p.cols) {
-      // padding columns up to a whole zero-point word have the coefficient 0
+      // padding columns up to a whole load of zero points have the coefficient 0
       const int v1 = static_cast<int>(std::min<int64_t>(int64_t{v0} + p.cols, std::min<int64_t>(ceil_div(vocab, 16) * 16, N)));
       const HeadOut to{nullptr, mem.coeff, p.cols, v0, v1, vocab, static_cast<size_t>(rows)};
       if (int rc = launch_head<BITS, true>(p.logit_height, most_tiles(rows, 1, p.logit_height), st, act ? mem.gathered : hx, rows, act, l,
                                            mem.logit_plan, hr, to))
         return rc;
       const TOut out{nullptr, nullptr, mem.part, static_cast<size_t>(rows), v0 > 0};
-      if (int rc = run_transposed(BITS, most_tiles(rows, 1, height), mem.coeff, rows, p.cols, true, l, mem.plan, v0, v1,
+      if (int rc = run_transposed(BITS, most_tiles(rows, 1, height), mem.coeff, rows, p.cols, true, l, mem.plan, v0, v1, vocab,
                                   p.cols, p.product.most, out, st))
         return rc;
     }

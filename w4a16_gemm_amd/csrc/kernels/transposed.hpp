@@ -170,7 +170,7 @@ __device__ __forceinline__ void transposed_product(const TLoader<MB, BITS>& ld, 
       for (int i = 0; i < 8; ++i)
         w[i] = *reinterpret_cast<const uint32_t*>(st + c_lane + s * 4 * L::CHUNK + i * L::ROW);
       const uint4 sv = *reinterpret_cast<const uint4*>(st + s_lane + 64 * s);
-      const uint32_t sc[4] = {sv.x, sv.y, sv.z, sv.w};
+      uint32_t sc[4] = {sv.x, sv.y, sv.z, sv.w};
       uint32_t z[4];
       if constexpr (BITS == 4) {
         zero_pairs4(zeros.word(*reinterpret_cast<const uint32_t*>(st + z_lane + 16 * s)), z);
@@ -184,9 +184,14 @@ __device__ __forceinline__ void transposed_product(const TLoader<MB, BITS>& ld, 
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
         af[mb] = *reinterpret_cast<const half8_t*>(st + a_lane + 16 * ((4 * s + lq) ^ (lr >> 1)) + 2048 * mb);
-      if (t == ld.KT - 1 && 8 * (4 * s + lq) >= last) {   // outputs past the end: nothing of dy there
+      if (t == ld.KT - 1) {   // outputs past the end: nothing of dy there, weights of 0
+        const int left = last - 8 * (4 * s + lq);
 #pragma unroll
-        for (int mb = 0; mb < MB; ++mb) af[mb] = half8_t{};
+        for (int p = 0; p < 4; ++p) sc[p] = 2 * p + 1 < left ? sc[p] : 2 * p < left ? sc[p] & 0xFFFFu : 0u;
+        if (left <= 0) {
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) af[mb] = half8_t{};
+        }
       }
       uint32_t b[4][4];   // [block][pair of outputs]
 #pragma unroll
@@ -264,7 +269,7 @@ __device__ __forceinline__ void each_run(const float4_t (&acc)[MB][4], int tid, 
 
 template <int MB, int BITS>
 __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int a_pitch, int a0, const Layers& l,
-                                                int n_begin, int n_end, int k0, const int32_t* source,
+                                                int n_begin, int n_end, int n_valid, int k0, const int32_t* source,
                                                 const RowTile& tile, const TOut& to, int piece, int pieces,
                                                 unsigned char* smem) {
   const int tid = threadIdx.x;
@@ -273,7 +278,7 @@ __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int
   float4_t acc[MB][4];
   if (n_begin < n_end) {
     const TLoader<MB, BITS> ld(a, a_rows, a_pitch, a0, l, n_begin, n_end, k0, source, rows, smem, tid, wave);
-    transposed_product<MB, BITS>(ld, l.zeros, smem, n_end - n_begin, tid, wave, acc);
+    transposed_product<MB, BITS>(ld, l.zeros, smem, min(n_end, n_valid) - n_begin, tid, wave, acc);
   } else {   // a part without outputs: nothing to add
     if (to.add) return;
 #pragma unroll
@@ -306,13 +311,14 @@ __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int
 }
 
 // a [a_rows][a_pitch]: by_place: row p belongs to place p of the plan's order, else row s to
-// slot s.  The outputs [n_begin, n_end) against columns [0, n_end - n_begin) of a.  A tile
+// slot s.  The outputs [n_begin, n_end) against columns [0, n_end - n_begin) of a; those from
+// n_valid > n_end - 16 on, whose columns of a are 0, count as 0 whatever their scales.  A tile
 // in parts takes ceil(n_most / parts) outputs each, n_most >= n_end - n_begin (the same for
 // every launch that adds to the same sums).  Sums go to the places or slots alike.
 template <int BITS>
 __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restrict__ a, int a_rows, int a_pitch,
                                                          int by_place, Layers layers, SlotPlan plan, int n_begin,
-                                                         int n_end, int n_most, int most, TOut to) {
+                                                         int n_end, int n_valid, int n_most, int most, TOut to) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, K = layers.K;
   RowTile tile;
@@ -335,11 +341,11 @@ __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restric
   const int len = (n_most + 64 * pieces - 1) / (64 * pieces) * 64;
   const int a0 = piece * len, n0 = n_begin + a0, n1 = min(n_end, n0 + len);
   if (tile.height == 256)
-    transposed_tile<8, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, tile, to, piece, pieces, smem);
+    transposed_tile<8, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
   else if (tile.height == 128)
-    transposed_tile<4, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, tile, to, piece, pieces, smem);
+    transposed_tile<4, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
   else
-    transposed_tile<2, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, k0, rows, tile, to, piece, pieces, smem);
+    transposed_tile<2, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
 }
 
 // Partial sums part[piece][slot][K] of the slots [m T, (m + 1) T) -> dx[m], in a fixed

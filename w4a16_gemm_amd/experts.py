@@ -159,10 +159,10 @@ def _gemm(bits, x, qweight, scales, qzeros, g_idx, group_size, index, out, strea
         if out is None:
             out = torch.empty(lead + (N,), dtype=torch.float16, device=device)
         need = _workspace_bytes("w4a16_experts_gemm_workspace", M, T, E, N, K, int(g_idx is not None))
-        ws = _workspace(max(need, 1), device)
+        ws = _workspace(need, device)
         _check(getattr(_lib(), f"w{bits}a16_experts_gemm")(
             x.data_ptr(), qweight.data_ptr(), scales.data_ptr(), _ptr(qzeros), _ptr(g_idx), group_size,
-            index.data_ptr(), M, T, E, N, K, out.data_ptr(), ws.data_ptr(), need, _handle(device)))
+            index.data_ptr(), M, T, E, N, K, out.data_ptr(), _ptr(ws), need, _handle(device)))
     return out
 
 
