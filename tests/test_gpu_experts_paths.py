@@ -464,3 +464,21 @@ def test_gradient_of_the_layer_is_that_of_its_restored_weights(M):
     index = np.zeros((M, 1), np.int32)
     ref = oracle.experts_backward(dy[:, None], W[None], index, dx0)
     within("dx", got, ref, backward_tol(dy[:, None], W[None], index, dx0, ref))
+
+
+@pytest.mark.parametrize("M,N,vocab,K,act,none", [(37, 140008, 140001, 64, False, 0.3), (64, 151936, 151936, 128, False, 0.0),
+                                                  (1, 135000, 134999, 192, False, 0.0), (5, 140008, 140008, 64, False, 1.0),
+                                                  (100, 70000, 69990, 64, False, 0.1), (50, 140008, 140008, 64, True, 0.2)])
+def test_loss_of_few_rows_against_wide_heads(M, N, vocab, K, act, none):
+    note(f"few rows, wide head M={M} N={N} K={K} act={act}")
+    rng = np.random.default_rng([112, M, N])
+    layer = Layers(1, N, K, 4, 64, act=act, experts=False)
+    x, target = f16(rng, (M, K), 2.0), rng.integers(0, vocab, M).astype(np.int32)
+    target[rng.random(M) < none] = -100
+    got = w4.w4a16_head_loss(dev(x), *layer.args, dev(target), vocab=vocab)
+    loss, lse, _ = oracle.head_loss(x, layer.W[0], target, vocab)
+    tol = loss_tol(x, layer.W[0][:vocab], lse)
+    within("loss", got[0], loss, tol[0])
+    within("lse", got[1], lse, tol[1])
+    again = w4.w4a16_head_loss(dev(x), *layer.args, dev(target), vocab=vocab)
+    assert same(got[0], again[0]) and same(got[1], again[1])

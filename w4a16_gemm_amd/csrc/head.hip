@@ -59,7 +59,7 @@ LossMemory loss_memory(Carver& ws, int rows, int N, int K, bool act) {
   return m;
 }
 
-// height: of the plan's full tiles.
+// height: of the plan's full tiles; without a plan 64, for at most 64 rows.
 template <int BITS, bool GRAD>
 int launch_head(int height, int64_t row_tiles, hipStream_t st, const half_t* x, int x_rows, bool gathered,
                 const Layers& l, const SlotPlan& plan, const HeadRows& rows, const HeadOut& to) {
@@ -95,16 +95,19 @@ int head_loss(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
   for (int64_t m0 = 0; m0 < M; m0 += most) {
     const int rows = static_cast<int>(std::min<int64_t>(most, M - m0));
     const half_t* hx = reinterpret_cast<const half_t*>(x) + m0 * K;
-    run_plan(mem.plan, target + m0, rows, 1, vocab, height, false, st);
-    if (act) run_gather(mem.plan, hx, nullptr, l, rows, 1, mem.gathered, st);
+    // up to 64 rows are ordered by every workgroup itself (37 rows: a launch less, 64 -> 58 us)
+    const bool planned = act || M > 64 || height != 64;
+    SlotPlan plan = mem.plan;
+    if (planned) run_plan(plan, target + m0, rows, 1, vocab, height, false, st);
+    else plan.counts = nullptr;
+    if (act) run_gather(plan, hx, nullptr, l, rows, 1, mem.gathered, st);
     const HeadRows hr{target + m0, mem.label, nullptr};
     const HeadOut to{mem.part, nullptr, 0, 0, vocab, vocab, static_cast<size_t>(rows)};
-    if (int rc = launch_head<BITS, false>(height, most_tiles(rows, 1, height), st, act ? mem.gathered : hx, rows, act, l, mem.plan,
-                                          hr, to))
-      return rc;
+    const int64_t row_tiles = planned ? most_tiles(rows, 1, height) : 1;
+    if (int rc = launch_head<BITS, false>(height, row_tiles, st, act ? mem.gathered : hx, rows, act, l, plan, hr, to)) return rc;
     hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 16))), dim3(1024), 0, st, mem.part,
-                       static_cast<int>(ceil_div(vocab, 256)), static_cast<size_t>(rows), mem.plan, mem.label, rows,
-                       loss + m0, lse + m0);
+                       static_cast<int>(ceil_div(vocab, 256)), static_cast<size_t>(rows), plan, target + m0, vocab,
+                       mem.label, rows, loss + m0, lse + m0);
   }
   return check_launch("head loss launch");
 }

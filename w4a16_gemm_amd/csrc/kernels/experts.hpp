@@ -7,8 +7,9 @@
 
 namespace w4a16 {
 
-// Stores a tile of accumulators as binary16: value(row, column, v) -> binary16 of the tile's
-// row and column, put(row, column, run of 8 columns) stores them.  An accumulator register
+// Stores a tile of accumulators as binary16: value(row, column, step, v, o) makes the binary16
+// values o of v in the tile's row and columns `column`, `column` + step and so on, put(row,
+// column, run of 8 columns) stores them.  An accumulator register
 // holds 16 (32) neighbouring columns of a row, 32 (64) bytes; to store whole 128-byte runs a
 // wavefront turns 32 rows at a time in LDS memory of its own (rows of 16 NB columns and 16
 // bytes of padding, so that the rows that one write meets lie in distinct banks).  The ring's
@@ -38,11 +39,15 @@ __device__ __forceinline__ void store_tile(const float4_t (&acc)[MB][NB], unsign
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+      for (int r = 0; r < 4; ++r) {
+        float v[NB];
+        half_t o[NB];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          turn[(16 * h + 4 * lq + r) * turn_pitch<NB>() + 16 * nb + lr] =
-              value(row0 + 16 * h + 4 * lq + r, wn * 16 * NB + 16 * nb + lr, acc[2 * m2 + h][nb][r]);
+        for (int nb = 0; nb < NB; ++nb) v[nb] = acc[2 * m2 + h][nb][r];
+        value(row0 + 16 * h + 4 * lq + r, wn * 16 * NB + lr, 16, v, o);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) turn[(16 * h + 4 * lq + r) * turn_pitch<NB>() + 16 * nb + lr] = o[nb];
+      }
     put_turned<NB, MB>(turn, tid, row0, put);
   }
 }
@@ -56,15 +61,27 @@ __device__ __forceinline__ void store_tile32(const f32x16_t (&acc)[MB / 2][NB / 
   for (int rb = 0; rb < MB / 2; ++rb) {
     const int row0 = wm * 16 * MB + 32 * rb;
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
+    for (int r = 0; r < 16; ++r) {
+      const int row = 8 * (r >> 2) + 4 * lh + (r & 3);
+      float v[NB / 2];
+      half_t o[NB / 2];
 #pragma unroll
-      for (int cb = 0; cb < NB / 2; ++cb) {
-        const int row = 8 * (r >> 2) + 4 * lh + (r & 3);
-        turn[row * turn_pitch<NB>() + 32 * cb + lc] = value(row0 + row, wn * 16 * NB + 32 * cb + lc, acc[rb][cb][r]);
-      }
+      for (int cb = 0; cb < NB / 2; ++cb) v[cb] = acc[rb][cb][r];
+      value(row0 + row, wn * 16 * NB + lc, 32, v, o);
+#pragma unroll
+      for (int cb = 0; cb < NB / 2; ++cb) turn[row * turn_pitch<NB>() + 32 * cb + lc] = o[cb];
+    }
     put_turned<NB, MB>(turn, tid, row0, put);
   }
 }
+
+struct RoundValues {
+  template <int COUNT>
+  __device__ __forceinline__ void operator()(int, int, int, const float (&v)[COUNT], half_t (&o)[COUNT]) const {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) o[i] = static_cast<half_t>(v[i]);
+  }
+};
 
 template <int NB, int MB, int BITS>
 __device__ __forceinline__ void experts_tile(const half_t* x, int x_rows, const Layers& l, half_t* y, unsigned char* smem,
@@ -73,7 +90,7 @@ __device__ __forceinline__ void experts_tile(const half_t* x, int x_rows, const 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const TileLoader<NB, MB, BITS> ld(x, x_rows, l, smem, source, rows, n0, tid, wave);
   const int N = l.N;
-  auto value = [&](int, int, float v) { return static_cast<half_t>(v); };
+  const RoundValues value;
   auto put = [&](int row, int col, half8_t v) {
     if (row < rows && n0 + col < N) *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slots[row]) * N + n0 + col) = v;
   };

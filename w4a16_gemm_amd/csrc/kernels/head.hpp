@@ -18,7 +18,7 @@
 
 namespace w4a16 {
 
-constexpr float kCoeffScale = 16384.f;
+constexpr float kCoeffLog2 = 14.f, kCoeffScale = 16384.f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -76,6 +76,38 @@ struct HeadTileRows {
   float* lse;        // backward
 };
 
+// c 2^14 of logits, as binary16, and the remainder of the target's c (backward).  All but the
+// target's take one fma before the exponential: the rounding of lse log2 e is 2^-24 of that,
+// far below binary16's; the target's c may be small against its p and keeps the difference.
+// (Two operations per coefficient less: the coefficients of a piece of 1229 rows 267 -> 244 us,
+// of 8192 1033 -> 990 us.)
+struct HeadCoeff {
+  const HeadTileRows& own;
+  const RowTile& tile;
+  const HeadRows& rows;
+  int n0, vocab;
+
+  template <int COUNT>
+  __device__ __forceinline__ void operator()(int row, int col, int step, const float (&v)[COUNT], half_t (&o)[COUNT]) const {
+    const float lse = own.lse[row], base = __builtin_fmaf(lse, kLog2e, -kCoeffLog2);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(v[i], kLog2e, -base));
+      o[i] = static_cast<half_t>(n0 + col + step * i < vocab ? e : 0.f);
+    }
+    const int at = own.label[row] - n0 - col;   // step i: the target's is v[i]
+    if (static_cast<uint32_t>(at) < static_cast<uint32_t>(step * COUNT) && at % step == 0) {
+#pragma unroll
+      for (int i = 0; i < COUNT; ++i)
+        if (at == step * i) {
+          const float c = exp_diff(v[i], lse) - 1.f;
+          o[i] = static_cast<half_t>(c * kCoeffScale);
+          if (row < tile.rows) rows.label[tile.first + row] = c - static_cast<float>(o[i]) * (1.f / kCoeffScale);
+        }
+    }
+  }
+};
+
 template <int MB, int BITS, bool GRAD>
 __device__ __forceinline__ void head_tile(const half_t* x, int x_rows, const Layers& l, unsigned char* smem,
                                           const HeadTileRows& own, const RowTile& tile, const HeadRows& rows,
@@ -120,16 +152,7 @@ __device__ __forceinline__ void head_tile(const half_t* x, int x_rows, const Lay
           join(join(red[tid], red[BM + tid]), join(red[2 * BM + tid], red[3 * BM + tid]));
   } else {
     store_tile<4, MB>(
-        acc, smem, tid,
-        [&](int row, int col, float v) {
-          float c = n0 + col < to.vocab ? exp_diff(v, own.lse[row]) : 0.f;
-          const bool is_label = n0 + col == own.label[row];
-          if (is_label) c -= 1.f;
-          const half_t h = static_cast<half_t>(c * kCoeffScale);
-          if (is_label && row < tile.rows)
-            rows.label[tile.first + row] = c - static_cast<float>(h) * (1.f / kCoeffScale);
-          return h;
-        },
+        acc, smem, tid, HeadCoeff{own, tile, rows, n0, to.vocab},
         [&](int row, int col, half8_t v) {
           if (row < tile.rows && n0 + col < to.v1)
             *reinterpret_cast<half8_t*>(to.coeff + static_cast<size_t>(tile.first + row) * to.pitch + n0 + col - to.v0) = v;
@@ -162,6 +185,16 @@ __global__ __launch_bounds__(512) void head_kernel(const half_t* __restrict__ x,
     head_tile<4, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
   else
     head_tile<2, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
+}
+
+// The order of up to 64 rows by their targets, as the plan's: rows with a target first.  By
+// the first wavefront of a workgroup, into LDS; returns the number of rows with a target.
+__device__ __forceinline__ int order_rows(const int32_t* target, int M, int vocab, int lane, int32_t* order) {
+  const int t = lane < M ? target[lane] : -1;
+  const unsigned long long with = __ballot(t >= 0 && t < vocab);
+  const int valid = __popcll(with), before = __popcll(with & ((1ull << lane) - 1));
+  order[with >> lane & 1 ? before : valid + lane - before] = lane;
+  return valid;
 }
 
 // The same on tiles of up to 64 rows (low.hpp).
@@ -214,16 +247,7 @@ __device__ __forceinline__ void head_low_tile(const half_t* x, int x_rows, const
     }
   } else {
     store_low<RB>(
-        acc, smem, tid,
-        [&](int row, int col, float v) {
-          float c = n0 + col < to.vocab ? exp_diff(v, own.lse[row]) : 0.f;
-          const bool is_label = n0 + col == own.label[row];
-          if (is_label) c -= 1.f;
-          const half_t h = static_cast<half_t>(c * kCoeffScale);
-          if (is_label && row < tile.rows)
-            rows.label[tile.first + row] = c - static_cast<float>(h) * (1.f / kCoeffScale);
-          return h;
-        },
+        acc, smem, tid, HeadCoeff{own, tile, rows, n0, to.vocab},
         [&](int row, int col, half8_t v) {
           if (row < tile.rows && n0 + col < to.v1)
             *reinterpret_cast<half8_t*>(to.coeff + static_cast<size_t>(tile.first + row) * to.pitch + n0 + col - to.v0) = v;
@@ -231,23 +255,39 @@ __device__ __forceinline__ void head_low_tile(const half_t* x, int x_rows, const
   }
 }
 
+// plan.counts NULL: up to 64 rows without a plan, each workgroup orders them itself.
 template <int BITS, bool GRAD>
 __global__ __launch_bounds__(512, 4) void head_low_kernel(const half_t* __restrict__ x, int x_rows, int gathered,
                                                           Layers layers, SlotPlan plan, HeadRows rows, HeadOut to) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x;
-  RowTile tile;
-  int ct;
-  if (!find_tile(plan, (to.v1 - to.v0 + 255) / 256, blockIdx.x, tile, ct)) return;
   int32_t* words = reinterpret_cast<int32_t*>(smem + low_lds<BITS>() - kLowRowsLds);
   const HeadTileRows own{words, words + 64, reinterpret_cast<float*>(words + 128)};
-  if (tid < 64) {
-    const int place = tile.first + min(tid, tile.rows - 1), m = plan.order[place];
-    own.source[tid] = gathered ? place : m;
-    own.label[tid] = rows.target[m];
-    if (GRAD) own.lse[tid] = rows.lse[m];
+  RowTile tile;
+  int ct;
+  if (plan.counts) {
+    if (!find_tile(plan, (to.v1 - to.v0 + 255) / 256, blockIdx.x, tile, ct)) return;
+    if (tid < 64) {
+      const int place = tile.first + min(tid, tile.rows - 1), m = plan.order[place];
+      own.source[tid] = gathered ? place : m;
+      own.label[tid] = rows.target[m];
+      if (GRAD) own.lse[tid] = rows.lse[m];
+    }
+    __syncthreads();
+  } else {
+    ct = blockIdx.x;
+    if (ct * 256 >= to.v1 - to.v0) return;
+    if (tid < 64) {
+      const int valid = order_rows(rows.target, x_rows, to.vocab, tid, own.source);
+      if (tid == 0) words[192] = valid;
+    }
+    __syncthreads();
+    tile = {};
+    tile.rows = words[192];
+    if (tile.rows == 0) return;
+    if (tid < tile.rows) own.label[tid] = rows.target[own.source[tid]];
+    __syncthreads();
   }
-  __syncthreads();
   const int n0 = to.v0 + 256 * ct;
   if (tile.rows > 32)
     head_low_tile<2, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
@@ -258,11 +298,20 @@ __global__ __launch_bounds__(512, 4) void head_low_kernel(const half_t* __restri
 // Joins the column tiles of 16 places per workgroup, 64 of them side by side in a fixed
 // order; rows without a target get zeros.
 __global__ __launch_bounds__(1024) void head_join_kernel(const MaxSum* __restrict__ part, int tiles, size_t places,
-                                                         SlotPlan plan, const float* __restrict__ label, int M,
+                                                         SlotPlan plan, const int32_t* __restrict__ target, int vocab,
+                                                         const float* __restrict__ label, int M,
                                                          float* __restrict__ loss, float* __restrict__ lse) {
   __shared__ MaxSum red[64][16];
+  __shared__ int32_t few[65];   // without a plan: the order, and the rows with a target
   const int at = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int p = blockIdx.x * 16 + at, valid = plan.counts[1];
+  if (!plan.counts) {
+    if (threadIdx.x < 64) {
+      const int valid = order_rows(target, M, vocab, threadIdx.x, few);
+      if (threadIdx.x == 0) few[64] = valid;
+    }
+    __syncthreads();
+  }
+  const int p = blockIdx.x * 16 + at, valid = plan.counts ? plan.counts[1] : few[64];
   MaxSum a = {-INFINITY, 0.f};
   if (p < valid) {
     int t = group;
@@ -281,7 +330,7 @@ __global__ __launch_bounds__(1024) void head_join_kernel(const MaxSum* __restric
     __syncthreads();
   }
   if (group != 0 || p >= M) return;
-  const int m = plan.order[p];
+  const int m = plan.counts ? plan.order[p] : few[p];
   if (p >= valid) {
     loss[m] = 0.f;
     lse[m] = 0.f;

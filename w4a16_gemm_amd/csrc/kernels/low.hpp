@@ -19,7 +19,7 @@
 //    distinct banks.
 #pragma once
 
-#include "tile.hpp"
+#include "experts.hpp"
 
 namespace w4a16 {
 
@@ -203,7 +203,10 @@ __device__ __forceinline__ void store_low(const LowSums<RB>& acc, unsigned char*
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       const int row = 8 * (r >> 2) + 4 * lh + (r & 3);
-      turn[row * PITCH + lc] = value(32 * b + row, 32 * wave + lc, acc.b[b][r]);
+      const float v[1] = {acc.b[b][r]};
+      half_t o[1];
+      value(32 * b + row, 32 * wave + lc, 32, v, o);
+      turn[row * PITCH + lc] = o[0];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -223,7 +226,7 @@ __device__ __forceinline__ void low_tile(const half_t* x, int x_rows, const Laye
   low_product(ld, l.zeros, smem, tid, wave, acc);
   __syncthreads();
   store_low<RB>(
-      acc, smem, tid, [&](int, int, float v) { return static_cast<half_t>(v); },
+      acc, smem, tid, RoundValues(),
       [&](int row, int col, half8_t v) {
         if (row < rows && n0 + col < N) *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slots[row]) * N + n0 + col) = v;
       });
