@@ -136,22 +136,23 @@ int launch_forward(dim3 grid, hipStream_t st, const half_t* x, int x_rows, int g
   return check_launch("experts launch");
 }
 
-template <int STEPS, int BITS>
+template <int STEPS, int BITS, bool LONG, bool WAVE>
 int launch_few_t(const FewShape& f, hipStream_t st, const half_t* x, int by_slot, int T, const int32_t* index, int S,
                  int E, const Layers& l, half_t* y) {
-  auto kern = experts_few_kernel<STEPS, BITS>;
-  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), few_lds(16));
+  auto kern = experts_few_kernel<STEPS, BITS, LONG, WAVE>;
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), few_lds<WAVE>(16));
   if (int rc = lds_status(lds_ok)) return rc;
-  hipLaunchKernelGGL(kern, dim3(kUnits), dim3(64 * f.waves), few_lds(f.waves), st, x, by_slot, T, index, S, E, l, f.chunks,
-                     y);
+  hipLaunchKernelGGL(kern, dim3(kUnits), dim3(64 * f.waves), few_lds<WAVE>(f.waves), st, x, by_slot, T, index, S, E, l,
+                     f.chunks, y);
   return check_launch("experts launch");
 }
 
-template <int BITS>
+template <int BITS, bool WAVE>
 int launch_few(const FewShape& f, hipStream_t st, const half_t* x, int by_slot, int T, const int32_t* index, int S, int E,
                const Layers& l, half_t* y) {
-  if (f.steps == 1) return launch_few_t<1, BITS>(f, st, x, by_slot, T, index, S, E, l, y);
-  return launch_few_t<2, BITS>(f, st, x, by_slot, T, index, S, E, l, y);
+  if (f.chunks > 1) return launch_few_t<2, BITS, true, WAVE>(f, st, x, by_slot, T, index, S, E, l, y);   // 17 or more steps
+  if (f.steps == 1) return launch_few_t<1, BITS, false, WAVE>(f, st, x, by_slot, T, index, S, E, l, y);
+  return launch_few_t<2, BITS, false, WAVE>(f, st, x, by_slot, T, index, S, E, l, y);
 }
 
 template <int BITS>
@@ -179,7 +180,8 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
   const FewShape few = pick_few(S, E, K);
   if (few.ok) {
     if (act) hipLaunchKernelGGL(gather_rows_kernel, dim3(S), dim3(256), 0, st, hx, index, E, l, T, mem.gathered);
-    return launch_few<BITS>(few, st, act ? mem.gathered : hx, act, T, index, S, E, l, reinterpret_cast<half_t*>(y));
+    auto launch = S <= 64 ? launch_few<BITS, true> : launch_few<BITS, false>;
+    return launch(few, st, act ? mem.gathered : hx, act, T, index, S, E, l, reinterpret_cast<half_t*>(y));
   }
   run_plan(mem.plan, index, S, E, E, shape.height, true, st);
   if (act)
