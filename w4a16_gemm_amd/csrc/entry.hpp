@@ -107,7 +107,9 @@ SlotPlan take_plan(Carver& ws, int64_t S, int64_t tiles, bool tile_of) {
 
 constexpr int kUnits = 256;   // compute units
 
-// Cost of a row tile against one of 256 rows: the weights are expanded for fewer rows.
+// Cost of a row tile against one of 256 rows: the weights are expanded for fewer rows.  (64
+// experts of 256 / 128 / 64 rows, N and K 4096, 4 bits, whole calls: 549 / 366 / 268 us, back
+// 564 / 401 / 298 us.)
 double height_cost(int height) { return height == 256 ? 1.0 : height == 128 ? 0.64 : 0.45; }
 
 // Row tiles of S slots over E experts, whose sizes are known on the device only: taken as
