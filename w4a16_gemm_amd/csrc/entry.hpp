@@ -91,8 +91,8 @@ Layers make_layers(const int32_t* qweight, const uint16_t* scales, const int32_t
   return l;
 }
 
-// Row tiles that S slots of E experts can need, one more expert for the slots without one.
-int64_t most_tiles(int64_t S, int E, int height) { return S / height + (E + 1 < S ? E + 1 : S); }
+// Row tiles that S slots of E experts can need.
+int64_t most_tiles(int64_t S, int E, int height) { return S / height + (E < S ? E : S); }
 
 SlotPlan take_plan(Carver& ws, int64_t S, int64_t tiles, bool tile_of) {
   SlotPlan p;
@@ -160,13 +160,13 @@ int lds_status(hipError_t e) {
 
 // Launches that the entry points share (experts.hip).
 // The slots of index grouped by expert; arguments as plan_slots_kernel.
-void run_plan(const SlotPlan& p, const int32_t* index, int S, int E, int limit, int height, bool fill, hipStream_t st);
+void run_plan(const SlotPlan& p, const int32_t* index, int S, int E, int limit, int height, hipStream_t st);
 // Act order: the valid slots' rows in stored channel order; the orders' inverses.
 void run_gather(const SlotPlan& p, const half_t* x, const int32_t* index, const Layers& l, int S, int T, half_t* out,
                 hipStream_t st);
 void run_invert(const Layers& l, int E, int32_t* inverse, hipStream_t st);
 // The transposed product over at most `tiles` row tiles; arguments as transposed_kernel.
 int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                   const SlotPlan& p, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st);
+                   const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st);
 
 }  // namespace w4a16

@@ -16,9 +16,9 @@
 
 namespace w4a16 {
 
-void run_plan(const SlotPlan& p, const int32_t* index, int S, int E, int limit, int height, bool fill, hipStream_t st) {
+void run_plan(const SlotPlan& p, const int32_t* index, int S, int E, int limit, int height, hipStream_t st) {
   hipLaunchKernelGGL(plan_slots_kernel, dim3(1), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (E + 1), st, index, S,
-                     E, limit, height, fill ? 1 : 0, p);
+                     E, limit, height, p);
 }
 
 void run_gather(const SlotPlan& p, const half_t* x, const int32_t* index, const Layers& l, int S, int T, half_t* out,
@@ -34,12 +34,12 @@ namespace {
 
 template <int BITS>
 int launch_transposed(int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                      const SlotPlan& p, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st) {
+                      const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st) {
   auto kern = transposed_kernel<BITS>;
   static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), transposed_lds<BITS>());
   if (int rc = lds_status(lds_ok)) return rc;
   const dim3 grid(static_cast<unsigned>(piece_blocks(tiles * ceil_div(l.K, 256))));
-  hipLaunchKernelGGL(kern, grid, dim3(512), transposed_lds<BITS>(), st, a, a_rows, a_pitch, by_place ? 1 : 0, l, p, n_begin,
+  hipLaunchKernelGGL(kern, grid, dim3(512), transposed_lds<BITS>(), st, a, a_rows, a_pitch, by_place ? 1 : 0, l, p, slots, n_begin,
                      n_end, n_valid, n_most, most, to);
   return check_launch("transposed product launch");
 }
@@ -47,9 +47,9 @@ int launch_transposed(int64_t tiles, const half_t* a, int a_rows, int a_pitch, b
 }  // namespace
 
 int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                   const SlotPlan& p, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st) {
-  return bits == 4 ? launch_transposed<4>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, n_valid, n_most, most, to, st)
-                   : launch_transposed<8>(tiles, a, a_rows, a_pitch, by_place, l, p, n_begin, n_end, n_valid, n_most, most, to, st);
+                   const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st) {
+  return bits == 4 ? launch_transposed<4>(tiles, a, a_rows, a_pitch, by_place, l, p, slots, n_begin, n_end, n_valid, n_most, most, to, st)
+                   : launch_transposed<8>(tiles, a, a_rows, a_pitch, by_place, l, p, slots, n_begin, n_end, n_valid, n_most, most, to, st);
 }
 
 namespace {
@@ -132,12 +132,12 @@ int check_forward(int M, int T, int E, int N, int K, bool act) {
 }
 
 template <int NB, int BITS>
-int launch_forward(dim3 grid, hipStream_t st, const half_t* x, int x_rows, int gathered, int T, const Layers& l,
+int launch_forward(dim3 grid, hipStream_t st, const half_t* x, int x_rows, int gathered, int S, int T, const Layers& l,
                    const SlotPlan& plan, half_t* y) {
   auto kern = experts_gemm_kernel<NB, BITS>;
   static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), tile_lds<BITS>());
   if (int rc = lds_status(lds_ok)) return rc;
-  hipLaunchKernelGGL(kern, grid, dim3(512), tile_lds<BITS>(), st, x, x_rows, gathered, T, l, plan, y);
+  hipLaunchKernelGGL(kern, grid, dim3(512), tile_lds<BITS>(), st, x, x_rows, gathered, S, T, l, plan, y);
   return check_launch("experts launch");
 }
 
@@ -188,7 +188,7 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
     auto launch = S <= 64 ? launch_few<BITS, true> : launch_few<BITS, false>;
     return launch(few, st, act ? mem.gathered : hx, act, T, index, S, E, l, reinterpret_cast<half_t*>(y));
   }
-  run_plan(mem.plan, index, S, E, E, shape.height, true, st);
+  run_plan(mem.plan, index, S, E, E, shape.height, st);
   if (act)
     run_gather(mem.plan, hx, index, l, S, T, mem.gathered, st);
   const dim3 grid(static_cast<unsigned>(up8(most_tiles(S, E, shape.height) * ceil_div(N, 64 * shape.nb))));
@@ -197,12 +197,12 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
   if (shape.height == 64 && shape.nb == 4) {
     static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(experts_low_kernel<BITS>), low_lds<BITS>());
     if (int rc = lds_status(lds_ok)) return rc;
-    hipLaunchKernelGGL(experts_low_kernel<BITS>, grid, dim3(512), low_lds<BITS>(), st, rows, act ? S : M, act ? 1 : 0, T, l,
+    hipLaunchKernelGGL(experts_low_kernel<BITS>, grid, dim3(512), low_lds<BITS>(), st, rows, act ? S : M, act ? 1 : 0, S, T, l,
                        mem.plan, hy);
     return check_launch("experts launch");
   }
-  if (shape.nb == 4) return launch_forward<4, BITS>(grid, st, rows, act ? S : M, act, T, l, mem.plan, hy);
-  return launch_forward<1, BITS>(grid, st, rows, act ? S : M, act, T, l, mem.plan, hy);
+  if (shape.nb == 4) return launch_forward<4, BITS>(grid, st, rows, act ? S : M, act, S, T, l, mem.plan, hy);
+  return launch_forward<1, BITS>(grid, st, rows, act ? S : M, act, S, T, l, mem.plan, hy);
 }
 
 // --- backward ---------------------------------------------------------------------------
@@ -249,12 +249,12 @@ int launch_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* 
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Layers l = make_layers(qweight, scales, qzeros, group_size, N, K, BITS, act);
   const bool direct = is_direct(T, act);
-  run_plan(mem.plan, index, S, E, E, shape.height, direct, st);
+  run_plan(mem.plan, index, S, E, E, shape.height, st);
   const half_t* h0 = reinterpret_cast<const half_t*>(dx0);
   half_t* hx = reinterpret_cast<half_t*>(dx);
   const TOut to{direct ? hx : nullptr, direct ? h0 : nullptr, mem.part, static_cast<size_t>(S), 0};
   if (int rc = run_transposed(BITS, most_tiles(S, E, shape.height), reinterpret_cast<const half_t*>(dy), S, N, false, l,
-                              mem.plan, 0, N, N, N, shape.most, to, st))
+                              mem.plan, S, 0, N, N, N, shape.most, to, st))
     return rc;
   if (mem.part) {
     if (act) {

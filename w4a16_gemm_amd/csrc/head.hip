@@ -98,7 +98,7 @@ int head_loss(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
     // up to 64 rows are ordered by every workgroup itself (37 rows: a launch less, 64 -> 58 us)
     const bool planned = act || M > 64 || height != 64;
     SlotPlan plan = mem.plan;
-    if (planned) run_plan(plan, target + m0, rows, 1, vocab, height, false, st);
+    if (planned) run_plan(plan, target + m0, rows, 1, vocab, height, st);
     else plan.counts = nullptr;
     if (act) run_gather(plan, hx, nullptr, l, rows, 1, mem.gathered, st);
     const HeadRows hr{target + m0, mem.label, nullptr};
@@ -182,8 +182,8 @@ int head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qwe
     const int rows = static_cast<int>(std::min<int64_t>(most, M - m0));
     const half_t* hx = reinterpret_cast<const half_t*>(x) + m0 * K;
     const int height = p.product.height;
-    run_plan(mem.plan, target + m0, rows, 1, vocab, height, false, st);
-    if (p.logit_height != height) run_plan(mem.logit_plan, target + m0, rows, 1, vocab, p.logit_height, false, st);
+    run_plan(mem.plan, target + m0, rows, 1, vocab, height, st);
+    if (p.logit_height != height) run_plan(mem.logit_plan, target + m0, rows, 1, vocab, p.logit_height, st);
     if (act) run_gather(mem.plan, hx, nullptr, l, rows, 1, mem.gathered, st);
     const HeadRows hr{target + m0, mem.remainder, lse + m0};
     for (int v0 = 0; v0 < vocab; v0 += p.cols) {
@@ -194,7 +194,7 @@ int head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qwe
                                            mem.logit_plan, hr, to))
         return rc;
       const TOut out{nullptr, nullptr, mem.part, static_cast<size_t>(rows), v0 > 0};
-      if (int rc = run_transposed(BITS, most_tiles(rows, 1, height), mem.coeff, rows, p.cols, true, l, mem.plan, v0, v1, vocab,
+      if (int rc = run_transposed(BITS, most_tiles(rows, 1, height), mem.coeff, rows, p.cols, true, l, mem.plan, rows, v0, v1, vocab,
                                   p.cols, p.product.most, out, st))
         return rc;
     }

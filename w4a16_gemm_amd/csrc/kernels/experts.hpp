@@ -110,11 +110,14 @@ __device__ __forceinline__ void experts_tile(const half_t* x, int x_rows, const 
 // gathered: x holds the valid slots' rows in the plan's order (act order), else row m of x
 // is that of slots [m T, (m + 1) T).
 template <int NB, int BITS>
-__global__ __launch_bounds__(512) void experts_gemm_kernel(const half_t* __restrict__ x, int x_rows, int gathered, int T,
-                                                           Layers layers, SlotPlan plan, half_t* __restrict__ y) {
+__global__ __launch_bounds__(512) void experts_gemm_kernel(const half_t* __restrict__ x, int x_rows, int gathered, int S,
+                                                           int T, Layers layers, SlotPlan plan, half_t* __restrict__ y) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int BN = 64 * NB;
   const int tid = threadIdx.x, N = layers.N;
+  each_empty(plan, S, [&](int slot) {
+    for (int n = 8 * tid; n < N; n += 8 * 512) *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slot) * N + n) = half8_t{};
+  });
   RowTile tile;
   int col;
   if (!find_tile(plan, (N + BN - 1) / BN, blockIdx.x, tile, col)) return;
@@ -127,12 +130,6 @@ __global__ __launch_bounds__(512) void experts_gemm_kernel(const half_t* __restr
   }
   __syncthreads();
   const int n0 = col * BN;
-  if (tile.expert < 0) {   // slots without an expert
-    const int cols = min(BN, N - n0);
-    for (int i = tid; i < tile.rows * (cols / 8); i += 512)
-      *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slots[i / (cols / 8)]) * N + n0 + i % (cols / 8) * 8) = half8_t{};
-    return;
-  }
   const Layers l = layers.at<BITS>(tile.expert);
   if (tile.height == 256)
     experts_tile<NB, 8, BITS>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);

@@ -234,10 +234,13 @@ __device__ __forceinline__ void low_tile(const half_t* x, int x_rows, const Laye
 
 // experts_gemm_kernel for plans of 64-row tiles.
 template <int BITS>
-__global__ __launch_bounds__(512, 4) void experts_low_kernel(const half_t* __restrict__ x, int x_rows, int gathered, int T,
-                                                             Layers layers, SlotPlan plan, half_t* __restrict__ y) {
+__global__ __launch_bounds__(512, 4) void experts_low_kernel(const half_t* __restrict__ x, int x_rows, int gathered, int S,
+                                                             int T, Layers layers, SlotPlan plan, half_t* __restrict__ y) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, N = layers.N;
+  each_empty(plan, S, [&](int slot) {
+    for (int n = 8 * tid; n < N; n += 8 * 512) *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slot) * N + n) = half8_t{};
+  });
   RowTile tile;
   int col;
   if (!find_tile(plan, (N + 255) / 256, blockIdx.x, tile, col)) return;
@@ -250,12 +253,6 @@ __global__ __launch_bounds__(512, 4) void experts_low_kernel(const half_t* __res
   }
   __syncthreads();
   const int n0 = col * 256;
-  if (tile.expert < 0) {   // slots without an expert
-    const int cols = min(256, N - n0);
-    for (int i = tid; i < tile.rows * (cols / 8); i += 512)
-      *reinterpret_cast<half8_t*>(y + static_cast<size_t>(slots[i / (cols / 8)]) * N + n0 + i % (cols / 8) * 8) = half8_t{};
-    return;
-  }
   const Layers l = layers.at<BITS>(tile.expert);
   if (tile.rows > 32)
     low_tile<2, BITS>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);

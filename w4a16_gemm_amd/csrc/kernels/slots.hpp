@@ -5,7 +5,7 @@
 //  * the second pass ranks the 64 slots of a load among themselves by ballots over the bits
 //    of the expert's number (10 at most), so that the order is stable and does not depend on
 //    timing.
-// Slots without an expert come last.  Bound by the latency of the two passes: 8 loads of 64
+// Slots without an expert come last, in no tile.  Bound by the latency of the two passes: 8 loads of 64
 // slots per wavefront are in flight at once.  And the channel orders of act order.
 #pragma once
 
@@ -14,10 +14,9 @@
 namespace w4a16 {
 
 // Slots with index outside [0, limit) have no expert; index NULL: expert 0 for every slot.
-// E == limit, or E == 1: every slot with an index inside belongs to expert 0.  fill: row
-// tiles for the slots without an expert as well.
+// E == limit, or E == 1: every slot with an index inside belongs to expert 0.
 __global__ __launch_bounds__(kPlanThreads) void plan_slots_kernel(const int32_t* __restrict__ index, int S, int E,
-                                                                  int limit, int height, int fill, SlotPlan plan) {
+                                                                  int limit, int height, SlotPlan plan) {
   extern __shared__ int32_t hist[];   // [kPlanWaves][E + 1]
   __shared__ int32_t first[kMaxExperts + 2];
   __shared__ int32_t tile0[kMaxExperts + 2];
@@ -55,7 +54,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_slots_kernel(const int32_t*
       hist[w * bins + tid] = count;
       count += c;
     }
-    if (tid < E || fill) tiles = count / height + (count % height != 0);
+    if (tid < E) tiles = count / height + (count % height != 0);
   }
   // exclusive scan of (count, tiles) over the experts
   int pc = count, pt = tiles;
@@ -78,7 +77,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_slots_kernel(const int32_t*
   if (tid < bins)
     for (int i = 0; i < tiles; ++i) {
       RowTile t;
-      t.expert = tid < E ? tid : -1;
+      t.expert = tid;
       t.first = pc + i * height;
       t.rows = min(height, count - i * height);
       t.height = rest_height(t.rows, height);

@@ -310,17 +310,24 @@ __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int
   });
 }
 
-// a [a_rows][a_pitch]: by_place: row p belongs to place p of the plan's order, else row s to
+// slots: of the plan.  a [a_rows][a_pitch]: by_place: row p belongs to place p of the plan's order, else row s to
 // slot s.  The outputs [n_begin, n_end) against columns [0, n_end - n_begin) of a; those from
 // n_valid > n_end - 16 on, whose columns of a are 0, count as 0 whatever their scales.  A tile
 // in parts takes ceil(n_most / parts) outputs each, n_most >= n_end - n_begin (the same for
 // every launch that adds to the same sums).  Sums go to the places or slots alike.
 template <int BITS>
 __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restrict__ a, int a_rows, int a_pitch,
-                                                         int by_place, Layers layers, SlotPlan plan, int n_begin,
+                                                         int by_place, Layers layers, SlotPlan plan, int slots, int n_begin,
                                                          int n_end, int n_valid, int n_most, int most, TOut to) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x, K = layers.K;
+  if (to.out)   // slots without an expert: dx0 alone
+    each_empty(plan, slots, [&](int slot) {
+      for (int k = 8 * tid; k < K; k += 8 * 512) {
+        const size_t at = static_cast<size_t>(slot) * K + k;
+        *reinterpret_cast<half8_t*>(to.out + at) = to.dx0 ? *reinterpret_cast<const half8_t*>(to.dx0 + at) : half8_t{};
+      }
+    });
   RowTile tile;
   int col, piece, pieces;
   if (!find_piece(plan, (K + 255) / 256, most, blockIdx.x, tile, col, piece, pieces)) return;
@@ -328,15 +335,6 @@ __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restric
   int32_t* rows = reinterpret_cast<int32_t*>(smem + transposed_lds<BITS>() - kTileRowsLds);
   if (tid < tile.rows) rows[tid] = by_place ? tile.first + tid : plan.order[tile.first + tid];
   __syncthreads();
-  if (tile.expert < 0) {   // slots without an expert: dx0 alone (only where out takes the sums)
-    if (piece > 0) return;
-    const int runs = min(256, K - k0) / 8;
-    for (int i = tid; i < tile.rows * runs; i += 512) {
-      const size_t at = static_cast<size_t>(rows[i / runs]) * K + k0 + i % runs * 8;
-      *reinterpret_cast<half8_t*>(to.out + at) = to.dx0 ? *reinterpret_cast<const half8_t*>(to.dx0 + at) : half8_t{};
-    }
-    return;
-  }
   const Layers l = layers.at<BITS>(tile.expert);
   const int len = (n_most + 64 * pieces - 1) / (64 * pieces) * 64;
   const int a0 = piece * len, n0 = n_begin + a0, n1 = min(n_end, n0 + len);
