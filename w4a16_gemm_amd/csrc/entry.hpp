@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "internal.hpp"
 #include "kernels/plan.hpp"
@@ -107,38 +108,114 @@ SlotPlan take_plan(Carver& ws, int64_t S, int64_t tiles, bool tile_of) {
 
 constexpr int kUnits = 256;   // compute units
 
-// Cost of a row tile against one of 256 rows: the weights are expanded for fewer rows.  (64
-// experts of 256 / 128 / 64 rows, N and K 4096, 4 bits, whole calls: 549 / 366 / 268 us, back
-// 564 / 401 / 298 us.)
-double height_cost(int height) { return height == 256 ? 1.0 : height == 128 ? 0.64 : 0.45; }
+// A tile's place in a kernel: the height of the plan's full tiles; bm, the rows that the kernel's
+// ring has room for (256: a workgroup per compute unit, 128: two, with half the memory each; 64:
+// two of the 64-row kernel); its 64-column blocks, 4 or 1.
+struct TileShape {
+  int height, bm, nb;
+};
 
-// Row tiles of S slots over E experts, whose sizes are known on the device only: taken as
-// equal, with half a tile more for each where there is more than one.
-double tiles_of(int64_t S, int E, int height) {
-  if (E == 1) return static_cast<double>(ceil_div(S, height));
-  const double used = static_cast<double>(E < S ? E : S);
-  const double per = static_cast<double>(S) / used / height;
-  return used * (per <= 0.7 ? 1.0 : per + 0.5);
+// Time of a round of tiles against one of 256-row tiles of 256 columns: `full` with as many
+// workgroups as run at once (tile_slots), `one` with at most one per compute unit.  Measured:
+// whole calls of 64 experts of 256, 128 and 64 rows (N and K 4096, 4 bits), less 15 us (20 us) of
+// launches: bm 256 570 / 378 / 276 us, 128 - / 343 / 250 us, 64 203 us for the last; back 564 /
+// 401 / 298 us, 128 - / 362 / 262 us.  One per compute unit: eight experts of 256, 128, 64 rows
+// 117 / 75 / 61 us, 64 45 us.  With half the memory alone on a compute unit 8-bit tiles wait for
+// their shorter ring: 2588 rows against 2346 columns, K 2816 76 us, so 119 us.
+struct TileCost {
+  double one, full;
+};
+
+TileCost forward_cost(const TileShape& s, int rows) {
+  constexpr double one[2][3] = {{0.73, 0.43, 0.33}, {0.33, 0.22, 0.15}};
+  constexpr double full256[2][3] = {{1.0, 0.65, 0.47}, {0.40, 0.26, 0.20}};
+  constexpr double full128[2][3] = {{2.0, 1.18, 0.85}, {0.80, 0.41, 0.30}};
+  if (s.bm == 64) return {0.22, 0.68};
+  const int n = s.nb == 1, i = rows == 256 ? 0 : rows == 128 ? 1 : 2;
+  return s.bm == 256 ? TileCost{one[n][i], full256[n][i]} : TileCost{1.2 * one[n][i], full128[n][i]};
 }
 
-// Height of the full row tiles and the most parts of a tile of the transposed product (see
-// Pieces): parts of at least 512 outputs, partial sums of at most 512 MB.
+TileCost transposed_cost(const TileShape& s, int rows) {
+  if (s.bm == 256) return rows == 256 ? TileCost{1.0, 1.0} : rows == 128 ? TileCost{0.60, 0.70} : TileCost{0.45, 0.51};
+  return rows == 128 ? TileCost{0.75, 1.26} : TileCost{0.55, 0.89};
+}
+
+// Row tiles of S slots over E experts, their mean cost, and the largest with one per compute
+// unit.  The groups' sizes are known on the device only: taken as 0.7 to 1.3 of the mean where
+// there is more than one.
+struct TileMix {
+  double tiles = 0, one = 0, full = 0;
+};
+
+template <class Cost>
+TileMix mix_of(int64_t S, int E, const TileShape& shape, Cost cost) {
+  TileMix m;
+  const int64_t used = E < S ? E : S;
+  const double sizes[] = {1.0, 0.7, 0.85, 1.15, 1.3};
+  const int count = used == 1 ? 1 : 5;
+  for (int i = 0; i < count; ++i) {
+    const int64_t rows = std::max<int64_t>(1, static_cast<int64_t>(static_cast<double>(S) / used * sizes[i] + 0.5));
+    const auto add = [&](double n, int tile) {
+      const TileCost c = cost(shape, tile);
+      m.tiles += n, m.full += n * c.full;
+      if (n > 0) m.one = std::max(m.one, c.one);
+    };
+    add(static_cast<double>(rows / shape.height), shape.height);
+    const int rest = static_cast<int>(rows % shape.height);
+    if (rest) add(1, rest_height(rest, shape.height));
+  }
+  m.full /= m.tiles;
+  m.tiles *= static_cast<double>(used) / count;
+  return m;
+}
+
+// Time of a product of S slots over E experts with `cols` output columns.  One expert's rounds
+// are whole, of an estimated number of tiles half a round more on average.
+double forward_time(int64_t S, int E, int cols, const TileShape& shape) {
+  const TileMix m = mix_of(S, E, shape, forward_cost);
+  const double wgs = m.tiles * ceil_div(cols, 64 * shape.nb);
+  if (wgs <= kUnits) return m.one;
+  const double rounds = wgs / (8 * tile_slots(shape.bm));
+  return m.full * (rounds <= 1 ? 1.0 : E > 1 ? rounds + 0.5 : rounds < 8 ? std::ceil(rounds) : rounds);
+}
+
+// The shape of least time among those with nb blocks or fewer.
+TileShape pick_forward(int64_t S, int E, int cols, bool narrow) {
+  constexpr TileShape shapes[] = {{256, 256, 4}, {128, 256, 4}, {128, 128, 4}, {64, 64, 4},
+                                  {256, 256, 1}, {128, 256, 1}, {128, 128, 1}, {64, 256, 1}, {64, 128, 1}};
+  TileShape best = shapes[0];
+  double least = 1e300;
+  for (const TileShape& s : shapes) {
+    if (s.nb == 1 && !narrow) continue;
+    const double cost = forward_time(S, E, cols, s);
+    if (cost < 0.999 * least) least = cost, best = s;
+  }
+  return best;
+}
+
+// Shape of the tiles and the most parts of a tile of the transposed product (see Pieces): parts
+// of at least 512 outputs, partial sums of at most 512 MB.
 struct TransposedShape {
-  int height, most;
+  int height, bm, most;
 };
 
 TransposedShape pick_transposed(int64_t S, int E, int outputs, int K) {
+  constexpr TileShape shapes[] = {{256, 256, 4}, {128, 256, 4}, {64, 256, 4}, {128, 128, 4}, {64, 128, 4}};
   const int64_t fit = (int64_t{512} << 20) / (4 * S * K);
-  TransposedShape best{256, 1};
-  best.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({int64_t{16}, fit, outputs / 512})));
+  TransposedShape best{256, 256, 1};
+  best.most = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({int64_t{32}, fit, outputs / 512})));
   double least = 1e300;
-  for (int height : {256, 128, 64}) {
-    const int64_t chunk = ceil_div(static_cast<int64_t>(tiles_of(S, E, height) * ceil_div(K, 256) + 0.999), 8);
-    const int64_t rest = chunk % 32;
-    double tail = rest ? 1.0 : 0.0;
-    for (int f = 2; f <= best.most && f * rest <= 64; ++f) tail = std::min(tail, static_cast<double>(ceil_div(rest * f, 32)) / f + 0.02 * f);
-    const double cost = (static_cast<double>(chunk / 32) + tail) * height_cost(height);
-    if (cost < 0.999 * least) least = cost, best.height = height;
+  for (const TileShape& s : shapes) {
+    const TileMix m = mix_of(S, E, s, transposed_cost);
+    const int side = tile_slots(s.bm);
+    const int64_t chunk = ceil_div(static_cast<int64_t>(m.tiles * ceil_div(K, 256) + 0.999), 8);
+    const int64_t rest = chunk % side;
+    double tail = rest == 0 ? 0 : rest <= 32 ? m.one : m.full;
+    for (int f = 2; f <= best.most && f * rest <= 2 * side; ++f)
+      tail = std::min(tail, (f * rest <= 32 ? m.one : m.full * ceil_div(rest * f, side)) / f +
+                                f * part_cost(static_cast<int>(rest), outputs));
+    const double cost = static_cast<double>(chunk / side) * m.full + tail;
+    if (cost < 0.999 * least) least = cost, best.height = s.height, best.bm = s.bm;
   }
   return best;
 }
@@ -166,7 +243,8 @@ void run_gather(const SlotPlan& p, const half_t* x, const int32_t* index, const 
                 hipStream_t st);
 void run_invert(const Layers& l, int E, int32_t* inverse, hipStream_t st);
 // The transposed product over at most `tiles` row tiles; arguments as transposed_kernel.
-int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                   const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st);
+int run_transposed(int bits, int bm, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place,
+                   const Layers& l, const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most,
+                   const TOut& to, hipStream_t st);
 
 }  // namespace w4a16

@@ -32,24 +32,28 @@ void run_invert(const Layers& l, int E, int32_t* inverse, hipStream_t st) {
 
 namespace {
 
-template <int BITS>
+template <int BITS, int BM>
 int launch_transposed(int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                      const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st) {
-  auto kern = transposed_kernel<BITS>;
-  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), transposed_lds<BITS>());
+                      const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most,
+                      const TOut& to, hipStream_t st) {
+  auto kern = transposed_kernel<BITS, BM>;
+  constexpr size_t lds = transposed_lds<BITS, BM>();
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), lds);
   if (int rc = lds_status(lds_ok)) return rc;
-  const dim3 grid(static_cast<unsigned>(piece_blocks(tiles * ceil_div(l.K, 256))));
-  hipLaunchKernelGGL(kern, grid, dim3(512), transposed_lds<BITS>(), st, a, a_rows, a_pitch, by_place ? 1 : 0, l, p, slots, n_begin,
-                     n_end, n_valid, n_most, most, to);
-  return check_launch("transposed product launch");
+  const dim3 grid(static_cast<unsigned>(piece_blocks(tiles * ceil_div(l.K, 256), tile_slots(BM))));
+  hipLaunchKernelGGL(kern, grid, dim3(512), lds, st, a, a_rows, a_pitch, by_place ? 1 : 0, l, p, slots, n_begin, n_end,
+                     n_valid, n_most, most, to);
+  return check_launch("transposed launch");
 }
 
 }  // namespace
 
-int run_transposed(int bits, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place, const Layers& l,
-                   const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most, const TOut& to, hipStream_t st) {
-  return bits == 4 ? launch_transposed<4>(tiles, a, a_rows, a_pitch, by_place, l, p, slots, n_begin, n_end, n_valid, n_most, most, to, st)
-                   : launch_transposed<8>(tiles, a, a_rows, a_pitch, by_place, l, p, slots, n_begin, n_end, n_valid, n_most, most, to, st);
+int run_transposed(int bits, int bm, int64_t tiles, const half_t* a, int a_rows, int a_pitch, bool by_place,
+                   const Layers& l, const SlotPlan& p, int slots, int n_begin, int n_end, int n_valid, int n_most, int most,
+                   const TOut& to, hipStream_t st) {
+  auto launch = bits == 4 ? (bm == 256 ? launch_transposed<4, 256> : launch_transposed<4, 128>)
+                          : (bm == 256 ? launch_transposed<8, 256> : launch_transposed<8, 128>);
+  return launch(tiles, a, a_rows, a_pitch, by_place, l, p, slots, n_begin, n_end, n_valid, n_most, most, to, st);
 }
 
 namespace {
@@ -64,27 +68,9 @@ int check_experts(int M, int T, int E, int N, int K, int group_size, int bits) {
 
 // --- tile shapes ----------------------------------------------------------------------
 
-// Height of the full row tiles, and 64-column blocks of a column tile, for S slots over E
-// experts and `cols` output columns, by the rounds that the tiles need over the compute units
-// and a tile's cost: 64 columns instead of 256 0.35 (the rows are read for fewer columns).
 // Tiles of 64 columns against 256, K 4096: 300 rows of one expert, N 4096 40.0 / 43.0 us, 128 of
 // two 8-bit experts, N 1024 37.2 / 51.4 us.
-struct TileShape {
-  int height, nb;
-};
-
-TileShape pick_shape(int64_t S, int E, int cols) {
-  TileShape best{256, 4};
-  double least = 1e300;
-  for (int height : {256, 128, 64})
-    for (int nb : {4, 1}) {
-      const double wgs = tiles_of(S, E, height) * ceil_div(cols, 64 * nb);
-      const double rounds = wgs > 8 * kUnits ? wgs / kUnits : static_cast<double>(ceil_div(static_cast<int64_t>(wgs), kUnits));
-      const double cost = rounds * height_cost(height) * (nb == 4 ? 1.0 : 0.35);
-      if (cost < 0.999 * least) least = cost, best = {height, nb};
-    }
-  return best;
-}
+TileShape pick_shape(int64_t S, int E, int cols) { return pick_forward(S, E, cols, true); }
 
 // --- forward ----------------------------------------------------------------------------
 
@@ -131,13 +117,14 @@ int check_forward(int M, int T, int E, int N, int K, bool act) {
   return W4A16_OK;
 }
 
-template <int NB, int BITS>
+template <int NB, int BITS, int BM>
 int launch_forward(dim3 grid, hipStream_t st, const half_t* x, int x_rows, int gathered, int S, int T, const Layers& l,
                    const SlotPlan& plan, half_t* y) {
-  auto kern = experts_gemm_kernel<NB, BITS>;
-  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), tile_lds<BITS>());
+  auto kern = experts_gemm_kernel<NB, BITS, BM>;
+  constexpr size_t lds = tile_lds<BITS, BM>();
+  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(kern), lds);
   if (int rc = lds_status(lds_ok)) return rc;
-  hipLaunchKernelGGL(kern, grid, dim3(512), tile_lds<BITS>(), st, x, x_rows, gathered, S, T, l, plan, y);
+  hipLaunchKernelGGL(kern, grid, dim3(512), lds, st, x, x_rows, gathered, S, T, l, plan, y);
   return check_launch("experts launch");
 }
 
@@ -194,15 +181,16 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
   const dim3 grid(static_cast<unsigned>(up8(most_tiles(S, E, shape.height) * ceil_div(N, 64 * shape.nb))));
   const half_t* rows = act ? mem.gathered : hx;
   half_t* hy = reinterpret_cast<half_t*>(y);
-  if (shape.height == 64 && shape.nb == 4) {
+  if (shape.bm == 64) {
     static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(experts_low_kernel<BITS>), low_lds<BITS>());
     if (int rc = lds_status(lds_ok)) return rc;
     hipLaunchKernelGGL(experts_low_kernel<BITS>, grid, dim3(512), low_lds<BITS>(), st, rows, act ? S : M, act ? 1 : 0, S, T, l,
                        mem.plan, hy);
     return check_launch("experts launch");
   }
-  if (shape.nb == 4) return launch_forward<4, BITS>(grid, st, rows, act ? S : M, act, S, T, l, mem.plan, hy);
-  return launch_forward<1, BITS>(grid, st, rows, act ? S : M, act, S, T, l, mem.plan, hy);
+  auto launch = shape.nb == 4 ? (shape.bm == 256 ? launch_forward<4, BITS, 256> : launch_forward<4, BITS, 128>)
+                              : (shape.bm == 256 ? launch_forward<1, BITS, 256> : launch_forward<1, BITS, 128>);
+  return launch(grid, st, rows, act ? S : M, act, S, T, l, mem.plan, hy);
 }
 
 // --- backward ---------------------------------------------------------------------------
@@ -230,7 +218,7 @@ int check_backward(int M, int T, int E, int N, int K, bool act) {
   const int64_t S = static_cast<int64_t>(M) * T;
   if (S * N >= kMaxElements) return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d N=%d: 2^31 elements or more", M, T, N);
   const TransposedShape shape = pick_transposed(S, E, N, K);
-  if (piece_blocks(most_tiles(S, E, shape.height) * ceil_div(K, 256)) > kMaxBlocks || (!is_direct(T, act) && M > kMaxBlocks))
+  if (piece_blocks(most_tiles(S, E, shape.height) * ceil_div(K, 256), 64) > kMaxBlocks || (!is_direct(T, act) && M > kMaxBlocks))
     return fail(W4A16_ERR_UNSUPPORTED, "M=%d T=%d K=%d: more tiles or sums than one launch takes", M, T, K);
   return W4A16_OK;
 }
@@ -253,16 +241,16 @@ int launch_backward(const uint16_t* dy, const int32_t* qweight, const uint16_t* 
   const half_t* h0 = reinterpret_cast<const half_t*>(dx0);
   half_t* hx = reinterpret_cast<half_t*>(dx);
   const TOut to{direct ? hx : nullptr, direct ? h0 : nullptr, mem.part, static_cast<size_t>(S), 0};
-  if (int rc = run_transposed(BITS, most_tiles(S, E, shape.height), reinterpret_cast<const half_t*>(dy), S, N, false, l,
+  if (int rc = run_transposed(BITS, shape.bm, most_tiles(S, E, shape.height), reinterpret_cast<const half_t*>(dy), S, N, false, l,
                               mem.plan, S, 0, N, N, N, shape.most, to, st))
     return rc;
   if (mem.part) {
     if (act) {
       run_invert(l, E, mem.inverse, st);
-      hipLaunchKernelGGL(sum_ordered_kernel, dim3(M), dim3(512), 0, st, mem.part, static_cast<size_t>(S), shape.most, T,
+      hipLaunchKernelGGL(sum_ordered_kernel, dim3(M), dim3(512), 0, st, mem.part, static_cast<size_t>(S), shape.most, tile_slots(shape.bm), N, T,
                          index, E, mem.plan, mem.inverse, K, h0, hx);
     } else {
-      hipLaunchKernelGGL(sum_slots_kernel, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.most, T,
+      hipLaunchKernelGGL(sum_slots_kernel, dim3(M), dim3(256), 0, st, mem.part, static_cast<size_t>(S), shape.most, tile_slots(shape.bm), N, T,
                          index, E, mem.plan, K, direct ? 1 : 0, h0, hx);
     }
   }

@@ -24,19 +24,8 @@ int check_head(int M, int N, int K, int group_size, int vocab, int bits) {
   return W4A16_OK;
 }
 
-// Height of the full row tiles for M rows against `tiles` column tiles of 256, by the rounds
-// that the tiles need over the compute units (costs as in the products by expert).
-int pick_height(int M, int64_t tiles) {
-  int best = 256;
-  double least = 1e300;
-  for (int height : {256, 128, 64}) {
-    const double wgs = static_cast<double>(ceil_div(M, height) * tiles);
-    const double rounds = wgs > 8 * kUnits ? wgs / kUnits : static_cast<double>(ceil_div(static_cast<int64_t>(wgs), kUnits));
-    const double cost = rounds * height_cost(height);
-    if (cost < 0.999 * least) least = cost, best = height;
-  }
-  return best;
-}
+// Tiles of M rows against `tiles` column tiles of 256.
+TileShape pick_rows(int M, int64_t tiles) { return pick_forward(M, 1, static_cast<int>(256 * tiles), false); }
 
 int chunk_rows(int M) { return std::min(M, kChunkRows); }
 
@@ -52,22 +41,25 @@ struct LossMemory {
 LossMemory loss_memory(Carver& ws, int rows, int N, int K, bool act) {
   const int64_t tiles = ceil_div(N, 256);
   LossMemory m;
-  m.plan = take_plan(ws, rows, most_tiles(rows, 1, pick_height(rows, tiles)), false);
+  m.plan = take_plan(ws, rows, most_tiles(rows, 1, pick_rows(rows, tiles).height), false);
   m.part = ws.take<MaxSum>(static_cast<size_t>(tiles) * rows);
   m.label = ws.take<float>(rows);
   m.gathered = act ? ws.take<half_t>(static_cast<size_t>(rows) * K) : nullptr;
   return m;
 }
 
-// height: of the plan's full tiles; without a plan 64, for at most 64 rows.
+// Without a plan: the 64-row tiles, for at most 64 rows.
 template <int BITS, bool GRAD>
-int launch_head(int height, int64_t row_tiles, hipStream_t st, const half_t* x, int x_rows, bool gathered,
+int launch_head(int bm, int64_t row_tiles, hipStream_t st, const half_t* x, int x_rows, bool gathered,
                 const Layers& l, const SlotPlan& plan, const HeadRows& rows, const HeadOut& to) {
-  auto kern = height == 64 ? head_low_kernel<BITS, GRAD> : head_kernel<BITS, GRAD>;
-  const size_t lds = height == 64 ? low_lds<BITS>() : tile_lds<BITS>();
-  static const hipError_t low_ok = allow_lds(reinterpret_cast<const void*>(head_low_kernel<BITS, GRAD>), low_lds<BITS>());
-  static const hipError_t lds_ok = allow_lds(reinterpret_cast<const void*>(head_kernel<BITS, GRAD>), tile_lds<BITS>());
-  if (int rc = lds_status(height == 64 ? low_ok : lds_ok)) return rc;
+  auto kern = bm == 64    ? head_low_kernel<BITS, GRAD>
+              : bm == 128 ? head_kernel<BITS, GRAD, 128>
+                          : head_kernel<BITS, GRAD, 256>;
+  const size_t lds = bm == 64 ? low_lds<BITS>() : bm == 128 ? tile_lds<BITS, 128>() : tile_lds<BITS, 256>();
+  static const hipError_t ok[3] = {allow_lds(reinterpret_cast<const void*>(head_low_kernel<BITS, GRAD>), low_lds<BITS>()),
+                                   allow_lds(reinterpret_cast<const void*>(head_kernel<BITS, GRAD, 128>), tile_lds<BITS, 128>()),
+                                   allow_lds(reinterpret_cast<const void*>(head_kernel<BITS, GRAD, 256>), tile_lds<BITS, 256>())};
+  if (int rc = lds_status(ok[bm / 128])) return rc;
   const dim3 grid(static_cast<unsigned>(up8(row_tiles * ceil_div(to.v1 - to.v0, 256))));
   hipLaunchKernelGGL(kern, grid, dim3(512), lds, st, x, x_rows, gathered ? 1 : 0, l, plan, rows, to);
   return check_launch("head launch");
@@ -91,20 +83,20 @@ int head_loss(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.used);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Layers l = make_layers(qweight, scales, qzeros, group_size, N, K, BITS, act);
-  const int height = pick_height(most, ceil_div(N, 256));
+  const TileShape shape = pick_rows(most, ceil_div(N, 256));
   for (int64_t m0 = 0; m0 < M; m0 += most) {
     const int rows = static_cast<int>(std::min<int64_t>(most, M - m0));
     const half_t* hx = reinterpret_cast<const half_t*>(x) + m0 * K;
     // up to 64 rows are ordered by every workgroup itself (37 rows: a launch less, 64 -> 58 us)
-    const bool planned = act || M > 64 || height != 64;
+    const bool planned = act || M > 64 || shape.bm != 64;
     SlotPlan plan = mem.plan;
-    if (planned) run_plan(plan, target + m0, rows, 1, vocab, height, st);
+    if (planned) run_plan(plan, target + m0, rows, 1, vocab, shape.height, st);
     else plan.counts = nullptr;
     if (act) run_gather(plan, hx, nullptr, l, rows, 1, mem.gathered, st);
     const HeadRows hr{target + m0, mem.label, nullptr};
     const HeadOut to{mem.part, nullptr, 0, 0, vocab, vocab, static_cast<size_t>(rows)};
-    const int64_t row_tiles = planned ? most_tiles(rows, 1, height) : 1;
-    if (int rc = launch_head<BITS, false>(height, row_tiles, st, act ? mem.gathered : hx, rows, act, l, plan, hr, to)) return rc;
+    const int64_t row_tiles = planned ? most_tiles(rows, 1, shape.height) : 1;
+    if (int rc = launch_head<BITS, false>(shape.bm, row_tiles, st, act ? mem.gathered : hx, rows, act, l, plan, hr, to)) return rc;
     hipLaunchKernelGGL(head_join_kernel, dim3(static_cast<unsigned>(ceil_div(rows, 16))), dim3(1024), 0, st, mem.part,
                        static_cast<int>(ceil_div(vocab, 256)), static_cast<size_t>(rows), plan, target + m0, vocab,
                        mem.label, rows, loss + m0, lse + m0);
@@ -118,7 +110,8 @@ int head_loss(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
 // tile heights of its logits and of the product of its coefficients with its weights, and the
 // most parts of a tile of that product.
 struct PieceShape {
-  int cols, logit_height;
+  int cols;
+  TileShape logits;
   TransposedShape product;
 };
 
@@ -127,7 +120,7 @@ PieceShape pick_piece(int rows, int N, int K) {
   const int64_t fit = std::max<int64_t>(1, kCoeffElements / rows / 256) * 256;
   const int64_t pieces = ceil_div(N, fit);
   p.cols = static_cast<int>(ceil_div(ceil_div(N, pieces), 256) * 256);
-  p.logit_height = pick_height(rows, p.cols / 256);
+  p.logits = pick_rows(rows, p.cols / 256);
   p.product = pick_transposed(rows, 1, p.cols, K);
   return p;
 }
@@ -146,7 +139,7 @@ GradMemory grad_memory(Carver& ws, int rows, int N, int K, bool act) {
   GradMemory m;
   const int height = p.product.height;
   m.plan = take_plan(ws, rows, most_tiles(rows, 1, height), true);
-  m.logit_plan = p.logit_height == height ? m.plan : take_plan(ws, rows, most_tiles(rows, 1, p.logit_height), false);
+  m.logit_plan = p.logits.height == height ? m.plan : take_plan(ws, rows, most_tiles(rows, 1, p.logits.height), false);
   m.coeff = ws.take<half_t>(static_cast<size_t>(rows) * p.cols);
   m.part = ws.take<float>(static_cast<size_t>(p.product.most) * rows * K);
   m.remainder = ws.take<float>(rows);
@@ -183,23 +176,23 @@ int head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qwe
     const half_t* hx = reinterpret_cast<const half_t*>(x) + m0 * K;
     const int height = p.product.height;
     run_plan(mem.plan, target + m0, rows, 1, vocab, height, st);
-    if (p.logit_height != height) run_plan(mem.logit_plan, target + m0, rows, 1, vocab, p.logit_height, st);
+    if (p.logits.height != height) run_plan(mem.logit_plan, target + m0, rows, 1, vocab, p.logits.height, st);
     if (act) run_gather(mem.plan, hx, nullptr, l, rows, 1, mem.gathered, st);
     const HeadRows hr{target + m0, mem.remainder, lse + m0};
     for (int v0 = 0; v0 < vocab; v0 += p.cols) {
       // padding columns up to a whole load of zero points have the coefficient 0
       const int v1 = static_cast<int>(std::min<int64_t>(int64_t{v0} + p.cols, std::min<int64_t>(ceil_div(vocab, 16) * 16, N)));
       const HeadOut to{nullptr, mem.coeff, p.cols, v0, v1, vocab, static_cast<size_t>(rows)};
-      if (int rc = launch_head<BITS, true>(p.logit_height, most_tiles(rows, 1, p.logit_height), st, act ? mem.gathered : hx, rows, act, l,
+      if (int rc = launch_head<BITS, true>(p.logits.bm, most_tiles(rows, 1, p.logits.height), st, act ? mem.gathered : hx, rows, act, l,
                                            mem.logit_plan, hr, to))
         return rc;
       const TOut out{nullptr, nullptr, mem.part, static_cast<size_t>(rows), v0 > 0};
-      if (int rc = run_transposed(BITS, most_tiles(rows, 1, height), mem.coeff, rows, p.cols, true, l, mem.plan, rows, v0, v1, vocab,
+      if (int rc = run_transposed(BITS, p.product.bm, most_tiles(rows, 1, height), mem.coeff, rows, p.cols, true, l, mem.plan, rows, v0, v1, vocab,
                                   p.cols, p.product.most, out, st))
         return rc;
     }
     hipLaunchKernelGGL(head_dx_kernel<BITS>, dim3(rows), dim3(256), 0, st, mem.part, static_cast<size_t>(rows),
-                       p.product.most, mem.plan, l, act ? mem.inverse : nullptr, target + m0, mem.remainder, dloss + m0,
+                       p.product.most, tile_slots(p.product.bm), p.cols, mem.plan, l, act ? mem.inverse : nullptr, target + m0, mem.remainder, dloss + m0,
                        reinterpret_cast<half_t*>(dx) + m0 * K);
   }
   return check_launch("head backward launch");

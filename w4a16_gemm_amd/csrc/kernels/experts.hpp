@@ -83,12 +83,12 @@ struct RoundValues {
   }
 };
 
-template <int NB, int MB, int BITS>
+template <int NB, int MB, int BITS, int BM>
 __device__ __forceinline__ void experts_tile(const half_t* x, int x_rows, const Layers& l, half_t* y, unsigned char* smem,
                                              const int32_t* source, const int32_t* slots, int rows, int n0) {
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const TileLoader<NB, MB, BITS> ld(x, x_rows, l, smem, source, rows, n0, tid, wave);
+  const TileLoader<NB, MB, BITS, BM> ld(x, x_rows, l, smem, source, rows, n0, tid, wave);
   const int N = l.N;
   const RoundValues value;
   auto put = [&](int row, int col, half8_t v) {
@@ -109,8 +109,9 @@ __device__ __forceinline__ void experts_tile(const half_t* x, int x_rows, const 
 
 // gathered: x holds the valid slots' rows in the plan's order (act order), else row m of x
 // is that of slots [m T, (m + 1) T).
-template <int NB, int BITS>
-__global__ __launch_bounds__(512) void experts_gemm_kernel(const half_t* __restrict__ x, int x_rows, int gathered, int S,
+// BM: of tile.hpp, at least the plan's height.
+template <int NB, int BITS, int BM>
+__global__ __launch_bounds__(512, BM == 256 ? 2 : 4) void experts_gemm_kernel(const half_t* __restrict__ x, int x_rows, int gathered, int S,
                                                            int T, Layers layers, SlotPlan plan, half_t* __restrict__ y) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int BN = 64 * NB;
@@ -121,8 +122,8 @@ __global__ __launch_bounds__(512) void experts_gemm_kernel(const half_t* __restr
   RowTile tile;
   int col;
   if (!find_tile(plan, (N + BN - 1) / BN, blockIdx.x, tile, col)) return;
-  int32_t* slots = reinterpret_cast<int32_t*>(smem + tile_lds<BITS>() - kTileRowsLds);
-  int32_t* source = slots + 256;
+  int32_t* slots = reinterpret_cast<int32_t*>(smem + tile_lds<BITS, BM>() - 16 * BM);
+  int32_t* source = slots + BM;
   if (tid < tile.rows) {
     const int s = plan.order[tile.first + tid];
     slots[tid] = s;
@@ -131,12 +132,12 @@ __global__ __launch_bounds__(512) void experts_gemm_kernel(const half_t* __restr
   __syncthreads();
   const int n0 = col * BN;
   const Layers l = layers.at<BITS>(tile.expert);
-  if (tile.height == 256)
-    experts_tile<NB, 8, BITS>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
+  if (BM == 256 && tile.height == 256)
+    experts_tile<NB, BM == 256 ? 8 : 4, BITS, BM>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
   else if (tile.height == 128)
-    experts_tile<NB, 4, BITS>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
+    experts_tile<NB, 4, BITS, BM>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
   else
-    experts_tile<NB, 2, BITS>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
+    experts_tile<NB, 2, BITS, BM>(x, x_rows, l, y, smem, source, slots, tile.rows, n0);
 }
 
 }  // namespace w4a16

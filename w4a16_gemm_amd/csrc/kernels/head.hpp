@@ -108,14 +108,13 @@ struct HeadCoeff {
   }
 };
 
-template <int MB, int BITS, bool GRAD>
+template <int MB, int BITS, bool GRAD, int BM>
 __device__ __forceinline__ void head_tile(const half_t* x, int x_rows, const Layers& l, unsigned char* smem,
                                           const HeadTileRows& own, const RowTile& tile, const HeadRows& rows,
                                           const HeadOut& to, int n0, int ct) {
-  constexpr int BM = 32 * MB;
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const TileLoader<4, MB, BITS> ld(x, x_rows, l, smem, own.source, tile.rows, n0, tid, wave);
+  const TileLoader<4, MB, BITS, BM> ld(x, x_rows, l, smem, own.source, tile.rows, n0, tid, wave);
   float4_t acc[MB][4];
   tile_product(ld, l.zeros, smem, tid, wave, acc);
   __syncthreads();   // the ring's memory is used again
@@ -161,16 +160,16 @@ __device__ __forceinline__ void head_tile(const half_t* x, int x_rows, const Lay
 }
 
 // Logits of the rows of the plan's tiles against the columns [v0, v1), 256 at a time.
-template <int BITS, bool GRAD>
-__global__ __launch_bounds__(512) void head_kernel(const half_t* __restrict__ x, int x_rows, int gathered, Layers layers,
+template <int BITS, bool GRAD, int BM>
+__global__ __launch_bounds__(512, BM == 256 ? 2 : 4) void head_kernel(const half_t* __restrict__ x, int x_rows, int gathered, Layers layers,
                                                    SlotPlan plan, HeadRows rows, HeadOut to) {
   extern __shared__ __align__(16) unsigned char smem[];
   const int tid = threadIdx.x;
   RowTile tile;
   int ct;
   if (!find_tile(plan, (to.v1 - to.v0 + 255) / 256, blockIdx.x, tile, ct)) return;
-  int32_t* words = reinterpret_cast<int32_t*>(smem + tile_lds<BITS>() - kTileRowsLds);
-  const HeadTileRows own{words, words + 256, reinterpret_cast<float*>(words + 2 * 256)};
+  int32_t* words = reinterpret_cast<int32_t*>(smem + tile_lds<BITS, BM>() - 16 * BM);
+  const HeadTileRows own{words, words + BM, reinterpret_cast<float*>(words + 2 * BM)};
   if (tid < tile.height) {
     const int place = tile.first + min(tid, tile.rows - 1), m = plan.order[place];
     own.source[tid] = gathered ? place : m;
@@ -179,12 +178,12 @@ __global__ __launch_bounds__(512) void head_kernel(const half_t* __restrict__ x,
   }
   __syncthreads();
   const int n0 = to.v0 + 256 * ct;
-  if (tile.height == 256)
-    head_tile<8, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
+  if (BM == 256 && tile.height == 256)
+    head_tile<BM == 256 ? 8 : 4, BITS, GRAD, BM>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
   else if (tile.height == 128)
-    head_tile<4, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
+    head_tile<4, BITS, GRAD, BM>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
   else
-    head_tile<2, BITS, GRAD>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
+    head_tile<2, BITS, GRAD, BM>(x, x_rows, layers, smem, own, tile, rows, to, n0, ct);
 }
 
 // The order of up to 64 rows by their targets, as the plan's: rows with a target first.  By
@@ -345,7 +344,7 @@ __global__ __launch_bounds__(1024) void head_join_kernel(const MaxSum* __restric
 // dx[m] = dloss[m] (sum of the parts 2^-14 + remainder W^_target), rounded once; zeros for
 // rows without a target.  One workgroup per place, eight channels per thread.
 template <int BITS>
-__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ part, size_t places, int most,
+__global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ part, size_t places, int most, int side, int outputs,
                                                       SlotPlan plan, Layers l, const int32_t* __restrict__ inverse,
                                                       const int32_t* __restrict__ target,
                                                       const float* __restrict__ remainder,
@@ -357,7 +356,7 @@ __global__ __launch_bounds__(256) void head_dx_kernel(const float* __restrict__ 
   const int label = valid ? target[m] : 0;
   const float rest = valid ? remainder[p] : 0.f, d = valid ? dloss[m] : 0.f;
   const int tile = valid ? plan.tile_of[m] : 0;
-  const Pieces rule(max(1, plan.counts[0] * cols), most);
+  const Pieces rule(max(1, plan.counts[0] * cols), most, side, outputs);
   constexpr int PER = 32 / BITS;   // channels per word
   const uint32_t* codes = l.qw + static_cast<size_t>(label) * (K / PER);
   auto consts = [&](int k) {

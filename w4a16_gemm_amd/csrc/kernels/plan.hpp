@@ -84,23 +84,35 @@ __device__ __forceinline__ void each_empty(const SlotPlan& plan, int S, F f) {
   for (int64_t p = static_cast<int64_t>(plan.counts[1]) + blockIdx.x; p < S; p += gridDim.x) f(plan.order[p]);
 }
 
-// Products of too few tiles for whole rounds over the compute units: each XCD (32 of them)
-// takes `chunk` tiles, whole rounds of them as they are, the rest each in `pieces` parts of
-// the contraction, as many as make the rest's rounds shortest (two rounds at most).
+// Workgroups of an XCD (32 compute units) that run at once, by the rows that a tile's memory has
+// room for.
+__host__ __device__ constexpr int tile_slots(int bm) { return bm == 256 ? 32 : 64; }
+
+// What a part more of `rest` tiles costs, in the time of a tile: their partial sums are written
+// and read.  (512 KB per tile of 256 rows and 8 XCDs' tiles at 5 TB/s, a step of 64 outputs
+// being 2.3 us, are 23 rest / outputs; less than that is measured.)
+__host__ __device__ inline float part_cost(int rest, int outputs) { return 16.f * rest / outputs; }
+
+// Products of too few tiles for whole rounds over the compute units: each XCD (`side` workgroups
+// at once) takes `chunk` tiles, whole rounds of them as they are, the rest each in `pieces` parts
+// of the contraction, as many as make the rest's rounds shortest (two rounds at most).  Where
+// two workgroups share a compute unit, one alone takes 0.6 of their time.
 // Measured, whole calls: a training batch of 8192 slots over eight 8-bit experts (K 4096, N
 // 14336; about 36 row tiles of 16 columns, 2.25 rounds) 1683 -> 1348 us; 777 rows of two of
 // eight act-order experts of group 32 405 -> 361 us.
 struct Pieces {
   int chunk, whole, pieces;
 
-  __device__ __forceinline__ Pieces(int total, int most) {
+  __device__ __forceinline__ Pieces(int total, int most, int side, int outputs) {
     chunk = (total + 7) >> 3;
-    const int rest = chunk & 31;
+    const int rest = chunk % side;
     whole = chunk - rest;
     pieces = 1;
-    float least = 1.02f;
-    for (int f = 2; f <= most && f * rest <= 64; ++f) {
-      const float cost = static_cast<float>((rest * f + 31) >> 5) / f + 0.02f * f;
+    const float part = part_cost(rest, outputs);
+    float least = 1e30f;
+    for (int f = 1; f <= most && (f == 1 || f * rest <= 2 * side); ++f) {
+      const float rounds = side == 64 && f * rest <= 32 ? 0.6f : static_cast<float>((rest * f + side - 1) / side);
+      const float cost = rounds / f + part * f;
       if (cost < least) least = cost, pieces = f;
     }
   }
@@ -112,15 +124,15 @@ struct Pieces {
   }
 };
 
-// Workgroups that cover every part: 8 ((most chunk rounded down to 32) + 64).
-__host__ __device__ inline int64_t piece_blocks(int64_t tiles) { return 8 * ((tiles + 7) / 8 / 32 * 32 + 64); }
+// Workgroups that cover every part: 8 ((most chunk rounded down to `side`) + 2 side).
+__host__ __device__ inline int64_t piece_blocks(int64_t tiles, int side) { return 8 * ((tiles + 7) / 8 / side * side + 2 * side); }
 
 // The row tile, column and part of this workgroup; see find_tile.
-__device__ __forceinline__ bool find_piece(const SlotPlan& plan, int cols, int most, int bid, RowTile& tile, int& col,
+__device__ __forceinline__ bool find_piece(const SlotPlan& plan, int cols, int most, int side, int outputs, int bid, RowTile& tile, int& col,
                                            int& piece, int& pieces) {
   const int total = plan.counts[0] * cols;
   if (total == 0) return false;
-  const Pieces rule(total, most);
+  const Pieces rule(total, most, side, outputs);
   const int j = bid >> 3;
   int local = j;
   piece = 0, pieces = 1;

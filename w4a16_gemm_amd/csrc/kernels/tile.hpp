@@ -20,23 +20,26 @@
 
 namespace w4a16 {
 
-template <int BITS>
+// BM: rows that a stage has room for.  256: one workgroup per compute unit; 128: two.
+template <int BITS, int BM>
 struct TileStage {
-  static constexpr uint32_t A = 256 * 128;
+  static constexpr uint32_t A = BM * 128;
   static constexpr uint32_t C = 256 * 8 * BITS;
   static constexpr uint32_t S = 2 * 256 * 2;                // [half][output]
   static constexpr uint32_t Z = BITS == 4 ? 256 : 1024;     // the same; whole wavefronts' loads
   static constexpr uint32_t BYTES = A + C + S + Z;
+  static constexpr int COUNT = BITS == 8 && BM == 128 ? 2 : 3;   // as many as fit
 };
 
-constexpr size_t kTileRowsLds = 4 * 256 * 4;   // four words per row of the tile, behind the ring
+// Behind the ring: four words per row of the tile.
+template <int BITS, int BM>
+constexpr size_t tile_lds() { return TileStage<BITS, BM>::COUNT * static_cast<size_t>(TileStage<BITS, BM>::BYTES) + 16 * BM; }
+static_assert(tile_lds<4, 256>() <= 160 * 1024 && tile_lds<8, 256>() <= 160 * 1024, "fits a compute unit");
+static_assert(tile_lds<4, 128>() <= 80 * 1024 && tile_lds<8, 128>() <= 80 * 1024, "two workgroups per compute unit");
 
-template <int BITS>
-constexpr size_t tile_lds() { return 3 * static_cast<size_t>(TileStage<BITS>::BYTES) + kTileRowsLds; }
-
-template <int NB, int MB, int BITS>
+template <int NB, int MB, int BITS, int BM>
 struct TileLoader {
-  using L = TileStage<BITS>;
+  using L = TileStage<BITS, BM>;
   static constexpr int APT = MB / 2;     // row loads (16 B) per thread and stage
   static constexpr int CL = BITS / 4;    // code loads
   static constexpr int BN = 64 * NB, PARTS = BITS / 2, KBYTES = 8 * BITS;
@@ -76,10 +79,10 @@ struct TileLoader {
     z_pitch = l.zeros.sym ? 0 : N / (32 / BITS);
   }
 
-  // Tile t to stage t % 3; past the end the last one again.  Scales and zero points come
+  // Tile t to stage t % COUNT; past the end the last one again.  Scales and zero points come
   // first: waiting for tile t waits for no more than those of tile t + 1.
   __device__ __forceinline__ void load(int t) const {
-    const uint32_t stage = ring + (t % 3) * L::BYTES;
+    const uint32_t stage = ring + (t % L::COUNT) * L::BYTES;
     const int tc = min(t, KT - 1);
     const int g = (tc * 64 + 32 * half) >> gshift;
     const uint32_t scales = stage + L::A + L::C;
@@ -95,9 +98,9 @@ struct TileLoader {
 };
 
 // Constants of output `col` of the tile for the 32 channels `half` of a stage.
-template <int BITS>
+template <int BITS, int BM>
 __device__ __forceinline__ DequantConsts tile_consts(const unsigned char* scales, Zeros zeros, int half, int col) {
-  using L = TileStage<BITS>;
+  using L = TileStage<BITS, BM>;
   const uint32_t sc = *reinterpret_cast<const uint16_t*>(scales + (half * 256 + col) * 2);
   uint32_t z;
   if constexpr (BITS == 4)
@@ -109,11 +112,12 @@ __device__ __forceinline__ DequantConsts tile_consts(const unsigned char* scales
 
 // acc[mb][nb]: 16 x 16 blocks of the wavefront's 16 MB rows and 16 NB outputs.  Lane (r, q) has
 // the channels [16 q + 8 s, +8) in MFMA step s.
-template <int NB, int MB, int BITS>
-__device__ __forceinline__ void tile_product(const TileLoader<NB, MB, BITS>& ld, Zeros zeros, const unsigned char* smem,
+template <int NB, int MB, int BITS, int BM>
+__device__ __forceinline__ void tile_product(const TileLoader<NB, MB, BITS, BM>& ld, Zeros zeros, const unsigned char* smem,
                                              int tid, int wave, float4_t (&acc)[MB][NB]) {
-  using L = TileStage<BITS>;
-  constexpr int INFLIGHT = TileLoader<NB, MB, BITS>::APT + TileLoader<NB, MB, BITS>::CL;
+  using L = TileStage<BITS, BM>;
+  using Loader = TileLoader<NB, MB, BITS, BM>;
+  constexpr int INFLIGHT = (L::COUNT - 2) * (Loader::APT + Loader::CL);   // of the tiles after the next
   const int lane = tid & 63, wm = wave >> 2, wn = wave & 3, lr = lane & 15, lq = lane >> 4;
 #pragma unroll
   for (int mb = 0; mb < MB; ++mb)
@@ -121,15 +125,15 @@ __device__ __forceinline__ void tile_product(const TileLoader<NB, MB, BITS>& ld,
     for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = float4_t{0.f, 0.f, 0.f, 0.f};
   const int col = wn * 16 * NB + lr;
   const uint32_t a_lane = (wm * 16 * MB + lr) * 128;
-  ld.load(0);
-  ld.load(1);
+#pragma unroll
+  for (int t = 0; t < L::COUNT - 1; ++t) ld.load(t);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(INFLIGHT) : "memory");   // tile 0
   block_barrier();
   DequantConsts dc[NB];
   const int gmask = (1 << min(ld.gshift, 30)) - 1;
   for (int t = 0; t < ld.KT; ++t) {
-    ld.load(t + 2);
-    const unsigned char* st = smem + (t % 3) * L::BYTES;
+    ld.load(t + L::COUNT - 1);
+    const unsigned char* st = smem + (t % L::COUNT) * L::BYTES;
     uint32_t cw[NB][BITS / 2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
@@ -145,7 +149,7 @@ __device__ __forceinline__ void tile_product(const TileLoader<NB, MB, BITS>& ld,
     // constants are rebuilt only where the tile starts a new group
     if (((t * 64) & gmask) == 0) {
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) dc[nb] = tile_consts<BITS>(st + L::A + L::C, zeros, lq >> 1, col + 16 * nb);
+      for (int nb = 0; nb < NB; ++nb) dc[nb] = tile_consts<BITS, BM>(st + L::A + L::C, zeros, lq >> 1, col + 16 * nb);
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
@@ -178,11 +182,12 @@ __device__ __forceinline__ void tile_product(const TileLoader<NB, MB, BITS>& ld,
 
 // acc[rb][cb]: 32 x 32 blocks.  Lane (h, c) = (lane / 32, lane % 32) has the channels
 // [32 h + 8 s, +8) in MFMA step s.
-template <int NB, int MB, int BITS>
-__device__ __forceinline__ void tile_product32(const TileLoader<NB, MB, BITS>& ld, Zeros zeros, const unsigned char* smem,
+template <int NB, int MB, int BITS, int BM>
+__device__ __forceinline__ void tile_product32(const TileLoader<NB, MB, BITS, BM>& ld, Zeros zeros, const unsigned char* smem,
                                                int tid, int wave, f32x16_t (&acc)[MB / 2][NB / 2]) {
-  using L = TileStage<BITS>;
-  constexpr int INFLIGHT = TileLoader<NB, MB, BITS>::APT + TileLoader<NB, MB, BITS>::CL;
+  using L = TileStage<BITS, BM>;
+  using Loader = TileLoader<NB, MB, BITS, BM>;
+  constexpr int INFLIGHT = (L::COUNT - 2) * (Loader::APT + Loader::CL);   // of the tiles after the next
   constexpr int RB = MB / 2, CB = NB / 2;
   const int lane = tid & 63, wm = wave >> 2, wn = wave & 3, lc = lane & 31, lh = lane >> 5;
 #pragma unroll
@@ -193,15 +198,15 @@ __device__ __forceinline__ void tile_product32(const TileLoader<NB, MB, BITS>& l
       for (int r = 0; r < 16; ++r) acc[rb][cb][r] = 0.f;
   const int col = wn * 16 * NB + lc;
   const uint32_t a_lane = (wm * 16 * MB + lc) * 128;
-  ld.load(0);
-  ld.load(1);
+#pragma unroll
+  for (int t = 0; t < L::COUNT - 1; ++t) ld.load(t);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(INFLIGHT) : "memory");   // tile 0
   block_barrier();
   DequantConsts dc[CB];
   const int gmask = (1 << min(ld.gshift, 30)) - 1;
   for (int t = 0; t < ld.KT; ++t) {
-    ld.load(t + 2);
-    const unsigned char* st = smem + (t % 3) * L::BYTES;
+    ld.load(t + L::COUNT - 1);
+    const unsigned char* st = smem + (t % L::COUNT) * L::BYTES;
     uint4 cw[CB][BITS / 4];
 #pragma unroll
     for (int cb = 0; cb < CB; ++cb) {
@@ -216,7 +221,7 @@ __device__ __forceinline__ void tile_product32(const TileLoader<NB, MB, BITS>& l
     }
     if (((t * 64) & gmask) == 0) {
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) dc[cb] = tile_consts<BITS>(st + L::A + L::C, zeros, lh, col + 32 * cb);
+      for (int cb = 0; cb < CB; ++cb) dc[cb] = tile_consts<BITS, BM>(st + L::A + L::C, zeros, lh, col + 32 * cb);
     }
     // fragments one step ahead: the reads of step s + 1 are in flight during the MFMAs of s
     half8_t af[2][RB];

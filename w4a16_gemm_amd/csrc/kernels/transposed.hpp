@@ -27,26 +27,30 @@
 
 namespace w4a16 {
 
-template <int BITS>
+template <int BITS, int BM>
 struct TStage {
   static constexpr uint32_t ROW = 256 * BITS / 8;                 // code bytes of a row
   static constexpr uint32_t CHUNK = 8 * ROW + (BITS == 4 ? 32 : 64);
-  static constexpr uint32_t A = 256 * 64 * 2;
+  static constexpr uint32_t A = BM * 64 * 2;
   static constexpr uint32_t C = 8 * CHUNK;
   static constexpr uint32_t S = 8 * 64 * 2;                       // [column / 32][output]
   static constexpr uint32_t Z = BITS == 4 ? 256 : 1024;           // [column / 32][output], 64 lanes' loads
   static constexpr uint32_t BYTES = A + C + S + Z;
+  static constexpr int COUNT = BITS == 8 && BM == 128 ? 2 : 3;    // as in TileStage
   static_assert(BYTES % 16 == 0, "stage alignment");
 };
 
-template <int BITS>
-constexpr size_t transposed_lds() { return 3 * static_cast<size_t>(TStage<BITS>::BYTES) + kTileRowsLds; }
+// Behind the ring: a word per row of the tile.
+template <int BITS, int BM>
+constexpr size_t transposed_lds() { return TStage<BITS, BM>::COUNT * static_cast<size_t>(TStage<BITS, BM>::BYTES) + 4 * BM; }
+static_assert(transposed_lds<4, 256>() <= 160 * 1024 && transposed_lds<8, 256>() <= 160 * 1024, "fits a compute unit");
+static_assert(transposed_lds<4, 128>() <= 80 * 1024 && transposed_lds<8, 128>() <= 80 * 1024, "two workgroups per compute unit");
 
 // Loads of one tile: rows source[0 .. rows) of a [a_rows][a_pitch] from column a0 on against
 // the outputs [n_begin, n_end) and the channels from k0 on.
-template <int MB, int BITS>
+template <int MB, int BITS, int BM>
 struct TLoader {
-  using L = TStage<BITS>;
+  using L = TStage<BITS, BM>;
   static constexpr int APT = 32 * MB / 64;   // activation chunks (16 B) per thread and stage
   static constexpr int CL = BITS / 4;        // code loads per thread and stage
 
@@ -102,10 +106,10 @@ struct TLoader {
     z_tail = l.zeros.sym ? 0 : (min(zp, last / ZP * ZP) - zp) / (32 / BITS);
   }
 
-  // Tile t to stage t % 3; tiles past the end re-load the last one.  The scale and zero-point
+  // Tile t to stage t % COUNT; tiles past the end re-load the last one.  The scale and zero-point
   // loads come first: waiting for tile t never waits for more than those of tile t + 1.
   __device__ __forceinline__ void load(int t) const {
-    const uint32_t stage = ring + (t % 3) * L::BYTES;
+    const uint32_t stage = ring + (t % L::COUNT) * L::BYTES;
     const int tc = min(t, KT - 1);
     const bool tail = tc == KT - 1;
     const uint32_t scales = stage + L::A + L::C;
@@ -134,11 +138,12 @@ __device__ __forceinline__ uint32_t perm_bytes(uint32_t hi, uint32_t lo, uint32_
 }
 
 // acc[mb][i]: rows 16 mb + 4 q + reg of the wavefront's 16 MB, block i of its channels.
-template <int MB, int BITS>
-__device__ __forceinline__ void transposed_product(const TLoader<MB, BITS>& ld, Zeros zeros, unsigned char* smem,
+template <int MB, int BITS, int BM>
+__device__ __forceinline__ void transposed_product(const TLoader<MB, BITS, BM>& ld, Zeros zeros, unsigned char* smem,
                                                    int outputs, int tid, int wave, float4_t (&acc)[MB][4]) {
-  using L = TStage<BITS>;
-  constexpr int INFLIGHT = TLoader<MB, BITS>::APT + TLoader<MB, BITS>::CL;
+  using L = TStage<BITS, BM>;
+  using Loader = TLoader<MB, BITS, BM>;
+  constexpr int INFLIGHT = (L::COUNT - 2) * (Loader::APT + Loader::CL);
   const int lane = tid & 63;
   const int wm = wave >> 2, wn = wave & 3;
   const int lr = lane & 15, lq = lane >> 4;
@@ -155,14 +160,14 @@ __device__ __forceinline__ void transposed_product(const TLoader<MB, BITS>& ld, 
   const uint32_t half_sel = lr & 8 ? 0x07060302u : 0x05040100u;   // high or low halves of two words
   const int last = outputs - (ld.KT - 1) * 64;                    // outputs of the last tile
 
-  ld.load(0);
-  ld.load(1);
+#pragma unroll
+  for (int t = 0; t < L::COUNT - 1; ++t) ld.load(t);
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(INFLIGHT) : "memory");
   block_barrier();
 
   for (int t = 0; t < ld.KT; ++t) {
-    ld.load(t + 2);
-    const unsigned char* st = smem + (t % 3) * L::BYTES;
+    ld.load(t + L::COUNT - 1);
+    const unsigned char* st = smem + (t % L::COUNT) * L::BYTES;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       uint32_t w[8];
@@ -267,7 +272,7 @@ __device__ __forceinline__ void each_run(const float4_t (&acc)[MB][4], int tid, 
   }
 }
 
-template <int MB, int BITS>
+template <int MB, int BITS, int BM>
 __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int a_pitch, int a0, const Layers& l,
                                                 int n_begin, int n_end, int n_valid, int k0, const int32_t* source,
                                                 const RowTile& tile, const TOut& to, int piece, int pieces,
@@ -277,8 +282,8 @@ __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int
   const int rows = tile.rows;
   float4_t acc[MB][4];
   if (n_begin < n_end) {
-    const TLoader<MB, BITS> ld(a, a_rows, a_pitch, a0, l, n_begin, n_end, k0, source, rows, smem, tid, wave);
-    transposed_product<MB, BITS>(ld, l.zeros, smem, min(n_end, n_valid) - n_begin, tid, wave, acc);
+    const TLoader<MB, BITS, BM> ld(a, a_rows, a_pitch, a0, l, n_begin, n_end, k0, source, rows, smem, tid, wave);
+    transposed_product(ld, l.zeros, smem, min(n_end, n_valid) - n_begin, tid, wave, acc);
   } else {   // a part without outputs: nothing to add
     if (to.add) return;
 #pragma unroll
@@ -315,8 +320,8 @@ __device__ __forceinline__ void transposed_tile(const half_t* a, int a_rows, int
 // n_valid > n_end - 16 on, whose columns of a are 0, count as 0 whatever their scales.  A tile
 // in parts takes ceil(n_most / parts) outputs each, n_most >= n_end - n_begin (the same for
 // every launch that adds to the same sums).  Sums go to the places or slots alike.
-template <int BITS>
-__global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restrict__ a, int a_rows, int a_pitch,
+template <int BITS, int BM>
+__global__ __launch_bounds__(512, BM == 256 ? 2 : 4) void transposed_kernel(const half_t* __restrict__ a, int a_rows, int a_pitch,
                                                          int by_place, Layers layers, SlotPlan plan, int slots, int n_begin,
                                                          int n_end, int n_valid, int n_most, int most, TOut to) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -330,20 +335,20 @@ __global__ __launch_bounds__(512) void transposed_kernel(const half_t* __restric
     });
   RowTile tile;
   int col, piece, pieces;
-  if (!find_piece(plan, (K + 255) / 256, most, blockIdx.x, tile, col, piece, pieces)) return;
+  if (!find_piece(plan, (K + 255) / 256, most, tile_slots(BM), n_most, blockIdx.x, tile, col, piece, pieces)) return;
   const int k0 = col * 256;
-  int32_t* rows = reinterpret_cast<int32_t*>(smem + transposed_lds<BITS>() - kTileRowsLds);
+  int32_t* rows = reinterpret_cast<int32_t*>(smem + transposed_lds<BITS, BM>() - 4 * BM);
   if (tid < tile.rows) rows[tid] = by_place ? tile.first + tid : plan.order[tile.first + tid];
   __syncthreads();
   const Layers l = layers.at<BITS>(tile.expert);
   const int len = (n_most + 64 * pieces - 1) / (64 * pieces) * 64;
   const int a0 = piece * len, n0 = n_begin + a0, n1 = min(n_end, n0 + len);
-  if (tile.height == 256)
-    transposed_tile<8, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
+  if (BM == 256 && tile.height == 256)
+    transposed_tile<BM == 256 ? 8 : 4, BITS, BM>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
   else if (tile.height == 128)
-    transposed_tile<4, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
+    transposed_tile<4, BITS, BM>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
   else
-    transposed_tile<2, BITS>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
+    transposed_tile<2, BITS, BM>(a, a_rows, a_pitch, a0, l, n0, n1, n_valid, k0, rows, tile, to, piece, pieces, smem);
 }
 
 // Partial sums part[piece][slot][K] of the slots [m T, (m + 1) T) -> dx[m], in a fixed
@@ -384,12 +389,12 @@ __device__ __forceinline__ void store_sums(const float (&s)[8], half_t* out) {
 }
 
 // direct: tiles that are not in parts have been written already.
-__global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict__ part, size_t slots, int most, int T,
+__global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict__ part, size_t slots, int most, int side, int outputs, int T,
                                                         const int32_t* __restrict__ index, int E, SlotPlan plan, int K,
                                                         int direct, const half_t* __restrict__ dx0, half_t* __restrict__ out) {
   const size_t m = blockIdx.x;
   const int cols = (K + 255) / 256;
-  const SlotSums sums{part, slots, plan, Pieces(plan.counts[0] * cols, most), K, cols, E};
+  const SlotSums sums{part, slots, plan, Pieces(plan.counts[0] * cols, most, side, outputs), K, cols, E};
   for (int k = 8 * threadIdx.x; k < K; k += 8 * 256) {
     float s[8];
     start_sums(dx0 ? dx0 + m * K + k : nullptr, s);
@@ -412,7 +417,7 @@ __global__ __launch_bounds__(256) void sum_slots_kernel(const float* __restrict_
 // 74 us, 20 us).
 constexpr int kSumChannels = 8192;
 
-__global__ __launch_bounds__(512) void sum_ordered_kernel(const float* __restrict__ part, size_t slots, int most, int T,
+__global__ __launch_bounds__(512) void sum_ordered_kernel(const float* __restrict__ part, size_t slots, int most, int side, int outputs, int T,
                                                           const int32_t* __restrict__ index, int E, SlotPlan plan,
                                                           const int32_t* __restrict__ inverse, int K,
                                                           const half_t* __restrict__ dx0, half_t* __restrict__ out) {
@@ -420,7 +425,7 @@ __global__ __launch_bounds__(512) void sum_ordered_kernel(const float* __restric
   __shared__ __align__(16) float turn[kSumChannels];
   const size_t m = blockIdx.x;
   const int cols = (K + 255) / 256, k0 = 8 * threadIdx.x;
-  const SlotSums sums{part, slots, plan, Pieces(plan.counts[0] * cols, most), K, cols, E};
+  const SlotSums sums{part, slots, plan, Pieces(plan.counts[0] * cols, most, side, outputs), K, cols, E};
   for (int base = 0; base < K; base += kSumChannels) {
     float s[RUNS][8];
 #pragma unroll
