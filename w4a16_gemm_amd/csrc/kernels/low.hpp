@@ -2,7 +2,7 @@
 // product (64 rows are 256 operations per byte of 4-bit codes, below what the matrix cores
 // and the memory balance at).
 //  * The 8 wavefronts share the rows and split the outputs, 32 each, so that every weight is
-//    expanded once (in the tile of gemm.hpp two wavefronts expand the same columns), on
+//    expanded once (in tile.hpp two wavefronts expand the same columns), on
 //    32x32x16 MFMAs: lane (h, c) = (lane / 32, lane % 32) has the 8 channels 64 v + 32 h +
 //    8 s of output c in step s of the v-th 64 channels of a stage.
 //  * K advances through an LDS ring in stages of 64 bytes of codes per output (128 channels

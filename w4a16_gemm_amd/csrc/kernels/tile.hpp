@@ -1,7 +1,8 @@
 // The forward tile of the grouped products: BM = 32 MB rows by BN = 64 NB outputs of
 // y = x W^^T, by 8 wavefronts (2 along the rows x 4 along the outputs).
 //
-// K advances in tiles of 64 channels through a 3-stage LDS ring filled two tiles ahead by
+// K advances in tiles of 64 channels through an LDS ring of three stages (two at 8 bits where
+// two workgroups share a compute unit), filled as far ahead as that allows by
 // loads straight into LDS (direct.hpp); each wavefront expands the codes of its outputs in
 // registers right before its MFMAs, 16x16x32 ones where its blocks are 16 MB rows of 128 or an
 // odd number of 16-output blocks, else 32x32x16 ones (twice the work per issue).

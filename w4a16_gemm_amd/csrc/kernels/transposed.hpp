@@ -2,8 +2,8 @@
 // straight from the packed codes, which lie along k while the contraction runs along n.
 //
 // A workgroup of 8 wavefronts (2 along the rows x 4 along k) takes a tile of BM = 32 MB
-// rows by 256 channels k, the contraction in tiles of 64 outputs n through a 3-stage LDS
-// ring filled by direct-to-LDS loads two tiles ahead, as in the forward tile:
+// rows by 256 channels k, the contraction in tiles of 64 outputs n through an LDS
+// ring filled by direct-to-LDS loads ahead of its use, as in the forward tile:
 //  * dy: BM rows of 8 chunks of 8 outputs, chunk j of row r at slot j ^ (r / 2 % 8);
 //  * codes: 64 rows n of 256 channels, as they lie in memory, in 8 chunks of 8 rows; a
 //    chunk is followed by 32 bytes (64 at 8 bits) of padding, so that the four chunks that
