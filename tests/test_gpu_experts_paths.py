@@ -482,3 +482,98 @@ def test_loss_of_few_rows_against_wide_heads(M, N, vocab, K, act, none):
     within("lse", got[1], lse, tol[1])
     again = w4.w4a16_head_loss(dev(x), *layer.args, dev(target), vocab=vocab)
     assert same(got[0], again[0]) and same(got[1], again[1])
+
+
+# --- every kind of tile: full and small ones, alone and two to a compute unit -------------------
+
+LARGE = [
+    # M, T, E, N, K, bits, group, sym, act, index
+    (1138, 1, 20, 4672, 128, 4, 64, False, False, "distinct"),
+    (1138, 1, 20, 4672, 128, 8, 64, False, False, "mixed"),
+    (500, 2, 3, 16400, 64, 4, 32, False, False, "skewed"),
+    (500, 2, 3, 16400, 64, 8, 64, True, False, "distinct"),
+    (937, 1, 12, 2896, 192, 4, 64, False, True, "padded"),
+    (937, 1, 12, 2896, 192, 8, 64, False, False, "distinct"),
+    (2010, 2, 40, 528, 128, 4, 128, False, False, "mixed"),
+    (2010, 2, 40, 528, 128, 8, 128, False, False, "padded"),
+    (300, 1, 1, 5008, 320, 8, 64, False, False, "one"),
+    # few rows: long walks, many slots
+    (100, 2, 16, 520, 4096, 4, 128, False, False, "distinct"),
+    (100, 2, 16, 528, 4224, 8, 64, False, False, "mixed"),
+    (9, 3, 8, 528, 4096, 8, 128, False, True, "distinct"),
+]
+BACK = [
+    (66, 1, 40, 528, 2048, 4, 64, False, False, "distinct"),
+    (66, 1, 40, 528, 2048, 8, 64, False, False, "mixed"),
+    (502, 2, 20, 528, 4096, 4, 64, False, False, "mixed"),
+    (502, 2, 20, 528, 4096, 8, 64, True, False, "padded"),
+    (1004, 1, 8, 272, 4096, 4, 128, False, True, "distinct"),
+    (1000, 2, 8, 272, 4096, 8, 128, False, False, "skewed"),
+    (1600, 1, 8, 144, 4096, 4, 128, False, False, "distinct"),
+    (2000, 2, 3, 144, 4096, 8, 128, False, True, "distinct"),
+    (3000, 1, 2, 1552, 448, 4, 64, False, False, "distinct"),
+    (700, 1, 2, 4112, 448, 8, 64, False, False, "skewed"),
+]
+
+
+def _some(rng, M, n=150):
+    return np.sort(rng.choice(M, min(M, n), replace=False))
+
+
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_products_in_every_tile(shape):
+    M, T, E, N, K, bits, group, sym, act, how = shape
+    note(f"tiles {shape}")
+    rng = np.random.default_rng([113, M, N, K, bits])
+    layers = Layers(E, N, K, bits, group, sym, act)
+    x, index = f16(rng, (M, K)), make_index(rng, M, T, E, how)
+    y = layers.fn("experts_gemm")(dev(x), *layers.args, dev(index))
+    rows = _some(rng, M)
+    ref = oracle.experts_gemm(x[rows], layers.W, index[rows])
+    within("y", y[dev(rows)], ref, gemm_tol(x[rows], layers.W, index[rows], ref))
+    assert not y[dev(index < 0)].any()
+    # the same rows in other tiles
+    order = rng.permutation(M)
+    again = layers.fn("experts_gemm")(dev(x[order]), *layers.args, dev(index[order]))
+    within("again", again[dev(np.argsort(order)[rows])], ref, gemm_tol(x[rows], layers.W, index[rows], ref))
+
+
+@pytest.mark.parametrize("shape", BACK, ids=str)
+@pytest.mark.parametrize("add", [False, True], ids=["alone", "added"])
+def test_products_back_in_every_tile(shape, add):
+    M, T, E, N, K, bits, group, sym, act, how = shape
+    note(f"tiles back {shape} added={add}")
+    rng = np.random.default_rng([114, M, N, K, bits])
+    layers = Layers(E, N, K, bits, group, sym, act)
+    dy, index = f16(rng, (M, T, N), 0.05), make_index(rng, M, T, E, how)
+    dx0 = f16(rng, (M, K), 0.05) if add else None
+    run = lambda: layers.fn("experts_backward")(dev(dy), *layers.args, dev(index), K, dx=dev(dx0))   # noqa: E731
+    dx = run()
+    rows = _some(rng, M)
+    part = dx0[rows] if add else None
+    ref = oracle.experts_backward(dy[rows], layers.W, index[rows], part)
+    within("dx", dx[dev(rows)], ref, backward_tol(dy[rows], layers.W, index[rows], part, ref))
+    assert same(dx, run())
+
+
+@pytest.mark.parametrize("M,N,vocab,K,act", [(803, 16512, 16500, 64, False), (401, 18896, 18890, 128, False),
+                                             (5493, 528, 520, 64, False), (1200, 8208, 8208, 128, True),
+                                             (3000, 2064, 2050, 64, False)])
+@pytest.mark.parametrize("bits", [4, 8])
+def test_loss_in_every_tile(M, N, vocab, K, act, bits):
+    note(f"loss tiles M={M} N={N} K={K} bits={bits}")
+    rng = np.random.default_rng([115, M, N, bits])
+    layer = Layers(1, N, K, bits, 64, act=act, experts=False)
+    x, target = f16(rng, (M, K), 2.0), rng.integers(0, vocab, M).astype(np.int32)
+    target[rng.random(M) < 0.2] = -100
+    dloss = rng.uniform(0.1, 8, M).astype(np.float32)
+    loss, lse = layer.fn("head_loss")(dev(x), *layer.args, dev(target), vocab=vocab)
+    dx = layer.fn("head_loss_backward")(dev(dloss), dev(x), *layer.args, dev(target), lse, vocab=vocab)
+    rows, W = _some(rng, M, 120), layer.W[0]
+    rl, rs, coeff = oracle.head_loss(x[rows], W, target[rows], vocab)
+    tol = loss_tol(x[rows], W[:vocab], rs)
+    within("loss", loss[dev(rows)], rl, tol[0])
+    within("lse", lse[dev(rows)], rs, tol[1])
+    ref = oracle.head_loss_backward(dloss[rows], x[rows], W, target[rows], vocab)
+    within("dx", dx[dev(rows)], ref, 2 * dx_tol(dloss[rows], x[rows], W[:vocab], target[rows], rs, coeff, ref))
+    assert same(dx, layer.fn("head_loss_backward")(dev(dloss), dev(x), *layer.args, dev(target), lse, vocab=vocab))

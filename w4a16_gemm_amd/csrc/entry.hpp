@@ -110,7 +110,7 @@ constexpr int kUnits = 256;   // compute units
 
 // A tile's place in a kernel: the height of the plan's full tiles; bm, the rows that the kernel's
 // ring has room for (256: a workgroup per compute unit, 128: two, with half the memory each; 64:
-// two of the 64-row kernel); its 64-column blocks, 4 or 1.
+// two of the 64-row kernel); its 64-column blocks, 4 or (bm 256) 1.
 struct TileShape {
   int height, bm, nb;
 };
@@ -129,10 +129,10 @@ struct TileCost {
 TileCost forward_cost(const TileShape& s, int rows) {
   constexpr double one[2][3] = {{0.73, 0.43, 0.33}, {0.33, 0.22, 0.15}};
   constexpr double full256[2][3] = {{1.0, 0.65, 0.47}, {0.40, 0.26, 0.20}};
-  constexpr double full128[2][3] = {{2.0, 1.18, 0.85}, {0.80, 0.41, 0.30}};
+  constexpr double full128[3] = {2.0, 1.18, 0.85};
   if (s.bm == 64) return {0.22, 0.68};
   const int n = s.nb == 1, i = rows == 256 ? 0 : rows == 128 ? 1 : 2;
-  return s.bm == 256 ? TileCost{one[n][i], full256[n][i]} : TileCost{1.2 * one[n][i], full128[n][i]};
+  return s.bm == 256 ? TileCost{one[n][i], full256[n][i]} : TileCost{1.2 * one[0][i], full128[i]};
 }
 
 TileCost transposed_cost(const TileShape& s, int rows) {
@@ -179,10 +179,10 @@ double forward_time(int64_t S, int E, int cols, const TileShape& shape) {
   return m.full * (rounds <= 1 ? 1.0 : E > 1 ? rounds + 0.5 : rounds < 8 ? std::ceil(rounds) : rounds);
 }
 
-// The shape of least time among those with nb blocks or fewer.
+// The shape of least time; narrow: 64-column tiles as well.
 TileShape pick_forward(int64_t S, int E, int cols, bool narrow) {
   constexpr TileShape shapes[] = {{256, 256, 4}, {128, 256, 4}, {128, 128, 4}, {64, 64, 4},
-                                  {256, 256, 1}, {128, 256, 1}, {128, 128, 1}, {64, 256, 1}, {64, 128, 1}};
+                                  {256, 256, 1}, {128, 256, 1}, {64, 256, 1}};
   TileShape best = shapes[0];
   double least = 1e300;
   for (const TileShape& s : shapes) {

@@ -189,7 +189,7 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
     return check_launch("experts launch");
   }
   auto launch = shape.nb == 4 ? (shape.bm == 256 ? launch_forward<4, BITS, 256> : launch_forward<4, BITS, 128>)
-                              : (shape.bm == 256 ? launch_forward<1, BITS, 256> : launch_forward<1, BITS, 128>);
+                              : launch_forward<1, BITS, 256>;
   return launch(grid, st, rows, act ? S : M, act, S, T, l, mem.plan, hy);
 }
 
