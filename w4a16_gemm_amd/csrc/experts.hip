@@ -76,17 +76,19 @@ TileShape pick_shape(int64_t S, int E, int cols) { return pick_forward(S, E, col
 
 // Few rows per expert: the streaming kernel, at most 4096 channels per walk over its
 // wavefronts (16 of them with up to 2 steps of 128 channels; 3 and 4 steps spill registers).
-// Up to 32 rows, which are two of its tiles, on average: eight experts (N and K 4096) of 8 / 16 /
-// 32 / 48 rows 19.2 / 20.8 / 31.5 / 51.1 us, in 64-row tiles 62 us; at 8 bits 31.7 / 32.5 / 45.4
-// / 80.6 us, in tiles 67 us.
+// Up to 16 rows on average, and up to 32, which are two of its tiles and read the codes twice,
+// where the 64-row tiles would leave half of the compute units idle.  Against those tiles (K
+// 4096): 16 experts, N 4096, of 16 / 24 rows 34 / 54 us, in tiles 43 / 44 us; 8 of 16 / 24 / 32 rows 22 /
+// 31 / 33 us, in tiles 39 / 40 / 40 us; 8, N 14336, 53 / 84 / 91 us, in tiles 63 / 64 / 64 us.
 struct FewShape {
   bool ok;
   int waves, steps, chunks;
 };
 
-FewShape pick_few(int64_t S, int E, int K) {
+FewShape pick_few(int64_t S, int E, int N, int K) {
   FewShape f{};
-  f.ok = S <= kFewSlots && S <= 32 * std::min<int64_t>(E, S);
+  const int64_t used = std::min<int64_t>(E, S);
+  f.ok = S <= kFewSlots && (S <= 16 * used || (S <= 32 * used && used * ceil_div(N, 256) <= kUnits / 2));
   const int total = static_cast<int>(ceil_div(K, 128));
   f.chunks = static_cast<int>(ceil_div(total, 32));
   const int walk = static_cast<int>(ceil_div(total, f.chunks));
@@ -100,9 +102,9 @@ struct ForwardMemory {
   half_t* gathered;
 };
 
-ForwardMemory forward_memory(Carver& ws, int64_t S, int E, int K, bool act, int height) {
+ForwardMemory forward_memory(Carver& ws, int64_t S, int E, int N, int K, bool act, int height) {
   ForwardMemory m{};
-  if (!pick_few(S, E, K).ok) m.plan = take_plan(ws, S, most_tiles(S, E, height), false);
+  if (!pick_few(S, E, N, K).ok) m.plan = take_plan(ws, S, most_tiles(S, E, height), false);
   m.gathered = act ? ws.take<half_t>(static_cast<size_t>(S) * K) : nullptr;
   return m;
 }
@@ -162,14 +164,14 @@ int experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t* scal
   const int S = M * T;
   const TileShape shape = pick_shape(S, E, N);
   Carver ws{static_cast<unsigned char*>(workspace)};
-  const ForwardMemory mem = forward_memory(ws, S, E, K, act, shape.height);
+  const ForwardMemory mem = forward_memory(ws, S, E, N, K, act, shape.height);
   if (!workspace && ws.used > 0) return fail(W4A16_ERR_INVALID_ARG, "NULL buffer workspace");
   if (workspace_bytes < ws.used)
     return fail(W4A16_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace_bytes, ws.used);
   hipStream_t st = static_cast<hipStream_t>(stream);
   const Layers l = make_layers(qweight, scales, qzeros, group_size, N, K, BITS, act);
   const half_t* hx = reinterpret_cast<const half_t*>(x);
-  const FewShape few = pick_few(S, E, K);
+  const FewShape few = pick_few(S, E, N, K);
   if (few.ok) {
     if (act) hipLaunchKernelGGL(gather_rows_kernel, dim3(S), dim3(256), 0, st, hx, index, E, l, T, mem.gathered);
     auto launch = S <= 64 ? launch_few<BITS, true> : launch_few<BITS, false>;
@@ -356,7 +358,7 @@ size_t w4a16_experts_gemm_workspace(int M, int T, int E, int N, int K, int act_o
   if (!ok) return 0;
   Carver ws{nullptr};
   const int64_t S = static_cast<int64_t>(M) * T;
-  forward_memory(ws, S, E, K, act_order != 0, pick_shape(S, E, N).height);
+  forward_memory(ws, S, E, N, K, act_order != 0, pick_shape(S, E, N).height);
   return ws.used;
 }
 
