@@ -577,3 +577,26 @@ def test_loss_in_every_tile(M, N, vocab, K, act, bits):
     ref = oracle.head_loss_backward(dloss[rows], x[rows], W, target[rows], vocab)
     within("dx", dx[dev(rows)], ref, 2 * dx_tol(dloss[rows], x[rows], W[:vocab], target[rows], rs, coeff, ref))
     assert same(dx, layer.fn("head_loss_backward")(dev(dloss), dev(x), *layer.args, dev(target), lse, vocab=vocab))
+
+
+@pytest.mark.parametrize("E", [3, 200])
+def test_many_slots(E):
+    """More than 2^20 slots, rows and their routing."""
+    note(f"many slots E={E}")
+    rng = np.random.default_rng([116, E])
+    M, T, N, K = 400000, 3, 64, 64
+    layers = Layers(E, N, K, 4, 64, sym=True)
+    logits = rng.standard_normal((M, E), dtype=np.float32)
+    index, weights = w4.w4a16_route(dev(logits), T)
+    rows = np.r_[0:20, M // 2:M // 2 + 20, M - 20:M]
+    ri, rw, _ = oracle.route(logits[rows], T)
+    assert np.array_equal(index[dev(rows)].cpu().numpy(), ri)
+    within("weights", weights[dev(rows)], rw, weight_tol(logits[rows], rw))
+    x = f16(rng, (M, K))
+    y = w4.w4a16_experts_gemm(dev(x), *layers.args, index)
+    ref = oracle.experts_gemm(x[rows], layers.W, ri)
+    within("y", y[dev(rows)], ref, gemm_tol(x[rows], layers.W, ri, ref))
+    dx = w4.w4a16_experts_backward(y, *layers.args, index, K)
+    dy = y[dev(rows)].cpu().numpy()
+    ref = oracle.experts_backward(dy, layers.W, ri)
+    within("dx", dx[dev(rows)], ref, backward_tol(dy, layers.W, ri, None, ref))
