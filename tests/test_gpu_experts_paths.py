@@ -600,3 +600,21 @@ def test_many_slots(E):
     dy = y[dev(rows)].cpu().numpy()
     ref = oracle.experts_backward(dy, layers.W, ri)
     within("dx", dx[dev(rows)], ref, backward_tol(dy, layers.W, ri, None, ref))
+
+
+@pytest.mark.parametrize("E,how", [(5, "mixed"), (512, "padded"), (1, "one"), (7, "skewed"), (4, "none")])
+def test_ragged_groups_of_many_slots(E, how):
+    """Slots that several workgroups sort."""
+    note(f"many ragged slots E={E} {how}")
+    rng = np.random.default_rng([117, E])
+    M, T, N, K = (30011, 1 if E == 1 else 3, 64, 64)
+    layers = Layers(E, N, K, 4, 64)
+    index = make_index(rng, M, T, E, how)
+    x, dx0 = f16(rng, (M, K)), f16(rng, (M, K), 0.05)
+    y = w4.w4a16_experts_gemm(dev(x), *layers.args, dev(index))
+    ref = oracle.experts_gemm(x, layers.W, index)
+    within("y", y, ref, gemm_tol(x, layers.W, index, ref))
+    dy = f16(rng, (M, T, N), 0.05)
+    dx = w4.w4a16_experts_backward(dev(dy), *layers.args, dev(index), K, dx=dev(dx0))
+    ref = oracle.experts_backward(dy, layers.W, index, dx0)
+    within("dx", dx, ref, backward_tol(dy, layers.W, index, dx0, ref))

@@ -95,8 +95,10 @@ Layers make_layers(const int32_t* qweight, const uint16_t* scales, const int32_t
 // Row tiles that S slots of E experts can need.
 int64_t most_tiles(int64_t S, int E, int height) { return S / height + (E < S ? E : S); }
 
-SlotPlan take_plan(Carver& ws, int64_t S, int64_t tiles, bool tile_of) {
+SlotPlan take_plan(Carver& ws, int64_t S, int E, int64_t tiles, bool tile_of) {
   SlotPlan p;
+  const int blocks = plan_blocks(S);
+  p.sums = blocks > 1 ? ws.take<int32_t>(static_cast<size_t>(blocks + 2) * (E + 1)) : nullptr;
   p.tile_of = tile_of ? ws.take<int32_t>(S) : nullptr;
   p.counts = ws.take<int32_t>(2);
   p.order = ws.take<int32_t>(S);

@@ -17,8 +17,17 @@
 namespace w4a16 {
 
 void run_plan(const SlotPlan& p, const int32_t* index, int S, int E, int limit, int height, hipStream_t st) {
-  hipLaunchKernelGGL(plan_slots_kernel, dim3(1), dim3(kPlanThreads), sizeof(int32_t) * kPlanWaves * (E + 1), st, index, S,
-                     E, limit, height, p);
+  const size_t row = sizeof(int32_t) * (E + 1);
+  const int blocks = plan_blocks(S);
+  if (blocks == 1) {
+    hipLaunchKernelGGL(plan_slots_kernel, dim3(1), dim3(kPlanThreads), kPlanWaves * row, st, index, S, E, limit, height, p);
+    return;
+  }
+  const int per = static_cast<int>((static_cast<int64_t>(S) + blocks - 1) / blocks);
+  hipLaunchKernelGGL(plan_count_kernel, dim3(blocks), dim3(kPlanThreads), row, st, index, S, per, E, limit, p.sums);
+  hipLaunchKernelGGL(plan_scan_kernel, dim3(1), dim3(kPlanThreads), 0, st, blocks, E, height, p, p.sums);
+  hipLaunchKernelGGL(plan_place_kernel, dim3(blocks), dim3(kPlanThreads), kPlanWaves * row, st, index, S, per, E, limit,
+                     height, blocks, p, p.sums);
 }
 
 void run_gather(const SlotPlan& p, const half_t* x, const int32_t* index, const Layers& l, int S, int T, half_t* out,
@@ -104,7 +113,7 @@ struct ForwardMemory {
 
 ForwardMemory forward_memory(Carver& ws, int64_t S, int E, int N, int K, bool act, int height) {
   ForwardMemory m{};
-  if (!pick_few(S, E, N, K).ok) m.plan = take_plan(ws, S, most_tiles(S, E, height), false);
+  if (!pick_few(S, E, N, K).ok) m.plan = take_plan(ws, S, E, most_tiles(S, E, height), false);
   m.gathered = act ? ws.take<half_t>(static_cast<size_t>(S) * K) : nullptr;
   return m;
 }
@@ -210,7 +219,7 @@ bool is_direct(int T, bool act) { return T == 1 && !act; }
 BackwardMemory backward_memory(Carver& ws, int64_t S, int T, int E, int K, bool act, const TransposedShape& shape) {
   BackwardMemory m;
   const bool parts = !is_direct(T, act) || shape.most > 1;
-  m.plan = take_plan(ws, S, most_tiles(S, E, shape.height), parts);
+  m.plan = take_plan(ws, S, E, most_tiles(S, E, shape.height), parts);
   m.part = parts ? ws.take<float>(static_cast<size_t>(shape.most) * S * K) : nullptr;
   m.inverse = act ? ws.take<int32_t>(static_cast<size_t>(E) * K) : nullptr;
   return m;

@@ -41,7 +41,7 @@ struct LossMemory {
 LossMemory loss_memory(Carver& ws, int rows, int N, int K, bool act) {
   const int64_t tiles = ceil_div(N, 256);
   LossMemory m;
-  m.plan = take_plan(ws, rows, most_tiles(rows, 1, pick_rows(rows, tiles).height), false);
+  m.plan = take_plan(ws, rows, 1, most_tiles(rows, 1, pick_rows(rows, tiles).height), false);
   m.part = ws.take<MaxSum>(static_cast<size_t>(tiles) * rows);
   m.label = ws.take<float>(rows);
   m.gathered = act ? ws.take<half_t>(static_cast<size_t>(rows) * K) : nullptr;
@@ -138,8 +138,8 @@ GradMemory grad_memory(Carver& ws, int rows, int N, int K, bool act) {
   const PieceShape p = pick_piece(rows, N, K);
   GradMemory m;
   const int height = p.product.height;
-  m.plan = take_plan(ws, rows, most_tiles(rows, 1, height), true);
-  m.logit_plan = p.logits.height == height ? m.plan : take_plan(ws, rows, most_tiles(rows, 1, p.logits.height), false);
+  m.plan = take_plan(ws, rows, 1, most_tiles(rows, 1, height), true);
+  m.logit_plan = p.logits.height == height ? m.plan : take_plan(ws, rows, 1, most_tiles(rows, 1, p.logits.height), false);
   m.coeff = ws.take<half_t>(static_cast<size_t>(rows) * p.cols);
   m.part = ws.take<float>(static_cast<size_t>(p.product.most) * rows * K);
   m.remainder = ws.take<float>(rows);

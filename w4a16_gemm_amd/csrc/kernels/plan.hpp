@@ -31,7 +31,16 @@ struct SlotPlan {
   int32_t* order;    // [S] slots by expert, those without one last
   RowTile* tiles;
   int32_t* tile_of;  // [S] tile of every slot with an expert, or NULL: not needed
+  int32_t* sums;     // while it is made, see plan_blocks
 };
+
+// Workgroups that make a plan: one for up to kPlanSlots slots, else one for every 2048 slots, at
+// most 256.
+constexpr int kPlanSlots = 16384;
+inline int plan_blocks(int64_t S) {
+  const int64_t blocks = (S + 2047) / 2048;
+  return S <= kPlanSlots ? 1 : blocks < 256 ? static_cast<int>(blocks) : 256;
+}
 
 __host__ __device__ inline int rest_height(int rows, int height) {
   return rows <= 64 ? 64 : rows <= 128 && height > 128 ? 128 : height;
