@@ -10,8 +10,12 @@
 // issues itself are waited for correctly beside them: it counts fewer loads in flight than
 // there are, so its waits are longer than needed, never shorter.
 //
-// The destination is the LDS byte offset in m0 plus 16 (4) bytes per lane; writing m0 takes
-// one wait state before a load that reads it.
+// The destination is the LDS byte offset in m0 plus 16 (4) bytes per lane.  What the compiler
+// keeps between instructions that it sees, each statement keeps by itself: one wait state from
+// a write of m0 to a load that reads it, and five from a vector instruction's write of a
+// scalar register (v_readfirstlane, where the compiler holds a uniform value in a vector one) to
+// a load that reads it; m0 and the condition bit are clobbers.  One statement loads all of a
+// wavefront's rows (codes) of a stage, so the five states pass once for them.
 // Measured against the builtins, whole calls: transposed product of 8192 slots of 8 8-bit
 // experts (14336 outputs of 4096 channels) 1348 -> 1074 us, of 777 act-order rows on 4 bits 361 -> 286 us.
 #pragma once
@@ -31,16 +35,53 @@ __device__ __forceinline__ u32x4_t direct_rsrc(const void* p, uint32_t bytes) {
   return r;
 }
 
-// 16 bytes per lane from byte `lane_off + off` of the buffer; lds and off are the same in
-// every lane.
-__device__ __forceinline__ void direct_load16(u32x4_t rsrc, uint32_t lds, uint32_t lane_off, uint32_t off) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n"
-      "s_nop 0\n"
-      "buffer_load_dwordx4 %1, %2, %3 offen lds"
-      :
-      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(lane_off), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(off))
-      : "memory");
+// The warning that m0 is reserved says that it is not kept for the code around a statement;
+// that code need not.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+
+// COUNT times 16 bytes per lane, from byte `lane_off[i] + off` of the buffer to lds + STEP i;
+// lds and off are the same in every lane.
+template <int COUNT, int STEP>
+__device__ __forceinline__ void direct_loads16(u32x4_t rsrc, uint32_t lds, const uint32_t (&lane_off)[COUNT], uint32_t off) {
+  static_assert(COUNT == 1 || COUNT == 2 || COUNT == 4, "1, 2 or 4 loads");
+  const uint32_t to = __builtin_amdgcn_readfirstlane(lds), from = __builtin_amdgcn_readfirstlane(off);
+  if constexpr (COUNT == 1)
+    asm volatile(
+        "s_mov_b32 m0, %0\n"
+        "s_nop 4\n"
+        "buffer_load_dwordx4 %3, %1, %2 offen lds"
+        :
+        : "s"(to), "s"(rsrc), "s"(from), "v"(lane_off[0])
+        : "memory", "m0");
+  else if constexpr (COUNT == 2)
+    asm volatile(
+        "s_mov_b32 m0, %0\n"
+        "s_nop 4\n"
+        "buffer_load_dwordx4 %4, %1, %2 offen lds\n"
+        "s_add_u32 m0, m0, %3\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %5, %1, %2 offen lds"
+        :
+        : "s"(to), "s"(rsrc), "s"(from), "n"(STEP), "v"(lane_off[0]), "v"(lane_off[1])
+        : "memory", "m0", "scc");
+  else
+    asm volatile(
+        "s_mov_b32 m0, %0\n"
+        "s_nop 4\n"
+        "buffer_load_dwordx4 %4, %1, %2 offen lds\n"
+        "s_add_u32 m0, m0, %3\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %5, %1, %2 offen lds\n"
+        "s_add_u32 m0, m0, %3\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %6, %1, %2 offen lds\n"
+        "s_add_u32 m0, m0, %3\n"
+        "s_nop 0\n"
+        "buffer_load_dwordx4 %7, %1, %2 offen lds"
+        :
+        : "s"(to), "s"(rsrc), "s"(from), "n"(STEP), "v"(lane_off[0]), "v"(lane_off[1]), "v"(lane_off[2]), "v"(lane_off[3])
+        : "memory", "m0", "scc");
 }
 
 // BYTES = 16 or 4 per lane from the lane's own address.
@@ -54,7 +95,7 @@ __device__ __forceinline__ void direct_load(const void* p, uint32_t lds) {
         "global_load_lds_dwordx4 %1, off"
         :
         : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p)
-        : "memory");
+        : "memory", "m0");
   else
     asm volatile(
         "s_mov_b32 m0, %0\n"
@@ -62,7 +103,9 @@ __device__ __forceinline__ void direct_load(const void* p, uint32_t lds) {
         "global_load_lds_dword %1, off"
         :
         : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p)
-        : "memory");
+        : "memory", "m0");
 }
+
+#pragma clang diagnostic pop
 
 }  // namespace w4a16

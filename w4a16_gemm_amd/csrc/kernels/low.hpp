@@ -96,10 +96,8 @@ struct LowLoader {
       direct_load<16>(s_ptr + static_cast<size_t>(g) * s_pitch, scales + wave * 1024);
     else if (wave < 2 * SW)
       direct_load<BITS == 4 ? 4 : 16>(z_ptr + static_cast<size_t>(g) * z_pitch, BITS == 4 ? zeros + (wave - SW) * 256 : zeros);
-#pragma unroll
-    for (int i = 0; i < AL; ++i) direct_load16(xr, stage + (512 * i + wave * 64) * 16, a_off[i], tc * (BK * 2));
-#pragma unroll
-    for (int i = 0; i < 2; ++i) direct_load16(qr, stage + L::A + (512 * i + wave * 64) * 16, b_off[i], tc * 64);
+    direct_loads16<AL, 512 * 16>(xr, stage + wave * 1024, a_off, tc * (BK * 2));
+    direct_loads16<2, 512 * 16>(qr, stage + L::A + wave * 1024, b_off, tc * 64);
   }
 
   // Waits for this wavefront's loads of all but the newest COUNT - 2 stages.

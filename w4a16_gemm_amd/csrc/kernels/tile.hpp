@@ -91,10 +91,8 @@ struct TileLoader {
       direct_load<16>(s_ptr + static_cast<size_t>(g) * s_pitch, scales);
     else if (wave == 1)
       direct_load<BITS == 4 ? 4 : 16>(z_ptr + static_cast<size_t>(g) * z_pitch, scales + L::S);
-#pragma unroll
-    for (int i = 0; i < APT; ++i) direct_load16(xr, stage + (wave * APT + i) * 1024, a_off[i], tc * 128);
-#pragma unroll
-    for (int i = 0; i < CL; ++i) direct_load16(qr, stage + L::A + (512 * i + wave * 64) * 16, b_off[i], tc * KBYTES);
+    direct_loads16<APT, 1024>(xr, stage + wave * APT * 1024, a_off, tc * 128);
+    direct_loads16<CL, 512 * 16>(qr, stage + L::A + wave * 1024, b_off, tc * KBYTES);
   }
 };
 

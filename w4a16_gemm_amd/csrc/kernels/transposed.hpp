@@ -117,12 +117,11 @@ struct TLoader {
       direct_load<16>(s_ptr + static_cast<ptrdiff_t>(tc) * s_step + (tail ? s_tail : 0), scales);
     else if (wave == 1)
       direct_load<BITS == 4 ? 4 : 16>(z_ptr + static_cast<ptrdiff_t>(tc) * z_step + (tail ? z_tail : 0), scales + L::S);
+    direct_loads16<APT, 1024>(ar, stage + wave * APT * 1024, a_off, tc * 128);
+    uint32_t codes[CL];
 #pragma unroll
-    for (int i = 0; i < APT; ++i) direct_load16(ar, stage + (wave * APT + i) * 1024, a_off[i], tc * 128);
-#pragma unroll
-    for (int i = 0; i < CL; ++i)
-      direct_load16(qr, stage + L::A + wave * L::CHUNK + i * 1024, tail ? b_tail[i] : b_off[i],
-                    static_cast<uint32_t>(tc) * b_step);
+    for (int i = 0; i < CL; ++i) codes[i] = tail ? b_tail[i] : b_off[i];
+    direct_loads16<CL, 1024>(qr, stage + L::A + wave * L::CHUNK, codes, static_cast<uint32_t>(tc) * b_step);
   }
 };
 
