@@ -135,6 +135,18 @@ def test_scalar_operands_of_memory_instructions_have_settled(library):
     assert not found, f"{len(found)} of them, the first:\n" + "\n".join(found[:3])
 
 
+def test_16_byte_accesses_of_lds_are_aligned(library):
+    """What an instruction adds to its address keeps the address's own alignment."""
+    found = {}
+    for name, rows in library.items():
+        for op, operands, _, _ in rows:
+            if re.fullmatch(r"ds_(read|write)_b128", op):
+                offset = re.search(r"offset:(\d+)", operands)
+                if offset and int(offset.group(1)) % 16:
+                    found.setdefault(name, f"{op} {operands}")
+    assert not found, found
+
+
 SAMPLE = """
 <kernel>:
 \tv_readfirstlane_b32 s3, v2                                 // 000000000100: 7E060502

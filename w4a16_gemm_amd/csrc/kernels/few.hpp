@@ -25,7 +25,8 @@ namespace w4a16 {
 constexpr int kFewSlots = 512;
 constexpr int kFewBatch = 8;
 
-struct FewLds {
+// The partial tiles lie behind it: whole 16-byte accesses.
+struct alignas(16) FewLds {
   int32_t expert[kFewSlots];
   int32_t count[kMaxExperts];
   int32_t tile0[kMaxExperts + 1];   // first row tile of every expert
