@@ -196,7 +196,8 @@ TileShape pick_forward(int64_t S, int E, int cols, bool narrow) {
 }
 
 // Shape of the tiles and the most parts of a tile of the transposed product (see Pieces): parts
-// of at least 512 outputs, partial sums of at most 512 MB.
+// of at least 512 outputs, partial sums of at most 512 MB.  The times here choose the shape
+// alone; how many parts there are is the kernels' rule.
 struct TransposedShape {
   int height, bm, most;
 };
@@ -215,7 +216,7 @@ TransposedShape pick_transposed(int64_t S, int E, int outputs, int K) {
     double tail = rest == 0 ? 0 : rest <= 32 ? m.one : m.full;
     for (int f = 2; f <= best.most && f * rest <= 2 * side; ++f)
       tail = std::min(tail, (f * rest <= 32 ? m.one : m.full * ceil_div(rest * f, side)) / f +
-                                f * part_cost(static_cast<int>(rest), outputs));
+                                f * (static_cast<float>(kPartCost) * rest / outputs));
     const double cost = static_cast<double>(chunk / side) * m.full + tail;
     if (cost < 0.999 * least) least = cost, best.height = s.height, best.bm = s.bm;
   }

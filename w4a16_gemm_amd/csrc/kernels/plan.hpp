@@ -8,6 +8,7 @@
 #pragma once
 
 #include "nibbles.hpp"
+#include "parts.hpp"
 
 namespace w4a16 {
 
@@ -97,15 +98,9 @@ __device__ __forceinline__ void each_empty(const SlotPlan& plan, int S, F f) {
 // room for.
 __host__ __device__ constexpr int tile_slots(int bm) { return bm == 256 ? 32 : 64; }
 
-// What a part more of `rest` tiles costs, in the time of a tile: their partial sums are written
-// and read.  (512 KB per tile of 256 rows and 8 XCDs' tiles at 5 TB/s, a step of 64 outputs
-// being 2.3 us, are 23 rest / outputs; less than that is measured.)
-__host__ __device__ inline float part_cost(int rest, int outputs) { return 16.f * rest / outputs; }
-
 // Products of too few tiles for whole rounds over the compute units: each XCD (`side` workgroups
 // at once) takes `chunk` tiles, whole rounds of them as they are, the rest each in `pieces` parts
-// of the contraction, as many as make the rest's rounds shortest (two rounds at most).  Where
-// two workgroups share a compute unit, one alone takes 0.6 of their time.
+// of the contraction, as many as make the rest's rounds shortest (parts.hpp).
 // Measured, whole calls: a training batch of 8192 slots over eight 8-bit experts (K 4096, N
 // 14336; about 36 row tiles of 16 columns, 2.25 rounds) 1683 -> 1348 us; 777 rows of two of
 // eight act-order experts of group 32 405 -> 361 us.
@@ -116,14 +111,7 @@ struct Pieces {
     chunk = (total + 7) >> 3;
     const int rest = chunk % side;
     whole = chunk - rest;
-    pieces = 1;
-    const float part = part_cost(rest, outputs);
-    float least = 1e30f;
-    for (int f = 1; f <= most && (f == 1 || f * rest <= 2 * side); ++f) {
-      const float rounds = side == 64 && f * rest <= 32 ? 0.6f : static_cast<float>((rest * f + side - 1) / side);
-      const float cost = rounds / f + part * f;
-      if (cost < least) least = cost, pieces = f;
-    }
+    pieces = parts_of(rest, most, side, outputs);
   }
   // parts of tile id
   __device__ __forceinline__ int of(int id) const { return id % chunk < whole ? 1 : pieces; }
