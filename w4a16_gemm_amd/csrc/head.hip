@@ -12,7 +12,7 @@
 namespace w4a16 {
 namespace {
 
-constexpr int kChunkRows = 32768;                       // rows taken at once: bounds the workspace
+constexpr int kChunkRows = 32768;                       // rows taken at once at most: bounds the workspace
 constexpr int64_t kCoeffElements = int64_t{1} << 27;    // coefficients of one piece: 256 MB
 
 int check_head(int M, int N, int K, int group_size, int vocab, int bits) {
@@ -27,7 +27,12 @@ int check_head(int M, int N, int K, int group_size, int vocab, int bits) {
 // Tiles of M rows against `tiles` column tiles of 256.
 TileShape pick_rows(int M, int64_t tiles) { return pick_forward(M, 1, static_cast<int>(256 * tiles), false); }
 
-int chunk_rows(int M) { return std::min(M, kChunkRows); }
+// Rows taken at once: those whose tiles, 64 rows each at least, against all of N one launch takes
+// (fewer than kChunkRows from about N = 2^21 on).
+int chunk_rows(int M, int N) {
+  const int64_t tiles = kMaxBlocks / ceil_div(N, 256);   // 64 or more
+  return static_cast<int>(std::min<int64_t>({M, kChunkRows, 64 * (tiles - 1)}));
+}
 
 // --- forward ----------------------------------------------------------------------------
 
@@ -76,7 +81,7 @@ int head_loss(const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
                          {lse, 4, true, "lse"},         {workspace, 16, true, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   const bool act = g_idx != nullptr;
-  const int most = chunk_rows(M);
+  const int most = chunk_rows(M, N);
   Carver ws{static_cast<unsigned char*>(workspace)};
   const LossMemory mem = loss_memory(ws, most, N, K, act);
   if (workspace_bytes < ws.used)
@@ -162,7 +167,7 @@ int head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qwe
                          {workspace, 16, true, "workspace"}};
   if (int rc = check_buffers(bufs)) return rc;
   const bool act = g_idx != nullptr;
-  const int most = chunk_rows(M);
+  const int most = chunk_rows(M, N);
   Carver ws{static_cast<unsigned char*>(workspace)};
   const GradMemory mem = grad_memory(ws, most, N, K, act);
   if (workspace_bytes < ws.used)
@@ -210,7 +215,7 @@ size_t w4a16_head_loss_workspace(int M, int N, int K, int act_order) {
   clear_error();
   if (!ok) return 0;
   Carver ws{nullptr};
-  loss_memory(ws, chunk_rows(M), N, K, act_order != 0);
+  loss_memory(ws, chunk_rows(M, N), N, K, act_order != 0);
   return ws.used;
 }
 
@@ -233,7 +238,7 @@ size_t w4a16_head_loss_backward_workspace(int M, int N, int K, int act_order) {
   clear_error();
   if (!ok) return 0;
   Carver ws{nullptr};
-  grad_memory(ws, chunk_rows(M), N, K, act_order != 0);
+  grad_memory(ws, chunk_rows(M, N), N, K, act_order != 0);
   return ws.used;
 }
 
