@@ -183,7 +183,10 @@ __global__ __launch_bounds__(1024) void experts_few_kernel(const half_t* __restr
 #pragma unroll
     for (int q = 0; q < NQ; ++q)
       cw[t][q] = load_buffer16(codes, lr * pitch + k * BITS / 8 + 16u * q + static_cast<uint32_t>(b) * (16 * pitch));
-    sc[t] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(scales, 2 * (g * N + lr) + 32 * b, 0, 0));
+    // past K: the last channels' codes against rows of 0, with the scale 0 that lies behind the buffer,
+    // so that no infinite weight meets such a 0
+    const uint32_t at = channel(c, t) < K ? g * N + lr : static_cast<uint32_t>(N) * l.G;
+    sc[t] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(scales, 2 * at + 32 * b, 0, 0));
     zw[t] = __builtin_amdgcn_raw_buffer_load_b32(zeros, l.zeros.sym ? 0 : 4 * (g * (N / PER) + lr / PER) + 64 / PER * b, 0, 0);
   };
 
