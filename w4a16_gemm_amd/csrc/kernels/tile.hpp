@@ -13,6 +13,12 @@
 //    load, part p of output n at slot p ^ (n / 8 % 2) (p ^ (n / 4 % 4)), so that the lanes
 //    that read a part of 16 outputs at once meet distinct banks.
 // A row's result does not depend on the other rows of the tile, or on its place in it.
+//
+// With half the memory, two workgroups per compute unit, a wavefront has 128 registers: it expands
+// one block's weights, multiplies, and goes on to the next, where a tile alone on a compute unit
+// expands all first.  Expanded at once they spilled 2 to 17 registers, in the head's kernels up to 12 reloads
+// for 64 channels (losses of 803 rows against 16512 outputs, K 4096 165 -> 152 us, 100 against 128000, 8
+// bits, K 1536 96 -> 80 us; 32 experts of 64 rows, N and K 4096 181 -> 179 us).
 #pragma once
 
 #include "direct.hpp"
@@ -156,22 +162,35 @@ __device__ __forceinline__ void tile_product(const TileLoader<NB, MB, BITS, BM>&
 #pragma unroll
       for (int mb = 0; mb < MB; ++mb)
         af[mb] = *reinterpret_cast<const half8_t*>(st + a_lane + 16 * ((2 * lq + s) ^ (lr >> 1)) + 2048 * mb);
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
+      auto expand = [&](int nb) {
         if constexpr (BITS == 4) {
           bf[nb] = dequant_word(cw[nb][s], dc[nb]);
         } else {
           const half4_t lo = dequant_word8(cw[nb][2 * s], dc[nb]), hi = dequant_word8(cw[nb][2 * s + 1], dc[nb]);
           bf[nb] = half8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         }
+      };
+      auto multiply = [&](int mb, int nb) {
+        acc[mb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[mb], bf[nb], acc[mb][nb], 0, 0, 0);
+      };
+      if constexpr (BM == 128) {   // one block's weights at a time
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          expand(nb);
+#pragma unroll
+          for (int mb = 0; mb < MB; ++mb) multiply(mb, nb);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) expand(nb);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) multiply(mb, nb);
+        __builtin_amdgcn_s_setprio(0);
       }
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          acc[mb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(af[mb], bf[nb], acc[mb][nb], 0, 0, 0);
-      __builtin_amdgcn_s_setprio(0);
     }
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(INFLIGHT) : "memory");   // tile t + 1; own reads done
     block_barrier();
@@ -236,8 +255,7 @@ __device__ __forceinline__ void tile_product32(const TileLoader<NB, MB, BITS, BM
       }
       __builtin_amdgcn_sched_barrier(0);   // keep the reads ahead of this step's MFMAs
       half8_t bf[CB];
-#pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
+      auto expand = [&](int cb) {
         if constexpr (BITS == 4) {
           const uint4 c = cw[cb][0];
           bf[cb] = dequant_word(s == 0 ? c.x : s == 1 ? c.y : s == 2 ? c.z : c.w, dc[cb]);
@@ -246,14 +264,28 @@ __device__ __forceinline__ void tile_product32(const TileLoader<NB, MB, BITS, BM
           const half4_t lo = dequant_word8((s & 1) ? c.z : c.x, dc[cb]), hi = dequant_word8((s & 1) ? c.w : c.y, dc[cb]);
           bf[cb] = half8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
         }
+      };
+      auto multiply = [&](int rb, int cb) {
+        acc[rb][cb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[s & 1][rb], bf[cb], acc[rb][cb], 0, 0, 0);
+      };
+      if constexpr (BM == 128) {   // one block's weights at a time
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          expand(cb);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) multiply(rb, cb);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) expand(cb);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) multiply(rb, cb);
+        __builtin_amdgcn_s_setprio(0);
       }
-      __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-      for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
-          acc[rb][cb] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[s & 1][rb], bf[cb], acc[rb][cb], 0, 0, 0);
-      __builtin_amdgcn_s_setprio(0);
     }
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(INFLIGHT) : "memory");   // tile t + 1; own reads done
     block_barrier();
