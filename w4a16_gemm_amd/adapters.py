@@ -114,6 +114,13 @@ def _sizes(t, dims, name):
     return t.shape
 
 
+def _int32(value, name):
+    """A scalar argument; ctypes would pass the lowest 32 bits of a larger one."""
+    if not -2 ** 31 <= value < 2 ** 31:
+        raise ValueError(f"{name}={value} is beyond 32 bits")
+    return value
+
+
 def _matrix(t, name):
     return _sizes(t, 2, name)
 

@@ -8,7 +8,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from .adapters import (_check, _handle, _matrix, _on, _operands, _overlap, _ptr, _sizes, _torch, _workspace)
+from .adapters import (_check, _handle, _int32, _matrix, _on, _operands, _overlap, _ptr, _sizes, _torch, _workspace)
 
 _p, _i, _z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 
@@ -106,6 +106,7 @@ def w4a16_route(logits, top_k: int, renormalise: bool = True, index=None, weight
     torch = _torch()
     bits = _logit_bits(logits)
     M, E = _matrix(logits, "logits")
+    top_k = _int32(top_k, "top_k")
     device = _operands(((logits, logits.dtype, (M, E), "logits"), (index, torch.int32, (M, top_k), "index"),
                         (weights, torch.float32, (M, top_k), "weights")))
     if index is not None:

@@ -7,7 +7,7 @@ from __future__ import annotations
 import ctypes
 import functools
 
-from .adapters import _check, _handle, _matrix, _on, _operands, _overlap, _ptr, _torch, _workspace
+from .adapters import _check, _handle, _int32, _matrix, _on, _operands, _overlap, _ptr, _torch, _workspace
 from .experts import _inputs, _layer_specs
 
 _p, _i, _z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
@@ -45,7 +45,7 @@ def _loss(bits, x, qweight, scales, qzeros, g_idx, group_size, target, vocab, lo
     torch = _torch()
     M, K = _matrix(x, "x")
     _, N, layer = _layer_specs(qweight, scales, qzeros, g_idx, group_size, K, bits, False)
-    vocab = N if vocab is None else vocab
+    vocab = N if vocab is None else _int32(vocab, "vocab")
     f32 = torch.float32
     specs = ((x, torch.float16, (M, K), "x"), *layer, (target, torch.int32, (M,), "target"))
     if target is None:
@@ -88,7 +88,7 @@ def _loss_backward(bits, dloss, x, qweight, scales, qzeros, g_idx, group_size, t
     torch = _torch()
     M, K = _matrix(x, "x")
     _, N, layer = _layer_specs(qweight, scales, qzeros, g_idx, group_size, K, bits, False)
-    vocab = N if vocab is None else vocab
+    vocab = N if vocab is None else _int32(vocab, "vocab")
     f32 = torch.float32
     specs = ((x, torch.float16, (M, K), "x"), *layer, (target, torch.int32, (M,), "target"), (lse, f32, (M,), "lse"),
              (dloss, f32, (M,), "dloss"))
