@@ -14,8 +14,9 @@
  * channels; M, T > 0, S <= 2^27.  The layers' shapes are those of w4a16.h and besides K % 64
  * == 0, for 8-bit weights N % 16 == 0, N <= 2^24, fewer than 2^32 bytes of codes per expert, and
  * fewer than 2^31 elements of x, of dy and of the slots' rows of K channels under act order;
- * what one launch takes bounds S to 2^23 under act order, and M to 2^22 where the gradients
- * of several slots are summed or act order is undone.
+ * what one launch takes bounds S to 2^23 under act order, M to 2^22 where the gradients
+ * of several slots are summed or act order is undone, and the tiles of a product
+ * (about S / 256 + E row tiles of N / 256 columns, back K / 256) to 2^22.
  *   qweight   int32 [E][w4a16_qweight_words(N, K, act_order)] (w8a16: its own function): the
  *             experts' weight buffers one after the other
  *   scales    binary16 [E][G][N];  qzeros  int32 [E][G][N/8] (8 bits: [N/4]) or NULL: symmetric
@@ -78,7 +79,8 @@ int w8a16_experts_gemm(const uint16_t* x, const int32_t* qweight, const uint16_t
                        const int32_t* g_idx, int group_size, const int32_t* index, int M, int T, int E, int N, int K,
                        uint16_t* y, void* workspace, size_t workspace_bytes, void* stream);
 
-/* Workspace bytes of w4a16_experts_backward and w8a16_experts_backward. */
+/* Workspace bytes of w4a16_experts_backward and w8a16_experts_backward.  For T > 1, or under act
+ * order, a float per slot and channel and more, 4 M T K bytes: large batches go in several calls. */
 size_t w4a16_experts_backward_workspace(int M, int T, int E, int N, int K, int act_order);
 
 /* Gradient of the rows: dx[m] = binary16(dx0[m] + sum_t W^_e^T dy[m][t]), e = index[m][t], summed

@@ -41,7 +41,8 @@ size_t w4a16_head_loss_backward_workspace(int M, int N, int K, int act_order);
 /* dx[m] = binary16(dloss[m] (sum_v exp(l_v - lse[m]) W^_v - W^_target)) for the gradient of the
  * losses, dloss float [M] (a training program puts its loss scale there: dx is binary16); lse as
  * w4a16_head_loss gave it.  The probabilities enter the product as binary16 values times
- * 2^14, fp32 sums, one rounding at the end.  dx binary16 [M][K].  Errors as w4a16_head_loss. */
+ * 2^14, fp32 sums, one rounding at the end.  The rounding of lse, 2^-24 |lse|, is an error of every
+ * probability relative to it, and so an absolute one of the target's p - 1.  dx binary16 [M][K].  Errors as w4a16_head_loss. */
 int w4a16_head_loss_backward(const float* dloss, const uint16_t* x, const int32_t* qweight, const uint16_t* scales,
                              const int32_t* qzeros, const int32_t* g_idx, int group_size, const int32_t* target,
                              const float* lse, int M, int N, int K, int vocab, uint16_t* dx, void* workspace,

@@ -108,7 +108,9 @@ SlotPlan take_plan(Carver& ws, int64_t S, int E, int64_t tiles, bool tile_of) {
 
 // --- tile shapes ------------------------------------------------------------------------
 
-constexpr int kUnits = 256;   // compute units
+// Compute units of a whole device.  A constant, so that the workspace functions need no device and
+// agree with the calls; on fewer units the choices are slower ones, and no less right.
+constexpr int kUnits = 256;
 
 // A tile's place in a kernel: the height of the plan's full tiles; bm, the rows that the kernel's
 // ring has room for (256: a workgroup per compute unit, 128: two, with half the memory each; 64:

@@ -84,7 +84,8 @@ TileShape pick_shape(int64_t S, int E, int cols) { return pick_forward(S, E, col
 // --- forward ----------------------------------------------------------------------------
 
 // Few rows per expert: the streaming kernel, at most 4096 channels per walk over its
-// wavefronts (16 of them with up to 2 steps of 128 channels; 3 and 4 steps spill registers).
+// wavefronts (16 of them with up to 2 steps of 128 channels, without a spill; 3 and 4 steps spill 11
+// to 48 registers, and the 2 steps of a longer row 5 to 15, outside the loop over the units).
 // Up to 16 rows on average, and up to 32, which are two of its tiles and read the codes twice,
 // where the 64-row tiles would leave half of the compute units idle.  Against those tiles (K
 // 4096): 16 experts, N 4096, of 16 / 24 rows 34 / 54 us, in tiles 43 / 44 us; 8 of 16 / 24 / 32 rows 22 /

@@ -1,7 +1,7 @@
 // Softmax cross entropy over a quantised vocabulary head, in pieces of the vocabulary:
 //   l_v = W^_v x,  lse = log sum_v exp l_v,  loss = lse - l_target,
 //   dx = dloss (sum_v c_v W^_v),  c_v = exp(l_v - lse) - [v == target].
-// The logits of a 256-row by 256-column tile live in the accumulators of the large tile and
+// The logits of a tile of 64, 128 or 256 rows by 256 columns live in its accumulators and
 // never leave the compute unit: the forward pass writes the maximum and the sum of
 // exponentials of every row and column tile (8 bytes for 256 logits), which a second kernel
 // joins; the backward pass computes the logits of a piece again, writes its c as binary16
@@ -77,8 +77,9 @@ struct HeadTileRows {
 };
 
 // c 2^14 of logits, as binary16, and the remainder of the target's c (backward).  All but the
-// target's take one fma before the exponential: the rounding of lse log2 e is 2^-24 of that,
-// far below binary16's; the target's c may be small against its p and keeps the difference.
+// target's take one fma before the exponential: the rounding of lse log2 e is 2^-24 of that, as
+// that of lse itself is, and below binary16's up to an lse of 2^13; the target's c may be small
+// against its p and keeps the difference.
 // (Two operations per coefficient less: the coefficients of a piece of 1229 rows 267 -> 244 us,
 // of 8192 1033 -> 990 us.)
 struct HeadCoeff {

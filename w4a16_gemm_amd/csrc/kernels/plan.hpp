@@ -2,9 +2,9 @@
 // by expert, the list of row tiles over them, and the experts' packed layers.
 //
 // The sizes of the groups are known only on the device, so the products run over a list of
-// row tiles that plan_slots_kernel makes there: up to 256 slots of one expert, the remainder
-// of an expert in the smallest tile of 64, 128 or 256 rows that holds it (a product of 64
-// rows costs well below half of the 256-row one).
+// row tiles that is made there (slots.hpp): up to `height` slots of one expert, 64, 128 or 256
+// by the call's sizes, the remainder of an expert in the smallest tile up to that height that
+// holds it (a product of 64 rows costs well below half of the 256-row one).
 #pragma once
 
 #include "nibbles.hpp"
@@ -21,7 +21,7 @@ struct RowTile {
   int32_t expert;
   int32_t first;         // place of its first slot in the order
   int32_t rows;          // slots, at most `height`
-  int32_t height;        // 64, 128 or 256
+  int32_t height;        // 64, 128 or 256, at most the plan's
   int32_t panel_first;   // its panel: up to kPanelTiles tiles of one expert
   int32_t panel_tiles;
   int32_t pad[2];
