@@ -228,7 +228,7 @@ TransposedShape pick_transposed(int64_t S, int E, int outputs, int K) {
 int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 
 // Allows a kernel its dynamic LDS; once per kernel and process (the value is static at the
-// caller).
+// caller), on whichever device comes first: the runtime launches up to 160 KB without it as well.
 hipError_t allow_lds(const void* kernel, size_t bytes) {
   return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
